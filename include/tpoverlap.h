@@ -57,8 +57,9 @@ extern "C" {
 
 typedef struct tpo_ctx tpo_ctx; /* opaque */
 
-/* Input element type (Y is always bf16). */
-typedef enum { TPO_BF16 = 0, TPO_FP8_E4M3 = 1 } tpo_dtype;
+/* Input element type (Y is always bf16).  TPO_F32 is a type of tpo_layer_norm
+ * and tpo_layer_norm_bwd only. */
+typedef enum { TPO_BF16 = 0, TPO_FP8_E4M3 = 1, TPO_F32 = 2 } tpo_dtype;
 
 typedef enum {
   TPO_OK = 0,
@@ -381,6 +382,149 @@ const char* tpo_version(void);
 tpo_status tpo_ag_gemm_noalloc(int tp, int64_t n, int64_t k, int64_t m, int dtype, const void* const* x,
                                const void* w, void* y, const float* d_scale_inv_x,
                                const float* d_scale_inv_w, void* stream);
+
+/*
+ * Block operators: the parts of a transformer sublayer that sit next to its
+ * tensor-parallel projections.  Layer norm, a linear layer with bias,
+ * activation and residual in the product's epilogue, and the gated
+ * feed-forward projections, each with its backward pass.
+ *
+ * They run on a tpo_block handle, which owns a workspace and a device error
+ * word; the rules are the context's.  A call validates its arguments on the
+ * host, enqueues kernels on `stream` and returns; nothing is allocated, and a
+ * call may be captured into a CUDA graph.  The current device must be the
+ * handle's.  A handle is not thread-safe, and calls that overlap on the GPU
+ * (different streams) need different handles.  A device-side wait that runs
+ * out is sticky until tpo_block_sync_status reports it.
+ *
+ * Layout: n counts rows (tokens), k input features, m output features.  Every
+ * matrix is row-major with its own row pitch `ld` in elements (at least the
+ * row's length).  Pitches of the matrix products are multiples of 16 bytes and
+ * their addresses 16-byte aligned (a matrix of at most one row needs no
+ * pitch); k and m themselves may be any number from 1.  The layer norm takes
+ * any pitch and any address that its element type allows.  n = 0 is an empty
+ * batch: forward calls and input gradients write nothing, weight gradients
+ * become zero.  Outputs must not overlap inputs except where a call says so.
+ *
+ * Arithmetic: sums, norms, biases, activations and their derivatives are
+ * computed in fp32 from the inputs' values, and an output is rounded once, to
+ * its own type.  The backward products take the gradient of the
+ * pre-activation as a matrix operand, so it is rounded to bf16 in between (the
+ * gradient of the bias is summed before that rounding).  No call uses atomics
+ * on data: the same inputs, sizes and options give the same bits.
+ * NaN and infinities in the inputs spread as the formulas say, and only there:
+ * a row of the output never sees another row's input.
+ */
+typedef struct tpo_block tpo_block; /* opaque */
+
+/* Activations.  GELU is x Phi(x), GELU_TANH its tanh form
+ * x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))), SILU x / (1 + exp(-x)).
+ * RELU's derivative at 0 is 0. */
+typedef enum { TPO_ACT_NONE = 0, TPO_ACT_RELU = 1, TPO_ACT_GELU = 2, TPO_ACT_GELU_TANH = 3, TPO_ACT_SILU = 4 } tpo_act;
+
+/* The block operators, as tpo_block_workspace names them. */
+typedef enum {
+  TPO_OP_LAYER_NORM = 0,
+  TPO_OP_LAYER_NORM_BWD = 1,
+  TPO_OP_LINEAR = 2,
+  TPO_OP_LINEAR_BWD = 3,
+  TPO_OP_GATED = 4,
+  TPO_OP_GATED_BWD = 5
+} tpo_block_op;
+
+/* Bytes of workspace that one call of `op` with up to n rows needs (m is not
+ * used by the norms), or -1 with tpo_last_error set for sizes out of range.
+ * Forward calls need none; needs no GPU. */
+int64_t tpo_block_workspace(int op, int64_t n, int64_t k, int64_t m);
+
+/* Create a handle with `workspace_bytes` (0 or more) of workspace on the
+ * current CUDA device: the largest need of the calls it will serve.  A call
+ * whose need is larger returns TPO_ERR_INVALID_ARG and names it.  NULL on any
+ * error; tpo_last_error says why. */
+tpo_block* tpo_block_create(int64_t workspace_bytes);
+
+/* Release the handle (its pending work must have been synchronised or may
+ * still run: the release waits for the device).  NULL is a no-op. */
+tpo_status tpo_block_destroy(tpo_block* blk);
+
+/* Wait for the work on `stream`, read and clear the handle's error word. */
+tpo_status tpo_block_sync_status(tpo_block* blk, void* stream);
+
+/*
+ * Layer norm over the last dimension, row by row:
+ *   mean = sum x / k,  rstd = 1 / sqrt(sum (x - mean)^2 / k + eps)
+ *   y = (x - mean) rstd gamma + beta
+ *   dtype    of x and y: TPO_BF16 or TPO_F32
+ *   wdtype   of gamma and beta [k]: TPO_BF16 or TPO_F32; either pointer may be
+ *            NULL (gamma 1, beta 0)
+ *   mean, rstd  [n] fp32, written for the backward pass; NULL to skip
+ * The variance is the mean of squared differences (no cancellation of
+ * sums of squares).  y may be x itself, with the same pitch.
+ */
+tpo_status tpo_layer_norm(tpo_block* blk, int64_t n, int64_t k, int dtype, int wdtype, const void* x, int64_t ldx,
+                          const void* gamma, const void* beta, float eps, void* y, int64_t ldy, float* mean,
+                          float* rstd, void* stream);
+
+/*
+ * Gradient of tpo_layer_norm, with xhat = (x - mean) rstd and a = dy gamma:
+ *   dx = rstd (a - mean(a) - xhat mean(a xhat)) [+ dres]
+ *   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
+ * dres [n, k] (NULL: none) is the gradient that reaches x past the norm, as on
+ * a residual branch.  dx, dgamma and dbeta (of wdtype) may each be NULL; gamma
+ * NULL means 1.  dx may be dy or dres itself, with the same pitch.
+ */
+tpo_status tpo_layer_norm_bwd(tpo_block* blk, int64_t n, int64_t k, int dtype, int wdtype, const void* dy,
+                              int64_t lddy, const void* x, int64_t ldx, const void* gamma, const float* mean,
+                              const float* rstd, const void* dres, int64_t lddres, void* dx, int64_t lddx,
+                              void* dgamma, void* dbeta, void* stream);
+
+/*
+ * Linear layer with its epilogue:  y = act(z) + residual,  z = x w^T + bias
+ *   dtype      of x [n, k] and w [m, k]: TPO_BF16 or TPO_FP8_E4M3
+ *   bias       [m] bf16 or NULL;  act: a tpo_act
+ *   residual   [n, m] bf16 or NULL; may be y itself, with the same pitch
+ *   z          [n, m] bf16, the pre-activation for the backward pass, or NULL
+ *   y          [n, m] bf16
+ *   d_scale_inv_x, d_scale_inv_w  e4m3: device pointers to one fp32 each, the
+ *              product is multiplied by both before the bias; bf16: NULL
+ */
+tpo_status tpo_linear(tpo_block* blk, int64_t n, int64_t k, int64_t m, int dtype, const void* x, int64_t ldx,
+                      const void* w, int64_t ldw, const void* bias, int act, const void* residual, int64_t ldr,
+                      void* z, int64_t ldz, void* y, int64_t ldy, const float* d_scale_inv_x,
+                      const float* d_scale_inv_w, void* stream);
+
+/*
+ * Gradient of tpo_linear (bf16):  dz = dy act'(z);
+ *   dx [n, k] = dz w,  dw [m, k] = dz^T x,  db [m] = sum over rows of dz
+ * z is the forward call's (TPO_ACT_NONE: NULL).  dx, dw and db may each be
+ * NULL (w is then not needed for dx, x not for dw).  The residual's gradient
+ * is dy itself.
+ */
+tpo_status tpo_linear_bwd(tpo_block* blk, int64_t n, int64_t k, int64_t m, int act, const void* dy, int64_t lddy,
+                          const void* z, int64_t ldz, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                          void* dx, int64_t lddx, void* dw, int64_t lddw, void* db, void* stream);
+
+/*
+ * Gated feed-forward projections:  h = act(g) * u,  g = x wg^T,  u = x wu^T
+ * (SILU: SwiGLU, GELU: GeGLU, RELU: ReGLU, NONE: bilinear).
+ *   x [n, k], wg and wu [m, k] of dtype; h [n, m] bf16
+ *   g, u       [n, m] bf16 for the backward pass, both or neither NULL
+ *   scales     e4m3: device pointers for x, wg and wu; bf16: NULL
+ */
+tpo_status tpo_gated(tpo_block* blk, int64_t n, int64_t k, int64_t m, int dtype, const void* x, int64_t ldx,
+                     const void* wg, int64_t ldwg, const void* wu, int64_t ldwu, int act, void* g, int64_t ldg,
+                     void* u, int64_t ldu, void* h, int64_t ldh, const float* d_scale_inv_x,
+                     const float* d_scale_inv_wg, const float* d_scale_inv_wu, void* stream);
+
+/*
+ * Gradient of tpo_gated (bf16):  dg = dh u act'(g),  du = dh act(g);
+ *   dx [n, k] = dg wg + du wu,  dwg [m, k] = dg^T x,  dwu [m, k] = du^T x
+ * dx may be NULL, and dwg and dwu together.
+ */
+tpo_status tpo_gated_bwd(tpo_block* blk, int64_t n, int64_t k, int64_t m, int act, const void* dh, int64_t lddh,
+                         const void* g, int64_t ldg, const void* u, int64_t ldu, const void* x, int64_t ldx,
+                         const void* wg, int64_t ldwg, const void* wu, int64_t ldwu, void* dx, int64_t lddx,
+                         void* dwg, int64_t lddwg, void* dwu, int64_t lddwu, void* stream);
 
 #ifdef __cplusplus
 }

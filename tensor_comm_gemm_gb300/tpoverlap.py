@@ -16,7 +16,10 @@ from typing import Optional, Sequence
 
 from . import build as _build
 
-TPO_BF16, TPO_FP8_E4M3 = 0, 1
+TPO_BF16, TPO_FP8_E4M3, TPO_F32 = 0, 1, 2
+TPO_ACT_NONE, TPO_ACT_RELU, TPO_ACT_GELU, TPO_ACT_GELU_TANH, TPO_ACT_SILU = 0, 1, 2, 3, 4
+TPO_OP_LAYER_NORM, TPO_OP_LAYER_NORM_BWD, TPO_OP_LINEAR = 0, 1, 2
+TPO_OP_LINEAR_BWD, TPO_OP_GATED, TPO_OP_GATED_BWD = 3, 4, 5
 TPO_ERR_INVALID_ARG, TPO_ERR_UNSUPPORTED = 1, 2
 STATUS = {0: "TPO_OK", 1: "TPO_ERR_INVALID_ARG", 2: "TPO_ERR_UNSUPPORTED", 3: "TPO_ERR_CUDA",
           4: "TPO_ERR_TIMEOUT", 5: "TPO_ERR_OOM"}
@@ -29,7 +32,9 @@ TPO_MAX_TP, TPO_MAX_ROW_CHUNKS = 16, 64
 # Every symbol the public header declares.
 EXPORTS = ["tpo_ctx_create", "tpo_ctx_destroy", "tpo_ag_gemm", "tpo_gemm_rs", "tpo_gemm_ar", "tpo_set_opt",
            "tpo_get_opt", "tpo_sync_status", "tpo_last_device_error", "tpo_last_error", "tpo_staging_ptr",
-           "tpo_done_counters", "tpo_read_trace", "tpo_version", "tpo_ag_gemm_noalloc", "tpo_set_fp8_scales"]
+           "tpo_done_counters", "tpo_read_trace", "tpo_version", "tpo_ag_gemm_noalloc", "tpo_set_fp8_scales",
+           "tpo_block_workspace", "tpo_block_create", "tpo_block_destroy", "tpo_block_sync_status",
+           "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear", "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"]
 TPO_NOALLOC_MAX_STAGING_BYTES = 32 << 20
 
 
@@ -74,6 +79,22 @@ def lib(path: Optional[str] = None):
     L.tpo_set_fp8_scales.argtypes = [p, p, p]
     L.tpo_set_fp8_scales.restype = ctypes.c_int
     L.tpo_ag_gemm_noalloc.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    L.tpo_block_workspace.argtypes = [i32, i64, i64, i64]
+    L.tpo_block_workspace.restype = i64
+    L.tpo_block_create.argtypes = [i64]
+    L.tpo_block_create.restype = p
+    L.tpo_block_destroy.argtypes = [p]
+    L.tpo_block_sync_status.argtypes = [p, p]
+    L.tpo_layer_norm.argtypes = [p, i64, i64, i32, i32, p, i64, p, p, f32, p, i64, p, p, p]
+    L.tpo_layer_norm_bwd.argtypes = [p, i64, i64, i32, i32, p, i64, p, i64, p, p, p, p, i64, p, i64, p, p, p]
+    L.tpo_linear.argtypes = [p, i64, i64, i64, i32, p, i64, p, i64, p, i32, p, i64, p, i64, p, i64, p, p, p]
+    L.tpo_linear_bwd.argtypes = [p, i64, i64, i64, i32] + [p, i64] * 6 + [p, p]
+    L.tpo_gated.argtypes = [p, i64, i64, i64, i32, p, i64, p, i64, p, i64, i32] + [p, i64] * 3 + [p] * 4
+    L.tpo_gated_bwd.argtypes = [p, i64, i64, i64, i32] + [p, i64] * 9 + [p]
+    for name in ("tpo_block_destroy", "tpo_block_sync_status", "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear",
+                 "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"):
+        getattr(L, name).restype = ctypes.c_int
     for name in ("tpo_ctx_destroy", "tpo_ag_gemm", "tpo_gemm_rs", "tpo_gemm_ar", "tpo_set_opt", "tpo_get_opt",
                  "tpo_sync_status", "tpo_last_device_error", "tpo_read_trace"):
         getattr(L, name).restype = ctypes.c_int
@@ -270,3 +291,169 @@ def tpo_ag_gemm_noalloc(tp: int, n: int, k: int, m: int, dtype: int, x: Sequence
     xa = _ptr_array(x)
     _check(lib().tpo_ag_gemm_noalloc(tp, n, k, m, dtype, _addr(xa), _ptr(w), _ptr(y), _ptr(scale_inv_x),
                                      _ptr(scale_inv_w), _stream(stream)))
+
+
+# ------------------------------------------------------------------ block operators
+#
+# Tensors carry their sizes, row pitches and types: matrices are 2-D with unit
+# stride in the last dimension, vectors contiguous.
+
+def _dtype_codes():
+    import torch
+    return {torch.bfloat16: TPO_BF16, torch.float32: TPO_F32, torch.float8_e4m3fn: TPO_FP8_E4M3,
+            torch.uint8: TPO_FP8_E4M3}
+
+
+_CODES = {}      # torch dtype -> tpo_dtype, filled on first use (uint8 holds e4m3 codes)
+
+
+def _code(name, t) -> int:
+    if not _CODES:
+        _CODES.update(_dtype_codes())
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
+    return c
+
+
+def _mat(name, t, rows, cols, code):
+    """(pointer, pitch) of an [rows, cols] CUDA matrix of type `code`; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s has shape %s, expected (%d, %d)" % (name, tuple(shape), rows, cols))
+    if not t.is_cuda:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
+    if _code(name, t) != code:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must have unit stride in its last dimension" % name)
+    return t.data_ptr(), ld
+
+
+def _vec(name, t, count, code):
+    if t is None:
+        return None
+    if t.numel() != count or not t.is_contiguous():
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must hold %d contiguous elements" % (name, count))
+    if not t.is_cuda:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
+    if _code(name, t) != code:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
+    return t.data_ptr()
+
+
+def _shape2(name, t):
+    if t.dim() != 2:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be 2-D" % name)
+    return t.shape
+
+
+def tpo_block_workspace(op: int, n: int, k: int, m: int = 1) -> int:
+    b = lib().tpo_block_workspace(op, n, k, m)
+    if b < 0:
+        raise TpoError(TPO_ERR_INVALID_ARG, tpo_last_error())
+    return b
+
+
+def tpo_block_create(workspace_bytes: int = 0) -> int:
+    h = lib().tpo_block_create(workspace_bytes)
+    if not h:
+        raise TpoError(-1, tpo_last_error())
+    return h
+
+
+def tpo_block_destroy(block: int) -> None:
+    _check(lib().tpo_block_destroy(block))
+
+
+def tpo_block_sync_status(block: int, stream=None) -> int:
+    """Returns the status code (0 = TPO_OK) instead of raising, as tpo_sync_status."""
+    return lib().tpo_block_sync_status(block, _stream(stream))
+
+
+def tpo_layer_norm(block: int, x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    n, k = _shape2("x", x)
+    dt = _code("x", x)
+    w = gamma if gamma is not None else beta
+    wt = dt if w is None else _code("gamma", w)
+    px, ldx = _mat("x", x, n, k, dt)
+    py, ldy = _mat("y", y, n, k, dt)
+    _check(lib().tpo_layer_norm(block, n, k, dt, wt, px, ldx, _vec("gamma", gamma, k, wt), _vec("beta", beta, k, wt),
+                                eps, py, ldy, _vec("mean", mean, n, TPO_F32), _vec("rstd", rstd, n, TPO_F32),
+                                _stream(stream)))
+
+
+def tpo_layer_norm_bwd(block: int, dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None,
+                       stream=None) -> None:
+    n, k = _shape2("x", x)
+    dt = _code("x", x)
+    w = gamma if gamma is not None else dgamma if dgamma is not None else dbeta
+    wt = dt if w is None else _code("gamma", w)
+    pdy, lddy = _mat("dy", dy, n, k, dt)
+    px, ldx = _mat("x", x, n, k, dt)
+    pdr, lddr = _mat("dres", dres, n, k, dt)
+    pdx, lddx = _mat("dx", dx, n, k, dt)
+    _check(lib().tpo_layer_norm_bwd(block, n, k, dt, wt, pdy, lddy, px, ldx, _vec("gamma", gamma, k, wt),
+                                    _vec("mean", mean, n, TPO_F32), _vec("rstd", rstd, n, TPO_F32), pdr, lddr, pdx,
+                                    lddx, _vec("dgamma", dgamma, k, wt), _vec("dbeta", dbeta, k, wt),
+                                    _stream(stream)))
+
+
+def tpo_linear(block: int, x, w, y, bias=None, act: int = TPO_ACT_NONE, residual=None, z=None, scale_inv_x=None,
+               scale_inv_w=None, stream=None) -> None:
+    n, k = _shape2("x", x)
+    m = _shape2("w", w)[0]
+    dt = _code("x", x)
+    px, ldx = _mat("x", x, n, k, dt)
+    pw, ldw = _mat("w", w, m, k, dt)
+    py, ldy = _mat("y", y, n, m, TPO_BF16)
+    pr, ldr = _mat("residual", residual, n, m, TPO_BF16)
+    pz, ldz = _mat("z", z, n, m, TPO_BF16)
+    _check(lib().tpo_linear(block, n, k, m, dt, px, ldx, pw, ldw, _vec("bias", bias, m, TPO_BF16), act, pr, ldr, pz,
+                            ldz, py, ldy, _vec("scale_inv_x", scale_inv_x, 1, TPO_F32),
+                            _vec("scale_inv_w", scale_inv_w, 1, TPO_F32), _stream(stream)))
+
+
+def tpo_linear_bwd(block: int, dy, x, w, dx=None, dw=None, db=None, act: int = TPO_ACT_NONE, z=None,
+                   stream=None) -> None:
+    n, m = _shape2("dy", dy)
+    wide = next((t for t in (x, w, dx, dw) if t is not None), None)
+    k = 1 if wide is None else _shape2("x, w, dx and dw", wide)[1]
+    pdy, lddy = _mat("dy", dy, n, m, TPO_BF16)
+    pz, ldz = _mat("z", z, n, m, TPO_BF16)
+    px, ldx = _mat("x", x, n, k, TPO_BF16)
+    pw, ldw = _mat("w", w, m, k, TPO_BF16)
+    pdx, lddx = _mat("dx", dx, n, k, TPO_BF16)
+    pdw, lddw = _mat("dw", dw, m, k, TPO_BF16)
+    _check(lib().tpo_linear_bwd(block, n, k, m, act, pdy, lddy, pz, ldz, px, ldx, pw, ldw, pdx, lddx, pdw, lddw,
+                                _vec("db", db, m, TPO_BF16), _stream(stream)))
+
+
+def tpo_gated(block: int, x, wg, wu, h, act: int = TPO_ACT_SILU, g=None, u=None, scale_inv_x=None,
+              scale_inv_wg=None, scale_inv_wu=None, stream=None) -> None:
+    n, k = _shape2("x", x)
+    m = _shape2("wg", wg)[0]
+    dt = _code("x", x)
+    px, ldx = _mat("x", x, n, k, dt)
+    pwg, ldwg = _mat("wg", wg, m, k, dt)
+    pwu, ldwu = _mat("wu", wu, m, k, dt)
+    ph, ldh = _mat("h", h, n, m, TPO_BF16)
+    pg, ldg = _mat("g", g, n, m, TPO_BF16)
+    pu, ldu = _mat("u", u, n, m, TPO_BF16)
+    _check(lib().tpo_gated(block, n, k, m, dt, px, ldx, pwg, ldwg, pwu, ldwu, act, pg, ldg, pu, ldu, ph, ldh,
+                           _vec("scale_inv_x", scale_inv_x, 1, TPO_F32), _vec("scale_inv_wg", scale_inv_wg, 1, TPO_F32),
+                           _vec("scale_inv_wu", scale_inv_wu, 1, TPO_F32), _stream(stream)))
+
+
+def tpo_gated_bwd(block: int, dh, g, u, x, wg, wu, dx=None, dwg=None, dwu=None, act: int = TPO_ACT_SILU,
+                  stream=None) -> None:
+    n, m = _shape2("dh", dh)
+    k = _shape2("x", x)[1]
+    args = []
+    for name, t, rows, cols in (("dh", dh, n, m), ("g", g, n, m), ("u", u, n, m), ("x", x, n, k), ("wg", wg, m, k),
+                                ("wu", wu, m, k), ("dx", dx, n, k), ("dwg", dwg, m, k), ("dwu", dwu, m, k)):
+        args += _mat(name, t, rows, cols, TPO_BF16)
+    _check(lib().tpo_gated_bwd(block, n, k, m, act, *args, _stream(stream)))
