@@ -39,6 +39,7 @@ struct tpo_block {
   int device = 0;
   uint8_t* mem = nullptr;  // error words, then the workspace
   int64_t ws_bytes = 0;
+  tpo::Machine machine{};
   uint32_t* err() const { return reinterpret_cast<uint32_t*>(mem); }
   uint8_t* ws() const { return mem + kErrBytes; }
 };
@@ -180,6 +181,12 @@ tpo_block* tpo_block_create(int64_t workspace_bytes) {
     delete b;
     return nullptr;
   }
+  e = tpo::configure_products(&b->machine);
+  if (e != cudaSuccess) {
+    cuda_fail(e, "kernel configuration");
+    delete b;
+    return nullptr;
+  }
   b->ws_bytes = workspace_bytes;
   e = cudaMalloc(&b->mem, kErrBytes + static_cast<size_t>(workspace_bytes));
   if (e != cudaSuccess) {
@@ -295,10 +302,10 @@ tpo_status tpo_linear(tpo_block* b, int64_t n, int64_t k, int64_t m, int dtype, 
   if (n == 0) return TPO_OK;
   tpo::Epi e;
   e.kind = tpo::EPI_LINEAR, e.act = act, e.bias = bias, e.residual = residual, e.ldr = mr.ld;
-  e.out0 = y, e.ld0 = my.ld, e.out1 = z, e.ld1 = mz.ld, e.sx = d_scale_inv_x, e.sw0 = d_scale_inv_w;
-  const tpo::View a{x, mx.ld, 1}, bw{w, mw.ld, 1};
-  return launched(tpo::launch_simple_gemm(&a, &bw, 1, n, m, k, dtype == TPO_FP8_E4M3, e,
-                                          static_cast<cudaStream_t>(stream)));
+  e.out1 = z, e.ld1 = mz.ld, e.sx = d_scale_inv_x, e.sw0 = d_scale_inv_w;
+  const tpo::Product q{{{x, mx.ld, false}}, {{w, mw.ld, false}}, 1, n, m, k, y, my.ld};
+  return launched(tpo::launch_products(b->machine, &q, 1, dtype == TPO_FP8_E4M3, e, b->err(),
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 tpo_status tpo_linear_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act, const void* dy, int64_t lddy,
@@ -337,19 +344,12 @@ tpo_status tpo_linear_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act
     if (e != cudaSuccess) return launched(e);
     if (make_dz) dz = out, lddz = ws_pitch(m);
   }
-  if (dx) {
-    tpo::Epi e;
-    e.out0 = dx, e.ld0 = mdx.ld;
-    const tpo::View a{dz, lddz, 1}, bw{w, 1, mw.ld};
-    if (tpo_status st = launched(tpo::launch_simple_gemm(&a, &bw, 1, n, k, m, false, e, s))) return st;
-  }
-  if (dw) {
-    tpo::Epi e;
-    e.out0 = dw, e.ld0 = mdw.ld;
-    const tpo::View a{dz, 1, lddz}, bx{x, 1, mx.ld};
-    if (tpo_status st = launched(tpo::launch_simple_gemm(&a, &bx, 1, m, k, n, false, e, s))) return st;
-  }
-  return TPO_OK;
+  tpo::Product q[2];
+  int count = 0;
+  if (dx) q[count++] = {{{dz, lddz, false}}, {{w, mw.ld, true}}, 1, n, k, m, dx, mdx.ld};
+  if (dw) q[count++] = {{{dz, lddz, true}}, {{x, mx.ld, true}}, 1, m, k, n, dw, mdw.ld};
+  if (count == 0) return TPO_OK;
+  return launched(tpo::launch_products(b->machine, q, count, false, tpo::Epi(), b->err(), s));
 }
 
 tpo_status tpo_gated(tpo_block* b, int64_t n, int64_t k, int64_t m, int dtype, const void* x, int64_t ldx,
@@ -374,11 +374,11 @@ tpo_status tpo_gated(tpo_block* b, int64_t n, int64_t k, int64_t m, int dtype, c
   if (tpo_status st = check_block(b, 0)) return st;
   if (n == 0) return TPO_OK;
   tpo::Epi e;
-  e.kind = tpo::EPI_GATED, e.act = act, e.out0 = h, e.ld0 = mh.ld, e.out1 = g, e.ld1 = mog.ld, e.out2 = u;
-  e.ld2 = mou.ld, e.sx = d_scale_inv_x, e.sw0 = d_scale_inv_wg, e.sw1 = d_scale_inv_wu;
-  const tpo::View a{x, mx.ld, 1}, bw[2] = {{wg, mg.ld, 1}, {wu, mu.ld, 1}};
-  return launched(tpo::launch_simple_gemm(&a, bw, 1, n, m, k, dtype == TPO_FP8_E4M3, e,
-                                          static_cast<cudaStream_t>(stream)));
+  e.kind = tpo::EPI_GATED, e.act = act, e.out1 = g, e.ld1 = mog.ld, e.out2 = u, e.ld2 = mou.ld;
+  e.sx = d_scale_inv_x, e.sw0 = d_scale_inv_wg, e.sw1 = d_scale_inv_wu;
+  const tpo::Product q{{{x, mx.ld, false}}, {{wg, mg.ld, false}, {wu, mu.ld, false}}, 1, n, m, k, h, mh.ld};
+  return launched(tpo::launch_products(b->machine, &q, 1, dtype == TPO_FP8_E4M3, e, b->err(),
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 tpo_status tpo_gated_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act, const void* dh, int64_t lddh,
@@ -416,25 +416,15 @@ tpo_status tpo_gated_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act,
   uint8_t* du = dg + n * ld * 2;
   cudaError_t ce = tpo::launch_gated_act_bwd(n, m, act, dh, mdh.ld, g, mg.ld, u, mu.ld, dg, du, ld, s);
   if (ce != cudaSuccess) return launched(ce);
-  if (dx) {
-    tpo::Epi e;
-    e.out0 = dx, e.ld0 = mdx.ld;
-    const tpo::View a[2] = {{dg, ld, 1}, {du, ld, 1}}, bw[2] = {{wg, 1, mwg.ld}, {wu, 1, mwu.ld}};
-    if (tpo_status st = launched(tpo::launch_simple_gemm(a, bw, 2, n, k, m, false, e, s))) return st;
-  }
+  tpo::Product q[3];
+  int count = 0;
+  if (dx)
+    q[count++] = {{{dg, ld, false}, {du, ld, false}}, {{wg, mwg.ld, true}, {wu, mwu.ld, true}}, 2, n, k, m, dx, mdx.ld};
   if (dwg) {
-    const tpo::View bx{x, 1, mx.ld};
-    const void* d[2] = {dg, du};
-    void* out[2] = {dwg, dwu};
-    const int64_t lds[2] = {mdwg.ld, mdwu.ld};
-    for (int i = 0; i < 2; ++i) {
-      tpo::Epi e;
-      e.out0 = out[i], e.ld0 = lds[i];
-      const tpo::View a{d[i], 1, ld};
-      if (tpo_status st = launched(tpo::launch_simple_gemm(&a, &bx, 1, m, k, n, false, e, s))) return st;
-    }
+    q[count++] = {{{dg, ld, true}}, {{x, mx.ld, true}}, 1, m, k, n, dwg, mdwg.ld};
+    q[count++] = {{{du, ld, true}}, {{x, mx.ld, true}}, 1, m, k, n, dwu, mdwu.ld};
   }
-  return TPO_OK;
+  return launched(tpo::launch_products(b->machine, q, count, false, tpo::Epi(), b->err(), s));
 }
 
 }  // extern "C"

@@ -11,18 +11,26 @@
 
 namespace tpo {
 
-// A matrix operand as the simple kernels address it: element (i, j) at
-// p + i * row + j * col, in elements.
-struct View {
+// One matrix product C[M, N] = sum over `terms` of A_t[M, K] . B_t[N, K]^T.  An
+// operand is K-major (the contraction index contiguous: element (i, j) at
+// p + i * ld + j) or MN-major (p + j * ld + i).
+struct Operand {
   const void* p;
-  int64_t row, col;
+  int64_t ld;
+  bool mn_major;
+};
+struct Product {
+  Operand a[2], b[2];
+  int terms;
+  int64_t M, N, K;
+  void* out;  // bf16 [M, N]
+  int64_t ldo;
 };
 
-// One product C[M, N] = sum over terms of A_t[M, K] . B_t[N, K]^T.
 enum EpiKind : int {
-  EPI_PLAIN = 0,   // out0 = C
-  EPI_LINEAR = 1,  // out1 = C + bias (if wanted), out0 = act(C + bias) + residual
-  EPI_GATED = 2,   // out1 = A.B0^T, out2 = A.B1^T (if wanted), out0 = act(out1) * out2, unrounded
+  EPI_PLAIN = 0,   // out = C
+  EPI_LINEAR = 1,  // out1 = C + bias (if wanted), out = act(C + bias) + residual
+  EPI_GATED = 2,   // out1 = A.B0^T, out2 = A.B1^T (if wanted), out = act(out1) * out2 from the unrounded two
 };
 struct Epi {
   int kind = EPI_PLAIN;
@@ -30,10 +38,19 @@ struct Epi {
   const void* bias = nullptr;      // bf16 [N]
   const void* residual = nullptr;  // bf16 [M, N]
   int64_t ldr = 0;
-  void *out0 = nullptr, *out1 = nullptr, *out2 = nullptr;  // bf16
-  int64_t ld0 = 0, ld1 = 0, ld2 = 0;
+  void *out1 = nullptr, *out2 = nullptr;  // bf16
+  int64_t ld1 = 0, ld2 = 0;
   const float *sx = nullptr, *sw0 = nullptr, *sw1 = nullptr;  // e4m3 scales or NULL
 };
+
+// Places for CTA pairs and SMs on the current device; also sets the kernels' attributes.
+struct Machine {
+  int sms, pairs;
+};
+cudaError_t configure_products(Machine* m);
+// Runs `count` (1 to 3) products in one launch; more than one take EPI_PLAIN.
+cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, uint32_t* err,
+                            cudaStream_t s);
 
 struct NormArgs {
   int64_t n, k;
@@ -45,8 +62,6 @@ struct NormArgs {
   float eps;
 };
 
-cudaError_t launch_simple_gemm(const View* a, const View* b, int terms, int64_t M, int64_t N, int64_t K, bool fp8,
-                               const Epi& e, cudaStream_t s);
 // dz = dy act'(z) as bf16 [n, m] with pitch ldo (NULL: not written) and db = column sums (NULL: not wanted).
 cudaError_t launch_act_bwd(int64_t n, int64_t m, int act, const void* dy, int64_t lddy, const void* z, int64_t ldz,
                            void* dz, int64_t ldo, void* db, cudaStream_t s);

@@ -1,0 +1,557 @@
+// Matrix products of the block operators on CTA pairs (sm_103a).
+//
+// A persistent kernel: each pair of CTAs computes tiles of 256 rows by up to
+// 256 columns with the 2-SM tcgen05.mma (each CTA holds 128 rows of A and half
+// of the B tile; fp32 accumulators in tensor memory, two of them, so that one
+// tile's epilogue runs beside the next one's MMAs).  Warp 0 issues the TMA
+// loads, warp 1 of the even CTA the MMAs, warps 2 to 9 the epilogue.
+//
+// One launch runs up to three products one tile list after another, so that
+// the gradients of a layer (dx, and the weights' gradients) share one tail.
+// Operands may be K-major (rows of contraction elements) or MN-major (the
+// transposed matrix as it lies in memory), per product: both are loaded with
+// the 128-byte swizzle, as [rows][64 contraction elements] or as blocks of
+// [64 contraction rows][64 elements], and the MMA's descriptors say which.
+//
+// Every wait is bounded by the device global timer; on expiry the waiting
+// thread records it in the handle's error word and the CTA winds down.
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "act.h"
+#include "block.h"
+#include "ptx.h"
+
+namespace tpo {
+
+namespace {
+
+constexpr int TM = 128;              // rows of one CTA; a pair's tile has 256
+constexpr int TN = 256;              // most columns of a tile (accumulator width)
+constexpr int KB = 128;              // bytes of contraction elements per K block
+constexpr int A_BYTES = TM * KB;     // 16 KiB
+constexpr int B_BYTES = TN / 2 * KB;  // 16 KiB: half of the tile's B rows
+constexpr int STAGE = A_BYTES + B_BYTES;
+constexpr int STAGES = 6;
+constexpr int EPI_WARPS_N = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS_N;
+constexpr int CHUNK = 32;                   // columns of one epilogue step
+constexpr int BOX = 32 * CHUNK * 2;         // bytes of one output box: 32 rows of 64 bytes
+constexpr int OFF_EPI = STAGES * STAGE;
+constexpr int OFF_BARS = OFF_EPI + EPI_WARPS_N * 2 * BOX;
+constexpr int N_BARS = 2 * STAGES + 2 + 2 + 1;
+constexpr int OFF_TMEM = OFF_BARS + 8 * N_BARS;
+constexpr int SMEM = OFF_TMEM + 16 + 1024;  // and the slack to align the base
+static_assert(SMEM <= 232448, "shared memory of one CTA");
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+
+// An output matrix: its map for tensor stores, and its address for ragged edges.
+struct OutMat {
+  CUtensorMap map;
+  __nv_bfloat16* p;
+  int64_t ld;
+};
+struct Prob {
+  CUtensorMap a[2], b[2];
+  OutMat y;
+  int M, N;
+  int tiles_m, tiles;   // row tiles, tiles in all
+  int w;                // columns of a tile (EPI_GATED: of h; the accumulator has twice as many)
+  int kb_seg, kb;       // K blocks per term and in all
+  int a_mn, b_mn;
+};
+struct Args {
+  Prob q[3];
+  OutMat y1, y2;
+  int count, total;
+  int act;
+  const __nv_bfloat16 *bias, *residual;
+  int64_t ldr;
+  int has1;             // y1 (and for EPI_GATED y2) are stored
+  const float *sx, *sw0, *sw1;
+  uint32_t* err;
+};
+
+enum Site : uint32_t { S_EMPTY = 1, S_FULL = 2, S_TEMPTY = 3, S_TFULL = 4, S_DRAIN = 5 };
+
+__device__ void give_up(uint32_t* err, uint32_t site) {
+  if (atomicCAS(err, 0u, 1u) == 0u) {
+    err[1] = site;
+    err[2] = blockIdx.x;
+    __threadfence();
+  }
+}
+// Bounded wait; with honor_abort a failure recorded by any CTA also ends it.
+__device__ bool wait_bar(uint32_t* err, uint32_t bar, uint32_t parity, uint32_t site, bool honor_abort = true) {
+  if (mbar_test(bar, parity)) return true;
+  const unsigned long long t0 = gtime();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_test(bar, parity)) return true;
+    if ((i & 15u) == 0u) {
+      if (honor_abort && *reinterpret_cast<volatile uint32_t*>(err) != 0u) return false;
+      if (gtime() - t0 > WAIT_NS) {
+        give_up(err, site);
+        return false;
+      }
+    }
+  }
+}
+// The same for a converged warp, with one result and every lane ordered after the phase.
+__device__ __forceinline__ bool wait_bar_warp(uint32_t* err, uint32_t bar, uint32_t parity, uint32_t site) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(err, bar, parity, site) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  if (ok) (void)mbar_test(bar, parity);
+  return ok != 0;
+}
+
+// Descriptor of an MN-major tile: blocks of 64 elements by 64 contraction
+// rows (128 bytes each, 128-byte swizzle), 8-row groups 1024 bytes apart,
+// the next 64 elements 8192 bytes on.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  uint64_t v = smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
+  return v | (static_cast<uint64_t>(8192 >> 4) << 16);
+}
+
+struct TileAt {
+  int q, row, col;
+};
+// Tile t of the launch: products in order; within one, groups of 8 row tiles
+// are swept column by column, rows fastest, so that the tiles in flight share
+// their B tiles and a group's A rows stay in L2 over the sweep.
+__device__ __forceinline__ TileAt tile_at(const Args& p, int t) {
+  TileAt o;
+  o.q = 0;
+  while (t >= p.q[o.q].tiles) t -= p.q[o.q++].tiles;
+  const Prob& q = p.q[o.q];
+  const int cols = q.tiles / q.tiles_m;
+  const int grp = t / (8 * cols), first = grp * 8;
+  const int rows = min(8, q.tiles_m - first);
+  const int in = t - grp * 8 * cols;
+  o.row = (first + in % rows) * (2 * TM);
+  o.col = in / rows * q.w;
+  return o;
+}
+
+template <int KIND, bool FP8>
+__device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_t empty0, uint32_t rank, int pair,
+                          int pairs) {
+  constexpr int KEL = FP8 ? KB : KB / 2;
+  const uint32_t full_lead = map_to_rank(full0, 0);
+  uint32_t stage = 0, phase = 0, armed = 0;
+  bool ok = true;
+  for (int t = pair; ok && t < p.total; t += pairs) {
+    const TileAt T = tile_at(p, t);
+    const Prob& q = p.q[T.q];
+    const int hb = KIND == EPI_GATED ? q.w : q.w / 2;  // B rows this CTA loads
+    const int a0 = T.row + TM * static_cast<int>(rank);
+    const int b0 = KIND == EPI_GATED ? T.col : T.col + hb * static_cast<int>(rank);
+    const int b_boxes = (hb + 63) / 64;
+    const uint32_t bytes = 2u * (A_BYTES + (q.b_mn ? b_boxes * 8192u : static_cast<uint32_t>(hb) * KB));
+    const int kb = q.kb, a_mn = q.a_mn, b_mn = q.b_mn, kb_seg = q.kb_seg;
+    int seg = 0, kk = 0;
+    for (int i = 0; i < kb; ++i) {
+      const uint32_t eb = empty0 + 8u * stage;
+      if (!mbar_test(eb, phase ^ 1u) && !wait_bar(p.err, eb, phase ^ 1u, S_EMPTY)) {
+        ok = false;
+        break;
+      }
+      if (rank == 0) mbar_expect_tx(full0 + 8u * stage, bytes);
+      ++armed;
+      const uint32_t sa = sbase + stage * STAGE, sb = sa + A_BYTES, fb = full_lead + 8u * stage;
+      const CUtensorMap* ma = &q.a[seg];
+      const CUtensorMap* mb = &q.b[KIND == EPI_GATED ? rank : seg];
+      const int kx = kk * KEL;
+      if (a_mn) {
+        tma_load_2d_pair(sa, ma, fb, a0, kx);
+        tma_load_2d_pair(sa + 8192, ma, fb, a0 + 64, kx);
+      } else {
+        tma_load_2d_pair(sa, ma, fb, kx, a0);
+      }
+      if (b_mn) {
+        for (int j = 0; j < b_boxes; ++j) tma_load_2d_pair(sb + 8192u * j, mb, fb, b0 + 64 * j, kx);
+      } else {
+        tma_load_2d_pair(sb, mb, fb, kx, b0);
+      }
+      if (++kk == kb_seg) kk = 0, ++seg;
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+  }
+  if (!ok) {  // loads in flight must land before the CTA gives up its shared memory
+    if (rank == 0) {
+      for (uint32_t j = armed > STAGES ? armed - STAGES : 0u; j < armed; ++j)
+        wait_bar(p.err, full0 + 8u * (j % STAGES), (j / STAGES) & 1u, S_DRAIN, false);
+    } else if (armed > 0) {  // they signal the even CTA's barriers
+      const unsigned long long t0 = gtime();
+      while (gtime() - t0 < 200000ull) __nanosleep(1000);
+    }
+  }
+}
+
+template <int KIND, bool FP8>
+__device__ void mma_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t full0, uint32_t empty0,
+                         uint32_t tfull0, uint32_t tempty0, uint32_t drain, int pair, int pairs) {
+  uint32_t stage = 0, phase = 0, ul = 0;
+  bool ok = true;
+  for (int t = pair; ok && t < p.total; t += pairs, ++ul) {
+    const Prob& q = p.q[tile_at(p, t).q];
+    const uint32_t acc = ul & 1u;
+    const int a_mn = q.a_mn, b_mn = q.b_mn, kb = q.kb;
+    const uint32_t idesc = idesc_n(make_idesc(FP8, 2 * TM), KIND == EPI_GATED ? 2 * q.w : q.w) |
+                           (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+    const uint64_t da0 = a_mn ? desc_mn(sbase) : smem_desc_sw128(sbase);
+    const uint64_t db0 = b_mn ? desc_mn(sbase + A_BYTES) : smem_desc_sw128(sbase + A_BYTES);
+    const uint64_t step_a = a_mn ? 128u : 2u, step_b = b_mn ? 128u : 2u;
+    if (!wait_bar_warp(p.err, tempty0 + 8u * acc, ((ul >> 1) & 1u) ^ 1u, S_TEMPTY)) {
+      ok = false;
+      break;
+    }
+    tc_fence_after();
+    const uint32_t d = tmem + acc * TN;
+    for (int i = 0; i < kb; ++i) {
+      if (!wait_bar_warp(p.err, full0 + 8u * stage, phase, S_FULL)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t off = static_cast<uint64_t>(STAGE >> 4) * stage;
+      mma_kblock<2, FP8>(d, da0 + off, db0 + off, idesc, i > 0 ? 1u : 0u, step_a, step_b);
+      mma_commit_cg<2>(empty0 + 8u * stage);
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+    if (!ok) break;
+    mma_commit_cg<2>(tfull0 + 8u * acc);
+  }
+  if (!ok) {  // every MMA issued must complete before tensor memory is freed
+    mma_commit_local_cg<2>(drain);
+    if ((threadIdx.x & 31) == 0) wait_bar(p.err, drain, 0u, S_DRAIN, false);
+    __syncwarp();
+  }
+}
+
+template <int ACT, int KIND>
+__device__ __forceinline__ void apply_act(float (&v)[32], const uint32_t (&u)[32], float su) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    v[j] = act_f<ACT>(v[j]);
+    if constexpr (KIND == EPI_GATED) v[j] *= __uint_as_float(u[j]) * su;
+  }
+}
+
+// The epilogue of one warp: its 32 rows (the tensor-memory lanes its number
+// allows) of every other 32-column chunk of the tile.
+template <int KIND, bool FP8>
+__device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t tfull0, uint32_t tempty0,
+                              uint32_t rank, int pair, int pairs) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, half = (warp - 2) >> 2;
+  const uint32_t ebase = sbase + OFF_EPI + (warp - 2) * 2 * BOX;
+  const float s0 = FP8 ? __ldg(p.sx) * __ldg(p.sw0) : 1.0f;
+  const float s1 = FP8 && KIND == EPI_GATED ? __ldg(p.sx) * __ldg(p.sw1) : 1.0f;
+  uint32_t ul = 0, nst = 0;
+  // Rounds 32 values of row `lane` to bf16 into a staging box (64-byte swizzle)
+  // and stores it.  A tensor store writes whole 16-byte groups, past the end of
+  // rows that are no multiple of them: a chunk with such an edge is written
+  // element by element.
+  auto store = [&](const OutMat* out, const float(&v)[32], int ox, int oy, const Prob& q) {
+    if (ox + CHUNK > q.N && (q.N & 7)) {
+      if (oy + lane < q.M) {
+        __nv_bfloat16* o = out->p + static_cast<int64_t>(oy + lane) * out->ld + ox;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (ox + j < q.N) o[j] = __float2bfloat16_rn(v[j]);
+      }
+      return;
+    }
+    const uint32_t buf = ebase + (nst & 1u) * BOX;
+    ++nst;
+    if (lane == 0) bulk_wait_read<1>();  // the store before last has read this buffer
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * ch + 2 * j], v[8 * ch + 2 * j + 1]);
+        h[j] = *reinterpret_cast<const uint32_t*>(&b2);
+      }
+      st_shared_v4(buf + lane * 64 + (static_cast<uint32_t>(ch ^ ((lane >> 1) & 3)) << 4), h[0], h[1], h[2], h[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&out->map, buf, ox, oy);
+      bulk_commit();
+    }
+  };
+  for (int t = pair; t < p.total; t += pairs, ++ul) {
+    const TileAt T = tile_at(p, t);
+    const Prob& q = p.q[T.q];
+    const uint32_t acc = ul & 1u;
+    if (!wait_bar_warp(p.err, tfull0 + 8u * acc, (ul >> 1) & 1u, S_TFULL)) break;
+    tc_fence_after();
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * TN;
+    const int nch = (q.w + CHUNK - 1) / CHUNK;
+    const int oy = T.row + TM * static_cast<int>(rank) + quad * 32;
+    const int64_t row = static_cast<int64_t>(oy) + lane;
+    const int last = (nch - 1 - half) / 2 * 2 + half;  // this warp's last chunk (if it has any)
+    auto release = [&] {  // the accumulator is read: hand it back to the MMA warp
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(tempty0 + 8u * acc, 0));
+    };
+    if (half >= nch) release();
+#pragma unroll 1
+    for (int c = half; c < nch; c += 2) {
+      uint32_t r[32], u[32];
+      tmem_ld32_sync(taddr + c * CHUNK, r);
+      if constexpr (KIND == EPI_GATED) tmem_ld32_sync(taddr + q.w + c * CHUNK, u);
+      if (c == last) release();
+      const int ox = T.col + c * CHUNK;
+      if (ox >= q.N || oy >= q.M) continue;  // wholly past the output's edge
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * s0;
+      if constexpr (KIND == EPI_LINEAR) {
+        if (p.bias) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (ox + j < q.N) v[j] += __bfloat162float(p.bias[ox + j]);
+        }
+        if (p.has1) store(&p.y1, v, ox, oy, q);
+      }
+      if constexpr (KIND == EPI_GATED) {
+        if (p.has1) {
+          store(&p.y1, v, ox, oy, q);
+          float uf[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) uf[j] = __uint_as_float(u[j]) * s1;
+          store(&p.y2, uf, ox, oy, q);
+        }
+      }
+      if constexpr (KIND != EPI_PLAIN) {
+        switch (p.act) {
+          case TPO_ACT_RELU: apply_act<TPO_ACT_RELU, KIND>(v, u, s1); break;
+          case TPO_ACT_GELU: apply_act<TPO_ACT_GELU, KIND>(v, u, s1); break;
+          case TPO_ACT_GELU_TANH: apply_act<TPO_ACT_GELU_TANH, KIND>(v, u, s1); break;
+          case TPO_ACT_SILU: apply_act<TPO_ACT_SILU, KIND>(v, u, s1); break;
+          default: apply_act<TPO_ACT_NONE, KIND>(v, u, s1); break;
+        }
+      }
+      if constexpr (KIND == EPI_LINEAR) {
+        if (p.residual && row < q.M) {
+          const __nv_bfloat16* res = p.residual + row * p.ldr + ox;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            // 16-byte groups that lie inside the row; the ragged last one element by element
+            if (ox + 8 * ch + 8 <= q.N) {
+              const uint4 h = *reinterpret_cast<const uint4*>(res + 8 * ch);
+              const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                v[8 * ch + 2 * j] += __uint_as_float(hw[j] << 16);
+                v[8 * ch + 2 * j + 1] += __uint_as_float(hw[j] & 0xffff0000u);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (ox + 8 * ch + j < q.N) v[8 * ch + j] += __bfloat162float(res[8 * ch + j]);
+            }
+          }
+        }
+      }
+      store(&q.y, v, ox, oy, q);
+    }
+  }
+  if (lane == 0) bulk_wait<0>();
+  __syncwarp();
+}
+
+template <int KIND, bool FP8>
+__global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_constant__ Args p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
+  const uint32_t full0 = sbase + OFF_BARS, empty0 = full0 + 8 * STAGES, tfull0 = empty0 + 8 * STAGES,
+                 tempty0 = tfull0 + 16, drain = tempty0 + 16;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8u * s, 1);
+      mbar_init(empty0 + 8u * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8u * a, 1);
+      mbar_init(tempty0 + 8u * a, 2 * EPI_WARPS_N);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  cluster_sync();  // the peer's barriers exist before anyone signals them
+  if (warp == 1) {
+    tmem_alloc_cg<2>(sbase + OFF_TMEM, 2 * TN);
+    tmem_relinquish_cg<2>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ld_shared_u32(sbase + OFF_TMEM);
+  grid_dep_wait();  // from here on memory may depend on the launch before
+  if (warp == 0) {
+    if (lane == 0) load_role<KIND, FP8>(p, sbase, full0, empty0, rank, pair, pairs);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) mma_role<KIND, FP8>(p, sbase, tmem, full0, empty0, tfull0, tempty0, drain, pair, pairs);
+    __syncwarp();
+  } else {
+    epilogue_role<KIND, FP8>(p, sbase, tmem, tfull0, tempty0, rank, pair, pairs);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while its peer may still use it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<2>(tmem, 2 * TN);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+// A [outer, inner] matrix with rows `ld` elements apart.
+bool encode(CUtensorMap* map, const void* base, bool fp8, int64_t inner, int64_t outer, int64_t ld, int box_inner,
+            int box_outer, CUtensorMapSwizzle sw) {
+  const int elem = fp8 ? 1 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * elem};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t estr[2] = {1, 1};
+  return g_encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// K-major: boxes of `rows` rows by one K block; MN-major: 64 contraction rows by 64 elements.
+bool encode_operand(CUtensorMap* map, const Operand& o, bool fp8, int64_t rows, int64_t K, int box_rows) {
+  if (o.mn_major) return encode(map, o.p, fp8, rows, K, o.ld, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode(map, o.p, fp8, K, rows, o.ld, fp8 ? KB : KB / 2, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool encode_out(OutMat* o, void* p, int64_t ld, int64_t M, int64_t N) {
+  o->p = static_cast<__nv_bfloat16*>(p);
+  o->ld = ld;
+  return encode(&o->map, p, false, N, M, ld, CHUNK, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+template <int KIND, bool FP8>
+cudaError_t launch_pairs(const Args& p, int pairs, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, products_kernel<KIND, FP8>, p);
+}
+
+}  // namespace
+
+cudaError_t configure_products(Machine* m) {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r) ==
+            cudaSuccess && r == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return cudaErrorNotSupported;
+  const void* fns[] = {reinterpret_cast<const void*>(products_kernel<EPI_PLAIN, false>),
+                       reinterpret_cast<const void*>(products_kernel<EPI_LINEAR, false>),
+                       reinterpret_cast<const void*>(products_kernel<EPI_LINEAR, true>),
+                       reinterpret_cast<const void*>(products_kernel<EPI_GATED, false>),
+                       reinterpret_cast<const void*>(products_kernel<EPI_GATED, true>)};
+  for (const void* f : fns) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+  }
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&m->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(&m->pairs, products_kernel<EPI_PLAIN, false>, &cfg);
+  if (e == cudaSuccess && m->pairs < 1) e = cudaErrorNotSupported;
+  return e;
+}
+
+cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, uint32_t* err,
+                            cudaStream_t s) {
+  Args p;
+  std::memset(&p, 0, sizeof(p));
+  p.count = count;
+  bool ok = true;
+  for (int i = 0; i < count; ++i) {
+    const Product& c = q[i];
+    Prob& o = p.q[i];
+    o.M = static_cast<int>(c.M), o.N = static_cast<int>(c.N);
+    o.w = e.kind == EPI_GATED ? TN / 2 : TN;
+    const int hb = e.kind == EPI_GATED ? o.w : o.w / 2;
+    o.tiles_m = ceil_div(c.M, 2 * TM);
+    o.tiles = o.tiles_m * ceil_div(c.N, o.w);
+    o.kb_seg = ceil_div(c.K, fp8 ? KB : KB / 2);
+    o.kb = o.kb_seg * c.terms;
+    o.a_mn = c.a[0].mn_major, o.b_mn = c.b[0].mn_major;
+    for (int t = 0; t < c.terms && ok; ++t)
+      ok = encode_operand(&o.a[t], c.a[t], fp8, c.M, c.K, TM) && encode_operand(&o.b[t], c.b[t], fp8, c.N, c.K, hb);
+    if (ok && e.kind == EPI_GATED) ok = encode_operand(&o.b[1], c.b[1], fp8, c.N, c.K, hb);
+    ok = ok && encode_out(&o.y, c.out, c.ldo, c.M, c.N);
+    p.total += o.tiles;
+  }
+  if (e.out1) ok = ok && encode_out(&p.y1, e.out1, e.ld1, q[0].M, q[0].N);
+  if (e.out2) ok = ok && encode_out(&p.y2, e.out2, e.ld2, q[0].M, q[0].N);
+  if (!ok) return cudaErrorInvalidValue;
+  p.has1 = e.out1 != nullptr;
+  p.act = e.act;
+  p.bias = static_cast<const __nv_bfloat16*>(e.bias);
+  p.residual = static_cast<const __nv_bfloat16*>(e.residual);
+  p.ldr = e.ldr;
+  p.sx = e.sx, p.sw0 = e.sw0, p.sw1 = e.sw1;
+  p.err = err;
+  const int pairs = std::min(mc.pairs, p.total);
+  switch (e.kind) {
+    case EPI_LINEAR: return fp8 ? launch_pairs<EPI_LINEAR, true>(p, pairs, s) : launch_pairs<EPI_LINEAR, false>(p, pairs, s);
+    case EPI_GATED: return fp8 ? launch_pairs<EPI_GATED, true>(p, pairs, s) : launch_pairs<EPI_GATED, false>(p, pairs, s);
+    default: return launch_pairs<EPI_PLAIN, false>(p, pairs, s);
+  }
+}
+
+}  // namespace tpo

@@ -41,21 +41,12 @@
 
 #include <type_traits>
 
+#include "ptx.h"
 #include "tpo_params.h"
 
 namespace tpo {
 
 // ------------------------------------------------------------------ helpers
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ unsigned long long gtime() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
 
 __device__ __forceinline__ bool aborted(const Params& p) {
   return *reinterpret_cast<volatile uint32_t*>(&p.words->err[0]) != 0u;
@@ -70,38 +61,6 @@ __device__ void raise_error(const Params& p, uint32_t code, uint32_t site, uint3
   }
 }
 
-// ------------------------------------------------------------------ launch order
-
-// Programmatic dependent launch: a launch that the host marks may begin its
-// set-up (barriers, tensor memory) while the launch before it on the stream is
-// still running; griddepcontrol.wait then holds the thread until that launch
-// has completed and its memory is visible, so nothing before it touches global
-// memory.  Without the mark both instructions return at once.
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" :::); }
-
-// ------------------------------------------------------------------ mbarrier
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, P;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0u;
-}
 // Bounded wait for the phase of parity `parity` to complete.  With
 // `honor_abort`, a failure recorded by any CTA also ends the wait (false).
 __device__ bool mbar_wait(const Params& p, uint32_t bar, uint32_t parity, uint32_t site, bool honor_abort) {
@@ -121,17 +80,6 @@ __device__ bool mbar_wait(const Params& p, uint32_t bar, uint32_t parity, uint32
 // mbar_wait whose completion acquires at cluster scope: arrivals from the
 // other CTA of a pair (with release at cluster scope) order that CTA's earlier
 // writes before this thread's later accesses.
-__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, P;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0u;
-}
 __device__ bool mbar_wait_cluster(const Params& p, uint32_t bar, uint32_t parity, uint32_t site) {
   if (mbar_test_cluster(bar, parity)) return true;
   const unsigned long long t0 = gtime();
@@ -168,283 +116,6 @@ __device__ __forceinline__ bool mbar_wait_warp(const Params& p, uint32_t bar, ui
   if (ok) (void)mbar_test(bar, parity);
   return ok != 0;
 }
-__device__ __forceinline__ void fence_barrier_init() {
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-
-// ------------------------------------------------------------------ bulk copies / TMA
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-// A operands: [inner K, rows, slot] maps, so a tile's rows never run into the
-// next slot (rows past a slot's end read as zeros).
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-// Outputs: [m, rows, slot] maps; the store writes only the part of the box
-// inside the slot and inside m.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void bulk_wait() {
-  asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void fence_proxy_async_global() {
-  asm volatile("fence.proxy.async.global;" ::: "memory");
-}
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// 16-byte global accesses under an L2 cache policy.
-__device__ __forceinline__ void st_global_v4_keep(uint4* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
-                                                  uint64_t pol) {
-  asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(a), "r"(b), "r"(c),
-               "r"(d), "l"(pol)
-               : "memory");
-}
-__device__ __forceinline__ void ld_global_v4_keep(const uint4* p, uint32_t (&h)[4], uint64_t pol) {
-  asm volatile("ld.global.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;"
-               : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-               : "l"(p), "l"(pol)
-               : "memory");
-}
-
-// ------------------------------------------------------------------ release / acquire
-
-__device__ __forceinline__ void red_add_release(uint32_t* ptr, uint32_t v) {
-  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(ptr), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t atom_add_release(uint32_t* ptr, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.release.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(ptr), "r"(v) : "memory");
-  return old;
-}
-__device__ __forceinline__ void st_release(uint32_t* ptr, uint32_t v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(ptr), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* ptr) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ptr) : "memory");
-  return v;
-}
-
-// ------------------------------------------------------------------ tcgen05
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Shared-memory matrix descriptor for a K-major operand tile written by TMA with
-// the 128-byte swizzle: rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);  // start address, 16-byte units
-  d |= static_cast<uint64_t>(1) << 16;                 // leading byte offset (unused when swizzled)
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;         // stride byte offset: one 8-row atom
-  d |= static_cast<uint64_t>(1) << 46;                 // descriptor version (tcgen05)
-  d |= static_cast<uint64_t>(2) << 61;                 // swizzle mode: 128 bytes
-  return d;
-}
-
-// Instruction descriptor: dense, fp32 accumulator, K-major A and B,
-// A/B bf16 (kind::f16) or e4m3 (kind::f8f6f4), M = tile rows; the tile's
-// width N (a multiple of 32 up to BN) is added per tile with idesc_n.
-__host__ __device__ constexpr uint32_t make_idesc(bool fp8, int m) {
-  return (1u << 4) | ((fp8 ? 0u : 1u) << 7) | ((fp8 ? 0u : 1u) << 10) | (static_cast<uint32_t>(m >> 4) << 24);
-}
-__device__ __forceinline__ uint32_t idesc_n(uint32_t idesc, int n) {
-  return idesc | (static_cast<uint32_t>(n >> 3) << 17);
-}
-
-// Loads 32 columns of the warp's 32 tensor-memory lanes and waits for them in
-// one statement: the compiler never sees the registers before the data landed
-// (a separate wait would let it copy them while the load is still in flight).
-__device__ __forceinline__ void tmem_ld32_sync(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-
-__device__ __forceinline__ float round_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
-
-
-// ------------------------------------------------------------------ clusters (CTA pairs)
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Shared::cluster address of the same shared-memory offset in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// TMA load whose completion is signalled on a barrier that may live in the peer CTA.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int x,
-                                                 int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-      "%4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int x,
-                                                 int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-      "%4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-template <int CG>
-__device__ __forceinline__ void tmem_alloc_cg(uint32_t slot_smem, uint32_t ncols) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem), "r"(ncols)
-                 : "memory");
-  else
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem), "r"(ncols)
-                 : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tmem_relinquish_cg() {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  else
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-  else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-// The MMA issuer is a whole converged warp; inside each asm statement
-// elect.sync picks the one lane that issues.  (Issued from one thread of a
-// diverged warp, a tcgen05.mma took ~53 cycles of that thread and a K block's
-// four ~213, against ~73 for the four from a converged warp: with the stage
-// test and commit around them the single thread needed ~450 cycles per K
-// block, more than the tensor core's 384 at N = 192 or 256 at N = 128.)
-#define TPO_MMA_KBLOCK(CGS, KIND)                                                                         \
-  asm volatile("{\n\t.reg .pred E, A, T;\n\t.reg .b32 r;\n\t"                                              \
-               "setp.ne.b32 A, %4, 0;\n\tsetp.ne.b32 T, %5, 0;\n\t"                                        \
-               "elect.sync r|E, 0xffffffff;\n\t"                                                          \
-               "@E tcgen05.mma.cta_group::" CGS ".kind::" KIND " [%0], %1, %2, %3, A;\n\t"                 \
-               "@E tcgen05.mma.cta_group::" CGS ".kind::" KIND " [%0], %6, %7, %3, T;\n\t"                 \
-               "@E tcgen05.mma.cta_group::" CGS ".kind::" KIND " [%0], %8, %9, %3, T;\n\t"                 \
-               "@E tcgen05.mma.cta_group::" CGS ".kind::" KIND " [%0], %10, %11, %3, T;\n\t}" ::"r"(d),    \
-               "l"(a), "l"(b), "r"(idesc), "r"(acc0), "r"(1u), "l"(a + 2u), "l"(b + 2u), "l"(a + 4u),     \
-               "l"(b + 4u), "l"(a + 6u), "l"(b + 6u))
-// One 128-byte K block: four MMAs of K = 32 bytes (descriptor start addresses
-// 32 bytes apart); acc0 = 0 overwrites the accumulator with the first.
-// CG = 2 issues the 2-SM form (M = 256 over the pair).
-template <int CG, bool FP8>
-__device__ __forceinline__ void mma_kblock(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc0) {
-  if constexpr (CG == 1) {
-    if constexpr (FP8)
-      TPO_MMA_KBLOCK("1", "f8f6f4");
-    else
-      TPO_MMA_KBLOCK("1", "f16");
-  } else {
-    if constexpr (FP8)
-      TPO_MMA_KBLOCK("2", "f8f6f4");
-    else
-      TPO_MMA_KBLOCK("2", "f16");
-  }
-}
-#undef TPO_MMA_KBLOCK
-// Arrive on `bar` (same offset in every CTA of the group) once all prior MMAs
-// completed; a whole converged warp executes it, one elected lane commits.
-template <int CG>
-__device__ __forceinline__ void mma_commit_cg(uint32_t bar) {
-  if constexpr (CG == 1) {
-    asm volatile(
-        "{\n\t.reg .pred E;\n\t.reg .b32 r;\n\telect.sync r|E, 0xffffffff;\n\t"
-        "@E tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-        : "memory");
-  } else {
-    const uint16_t mask = 0x3;
-    asm volatile(
-        "{\n\t.reg .pred E;\n\t.reg .b32 r;\n\telect.sync r|E, 0xffffffff;\n\t"
-        "@E tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-            bar),
-        "h"(mask)
-        : "memory");
-  }
-}
-// Commit that arrives on this CTA's barrier only (whole warp, one elected lane).
-template <int CG>
-__device__ __forceinline__ void mma_commit_local_cg(uint32_t bar) {
-  if constexpr (CG == 1)
-    mma_commit_cg<1>(bar);
-  else
-    asm volatile(
-        "{\n\t.reg .pred E;\n\t.reg .b32 r;\n\telect.sync r|E, 0xffffffff;\n\t"
-        "@E tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-        : "memory");
-}
-
 // ------------------------------------------------------------------ tile schedule
 
 struct Tile {
