@@ -134,7 +134,7 @@ tpo_status launched(cudaError_t e) { return e == cudaSuccess ? TPO_OK : cuda_fai
 
 int64_t need_linear_bwd(int64_t n, int64_t m) { return n * ws_pitch(m) * 2; }
 int64_t need_gated_bwd(int64_t n, int64_t m) { return 2 * n * ws_pitch(m) * 2; }
-int64_t need_norm_bwd(int64_t, int64_t) { return 0; }
+int64_t need_norm_bwd(int64_t n, int64_t k) { return (n < tpo::NORM_PARTS ? n : tpo::NORM_PARTS) * 8 * k; }
 
 tpo_status zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, cudaStream_t s) {
   if (!p) return TPO_OK;
@@ -271,12 +271,13 @@ tpo_status tpo_layer_norm_bwd(tpo_block* b, int64_t n, int64_t k, int dtype, int
     if (tpo_status st = check_vec("gamma, dgamma and dbeta", v, welem)) return st;
   if (tpo_status st = check_vec("mean", mean, 4)) return st;
   if (tpo_status st = check_vec("rstd", rstd, 4)) return st;
-  if (tpo_status st = check_block(b, need_norm_bwd(n, k))) return st;
+  if (tpo_status st = check_block(b, dgamma || dbeta ? need_norm_bwd(n, k) : 0)) return st;
   tpo::NormArgs a{};
   a.n = n, a.k = k, a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.gamma = gamma, a.dres = dres;
   a.lddres = lddres, a.y = n > 0 ? dx : nullptr, a.ldy = lddx, a.dgamma = dgamma, a.dbeta = dbeta;
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
-  return launched(tpo::launch_norm_bwd(a, dtype, wdtype, static_cast<cudaStream_t>(stream)));
+  return launched(tpo::launch_norm_bwd(a, dtype, wdtype, reinterpret_cast<float*>(b->ws()),
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 tpo_status tpo_linear(tpo_block* b, int64_t n, int64_t k, int64_t m, int dtype, const void* x, int64_t ldx,
