@@ -132,7 +132,9 @@ tpo_status check_block(const tpo_block* b, int64_t need) {
 
 tpo_status launched(cudaError_t e) { return e == cudaSuccess ? TPO_OK : cuda_fail(e, "kernel launch"); }
 
-int64_t need_linear_bwd(int64_t n, int64_t m) { return n * ws_pitch(m) * 2; }
+// dz, then the bias gradient's per-block sums
+int64_t dz_bytes(int64_t n, int64_t m) { return n * ws_pitch(m) * 2; }
+int64_t need_linear_bwd(int64_t n, int64_t m) { return dz_bytes(n, m) + tpo::act_parts(n) * m * 4; }
 int64_t need_gated_bwd(int64_t n, int64_t m) { return 2 * n * ws_pitch(m) * 2; }
 int64_t need_norm_bwd(int64_t n, int64_t k) { return (n < tpo::NORM_PARTS ? n : tpo::NORM_PARTS) * 8 * k; }
 
@@ -330,7 +332,8 @@ tpo_status tpo_linear_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act
     if (tpo_status st = check_mat(mx)) return st;
   }
   if (tpo_status st = check_vec("db", db, 2)) return st;
-  if (tpo_status st = check_block(b, act == TPO_ACT_NONE ? 0 : need_linear_bwd(n, m))) return st;
+  const bool make_dz = act != TPO_ACT_NONE && (dx || dw);
+  if (tpo_status st = check_block(b, make_dz || db ? need_linear_bwd(n, m) : 0)) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n == 0) {
     if (tpo_status st = zero_rows(dw, mdw.ld, m, k, s)) return st;
@@ -338,10 +341,10 @@ tpo_status tpo_linear_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act
   }
   const void* dz = dy;
   int64_t lddz = mdy.ld;
-  const bool make_dz = act != TPO_ACT_NONE && (dx || dw);
   if (make_dz || db) {
     void* out = make_dz ? b->ws() : nullptr;
-    const cudaError_t e = tpo::launch_act_bwd(n, m, act, dy, mdy.ld, z, mz.ld, out, ws_pitch(m), db, s);
+    const cudaError_t e = tpo::launch_act_bwd(n, m, act, dy, mdy.ld, z, mz.ld, out, ws_pitch(m),
+                                              reinterpret_cast<float*>(b->ws() + dz_bytes(n, m)), db, s);
     if (e != cudaSuccess) return launched(e);
     if (make_dz) dz = out, lddz = ws_pitch(m);
   }

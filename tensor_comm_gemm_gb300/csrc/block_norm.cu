@@ -235,31 +235,6 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a, int tpr
   }
 }
 
-// Adds the `parts` rows of part[parts][2][k] (32 columns a block, one of 32
-// slices of the rows a warp) and rounds to the weights' type.
-template <class W>
-__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, int parts, int64_t k, W* dgamma,
-                                                           W* dbeta) {
-  __shared__ float s[32][33];
-  grid_dep_launch();
-  grid_dep_wait();
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  W* out = blockIdx.y ? dbeta : dgamma;
-  if (!out) return;
-  float v = 0.0f;
-  if (c < k)
-#pragma unroll 4
-    for (int p = slice; p < parts; p += 32) v += part[(static_cast<int64_t>(p) * 2 + blockIdx.y) * k + c];
-  s[slice][lane] = v;
-  __syncthreads();
-  v = s[lane][slice];
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + slice;
-  if (lane == 0 && o < k) put(out + o, v);
-}
-
 // ------------------------------------------------------------------ long rows
 
 __device__ float block_sum(float v, float* part) {
@@ -437,9 +412,7 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, int wdtype, float* par
         e = launch_pdl(norm_long_dx_kernel<T, W>, dim3(static_cast<unsigned>(a.n)), dim3(1024), 0, s, a);
     }
     if (e == cudaSuccess && wants)
-      e = launch_pdl(norm_reduce_kernel<W>, dim3(static_cast<unsigned>((a.k + 31) / 32), 2), dim3(1024), 0, s,
-                     static_cast<const float*>(part), parts, a.k, static_cast<W*>(a.dgamma),
-                     static_cast<W*>(a.dbeta));
+      e = launch_column_sums(part, parts, 2, a.k, a.dgamma, a.dbeta, wdtype, s);
     return e;
   });
 }

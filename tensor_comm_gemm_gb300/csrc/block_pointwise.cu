@@ -1,12 +1,20 @@
-// Pointwise parts of the backward passes: the gradient of the pre-activations
-// and its column sums, first form.
+// Pointwise parts of the backward passes (sm_103a): the gradient of the
+// pre-activations, with the bias gradient's column sums, and the addition of
+// per-block column sums.
+//
+// All are bound by memory: a thread takes eight consecutive columns (16 bytes
+// of bf16) of a row at a time.
+
+#include <algorithm>
 
 #include <cuda_bf16.h>
 
 #include <type_traits>
 
-#include "block.h"
 #include "act.h"
+#include "block.h"
+#include "pdl.h"
+#include "ptx.h"
 
 namespace tpo {
 
@@ -14,59 +22,158 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-// One thread per column, rows in order: the bias gradient's sum is fp32, before dz is rounded.
-template <int ACT>
-__global__ void act_bwd_kernel(int64_t n, int64_t m, const bf16* dy, int64_t lddy, const bf16* z, int64_t ldz,
-                               bf16* dz, int64_t ldo, bf16* db) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (j >= m) return;
-  float sum = 0.0f;
-  for (int64_t i = 0; i < n; ++i) {
-    float v = __bfloat162float(dy[i * lddy + j]);
-    if constexpr (ACT != TPO_ACT_NONE) v *= act_grad_f<ACT>(__bfloat162float(z[i * ldz + j]));
-    if (dz) dz[i * ldo + j] = __float2bfloat16_rn(v);
-    sum += v;
+// Columns [c, c + 8) of a row of m elements as fp32 (0 past its end); p is 16-byte aligned.
+__device__ __forceinline__ void load8(const bf16* p, int64_t c, int64_t m, float (&v)[8]) {
+  if (c + 8 <= m) {
+    const uint4 h = *reinterpret_cast<const uint4*>(p + c);
+    const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < m ? __bfloat162float(p[c + j]) : 0.0f;
   }
-  if (db) db[j] = __float2bfloat16_rn(sum);
+}
+// Rounds eight values to bf16 into a workspace row, whose pitch covers whole groups of eight.
+__device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
+  uint32_t h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    h[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// Block (x, y): columns [256 x, 256 x + 256) of the rows 8 y + w + 8 i gridDim.y,
+// warp w.  dz is stored if wanted; with `part`, the sums over the block's rows
+// (fp32, before dz is rounded) go to part[y][m].
+template <int ACT>
+__global__ void __launch_bounds__(256) act_bwd_kernel(int64_t n, int64_t m, const bf16* dy, int64_t lddy,
+                                                      const bf16* z, int64_t ldz, bf16* dz, int64_t ldo,
+                                                      float* part) {
+  __shared__ float red[8][256];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + lane * 8;
+  float sum[8] = {};
+  if (c < m)
+#pragma unroll 4
+    for (int64_t i = static_cast<int64_t>(blockIdx.y) * 8 + warp; i < n; i += static_cast<int64_t>(gridDim.y) * 8) {
+      float d[8];
+      load8(dy + i * lddy, c, m, d);
+      if constexpr (ACT != TPO_ACT_NONE) {
+        float v[8];
+        load8(z + i * ldz, c, m, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] *= act_grad_f<ACT>(v[j]);
+      }
+      if (dz) store8(dz + i * ldo + c, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += d[j];
+    }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[warp][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (o >= m) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) v += red[w][threadIdx.x];
+  part[static_cast<int64_t>(blockIdx.y) * m + o] = v;
 }
 
 template <int ACT>
-__global__ void gated_act_bwd_kernel(int64_t n, int64_t m, const bf16* dh, int64_t lddh, const bf16* g, int64_t ldg,
-                                     const bf16* u, int64_t ldu, bf16* dg, bf16* du, int64_t ldo) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t i = blockIdx.y;
-  if (j >= m) return;
-  const float d = __bfloat162float(dh[i * lddh + j]), gv = __bfloat162float(g[i * ldg + j]),
-              uv = __bfloat162float(u[i * ldu + j]);
-  dg[i * ldo + j] = __float2bfloat16_rn(d * uv * act_grad_f<ACT>(gv));
-  du[i * ldo + j] = __float2bfloat16_rn(d * act_f<ACT>(gv));
+__global__ void __launch_bounds__(256) gated_act_bwd_kernel(int64_t n, int64_t m, const bf16* dh, int64_t lddh,
+                                                            const bf16* g, int64_t ldg, const bf16* u, int64_t ldu,
+                                                            bf16* dg, bf16* du, int64_t ldo) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int64_t per_row = (m + 7) / 8, idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (idx >= n * per_row) return;
+  const int64_t i = idx / per_row, c = (idx - i * per_row) * 8;
+  float d[8], gv[8], uv[8], og[8], ou[8];
+  load8(dh + i * lddh, c, m, d);
+  load8(g + i * ldg, c, m, gv);
+  load8(u + i * ldu, c, m, uv);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    og[j] = d[j] * uv[j] * act_grad_f<ACT>(gv[j]);
+    ou[j] = d[j] * act_f<ACT>(gv[j]);
+  }
+  store8(dg + i * ldo + c, og);
+  store8(du + i * ldo + c, ou);
+}
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// out_y[c] = sum over p of part[p][y][c], y = blockIdx.y of gridDim.y vectors of
+// `cols`: 32 columns a block, one of 32 slices of p a warp, joined by shuffles
+// in a fixed order.
+template <class W>
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* part, int parts, int64_t cols, W* out0,
+                                                           W* out1) {
+  __shared__ float s[32][33];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  W* out = blockIdx.y ? out1 : out0;
+  if (!out) return;
+  float v = 0.0f;
+  if (c < cols)
+#pragma unroll 4
+    for (int p = slice; p < parts; p += 32) v += part[(static_cast<int64_t>(p) * gridDim.y + blockIdx.y) * cols + c];
+  s[slice][lane] = v;
+  __syncthreads();
+  v = s[lane][slice];
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + slice;
+  if (lane == 0 && o < cols) put(out + o, v);
 }
 
 }  // namespace
 
+cudaError_t launch_column_sums(const float* part, int parts, int vectors, int64_t cols, void* out0, void* out1,
+                               int dtype, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((cols + 31) / 32), vectors);
+  if (dtype == TPO_F32)
+    return launch_pdl(column_sums_kernel<float>, grid, dim3(1024), 0, s, part, parts, cols, static_cast<float*>(out0),
+                      static_cast<float*>(out1));
+  return launch_pdl(column_sums_kernel<bf16>, grid, dim3(1024), 0, s, part, parts, cols, static_cast<bf16*>(out0),
+                    static_cast<bf16*>(out1));
+}
+
 cudaError_t launch_act_bwd(int64_t n, int64_t m, int act, const void* dy, int64_t lddy, const void* z, int64_t ldz,
-                           void* dz, int64_t ldo, void* db, cudaStream_t s) {
-  return with_act(act, [&](auto a) {
-    act_bwd_kernel<decltype(a)::value><<<static_cast<unsigned>((m + 127) / 128), 128, 0, s>>>(
-        n, m, static_cast<const bf16*>(dy), lddy, static_cast<const bf16*>(z), ldz, static_cast<bf16*>(dz), ldo,
-        static_cast<bf16*>(db));
-    return cudaGetLastError();
+                           void* dz, int64_t ldo, float* part, void* db, cudaStream_t s) {
+  // about eight blocks per SM in all, at most ACT_PARTS over the rows
+  const int64_t cols = (m + 255) / 256;
+  const int64_t want = std::max<int64_t>(1, 1216 / cols);
+  const int parts = static_cast<int>(std::min<int64_t>({(n + 7) / 8, want, ACT_PARTS}));
+  cudaError_t e = with_act(act, [&](auto a) {
+    return launch_pdl(act_bwd_kernel<decltype(a)::value>, dim3(static_cast<unsigned>(cols), parts), dim3(256), 0, s, n,
+                      m, static_cast<const bf16*>(dy), lddy, static_cast<const bf16*>(z), ldz, static_cast<bf16*>(dz),
+                      ldo, db ? part : nullptr);
   });
+  if (e == cudaSuccess && db) e = launch_column_sums(part, parts, 1, m, db, nullptr, TPO_BF16, s);
+  return e;
 }
 
 cudaError_t launch_gated_act_bwd(int64_t n, int64_t m, int act, const void* dh, int64_t lddh, const void* g,
                                  int64_t ldg, const void* u, int64_t ldu, void* dg, void* du, int64_t ldo,
                                  cudaStream_t s) {
   return with_act(act, [&](auto a) {
-    for (int64_t i0 = 0; i0 < n; i0 += 65535) {  // grid.y holds 65535 rows
-      const int64_t rows = n - i0 < 65535 ? n - i0 : 65535;
-      gated_act_bwd_kernel<decltype(a)::value>
-          <<<dim3(static_cast<unsigned>((m + 127) / 128), static_cast<unsigned>(rows)), 128, 0, s>>>(
-              rows, m, static_cast<const bf16*>(dh) + i0 * lddh, lddh, static_cast<const bf16*>(g) + i0 * ldg, ldg,
-              static_cast<const bf16*>(u) + i0 * ldu, ldu, static_cast<bf16*>(dg) + i0 * ldo,
-              static_cast<bf16*>(du) + i0 * ldo, ldo);
-    }
-    return cudaGetLastError();
+    return launch_pdl(gated_act_bwd_kernel<decltype(a)::value>,
+                      dim3(static_cast<unsigned>((n * ((m + 7) / 8) + 255) / 256)), dim3(256), 0, s, n, m,
+                      static_cast<const bf16*>(dh), lddh, static_cast<const bf16*>(g), ldg,
+                      static_cast<const bf16*>(u), ldu, static_cast<bf16*>(dg), static_cast<bf16*>(du), ldo);
   });
 }
 
