@@ -447,6 +447,18 @@ tpo_block* tpo_block_create(int64_t workspace_bytes);
  * still run: the release waits for the device).  NULL is a no-op. */
 tpo_status tpo_block_destroy(tpo_block* blk);
 
+/*
+ * Options (integers, 0 by default) that choose how the products run; results
+ * agree within the rounding of fp32 sums.
+ *   "path"   0 by rule; 1 CTA pairs (256-row tiles); 2 clusters that cut the
+ *            contraction (for few rows), where a product has that form: the
+ *            forward products and dx
+ *   "split"  CTAs of such a cluster, 1..8; 0 by rule
+ * Unknown keys or values out of range: TPO_ERR_INVALID_ARG.
+ */
+tpo_status tpo_block_set_opt(tpo_block* blk, const char* key, int64_t value);
+tpo_status tpo_block_get_opt(tpo_block* blk, const char* key, int64_t* value);
+
 /* Wait for the work on `stream`, read and clear the handle's error word. */
 tpo_status tpo_block_sync_status(tpo_block* blk, void* stream);
 

@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <cstring>
 
 #include "block.h"
 
@@ -40,6 +41,7 @@ struct tpo_block {
   uint8_t* mem = nullptr;  // error words, then the workspace
   int64_t ws_bytes = 0;
   tpo::Machine machine{};
+  int64_t path = 0, split = 0;  // options
   uint32_t* err() const { return reinterpret_cast<uint32_t*>(mem); }
   uint8_t* ws() const { return mem + kErrBytes; }
 };
@@ -130,6 +132,14 @@ tpo_status check_block(const tpo_block* b, int64_t need) {
   return TPO_OK;
 }
 
+// One product on CTA pairs or, with few rows, on clusters that cut the contraction.
+cudaError_t run_product(tpo_block* b, const tpo::Product& q, bool fp8, const tpo::Epi& e, cudaStream_t s) {
+  tpo::SplitPlan plan;
+  if (tpo::use_split(b->machine, q, fp8, e.kind == tpo::EPI_GATED, b->path, b->split, &plan))
+    return tpo::launch_split(q, plan, fp8, e, b->err(), s);
+  return tpo::launch_products(b->machine, &q, 1, fp8, e, b->err(), s);
+}
+
 tpo_status launched(cudaError_t e) { return e == cudaSuccess ? TPO_OK : cuda_fail(e, "kernel launch"); }
 
 // dz, then the bias gradient's per-block sums
@@ -184,6 +194,7 @@ tpo_block* tpo_block_create(int64_t workspace_bytes) {
     return nullptr;
   }
   e = tpo::configure_products(&b->machine);
+  if (e == cudaSuccess) e = tpo::configure_split();
   if (e != cudaSuccess) {
     cuda_fail(e, "kernel configuration");
     delete b;
@@ -212,6 +223,26 @@ tpo_status tpo_block_destroy(tpo_block* b) {
   if (!b) return TPO_OK;
   cudaFree(b->mem);  // waits for the device's pending work
   delete b;
+  return TPO_OK;
+}
+
+tpo_status tpo_block_set_opt(tpo_block* b, const char* key, int64_t value) {
+  if (!key) return fail(TPO_ERR_INVALID_ARG, "NULL option key");
+  const bool path = std::strcmp(key, "path") == 0;
+  if (!path && std::strcmp(key, "split") != 0) return fail(TPO_ERR_INVALID_ARG, "unknown option '%s'", key);
+  if (value < 0 || value > (path ? 2 : 8))
+    return fail(TPO_ERR_INVALID_ARG, "option '%s'=%lld outside [0, %d]", key, (long long)value, path ? 2 : 8);
+  if (!b) return fail(TPO_ERR_INVALID_ARG, "NULL block handle");
+  (path ? b->path : b->split) = value;
+  return TPO_OK;
+}
+
+tpo_status tpo_block_get_opt(tpo_block* b, const char* key, int64_t* value) {
+  if (!key || !value) return fail(TPO_ERR_INVALID_ARG, "NULL option key or value");
+  const bool path = std::strcmp(key, "path") == 0;
+  if (!path && std::strcmp(key, "split") != 0) return fail(TPO_ERR_INVALID_ARG, "unknown option '%s'", key);
+  if (!b) return fail(TPO_ERR_INVALID_ARG, "NULL block handle");
+  *value = path ? b->path : b->split;
   return TPO_OK;
 }
 
@@ -307,8 +338,7 @@ tpo_status tpo_linear(tpo_block* b, int64_t n, int64_t k, int64_t m, int dtype, 
   e.kind = tpo::EPI_LINEAR, e.act = act, e.bias = bias, e.residual = residual, e.ldr = mr.ld;
   e.out1 = z, e.ld1 = mz.ld, e.sx = d_scale_inv_x, e.sw0 = d_scale_inv_w;
   const tpo::Product q{{{x, mx.ld, false}}, {{w, mw.ld, false}}, 1, n, m, k, y, my.ld};
-  return launched(tpo::launch_products(b->machine, &q, 1, dtype == TPO_FP8_E4M3, e, b->err(),
-                                       static_cast<cudaStream_t>(stream)));
+  return launched(run_product(b, q, dtype == TPO_FP8_E4M3, e, static_cast<cudaStream_t>(stream)));
 }
 
 tpo_status tpo_linear_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act, const void* dy, int64_t lddy,
@@ -351,9 +381,15 @@ tpo_status tpo_linear_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act
   tpo::Product q[2];
   int count = 0;
   if (dx) q[count++] = {{{dz, lddz, false}}, {{w, mw.ld, true}}, 1, n, k, m, dx, mdx.ld};
+  if (dx) {
+    tpo::SplitPlan plan;
+    if (tpo::use_split(b->machine, q[0], false, false, b->path, b->split, &plan)) {
+      if (tpo_status st = launched(tpo::launch_split(q[0], plan, false, tpo::Epi(), b->err(), s))) return st;
+      count = 0;
+    }
+  }
   if (dw) q[count++] = {{{dz, lddz, true}}, {{x, mx.ld, true}}, 1, m, k, n, dw, mdw.ld};
-  if (count == 0) return TPO_OK;
-  return launched(tpo::launch_products(b->machine, q, count, false, tpo::Epi(), b->err(), s));
+  return count ? launched(tpo::launch_products(b->machine, q, count, false, tpo::Epi(), b->err(), s)) : TPO_OK;
 }
 
 tpo_status tpo_gated(tpo_block* b, int64_t n, int64_t k, int64_t m, int dtype, const void* x, int64_t ldx,
@@ -381,8 +417,7 @@ tpo_status tpo_gated(tpo_block* b, int64_t n, int64_t k, int64_t m, int dtype, c
   e.kind = tpo::EPI_GATED, e.act = act, e.out1 = g, e.ld1 = mog.ld, e.out2 = u, e.ld2 = mou.ld;
   e.sx = d_scale_inv_x, e.sw0 = d_scale_inv_wg, e.sw1 = d_scale_inv_wu;
   const tpo::Product q{{{x, mx.ld, false}}, {{wg, mg.ld, false}, {wu, mu.ld, false}}, 1, n, m, k, h, mh.ld};
-  return launched(tpo::launch_products(b->machine, &q, 1, dtype == TPO_FP8_E4M3, e, b->err(),
-                                       static_cast<cudaStream_t>(stream)));
+  return launched(run_product(b, q, dtype == TPO_FP8_E4M3, e, static_cast<cudaStream_t>(stream)));
 }
 
 tpo_status tpo_gated_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act, const void* dh, int64_t lddh,
@@ -424,11 +459,18 @@ tpo_status tpo_gated_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act,
   int count = 0;
   if (dx)
     q[count++] = {{{dg, ld, false}, {du, ld, false}}, {{wg, mwg.ld, true}, {wu, mwu.ld, true}}, 2, n, k, m, dx, mdx.ld};
+  if (dx) {
+    tpo::SplitPlan plan;
+    if (tpo::use_split(b->machine, q[0], false, false, b->path, b->split, &plan)) {
+      if (tpo_status st = launched(tpo::launch_split(q[0], plan, false, tpo::Epi(), b->err(), s))) return st;
+      count = 0;
+    }
+  }
   if (dwg) {
     q[count++] = {{{dg, ld, true}}, {{x, mx.ld, true}}, 1, m, k, n, dwg, mdwg.ld};
     q[count++] = {{{du, ld, true}}, {{x, mx.ld, true}}, 1, m, k, n, dwu, mdwu.ld};
   }
-  return launched(tpo::launch_products(b->machine, q, count, false, tpo::Epi(), b->err(), s));
+  return count ? launched(tpo::launch_products(b->machine, q, count, false, tpo::Epi(), b->err(), s)) : TPO_OK;
 }
 
 }  // extern "C"

@@ -52,6 +52,19 @@ cudaError_t configure_products(Machine* m);
 cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, uint32_t* err,
                             cudaStream_t s);
 
+// The same for one product with few rows (M tokens): S CTAs of a cluster cut the contraction.
+struct SplitPlan {
+  int nt = 0;       // tokens of a tile
+  int split = 1;    // CTAs of a cluster
+  int stages = 0, per_sm = 0;
+};
+cudaError_t configure_split();
+SplitPlan plan_split(const Machine& mc, int64_t features, int64_t tokens, int64_t K, int terms, bool fp8, bool gated);
+// Whether the product takes that form (path 0: by rule, 1: never, 2: always; split 0: by rule), and its plan.
+bool use_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t path, int64_t split, SplitPlan* plan);
+cudaError_t launch_split(const Product& q, const SplitPlan& plan, bool fp8, const Epi& e, uint32_t* err,
+                         cudaStream_t s);
+
 struct NormArgs {
   int64_t n, k;
   const void *x, *dy, *dres, *gamma, *beta;

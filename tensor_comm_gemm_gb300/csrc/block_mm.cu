@@ -18,12 +18,10 @@
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
-
-#include <cudaTypedefs.h>
 
 #include "act.h"
 #include "block.h"
+#include "block_dev.h"
 #include "ptx.h"
 
 namespace tpo {
@@ -32,7 +30,6 @@ namespace {
 
 constexpr int TM = 128;              // rows of one CTA; a pair's tile has 256
 constexpr int TN = 256;              // most columns of a tile (accumulator width)
-constexpr int KB = 128;              // bytes of contraction elements per K block
 constexpr int A_BYTES = TM * KB;     // 16 KiB
 constexpr int B_BYTES = TN / 2 * KB;  // 16 KiB: half of the tile's B rows
 constexpr int STAGE = A_BYTES + B_BYTES;
@@ -47,7 +44,6 @@ constexpr int N_BARS = 2 * STAGES + 2 + 2 + 1;
 constexpr int OFF_TMEM = OFF_BARS + 8 * N_BARS;
 constexpr int SMEM = OFF_TMEM + 16 + 1024;  // and the slack to align the base
 static_assert(SMEM <= 232448, "shared memory of one CTA");
-constexpr unsigned long long WAIT_NS = 2000000000ull;
 
 // An output matrix: its map for tensor stores, and its address for ragged edges.
 struct OutMat {
@@ -75,48 +71,6 @@ struct Args {
   const float *sx, *sw0, *sw1;
   uint32_t* err;
 };
-
-enum Site : uint32_t { S_EMPTY = 1, S_FULL = 2, S_TEMPTY = 3, S_TFULL = 4, S_DRAIN = 5 };
-
-__device__ void give_up(uint32_t* err, uint32_t site) {
-  if (atomicCAS(err, 0u, 1u) == 0u) {
-    err[1] = site;
-    err[2] = blockIdx.x;
-    __threadfence();
-  }
-}
-// Bounded wait; with honor_abort a failure recorded by any CTA also ends it.
-__device__ bool wait_bar(uint32_t* err, uint32_t bar, uint32_t parity, uint32_t site, bool honor_abort = true) {
-  if (mbar_test(bar, parity)) return true;
-  const unsigned long long t0 = gtime();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_test(bar, parity)) return true;
-    if ((i & 15u) == 0u) {
-      if (honor_abort && *reinterpret_cast<volatile uint32_t*>(err) != 0u) return false;
-      if (gtime() - t0 > WAIT_NS) {
-        give_up(err, site);
-        return false;
-      }
-    }
-  }
-}
-// The same for a converged warp, with one result and every lane ordered after the phase.
-__device__ __forceinline__ bool wait_bar_warp(uint32_t* err, uint32_t bar, uint32_t parity, uint32_t site) {
-  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait_bar(err, bar, parity, site) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  if (ok) (void)mbar_test(bar, parity);
-  return ok != 0;
-}
-
-// Descriptor of an MN-major tile: blocks of 64 elements by 64 contraction
-// rows (128 bytes each, 128-byte swizzle), 8-row groups 1024 bytes apart,
-// the next 64 elements 8192 bytes on.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-  uint64_t v = smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
-  return v | (static_cast<uint64_t>(8192 >> 4) << 16);
-}
 
 struct TileAt {
   int q, row, col;
@@ -425,34 +379,11 @@ __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_const
 
 // ------------------------------------------------------------------ host side
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-// A [outer, inner] matrix with rows `ld` elements apart.
-bool encode(CUtensorMap* map, const void* base, bool fp8, int64_t inner, int64_t outer, int64_t ld, int box_inner,
-            int box_outer, CUtensorMapSwizzle sw) {
-  const int elem = fp8 ? 1 : 2;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * elem};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
-  const cuuint32_t estr[2] = {1, 1};
-  return g_encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// K-major: boxes of `rows` rows by one K block; MN-major: 64 contraction rows by 64 elements.
-bool encode_operand(CUtensorMap* map, const Operand& o, bool fp8, int64_t rows, int64_t K, int box_rows) {
-  if (o.mn_major) return encode(map, o.p, fp8, rows, K, o.ld, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-  return encode(map, o.p, fp8, K, rows, o.ld, fp8 ? KB : KB / 2, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
 bool encode_out(OutMat* o, void* p, int64_t ld, int64_t M, int64_t N) {
   o->p = static_cast<__nv_bfloat16*>(p);
   o->ld = ld;
   return encode(&o->map, p, false, N, M, ld, CHUNK, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
-
-int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 template <int KIND, bool FP8>
 cudaError_t launch_pairs(const Args& p, int pairs, cudaStream_t s) {
@@ -476,14 +407,7 @@ cudaError_t launch_pairs(const Args& p, int pairs, cudaStream_t s) {
 }  // namespace
 
 cudaError_t configure_products(Machine* m) {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r) ==
-            cudaSuccess && r == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  if (!g_encode) return cudaErrorNotSupported;
+  if (!load_encode()) return cudaErrorNotSupported;
   const void* fns[] = {reinterpret_cast<const void*>(products_kernel<EPI_PLAIN, false>),
                        reinterpret_cast<const void*>(products_kernel<EPI_LINEAR, false>),
                        reinterpret_cast<const void*>(products_kernel<EPI_LINEAR, true>),

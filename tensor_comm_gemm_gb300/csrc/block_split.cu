@@ -1,0 +1,339 @@
+// Matrix products of the block operators with few rows (sm_103a): decoding
+// steps and short prompts.
+//
+// Bound by reading the weights once, so the roles are swapped: a tile is 128
+// output features (the MMA's M: rows of w; for the gated form 64 rows of wg
+// and 64 of wu) by up to 256 tokens (its N), and the contraction is cut among
+// the S CTAs of a cluster, so that every SM streams weights even when the
+// output is small.  Each CTA runs a TMA -> tcgen05.mma pipeline over its K
+// blocks; then the fp32 accumulators go to shared memory as [token][feature],
+// and after one cluster barrier every CTA adds its share of the outputs over
+// the cluster's shared memories, in the order of the ranks, and runs the
+// epilogue on it.
+
+#include <algorithm>
+#include <cstring>
+
+#include "act.h"
+#include "block.h"
+#include "block_dev.h"
+#include "ptx.h"
+
+namespace tpo {
+
+namespace {
+
+constexpr int FT = 128;                // accumulator rows of a tile
+constexpr int A_BYTES = FT * KB;       // weights of one K block
+constexpr int MAX_STAGES = 8;
+constexpr int THREADS = 256;           // warp 0 TMA, warp 1 MMA, warps 4-7 drain; all add
+constexpr int SMEM_TAIL = 8 * (2 * MAX_STAGES + 2) + 16 + 1024;  // barriers, tensor memory slot, slack to align
+constexpr int SMEM_ONE = 232448;       // one CTA per SM
+constexpr int SMEM_TWO = 115712;       // two
+
+struct Args {
+  CUtensorMap a[2], b[2];
+  int M, N;             // features and tokens
+  int tiles_f;          // feature tiles
+  int nt;               // tokens of a tile (16 .. 256, a multiple of 16)
+  int kb_seg, kb;       // K blocks per term and in all
+  int a_mn;
+  int stages, tmem_cols;
+  int act;
+  const __nv_bfloat16 *bias, *residual;
+  __nv_bfloat16 *out, *out1, *out2;  // [tokens, features]
+  int64_t ldr, ldo, ld1, ld2;
+  const float *sx, *sw0, *sw1;
+  uint32_t* err;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float act_any(int act, float z) {
+  switch (act) {
+    case TPO_ACT_RELU: return act_f<TPO_ACT_RELU>(z);
+    case TPO_ACT_GELU: return act_f<TPO_ACT_GELU>(z);
+    case TPO_ACT_GELU_TANH: return act_f<TPO_ACT_GELU_TANH>(z);
+    case TPO_ACT_SILU: return act_f<TPO_ACT_SILU>(z);
+    default: return z;
+  }
+}
+
+// Four consecutive features of one token; p is 8-byte aligned, `count` of them exist.
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&v)[4], int count) {
+  if (count >= 4) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    for (int j = 0; j < count; ++j) p[j] = __float2bfloat16_rn(v[j]);
+  }
+}
+__device__ __forceinline__ void add4(const __nv_bfloat16* p, float (&v)[4], int count) {
+  for (int j = 0; j < 4; ++j)
+    if (j < count) v[j] += __bfloat162float(p[j]);
+}
+
+template <int KIND, bool FP8>
+__global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant__ Args p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  grid_dep_launch();
+  constexpr int KEL = FP8 ? KB : KB / 2;
+  constexpr int FEATURES = KIND == EPI_GATED ? FT / 2 : FT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t stage_bytes = A_BYTES + static_cast<uint32_t>(p.nt) * KB;
+  const uint32_t full0 = sbase + stage_bytes * p.stages, empty0 = full0 + 8 * MAX_STAGES,
+                 tfull = empty0 + 8 * MAX_STAGES, slot = tfull + 16;
+  const int S = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int tile = static_cast<int>(blockIdx.x) / S;
+  const int f0 = tile % p.tiles_f * FEATURES, t0 = tile / p.tiles_f * p.nt;
+  const int lo = static_cast<int>(static_cast<int64_t>(p.kb) * rank / S),
+            hi = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / S);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full0 + 8u * s, 1);
+      mbar_init(empty0 + 8u * s, 1);
+    }
+    mbar_init(tfull, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_cg<1>(slot, p.tmem_cols);
+    tmem_relinquish_cg<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ld_shared_u32(slot);
+  grid_dep_wait();
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, armed = 0;
+      for (int i = lo; i < hi; ++i) {
+        const uint32_t eb = empty0 + 8u * stage, fb = full0 + 8u * stage;
+        if (!mbar_test(eb, phase ^ 1u) && !wait_bar(p.err, eb, phase ^ 1u, S_EMPTY)) {
+          ok = false;
+          break;
+        }
+        mbar_expect_tx(fb, stage_bytes);
+        ++armed;
+        const int seg = i >= p.kb_seg ? 1 : 0, kx = (i - seg * p.kb_seg) * KEL;
+        const uint32_t sa = sbase + stage * stage_bytes;
+        if constexpr (KIND == EPI_GATED) {
+          tma_load_2d(sa, &p.a[0], fb, kx, f0);
+          tma_load_2d(sa + A_BYTES / 2, &p.a[1], fb, kx, f0);
+          tma_load_2d(sa + A_BYTES, &p.b[0], fb, kx, t0);
+        } else {
+          if (p.a_mn) {
+            tma_load_2d(sa, &p.a[seg], fb, f0, kx);
+            tma_load_2d(sa + A_BYTES / 2, &p.a[seg], fb, f0 + 64, kx);
+          } else {
+            tma_load_2d(sa, &p.a[seg], fb, kx, f0);
+          }
+          tma_load_2d(sa + A_BYTES, &p.b[seg], fb, kx, t0);
+        }
+        if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
+      }
+      if (!ok) {  // loads in flight must land before the CTA gives up its shared memory
+        const uint32_t n = static_cast<uint32_t>(p.stages);
+        for (uint32_t j = armed > n ? armed - n : 0u; j < armed; ++j)
+          wait_bar(p.err, full0 + 8u * (j % n), (j / n) & 1u, S_DRAIN, false);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_n(make_idesc(FP8, FT), p.nt) | (p.a_mn ? 1u << 15 : 0u);
+    const uint64_t da0 = p.a_mn ? desc_mn(sbase) : smem_desc_sw128(sbase);
+    const uint64_t db0 = smem_desc_sw128(sbase + A_BYTES);
+    const uint64_t step_a = p.a_mn ? 128u : 2u;
+    uint32_t stage = 0, phase = 0;
+    for (int i = lo; i < hi; ++i) {
+      if (!wait_bar_warp(p.err, full0 + 8u * stage, phase, S_FULL)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t off = static_cast<uint64_t>(stage_bytes >> 4) * stage;
+      mma_kblock<1, FP8>(tmem, da0 + off, db0 + off, idesc, i > lo ? 1u : 0u, step_a);
+      mma_commit_cg<1>(empty0 + 8u * stage);
+      if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
+    }
+    // also after a failure: every MMA issued must complete before tensor memory is freed
+    mma_commit_cg<1>(tfull);
+    if (!wait_bar_warp(p.err, tfull, 0, S_TFULL) && lane == 0) wait_bar(p.err, tfull, 0, S_DRAIN, false);
+    __syncwarp();
+  }
+  // ---- the accumulator, [token][feature] in fp32, over the pipeline's memory
+  const int tokens = min(p.nt, p.N - t0);
+  if (warp >= 4) {
+    if (wait_bar_warp(p.err, tfull, 0, S_TFULL)) {
+      tc_fence_after();
+      const int quad = warp & 3;
+      for (int c = 0; c < tokens; c += 32) {
+        uint32_t r[32];
+        tmem_ld32_sync(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, r);
+        const uint32_t at = sbase + static_cast<uint32_t>(c * FT + quad * 32 + lane) * 4u;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c + j < tokens) st_shared_u32(at + static_cast<uint32_t>(j * FT) * 4u, r[j]);
+      }
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<1>(tmem, p.tmem_cols);
+  }
+  // ---- sums over the cluster and the epilogue: four features of one token at a time
+  constexpr int QUADS = FEATURES / 4;
+  const float s0 = FP8 ? __ldg(p.sx) * __ldg(p.sw0) : 1.0f;
+  const float s1 = FP8 && KIND == EPI_GATED ? __ldg(p.sx) * __ldg(p.sw1) : 1.0f;
+  const bool good = *reinterpret_cast<volatile uint32_t*>(p.err) == 0u;
+  for (int i = rank * THREADS + static_cast<int>(threadIdx.x); good && i < tokens * QUADS; i += S * THREADS) {
+    const int tok = i / QUADS, fq = i % QUADS * 4;
+    const int64_t row = t0 + tok;
+    const int col = f0 + fq, count = p.M - col;
+    if (count <= 0) continue;
+    const uint32_t at = sbase + static_cast<uint32_t>(tok * FT + fq) * 4u;
+    float v[4] = {}, u[4] = {};
+    for (int s = 0; s < S; ++s) {
+      const uint32_t peer = map_to_rank(at, s);
+      const float4 x = ld_cluster_f4(peer);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      if constexpr (KIND == EPI_GATED) {
+        const float4 y = ld_cluster_f4(peer + FT / 2 * 4);
+        u[0] += y.x, u[1] += y.y, u[2] += y.z, u[3] += y.w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= s0, u[j] *= s1;
+    if constexpr (KIND == EPI_LINEAR) {
+      if (p.bias) add4(p.bias + col, v, count);
+      if (p.out1) put4(p.out1 + row * p.ld1 + col, v, count);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = act_any(p.act, v[j]);
+      if (p.residual) add4(p.residual + row * p.ldr + col, v, count);
+    }
+    if constexpr (KIND == EPI_GATED) {
+      if (p.out1) {
+        put4(p.out1 + row * p.ld1 + col, v, count);
+        put4(p.out2 + row * p.ld2 + col, u, count);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = act_any(p.act, v[j]) * u[j];
+    }
+    put4(p.out + row * p.ldo + col, v, count);
+  }
+  cluster_sync();  // no CTA leaves while a peer reads its shared memory
+}
+
+template <int KIND, bool FP8>
+cudaError_t launch_split_as(const Args& p, int tiles, int S, int smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, split_kernel<KIND, FP8>, p);
+}
+
+}  // namespace
+
+cudaError_t configure_split() {
+  const void* fns[] = {reinterpret_cast<const void*>(split_kernel<EPI_PLAIN, false>),
+                       reinterpret_cast<const void*>(split_kernel<EPI_LINEAR, false>),
+                       reinterpret_cast<const void*>(split_kernel<EPI_LINEAR, true>),
+                       reinterpret_cast<const void*>(split_kernel<EPI_GATED, false>),
+                       reinterpret_cast<const void*>(split_kernel<EPI_GATED, true>)};
+  for (const void* f : fns) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ONE);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+SplitPlan plan_split(const Machine& mc, int64_t M, int64_t N, int64_t K, int terms, bool fp8, bool gated) {
+  SplitPlan o;
+  const int kb = ceil_div(K, fp8 ? KB : KB / 2) * terms;
+  const int tiles_t = ceil_div(N, 256);
+  o.nt = ceil_div(ceil_div(N, tiles_t), 16) * 16;
+  const int64_t tiles = static_cast<int64_t>(tiles_t) * ceil_div(M, gated ? FT / 2 : FT);
+  const int stage = A_BYTES + o.nt * KB;
+  // two CTAs per SM while they hold at least three stages each
+  o.per_sm = (SMEM_TWO - SMEM_TAIL) / stage >= 3 ? 2 : 1;
+  o.stages = std::min(MAX_STAGES, ((o.per_sm == 2 ? SMEM_TWO : SMEM_ONE) - SMEM_TAIL) / stage);
+  const int64_t places = static_cast<int64_t>(mc.sms) * o.per_sm;
+  o.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, kb, places / tiles})));
+  return o;
+}
+
+bool use_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t path, int64_t split,
+               SplitPlan* plan) {
+  if (path == 1 || (path == 0 && q.M > 256)) return false;
+  *plan = plan_split(mc, q.N, q.M, q.K, q.terms, fp8, gated);
+  if (split > 0) plan->split = static_cast<int>(std::min<int64_t>(split, ceil_div(q.K, fp8 ? KB : KB / 2) * q.terms));
+  return true;
+}
+
+cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, const Epi& e, uint32_t* err,
+                         cudaStream_t s) {
+  Args p;
+  std::memset(&p, 0, sizeof(p));
+  const bool gated = e.kind == EPI_GATED;
+  // the roles are swapped: B's rows (features) are the MMA's M, A's rows (tokens) its N
+  p.M = static_cast<int>(c.N), p.N = static_cast<int>(c.M);
+  p.tiles_f = ceil_div(c.N, gated ? FT / 2 : FT);
+  p.nt = plan.nt;
+  p.kb_seg = ceil_div(c.K, fp8 ? KB : KB / 2);
+  p.kb = p.kb_seg * c.terms;
+  p.a_mn = c.b[0].mn_major;
+  p.stages = plan.stages;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < p.nt) p.tmem_cols *= 2;
+  bool ok = true;
+  for (int t = 0; t < c.terms && ok; ++t)
+    ok = encode_operand(&p.a[t], c.b[t], fp8, c.N, c.K, gated ? FT / 2 : FT) &&
+         encode_operand(&p.b[t], c.a[t], fp8, c.M, c.K, p.nt);
+  if (ok && gated) ok = encode_operand(&p.a[1], c.b[1], fp8, c.N, c.K, FT / 2);
+  if (!ok) return cudaErrorInvalidValue;
+  p.act = e.act;
+  p.bias = static_cast<const __nv_bfloat16*>(e.bias);
+  p.residual = static_cast<const __nv_bfloat16*>(e.residual);
+  p.out = static_cast<__nv_bfloat16*>(c.out);
+  p.out1 = static_cast<__nv_bfloat16*>(e.out1);
+  p.out2 = static_cast<__nv_bfloat16*>(e.out2);
+  p.ldr = e.ldr, p.ldo = c.ldo, p.ld1 = e.ld1, p.ld2 = e.ld2;
+  p.sx = e.sx, p.sw0 = e.sw0, p.sw1 = e.sw1;
+  p.err = err;
+  const int tiles = p.tiles_f * ceil_div(c.M, p.nt);
+  const int smem = p.stages * (A_BYTES + p.nt * KB) + SMEM_TAIL;
+  switch (e.kind) {
+    case EPI_LINEAR: return fp8 ? launch_split_as<EPI_LINEAR, true>(p, tiles, plan.split, smem, s)
+                                : launch_split_as<EPI_LINEAR, false>(p, tiles, plan.split, smem, s);
+    case EPI_GATED: return fp8 ? launch_split_as<EPI_GATED, true>(p, tiles, plan.split, smem, s)
+                               : launch_split_as<EPI_GATED, false>(p, tiles, plan.split, smem, s);
+    default: return launch_split_as<EPI_PLAIN, false>(p, tiles, plan.split, smem, s);
+  }
+}
+
+}  // namespace tpo

@@ -33,7 +33,7 @@ TPO_MAX_TP, TPO_MAX_ROW_CHUNKS = 16, 64
 EXPORTS = ["tpo_ctx_create", "tpo_ctx_destroy", "tpo_ag_gemm", "tpo_gemm_rs", "tpo_gemm_ar", "tpo_set_opt",
            "tpo_get_opt", "tpo_sync_status", "tpo_last_device_error", "tpo_last_error", "tpo_staging_ptr",
            "tpo_done_counters", "tpo_read_trace", "tpo_version", "tpo_ag_gemm_noalloc", "tpo_set_fp8_scales",
-           "tpo_block_workspace", "tpo_block_create", "tpo_block_destroy", "tpo_block_sync_status",
+           "tpo_block_workspace", "tpo_block_create", "tpo_block_set_opt", "tpo_block_get_opt", "tpo_block_destroy", "tpo_block_sync_status",
            "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear", "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"]
 TPO_NOALLOC_MAX_STAGING_BYTES = 32 << 20
 
@@ -85,6 +85,8 @@ def lib(path: Optional[str] = None):
     L.tpo_block_create.argtypes = [i64]
     L.tpo_block_create.restype = p
     L.tpo_block_destroy.argtypes = [p]
+    L.tpo_block_set_opt.argtypes = [p, ctypes.c_char_p, i64]
+    L.tpo_block_get_opt.argtypes = [p, ctypes.c_char_p, ctypes.POINTER(i64)]
     L.tpo_block_sync_status.argtypes = [p, p]
     L.tpo_layer_norm.argtypes = [p, i64, i64, i32, i32, p, i64, p, p, f32, p, i64, p, p, p]
     L.tpo_layer_norm_bwd.argtypes = [p, i64, i64, i32, i32, p, i64, p, i64, p, p, p, p, i64, p, i64, p, p, p]
@@ -92,7 +94,7 @@ def lib(path: Optional[str] = None):
     L.tpo_linear_bwd.argtypes = [p, i64, i64, i64, i32] + [p, i64] * 6 + [p, p]
     L.tpo_gated.argtypes = [p, i64, i64, i64, i32, p, i64, p, i64, p, i64, i32] + [p, i64] * 3 + [p] * 4
     L.tpo_gated_bwd.argtypes = [p, i64, i64, i64, i32] + [p, i64] * 9 + [p]
-    for name in ("tpo_block_destroy", "tpo_block_sync_status", "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear",
+    for name in ("tpo_block_destroy", "tpo_block_set_opt", "tpo_block_get_opt", "tpo_block_sync_status", "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear",
                  "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("tpo_ctx_destroy", "tpo_ag_gemm", "tpo_gemm_rs", "tpo_gemm_ar", "tpo_set_opt", "tpo_get_opt",
@@ -367,6 +369,16 @@ def tpo_block_create(workspace_bytes: int = 0) -> int:
 
 def tpo_block_destroy(block: int) -> None:
     _check(lib().tpo_block_destroy(block))
+
+
+def tpo_block_set_opt(block: int, key: str, value: int) -> None:
+    _check(lib().tpo_block_set_opt(block, key.encode(), int(value)))
+
+
+def tpo_block_get_opt(block: int, key: str) -> int:
+    v = ctypes.c_int64()
+    _check(lib().tpo_block_get_opt(block, key.encode(), ctypes.byref(v)))
+    return v.value
 
 
 def tpo_block_sync_status(block: int, stream=None) -> int:

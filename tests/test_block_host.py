@@ -45,6 +45,16 @@ def test_create_and_null_handles(lib):
     assert lib.tpo_block_sync_status(None, None) == INVALID
 
 
+def test_options_refuse(lib):
+    for key, value, word in ((b"path", 3, "path"), (b"path", -1, "path"), (b"split", 9, "split"), (b"other", 0, "other"),
+                             (b"path", 1, "handle")):
+        assert lib.tpo_block_set_opt(None, key, value) == INVALID
+        assert word in t.tpo_last_error()
+    assert lib.tpo_block_set_opt(None, None, 0) == INVALID
+    assert lib.tpo_block_get_opt(None, b"path", None) == INVALID
+    assert lib.tpo_block_get_opt(None, b"path", ctypes.byref(ctypes.c_int64())) == INVALID
+
+
 def linear(lib, n=4, k=16, m=8, dtype=0, x=P, ldx=16, w=P, ldw=16, bias=None, act=0, r=None, ldr=8, z=None, ldz=8,
            y=P, ldy=8, sx=None, sw=None):
     return lib.tpo_linear(None, n, k, m, dtype, x, ldx, w, ldw, bias, act, r, ldr, z, ldz, y, ldy, sx, sw, None)

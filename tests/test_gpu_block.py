@@ -33,6 +33,16 @@ def block(_built):
     t.tpo_block_destroy(b)
 
 
+@pytest.fixture(params=["rule", "pairs", "clusters", "clusters of 8"])
+def any_path(request, block):
+    """Every form of the products, whatever the rule would take."""
+    t.tpo_block_set_opt(block, "path", dict(rule=0, pairs=1).get(request.param, 2))
+    t.tpo_block_set_opt(block, "split", 8 if request.param.endswith("8") else 0)
+    yield block
+    t.tpo_block_set_opt(block, "path", 0)
+    t.tpo_block_set_opt(block, "split", 0)
+
+
 def rnd(gen, *shape, dtype=BF16, scale=1.0):
     return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(dtype)
 
@@ -97,7 +107,7 @@ SHAPES = [  # n, k, m
 
 @pytest.mark.parametrize("n,k,m", SHAPES)
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-def test_linear(block, n, k, m, dtype):
+def test_linear(any_path, block, n, k, m, dtype):
     i = SHAPES.index((n, k, m))
     g = gen_of(100 + i)
     act = R.ACTS[i % 5]
@@ -123,7 +133,7 @@ def test_linear(block, n, k, m, dtype):
 
 @pytest.mark.parametrize("act", R.ACTS)
 @pytest.mark.parametrize("n", [1, 70, 600])
-def test_linear_every_epilogue(block, act, n):
+def test_linear_every_epilogue(any_path, block, act, n):
     g = gen_of(n)
     k, m = 192, 328
     x, w, bias, res = rnd(g, n, k), rnd(g, m, k, scale=3 * k ** -0.5), rnd(g, m), rnd(g, n, m)
@@ -141,7 +151,7 @@ def test_linear_every_epilogue(block, act, n):
 
 
 @pytest.mark.parametrize("n", [1, 40, 700])
-def test_linear_residual_in_place(block, n):
+def test_linear_residual_in_place(any_path, block, n):
     g = gen_of(n)
     x, w, res = rnd(g, n, 256), rnd(g, 520, 256, scale=0.1), rnd(g, n, 520)
     want = R.linear(d(x), d(w), residual=d(res))
@@ -151,7 +161,7 @@ def test_linear_residual_in_place(block, n):
 
 
 @pytest.mark.parametrize("n", [3, 300])
-def test_not_finite_values_stay_in_their_row(block, n):
+def test_not_finite_values_stay_in_their_row(any_path, block, n):
     g = gen_of(9)
     x, w = rnd(g, n, 264), rnd(g, 136, 264, scale=0.1)
     x[1, 5] = float("nan")
@@ -173,7 +183,7 @@ def test_not_finite_values_stay_in_their_row(block, n):
         assert (y[2][ok] == want.to(BF16).double()[ok]).all(), act
 
 
-def test_large_values_of_the_activations(block):
+def test_large_values_of_the_activations(any_path, block):
     """Pre-activations far outside the functions' curved part, both signs."""
     z = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 5.0, -5.0, 9.0, -9.0, 30.0, -30.0, 89.0, -89.0, 200.0, -200.0, 3e4, -3e4,
                       1e30, -1e30], device="cuda").to(BF16)
@@ -198,7 +208,7 @@ def test_large_values_of_the_activations(block):
 
 
 @pytest.mark.parametrize("n,k,m", SHAPES)
-def test_linear_bwd(block, n, k, m):
+def test_linear_bwd(any_path, block, n, k, m):
     i = SHAPES.index((n, k, m))
     g = gen_of(200 + i)
     act = R.ACTS[(i + 1) % 5]
@@ -237,7 +247,7 @@ def test_linear_bwd_parts(block, which, act):
 
 @pytest.mark.parametrize("n,k,m", SHAPES)
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-def test_gated(block, n, k, m, dtype):
+def test_gated(any_path, block, n, k, m, dtype):
     i = SHAPES.index((n, k, m))
     gen = gen_of(300 + i)
     act = R.ACTS[(i + 4) % 5]
@@ -261,7 +271,7 @@ def test_gated(block, n, k, m, dtype):
 
 
 @pytest.mark.parametrize("n,k,m", SHAPES)
-def test_gated_bwd(block, n, k, m):
+def test_gated_bwd(any_path, block, n, k, m):
     i = SHAPES.index((n, k, m))
     gen = gen_of(400 + i)
     act = R.ACTS[(i + 2) % 5]
@@ -474,7 +484,7 @@ def _layer(n, k, m, seed):
 
 
 @pytest.mark.parametrize("n,k,m", [(1, 256, 384), (50, 520, 264), (700, 512, 1024)])
-def test_layer_step_matches_its_steps(block, n, k, m):
+def test_layer_step_matches_its_steps(any_path, block, n, k, m):
     """The whole feed-forward sublayer, forward and backward, each step against its definition on that step's inputs."""
     s = _layer(n, k, m, n)
     _all_calls(block, s)
@@ -495,7 +505,7 @@ def test_layer_step_matches_its_steps(block, n, k, m):
 
 
 @pytest.mark.parametrize("n,k,m", [(1, 256, 384), (33, 520, 264), (1100, 512, 1032)])
-def test_repeats_streams_and_graphs_give_the_same_bits(block, n, k, m):
+def test_repeats_streams_and_graphs_give_the_same_bits(any_path, block, n, k, m):
     s = _layer(n, k, m, 5)
     first = [v.clone() for v in _all_calls(block, s)]
     for _ in range(3):
@@ -549,7 +559,7 @@ def test_workspace_and_device_checks():
         t.tpo_block_destroy(b)
 
 
-def test_offsets_past_32_bits(block):
+def test_offsets_past_32_bits(any_path, block):
     """Matrices whose last elements lie past 2^31 elements from their first."""
     pitch = 1 << 24
     big = torch.zeros(144, pitch, dtype=BF16, device="cuda")  # 2.4e9 elements, 4.8 GB
