@@ -347,6 +347,10 @@ __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_const
     }
     mbar_init(drain, 1);
     fence_barrier_init();
+    for (int i = 0; i < p.count; ++i) {
+      tma_prefetch_map(&p.q[i].a[0]);
+      tma_prefetch_map(&p.q[i].b[0]);
+    }
   }
   __syncwarp();
   cluster_sync();  // the peer's barriers exist before anyone signals them
@@ -383,6 +387,50 @@ bool encode_out(OutMat* o, void* p, int64_t ld, int64_t M, int64_t N) {
   o->p = static_cast<__nv_bfloat16*>(p);
   o->ld = ld;
   return encode(&o->map, p, false, N, M, ld, CHUNK, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// Clock cycles of one K block of a tile w columns wide (w of h for the gated
+// form, whose accumulator has twice as many): the tensor cores take two per
+// accumulator column, and a CTA takes in about 68 bytes of operands a cycle
+// from L2 when all of them load (256 columns: 512 and 482).
+double kblock_cycles(int w, bool gated, bool b_mn) {
+  const int cols = gated ? 2 * w : w, rows = b_mn ? (cols / 2 + 63) / 64 * 64 : cols / 2;
+  return std::max(2.0 * cols, (TM + rows) * KB / 68.0);
+}
+
+// The column tiles' width, one for all products of a launch: a model of the
+// launch as rounds of one tile per pair, each as long as its longest tile, and
+// the last tile's epilogue.  Narrower tiles than 256 cost more per column, so
+// they are taken where they fill a last round or spread few tiles over the
+// pairs.
+int plan_width(const Product* q, int count, bool fp8, bool gated, int pairs, double* cycles) {
+  int best = 0;
+  double best_cost = 0;
+  const int most = gated ? TN / 2 : TN, step = CHUNK;
+  for (int w = most; w >= step; w -= step) {
+    int64_t tiles[3] = {}, total = 0;
+    double cost[3] = {};
+    for (int i = 0; i < count; ++i) {
+      tiles[i] = static_cast<int64_t>(ceil_div(q[i].M, 2 * TM)) * ceil_div(q[i].N, w);
+      total += tiles[i];
+      const int kb = ceil_div(q[i].K, fp8 ? KB : KB / 2) * q[i].terms;
+      // a tile cannot end before its accumulator has been drained
+      cost[i] = std::max(kb * kblock_cycles(w, gated, q[i].b[0].mn_major), 8.0 * w * (gated ? 2 : 1) + 300);
+    }
+    // round r runs tiles [r pairs, (r + 1) pairs) of the products laid end to end
+    double sum = 0;
+    int64_t done = 0;
+    for (int i = 0; i < count; ++i) {
+      const int64_t end = done + tiles[i];
+      const int64_t r0 = (done + pairs - 1) / pairs, r1 = (end + pairs - 1) / pairs;  // rounds that start in it
+      sum += static_cast<double>(r1 - r0) * cost[i];
+      done = end;
+    }
+    sum += 12.0 * w * (gated ? 2 : 1);
+    if (!best || sum < 0.99 * best_cost) best = w, best_cost = sum;
+  }
+  if (cycles) *cycles = best_cost;
+  return best;
 }
 
 template <int KIND, bool FP8>
@@ -442,12 +490,13 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
   Args p;
   std::memset(&p, 0, sizeof(p));
   p.count = count;
+  const int w = plan_width(q, count, fp8, e.kind == EPI_GATED, mc.pairs, nullptr);
   bool ok = true;
   for (int i = 0; i < count; ++i) {
     const Product& c = q[i];
     Prob& o = p.q[i];
     o.M = static_cast<int>(c.M), o.N = static_cast<int>(c.N);
-    o.w = e.kind == EPI_GATED ? TN / 2 : TN;
+    o.w = w;
     const int hb = e.kind == EPI_GATED ? o.w : o.w / 2;
     o.tiles_m = ceil_div(c.M, 2 * TM);
     o.tiles = o.tiles_m * ceil_div(c.N, o.w);

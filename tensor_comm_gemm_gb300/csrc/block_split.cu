@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <cstdlib>
 
 #include "act.h"
 #include "block.h"
@@ -26,6 +27,7 @@ namespace {
 constexpr int FT = 128;                // accumulator rows of a tile
 constexpr int A_BYTES = FT * KB;       // weights of one K block
 constexpr int MAX_STAGES = 8;
+constexpr int MAX_SPLIT = 8;           // CTAs of a cluster
 constexpr int THREADS = 256;           // warp 0 TMA, warp 1 MMA, warps 4-7 drain; all add
 constexpr int SMEM_TAIL = 8 * (2 * MAX_STAGES + 2) + 16 + 1024;  // barriers, tensor memory slot, slack to align
 constexpr int SMEM_ONE = 232448;       // one CTA per SM
@@ -76,9 +78,19 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&v)[4], int 
     for (int j = 0; j < count; ++j) p[j] = __float2bfloat16_rn(v[j]);
   }
 }
-__device__ __forceinline__ void add4(const __nv_bfloat16* p, float (&v)[4], int count) {
+// Four consecutive bf16 values (0 past `count`), as they lie in memory.
+__device__ __forceinline__ uint2 get4(const __nv_bfloat16* p, int count) {
+  if (count >= 4) return *reinterpret_cast<const uint2*>(p);
+  uint32_t h[4] = {};
   for (int j = 0; j < 4; ++j)
-    if (j < count) v[j] += __bfloat162float(p[j]);
+    if (j < count) h[j] = __bfloat16_as_ushort(p[j]);
+  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+__device__ __forceinline__ void add4(uint2 h, float (&v)[4]) {
+  v[0] += __uint_as_float(h.x << 16);
+  v[1] += __uint_as_float(h.x & 0xffff0000u);
+  v[2] += __uint_as_float(h.y << 16);
+  v[3] += __uint_as_float(h.y & 0xffff0000u);
 }
 
 template <int KIND, bool FP8>
@@ -104,6 +116,10 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     }
     mbar_init(tfull, 1);
     fence_barrier_init();
+    for (int t = 0; t < 2; ++t) {
+      tma_prefetch_map(&p.a[t]);
+      tma_prefetch_map(&p.b[t]);
+    }
   }
   if (warp == 1) {
     tmem_alloc_cg<1>(slot, p.tmem_cols);
@@ -114,6 +130,18 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = ld_shared_u32(slot);
   grid_dep_wait();
+  // the bias and residual of this thread's first outputs, in flight beside the product
+  constexpr int QUADS = FEATURES / 4;  // groups of four features of a token
+  const int tokens = min(p.nt, p.N - t0);
+  const int first = rank * THREADS + static_cast<int>(threadIdx.x);
+  uint2 pre_b = make_uint2(0, 0), pre_r = pre_b;
+  auto fetch = [&](int i) {
+    const int col = f0 + i % QUADS * 4, count = p.M - col;
+    if (KIND != EPI_LINEAR || i >= tokens * QUADS || count <= 0) return;
+    if (p.bias) pre_b = get4(p.bias + col, count);
+    if (p.residual) pre_r = get4(p.residual + (t0 + i / QUADS) * p.ldr + col, count);
+  };
+  fetch(first);
   bool ok = true;
   if (warp == 0) {
     if (lane == 0) {
@@ -173,7 +201,6 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     __syncwarp();
   }
   // ---- the accumulator, [token][feature] in fp32, over the pipeline's memory
-  const int tokens = min(p.nt, p.N - t0);
   if (warp >= 4) {
     if (wait_bar_warp(p.err, tfull, 0, S_TFULL)) {
       tc_fence_after();
@@ -196,34 +223,39 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     tmem_dealloc_cg<1>(tmem, p.tmem_cols);
   }
   // ---- sums over the cluster and the epilogue: four features of one token at a time
-  constexpr int QUADS = FEATURES / 4;
   const float s0 = FP8 ? __ldg(p.sx) * __ldg(p.sw0) : 1.0f;
   const float s1 = FP8 && KIND == EPI_GATED ? __ldg(p.sx) * __ldg(p.sw1) : 1.0f;
   const bool good = *reinterpret_cast<volatile uint32_t*>(p.err) == 0u;
-  for (int i = rank * THREADS + static_cast<int>(threadIdx.x); good && i < tokens * QUADS; i += S * THREADS) {
+  for (int i = first; good && i < tokens * QUADS; i += S * THREADS) {
     const int tok = i / QUADS, fq = i % QUADS * 4;
     const int64_t row = t0 + tok;
     const int col = f0 + fq, count = p.M - col;
     if (count <= 0) continue;
+    if (i != first) fetch(i);
     const uint32_t at = sbase + static_cast<uint32_t>(tok * FT + fq) * 4u;
-    float v[4] = {}, u[4] = {};
-    for (int s = 0; s < S; ++s) {
+    float4 x[MAX_SPLIT], y[MAX_SPLIT];  // all in flight before the first is added
+#pragma unroll
+    for (int s = 0; s < MAX_SPLIT; ++s) {
+      if (s >= S) break;
       const uint32_t peer = map_to_rank(at, s);
-      const float4 x = ld_cluster_f4(peer);
-      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-      if constexpr (KIND == EPI_GATED) {
-        const float4 y = ld_cluster_f4(peer + FT / 2 * 4);
-        u[0] += y.x, u[1] += y.y, u[2] += y.z, u[3] += y.w;
-      }
+      x[s] = ld_cluster_f4(peer);
+      if constexpr (KIND == EPI_GATED) y[s] = ld_cluster_f4(peer + FT / 2 * 4);
+    }
+    float v[4] = {}, u[4] = {};
+#pragma unroll
+    for (int s = 0; s < MAX_SPLIT; ++s) {
+      if (s >= S) break;
+      v[0] += x[s].x, v[1] += x[s].y, v[2] += x[s].z, v[3] += x[s].w;
+      if constexpr (KIND == EPI_GATED) u[0] += y[s].x, u[1] += y[s].y, u[2] += y[s].z, u[3] += y[s].w;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= s0, u[j] *= s1;
     if constexpr (KIND == EPI_LINEAR) {
-      if (p.bias) add4(p.bias + col, v, count);
+      if (p.bias) add4(pre_b, v);
       if (p.out1) put4(p.out1 + row * p.ld1 + col, v, count);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = act_any(p.act, v[j]);
-      if (p.residual) add4(p.residual + row * p.ldr + col, v, count);
+      if (p.residual) add4(pre_r, v);
     }
     if constexpr (KIND == EPI_GATED) {
       if (p.out1) {
@@ -282,8 +314,9 @@ SplitPlan plan_split(const Machine& mc, int64_t M, int64_t N, int64_t K, int ter
   // two CTAs per SM while they hold at least three stages each
   o.per_sm = (SMEM_TWO - SMEM_TAIL) / stage >= 3 ? 2 : 1;
   o.stages = std::min(MAX_STAGES, ((o.per_sm == 2 ? SMEM_TWO : SMEM_ONE) - SMEM_TAIL) / stage);
+  if (getenv("TPO_STG")) o.stages = std::min(o.stages, atoi(getenv("TPO_STG")));
   const int64_t places = static_cast<int64_t>(mc.sms) * o.per_sm;
-  o.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, kb, places / tiles})));
+  o.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({MAX_SPLIT, kb, places / tiles})));
   return o;
 }
 
