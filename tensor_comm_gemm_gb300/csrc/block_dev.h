@@ -52,6 +52,57 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
   return v | (static_cast<uint64_t>(8192 >> 4) << 16);
 }
 
+// Tensor loads of one pipeline stage, issued by a converged warp: inside the
+// statement elect.sync picks the lane, which first arms `arm` with the stage's
+// bytes (if arming is not 0) and then issues the loads, all completing on
+// `bar`.  One thread of a diverged warp needs ~80 cycles for each load and the
+// index arithmetic around it runs at the latency of every instruction; the
+// whole warp keeps the operands in uniform registers and issues two loads in
+// less than 50.  (Measured on all SMs: 120 bytes per cycle and SM from L2 with
+// two 16 KiB boxes a stage, 88 from a single thread.)
+struct Box {
+  uint32_t dst;
+  uint64_t map;
+  int x, y;
+};
+#define TPO_LOAD(CG, D, M, X, Y)                                                                              \
+  "@E cp.async.bulk.tensor.2d" CG ".shared::cluster.global.mbarrier::complete_tx::bytes [" D "], [" M ", {" X \
+  ", " Y "}], [%3];\n\t"
+#define TPO_ARM                                                                                               \
+  "{\n\t.reg .pred E, F;\n\t.reg .b32 r;\n\telect.sync r|E, 0xffffffff;\n\tsetp.ne.and.b32 F, %0, 0, E;\n\t" \
+  "@F mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %2;\n\t"
+#define TPO_BOX(b) "r"(b.dst), "l"(b.map), "r"(b.x), "r"(b.y)
+#define TPO_STAGE_LOADS(CG)                                                                                   \
+  if constexpr (N == 2)                                                                                       \
+    asm volatile(TPO_ARM TPO_LOAD(CG, "%4", "%5", "%6", "%7") TPO_LOAD(CG, "%8", "%9", "%10", "%11") "}" ::"r"( \
+                     arming), "r"(arm), "r"(bytes), "r"(bar), TPO_BOX(b[0]), TPO_BOX(b[1])                    \
+                 : "memory");                                                                                 \
+  else if constexpr (N == 3)                                                                                  \
+    asm volatile(TPO_ARM TPO_LOAD(CG, "%4", "%5", "%6", "%7") TPO_LOAD(CG, "%8", "%9", "%10", "%11")          \
+                     TPO_LOAD(CG, "%12", "%13", "%14", "%15") "}" ::"r"(arming),                              \
+                 "r"(arm), "r"(bytes), "r"(bar), TPO_BOX(b[0]), TPO_BOX(b[1]), TPO_BOX(b[2])                  \
+                 : "memory");                                                                                 \
+  else                                                                                                        \
+    asm volatile(TPO_ARM TPO_LOAD(CG, "%4", "%5", "%6", "%7") TPO_LOAD(CG, "%8", "%9", "%10", "%11")          \
+                     TPO_LOAD(CG, "%12", "%13", "%14", "%15") TPO_LOAD(CG, "%16", "%17", "%18", "%19") "}" :: \
+                         "r"(arming), "r"(arm), "r"(bytes), "r"(bar), TPO_BOX(b[0]), TPO_BOX(b[1]),           \
+                 TPO_BOX(b[2]), TPO_BOX(b[3])                                                                 \
+                 : "memory")
+// CG 2: `bar` may be the pair's even CTA's (a shared::cluster address).
+template <int CG, int N>
+__device__ __forceinline__ void stage_loads(uint32_t arming, uint32_t arm, uint32_t bytes, uint32_t bar,
+                                            const Box (&b)[N]) {
+  if constexpr (CG == 2) {
+    TPO_STAGE_LOADS(".cta_group::2");
+  } else {
+    TPO_STAGE_LOADS("");
+  }
+}
+#undef TPO_LOAD
+#undef TPO_ARM
+#undef TPO_BOX
+#undef TPO_STAGE_LOADS
+
 // ------------------------------------------------------------------ host side (block_maps.cu)
 
 bool load_encode();  // the driver's tensor-map encoder; false if there is none

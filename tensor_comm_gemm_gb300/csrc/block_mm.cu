@@ -57,7 +57,7 @@ struct Prob {
   int M, N;
   int tiles_m, tiles;   // row tiles, tiles in all
   int w;                // columns of a tile (EPI_GATED: of h; the accumulator has twice as many)
-  int kb_seg, kb;       // K blocks per term and in all
+  int terms, kb_seg, kb;  // K blocks per term and in all
   int a_mn, b_mn;
 };
 struct Args {
@@ -92,59 +92,92 @@ __device__ __forceinline__ TileAt tile_at(const Args& p, int t) {
   return o;
 }
 
+struct Ring {  // the load warp's place in the pipeline
+  uint32_t stage, phase, armed;
+};
+
+// Loads one tile's K blocks.  AMN: A is MN-major; BN_BOXES: MN-major boxes of
+// this CTA's share of B (0: B is K-major).  A stage is one A block and one B
+// block; the pair's bytes are expected on the even CTA's barrier.
+template <bool FP8, bool AMN, int BN_BOXES>
+__device__ __forceinline__ bool load_tile(const Args& p, Ring& g, uint32_t sbase, uint32_t full0, uint32_t full_lead,
+                                          uint32_t empty0, uint32_t lead, uint32_t bytes, const CUtensorMap* ma,
+                                          const CUtensorMap* mb, int terms, int kb_seg, int a0, int b0) {
+  constexpr int KEL = FP8 ? KB : KB / 2;
+  constexpr int NA = AMN ? 2 : 1, NB = BN_BOXES ? BN_BOXES : 1;
+  for (int seg = 0; seg < terms; ++seg, ++ma, ++mb) {
+    const uint64_t a = reinterpret_cast<uint64_t>(ma), b = reinterpret_cast<uint64_t>(mb);
+    int kx = 0;
+    for (int kk = 0; kk < kb_seg; ++kk, kx += KEL) {
+      if (!wait_bar_warp(p.err, empty0 + 8u * g.stage, g.phase ^ 1u, S_EMPTY)) return false;
+      const uint32_t sa = sbase + g.stage * STAGE, sb = sa + A_BYTES;
+      Box x[NA + NB];
+      if constexpr (AMN) {
+        x[0] = {sa, a, a0, kx};
+        x[1] = {sa + 8192u, a, a0 + 64, kx};
+      } else {
+        x[0] = {sa, a, kx, a0};
+      }
+      if constexpr (BN_BOXES > 0) {
+        x[NA] = {sb, b, b0, kx};
+        if constexpr (BN_BOXES > 1) x[NA + 1] = {sb + 8192u, b, b0 + 64, kx};
+      } else {
+        x[NA] = {sb, b, kx, b0};
+      }
+      stage_loads<2>(lead, full0 + 8u * g.stage, bytes, full_lead + 8u * g.stage, x);
+      ++g.armed;
+      if (++g.stage == STAGES) g.stage = 0, g.phase ^= 1u;
+    }
+  }
+  return true;
+}
+
+// The load warp, converged (one elected lane issues each stage's loads).
 template <int KIND, bool FP8>
 __device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_t empty0, uint32_t rank, int pair,
                           int pairs) {
-  constexpr int KEL = FP8 ? KB : KB / 2;
-  const uint32_t full_lead = map_to_rank(full0, 0);
-  uint32_t stage = 0, phase = 0, armed = 0;
+  const uint32_t full_lead = map_to_rank(full0, 0), lead = rank == 0 ? 1u : 0u;
+  Ring g{0, 0, 0};
   bool ok = true;
   for (int t = pair; ok && t < p.total; t += pairs) {
     const TileAt T = tile_at(p, t);
     const Prob& q = p.q[T.q];
-    const int hb = KIND == EPI_GATED ? q.w : q.w / 2;  // B rows this CTA loads
     const int a0 = T.row + TM * static_cast<int>(rank);
-    const int b0 = KIND == EPI_GATED ? T.col : T.col + hb * static_cast<int>(rank);
-    const int b_boxes = (hb + 63) / 64;
-    const uint32_t bytes = 2u * (A_BYTES + (q.b_mn ? b_boxes * 8192u : static_cast<uint32_t>(hb) * KB));
-    const int kb = q.kb, a_mn = q.a_mn, b_mn = q.b_mn, kb_seg = q.kb_seg;
-    int seg = 0, kk = 0;
-    for (int i = 0; i < kb; ++i) {
-      const uint32_t eb = empty0 + 8u * stage;
-      if (!mbar_test(eb, phase ^ 1u) && !wait_bar(p.err, eb, phase ^ 1u, S_EMPTY)) {
-        ok = false;
-        break;
-      }
-      if (rank == 0) mbar_expect_tx(full0 + 8u * stage, bytes);
-      ++armed;
-      const uint32_t sa = sbase + stage * STAGE, sb = sa + A_BYTES, fb = full_lead + 8u * stage;
-      const CUtensorMap* ma = &q.a[seg];
-      const CUtensorMap* mb = &q.b[KIND == EPI_GATED ? rank : seg];
-      const int kx = kk * KEL;
-      if (a_mn) {
-        tma_load_2d_pair(sa, ma, fb, a0, kx);
-        tma_load_2d_pair(sa + 8192, ma, fb, a0 + 64, kx);
+    if constexpr (KIND == EPI_GATED) {
+      // the even CTA holds the tile's rows of wg, the odd one those of wu
+      ok = load_tile<FP8, false, 0>(p, g, sbase, full0, full_lead, empty0, lead, 2u * (A_BYTES + q.w * KB), &q.a[0],
+                                    &q.b[rank], 1, q.kb_seg, a0, T.col);
+    } else {
+      const int hb = q.w / 2, b0 = T.col + hb * static_cast<int>(rank), terms = q.terms, kbs = q.kb_seg;
+      const int boxes = q.b_mn ? (hb + 63) / 64 : 0;
+      const uint32_t bytes = 2u * (A_BYTES + (boxes ? boxes * 8192u : static_cast<uint32_t>(hb) * KB));
+      if constexpr (KIND == EPI_PLAIN) {
+        if (q.a_mn)
+          ok = boxes == 2 ? load_tile<FP8, true, 2>(p, g, sbase, full0, full_lead, empty0, lead, bytes, q.a, q.b,
+                                                    terms, kbs, a0, b0)
+                          : load_tile<FP8, true, 1>(p, g, sbase, full0, full_lead, empty0, lead, bytes, q.a, q.b,
+                                                    terms, kbs, a0, b0);
+        else
+          ok = boxes == 2 ? load_tile<FP8, false, 2>(p, g, sbase, full0, full_lead, empty0, lead, bytes, q.a, q.b,
+                                                     terms, kbs, a0, b0)
+                          : load_tile<FP8, false, 1>(p, g, sbase, full0, full_lead, empty0, lead, bytes, q.a, q.b,
+                                                     terms, kbs, a0, b0);
       } else {
-        tma_load_2d_pair(sa, ma, fb, kx, a0);
+        ok = load_tile<FP8, false, 0>(p, g, sbase, full0, full_lead, empty0, lead, bytes, q.a, q.b, terms, kbs, a0,
+                                      b0);
       }
-      if (b_mn) {
-        for (int j = 0; j < b_boxes; ++j) tma_load_2d_pair(sb + 8192u * j, mb, fb, b0 + 64 * j, kx);
-      } else {
-        tma_load_2d_pair(sb, mb, fb, kx, b0);
-      }
-      if (++kk == kb_seg) kk = 0, ++seg;
-      if (++stage == STAGES) stage = 0, phase ^= 1u;
     }
   }
-  if (!ok) {  // loads in flight must land before the CTA gives up its shared memory
+  if (!ok && (threadIdx.x & 31) == 0) {  // loads in flight must land before the CTA gives up its shared memory
     if (rank == 0) {
-      for (uint32_t j = armed > STAGES ? armed - STAGES : 0u; j < armed; ++j)
+      for (uint32_t j = g.armed > STAGES ? g.armed - STAGES : 0u; j < g.armed; ++j)
         wait_bar(p.err, full0 + 8u * (j % STAGES), (j / STAGES) & 1u, S_DRAIN, false);
-    } else if (armed > 0) {  // they signal the even CTA's barriers
+    } else if (g.armed > 0) {  // they signal the even CTA's barriers
       const unsigned long long t0 = gtime();
       while (gtime() - t0 < 200000ull) __nanosleep(1000);
     }
   }
+  __syncwarp();
 }
 
 template <int KIND, bool FP8>
@@ -331,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_const
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
   grid_dep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank();
   const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
   const uint32_t full0 = sbase + OFF_BARS, empty0 = full0 + 8 * STAGES, tfull0 = empty0 + 8 * STAGES,
@@ -364,8 +397,7 @@ __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_const
   const uint32_t tmem = ld_shared_u32(sbase + OFF_TMEM);
   grid_dep_wait();  // from here on memory may depend on the launch before
   if (warp == 0) {
-    if (lane == 0) load_role<KIND, FP8>(p, sbase, full0, empty0, rank, pair, pairs);
-    __syncwarp();
+    load_role<KIND, FP8>(p, sbase, full0, empty0, rank, pair, pairs);
   } else if (warp == 1) {
     if (rank == 0) mma_role<KIND, FP8>(p, sbase, tmem, full0, empty0, tfull0, tempty0, drain, pair, pairs);
     __syncwarp();
@@ -501,6 +533,7 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
     o.tiles_m = ceil_div(c.M, 2 * TM);
     o.tiles = o.tiles_m * ceil_div(c.N, o.w);
     o.kb_seg = ceil_div(c.K, fp8 ? KB : KB / 2);
+    o.terms = c.terms;
     o.kb = o.kb_seg * c.terms;
     o.a_mn = c.a[0].mn_major, o.b_mn = c.b[0].mn_major;
     for (int t = 0; t < c.terms && ok; ++t)

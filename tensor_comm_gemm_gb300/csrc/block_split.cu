@@ -144,39 +144,45 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
   fetch(first);
   bool ok = true;
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, armed = 0;
+    // the load warp, converged
+    const uint32_t stages = static_cast<uint32_t>(p.stages), kb_seg = static_cast<uint32_t>(p.kb_seg);
+    uint32_t stage = 0, phase = 0, armed = 0;
+    // `boxes` issues the loads of one stage at `sa`, K offset kx of term seg
+    auto run = [&](auto boxes) {
+      int seg = lo >= static_cast<int>(kb_seg) ? 1 : 0, kk = lo - seg * static_cast<int>(kb_seg);
       for (int i = lo; i < hi; ++i) {
-        const uint32_t eb = empty0 + 8u * stage, fb = full0 + 8u * stage;
-        if (!mbar_test(eb, phase ^ 1u) && !wait_bar(p.err, eb, phase ^ 1u, S_EMPTY)) {
+        if (!wait_bar_warp(p.err, empty0 + 8u * stage, phase ^ 1u, S_EMPTY)) {
           ok = false;
-          break;
+          return;
         }
-        mbar_expect_tx(fb, stage_bytes);
+        const uint32_t fb = full0 + 8u * stage;
+        boxes(fb, sbase + stage * stage_bytes, seg, kk * KEL);
         ++armed;
-        const int seg = i >= p.kb_seg ? 1 : 0, kx = (i - seg * p.kb_seg) * KEL;
-        const uint32_t sa = sbase + stage * stage_bytes;
-        if constexpr (KIND == EPI_GATED) {
-          tma_load_2d(sa, &p.a[0], fb, kx, f0);
-          tma_load_2d(sa + A_BYTES / 2, &p.a[1], fb, kx, f0);
-          tma_load_2d(sa + A_BYTES, &p.b[0], fb, kx, t0);
-        } else {
-          if (p.a_mn) {
-            tma_load_2d(sa, &p.a[seg], fb, f0, kx);
-            tma_load_2d(sa + A_BYTES / 2, &p.a[seg], fb, f0 + 64, kx);
-          } else {
-            tma_load_2d(sa, &p.a[seg], fb, kx, f0);
-          }
-          tma_load_2d(sa + A_BYTES, &p.b[seg], fb, kx, t0);
-        }
-        if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
+        if (++kk == static_cast<int>(kb_seg)) kk = 0, ++seg;
+        if (++stage == stages) stage = 0, phase ^= 1u;
       }
-      if (!ok) {  // loads in flight must land before the CTA gives up its shared memory
-        const uint32_t n = static_cast<uint32_t>(p.stages);
-        for (uint32_t j = armed > n ? armed - n : 0u; j < armed; ++j)
-          wait_bar(p.err, full0 + 8u * (j % n), (j / n) & 1u, S_DRAIN, false);
-      }
-    }
+    };
+    const uint64_t ma = reinterpret_cast<uint64_t>(&p.a[0]), mb = reinterpret_cast<uint64_t>(&p.b[0]);
+    constexpr uint64_t kMap = sizeof(CUtensorMap);
+    if (KIND == EPI_GATED)
+      run([&](uint32_t fb, uint32_t sa, int, int kx) {
+        const Box x[3] = {{sa, ma, kx, f0}, {sa + A_BYTES / 2, ma + kMap, kx, f0}, {sa + A_BYTES, mb, kx, t0}};
+        stage_loads<1>(1u, fb, stage_bytes, fb, x);
+      });
+    else if (p.a_mn)
+      run([&](uint32_t fb, uint32_t sa, int seg, int kx) {
+        const Box x[3] = {{sa, ma + seg * kMap, f0, kx}, {sa + A_BYTES / 2, ma + seg * kMap, f0 + 64, kx},
+                          {sa + A_BYTES, mb + seg * kMap, kx, t0}};
+        stage_loads<1>(1u, fb, stage_bytes, fb, x);
+      });
+    else
+      run([&](uint32_t fb, uint32_t sa, int seg, int kx) {
+        const Box x[2] = {{sa, ma + seg * kMap, kx, f0}, {sa + A_BYTES, mb + seg * kMap, kx, t0}};
+        stage_loads<1>(1u, fb, stage_bytes, fb, x);
+      });
+    if (!ok && lane == 0)  // loads in flight must land before the CTA gives up its shared memory
+      for (uint32_t j = armed > stages ? armed - stages : 0u; j < armed; ++j)
+        wait_bar(p.err, full0 + 8u * (j % stages), (j / stages) & 1u, S_DRAIN, false);
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = idesc_n(make_idesc(FP8, FT), p.nt) | (p.a_mn ? 1u << 15 : 0u);
