@@ -194,7 +194,7 @@ tpo_block* tpo_block_create(int64_t workspace_bytes) {
     return nullptr;
   }
   e = tpo::configure_products(&b->machine);
-  if (e == cudaSuccess) e = tpo::configure_split();
+  if (e == cudaSuccess) e = tpo::configure_split(&b->machine);
   if (e != cudaSuccess) {
     cuda_fail(e, "kernel configuration");
     delete b;

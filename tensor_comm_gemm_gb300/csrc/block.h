@@ -43,11 +43,20 @@ struct Epi {
   const float *sx = nullptr, *sw0 = nullptr, *sw1 = nullptr;  // e4m3 scales or NULL
 };
 
-// Places for CTA pairs and SMs on the current device; also sets the kernels' attributes.
+// What the current device holds at a time.
+constexpr int MAX_SPLIT = 8;  // CTAs of a cluster that cuts a contraction
 struct Machine {
-  int sms, pairs;
+  int sms, pairs;                    // CTA pairs of the product kernel
+  int clusters[2][MAX_SPLIT + 1];    // clusters of s CTAs, with one or two CTAs per SM
 };
+// Also set the kernels' attributes.
 cudaError_t configure_products(Machine* m);
+// The column tiles' width, one for all products of a launch, and the launch's
+// modelled time: rounds of one tile per pair, each as long as its tile, and
+// the last tile's epilogue.  Narrower tiles than the widest cost more per
+// column, so they are taken where they fill a last round or spread few tiles
+// over the pairs.
+int plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, double* us);
 // Runs `count` (1 to 3) products in one launch; more than one take EPI_PLAIN.
 cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, uint32_t* err,
                             cudaStream_t s);
@@ -56,10 +65,9 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
 struct SplitPlan {
   int nt = 0;       // tokens of a tile
   int split = 1;    // CTAs of a cluster
-  int stages = 0, per_sm = 0;
+  int stages = 0;
 };
-cudaError_t configure_split();
-SplitPlan plan_split(const Machine& mc, int64_t features, int64_t tokens, int64_t K, int terms, bool fp8, bool gated);
+cudaError_t configure_split(Machine* m);
 // Whether the product takes that form (path 0: by rule, 1: never, 2: always; split 0: by rule), and its plan.
 bool use_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t path, int64_t split, SplitPlan* plan);
 cudaError_t launch_split(const Product& q, const SplitPlan& plan, bool fp8, const Epi& e, uint32_t* err,

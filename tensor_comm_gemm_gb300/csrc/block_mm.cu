@@ -31,16 +31,15 @@ namespace {
 constexpr int TM = 128;              // rows of one CTA; a pair's tile has 256
 constexpr int TN = 256;              // most columns of a tile (accumulator width)
 constexpr int A_BYTES = TM * KB;     // 16 KiB
-constexpr int B_BYTES = TN / 2 * KB;  // 16 KiB: half of the tile's B rows
-constexpr int STAGE = A_BYTES + B_BYTES;
-constexpr int STAGES = 6;
+constexpr int STAGE_AREA = 196608;   // pipeline stages: an A block and half of the tile's B rows each
+constexpr int MAX_STAGES = 12;       // 6 with 256-column tiles
 constexpr int EPI_WARPS_N = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS_N;
 constexpr int CHUNK = 32;                   // columns of one epilogue step
 constexpr int BOX = 32 * CHUNK * 2;         // bytes of one output box: 32 rows of 64 bytes
-constexpr int OFF_EPI = STAGES * STAGE;
+constexpr int OFF_EPI = STAGE_AREA;
 constexpr int OFF_BARS = OFF_EPI + EPI_WARPS_N * 2 * BOX;
-constexpr int N_BARS = 2 * STAGES + 2 + 2 + 1;
+constexpr int N_BARS = 2 * MAX_STAGES + 2 + 2 + 1;
 constexpr int OFF_TMEM = OFF_BARS + 8 * N_BARS;
 constexpr int SMEM = OFF_TMEM + 16 + 1024;  // and the slack to align the base
 static_assert(SMEM <= 232448, "shared memory of one CTA");
@@ -64,9 +63,11 @@ struct Args {
   Prob q[3];
   OutMat y1, y2;
   int count, total;
+  uint32_t stages, stage_bytes;
   int act;
   const __nv_bfloat16 *bias, *residual;
   int64_t ldr;
+  int bias_vec;         // the bias is 16-byte aligned
   int has1;             // y1 (and for EPI_GATED y2) are stored
   const float *sx, *sw0, *sw1;
   uint32_t* err;
@@ -94,6 +95,7 @@ __device__ __forceinline__ TileAt tile_at(const Args& p, int t) {
 
 struct Ring {  // the load warp's place in the pipeline
   uint32_t stage, phase, armed;
+  uint32_t stages, bytes;  // stages of the ring, bytes of each
 };
 
 // Loads one tile's K blocks.  AMN: A is MN-major; BN_BOXES: MN-major boxes of
@@ -106,27 +108,27 @@ __device__ __forceinline__ bool load_tile(const Args& p, Ring& g, uint32_t sbase
   constexpr int KEL = FP8 ? KB : KB / 2;
   constexpr int NA = AMN ? 2 : 1, NB = BN_BOXES ? BN_BOXES : 1;
   for (int seg = 0; seg < terms; ++seg, ++ma, ++mb) {
-    const uint64_t a = reinterpret_cast<uint64_t>(ma), b = reinterpret_cast<uint64_t>(mb);
+    const uint64_t map_a = reinterpret_cast<uint64_t>(ma), map_b = reinterpret_cast<uint64_t>(mb);
     int kx = 0;
     for (int kk = 0; kk < kb_seg; ++kk, kx += KEL) {
       if (!wait_bar_warp(p.err, empty0 + 8u * g.stage, g.phase ^ 1u, S_EMPTY)) return false;
-      const uint32_t sa = sbase + g.stage * STAGE, sb = sa + A_BYTES;
+      const uint32_t sa = sbase + g.stage * g.bytes, sb = sa + A_BYTES;
       Box x[NA + NB];
       if constexpr (AMN) {
-        x[0] = {sa, a, a0, kx};
-        x[1] = {sa + 8192u, a, a0 + 64, kx};
+        x[0] = {sa, map_a, a0, kx};
+        x[1] = {sa + 8192u, map_a, a0 + 64, kx};
       } else {
-        x[0] = {sa, a, kx, a0};
+        x[0] = {sa, map_a, kx, a0};
       }
       if constexpr (BN_BOXES > 0) {
-        x[NA] = {sb, b, b0, kx};
-        if constexpr (BN_BOXES > 1) x[NA + 1] = {sb + 8192u, b, b0 + 64, kx};
+        x[NA] = {sb, map_b, b0, kx};
+        if constexpr (BN_BOXES > 1) x[NA + 1] = {sb + 8192u, map_b, b0 + 64, kx};
       } else {
-        x[NA] = {sb, b, kx, b0};
+        x[NA] = {sb, map_b, kx, b0};
       }
       stage_loads<2>(lead, full0 + 8u * g.stage, bytes, full_lead + 8u * g.stage, x);
       ++g.armed;
-      if (++g.stage == STAGES) g.stage = 0, g.phase ^= 1u;
+      if (++g.stage == g.stages) g.stage = 0, g.phase ^= 1u;
     }
   }
   return true;
@@ -137,7 +139,7 @@ template <int KIND, bool FP8>
 __device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_t empty0, uint32_t rank, int pair,
                           int pairs) {
   const uint32_t full_lead = map_to_rank(full0, 0), lead = rank == 0 ? 1u : 0u;
-  Ring g{0, 0, 0};
+  Ring g{0, 0, 0, p.stages, p.stage_bytes};
   bool ok = true;
   for (int t = pair; ok && t < p.total; t += pairs) {
     const TileAt T = tile_at(p, t);
@@ -170,8 +172,8 @@ __device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_
   }
   if (!ok && (threadIdx.x & 31) == 0) {  // loads in flight must land before the CTA gives up its shared memory
     if (rank == 0) {
-      for (uint32_t j = g.armed > STAGES ? g.armed - STAGES : 0u; j < g.armed; ++j)
-        wait_bar(p.err, full0 + 8u * (j % STAGES), (j / STAGES) & 1u, S_DRAIN, false);
+      for (uint32_t j = g.armed > g.stages ? g.armed - g.stages : 0u; j < g.armed; ++j)
+        wait_bar(p.err, full0 + 8u * (j % g.stages), (j / g.stages) & 1u, S_DRAIN, false);
     } else if (g.armed > 0) {  // they signal the even CTA's barriers
       const unsigned long long t0 = gtime();
       while (gtime() - t0 < 200000ull) __nanosleep(1000);
@@ -183,6 +185,7 @@ __device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_
 template <int KIND, bool FP8>
 __device__ void mma_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t full0, uint32_t empty0,
                          uint32_t tfull0, uint32_t tempty0, uint32_t drain, int pair, int pairs) {
+  const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
   uint32_t stage = 0, phase = 0, ul = 0;
   bool ok = true;
   for (int t = pair; ok && t < p.total; t += pairs, ++ul) {
@@ -206,10 +209,10 @@ __device__ void mma_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t 
         break;
       }
       tc_fence_after();
-      const uint64_t off = static_cast<uint64_t>(STAGE >> 4) * stage;
+      const uint64_t off = static_cast<uint64_t>(stage_bytes >> 4) * stage;
       mma_kblock<2, FP8>(d, da0 + off, db0 + off, idesc, i > 0 ? 1u : 0u, step_a, step_b);
       mma_commit_cg<2>(empty0 + 8u * stage);
-      if (++stage == STAGES) stage = 0, phase ^= 1u;
+      if (++stage == stages) stage = 0, phase ^= 1u;
     }
     if (!ok) break;
     mma_commit_cg<2>(tfull0 + 8u * acc);
@@ -218,6 +221,28 @@ __device__ void mma_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t 
     mma_commit_local_cg<2>(drain);
     if ((threadIdx.x & 31) == 0) wait_bar(p.err, drain, 0u, S_DRAIN, false);
     __syncwarp();
+  }
+}
+
+// Adds the first `count` (at most 32) of 32 consecutive bf16 values; `vec`: p is 16-byte aligned.
+__device__ __forceinline__ void add_row(const __nv_bfloat16* p, int count, bool vec, float (&v)[32]) {
+  if (vec && count >= 32) {
+    uint4 h[4];
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) h[ch] = *reinterpret_cast<const uint4*>(p + 8 * ch);
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+      const uint32_t w[4] = {h[ch].x, h[ch].y, h[ch].z, h[ch].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * ch + 2 * j] += __uint_as_float(w[j] << 16);
+        v[8 * ch + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < count) v[j] += __bfloat162float(p[j]);
   }
 }
 
@@ -305,11 +330,7 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * s0;
       if constexpr (KIND == EPI_LINEAR) {
-        if (p.bias) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (ox + j < q.N) v[j] += __bfloat162float(p.bias[ox + j]);
-        }
+        if (p.bias) add_row(p.bias + ox, q.N - ox, p.bias_vec, v);
         if (p.has1) store(&p.y1, v, ox, oy, q);
       }
       if constexpr (KIND == EPI_GATED) {
@@ -332,24 +353,7 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
       }
       if constexpr (KIND == EPI_LINEAR) {
         if (p.residual && row < q.M) {
-          const __nv_bfloat16* res = p.residual + row * p.ldr + ox;
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            // 16-byte groups that lie inside the row; the ragged last one element by element
-            if (ox + 8 * ch + 8 <= q.N) {
-              const uint4 h = *reinterpret_cast<const uint4*>(res + 8 * ch);
-              const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                v[8 * ch + 2 * j] += __uint_as_float(hw[j] << 16);
-                v[8 * ch + 2 * j + 1] += __uint_as_float(hw[j] & 0xffff0000u);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (ox + 8 * ch + j < q.N) v[8 * ch + j] += __bfloat162float(res[8 * ch + j]);
-            }
-          }
+          add_row(p.residual + row * p.ldr + ox, q.N - ox, true, v);
         }
       }
       store(&q.y, v, ox, oy, q);
@@ -367,10 +371,10 @@ __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_const
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank();
   const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
-  const uint32_t full0 = sbase + OFF_BARS, empty0 = full0 + 8 * STAGES, tfull0 = empty0 + 8 * STAGES,
+  const uint32_t full0 = sbase + OFF_BARS, empty0 = full0 + 8 * MAX_STAGES, tfull0 = empty0 + 8 * MAX_STAGES,
                  tempty0 = tfull0 + 16, drain = tempty0 + 16;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < MAX_STAGES; ++s) {
       mbar_init(full0 + 8u * s, 1);
       mbar_init(empty0 + 8u * s, 1);
     }
@@ -421,49 +425,45 @@ bool encode_out(OutMat* o, void* p, int64_t ld, int64_t M, int64_t N) {
   return encode(&o->map, p, false, N, M, ld, CHUNK, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// Clock cycles of one K block of a tile w columns wide (w of h for the gated
-// form, whose accumulator has twice as many): the tensor cores take two per
-// accumulator column, and a CTA takes in about 68 bytes of operands a cycle
-// from L2 when all of them load (256 columns: 512 and 482).
-double kblock_cycles(int w, bool gated, bool b_mn) {
-  const int cols = gated ? 2 * w : w, rows = b_mn ? (cols / 2 + 63) / 64 * 64 : cols / 2;
-  return std::max(2.0 * cols, (TM + rows) * KB / 68.0);
+// Bytes of a CTA's share of a B block of a tile w columns wide (w of h for the
+// gated form, whose accumulator has twice as many).
+int b_bytes(int w, bool gated, bool b_mn) {
+  const int rows = gated ? w : w / 2;
+  return b_mn ? (rows + 63) / 64 * 8192 : rows * KB;
 }
 
-// The column tiles' width, one for all products of a launch: a model of the
-// launch as rounds of one tile per pair, each as long as its longest tile, and
-// the last tile's epilogue.  Narrower tiles than 256 cost more per column, so
-// they are taken where they fill a last round or spread few tiles over the
-// pairs.
-int plan_width(const Product* q, int count, bool fp8, bool gated, int pairs, double* cycles) {
+// Time in ns of one K block of a tile with `cols` accumulator columns, when
+// all pairs work: measured on 8192-long contractions at 32 to 256 columns, 175
+// to 195 ns up to 128, then 218, 254, 282 and 320 (the tensor cores' two
+// cycles a column at the clock the power limit leaves).
+double kblock_ns(int cols) { return std::max(1.25 * cols, 165.0 + 0.25 * cols); }
+
+}  // namespace
+
+int plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, double* us) {
   int best = 0;
-  double best_cost = 0;
-  const int most = gated ? TN / 2 : TN, step = CHUNK;
-  for (int w = most; w >= step; w -= step) {
-    int64_t tiles[3] = {}, total = 0;
-    double cost[3] = {};
-    for (int i = 0; i < count; ++i) {
-      tiles[i] = static_cast<int64_t>(ceil_div(q[i].M, 2 * TM)) * ceil_div(q[i].N, w);
-      total += tiles[i];
-      const int kb = ceil_div(q[i].K, fp8 ? KB : KB / 2) * q[i].terms;
-      // a tile cannot end before its accumulator has been drained
-      cost[i] = std::max(kb * kblock_cycles(w, gated, q[i].b[0].mn_major), 8.0 * w * (gated ? 2 : 1) + 300);
-    }
-    // round r runs tiles [r pairs, (r + 1) pairs) of the products laid end to end
-    double sum = 0;
+  double best_ns = 0;
+  const int most = gated ? TN / 2 : TN;
+  for (int w = most; w >= CHUNK; w -= CHUNK) {
+    const int cols = gated ? 2 * w : w;
+    double ns = 12.0 * cols;  // the last tile's epilogue
     int64_t done = 0;
     for (int i = 0; i < count; ++i) {
-      const int64_t end = done + tiles[i];
-      const int64_t r0 = (done + pairs - 1) / pairs, r1 = (end + pairs - 1) / pairs;  // rounds that start in it
-      sum += static_cast<double>(r1 - r0) * cost[i];
+      const int kb = ceil_div(q[i].K, fp8 ? KB : KB / 2) * q[i].terms;
+      // a tile is as long as its K blocks, or the draining of its accumulator
+      const double tile = std::max(kb * kblock_ns(cols), 8.0 * cols + 300);
+      const int64_t end = done + static_cast<int64_t>(ceil_div(q[i].M, 2 * TM)) * ceil_div(q[i].N, w);
+      // rounds of one tile per pair over the products laid end to end: those that start in this one
+      ns += static_cast<double>((end + mc.pairs - 1) / mc.pairs - (done + mc.pairs - 1) / mc.pairs) * tile;
       done = end;
     }
-    sum += 12.0 * w * (gated ? 2 : 1);
-    if (!best || sum < 0.99 * best_cost) best = w, best_cost = sum;
+    if (!best || ns < 0.99 * best_ns) best = w, best_ns = ns;
   }
-  if (cycles) *cycles = best_cost;
+  if (us) *us = 4.0 + best_ns * 1e-3;
   return best;
 }
+
+namespace {
 
 template <int KIND, bool FP8>
 cudaError_t launch_pairs(const Args& p, int pairs, cudaStream_t s) {
@@ -522,7 +522,8 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
   Args p;
   std::memset(&p, 0, sizeof(p));
   p.count = count;
-  const int w = plan_width(q, count, fp8, e.kind == EPI_GATED, mc.pairs, nullptr);
+  const int w = plan_width(mc, q, count, fp8, e.kind == EPI_GATED, nullptr);
+  int stage = 0;
   bool ok = true;
   for (int i = 0; i < count; ++i) {
     const Product& c = q[i];
@@ -530,6 +531,7 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
     o.M = static_cast<int>(c.M), o.N = static_cast<int>(c.N);
     o.w = w;
     const int hb = e.kind == EPI_GATED ? o.w : o.w / 2;
+    stage = std::max(stage, A_BYTES + b_bytes(o.w, e.kind == EPI_GATED, c.b[0].mn_major));
     o.tiles_m = ceil_div(c.M, 2 * TM);
     o.tiles = o.tiles_m * ceil_div(c.N, o.w);
     o.kb_seg = ceil_div(c.K, fp8 ? KB : KB / 2);
@@ -545,9 +547,12 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
   if (e.out1) ok = ok && encode_out(&p.y1, e.out1, e.ld1, q[0].M, q[0].N);
   if (e.out2) ok = ok && encode_out(&p.y2, e.out2, e.ld2, q[0].M, q[0].N);
   if (!ok) return cudaErrorInvalidValue;
+  p.stage_bytes = static_cast<uint32_t>(stage);
+  p.stages = static_cast<uint32_t>(std::min(MAX_STAGES, STAGE_AREA / stage));
   p.has1 = e.out1 != nullptr;
   p.act = e.act;
   p.bias = static_cast<const __nv_bfloat16*>(e.bias);
+  p.bias_vec = reinterpret_cast<uintptr_t>(e.bias) % 16 == 0;
   p.residual = static_cast<const __nv_bfloat16*>(e.residual);
   p.ldr = e.ldr;
   p.sx = e.sx, p.sw0 = e.sw0, p.sw1 = e.sw1;

@@ -13,7 +13,6 @@
 
 #include <algorithm>
 #include <cstring>
-#include <cstdlib>
 
 #include "act.h"
 #include "block.h"
@@ -27,11 +26,10 @@ namespace {
 constexpr int FT = 128;                // accumulator rows of a tile
 constexpr int A_BYTES = FT * KB;       // weights of one K block
 constexpr int MAX_STAGES = 8;
-constexpr int MAX_SPLIT = 8;           // CTAs of a cluster
 constexpr int THREADS = 256;           // warp 0 TMA, warp 1 MMA, warps 4-7 drain; all add
 constexpr int SMEM_TAIL = 8 * (2 * MAX_STAGES + 2) + 16 + 1024;  // barriers, tensor memory slot, slack to align
 constexpr int SMEM_ONE = 232448;       // one CTA per SM
-constexpr int SMEM_TWO = 115712;       // two
+constexpr int SMEM_TWO = 114688;       // two
 
 struct Args {
   CUtensorMap a[2], b[2];
@@ -297,7 +295,7 @@ cudaError_t launch_split_as(const Args& p, int tiles, int S, int smem, cudaStrea
 
 }  // namespace
 
-cudaError_t configure_split() {
+cudaError_t configure_split(Machine* m) {
   const void* fns[] = {reinterpret_cast<const void*>(split_kernel<EPI_PLAIN, false>),
                        reinterpret_cast<const void*>(split_kernel<EPI_LINEAR, false>),
                        reinterpret_cast<const void*>(split_kernel<EPI_LINEAR, true>),
@@ -307,31 +305,62 @@ cudaError_t configure_split() {
     const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ONE);
     if (e != cudaSuccess) return e;
   }
+  for (int per_sm = 1; per_sm <= 2; ++per_sm)
+    for (int s = 1; s <= MAX_SPLIT; ++s) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(s));
+      cfg.blockDim = dim3(THREADS);
+      cfg.dynamicSmemBytes = per_sm == 2 ? SMEM_TWO : SMEM_ONE;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&m->clusters[per_sm - 1][s], split_kernel<EPI_GATED, false>, &cfg);
+      if (e != cudaSuccess) return e;
+    }
   return cudaSuccess;
 }
 
-SplitPlan plan_split(const Machine& mc, int64_t M, int64_t N, int64_t K, int terms, bool fp8, bool gated) {
+// Tokens of a tile, stages and the cluster size: the largest with which all
+// tiles are resident at once (a second round of clusters costs more than
+// longer slices) and a CTA still has four K blocks (below that the cluster's
+// additions cost more than the slices save).
+static SplitPlan plan_split(const Machine& mc, const Product& q, bool fp8, bool gated, double* us) {
   SplitPlan o;
-  const int kb = ceil_div(K, fp8 ? KB : KB / 2) * terms;
-  const int tiles_t = ceil_div(N, 256);
-  o.nt = ceil_div(ceil_div(N, tiles_t), 16) * 16;
-  const int64_t tiles = static_cast<int64_t>(tiles_t) * ceil_div(M, gated ? FT / 2 : FT);
+  const int kb = ceil_div(q.K, fp8 ? KB : KB / 2) * q.terms;
+  const int tiles_t = ceil_div(q.M, 256);
+  o.nt = ceil_div(ceil_div(q.M, tiles_t), 16) * 16;
+  const int64_t tiles = static_cast<int64_t>(tiles_t) * ceil_div(q.N, gated ? FT / 2 : FT);
   const int stage = A_BYTES + o.nt * KB;
   // two CTAs per SM while they hold at least three stages each
-  o.per_sm = (SMEM_TWO - SMEM_TAIL) / stage >= 3 ? 2 : 1;
-  o.stages = std::min(MAX_STAGES, ((o.per_sm == 2 ? SMEM_TWO : SMEM_ONE) - SMEM_TAIL) / stage);
-  if (getenv("TPO_STG")) o.stages = std::min(o.stages, atoi(getenv("TPO_STG")));
-  const int64_t places = static_cast<int64_t>(mc.sms) * o.per_sm;
-  o.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({MAX_SPLIT, kb, places / tiles})));
+  const int per_sm = (SMEM_TWO - SMEM_TAIL) / stage >= 3 ? 2 : 1;
+  o.stages = std::min(MAX_STAGES, ((per_sm == 2 ? SMEM_TWO : SMEM_ONE) - SMEM_TAIL) / stage);
+  o.split = 1;
+  for (int s = 2; s <= MAX_SPLIT && s * 4 <= kb; ++s)
+    if (tiles <= mc.clusters[per_sm - 1][s]) o.split = s;
+  // measured at one CTA per SM: 8.0 us and 0.32 us a K block with 192 tokens, 9.1 and 0.39 with 256
+  const int64_t places = std::max(1, mc.clusters[per_sm - 1][o.split]);
+  *us = 4.5 + 0.018 * o.nt +
+        static_cast<double>((tiles + places - 1) / places) * ((kb + o.split - 1) / o.split) * (0.13 + 0.001 * o.nt);
   return o;
 }
 
+// By rule: up to 128 tokens always (at 96 and 128 tokens it is level with the
+// pairs on 14336x4096 and 1024x1024, and ahead on 4096x4096, 13.5 to 17.2 us,
+// and 3584x8192, 17.3 to 27), up to 256 where the models say so, never above
+// (512 tokens, 4096x4096: 21.8 us, 18.2 on pairs).
 bool use_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t path, int64_t split,
                SplitPlan* plan) {
   if (path == 1 || (path == 0 && q.M > 256)) return false;
-  *plan = plan_split(mc, q.N, q.M, q.K, q.terms, fp8, gated);
+  double split_us = 0, pairs_us = 0;
+  *plan = plan_split(mc, q, fp8, gated, &split_us);
   if (split > 0) plan->split = static_cast<int>(std::min<int64_t>(split, ceil_div(q.K, fp8 ? KB : KB / 2) * q.terms));
-  return true;
+  if (path == 2 || q.M <= 128) return true;
+  plan_width(mc, &q, 1, fp8, gated, &pairs_us);
+  return split_us < pairs_us;
 }
 
 cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, const Epi& e, uint32_t* err,
