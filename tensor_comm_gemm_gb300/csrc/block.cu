@@ -280,7 +280,7 @@ tpo_status tpo_layer_norm(tpo_block* b, int64_t n, int64_t k, int dtype, int wdt
   tpo::NormArgs a{};
   a.n = n, a.k = k, a.x = x, a.ldx = ldx, a.gamma = gamma, a.beta = beta, a.eps = eps;
   a.y = y, a.ldy = ldy, a.mean = mean, a.rstd = rstd;
-  return launched(tpo::launch_norm(a, dtype, wdtype, static_cast<cudaStream_t>(stream)));
+  return launched(tpo::launch_norm(b->machine, a, dtype, wdtype, static_cast<cudaStream_t>(stream)));
 }
 
 tpo_status tpo_layer_norm_bwd(tpo_block* b, int64_t n, int64_t k, int dtype, int wdtype, const void* dy,
@@ -309,7 +309,7 @@ tpo_status tpo_layer_norm_bwd(tpo_block* b, int64_t n, int64_t k, int dtype, int
   a.n = n, a.k = k, a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.gamma = gamma, a.dres = dres;
   a.lddres = lddres, a.y = n > 0 ? dx : nullptr, a.ldy = lddx, a.dgamma = dgamma, a.dbeta = dbeta;
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
-  return launched(tpo::launch_norm_bwd(a, dtype, wdtype, reinterpret_cast<float*>(b->ws()),
+  return launched(tpo::launch_norm_bwd(b->machine, a, dtype, wdtype, reinterpret_cast<float*>(b->ws()),
                                        static_cast<cudaStream_t>(stream)));
 }
 

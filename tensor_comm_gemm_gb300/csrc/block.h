@@ -96,10 +96,10 @@ cudaError_t launch_act_bwd(int64_t n, int64_t m, int act, const void* dy, int64_
 cudaError_t launch_gated_act_bwd(int64_t n, int64_t m, int act, const void* dh, int64_t lddh, const void* g,
                                  int64_t ldg, const void* u, int64_t ldu, void* dg, void* du, int64_t ldo,
                                  cudaStream_t s);
-cudaError_t launch_norm(const NormArgs& a, int dtype, int wdtype, cudaStream_t s);
+cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdtype, cudaStream_t s);
 // part: workspace of min(n, NORM_PARTS) x 2 x k floats, the blocks' sums for dgamma and dbeta.
 constexpr int NORM_PARTS = 304;
-cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, int wdtype, float* part, cudaStream_t s);
+cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int wdtype, float* part, cudaStream_t s);
 
 void set_last_error(const char* msg);  // ctx.cu: the message tpo_last_error returns
 

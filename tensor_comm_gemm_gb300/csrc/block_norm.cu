@@ -8,12 +8,17 @@
 // of the vector, take VEC = 1.  Rows too long for that are walked by one block
 // in several passes.
 //
-// Backward, a block takes rows g, g + G, ... and keeps the sums over its rows
-// of dy xhat and dy for the columns its threads own in fp32 registers; they go
-// to the workspace once, and a second kernel adds the blocks' sums in a fixed
-// order.
+// With many rows a block is persistent: its row groups take rows g, g + G, ...,
+// and every thread keeps the vectors of its next rows in flight with
+// asynchronous copies into its own part of shared memory (three to four rows
+// ahead, ~190 KB per SM), so no barrier is needed before they are read.
+//
+// Backward, a block also keeps the sums over its rows of dy xhat and dy for the
+// columns its threads own in fp32 registers; they go to the workspace once,
+// and a second kernel adds the blocks' sums in a fixed order.
 
 #include <algorithm>
+#include <cstring>
 
 #include <cuda_bf16.h>
 
@@ -123,6 +128,383 @@ __global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int tpr) {
   }
 }
 
+// ------------------------------------------------------------------ many rows
+
+// One value (L = 1) or two at a time (L = 2: the packed fp32 operations, which
+// halve the instructions that otherwise bound these kernels).
+template <int L>
+struct Num;
+template <>
+struct Num<1> {
+  float v;
+};
+template <>
+struct Num<2> {
+  uint64_t v;
+};
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+template <int L>
+__device__ __forceinline__ Num<L> all(float x) {
+  if constexpr (L == 1) return {x};
+  else return {pack2(x, x)};
+}
+__device__ __forceinline__ Num<1> add(Num<1> a, Num<1> b) { return {a.v + b.v}; }
+__device__ __forceinline__ Num<1> mul(Num<1> a, Num<1> b) { return {a.v * b.v}; }
+__device__ __forceinline__ Num<1> fma(Num<1> a, Num<1> b, Num<1> c) { return {fmaf(a.v, b.v, c.v)}; }
+__device__ __forceinline__ Num<2> add(Num<2> a, Num<2> b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return {r};
+}
+__device__ __forceinline__ Num<2> mul(Num<2> a, Num<2> b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return {r};
+}
+__device__ __forceinline__ Num<2> fma(Num<2> a, Num<2> b, Num<2> c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return {r};
+}
+__device__ __forceinline__ float total(Num<1> a) { return a.v; }
+__device__ __forceinline__ float total(Num<2> a) {
+  float x, y;
+  unpack2(a.v, x, y);
+  return x + y;
+}
+
+// A vector's elements as fp32, and back (rounded).
+template <class T, int VEC, int L>
+__device__ __forceinline__ void to_nums(const Vec<T, VEC>& v, Num<L> (&o)[VEC / L]) {
+  if constexpr (L == 1) {
+    o[0].v = to_f(v.e[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) o[j].v = pack2(v.e[2 * j], v.e[2 * j + 1]);
+  } else {
+    uint32_t w[VEC / 2];
+    memcpy(w, &v, sizeof(w));
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) o[j].v = pack2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+  }
+}
+template <class T, int VEC, int L>
+__device__ __forceinline__ Vec<T, VEC> from_nums(const Num<L> (&a)[VEC / L]) {
+  Vec<T, VEC> v;
+  if constexpr (L == 1) {
+    put(&v.e[0], a[0].v);
+  } else {
+    uint32_t w[VEC / 2];
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+      float x, y;
+      unpack2(a[j].v, x, y);
+      if constexpr (sizeof(T) == 4) {
+        v.e[2 * j] = x;
+        v.e[2 * j + 1] = y;
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        memcpy(&w[j], &h, 4);
+      }
+    }
+    if constexpr (sizeof(T) == 2) memcpy(&v, w, sizeof(w));
+  }
+  return v;
+}
+
+// Asynchronous copy of one vector (4 or 16 bytes) to this thread's shared
+// memory; zeros (and no access to src) if it does not exist.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool exists) {
+  const int n = exists ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `ahead` of this thread's latest copy groups are in flight.
+__device__ __forceinline__ void copy_wait(int ahead) {
+  if (ahead >= 3)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (ahead == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+// Sums over the `tpr` threads of a row group, as row_sum, with a barrier of the group alone.
+__device__ __forceinline__ float2 group_sum(float a, float b, int tpr, float2* red) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1)
+    if (d < tpr) {
+      a += __shfl_xor_sync(0xffffffffu, a, d);
+      b += __shfl_xor_sync(0xffffffffu, b, d);
+    }
+  if (tpr > 32) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5, first = warp & ~(per - 1);
+    if (lane == 0) red[warp] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + first / per), "r"(tpr) : "memory");
+    const float2 v = red[first + (lane & (per - 1))];
+    a = v.x;
+    b = v.y;
+#pragma unroll
+    for (int d = 8; d; d >>= 1)
+      if (d < per) {
+        a += __shfl_xor_sync(0xffffffffu, a, d);
+        b += __shfl_xor_sync(0xffffffffu, b, d);
+      }
+  }
+  return make_float2(a, b);
+}
+
+constexpr int RING_THREADS = 512;
+
+// Forward: `depth` rows of each group are in flight or in use.  FULL: the
+// group's vectors are exactly a row's.
+template <class T, class W, int VEC, int NV, bool FULL>
+__global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormArgs a, int tpr, int depth) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[4][RING_THREADS / 32];
+  constexpr int B = VEC * sizeof(T), L = VEC > 1 ? 2 : 1, NN = VEC / L;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & (tpr - 1), groups = RING_THREADS / tpr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / tpr;
+  const int k = static_cast<int>(a.k);
+  uint8_t* const mine = ring + threadIdx.x * B;
+  auto fetch = [&](int64_t r, int slot) {
+    const bool live = r < a.n;
+    const T* x = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * tpr) * VEC;
+      copy_async<B>(smem_u32(mine) + (slot * NV + i) * (RING_THREADS * B), x + (FULL || c < k ? c : 0),
+                    live && (FULL || c < k));
+    }
+    copy_commit();
+  };
+  for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
+  const W *gamma = static_cast<const W*>(a.gamma), *beta = static_cast<const W*>(a.beta);
+  const float inv_k = 1.0f / static_cast<float>(k);
+  int slot = 0, buf = 0;
+  // every group of the block runs the same number of rounds: warps that hold several rows stay whole
+  const int64_t sets = (a.n + groups - 1) / groups;
+  for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
+    const bool live = row < a.n;
+    copy_wait(depth - 1);
+    Num<L> v[NV][NN], s = all<L>(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(mine + (slot * NV + i) * (RING_THREADS * B)), v[i]);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) s = add(s, v[i][j]);
+    }
+    fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+    const float mean = group_sum(total(s), 0.0f, tpr, red[buf]).x * inv_k;
+    const Num<L> minus = all<L>(-mean);
+    s = all<L>(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < NN; ++j) {
+        v[i][j] = add(v[i][j], minus);
+        if constexpr (!FULL)
+          if ((lane + i * tpr) * VEC >= k) v[i][j] = all<L>(0.0f);
+        s = fma(v[i][j], v[i][j], s);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(group_sum(total(s), 0.0f, tpr, red[buf + 1]).x * inv_k + a.eps);
+    const Num<L> scale = all<L>(rstd);
+    T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * tpr) * VEC;
+      if (!FULL && c >= k) continue;
+      Num<L> g[NN], b[NN];
+      if (gamma) to_nums<W, VEC, L>(load<W, VEC>(gamma + c), g);
+      if (beta) to_nums<W, VEC, L>(load<W, VEC>(beta + c), b);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) {
+        v[i][j] = mul(v[i][j], scale);
+        if (gamma) v[i][j] = mul(v[i][j], g[j]);
+        if (beta) v[i][j] = add(v[i][j], b[j]);
+      }
+      if (live) *reinterpret_cast<Vec<T, VEC>*>(y + c) = from_nums<T, VEC, L>(v[i]);
+    }
+    if (live && lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    if (++slot == depth) slot = 0;
+    buf ^= 2;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Adds the sums of a block's row groups one group after another (a fixed
+// order) and stores them: part[blockIdx.x][2][k].  `sums`: k floats of shared memory.
+template <int VEC, int NV>
+__device__ __forceinline__ void store_sums(const float (&dg)[NV][VEC], const float (&db)[NV][VEC], int64_t k, int tpr,
+                                           float* sums, float* part) {
+  const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * k;
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+    for (int q = 0; q < groups; ++q) {
+      if (groups > 1) __syncthreads();
+      if (q != group) continue;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const int c = (lane + i * tpr) * VEC + j;
+          if (c >= k) continue;
+          float v = which ? db[i][j] : dg[i][j];
+          if (q > 0) v += sums[c];
+          if (q + 1 < groups)
+            sums[c] = v;
+          else
+            out[which * k + c] = v;
+        }
+    }
+}
+
+// Backward, rows in flight as forward: x, dy and (if given) dres of a row.
+template <class T, class W, int VEC, int NV>
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const NormArgs a, int tpr, int depth,
+                                                                        float* part) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][RING_THREADS / 32];
+  constexpr int B = VEC * sizeof(T), L = VEC > 1 ? 2 : 1, NN = VEC / L;
+  constexpr bool KEEP = NV * VEC <= 16;  // xhat and dy gamma stay in registers from the sums to dx
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & (tpr - 1), groups = RING_THREADS / tpr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / tpr;
+  const int k = static_cast<int>(a.k);
+  const int arrays = a.dres && a.y ? 3 : 2;
+  uint8_t* const mine = ring + threadIdx.x * B;
+  auto at = [&](int slot, int which, int i) { return mine + ((slot * arrays + which) * NV + i) * (RING_THREADS * B); };
+  // a vector past the row's end, or of a row past the last, is zeros: it adds nothing to any sum
+  auto fetch = [&](int64_t r, int slot) {
+    const bool live = r < a.n;
+    const int64_t q = live ? r : 0;
+    const T *x = static_cast<const T*>(a.x) + q * a.ldx, *dy = static_cast<const T*>(a.dy) + q * a.lddy;
+    const T* dres = static_cast<const T*>(a.dres) + q * a.lddres;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * tpr) * VEC;
+      const bool in = live && c < k;
+      const int o = in ? c : 0;
+      copy_async<B>(smem_u32(at(slot, 0, i)), x + o, in);
+      copy_async<B>(smem_u32(at(slot, 1, i)), dy + o, in);
+      if (arrays == 3) copy_async<B>(smem_u32(at(slot, 2, i)), dres + o, in);
+    }
+    copy_commit();
+  };
+  for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
+  const W* gamma = static_cast<const W*>(a.gamma);
+  Num<L> dg[NV][NN], db[NV][NN];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < NN; ++j) dg[i][j] = db[i][j] = all<L>(0.0f);
+  const float inv_k = 1.0f / static_cast<float>(k);
+  int slot = 0, buf = 0;
+  float mean = row < a.n ? a.mean[row] : 0.0f, rstd = row < a.n ? a.rstd[row] : 0.0f;
+  const int64_t sets = (a.n + groups - 1) / groups;
+  for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
+    const bool live = row < a.n;
+    const float mean_n = row + step < a.n ? a.mean[row + step] : 0.0f;
+    const float rstd_n = row + step < a.n ? a.rstd[row + step] : 0.0f;
+    copy_wait(depth - 1);
+    const Num<L> minus = all<L>(-mean), scale = all<L>(rstd);
+    Num<L> s1 = all<L>(0.0f), s2 = s1;
+    // xhat and w = dy gamma of vector i
+    auto values = [&](int i, Num<L>(&h)[NN], Num<L>(&w)[NN], bool first) {
+      const int c = (lane + i * tpr) * VEC;
+      Num<L> g[NN];
+      to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 0, i)), h);
+      to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 1, i)), w);
+      if (gamma) to_nums<W, VEC, L>(load<W, VEC>(gamma + (c < k ? c : 0)), g);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) {
+        h[j] = mul(add(h[j], minus), scale);
+        if (first) {
+          dg[i][j] = fma(w[j], h[j], dg[i][j]);
+          db[i][j] = add(db[i][j], w[j]);
+        }
+        if (gamma) w[j] = mul(w[j], g[j]);
+      }
+    };
+    Num<L> hk[KEEP ? NV : 1][NN], wk[KEEP ? NV : 1][NN];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Num<L>(&h)[NN] = hk[KEEP ? i : 0];
+      Num<L>(&w)[NN] = wk[KEEP ? i : 0];
+      values(i, h, w, true);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) {
+        s1 = add(s1, w[j]);
+        s2 = fma(w[j], h[j], s2);
+      }
+    }
+    if (a.y) {
+      const float2 t = group_sum(total(s1), total(s2), tpr, red[buf]);
+      const Num<L> m1 = all<L>(-t.x * inv_k), m2 = all<L>(-t.y * inv_k);
+      T* o = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        Num<L>(&h)[NN] = hk[KEEP ? i : 0];
+        Num<L>(&w)[NN] = wk[KEEP ? i : 0];
+        if constexpr (!KEEP) values(i, h, w, false);
+        Num<L> r[NN];
+        if (arrays == 3) to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 2, i)), r);
+#pragma unroll
+        for (int j = 0; j < NN; ++j) {
+          const Num<L> q = fma(h[j], m2, add(w[j], m1));
+          r[j] = arrays == 3 ? fma(q, scale, r[j]) : mul(q, scale);
+        }
+        const int c = (lane + i * tpr) * VEC;
+        if (live && c < k) *reinterpret_cast<Vec<T, VEC>*>(o + c) = from_nums<T, VEC, L>(r);
+      }
+    }
+    fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+    if (++slot == depth) slot = 0;
+    buf ^= 1;
+    mean = mean_n;
+    rstd = rstd_n;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!part) return;
+  __syncthreads();  // the ring is free: it holds the columns' sums now
+  float fg[NV][VEC], fb[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < NN; ++j) {
+      if constexpr (L == 2) {
+        unpack2(dg[i][j].v, fg[i][2 * j], fg[i][2 * j + 1]);
+        unpack2(db[i][j].v, fb[i][2 * j], fb[i][2 * j + 1]);
+      } else {
+        fg[i][j] = dg[i][j].v;
+        fb[i][j] = db[i][j].v;
+      }
+    }
+  store_sums<VEC, NV>(fg, fb, a.k, tpr, reinterpret_cast<float*>(ring), part);
+}
+
+// ------------------------------------------------------------------ rows of any alignment
+
 // The gradient: block g takes the row sets g, g + gridDim.x, ... of blockDim.x
 // / tpr rows each; the next set's loads are in flight while a set is summed.
 // part: [gridDim.x][2][k] fp32, this block's sums (NULL: not wanted).
@@ -211,28 +593,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a, int tpr
     rstd = rstd_n;
   }
   if (!part) return;
-  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * a.k;
-  // the block's row groups one after another: a fixed order of additions
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    for (int q = 0; q < groups; ++q) {
-      if (groups > 1) __syncthreads();
-      if (q != group) continue;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int c = (lane + i * tpr) * VEC + j;
-          if (c >= a.k) continue;
-          float v = which ? db[i][j] : dg[i][j];
-          if (q > 0) v += sums[c];
-          if (q + 1 < groups)
-            sums[c] = v;
-          else
-            out[which * a.k + c] = v;
-        }
-    }
-  }
+  store_sums<VEC, NV>(dg, db, a.k, tpr, sums, part);
 }
 
 // ------------------------------------------------------------------ long rows
@@ -357,17 +718,51 @@ Share share(int64_t vecs, int nv, int most_nv, int most_tpr) {
   return s;
 }
 
+// Rows in flight per group and the shared memory they take; depth < 2: they do not fit.
+struct Ring {
+  int depth;
+  size_t smem;
+};
+Ring ring_of(int nv, int vec_bytes, int arrays, int64_t k, size_t most) {
+  const size_t slot = static_cast<size_t>(RING_THREADS) * nv * vec_bytes * arrays;
+  Ring r;
+  r.depth = static_cast<int>(std::min<size_t>(4, most / slot));
+  r.smem = std::max(slot * r.depth, static_cast<size_t>(k) * 4);  // also holds one row of fp32 sums
+  return r;
+}
+
+template <class K>
+cudaError_t allow_smem(K* kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+}
+
 }  // namespace
 
-cudaError_t launch_norm(const NormArgs& a, int dtype, int wdtype, cudaStream_t s) {
+cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdtype, cudaStream_t s) {
   return with_types(dtype, wdtype, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
     constexpr int V = 16 / sizeof(T);
     const bool vec = a.k % V == 0 && vec_ok(a.x, a.ldx, a.n, sizeof(T)) && vec_ok(a.y, a.ldy, a.n, sizeof(T)) &&
                      vec_ok(a.gamma, 0, 1, 4) && vec_ok(a.beta, 0, 1, 4);
-    // few rows: as many threads per row as there are vectors; many: four vectors a thread
-    const Share h = share(vec ? a.k / V : a.k, a.n >= 608 ? 4 : 1, 8, 512);
+    const int64_t vecs = vec ? a.k / V : a.k;
+    // Several rows for every group of a persistent block (two blocks of 512
+    // threads per SM, four vectors a thread): keep rows in flight.  Fewer rows:
+    // one row per group, as many threads as it has vectors (latency).
+    const Share m = share(vecs, 4, 8, RING_THREADS);
+    if (m.tpr && vec && a.n >= static_cast<int64_t>(mc.sms) * 4 * (RING_THREADS / m.tpr)) {
+      const Ring r = ring_of(m.nv, 16, 1, 0, 100 * 1024);
+      const int64_t sets = (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr);
+      const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sets, 2 * mc.sms)));
+      auto run = [&](auto kernel) {
+        cudaError_t e = allow_smem(kernel);
+        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(RING_THREADS), r.smem, s, a, m.tpr, r.depth);
+      };
+      const bool full = static_cast<int64_t>(m.tpr) * m.nv == vecs;
+      if (m.nv == 4) return full ? run(norm_ring_kernel<T, W, V, 4, true>) : run(norm_ring_kernel<T, W, V, 4, false>);
+      return full ? run(norm_ring_kernel<T, W, V, 8, true>) : run(norm_ring_kernel<T, W, V, 8, false>);
+    }
+    const Share h = share(vecs, 1, 8, 512);
     if (!h.tpr) return launch_pdl(norm_long_kernel<T, W>, dim3(static_cast<unsigned>(a.n)), dim3(1024), 0, s, a);
     const int threads = std::max(h.tpr, 128), rows = threads / h.tpr;
     const dim3 grid(static_cast<unsigned>((a.n + rows - 1) / rows));
@@ -379,7 +774,7 @@ cudaError_t launch_norm(const NormArgs& a, int dtype, int wdtype, cudaStream_t s
   });
 }
 
-cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, int wdtype, float* part, cudaStream_t s) {
+cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int wdtype, float* part, cudaStream_t s) {
   return with_types(dtype, wdtype, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
@@ -388,20 +783,45 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, int wdtype, float* par
     const bool vec = a.k % V == 0 && vec_ok(a.x, a.ldx, a.n, sizeof(T)) && vec_ok(a.dy, a.lddy, a.n, sizeof(T)) &&
                      vec_ok(a.dres, a.lddres, a.n, sizeof(T)) && vec_ok(a.y, a.ldy, a.n, sizeof(T)) &&
                      vec_ok(a.gamma, 0, 1, 4);
-    const Share h = share(vec ? a.k / V : a.k, 1, vec ? 2 : 16, 512);
+    const int64_t vecs = vec ? a.k / V : a.k;
     if (!wants) part = nullptr;
     int parts = 0;
     cudaError_t e = cudaSuccess;
-    if (h.tpr && a.n > 0) {
-      const int threads = std::max(h.tpr, 256), rows = threads / h.tpr;
-      parts = static_cast<int>(std::min<int64_t>((a.n + rows - 1) / rows, NORM_PARTS));
-      const size_t smem = rows > 1 ? static_cast<size_t>(a.k) * 4 : 0;
-      e = with_nv(h.nv, [&](auto nv) {
-        constexpr int NV = decltype(nv)::value;
-        constexpr int NW = NV <= 2 ? NV : 2;
-        if (vec) return launch_pdl(norm_bwd_kernel<T, W, V, NW>, dim3(parts), dim3(threads), smem, s, a, h.tpr, part);
-        return launch_pdl(norm_bwd_kernel<T, W, 1, NV>, dim3(parts), dim3(threads), smem, s, a, h.tpr, part);
-      });
+    // 16-byte vectors, or single 4-byte elements, can be copied asynchronously
+    const bool async = vec || sizeof(T) == 4;
+    const Share h = share(vecs, vec ? 2 : 4, vec ? (sizeof(T) == 4 ? 8 : 4) : 16, RING_THREADS);
+    const Ring r = ring_of(h.nv, vec ? 16 : 4, a.dres && a.y ? 3 : 2, a.k, 200 * 1024);
+    if (async && h.tpr && r.depth >= 2 && a.n > 0) {
+      const int64_t sets = (a.n + RING_THREADS / h.tpr - 1) / (RING_THREADS / h.tpr);
+      parts = static_cast<int>(std::min<int64_t>({sets, mc.sms, NORM_PARTS}));
+      auto run = [&](auto kernel) {
+        const cudaError_t c = allow_smem(kernel);
+        return c != cudaSuccess ? c : launch_pdl(kernel, dim3(parts), dim3(RING_THREADS), r.smem, s, a, h.tpr, r.depth, part);
+      };
+      if (vec && h.nv == 2)
+        e = run(norm_bwd_ring_kernel<T, W, V, 2>);
+      else if (vec && h.nv == 4)
+        e = run(norm_bwd_ring_kernel<T, W, V, 4>);
+      else if constexpr (sizeof(T) == 4) {
+        if (vec)
+          e = run(norm_bwd_ring_kernel<T, W, V, 8>);
+        else if (h.nv == 4)
+          e = run(norm_bwd_ring_kernel<T, W, 1, 4>);
+        else if (h.nv == 8)
+          e = run(norm_bwd_ring_kernel<T, W, 1, 8>);
+        else
+          e = run(norm_bwd_ring_kernel<T, W, 1, 16>);
+      }
+    } else if (const Share q = share(a.k, 1, 8, 512); !async && q.tpr && a.n > 0) {
+      if constexpr (sizeof(T) == 2) {
+        const int threads = std::max(q.tpr, 256), rows = threads / q.tpr;
+        parts = static_cast<int>(std::min<int64_t>((a.n + rows - 1) / rows, NORM_PARTS));
+        const size_t smem = rows > 1 ? static_cast<size_t>(a.k) * 4 : 0;
+        e = with_nv(q.nv, [&](auto nv) {
+          constexpr int NV = decltype(nv)::value <= 8 ? decltype(nv)::value : 8;
+          return launch_pdl(norm_bwd_kernel<T, W, 1, NV>, dim3(parts), dim3(threads), smem, s, a, q.tpr, part);
+        });
+      }
     } else if (a.n > 0) {
       // the weights' gradients first: dx may overwrite dy
       parts = static_cast<int>(std::min<int64_t>(a.n, 32));
