@@ -81,6 +81,7 @@ struct NormArgs {
   float *mean, *rstd;              // forward: written; backward: read
   void *dgamma, *dbeta;
   float eps;
+  uint32_t* err;                   // the handle's error word
 };
 
 // out0 and out1 (of TPO_BF16 or TPO_F32, NULL: not wanted) from per-block sums part[parts][vectors][cols].

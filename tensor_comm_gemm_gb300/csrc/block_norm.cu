@@ -219,15 +219,9 @@ __device__ __forceinline__ Vec<T, VEC> from_nums(const Num<L> (&a)[VEC / L]) {
   return v;
 }
 
-// Asynchronous copy of one vector (4 or 16 bytes) to this thread's shared
-// memory; zeros (and no access to src) if it does not exist.
-template <int BYTES>
+// Asynchronous copy of 16 bytes to shared memory; zeros (and no access to src) if they do not exist.
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool exists) {
-  const int n = exists ? BYTES : 0;
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(exists ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most `ahead` of this thread's latest copy groups are in flight.
@@ -236,8 +230,44 @@ __device__ __forceinline__ void copy_wait(int ahead) {
     asm volatile("cp.async.wait_group 3;" ::: "memory");
   else if (ahead == 2)
     asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else
+  else if (ahead == 1)
     asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+// Rows in flight.  With VEC > 1 (16-byte rows) a thread copies the vectors that
+// it will read itself, so it needs no barrier before them.  With VEC = 1 the
+// group copies the whole 16-byte units inside the row, to the same offset
+// modulo 16, and reads single elements after a barrier; the few elements
+// outside those units are read from global memory.
+__device__ __forceinline__ uint32_t row_bytes(int k, int elem) { return ((k * elem + 15) & ~15) + 16; }
+template <class T>
+__device__ __forceinline__ void copy_units(const T* src, int k, uint32_t dst, int lane, int tpr) {
+  const uint64_t p = reinterpret_cast<uint64_t>(src), lo = (p + 15) & ~15ull, hi = (p + k * sizeof(T)) & ~15ull;
+  const int units = hi > lo ? static_cast<int>((hi - lo) >> 4) : 0;
+  const uint32_t to = dst + ((p & 15) ? 16u : 0u);
+  for (int u = lane; u < units; u += tpr) copy_async(to + 16u * u, reinterpret_cast<const void*>(lo + 16ull * u), true);
+}
+template <class T>
+struct Units {  // a row that copy_units has copied
+  const T* src;
+  const uint8_t* at;  // element c at `at + c * sizeof(T)`
+  int lo, hi;         // elements [lo, hi) are there
+  __device__ __forceinline__ Units(const T* p, const uint8_t* slot, int k) : src(p) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uint64_t>(p)) & 15u;
+    at = slot + off;
+    lo = static_cast<int>(((16u - off) & 15u) / sizeof(T));
+    hi = k - static_cast<int>(((off + static_cast<uint32_t>(k) * sizeof(T)) & 15u) / sizeof(T));
+  }
+  __device__ __forceinline__ T operator[](int c) const {
+    return c >= lo && c < hi ? *reinterpret_cast<const T*>(at + c * sizeof(T)) : src[c];
+  }
+};
+__device__ __forceinline__ void group_barrier(int tpr) {
+  if (tpr > 32)
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / tpr), "r"(tpr) : "memory");
+  else
+    __syncwarp();
 }
 // Sums over the `tpr` threads of a row group, as row_sum, with a barrier of the group alone.
 __device__ __forceinline__ float2 group_sum(float a, float b, int tpr, float2* red) {
@@ -250,7 +280,7 @@ __device__ __forceinline__ float2 group_sum(float a, float b, int tpr, float2* r
   if (tpr > 32) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5, first = warp & ~(per - 1);
     if (lane == 0) red[warp] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + first / per), "r"(tpr) : "memory");
+    group_barrier(tpr);
     const float2 v = red[first + (lane & (per - 1))];
     a = v.x;
     b = v.y;
@@ -269,45 +299,75 @@ constexpr int RING_THREADS = 512;
 // Forward: `depth` rows of each group are in flight or in use.  FULL: the
 // group's vectors are exactly a row's.
 template <class T, class W, int VEC, int NV, bool FULL>
-__global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormArgs a, int tpr, int depth) {
+__global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormArgs a, int tpr, int depth, int weights) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[4][RING_THREADS / 32];
-  constexpr int B = VEC * sizeof(T), L = VEC > 1 ? 2 : 1, NN = VEC / L;
+  constexpr int L = VEC > 1 ? 2 : 1, NN = VEC / L;
   grid_dep_launch();
   grid_dep_wait();
-  const int lane = threadIdx.x & (tpr - 1), groups = RING_THREADS / tpr;
+  const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = RING_THREADS / tpr;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / tpr;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
   const int k = static_cast<int>(a.k);
-  uint8_t* const mine = ring + threadIdx.x * B;
+  // slot s of this thread's vectors, or of its group's row
+  const uint32_t slot_bytes = VEC > 1 ? NV * RING_THREADS * 16 : groups * row_bytes(k, sizeof(T));
+  uint8_t* const mine = ring + (VEC > 1 ? threadIdx.x * 16 : group * row_bytes(k, sizeof(T)));
   auto fetch = [&](int64_t r, int slot) {
     const bool live = r < a.n;
     const T* x = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
+    const uint32_t to = smem_u32(mine) + slot * slot_bytes;
+    if constexpr (VEC > 1) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * tpr) * VEC;
-      copy_async<B>(smem_u32(mine) + (slot * NV + i) * (RING_THREADS * B), x + (FULL || c < k ? c : 0),
-                    live && (FULL || c < k));
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * tpr) * VEC;
+        copy_async(to + i * (RING_THREADS * 16), x + (FULL || c < k ? c : 0), live && (FULL || c < k));
+      }
+    } else if (live) {
+      copy_units(x, k, to, lane, tpr);
     }
     copy_commit();
   };
-  for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
+  for (int d = 0; d < depth - (VEC == 1); ++d) fetch(row + d * step, d);
+  // gamma and beta stay in shared memory if they fit beside the rows
   const W *gamma = static_cast<const W*>(a.gamma), *beta = static_cast<const W*>(a.beta);
+  if (weights) {
+    W* keep = reinterpret_cast<W*>(ring + depth * slot_bytes);
+    for (int c = threadIdx.x * VEC; c < k; c += RING_THREADS * VEC) {
+      if (gamma) *reinterpret_cast<Vec<W, VEC>*>(keep + c) = load<W, VEC>(gamma + c);
+      if (beta) *reinterpret_cast<Vec<W, VEC>*>(keep + k + c) = load<W, VEC>(beta + c);
+    }
+    if (gamma) gamma = keep;
+    if (beta) beta = keep + k;
+    __syncthreads();
+  }
   const float inv_k = 1.0f / static_cast<float>(k);
   int slot = 0, buf = 0;
   // every group of the block runs the same number of rounds: warps that hold several rows stay whole
   const int64_t sets = (a.n + groups - 1) / groups;
   for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
     const bool live = row < a.n;
-    copy_wait(depth - 1);
     Num<L> v[NV][NN], s = all<L>(0.0f);
+    if constexpr (VEC > 1) {
+      copy_wait(depth - 1);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(mine + (slot * NV + i) * (RING_THREADS * B)), v[i]);
+      for (int i = 0; i < NV; ++i)
+        to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(mine + slot * slot_bytes + i * (RING_THREADS * 16)), v[i]);
+      fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+    } else {
+      copy_wait(depth - 2);
+      group_barrier(tpr);  // the row is there, and every thread is done with the one before
+      fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+      const Units<T> x(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx, mine + slot * slot_bytes, k);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = lane + i * tpr;
+        v[i][0].v = live && c < k ? to_f(x[c]) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < NN; ++j) s = add(s, v[i][j]);
-    }
-    fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
     const float mean = group_sum(total(s), 0.0f, tpr, red[buf]).x * inv_k;
     const Num<L> minus = all<L>(-mean);
     s = all<L>(0.0f);
@@ -349,18 +409,28 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Adds the sums of a block's row groups one group after another (a fixed
-// order) and stores them: part[blockIdx.x][2][k].  `sums`: k floats of shared memory.
+// Adds the sums of a block's row groups, inside a warp by shuffles and then one
+// after another (a fixed order), and stores them: part[blockIdx.x][2][k].
+// `sums`: k floats of shared memory.
 template <int VEC, int NV>
-__device__ __forceinline__ void store_sums(const float (&dg)[NV][VEC], const float (&db)[NV][VEC], int64_t k, int tpr,
-                                           float* sums, float* part) {
-  const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+__device__ __forceinline__ void store_sums(float (&dg)[NV][VEC], float (&db)[NV][VEC], int64_t k, int tpr, float* sums,
+                                           float* part) {
+  for (int d = tpr; d < 32; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        dg[i][j] += __shfl_xor_sync(0xffffffffu, dg[i][j], d);
+        db[i][j] += __shfl_xor_sync(0xffffffffu, db[i][j], d);
+      }
+  const int wide = tpr < 32 ? 32 : tpr;  // threads that now hold one set of sums
+  const int lane = threadIdx.x & (wide - 1), group = threadIdx.x / wide, groups = blockDim.x / wide;
   float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * k;
 #pragma unroll
   for (int which = 0; which < 2; ++which)
     for (int q = 0; q < groups; ++q) {
       if (groups > 1) __syncthreads();
-      if (q != group) continue;
+      if (q != group || lane >= tpr) continue;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -383,36 +453,55 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
                                                                         float* part) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][RING_THREADS / 32];
-  constexpr int B = VEC * sizeof(T), L = VEC > 1 ? 2 : 1, NN = VEC / L;
+  constexpr int L = VEC > 1 ? 2 : 1, NN = VEC / L;
   constexpr bool KEEP = NV * VEC <= 16;  // xhat and dy gamma stay in registers from the sums to dx
   grid_dep_launch();
   grid_dep_wait();
-  const int lane = threadIdx.x & (tpr - 1), groups = RING_THREADS / tpr;
+  const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = RING_THREADS / tpr;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / tpr;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
   const int k = static_cast<int>(a.k);
   const int arrays = a.dres && a.y ? 3 : 2;
-  uint8_t* const mine = ring + threadIdx.x * B;
-  auto at = [&](int slot, int which, int i) { return mine + ((slot * arrays + which) * NV + i) * (RING_THREADS * B); };
+  // slot s, matrix w: this thread's vectors, or its group's row
+  const uint32_t part_bytes = VEC > 1 ? NV * RING_THREADS * 16 : groups * row_bytes(k, sizeof(T));
+  uint8_t* const mine = ring + (VEC > 1 ? threadIdx.x * 16 : group * row_bytes(k, sizeof(T)));
+  auto at = [&](int slot, int which) { return mine + (slot * arrays + which) * part_bytes; };
   // a vector past the row's end, or of a row past the last, is zeros: it adds nothing to any sum
   auto fetch = [&](int64_t r, int slot) {
     const bool live = r < a.n;
     const int64_t q = live ? r : 0;
     const T *x = static_cast<const T*>(a.x) + q * a.ldx, *dy = static_cast<const T*>(a.dy) + q * a.lddy;
     const T* dres = static_cast<const T*>(a.dres) + q * a.lddres;
+    const uint32_t tx = smem_u32(at(slot, 0)), td = smem_u32(at(slot, 1)), tr = smem_u32(at(slot, 2));
+    if constexpr (VEC > 1) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * tpr) * VEC;
-      const bool in = live && c < k;
-      const int o = in ? c : 0;
-      copy_async<B>(smem_u32(at(slot, 0, i)), x + o, in);
-      copy_async<B>(smem_u32(at(slot, 1, i)), dy + o, in);
-      if (arrays == 3) copy_async<B>(smem_u32(at(slot, 2, i)), dres + o, in);
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * tpr) * VEC;
+        const bool in = live && c < k;
+        const int o = in ? c : 0;
+        copy_async(tx + i * (RING_THREADS * 16), x + o, in);
+        copy_async(td + i * (RING_THREADS * 16), dy + o, in);
+        if (arrays == 3) copy_async(tr + i * (RING_THREADS * 16), dres + o, in);
+      }
+    } else if (live) {
+      copy_units(x, k, tx, lane, tpr);
+      copy_units(dy, k, td, lane, tpr);
+      if (arrays == 3) copy_units(dres, k, tr, lane, tpr);
     }
     copy_commit();
   };
-  for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
+  for (int d = 0; d < depth - (VEC == 1); ++d) fetch(row + d * step, d);
   const W* gamma = static_cast<const W*>(a.gamma);
+  // bf16 gamma of few vectors stays in registers
+  constexpr bool GREG = KEEP && sizeof(W) == 2;
+  Vec<W, VEC> gk[GREG ? NV : 1];
+  if constexpr (GREG)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * tpr) * VEC;
+      gk[i] = {};
+      if (gamma && c < k) gk[i] = load<W, VEC>(gamma + c);
+    }
   Num<L> dg[NV][NN], db[NV][NN];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -426,16 +515,29 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
     const bool live = row < a.n;
     const float mean_n = row + step < a.n ? a.mean[row + step] : 0.0f;
     const float rstd_n = row + step < a.n ? a.rstd[row + step] : 0.0f;
-    copy_wait(depth - 1);
+    copy_wait(VEC > 1 ? depth - 1 : depth - 2);
+    if constexpr (VEC == 1) {
+      group_barrier(tpr);  // the row is there, and every thread is done with the one before
+      fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+    }
+    const int64_t q = live ? row : 0;
+    const Units<T> ux(static_cast<const T*>(a.x) + q * a.ldx, at(slot, 0), k),
+        ud(static_cast<const T*>(a.dy) + q * a.lddy, at(slot, 1), k);
     const Num<L> minus = all<L>(-mean), scale = all<L>(rstd);
     Num<L> s1 = all<L>(0.0f), s2 = s1;
     // xhat and w = dy gamma of vector i
     auto values = [&](int i, Num<L>(&h)[NN], Num<L>(&w)[NN], bool first) {
       const int c = (lane + i * tpr) * VEC;
       Num<L> g[NN];
-      to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 0, i)), h);
-      to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 1, i)), w);
-      if (gamma) to_nums<W, VEC, L>(load<W, VEC>(gamma + (c < k ? c : 0)), g);
+      if constexpr (VEC > 1) {
+        to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 0) + i * (RING_THREADS * 16)), h);
+        to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 1) + i * (RING_THREADS * 16)), w);
+      } else {
+        const bool in = live && c < k;
+        h[0].v = in ? to_f(ux[c]) : 0.0f;
+        w[0].v = in ? to_f(ud[c]) : 0.0f;
+      }
+      if (gamma) to_nums<W, VEC, L>(GREG ? gk[GREG ? i : 0] : load<W, VEC>(gamma + (c < k ? c : 0)), g);
 #pragma unroll
       for (int j = 0; j < NN; ++j) {
         h[j] = mul(add(h[j], minus), scale);
@@ -462,23 +564,29 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
       const float2 t = group_sum(total(s1), total(s2), tpr, red[buf]);
       const Num<L> m1 = all<L>(-t.x * inv_k), m2 = all<L>(-t.y * inv_k);
       T* o = static_cast<T*>(a.y) + row * a.ldy;
+      const Units<T> ur((arrays == 3 ? static_cast<const T*>(a.dres) + q * a.lddres : nullptr), at(slot, 2), k);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         Num<L>(&h)[NN] = hk[KEEP ? i : 0];
         Num<L>(&w)[NN] = wk[KEEP ? i : 0];
         if constexpr (!KEEP) values(i, h, w, false);
         Num<L> r[NN];
-        if (arrays == 3) to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 2, i)), r);
+        const int c = (lane + i * tpr) * VEC;
+        if (arrays == 3) {
+          if constexpr (VEC > 1)
+            to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 2) + i * (RING_THREADS * 16)), r);
+          else
+            r[0].v = live && c < k ? to_f(ur[c]) : 0.0f;
+        }
 #pragma unroll
         for (int j = 0; j < NN; ++j) {
           const Num<L> q = fma(h[j], m2, add(w[j], m1));
           r[j] = arrays == 3 ? fma(q, scale, r[j]) : mul(q, scale);
         }
-        const int c = (lane + i * tpr) * VEC;
         if (live && c < k) *reinterpret_cast<Vec<T, VEC>*>(o + c) = from_nums<T, VEC, L>(r);
       }
     }
-    fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+    if constexpr (VEC > 1) fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
     if (++slot == depth) slot = 0;
     buf ^= 1;
     mean = mean_n;
@@ -501,99 +609,6 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
       }
     }
   store_sums<VEC, NV>(fg, fb, a.k, tpr, reinterpret_cast<float*>(ring), part);
-}
-
-// ------------------------------------------------------------------ rows of any alignment
-
-// The gradient: block g takes the row sets g, g + gridDim.x, ... of blockDim.x
-// / tpr rows each; the next set's loads are in flight while a set is summed.
-// part: [gridDim.x][2][k] fp32, this block's sums (NULL: not wanted).
-template <class T, class W, int VEC, int NV>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a, int tpr, float* part) {
-  __shared__ float2 red[2][32];
-  extern __shared__ float sums[];  // one row of columns, to add the block's row groups
-  grid_dep_launch();
-  grid_dep_wait();
-  const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  const W* gamma = static_cast<const W*>(a.gamma);
-  Vec<T, VEC> x[NV], dy[NV], xn[NV], dyn[NV];
-  float dg[NV][VEC] = {}, db[NV][VEC] = {};
-  float mean = 0.0f, rstd = 0.0f, mean_n = 0.0f, rstd_n = 0.0f;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
-  const int64_t sets = (a.n + groups - 1) / groups;  // row sets in all
-  auto fetch = [&](int64_t r, Vec<T, VEC>(&px)[NV], Vec<T, VEC>(&pd)[NV], float& m, float& q) {
-    if (r >= a.n) return;
-    const T *sx = static_cast<const T*>(a.x) + r * a.ldx, *sd = static_cast<const T*>(a.dy) + r * a.lddy;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * tpr) * VEC;
-      if (c < a.k) {
-        px[i] = load<T, VEC>(sx + c);
-        pd[i] = load<T, VEC>(sd + c);
-      }
-    }
-    m = a.mean[r];
-    q = a.rstd[r];
-  };
-  fetch(row, x, dy, mean, rstd);
-  const float inv_k = 1.0f / static_cast<float>(a.k);
-  int buf = 0;
-  for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step, buf ^= 1) {
-    const bool live = row < a.n;
-    fetch(row + step, xn, dyn, mean_n, rstd_n);
-    float s1 = 0.0f, s2 = 0.0f;
-    if (live)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (lane + i * tpr) * VEC;
-        if (c >= a.k) continue;
-        Vec<W, VEC> g;
-        if (gamma) g = load<W, VEC>(gamma + c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float d = to_f(dy[i].e[j]), h = (to_f(x[i].e[j]) - mean) * rstd;
-          const float w = gamma ? d * to_f(g.e[j]) : d;
-          s1 += w;
-          s2 += w * h;
-          dg[i][j] += d * h;
-          db[i][j] += d;
-        }
-      }
-    if (a.y) {
-      const float2 t = row_sum(s1, s2, tpr, red[buf]);
-      const float m1 = t.x * inv_k, m2 = t.y * inv_k;
-      if (live) {
-        T* o = static_cast<T*>(a.y) + row * a.ldy;
-        const T* dres = a.dres ? static_cast<const T*>(a.dres) + row * a.lddres : nullptr;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (lane + i * tpr) * VEC;
-          if (c >= a.k) continue;
-          Vec<W, VEC> g;
-          if (gamma) g = load<W, VEC>(gamma + c);
-          Vec<T, VEC> r, e;
-          if (dres) e = load<T, VEC>(dres + c);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float d = to_f(dy[i].e[j]), h = (to_f(x[i].e[j]) - mean) * rstd;
-            const float w = gamma ? d * to_f(g.e[j]) : d;
-            put(&r.e[j], rstd * (w - m1 - h * m2) + (dres ? to_f(e.e[j]) : 0.0f));
-          }
-          *reinterpret_cast<Vec<T, VEC>*>(o + c) = r;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      x[i] = xn[i];
-      dy[i] = dyn[i];
-    }
-    mean = mean_n;
-    rstd = rstd_n;
-  }
-  if (!part) return;
-  store_sums<VEC, NV>(dg, db, a.k, tpr, sums, part);
 }
 
 // ------------------------------------------------------------------ long rows
@@ -692,8 +707,7 @@ cudaError_t with_nv(int nv, F f) {
     case 1: return f(std::integral_constant<int, 1>());
     case 2: return f(std::integral_constant<int, 2>());
     case 4: return f(std::integral_constant<int, 4>());
-    case 8: return f(std::integral_constant<int, 8>());
-    default: return f(std::integral_constant<int, 16>());
+    default: return f(std::integral_constant<int, 8>());
   }
 }
 
@@ -723,11 +737,12 @@ struct Ring {
   int depth;
   size_t smem;
 };
-Ring ring_of(int nv, int vec_bytes, int arrays, int64_t k, size_t most) {
-  const size_t slot = static_cast<size_t>(RING_THREADS) * nv * vec_bytes * arrays;
+Ring ring_of(bool vec, const Share& h, int arrays, int64_t k, int elem, size_t most) {
+  const size_t slot = arrays * (vec ? static_cast<size_t>(RING_THREADS) * h.nv * 16
+                                    : static_cast<size_t>(RING_THREADS / h.tpr) * (((k * elem + 15) & ~15ll) + 16));
   Ring r;
   r.depth = static_cast<int>(std::min<size_t>(4, most / slot));
-  r.smem = std::max(slot * r.depth, static_cast<size_t>(k) * 4);  // also holds one row of fp32 sums
+  r.smem = slot * r.depth;
   return r;
 }
 
@@ -747,27 +762,34 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
                      vec_ok(a.gamma, 0, 1, 4) && vec_ok(a.beta, 0, 1, 4);
     const int64_t vecs = vec ? a.k / V : a.k;
     // Several rows for every group of a persistent block (two blocks of 512
-    // threads per SM, four vectors a thread): keep rows in flight.  Fewer rows:
-    // one row per group, as many threads as it has vectors (latency).
-    const Share m = share(vecs, 4, 8, RING_THREADS);
-    if (m.tpr && vec && a.n >= static_cast<int64_t>(mc.sms) * 4 * (RING_THREADS / m.tpr)) {
-      const Ring r = ring_of(m.nv, 16, 1, 0, 100 * 1024);
-      const int64_t sets = (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr);
+    // threads per SM): keep rows in flight.  Fewer rows: one row per group, as
+    // many threads as it has vectors (latency).  8192 rows of 8192, four
+    // vectors a thread: 53 us; two: 70; eight: 98.
+    const Share m = vec ? share(vecs, 4, 4, RING_THREADS) : share(vecs, 8, 16, RING_THREADS);
+    const int64_t sets = m.tpr ? (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr) : 0;
+    if (sets >= (vec ? 4 : 1) * static_cast<int64_t>(mc.sms)) {
+      const size_t wb = vec && a.k * sizeof(W) <= 16384 && (a.gamma || a.beta) ? 2 * a.k * sizeof(W) : 0;
+      const Ring r = ring_of(vec, m, 1, a.k, sizeof(T), 110 * 1024 - wb);
       const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sets, 2 * mc.sms)));
       auto run = [&](auto kernel) {
-        cudaError_t e = allow_smem(kernel);
-        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(RING_THREADS), r.smem, s, a, m.tpr, r.depth);
+        const cudaError_t e = allow_smem(kernel);
+        return e != cudaSuccess ? e
+                                : launch_pdl(kernel, grid, dim3(RING_THREADS), r.smem + wb, s, a, m.tpr, r.depth,
+                                             static_cast<int>(wb != 0));
       };
-      const bool full = static_cast<int64_t>(m.tpr) * m.nv == vecs;
-      if (m.nv == 4) return full ? run(norm_ring_kernel<T, W, V, 4, true>) : run(norm_ring_kernel<T, W, V, 4, false>);
-      return full ? run(norm_ring_kernel<T, W, V, 8, true>) : run(norm_ring_kernel<T, W, V, 8, false>);
+      if (r.depth >= 2) {
+        if (vec)
+          return static_cast<int64_t>(m.tpr) * 4 == vecs ? run(norm_ring_kernel<T, W, V, 4, true>)
+                                                         : run(norm_ring_kernel<T, W, V, 4, false>);
+        return m.nv == 8 ? run(norm_ring_kernel<T, W, 1, 8, false>) : run(norm_ring_kernel<T, W, 1, 16, false>);
+      }
     }
     const Share h = share(vecs, 1, 8, 512);
     if (!h.tpr) return launch_pdl(norm_long_kernel<T, W>, dim3(static_cast<unsigned>(a.n)), dim3(1024), 0, s, a);
     const int threads = std::max(h.tpr, 128), rows = threads / h.tpr;
     const dim3 grid(static_cast<unsigned>((a.n + rows - 1) / rows));
     return with_nv(h.nv, [&](auto nv) {
-      constexpr int NV = decltype(nv)::value <= 8 ? decltype(nv)::value : 8;
+      constexpr int NV = decltype(nv)::value;
       if (vec) return launch_pdl(norm_kernel<T, W, V, NV>, grid, dim3(threads), 0, s, a, h.tpr);
       return launch_pdl(norm_kernel<T, W, 1, NV>, grid, dim3(threads), 0, s, a, h.tpr);
     });
@@ -787,41 +809,28 @@ cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int
     if (!wants) part = nullptr;
     int parts = 0;
     cudaError_t e = cudaSuccess;
-    // 16-byte vectors, or single 4-byte elements, can be copied asynchronously
-    const bool async = vec || sizeof(T) == 4;
-    const Share h = share(vecs, vec ? 2 : 4, vec ? (sizeof(T) == 4 ? 8 : 4) : 16, RING_THREADS);
-    const Ring r = ring_of(h.nv, vec ? 16 : 4, a.dres && a.y ? 3 : 2, a.k, 200 * 1024);
-    if (async && h.tpr && r.depth >= 2 && a.n > 0) {
+    // 16 elements a thread (rows up to 8192), else 32 of whole vectors
+    constexpr int NV = 16 / V;
+    Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS) : share(vecs, 8, 16, RING_THREADS);
+    if (!vec && h.tpr == RING_THREADS && h.nv == 16 && vecs <= 12 * RING_THREADS) h.nv = 12;
+    const Ring r = h.tpr ? ring_of(vec, h, a.dres && a.y ? 3 : 2, a.k, sizeof(T), 200 * 1024) : Ring{0, 0};
+    if (r.depth >= 2 && a.n > 0) {
       const int64_t sets = (a.n + RING_THREADS / h.tpr - 1) / (RING_THREADS / h.tpr);
       parts = static_cast<int>(std::min<int64_t>({sets, mc.sms, NORM_PARTS}));
+      // the slots later hold a row of fp32 sums
+      const size_t smem = std::max(r.smem, static_cast<size_t>(a.k) * 4);
       auto run = [&](auto kernel) {
         const cudaError_t c = allow_smem(kernel);
-        return c != cudaSuccess ? c : launch_pdl(kernel, dim3(parts), dim3(RING_THREADS), r.smem, s, a, h.tpr, r.depth, part);
+        return c != cudaSuccess ? c : launch_pdl(kernel, dim3(parts), dim3(RING_THREADS), smem, s, a, h.tpr, r.depth, part);
       };
-      if (vec && h.nv == 2)
-        e = run(norm_bwd_ring_kernel<T, W, V, 2>);
-      else if (vec && h.nv == 4)
-        e = run(norm_bwd_ring_kernel<T, W, V, 4>);
-      else if constexpr (sizeof(T) == 4) {
-        if (vec)
-          e = run(norm_bwd_ring_kernel<T, W, V, 8>);
-        else if (h.nv == 4)
-          e = run(norm_bwd_ring_kernel<T, W, 1, 4>);
-        else if (h.nv == 8)
-          e = run(norm_bwd_ring_kernel<T, W, 1, 8>);
-        else
-          e = run(norm_bwd_ring_kernel<T, W, 1, 16>);
-      }
-    } else if (const Share q = share(a.k, 1, 8, 512); !async && q.tpr && a.n > 0) {
-      if constexpr (sizeof(T) == 2) {
-        const int threads = std::max(q.tpr, 256), rows = threads / q.tpr;
-        parts = static_cast<int>(std::min<int64_t>((a.n + rows - 1) / rows, NORM_PARTS));
-        const size_t smem = rows > 1 ? static_cast<size_t>(a.k) * 4 : 0;
-        e = with_nv(q.nv, [&](auto nv) {
-          constexpr int NV = decltype(nv)::value <= 8 ? decltype(nv)::value : 8;
-          return launch_pdl(norm_bwd_kernel<T, W, 1, NV>, dim3(parts), dim3(threads), smem, s, a, q.tpr, part);
-        });
-      }
+      if (vec)
+        e = h.nv == NV ? run(norm_bwd_ring_kernel<T, W, V, NV>) : run(norm_bwd_ring_kernel<T, W, V, 2 * NV>);
+      else if (h.nv == 8)
+        e = run(norm_bwd_ring_kernel<T, W, 1, 8>);
+      else if (h.nv == 12)
+        e = run(norm_bwd_ring_kernel<T, W, 1, 12>);
+      else
+        e = run(norm_bwd_ring_kernel<T, W, 1, 16>);
     } else if (a.n > 0) {
       // the weights' gradients first: dx may overwrite dy
       parts = static_cast<int>(std::min<int64_t>(a.n, 32));
