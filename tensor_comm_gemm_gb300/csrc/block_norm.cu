@@ -52,25 +52,32 @@ __device__ __forceinline__ Vec<T, VEC> load(const T* p) {
 // Sums of two values over the `tpr` threads of a row, the same bits in each of
 // them; `red` holds two floats per warp and is free for the next call after
 // the one that follows (the callers alternate between two).
-__device__ __forceinline__ float2 row_sum(float a, float b, int tpr, float2* red) {
+__device__ __forceinline__ float2 lanes_sum(float a, float b, int lanes) {
 #pragma unroll
   for (int d = 16; d; d >>= 1)
-    if (d < tpr) {
+    if (d < lanes) {
       a += __shfl_xor_sync(0xffffffffu, a, d);
       b += __shfl_xor_sync(0xffffffffu, b, d);
     }
-  if (tpr > 32) {
-    const int warp = threadIdx.x >> 5, per = tpr >> 5, first = warp & ~(per - 1);
-    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
-    __syncthreads();
-    a = b = 0.0f;
-    for (int w = 0; w < per; ++w) {
-      const float2 v = red[first + w];
-      a += v.x;
-      b += v.y;
-    }
-  }
   return make_float2(a, b);
+}
+// Barrier of the `tpr` threads of a row (their block's own numbers from 1 on).
+__device__ __forceinline__ void group_barrier(int tpr) {
+  if (tpr > 32)
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / tpr), "r"(tpr) : "memory");
+  else
+    __syncwarp();
+}
+__device__ __forceinline__ float2 row_sum(float a, float b, int tpr, float2* red) {
+  float2 v = lanes_sum(a, b, tpr);
+  if (tpr > 32) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5;
+    if (lane == 0) red[warp] = v;
+    group_barrier(tpr);
+    v = red[(warp & ~(per - 1)) + (lane & (per - 1))];
+    v = lanes_sum(v.x, v.y, per);
+  }
+  return v;
 }
 
 template <class T, class W, int VEC, int NV>
@@ -237,61 +244,39 @@ __device__ __forceinline__ void copy_wait(int ahead) {
 }
 // Rows in flight.  With VEC > 1 (16-byte rows) a thread copies the vectors that
 // it will read itself, so it needs no barrier before them.  With VEC = 1 the
-// group copies the whole 16-byte units inside the row, to the same offset
-// modulo 16, and reads single elements after a barrier; the few elements
-// outside those units are read from global memory.
-__device__ __forceinline__ uint32_t row_bytes(int k, int elem) { return ((k * elem + 15) & ~15) + 16; }
-template <class T>
-__device__ __forceinline__ void copy_units(const T* src, int k, uint32_t dst, int lane, int tpr) {
-  const uint64_t p = reinterpret_cast<uint64_t>(src), lo = (p + 15) & ~15ull, hi = (p + k * sizeof(T)) & ~15ull;
-  const int units = hi > lo ? static_cast<int>((hi - lo) >> 4) : 0;
-  const uint32_t to = dst + ((p & 15) ? 16u : 0u);
-  for (int u = lane; u < units; u += tpr) copy_async(to + 16u * u, reinterpret_cast<const void*>(lo + 16ull * u), true);
+// group copies the aligned 16-byte units that hold the row, to the same offset
+// modulo 16, and reads single elements after a barrier.  Units at a row's ends
+// bring a few bytes of what lies beside it, which nobody reads; where that
+// would be outside the matrix (before row 0, behind the last row) only the
+// row's own bytes are touched.
+__host__ __device__ inline uint32_t row_bytes(int k, int elem) {
+  return ((static_cast<uint32_t>(k) * elem + 15u) & ~15u) + 16u;
 }
 template <class T>
-struct Units {  // a row that copy_units has copied
-  const T* src;
-  const uint8_t* at;  // element c at `at + c * sizeof(T)`
-  int lo, hi;         // elements [lo, hi) are there
-  __device__ __forceinline__ Units(const T* p, const uint8_t* slot, int k) : src(p) {
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uint64_t>(p)) & 15u;
-    at = slot + off;
-    lo = static_cast<int>(((16u - off) & 15u) / sizeof(T));
-    hi = k - static_cast<int>(((off + static_cast<uint32_t>(k) * sizeof(T)) & 15u) / sizeof(T));
-  }
-  __device__ __forceinline__ T operator[](int c) const {
-    return c >= lo && c < hi ? *reinterpret_cast<const T*>(at + c * sizeof(T)) : src[c];
-  }
-};
-__device__ __forceinline__ void group_barrier(int tpr) {
-  if (tpr > 32)
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / tpr), "r"(tpr) : "memory");
-  else
-    __syncwarp();
-}
-// Sums over the `tpr` threads of a row group, as row_sum, with a barrier of the group alone.
-__device__ __forceinline__ float2 group_sum(float a, float b, int tpr, float2* red) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1)
-    if (d < tpr) {
-      a += __shfl_xor_sync(0xffffffffu, a, d);
-      b += __shfl_xor_sync(0xffffffffu, b, d);
-    }
-  if (tpr > 32) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5, first = warp & ~(per - 1);
-    if (lane == 0) red[warp] = make_float2(a, b);
-    group_barrier(tpr);
-    const float2 v = red[first + (lane & (per - 1))];
-    a = v.x;
-    b = v.y;
-#pragma unroll
-    for (int d = 8; d; d >>= 1)
-      if (d < per) {
-        a += __shfl_xor_sync(0xffffffffu, a, d);
-        b += __shfl_xor_sync(0xffffffffu, b, d);
+__device__ __forceinline__ void copy_units(const T* src, int k, uint32_t dst, int lane, int tpr, bool first, bool last) {
+  const uint64_t p = reinterpret_cast<uint64_t>(src), lo = p & ~15ull, end = p + static_cast<uint64_t>(k) * sizeof(T);
+  const int units = static_cast<int>((end - lo + 15) >> 4);
+  for (int u = lane; u < units; u += tpr) {
+    const uint64_t at = lo + 16ull * u;
+    if (first && at < p) {  // the row's own elements of its first unit
+      const int own = min(k, static_cast<int>((at + 16 - p) / sizeof(T)));
+      for (int c = 0; c < own; ++c) {
+        const uint32_t to = dst + static_cast<uint32_t>(p & 15) + c * static_cast<uint32_t>(sizeof(T));
+        if constexpr (sizeof(T) == 4)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(src[c]) : "memory");
+        else
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(__bfloat16_as_ushort(src[c])) : "memory");
       }
+    } else {
+      const int bytes = last && at + 16 > end ? static_cast<int>(end - at) : 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16u * u), "l"(at), "r"(bytes) : "memory");
+    }
   }
-  return make_float2(a, b);
+}
+// Where element 0 of such a row is.
+template <class T>
+__device__ __forceinline__ const T* unit_row(const T* src, const uint8_t* slot) {
+  return reinterpret_cast<const T*>(slot + (reinterpret_cast<uint64_t>(src) & 15));
 }
 
 constexpr int RING_THREADS = 512;
@@ -323,7 +308,7 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
         copy_async(to + i * (RING_THREADS * 16), x + (FULL || c < k ? c : 0), live && (FULL || c < k));
       }
     } else if (live) {
-      copy_units(x, k, to, lane, tpr);
+      copy_units(x, k, to, lane, tpr, r == 0, r == a.n - 1);
     }
     copy_commit();
   };
@@ -357,18 +342,16 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
       copy_wait(depth - 2);
       group_barrier(tpr);  // the row is there, and every thread is done with the one before
       fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
-      const Units<T> x(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx, mine + slot * slot_bytes, k);
+      const T* x = unit_row(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx, mine + slot * slot_bytes) + lane;
+      const int own = live ? k - lane : 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = lane + i * tpr;
-        v[i][0].v = live && c < k ? to_f(x[c]) : 0.0f;
-      }
+      for (int i = 0; i < NV; ++i) v[i][0].v = i * tpr < own ? to_f(x[i * tpr]) : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < NN; ++j) s = add(s, v[i][j]);
-    const float mean = group_sum(total(s), 0.0f, tpr, red[buf]).x * inv_k;
+    const float mean = row_sum(total(s), 0.0f, tpr, red[buf]).x * inv_k;
     const Num<L> minus = all<L>(-mean);
     s = all<L>(0.0f);
 #pragma unroll
@@ -381,7 +364,7 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
         s = fma(v[i][j], v[i][j], s);
       }
     }
-    const float rstd = 1.0f / sqrtf(group_sum(total(s), 0.0f, tpr, red[buf + 1]).x * inv_k + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum(total(s), 0.0f, tpr, red[buf + 1]).x * inv_k + a.eps);
     const Num<L> scale = all<L>(rstd);
     T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
@@ -409,42 +392,30 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Adds the sums of a block's row groups, inside a warp by shuffles and then one
-// after another (a fixed order), and stores them: part[blockIdx.x][2][k].
-// `sums`: k floats of shared memory.
-template <int VEC, int NV>
-__device__ __forceinline__ void store_sums(float (&dg)[NV][VEC], float (&db)[NV][VEC], int64_t k, int tpr, float* sums,
-                                           float* part) {
-  for (int d = tpr; d < 32; d <<= 1)
+// Adds the sums of a block's row groups in their order and stores them:
+// part[blockIdx.x][2][k].  `sums`: [groups][2][k] floats of shared memory.
+template <int VEC, int NV, int L>
+__device__ __forceinline__ void store_sums(const Num<L> (&dg)[NV][VEC / L], const Num<L> (&db)[NV][VEC / L], int k,
+                                           int tpr, float* sums, float* part) {
+  const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+  float* mine = sums + group * 2 * k;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int c = (lane + i * tpr) * VEC;
+    if (c < k)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        dg[i][j] += __shfl_xor_sync(0xffffffffu, dg[i][j], d);
-        db[i][j] += __shfl_xor_sync(0xffffffffu, db[i][j], d);
+      for (int j = 0; j < VEC / L; ++j) {  // k is even where values come in pairs
+        memcpy(mine + c + j * L, &dg[i][j], sizeof(Num<L>));
+        memcpy(mine + k + c + j * L, &db[i][j], sizeof(Num<L>));
       }
-  const int wide = tpr < 32 ? 32 : tpr;  // threads that now hold one set of sums
-  const int lane = threadIdx.x & (wide - 1), group = threadIdx.x / wide, groups = blockDim.x / wide;
+  }
+  __syncthreads();
   float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * k;
-#pragma unroll
-  for (int which = 0; which < 2; ++which)
-    for (int q = 0; q < groups; ++q) {
-      if (groups > 1) __syncthreads();
-      if (q != group || lane >= tpr) continue;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int c = (lane + i * tpr) * VEC + j;
-          if (c >= k) continue;
-          float v = which ? db[i][j] : dg[i][j];
-          if (q > 0) v += sums[c];
-          if (q + 1 < groups)
-            sums[c] = v;
-          else
-            out[which * k + c] = v;
-        }
-    }
+  for (int c = threadIdx.x; c < 2 * k; c += blockDim.x) {
+    float v = 0.0f;
+    for (int q = 0; q < groups; ++q) v += sums[q * 2 * k + c];
+    out[c] = v;
+  }
 }
 
 // Backward, rows in flight as forward: x, dy and (if given) dres of a row.
@@ -484,9 +455,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
         if (arrays == 3) copy_async(tr + i * (RING_THREADS * 16), dres + o, in);
       }
     } else if (live) {
-      copy_units(x, k, tx, lane, tpr);
-      copy_units(dy, k, td, lane, tpr);
-      if (arrays == 3) copy_units(dres, k, tr, lane, tpr);
+      const bool first = r == 0, last = r == a.n - 1;
+      copy_units(x, k, tx, lane, tpr, first, last);
+      copy_units(dy, k, td, lane, tpr, first, last);
+      if (arrays == 3) copy_units(dres, k, tr, lane, tpr, first, last);
     }
     copy_commit();
   };
@@ -521,8 +493,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
       fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
     }
     const int64_t q = live ? row : 0;
-    const Units<T> ux(static_cast<const T*>(a.x) + q * a.ldx, at(slot, 0), k),
-        ud(static_cast<const T*>(a.dy) + q * a.lddy, at(slot, 1), k);
+    // VEC = 1: this thread's first element of each row, and how far the row reaches past it
+    const T* ux = unit_row(static_cast<const T*>(a.x) + q * a.ldx, at(slot, 0)) + lane;
+    const T* ud = unit_row(static_cast<const T*>(a.dy) + q * a.lddy, at(slot, 1)) + lane;
+    const int own = live ? k - lane : 0;
     const Num<L> minus = all<L>(-mean), scale = all<L>(rstd);
     Num<L> s1 = all<L>(0.0f), s2 = s1;
     // xhat and w = dy gamma of vector i
@@ -533,9 +507,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
         to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 0) + i * (RING_THREADS * 16)), h);
         to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 1) + i * (RING_THREADS * 16)), w);
       } else {
-        const bool in = live && c < k;
-        h[0].v = in ? to_f(ux[c]) : 0.0f;
-        w[0].v = in ? to_f(ud[c]) : 0.0f;
+        const bool in = i * tpr < own;
+        h[0].v = in ? to_f(ux[i * tpr]) : 0.0f;
+        w[0].v = in ? to_f(ud[i * tpr]) : 0.0f;
       }
       if (gamma) to_nums<W, VEC, L>(GREG ? gk[GREG ? i : 0] : load<W, VEC>(gamma + (c < k ? c : 0)), g);
 #pragma unroll
@@ -561,10 +535,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
       }
     }
     if (a.y) {
-      const float2 t = group_sum(total(s1), total(s2), tpr, red[buf]);
+      const float2 t = row_sum(total(s1), total(s2), tpr, red[buf]);
       const Num<L> m1 = all<L>(-t.x * inv_k), m2 = all<L>(-t.y * inv_k);
       T* o = static_cast<T*>(a.y) + row * a.ldy;
-      const Units<T> ur((arrays == 3 ? static_cast<const T*>(a.dres) + q * a.lddres : nullptr), at(slot, 2), k);
+      const T* ur = unit_row(static_cast<const T*>(a.dres) + q * a.lddres, at(slot, 2)) + lane;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         Num<L>(&h)[NN] = hk[KEEP ? i : 0];
@@ -576,7 +550,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
           if constexpr (VEC > 1)
             to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 2) + i * (RING_THREADS * 16)), r);
           else
-            r[0].v = live && c < k ? to_f(ur[c]) : 0.0f;
+            r[0].v = i * tpr < own ? to_f(ur[i * tpr]) : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < NN; ++j) {
@@ -595,20 +569,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!part) return;
   __syncthreads();  // the ring is free: it holds the columns' sums now
-  float fg[NV][VEC], fb[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < NN; ++j) {
-      if constexpr (L == 2) {
-        unpack2(dg[i][j].v, fg[i][2 * j], fg[i][2 * j + 1]);
-        unpack2(db[i][j].v, fb[i][2 * j], fb[i][2 * j + 1]);
-      } else {
-        fg[i][j] = dg[i][j].v;
-        fb[i][j] = db[i][j].v;
-      }
-    }
-  store_sums<VEC, NV>(fg, fb, a.k, tpr, reinterpret_cast<float*>(ring), part);
+  store_sums<VEC, NV, L>(dg, db, k, tpr, reinterpret_cast<float*>(ring), part);
 }
 
 // ------------------------------------------------------------------ long rows
@@ -732,6 +693,16 @@ Share share(int64_t vecs, int nv, int most_nv, int most_tpr) {
   return s;
 }
 
+// Single elements: 8, 12 or 16 a thread, whichever leaves the fewest threads idle.
+Share share_single(int64_t k) {
+  Share best{0, 0};
+  for (int nv : {8, 12, 16}) {
+    const Share s = share(k, nv, nv, 512);
+    if (s.tpr && (!best.tpr || s.tpr * s.nv < best.tpr * best.nv)) best = s;
+  }
+  return best;
+}
+
 // Rows in flight per group and the shared memory they take; depth < 2: they do not fit.
 struct Ring {
   int depth;
@@ -765,9 +736,9 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
     // threads per SM): keep rows in flight.  Fewer rows: one row per group, as
     // many threads as it has vectors (latency).  8192 rows of 8192, four
     // vectors a thread: 53 us; two: 70; eight: 98.
-    const Share m = vec ? share(vecs, 4, 4, RING_THREADS) : share(vecs, 8, 16, RING_THREADS);
+    const Share m = vec ? share(vecs, 4, 4, RING_THREADS) : share_single(a.k);
     const int64_t sets = m.tpr ? (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr) : 0;
-    if (sets >= (vec ? 4 : 1) * static_cast<int64_t>(mc.sms)) {
+    if (sets >= (vec ? 2 : 1) * static_cast<int64_t>(mc.sms)) {
       const size_t wb = vec && a.k * sizeof(W) <= 16384 && (a.gamma || a.beta) ? 2 * a.k * sizeof(W) : 0;
       const Ring r = ring_of(vec, m, 1, a.k, sizeof(T), 110 * 1024 - wb);
       const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sets, 2 * mc.sms)));
@@ -781,7 +752,8 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
         if (vec)
           return static_cast<int64_t>(m.tpr) * 4 == vecs ? run(norm_ring_kernel<T, W, V, 4, true>)
                                                          : run(norm_ring_kernel<T, W, V, 4, false>);
-        return m.nv == 8 ? run(norm_ring_kernel<T, W, 1, 8, false>) : run(norm_ring_kernel<T, W, 1, 16, false>);
+        if (m.nv == 8) return run(norm_ring_kernel<T, W, 1, 8, false>);
+        return m.nv == 12 ? run(norm_ring_kernel<T, W, 1, 12, false>) : run(norm_ring_kernel<T, W, 1, 16, false>);
       }
     }
     const Share h = share(vecs, 1, 8, 512);
@@ -811,14 +783,13 @@ cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int
     cudaError_t e = cudaSuccess;
     // 16 elements a thread (rows up to 8192), else 32 of whole vectors
     constexpr int NV = 16 / V;
-    Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS) : share(vecs, 8, 16, RING_THREADS);
-    if (!vec && h.tpr == RING_THREADS && h.nv == 16 && vecs <= 12 * RING_THREADS) h.nv = 12;
+    const Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS) : share_single(a.k);
     const Ring r = h.tpr ? ring_of(vec, h, a.dres && a.y ? 3 : 2, a.k, sizeof(T), 200 * 1024) : Ring{0, 0};
     if (r.depth >= 2 && a.n > 0) {
       const int64_t sets = (a.n + RING_THREADS / h.tpr - 1) / (RING_THREADS / h.tpr);
       parts = static_cast<int>(std::min<int64_t>({sets, mc.sms, NORM_PARTS}));
-      // the slots later hold a row of fp32 sums
-      const size_t smem = std::max(r.smem, static_cast<size_t>(a.k) * 4);
+      // the slots later hold every group's fp32 sums
+      const size_t smem = std::max(r.smem, static_cast<size_t>(RING_THREADS / h.tpr) * 8 * a.k);
       auto run = [&](auto kernel) {
         const cudaError_t c = allow_smem(kernel);
         return c != cudaSuccess ? c : launch_pdl(kernel, dim3(parts), dim3(RING_THREADS), smem, s, a, h.tpr, r.depth, part);
