@@ -49,40 +49,63 @@ __device__ __forceinline__ Vec<T, VEC> load(const T* p) {
   return *reinterpret_cast<const Vec<T, VEC>*>(p);
 }
 
-// Sums of two values over the `tpr` threads of a row, the same bits in each of
-// them; `red` holds two floats per warp and is free for the next call after
-// the one that follows (the callers alternate between two).
-__device__ __forceinline__ float2 lanes_sum(float a, float b, int lanes) {
+// Sums over the `tpr` threads of a row, the same bits in each of them; `red`
+// holds a value per warp and is free for the call after the next (the callers
+// alternate between two).
+__device__ __forceinline__ float lanes_sum(float a, int lanes) {
 #pragma unroll
   for (int d = 16; d; d >>= 1)
-    if (d < lanes) {
-      a += __shfl_xor_sync(0xffffffffu, a, d);
-      b += __shfl_xor_sync(0xffffffffu, b, d);
-    }
-  return make_float2(a, b);
+    if (d < lanes) a += __shfl_xor_sync(0xffffffffu, a, d);
+  return a;
 }
-// Barrier of the `tpr` threads of a row (their block's own numbers from 1 on).
+// Barrier of the `tpr` threads of a row.  (A kernel with it holds all 16 of a
+// block's barriers, so at most four such blocks run on an SM.)
 __device__ __forceinline__ void group_barrier(int tpr) {
   if (tpr > 32)
     asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / tpr), "r"(tpr) : "memory");
   else
     __syncwarp();
 }
-__device__ __forceinline__ float2 row_sum(float a, float b, int tpr, float2* red) {
-  float2 v = lanes_sum(a, b, tpr);
+// ALONE: the rows' groups keep their own pace; otherwise the block's rows go together.
+template <bool ALONE>
+__device__ __forceinline__ float row_sum(float a, int tpr, float* red) {
+  a = lanes_sum(a, tpr);
   if (tpr > 32) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5;
-    if (lane == 0) red[warp] = v;
-    group_barrier(tpr);
-    v = red[(warp & ~(per - 1)) + (lane & (per - 1))];
-    v = lanes_sum(v.x, v.y, per);
+    if (lane == 0) red[warp] = a;
+    if constexpr (ALONE)
+      group_barrier(tpr);
+    else
+      __syncthreads();
+    a = lanes_sum(red[(warp & ~(per - 1)) + (lane & (per - 1))], per);
   }
-  return v;
+  return a;
+}
+__device__ __forceinline__ void lanes_sums(float& a, float& b, int lanes) {  // both chains at once
+#pragma unroll
+  for (int d = 16; d; d >>= 1)
+    if (d < lanes) {
+      a += __shfl_xor_sync(0xffffffffu, a, d);
+      b += __shfl_xor_sync(0xffffffffu, b, d);
+    }
+}
+__device__ __forceinline__ float2 row_sums(float a, float b, int tpr, float2* red) {
+  lanes_sums(a, b, tpr);
+  if (tpr > 32) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5;
+    if (lane == 0) red[warp] = make_float2(a, b);
+    group_barrier(tpr);
+    const float2 v = red[(warp & ~(per - 1)) + (lane & (per - 1))];
+    a = v.x;
+    b = v.y;
+    lanes_sums(a, b, per);
+  }
+  return make_float2(a, b);
 }
 
 template <class T, class W, int VEC, int NV>
 __global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int tpr) {
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][32];
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & (tpr - 1);
@@ -102,7 +125,7 @@ __global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int tpr) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) s += to_f(v[i].e[j]);
   const float inv_k = 1.0f / static_cast<float>(a.k);
-  const float mean = row_sum(s, 0.0f, tpr, red[0]).x * inv_k;
+  const float mean = row_sum<false>(s, tpr, red[0]) * inv_k;
   s = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -112,7 +135,7 @@ __global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int tpr) {
         const float d = to_f(v[i].e[j]) - mean;
         s += d * d;
       }
-  const float rstd = 1.0f / sqrtf(row_sum(s, 0.0f, tpr, red[1]).x * inv_k + a.eps);
+  const float rstd = rsqrtf(row_sum<false>(s, tpr, red[1]) * inv_k + a.eps);
   if (!live) return;
   const W *gamma = static_cast<const W*>(a.gamma), *beta = static_cast<const W*>(a.beta);
   T* y = static_cast<T*>(a.y) + row * a.ldy;
@@ -279,18 +302,34 @@ __device__ __forceinline__ const T* unit_row(const T* src, const uint8_t* slot) 
   return reinterpret_cast<const T*>(slot + (reinterpret_cast<uint64_t>(src) & 15));
 }
 
+// A group is whole warps.  With VEC = 1, warp w of it holds the elements
+// [w NV 32, (w + 1) NV 32), lane l every 32nd of them: the offsets between a
+// thread's elements are known to the compiler, which saves a third of the
+// instructions.  Whole vectors are dealt out over the group instead (thread l
+// has l, l + tpr, ...), which keeps the group's accesses of one step together:
+// 16384 x 4096 backward 78 us, 87 with vectors dealt out by warp.
 constexpr int RING_THREADS = 512;
+template <int VEC, int NV>
+__device__ __forceinline__ int first_column(int tpr) {
+  const int lane = static_cast<int>(threadIdx.x & (tpr - 1));
+  return VEC > 1 ? lane * VEC : (lane >> 5) * NV * 32 + (lane & 31);
+}
+template <int VEC>
+__device__ __forceinline__ int column_step(int tpr) {
+  return VEC > 1 ? tpr * VEC : 32;
+}
 
 // Forward: `depth` rows of each group are in flight or in use.  FULL: the
 // group's vectors are exactly a row's.
 template <class T, class W, int VEC, int NV, bool FULL>
-__global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormArgs a, int tpr, int depth, int weights) {
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int tpr, int depth, int weights) {
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[4][RING_THREADS / 32];
+  __shared__ float red[4][RING_THREADS / 32];
   constexpr int L = VEC > 1 ? 2 : 1, NN = VEC / L;
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = RING_THREADS / tpr;
+  const int c0 = first_column<VEC, NV>(tpr), step_c = column_step<VEC>(tpr);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
   const int k = static_cast<int>(a.k);
@@ -304,7 +343,7 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
     if constexpr (VEC > 1) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (lane + i * tpr) * VEC;
+        const int c = (c0 + i * step_c);
         copy_async(to + i * (RING_THREADS * 16), x + (FULL || c < k ? c : 0), live && (FULL || c < k));
       }
     } else if (live) {
@@ -327,7 +366,7 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
   }
   const float inv_k = 1.0f / static_cast<float>(k);
   int slot = 0, buf = 0;
-  // every group of the block runs the same number of rounds: warps that hold several rows stay whole
+  // every group of the block runs the same number of rounds
   const int64_t sets = (a.n + groups - 1) / groups;
   for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
     const bool live = row < a.n;
@@ -342,16 +381,16 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
       copy_wait(depth - 2);
       group_barrier(tpr);  // the row is there, and every thread is done with the one before
       fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
-      const T* x = unit_row(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx, mine + slot * slot_bytes) + lane;
-      const int own = live ? k - lane : 0;
+      const T* x = unit_row(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx, mine + slot * slot_bytes) + c0;
+      const int own = live ? k - c0 : 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i][0].v = i * tpr < own ? to_f(x[i * tpr]) : 0.0f;
+      for (int i = 0; i < NV; ++i) v[i][0].v = i * 32 < own ? to_f(x[i * 32]) : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < NN; ++j) s = add(s, v[i][j]);
-    const float mean = row_sum(total(s), 0.0f, tpr, red[buf]).x * inv_k;
+    const float mean = row_sum<true>(total(s), tpr, red[buf]) * inv_k;
     const Num<L> minus = all<L>(-mean);
     s = all<L>(0.0f);
 #pragma unroll
@@ -360,16 +399,16 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
       for (int j = 0; j < NN; ++j) {
         v[i][j] = add(v[i][j], minus);
         if constexpr (!FULL)
-          if ((lane + i * tpr) * VEC >= k) v[i][j] = all<L>(0.0f);
+          if ((c0 + i * step_c) >= k) v[i][j] = all<L>(0.0f);
         s = fma(v[i][j], v[i][j], s);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum(total(s), 0.0f, tpr, red[buf + 1]).x * inv_k + a.eps);
+    const float rstd = rsqrtf(row_sum<true>(total(s), tpr, red[buf + 1]) * inv_k + a.eps);
     const Num<L> scale = all<L>(rstd);
     T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * tpr) * VEC;
+      const int c = (c0 + i * step_c);
       if (!FULL && c >= k) continue;
       Num<L> g[NN], b[NN];
       if (gamma) to_nums<W, VEC, L>(load<W, VEC>(gamma + c), g);
@@ -397,11 +436,12 @@ __global__ void __launch_bounds__(RING_THREADS, 2) norm_ring_kernel(const NormAr
 template <int VEC, int NV, int L>
 __device__ __forceinline__ void store_sums(const Num<L> (&dg)[NV][VEC / L], const Num<L> (&db)[NV][VEC / L], int k,
                                            int tpr, float* sums, float* part) {
-  const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+  const int c0 = first_column<VEC, NV>(tpr), step_c = column_step<VEC>(tpr);
+  const int group = threadIdx.x / tpr, groups = blockDim.x / tpr;
   float* mine = sums + group * 2 * k;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * tpr) * VEC;
+    const int c = (c0 + i * step_c);
     if (c < k)
 #pragma unroll
       for (int j = 0; j < VEC / L; ++j) {  // k is even where values come in pairs
@@ -429,6 +469,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = RING_THREADS / tpr;
+  const int c0 = first_column<VEC, NV>(tpr), step_c = column_step<VEC>(tpr);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
   const int k = static_cast<int>(a.k);
@@ -447,7 +488,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
     if constexpr (VEC > 1) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (lane + i * tpr) * VEC;
+        const int c = (c0 + i * step_c);
         const bool in = live && c < k;
         const int o = in ? c : 0;
         copy_async(tx + i * (RING_THREADS * 16), x + o, in);
@@ -470,7 +511,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   if constexpr (GREG)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * tpr) * VEC;
+      const int c = (c0 + i * step_c);
       gk[i] = {};
       if (gamma && c < k) gk[i] = load<W, VEC>(gamma + c);
     }
@@ -494,22 +535,22 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
     }
     const int64_t q = live ? row : 0;
     // VEC = 1: this thread's first element of each row, and how far the row reaches past it
-    const T* ux = unit_row(static_cast<const T*>(a.x) + q * a.ldx, at(slot, 0)) + lane;
-    const T* ud = unit_row(static_cast<const T*>(a.dy) + q * a.lddy, at(slot, 1)) + lane;
-    const int own = live ? k - lane : 0;
+    const T* ux = unit_row(static_cast<const T*>(a.x) + q * a.ldx, at(slot, 0)) + c0;
+    const T* ud = unit_row(static_cast<const T*>(a.dy) + q * a.lddy, at(slot, 1)) + c0;
+    const int own = live ? k - c0 : 0;
     const Num<L> minus = all<L>(-mean), scale = all<L>(rstd);
     Num<L> s1 = all<L>(0.0f), s2 = s1;
     // xhat and w = dy gamma of vector i
     auto values = [&](int i, Num<L>(&h)[NN], Num<L>(&w)[NN], bool first) {
-      const int c = (lane + i * tpr) * VEC;
+      const int c = (c0 + i * step_c);
       Num<L> g[NN];
       if constexpr (VEC > 1) {
         to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 0) + i * (RING_THREADS * 16)), h);
         to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 1) + i * (RING_THREADS * 16)), w);
       } else {
-        const bool in = i * tpr < own;
-        h[0].v = in ? to_f(ux[i * tpr]) : 0.0f;
-        w[0].v = in ? to_f(ud[i * tpr]) : 0.0f;
+        const bool in = i * 32 < own;
+        h[0].v = in ? to_f(ux[i * 32]) : 0.0f;
+        w[0].v = in ? to_f(ud[i * 32]) : 0.0f;
       }
       if (gamma) to_nums<W, VEC, L>(GREG ? gk[GREG ? i : 0] : load<W, VEC>(gamma + (c < k ? c : 0)), g);
 #pragma unroll
@@ -535,22 +576,22 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
       }
     }
     if (a.y) {
-      const float2 t = row_sum(total(s1), total(s2), tpr, red[buf]);
+      const float2 t = row_sums(total(s1), total(s2), tpr, red[buf]);
       const Num<L> m1 = all<L>(-t.x * inv_k), m2 = all<L>(-t.y * inv_k);
       T* o = static_cast<T*>(a.y) + row * a.ldy;
-      const T* ur = unit_row(static_cast<const T*>(a.dres) + q * a.lddres, at(slot, 2)) + lane;
+      const T* ur = unit_row(static_cast<const T*>(a.dres) + q * a.lddres, at(slot, 2)) + c0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         Num<L>(&h)[NN] = hk[KEEP ? i : 0];
         Num<L>(&w)[NN] = wk[KEEP ? i : 0];
         if constexpr (!KEEP) values(i, h, w, false);
         Num<L> r[NN];
-        const int c = (lane + i * tpr) * VEC;
+        const int c = (c0 + i * step_c);
         if (arrays == 3) {
           if constexpr (VEC > 1)
             to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 2) + i * (RING_THREADS * 16)), r);
           else
-            r[0].v = i * tpr < own ? to_f(ur[i * tpr]) : 0.0f;
+            r[0].v = i * 32 < own ? to_f(ur[i * 32]) : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < NN; ++j) {
@@ -680,8 +721,8 @@ bool vec_ok(const void* p, int64_t ld, int64_t rows, int elem) {
 struct Share {
   int nv, tpr;
 };
-Share share(int64_t vecs, int nv, int most_nv, int most_tpr) {
-  Share s{nv, 1};
+Share share(int64_t vecs, int nv, int most_nv, int most_tpr, int least_tpr = 1) {
+  Share s{nv, least_tpr};
   while (static_cast<int64_t>(s.tpr) * s.nv < vecs) {
     if (s.tpr < most_tpr)
       s.tpr *= 2;
@@ -696,8 +737,8 @@ Share share(int64_t vecs, int nv, int most_nv, int most_tpr) {
 // Single elements: 8, 12 or 16 a thread, whichever leaves the fewest threads idle.
 Share share_single(int64_t k) {
   Share best{0, 0};
-  for (int nv : {8, 12, 16}) {
-    const Share s = share(k, nv, nv, 512);
+  for (int nv : {16, 12, 8}) {
+    const Share s = share(k, nv, nv, 512, 32);
     if (s.tpr && (!best.tpr || s.tpr * s.nv < best.tpr * best.nv)) best = s;
   }
   return best;
@@ -732,16 +773,17 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
     const bool vec = a.k % V == 0 && vec_ok(a.x, a.ldx, a.n, sizeof(T)) && vec_ok(a.y, a.ldy, a.n, sizeof(T)) &&
                      vec_ok(a.gamma, 0, 1, 4) && vec_ok(a.beta, 0, 1, 4);
     const int64_t vecs = vec ? a.k / V : a.k;
-    // Several rows for every group of a persistent block (two blocks of 512
+    // Several rows for every group of a persistent block (one block of 512
     // threads per SM): keep rows in flight.  Fewer rows: one row per group, as
     // many threads as it has vectors (latency).  8192 rows of 8192, four
-    // vectors a thread: 53 us; two: 70; eight: 98.
-    const Share m = vec ? share(vecs, 4, 4, RING_THREADS) : share_single(a.k);
+    // vectors a thread: 49 us; two blocks per SM, with 64 registers a thread:
+    // 57, and then 70 with two vectors and 98 with eight.
+    const Share m = vec ? share(vecs, 4, 4, RING_THREADS, 32) : share_single(a.k);
     const int64_t sets = m.tpr ? (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr) : 0;
     if (sets >= (vec ? 2 : 1) * static_cast<int64_t>(mc.sms)) {
       const size_t wb = vec && a.k * sizeof(W) <= 16384 && (a.gamma || a.beta) ? 2 * a.k * sizeof(W) : 0;
-      const Ring r = ring_of(vec, m, 1, a.k, sizeof(T), 110 * 1024 - wb);
-      const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sets, 2 * mc.sms)));
+      const Ring r = ring_of(vec, m, 1, a.k, sizeof(T), 200 * 1024 - wb);
+      const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sets, mc.sms)));
       auto run = [&](auto kernel) {
         const cudaError_t e = allow_smem(kernel);
         return e != cudaSuccess ? e
@@ -783,7 +825,7 @@ cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int
     cudaError_t e = cudaSuccess;
     // 16 elements a thread (rows up to 8192), else 32 of whole vectors
     constexpr int NV = 16 / V;
-    const Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS) : share_single(a.k);
+    const Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS, 32) : share_single(a.k);
     const Ring r = h.tpr ? ring_of(vec, h, a.dres && a.y ? 3 : 2, a.k, sizeof(T), 200 * 1024) : Ring{0, 0};
     if (r.depth >= 2 && a.n > 0) {
       const int64_t sets = (a.n + RING_THREADS / h.tpr - 1) / (RING_THREADS / h.tpr);
