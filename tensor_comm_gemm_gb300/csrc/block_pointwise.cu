@@ -48,9 +48,36 @@ __device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// One row's eight columns from c on: dz from dy and z, stored if wanted, and added to the sums.  WHOLE: all eight exist.
+template <int ACT, bool WHOLE>
+__device__ __forceinline__ void act_bwd_rows(int64_t first, int64_t n, int64_t step, int64_t c, int64_t m,
+                                             const bf16* dy, int64_t lddy, const bf16* z, int64_t ldz, bf16* dz,
+                                             int64_t ldo, float (&sum)[8]) {
+  constexpr int R = 4;  // rows whose loads are in flight together
+  for (int64_t i0 = first; i0 < n; i0 += R * step) {
+    float d[R][8], v[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t i = i0 + r * step < n ? i0 + r * step : i0;
+      load8(dy + i * lddy, c, WHOLE ? c + 8 : m, d[r]);
+      if constexpr (ACT != TPO_ACT_NONE) load8(z + i * ldz, c, WHOLE ? c + 8 : m, v[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (i0 + r * step >= n) break;
+      if constexpr (ACT != TPO_ACT_NONE)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[r][j] *= act_grad_f<ACT>(v[r][j]);
+      if (dz) store8(dz + (i0 + r * step) * ldo + c, d[r]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += d[r][j];
+    }
+  }
+}
+
 // Block (x, y): columns [256 x, 256 x + 256) of the rows 8 y + w + 8 i gridDim.y,
-// warp w.  dz is stored if wanted; with `part`, the sums over the block's rows
-// (fp32, before dz is rounded) go to part[y][m].
+// warp w.  With `part`, the sums over the block's rows (fp32, before dz is
+// rounded) go to part[y][m].
 template <int ACT>
 __global__ void __launch_bounds__(256) act_bwd_kernel(int64_t n, int64_t m, const bf16* dy, int64_t lddy,
                                                       const bf16* z, int64_t ldz, bf16* dz, int64_t ldo,
@@ -60,22 +87,12 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(int64_t n, int64_t m, cons
   grid_dep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + lane * 8;
+  const int64_t first = static_cast<int64_t>(blockIdx.y) * 8 + warp, step = static_cast<int64_t>(gridDim.y) * 8;
   float sum[8] = {};
-  if (c < m)
-#pragma unroll 4
-    for (int64_t i = static_cast<int64_t>(blockIdx.y) * 8 + warp; i < n; i += static_cast<int64_t>(gridDim.y) * 8) {
-      float d[8];
-      load8(dy + i * lddy, c, m, d);
-      if constexpr (ACT != TPO_ACT_NONE) {
-        float v[8];
-        load8(z + i * ldz, c, m, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] *= act_grad_f<ACT>(v[j]);
-      }
-      if (dz) store8(dz + i * ldo + c, d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += d[j];
-    }
+  if (c + 8 <= m)
+    act_bwd_rows<ACT, true>(first, n, step, c, m, dy, lddy, z, ldz, dz, ldo, sum);
+  else if (c < m)
+    act_bwd_rows<ACT, false>(first, n, step, c, m, dy, lddy, z, ldz, dz, ldo, sum);
   if (!part) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) red[warp][lane * 8 + j] = sum[j];

@@ -300,21 +300,18 @@ def tpo_ag_gemm_noalloc(tp: int, n: int, k: int, m: int, dtype: int, x: Sequence
 # Tensors carry their sizes, row pitches and types: matrices are 2-D with unit
 # stride in the last dimension, vectors contiguous.
 
-def _dtype_codes():
-    import torch
-    return {torch.bfloat16: TPO_BF16, torch.float32: TPO_F32, torch.float8_e4m3fn: TPO_FP8_E4M3,
-            torch.uint8: TPO_FP8_E4M3}
-
-
 _CODES = {}      # torch dtype -> tpo_dtype, filled on first use (uint8 holds e4m3 codes)
 
 
 def _code(name, t) -> int:
-    if not _CODES:
-        _CODES.update(_dtype_codes())
     c = _CODES.get(t.dtype)
     if c is None:
-        raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
+        import torch
+        _CODES.update({torch.bfloat16: TPO_BF16, torch.float32: TPO_F32, torch.float8_e4m3fn: TPO_FP8_E4M3,
+                       torch.uint8: TPO_FP8_E4M3})
+        c = _CODES.get(t.dtype)
+        if c is None:
+            raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
     return c
 
 
@@ -322,12 +319,11 @@ def _mat(name, t, rows, cols, code):
     """(pointer, pitch) of an [rows, cols] CUDA matrix of type `code`; (None, 0) for None."""
     if t is None:
         return None, 0
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
-        raise TpoError(TPO_ERR_INVALID_ARG, "%s has shape %s, expected (%d, %d)" % (name, tuple(shape), rows, cols))
+    if t.shape != (rows, cols):
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s has shape %s, expected (%d, %d)" % (name, tuple(t.shape), rows, cols))
     if not t.is_cuda:
         raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
-    if _code(name, t) != code:
+    if _CODES.get(t.dtype) != code and _code(name, t) != code:
         raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
@@ -342,15 +338,23 @@ def _vec(name, t, count, code):
         raise TpoError(TPO_ERR_INVALID_ARG, "%s must hold %d contiguous elements" % (name, count))
     if not t.is_cuda:
         raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
-    if _code(name, t) != code:
+    if _CODES.get(t.dtype) != code and _code(name, t) != code:
         raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
     return t.data_ptr()
 
 
+def _stream_of(stream, t) -> int:
+    """The given stream, or the current one of t's device."""
+    if stream is None and _RAW_STREAM is not None:
+        return _RAW_STREAM(t.get_device())
+    return _stream(stream)
+
+
 def _shape2(name, t):
-    if t.dim() != 2:
+    s = t.shape
+    if len(s) != 2:
         raise TpoError(TPO_ERR_INVALID_ARG, "%s must be 2-D" % name)
-    return t.shape
+    return s
 
 
 def tpo_block_workspace(op: int, n: int, k: int, m: int = 1) -> int:
@@ -395,7 +399,7 @@ def tpo_layer_norm(block: int, x, gamma, beta, y, mean=None, rstd=None, eps: flo
     py, ldy = _mat("y", y, n, k, dt)
     _check(lib().tpo_layer_norm(block, n, k, dt, wt, px, ldx, _vec("gamma", gamma, k, wt), _vec("beta", beta, k, wt),
                                 eps, py, ldy, _vec("mean", mean, n, TPO_F32), _vec("rstd", rstd, n, TPO_F32),
-                                _stream(stream)))
+                                _stream_of(stream, x)))
 
 
 def tpo_layer_norm_bwd(block: int, dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None,
@@ -411,7 +415,7 @@ def tpo_layer_norm_bwd(block: int, dy, x, gamma, mean, rstd, dx, dgamma=None, db
     _check(lib().tpo_layer_norm_bwd(block, n, k, dt, wt, pdy, lddy, px, ldx, _vec("gamma", gamma, k, wt),
                                     _vec("mean", mean, n, TPO_F32), _vec("rstd", rstd, n, TPO_F32), pdr, lddr, pdx,
                                     lddx, _vec("dgamma", dgamma, k, wt), _vec("dbeta", dbeta, k, wt),
-                                    _stream(stream)))
+                                    _stream_of(stream, dy)))
 
 
 def tpo_linear(block: int, x, w, y, bias=None, act: int = TPO_ACT_NONE, residual=None, z=None, scale_inv_x=None,
@@ -426,7 +430,7 @@ def tpo_linear(block: int, x, w, y, bias=None, act: int = TPO_ACT_NONE, residual
     pz, ldz = _mat("z", z, n, m, TPO_BF16)
     _check(lib().tpo_linear(block, n, k, m, dt, px, ldx, pw, ldw, _vec("bias", bias, m, TPO_BF16), act, pr, ldr, pz,
                             ldz, py, ldy, _vec("scale_inv_x", scale_inv_x, 1, TPO_F32),
-                            _vec("scale_inv_w", scale_inv_w, 1, TPO_F32), _stream(stream)))
+                            _vec("scale_inv_w", scale_inv_w, 1, TPO_F32), _stream_of(stream, x)))
 
 
 def tpo_linear_bwd(block: int, dy, x, w, dx=None, dw=None, db=None, act: int = TPO_ACT_NONE, z=None,
@@ -441,7 +445,7 @@ def tpo_linear_bwd(block: int, dy, x, w, dx=None, dw=None, db=None, act: int = T
     pdx, lddx = _mat("dx", dx, n, k, TPO_BF16)
     pdw, lddw = _mat("dw", dw, m, k, TPO_BF16)
     _check(lib().tpo_linear_bwd(block, n, k, m, act, pdy, lddy, pz, ldz, px, ldx, pw, ldw, pdx, lddx, pdw, lddw,
-                                _vec("db", db, m, TPO_BF16), _stream(stream)))
+                                _vec("db", db, m, TPO_BF16), _stream_of(stream, dy)))
 
 
 def tpo_gated(block: int, x, wg, wu, h, act: int = TPO_ACT_SILU, g=None, u=None, scale_inv_x=None,
@@ -457,7 +461,7 @@ def tpo_gated(block: int, x, wg, wu, h, act: int = TPO_ACT_SILU, g=None, u=None,
     pu, ldu = _mat("u", u, n, m, TPO_BF16)
     _check(lib().tpo_gated(block, n, k, m, dt, px, ldx, pwg, ldwg, pwu, ldwu, act, pg, ldg, pu, ldu, ph, ldh,
                            _vec("scale_inv_x", scale_inv_x, 1, TPO_F32), _vec("scale_inv_wg", scale_inv_wg, 1, TPO_F32),
-                           _vec("scale_inv_wu", scale_inv_wu, 1, TPO_F32), _stream(stream)))
+                           _vec("scale_inv_wu", scale_inv_wu, 1, TPO_F32), _stream_of(stream, x)))
 
 
 def tpo_gated_bwd(block: int, dh, g, u, x, wg, wu, dx=None, dwg=None, dwu=None, act: int = TPO_ACT_SILU,
@@ -468,4 +472,4 @@ def tpo_gated_bwd(block: int, dh, g, u, x, wg, wu, dx=None, dwg=None, dwu=None, 
     for name, t, rows, cols in (("dh", dh, n, m), ("g", g, n, m), ("u", u, n, m), ("x", x, n, k), ("wg", wg, m, k),
                                 ("wu", wu, m, k), ("dx", dx, n, k), ("dwg", dwg, m, k), ("dwu", dwu, m, k)):
         args += _mat(name, t, rows, cols, TPO_BF16)
-    _check(lib().tpo_gated_bwd(block, n, k, m, act, *args, _stream(stream)))
+    _check(lib().tpo_gated_bwd(block, n, k, m, act, *args, _stream_of(stream, dh)))
