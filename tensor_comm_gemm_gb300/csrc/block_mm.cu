@@ -224,26 +224,30 @@ __device__ void mma_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t 
   }
 }
 
-// Adds the first `count` (at most 32) of 32 consecutive bf16 values; `vec`: p is 16-byte aligned.
-__device__ __forceinline__ void add_row(const __nv_bfloat16* p, int count, bool vec, float (&v)[32]) {
-  if (vec && count >= 32) {
-    uint4 h[4];
+// 32 consecutive bf16 values as they lie in memory, and their addition.
+struct Row32 {
+  uint4 h[4];
+};
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, Row32& r) {
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) h[ch] = *reinterpret_cast<const uint4*>(p + 8 * ch);
+  for (int ch = 0; ch < 4; ++ch) r.h[ch] = *reinterpret_cast<const uint4*>(p + 8 * ch);
+}
+__device__ __forceinline__ void add_row(const Row32& r, float (&v)[32]) {
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
-      const uint32_t w[4] = {h[ch].x, h[ch].y, h[ch].z, h[ch].w};
+  for (int ch = 0; ch < 4; ++ch) {
+    const uint32_t w[4] = {r.h[ch].x, r.h[ch].y, r.h[ch].z, r.h[ch].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[8 * ch + 2 * j] += __uint_as_float(w[j] << 16);
-        v[8 * ch + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-      }
+    for (int j = 0; j < 4; ++j) {
+      v[8 * ch + 2 * j] += __uint_as_float(w[j] << 16);
+      v[8 * ch + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < count) v[j] += __bfloat162float(p[j]);
   }
+}
+// The first `count` (fewer than 32, or of any alignment) one by one.
+__device__ __forceinline__ void add_some(const __nv_bfloat16* p, int count, float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < count) v[j] += __bfloat162float(p[j]);
 }
 
 template <int ACT, int KIND>
@@ -305,12 +309,20 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
     const TileAt T = tile_at(p, t);
     const Prob& q = p.q[T.q];
     const uint32_t acc = ul & 1u;
-    if (!wait_bar_warp(p.err, tfull0 + 8u * acc, (ul >> 1) & 1u, S_TFULL)) break;
-    tc_fence_after();
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * TN;
     const int nch = (q.w + CHUNK - 1) / CHUNK;
     const int oy = T.row + TM * static_cast<int>(rank) + quad * 32;
     const int64_t row = static_cast<int64_t>(oy) + lane;
+    // the residual of this warp's next chunk, in flight beside the MMAs and the chunk before it
+    Row32 res;
+    auto fetch_residual = [&](int c) {
+      const int ox = T.col + c * CHUNK;
+      if (KIND == EPI_LINEAR && p.residual && c < nch && row < q.M && ox + CHUNK <= q.N)
+        load_row(p.residual + row * p.ldr + ox, res);
+    };
+    fetch_residual(half);
+    if (!wait_bar_warp(p.err, tfull0 + 8u * acc, (ul >> 1) & 1u, S_TFULL)) break;
+    tc_fence_after();
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * TN;
     const int last = (nch - 1 - half) / 2 * 2 + half;  // this warp's last chunk (if it has any)
     auto release = [&] {  // the accumulator is read: hand it back to the MMA warp
       tc_fence_before();
@@ -330,7 +342,15 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * s0;
       if constexpr (KIND == EPI_LINEAR) {
-        if (p.bias) add_row(p.bias + ox, q.N - ox, p.bias_vec, v);
+        if (p.bias) {
+          if (p.bias_vec && ox + CHUNK <= q.N) {
+            Row32 b;
+            load_row(p.bias + ox, b);
+            add_row(b, v);
+          } else {
+            add_some(p.bias + ox, q.N - ox, v);
+          }
+        }
         if (p.has1) store(&p.y1, v, ox, oy, q);
       }
       if constexpr (KIND == EPI_GATED) {
@@ -353,8 +373,12 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
       }
       if constexpr (KIND == EPI_LINEAR) {
         if (p.residual && row < q.M) {
-          add_row(p.residual + row * p.ldr + ox, q.N - ox, true, v);
+          if (ox + CHUNK <= q.N)
+            add_row(res, v);
+          else
+            add_some(p.residual + row * p.ldr + ox, q.N - ox, v);
         }
+        fetch_residual(c + 2);
       }
       store(&q.y, v, ox, oy, q);
     }
