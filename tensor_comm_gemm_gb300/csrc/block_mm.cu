@@ -456,11 +456,13 @@ int b_bytes(int w, bool gated, bool b_mn) {
   return b_mn ? (rows + 63) / 64 * 8192 : rows * KB;
 }
 
-// Time in ns of one K block of a tile with `cols` accumulator columns, when
-// all pairs work: measured on 8192-long contractions at 32 to 256 columns, 175
-// to 195 ns up to 128, then 218, 254, 282 and 320 (the tensor cores' two
-// cycles a column at the clock the power limit leaves).
-double kblock_ns(int cols) { return std::max(1.25 * cols, 165.0 + 0.25 * cols); }
+// Time in ns of one K block of a tile with `cols` accumulator columns: when all
+// pairs work for long, and the power limit sets the clock (measured 355, 312,
+// 280 and 212 at 256, 224, 192 and 128 columns), and in a round that leaves
+// pairs idle or is short (two cycles a column at the full clock; below 128
+// columns the loads' latency over the stages in flight, 175 to 190).
+double kblock_full_ns(int cols) { return std::max(71.0 + 1.1 * cols, 165.0 + 0.31 * cols); }
+double kblock_free_ns(int cols) { return std::max(1.05 * cols, 165.0 + 0.20 * cols); }
 
 }  // namespace
 
@@ -470,17 +472,24 @@ int plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool ga
   const int most = gated ? TN / 2 : TN;
   for (int w = most; w >= CHUNK; w -= CHUNK) {
     const int cols = gated ? 2 * w : w;
-    double ns = 12.0 * cols;  // the last tile's epilogue
-    int64_t done = 0;
+    double ns = 12.0 * cols, full = 0, free = 0;  // the last tile's epilogue; a tile of the last product
+    int64_t total = 0;
     for (int i = 0; i < count; ++i) {
       const int kb = ceil_div(q[i].K, fp8 ? KB : KB / 2) * q[i].terms;
       // a tile is as long as its K blocks, or the draining of its accumulator
-      const double tile = std::max(kb * kblock_ns(cols), 8.0 * cols + 300);
-      const int64_t end = done + static_cast<int64_t>(ceil_div(q[i].M, 2 * TM)) * ceil_div(q[i].N, w);
-      // rounds of one tile per pair over the products laid end to end: those that start in this one
-      ns += static_cast<double>((end + mc.pairs - 1) / mc.pairs - (done + mc.pairs - 1) / mc.pairs) * tile;
-      done = end;
+      const double drain = 8.0 * cols + 300;
+      full = std::max(kb * kblock_full_ns(cols), drain);
+      free = std::max(kb * kblock_free_ns(cols), drain);
+      const int64_t tiles = static_cast<int64_t>(ceil_div(q[i].M, 2 * TM)) * ceil_div(q[i].N, w);
+      ns += static_cast<double>(tiles) / mc.pairs * full;
+      total += tiles;
     }
+    // the last round, only partly filled, takes a whole tile's time at the clock that it has
+    const double part = static_cast<double>(total % mc.pairs) / mc.pairs;
+    if (total <= mc.pairs)
+      ns = 12.0 * cols + free;
+    else if (part > 0)
+      ns += std::max(0.0, free - part * full);
     if (!best || ns < 0.99 * best_ns) best = w, best_ns = ns;
   }
   if (us) *us = 4.0 + best_ns * 1e-3;
