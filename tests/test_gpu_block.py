@@ -580,3 +580,12 @@ def test_offsets_past_32_bits(any_path, block):
     want = R.linear_bwd(d(y), d(x), d(w))
     R.check("dx", back, want["dx"])
     R.check("dw", dw, want["dw"])
+
+
+# the stages' roundings to bf16 (norm, g, u, h, dh, dg, du, dnorm) add up to a few 2^-8 of each result's size
+@pytest.mark.parametrize("args", ["--tokens 300 --hidden 256 --ffn 384 --train", "--tokens 1 --hidden 512 --ffn 768",
+                                  "--tokens 512 --hidden 256 --ffn 512 --tp 2"])
+def test_example_layer(args):
+    from tensor_comm_gemm_gb300 import ffn_layer
+    errors = ffn_layer.main(args.split() + ["--check", "--calls", "2"])
+    assert errors and all(e < 4 * R.U16 for e in errors.values()), errors
