@@ -383,7 +383,7 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
       store(&q.y, v, ox, oy, q);
     }
   }
-  if (lane == 0) bulk_wait<0>();
+  if (lane == 0) bulk_wait_read<0>();  // the boxes are read; the stores themselves end with the kernel
   __syncwarp();
 }
 

@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
       tc_fence_before();
     }
   }
-  __syncthreads();
-  cluster_sync();
+  __syncwarp();
+  cluster_sync();  // every thread of the cluster
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_cg<1>(tmem, p.tmem_cols);
@@ -271,7 +271,8 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     }
     put4(p.out + row * p.ldo + col, v, count);
   }
-  cluster_sync();  // no CTA leaves while a peer reads its shared memory
+  __syncwarp();
+  cluster_sync_relaxed();  // no CTA leaves while a peer reads its shared memory
 }
 
 template <int KIND, bool FP8>
