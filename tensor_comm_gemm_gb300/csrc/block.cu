@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <new>
 
 #include "block.h"
 
@@ -178,7 +179,11 @@ tpo_block* tpo_block_create(int64_t workspace_bytes) {
     fail(TPO_ERR_INVALID_ARG, "workspace_bytes=%lld is negative", (long long)workspace_bytes);
     return nullptr;
   }
-  tpo_block* b = new tpo_block();
+  tpo_block* b = new (std::nothrow) tpo_block();
+  if (!b) {
+    fail(TPO_ERR_OOM, "no host memory for a handle");
+    return nullptr;
+  }
   int major = 0, minor = 0;
   cudaError_t e = cudaGetDevice(&b->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, b->device);

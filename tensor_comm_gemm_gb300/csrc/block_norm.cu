@@ -272,6 +272,9 @@ __device__ __forceinline__ void copy_wait(int ahead) {
 // bring a few bytes of what lies beside it, which nobody reads; where that
 // would be outside the matrix (before row 0, behind the last row) only the
 // row's own bytes are touched.
+__host__ __device__ inline uint32_t weight_bytes(int k, int elem) {
+  return (static_cast<uint32_t>(k) * elem + 15u) & ~15u;
+}
 __host__ __device__ inline uint32_t row_bytes(int k, int elem) {
   return ((static_cast<uint32_t>(k) * elem + 15u) & ~15u) + 16u;
 }
@@ -309,6 +312,16 @@ __device__ __forceinline__ const T* unit_row(const T* src, const uint8_t* slot) 
 // has l, l + tpr, ...), which keeps the group's accesses of one step together:
 // 16384 x 4096 backward 78 us, 87 with vectors dealt out by warp.
 constexpr int RING_THREADS = 512;
+// Copies k weights to shared memory and adds zeros up to `all` (the block joins afterwards).
+template <class W, int VEC>
+__device__ __forceinline__ void keep_weights(W* to, const W* from, int k, int all) {
+  if (from)
+    for (int c = threadIdx.x * VEC; c < all; c += RING_THREADS * VEC) {
+      Vec<W, VEC> v = {};
+      if (c < k) v = load<W, VEC>(from + c);
+      *reinterpret_cast<Vec<W, VEC>*>(to + c) = v;
+    }
+}
 template <int VEC, int NV>
 __device__ __forceinline__ int first_column(int tpr) {
   const int lane = static_cast<int>(threadIdx.x & (tpr - 1));
@@ -322,8 +335,8 @@ __device__ __forceinline__ int column_step(int tpr) {
 // Forward: `depth` rows of each group are in flight or in use.  FULL: the
 // group's vectors are exactly a row's.
 template <class T, class W, int VEC, int NV, bool FULL>
-__global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int tpr, int depth, int weights) {
-  extern __shared__ __align__(16) uint8_t ring[];
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int tpr, int depth) {
+  extern __shared__ __align__(16) uint8_t smem[];  // gamma, beta, the rows in flight, slack to read past them
   __shared__ float red[4][RING_THREADS / 32];
   constexpr int L = VEC > 1 ? 2 : 1, NN = VEC / L;
   grid_dep_launch();
@@ -333,6 +346,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
   const int k = static_cast<int>(a.k);
+  W* const gamma = reinterpret_cast<W*>(smem);
+  W* const beta = reinterpret_cast<W*>(smem + weight_bytes(k, sizeof(W)));
+  uint8_t* const ring = smem + 2 * weight_bytes(k, sizeof(W));
   // slot s of this thread's vectors, or of its group's row
   const uint32_t slot_bytes = VEC > 1 ? NV * RING_THREADS * 16 : groups * row_bytes(k, sizeof(T));
   uint8_t* const mine = ring + (VEC > 1 ? threadIdx.x * 16 : group * row_bytes(k, sizeof(T)));
@@ -352,18 +368,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
     copy_commit();
   };
   for (int d = 0; d < depth - (VEC == 1); ++d) fetch(row + d * step, d);
-  // gamma and beta stay in shared memory if they fit beside the rows
-  const W *gamma = static_cast<const W*>(a.gamma), *beta = static_cast<const W*>(a.beta);
-  if (weights) {
-    W* keep = reinterpret_cast<W*>(ring + depth * slot_bytes);
-    for (int c = threadIdx.x * VEC; c < k; c += RING_THREADS * VEC) {
-      if (gamma) *reinterpret_cast<Vec<W, VEC>*>(keep + c) = load<W, VEC>(gamma + c);
-      if (beta) *reinterpret_cast<Vec<W, VEC>*>(keep + k + c) = load<W, VEC>(beta + c);
-    }
-    if (gamma) gamma = keep;
-    if (beta) beta = keep + k;
-    __syncthreads();
-  }
+  keep_weights<W, VEC>(gamma, static_cast<const W*>(a.gamma), k, k);
+  keep_weights<W, VEC>(beta, static_cast<const W*>(a.beta), k, k);
+  __syncthreads();
+  const bool has_gamma = a.gamma != nullptr, has_beta = a.beta != nullptr;
   const float inv_k = 1.0f / static_cast<float>(k);
   int slot = 0, buf = 0;
   // every group of the block runs the same number of rounds
@@ -384,7 +392,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
       const T* x = unit_row(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx, mine + slot * slot_bytes) + c0;
       const int own = live ? k - c0 : 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i][0].v = i * 32 < own ? to_f(x[i * 32]) : 0.0f;
+      for (int i = 0; i < NV; ++i) {
+        const float e = to_f(x[i * 32]);  // past the row's end: whatever lies there, in shared memory all the same
+        v[i][0].v = i * 32 < own ? e : 0.0f;
+      }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -411,13 +422,13 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
       const int c = (c0 + i * step_c);
       if (!FULL && c >= k) continue;
       Num<L> g[NN], b[NN];
-      if (gamma) to_nums<W, VEC, L>(load<W, VEC>(gamma + c), g);
-      if (beta) to_nums<W, VEC, L>(load<W, VEC>(beta + c), b);
+      if (has_gamma) to_nums<W, VEC, L>(load<W, VEC>(gamma + c), g);
+      if (has_beta) to_nums<W, VEC, L>(load<W, VEC>(beta + c), b);
 #pragma unroll
       for (int j = 0; j < NN; ++j) {
         v[i][j] = mul(v[i][j], scale);
-        if (gamma) v[i][j] = mul(v[i][j], g[j]);
-        if (beta) v[i][j] = add(v[i][j], b[j]);
+        if (has_gamma) v[i][j] = mul(v[i][j], g[j]);
+        if (has_beta) v[i][j] = add(v[i][j], b[j]);
       }
       if (live) *reinterpret_cast<Vec<T, VEC>*>(y + c) = from_nums<T, VEC, L>(v[i]);
     }
@@ -462,7 +473,7 @@ __device__ __forceinline__ void store_sums(const Num<L> (&dg)[NV][VEC / L], cons
 template <class T, class W, int VEC, int NV>
 __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const NormArgs a, int tpr, int depth,
                                                                         float* part) {
-  extern __shared__ __align__(16) uint8_t ring[];
+  extern __shared__ __align__(16) uint8_t smem[];  // gamma, the rows in flight, slack to read past them
   __shared__ float2 red[2][RING_THREADS / 32];
   constexpr int L = VEC > 1 ? 2 : 1, NN = VEC / L;
   constexpr bool KEEP = NV * VEC <= 16;  // xhat and dy gamma stay in registers from the sums to dx
@@ -474,6 +485,11 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
   const int k = static_cast<int>(a.k);
   const int arrays = a.dres && a.y ? 3 : 2;
+  // bf16 gamma of few vectors stays in registers, other gammas in shared memory
+  constexpr bool GREG = KEEP && VEC > 1 && sizeof(W) == 2;
+  W* const gamma = reinterpret_cast<W*>(smem);
+  uint8_t* const ring = smem + (GREG ? 0u : weight_bytes(tpr * NV * VEC, sizeof(W)));
+  const bool has_gamma = a.gamma != nullptr;
   // slot s, matrix w: this thread's vectors, or its group's row
   const uint32_t part_bytes = VEC > 1 ? NV * RING_THREADS * 16 : groups * row_bytes(k, sizeof(T));
   uint8_t* const mine = ring + (VEC > 1 ? threadIdx.x * 16 : group * row_bytes(k, sizeof(T)));
@@ -504,17 +520,18 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
     copy_commit();
   };
   for (int d = 0; d < depth - (VEC == 1); ++d) fetch(row + d * step, d);
-  const W* gamma = static_cast<const W*>(a.gamma);
-  // bf16 gamma of few vectors stays in registers
-  constexpr bool GREG = KEEP && sizeof(W) == 2;
   Vec<W, VEC> gk[GREG ? NV : 1];
-  if constexpr (GREG)
+  if constexpr (GREG) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (c0 + i * step_c);
+      const int c = c0 + i * step_c;
       gk[i] = {};
-      if (gamma && c < k) gk[i] = load<W, VEC>(gamma + c);
+      if (has_gamma && c < k) gk[i] = load<W, VEC>(static_cast<const W*>(a.gamma) + c);
     }
+  } else {
+    keep_weights<W, VEC>(gamma, static_cast<const W*>(a.gamma), k, tpr * NV * VEC);  // zeros past the row's end
+    __syncthreads();
+  }
   Num<L> dg[NV][NN], db[NV][NN];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -548,11 +565,18 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
         to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 0) + i * (RING_THREADS * 16)), h);
         to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 1) + i * (RING_THREADS * 16)), w);
       } else {
+        // past the row's end: whatever lies there, in shared memory all the same
+        const float ex = to_f(ux[i * 32]), ed = to_f(ud[i * 32]);
         const bool in = i * 32 < own;
-        h[0].v = in ? to_f(ux[i * 32]) : 0.0f;
-        w[0].v = in ? to_f(ud[i * 32]) : 0.0f;
+        h[0].v = in ? ex : 0.0f;
+        w[0].v = in ? ed : 0.0f;
       }
-      if (gamma) to_nums<W, VEC, L>(GREG ? gk[GREG ? i : 0] : load<W, VEC>(gamma + (c < k ? c : 0)), g);
+      if (has_gamma) {
+        if constexpr (GREG)
+          to_nums<W, VEC, L>(gk[i], g);
+        else
+          to_nums<W, VEC, L>(load<W, VEC>(gamma + c), g);
+      }
 #pragma unroll
       for (int j = 0; j < NN; ++j) {
         h[j] = mul(add(h[j], minus), scale);
@@ -560,7 +584,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
           dg[i][j] = fma(w[j], h[j], dg[i][j]);
           db[i][j] = add(db[i][j], w[j]);
         }
-        if (gamma) w[j] = mul(w[j], g[j]);
+        if (has_gamma) w[j] = mul(w[j], g[j]);
       }
     };
     Num<L> hk[KEEP ? NV : 1][NN], wk[KEEP ? NV : 1][NN];
@@ -591,7 +615,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
           if constexpr (VEC > 1)
             to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 2) + i * (RING_THREADS * 16)), r);
           else
-            r[0].v = i * 32 < own ? to_f(ur[i * 32]) : 0.0f;
+            r[0].v = to_f(ur[i * 32]);
         }
 #pragma unroll
         for (int j = 0; j < NN; ++j) {
@@ -744,23 +768,29 @@ Share share_single(int64_t k) {
   return best;
 }
 
-// Rows in flight per group and the shared memory they take; depth < 2: they do not fit.
+// Rows in flight per group and the shared memory of a block that also keeps
+// `fixed` bytes of weights; depth < 2: they do not fit.
+constexpr size_t RING_SMEM = 226 * 1024;
 struct Ring {
   int depth;
   size_t smem;
 };
-Ring ring_of(bool vec, const Share& h, int arrays, int64_t k, int elem, size_t most) {
+Ring ring_of(bool vec, const Share& h, int arrays, int64_t k, int elem, size_t fixed) {
+  if (!h.tpr) return {0, 0};
   const size_t slot = arrays * (vec ? static_cast<size_t>(RING_THREADS) * h.nv * 16
-                                    : static_cast<size_t>(RING_THREADS / h.tpr) * (((k * elem + 15) & ~15ll) + 16));
+                                    : static_cast<size_t>(RING_THREADS / h.tpr) * row_bytes(static_cast<int>(k), elem));
+  // single elements are also read past the row's end
+  const size_t rest = fixed + (vec ? 0 : static_cast<size_t>(h.tpr) * h.nv * elem);
+  if (rest >= RING_SMEM) return {0, 0};
   Ring r;
-  r.depth = static_cast<int>(std::min<size_t>(4, most / slot));
-  r.smem = slot * r.depth;
+  r.depth = static_cast<int>(std::min<size_t>(4, (RING_SMEM - rest) / slot));
+  r.smem = rest + slot * r.depth;
   return r;
 }
 
 template <class K>
 cudaError_t allow_smem(K* kernel) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_SMEM);
 }
 
 }  // namespace
@@ -780,15 +810,13 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
     // 57, and then 70 with two vectors and 98 with eight.
     const Share m = vec ? share(vecs, 4, 4, RING_THREADS, 32) : share_single(a.k);
     const int64_t sets = m.tpr ? (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr) : 0;
-    if (sets >= (vec ? 2 : 1) * static_cast<int64_t>(mc.sms)) {
-      const size_t wb = vec && a.k * sizeof(W) <= 16384 && (a.gamma || a.beta) ? 2 * a.k * sizeof(W) : 0;
-      const Ring r = ring_of(vec, m, 1, a.k, sizeof(T), 200 * 1024 - wb);
+    // (rows of up to 64 vectors would leave half of a group's threads idle)
+    if (sets >= (vec ? 2 : 1) * static_cast<int64_t>(mc.sms) && (!vec || vecs > 64)) {
+      const Ring r = ring_of(vec, m, 1, a.k, sizeof(T), 2 * weight_bytes(static_cast<int>(a.k), sizeof(W)));
       const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sets, mc.sms)));
       auto run = [&](auto kernel) {
         const cudaError_t e = allow_smem(kernel);
-        return e != cudaSuccess ? e
-                                : launch_pdl(kernel, grid, dim3(RING_THREADS), r.smem + wb, s, a, m.tpr, r.depth,
-                                             static_cast<int>(wb != 0));
+        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(RING_THREADS), r.smem, s, a, m.tpr, r.depth);
       };
       if (r.depth >= 2) {
         if (vec)
@@ -826,12 +854,13 @@ cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int
     // 16 elements a thread (rows up to 8192), else 32 of whole vectors
     constexpr int NV = 16 / V;
     const Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS, 32) : share_single(a.k);
-    const Ring r = h.tpr ? ring_of(vec, h, a.dres && a.y ? 3 : 2, a.k, sizeof(T), 200 * 1024) : Ring{0, 0};
+    const size_t kept = vec && h.nv == NV && sizeof(W) == 2 ? 0 : weight_bytes(h.tpr * h.nv * (vec ? V : 1), sizeof(W));
+    const Ring r = ring_of(vec, h, a.dres && a.y ? 3 : 2, a.k, sizeof(T), kept);
     if (r.depth >= 2 && a.n > 0) {
       const int64_t sets = (a.n + RING_THREADS / h.tpr - 1) / (RING_THREADS / h.tpr);
       parts = static_cast<int>(std::min<int64_t>({sets, mc.sms, NORM_PARTS}));
       // the slots later hold every group's fp32 sums
-      const size_t smem = std::max(r.smem, static_cast<size_t>(RING_THREADS / h.tpr) * 8 * a.k);
+      const size_t smem = std::max(r.smem, kept + static_cast<size_t>(RING_THREADS / h.tpr) * 8 * a.k);
       auto run = [&](auto kernel) {
         const cudaError_t c = allow_smem(kernel);
         return c != cudaSuccess ? c : launch_pdl(kernel, dim3(parts), dim3(RING_THREADS), smem, s, a, h.tpr, r.depth, part);
