@@ -31,22 +31,27 @@ namespace {
 constexpr int TM = 128;              // rows of one CTA; a pair's tile has 256
 constexpr int TN = 256;              // most columns of a tile (accumulator width)
 constexpr int A_BYTES = TM * KB;     // 16 KiB
-constexpr int STAGE_AREA = 196608;   // pipeline stages: an A block and half of the tile's B rows each
-constexpr int MAX_STAGES = 12;       // 6 with 256-column tiles
+constexpr int MAX_STAGES = 12;       // pipeline stages: an A block and half of the tile's B rows each
 constexpr int EPI_WARPS_N = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS_N;
 constexpr int CHUNK = 32;                   // columns of one epilogue step
 constexpr int BOX = 32 * CHUNK * 2;         // bytes of one output box: 32 rows of 64 bytes
-constexpr int OFF_EPI = STAGE_AREA;
-constexpr int OFF_BARS = OFF_EPI + EPI_WARPS_N * 2 * BOX;
+// The plain epilogue of products with few K blocks (weight gradients of few
+// tokens), which the stores bound, takes 64 columns at a time, boxes of
+// 128-byte rows, and gives a pipeline stage up for them: 4096x4096 from 16
+// tokens 13.9 us, 15.7 with the narrow boxes; with 64 K blocks 79 and 76.
+constexpr int STAGES_NARROW = 196608, STAGES_WIDE = 163840;  // bytes of pipeline stages
+constexpr int OFF_BARS = STAGES_NARROW + EPI_WARPS_N * 2 * BOX;  // behind the staging boxes, two a warp
+static_assert(OFF_BARS == STAGES_WIDE + EPI_WARPS_N * 2 * 2 * BOX, "one layout behind the stages and boxes");
+constexpr int WIDE_KB = 16;  // K blocks of a product up to which its launch takes the wide boxes
 constexpr int N_BARS = 2 * MAX_STAGES + 2 + 2 + 1;
 constexpr int OFF_TMEM = OFF_BARS + 8 * N_BARS;
 constexpr int SMEM = OFF_TMEM + 16 + 1024;  // and the slack to align the base
 static_assert(SMEM <= 232448, "shared memory of one CTA");
 
-// An output matrix: its map for tensor stores, and its address for ragged edges.
+// An output matrix: its maps for tensor stores (boxes of 32 and 64 columns), and its address for ragged edges.
 struct OutMat {
-  CUtensorMap map;
+  CUtensorMap map, wide;
   __nv_bfloat16* p;
   int64_t ld;
 };
@@ -64,6 +69,7 @@ struct Args {
   OutMat y1, y2;
   int count, total;
   uint32_t stages, stage_bytes;
+  int wide;             // 64-column boxes
   int act;
   const __nv_bfloat16 *bias, *residual;
   int64_t ldr;
@@ -266,7 +272,9 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
                               uint32_t rank, int pair, int pairs) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = (warp - 2) >> 2;
-  const uint32_t ebase = sbase + OFF_EPI + (warp - 2) * 2 * BOX;
+  const bool wide = KIND == EPI_PLAIN && p.wide;
+  const uint32_t box_bytes = wide ? 2 * BOX : BOX;
+  const uint32_t ebase = sbase + (wide ? STAGES_WIDE : STAGES_NARROW) + (warp - 2) * 2 * box_bytes;
   const float s0 = FP8 ? __ldg(p.sx) * __ldg(p.sw0) : 1.0f;
   const float s1 = FP8 && KIND == EPI_GATED ? __ldg(p.sx) * __ldg(p.sw1) : 1.0f;
   uint32_t ul = 0, nst = 0;
@@ -284,7 +292,7 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
       }
       return;
     }
-    const uint32_t buf = ebase + (nst & 1u) * BOX;
+    const uint32_t buf = ebase + (nst & 1u) * box_bytes;
     ++nst;
     if (lane == 0) bulk_wait_read<1>();  // the store before last has read this buffer
     __syncwarp();
@@ -309,6 +317,59 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
     const TileAt T = tile_at(p, t);
     const Prob& q = p.q[T.q];
     const uint32_t acc = ul & 1u;
+    if (wide) {
+      if (!wait_bar_warp(p.err, tfull0 + 8u * acc, (ul >> 1) & 1u, S_TFULL)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * TN;
+      const int oy = T.row + TM * static_cast<int>(rank) + quad * 32, nw = (q.w + 63) / 64;
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(tempty0 + 8u * acc, 0));
+      };
+      if (half >= nw) release();
+#pragma unroll 1
+      for (int c = half; c < nw; c += 2) {
+        uint32_t r[64];
+        tmem_ld64_sync(taddr + c * 64, r);
+        if (c + 2 >= nw) release();
+        const int ox = T.col + c * 64, cols = min(64, q.w - c * 64);
+        if (ox >= q.N || oy >= q.M) continue;  // wholly past the output's edge
+        if (cols == 64 && (ox + 64 <= q.N || !(q.N & 7))) {
+          const uint32_t buf = ebase + (nst & 1u) * box_bytes;
+          ++nst;
+          uint32_t h[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            h[j] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          if (lane == 0) bulk_wait_read<1>();  // the store before last has read this buffer
+          __syncwarp();
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch)  // row `lane` of 128 bytes, 128-byte swizzle
+            st_shared_v4(buf + lane * 128 + (static_cast<uint32_t>(ch ^ (lane & 7)) << 4), h[4 * ch], h[4 * ch + 1],
+                         h[4 * ch + 2], h[4 * ch + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&q.y.wide, buf, ox, oy);
+            bulk_commit();
+          }
+        } else {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          store(&q.y, v, ox, oy, q);
+          if (cols > 32 && ox + 32 < q.N) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[32 + j]);
+            store(&q.y, v, ox + 32, oy, q);
+          }
+        }
+      }
+      continue;
+    }
     const int nch = (q.w + CHUNK - 1) / CHUNK;
     const int oy = T.row + TM * static_cast<int>(rank) + quad * 32;
     const int64_t row = static_cast<int64_t>(oy) + lane;
@@ -443,10 +504,11 @@ __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_const
 
 // ------------------------------------------------------------------ host side
 
-bool encode_out(OutMat* o, void* p, int64_t ld, int64_t M, int64_t N) {
+bool encode_out(OutMat* o, void* p, int64_t ld, int64_t M, int64_t N, bool wide) {
   o->p = static_cast<__nv_bfloat16*>(p);
   o->ld = ld;
-  return encode(&o->map, p, false, N, M, ld, CHUNK, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  return encode(&o->map, p, false, N, M, ld, CHUNK, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
+         (!wide || encode(&o->wide, p, false, N, M, ld, 2 * CHUNK, 32, CU_TENSOR_MAP_SWIZZLE_128B));
 }
 
 // Bytes of a CTA's share of a B block of a tile w columns wide (w of h for the
@@ -557,6 +619,8 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
   p.count = count;
   const int w = plan_width(mc, q, count, fp8, e.kind == EPI_GATED, nullptr);
   int stage = 0;
+  for (int i = 0; i < count; ++i)
+    if (e.kind == EPI_PLAIN && ceil_div(q[i].K, KB / 2) * q[i].terms <= WIDE_KB) p.wide = 1;
   bool ok = true;
   for (int i = 0; i < count; ++i) {
     const Product& c = q[i];
@@ -574,14 +638,14 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
     for (int t = 0; t < c.terms && ok; ++t)
       ok = encode_operand(&o.a[t], c.a[t], fp8, c.M, c.K, TM) && encode_operand(&o.b[t], c.b[t], fp8, c.N, c.K, hb);
     if (ok && e.kind == EPI_GATED) ok = encode_operand(&o.b[1], c.b[1], fp8, c.N, c.K, hb);
-    ok = ok && encode_out(&o.y, c.out, c.ldo, c.M, c.N);
+    ok = ok && encode_out(&o.y, c.out, c.ldo, c.M, c.N, p.wide);
     p.total += o.tiles;
   }
-  if (e.out1) ok = ok && encode_out(&p.y1, e.out1, e.ld1, q[0].M, q[0].N);
-  if (e.out2) ok = ok && encode_out(&p.y2, e.out2, e.ld2, q[0].M, q[0].N);
+  if (e.out1) ok = ok && encode_out(&p.y1, e.out1, e.ld1, q[0].M, q[0].N, false);
+  if (e.out2) ok = ok && encode_out(&p.y2, e.out2, e.ld2, q[0].M, q[0].N, false);
   if (!ok) return cudaErrorInvalidValue;
   p.stage_bytes = static_cast<uint32_t>(stage);
-  p.stages = static_cast<uint32_t>(std::min(MAX_STAGES, STAGE_AREA / stage));
+  p.stages = static_cast<uint32_t>(std::min(MAX_STAGES, (p.wide ? STAGES_WIDE : STAGES_NARROW) / stage));
   p.has1 = e.out1 != nullptr;
   p.act = e.act;
   p.bias = static_cast<const __nv_bfloat16*>(e.bias);
