@@ -451,8 +451,7 @@ tpo_status tpo_block_destroy(tpo_block* blk);
  * Options (integers, 0 by default) that choose how the products run; results
  * agree within the rounding of fp32 sums.
  *   "path"   0 by rule; 1 CTA pairs (256-row tiles); 2 clusters that cut the
- *            contraction (for few rows), where a product has that form: the
- *            forward products and dx
+ *            contraction (for few rows, or small weights' gradients)
  *   "split"  CTAs of such a cluster, 1..8; 0 by rule
  * Unknown keys or values out of range: TPO_ERR_INVALID_ARG.
  */

@@ -141,6 +141,51 @@ cudaError_t run_product(tpo_block* b, const tpo::Product& q, bool fp8, const tpo
   return tpo::launch_products(b->machine, &q, 1, fp8, e, b->err(), s);
 }
 
+// The gradients' products: dx (if wanted) first, then the weights' gradients,
+// which are of one shape.  Each of the two kinds runs on clusters by itself or
+// on CTA pairs, there all in one launch: whichever the models add up to least.
+cudaError_t run_products(tpo_block* b, const tpo::Product* q, int count, int dx, cudaStream_t s) {
+  tpo::SplitPlan plans[3];
+  double alone[3] = {};
+  bool can[3] = {};
+  for (int i = 0; i < count; ++i)
+    can[i] = tpo::split_cost(b->machine, q[i], b->path, b->split, &plans[i], &alone[i]);
+  int best = 0;
+  double best_us = 0;
+  for (int choice = 0; choice < 4; ++choice) {  // bit 0: dx on clusters, bit 1: the weights' gradients
+    tpo::Product rest[3];
+    int left = 0;
+    double us = 0;
+    bool ok = true;
+    for (int i = 0; i < count; ++i) {
+      if (choice >> (i < dx ? 0 : 1) & 1) {
+        ok = ok && can[i];
+        us += alone[i];
+      } else {
+        rest[left++] = q[i];
+      }
+    }
+    if (!ok || ((choice & 1) && dx == 0) || ((choice & 2) && dx == count)) continue;
+    double pairs_us = 0;
+    int widths[3];
+    if (left) tpo::plan_width(b->machine, rest, left, false, false, widths, &pairs_us);
+    us += pairs_us;
+    if (b->path == 2) us = -choice;  // every product on clusters
+    if (choice == 0 || us < best_us) best = choice, best_us = us;
+  }
+  tpo::Product rest[3];
+  int left = 0;
+  for (int i = 0; i < count; ++i) {
+    if (!(best >> (i < dx ? 0 : 1) & 1)) {
+      rest[left++] = q[i];
+      continue;
+    }
+    const cudaError_t e = tpo::launch_split(q[i], plans[i], false, tpo::Epi(), b->err(), s);
+    if (e != cudaSuccess) return e;
+  }
+  return left ? tpo::launch_products(b->machine, rest, left, false, tpo::Epi(), b->err(), s) : cudaSuccess;
+}
+
 tpo_status launched(cudaError_t e) { return e == cudaSuccess ? TPO_OK : cuda_fail(e, "kernel launch"); }
 
 // dz, then the bias gradient's per-block sums
@@ -388,15 +433,8 @@ tpo_status tpo_linear_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act
   tpo::Product q[2];
   int count = 0;
   if (dx) q[count++] = {{{dz, lddz, false}}, {{w, mw.ld, true}}, 1, n, k, m, dx, mdx.ld};
-  if (dx) {
-    tpo::SplitPlan plan;
-    if (tpo::use_split(b->machine, q[0], false, false, b->path, b->split, &plan)) {
-      if (tpo_status st = launched(tpo::launch_split(q[0], plan, false, tpo::Epi(), b->err(), s))) return st;
-      count = 0;
-    }
-  }
   if (dw) q[count++] = {{{dz, lddz, true}}, {{x, mx.ld, true}}, 1, m, k, n, dw, mdw.ld};
-  return count ? launched(tpo::launch_products(b->machine, q, count, false, tpo::Epi(), b->err(), s)) : TPO_OK;
+  return launched(run_products(b, q, count, dx ? 1 : 0, s));
 }
 
 tpo_status tpo_gated(tpo_block* b, int64_t n, int64_t k, int64_t m, int dtype, const void* x, int64_t ldx,
@@ -466,18 +504,11 @@ tpo_status tpo_gated_bwd(tpo_block* b, int64_t n, int64_t k, int64_t m, int act,
   int count = 0;
   if (dx)
     q[count++] = {{{dg, ld, false}, {du, ld, false}}, {{wg, mwg.ld, true}, {wu, mwu.ld, true}}, 2, n, k, m, dx, mdx.ld};
-  if (dx) {
-    tpo::SplitPlan plan;
-    if (tpo::use_split(b->machine, q[0], false, false, b->path, b->split, &plan)) {
-      if (tpo_status st = launched(tpo::launch_split(q[0], plan, false, tpo::Epi(), b->err(), s))) return st;
-      count = 0;
-    }
-  }
   if (dwg) {
     q[count++] = {{{dg, ld, true}}, {{x, mx.ld, true}}, 1, m, k, n, dwg, mdwg.ld};
     q[count++] = {{{du, ld, true}}, {{x, mx.ld, true}}, 1, m, k, n, dwu, mdwu.ld};
   }
-  return count ? launched(tpo::launch_products(b->machine, q, count, false, tpo::Epi(), b->err(), s)) : TPO_OK;
+  return launched(run_products(b, q, count, dx ? 1 : 0, s));
 }
 
 }  // extern "C"

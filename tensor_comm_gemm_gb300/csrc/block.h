@@ -51,12 +51,12 @@ struct Machine {
 };
 // Also set the kernels' attributes.
 cudaError_t configure_products(Machine* m);
-// The column tiles' width, one for all products of a launch, and the launch's
-// modelled time.  Narrower tiles than the widest cost more per column, so they
+// The column tiles' width of each product of a launch (all after the first are
+// of one shape), and the launch's modelled time.  Narrower tiles than the widest cost more per column, so they
 // are taken where they fill a last round or spread few tiles over the pairs
 // (4096^3: 224 columns 84.8 us, 256 86.7, 192 88.2; 1777x4096x2*14336: 256
 // columns 246 us, 192 253).
-int plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, double* us);
+void plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, int* widths, double* us);
 // Runs `count` (1 to 3) products in one launch; more than one take EPI_PLAIN.
 cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, uint32_t* err,
                             cudaStream_t s);
@@ -70,6 +70,8 @@ struct SplitPlan {
 cudaError_t configure_split(Machine* m);
 // Whether the product takes that form (path 0: by rule, 1: never, 2: always; split 0: by rule), and its plan.
 bool use_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t path, int64_t split, SplitPlan* plan);
+// Its plan and modelled time for a bf16 product without an epilogue; false if path or the device rule it out.
+bool split_cost(const Machine& mc, const Product& q, int64_t path, int64_t split, SplitPlan* plan, double* us);
 cudaError_t launch_split(const Product& q, const SplitPlan& plan, bool fp8, const Epi& e, uint32_t* err,
                          cudaStream_t s);
 

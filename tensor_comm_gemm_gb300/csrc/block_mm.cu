@@ -525,37 +525,55 @@ int b_bytes(int w, bool gated, bool b_mn) {
 // columns the loads' latency over the stages in flight, 175 to 190).
 double kblock_full_ns(int cols) { return std::max(71.0 + 1.1 * cols, 165.0 + 0.31 * cols); }
 double kblock_free_ns(int cols) { return std::max(1.05 * cols, 165.0 + 0.20 * cols); }
+// Rows that do not begin on 128-byte lines touch two of them a box (measured
+// 225 ns a K block at least, and 300 with a transposed B).
+double kblock_least_ns(const Product& q, bool fp8) {
+  const int lines = fp8 ? 128 : 64;
+  double ns = 0;
+  for (int t = 0; t < q.terms; ++t)
+    if (q.a[t].ld % lines || q.b[t].ld % lines) ns = std::max(ns, q.b[t].mn_major && q.b[t].ld % lines ? 300.0 : 225.0);
+  return ns;
+}
 
 }  // namespace
 
-int plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, double* us) {
-  int best = 0;
-  double best_ns = 0;
-  const int most = gated ? TN / 2 : TN;
-  for (int w = most; w >= CHUNK; w -= CHUNK) {
-    const int cols = gated ? 2 * w : w;
-    double ns = 12.0 * cols, full = 0, free = 0;  // the last tile's epilogue; a tile of the last product
-    int64_t total = 0;
-    for (int i = 0; i < count; ++i) {
-      const int kb = ceil_div(q[i].K, fp8 ? KB : KB / 2) * q[i].terms;
-      // a tile is as long as its K blocks, or the draining of its accumulator
-      const double drain = 8.0 * cols + 300;
-      full = std::max(kb * kblock_full_ns(cols), drain);
-      free = std::max(kb * kblock_free_ns(cols), drain);
-      const int64_t tiles = static_cast<int64_t>(ceil_div(q[i].M, 2 * TM)) * ceil_div(q[i].N, w);
-      ns += static_cast<double>(tiles) / mc.pairs * full;
-      total += tiles;
-    }
-    // the last round, only partly filled, takes a whole tile's time at the clock that it has
-    const double part = static_cast<double>(total % mc.pairs) / mc.pairs;
-    if (total <= mc.pairs)
-      ns = 12.0 * cols + free;
-    else if (part > 0)
-      ns += std::max(0.0, free - part * full);
-    if (!best || ns < 0.99 * best_ns) best = w, best_ns = ns;
+void plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, int* widths, double* us) {
+  // the products' shapes: the first, and the others, which are alike
+  const int most = gated ? TN / 2 : TN, kinds = count > 1 ? 2 : 1;
+  double least[2] = {}, best_ns = 0;
+  int64_t rows[2] = {}, kbs[2] = {};
+  for (int i = 0; i < kinds; ++i) {
+    least[i] = kblock_least_ns(q[i], fp8);
+    rows[i] = static_cast<int64_t>(ceil_div(q[i].M, 2 * TM)) * (i == 0 ? 1 : count - 1);
+    kbs[i] = static_cast<int64_t>(ceil_div(q[i].K, fp8 ? KB : KB / 2)) * q[i].terms;
   }
+  int w[2] = {most, most}, best[2] = {0, 0};
+  for (w[0] = most; w[0] >= CHUNK; w[0] -= CHUNK)
+    for (w[1] = most; w[1] >= CHUNK; w[1] -= kinds > 1 ? 2 * CHUNK : most) {
+      double ns = 0, full = 0, free = 0, longest = 0;  // full, free: a tile of the last product
+      int64_t total = 0;
+      for (int i = 0; i < kinds; ++i) {
+        const int cols = gated ? 2 * w[i] : w[i];
+        // a tile is as long as its K blocks, or the draining of its accumulator
+        const double drain = 8.0 * cols + 300, k = static_cast<double>(kbs[i]);
+        full = std::max(k * std::max(kblock_full_ns(cols), least[i]), drain);
+        free = std::max(k * std::max(kblock_free_ns(cols), least[i]), drain);
+        longest = std::max(longest, free + 12.0 * cols);
+        const int64_t tiles = rows[i] * ceil_div(q[i].N, w[i]);
+        ns += static_cast<double>(tiles) / mc.pairs * full;
+        total += tiles;
+      }
+      const double tail = 12.0 * (gated ? 2 * w[kinds - 1] : w[kinds - 1]);  // the last tile's epilogue
+      // the last round, only partly filled, takes a whole tile's time at the clock that it has
+      const double part = static_cast<double>(total % mc.pairs) / mc.pairs;
+      if (total <= mc.pairs)
+        ns = longest;
+      else
+        ns = std::max(longest, ns + tail + (part > 0 ? std::max(0.0, free - part * full) : 0.0));
+      if (!best[0] || ns < 0.99 * best_ns) best[0] = w[0], best[1] = w[1], best_ns = ns;
+    }
+  for (int i = 0; i < count; ++i) widths[i] = best[i == 0 ? 0 : 1];
   if (us) *us = 4.0 + best_ns * 1e-3;
-  return best;
 }
 
 namespace {
@@ -617,7 +635,8 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
   Args p;
   std::memset(&p, 0, sizeof(p));
   p.count = count;
-  const int w = plan_width(mc, q, count, fp8, e.kind == EPI_GATED, nullptr);
+  int widths[3];
+  plan_width(mc, q, count, fp8, e.kind == EPI_GATED, widths, nullptr);
   int stage = 0;
   for (int i = 0; i < count; ++i)
     if (e.kind == EPI_PLAIN && ceil_div(q[i].K, KB / 2) * q[i].terms <= WIDE_KB) p.wide = 1;
@@ -626,7 +645,7 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
     const Product& c = q[i];
     Prob& o = p.q[i];
     o.M = static_cast<int>(c.M), o.N = static_cast<int>(c.N);
-    o.w = w;
+    o.w = widths[i];
     const int hb = e.kind == EPI_GATED ? o.w : o.w / 2;
     stage = std::max(stage, A_BYTES + b_bytes(o.w, e.kind == EPI_GATED, c.b[0].mn_major));
     o.tiles_m = ceil_div(c.M, 2 * TM);

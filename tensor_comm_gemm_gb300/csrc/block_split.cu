@@ -37,7 +37,8 @@ struct Args {
   int tiles_f;          // feature tiles
   int nt;               // tokens of a tile (16 .. 256, a multiple of 16)
   int kb_seg, kb;       // K blocks per term and in all
-  int a_mn;
+  int a_mn, b_mn;
+  int b_bytes;          // a stage's tokens: nt rows of a K block, or blocks of 64 tokens by 64 rows
   int stages, tmem_cols;
   int act;
   const __nv_bfloat16 *bias, *residual;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
   constexpr int KEL = FP8 ? KB : KB / 2;
   constexpr int FEATURES = KIND == EPI_GATED ? FT / 2 : FT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t stage_bytes = A_BYTES + static_cast<uint32_t>(p.nt) * KB;
+  const uint32_t stage_bytes = A_BYTES + static_cast<uint32_t>(p.b_bytes);
   const uint32_t full0 = sbase + stage_bytes * p.stages, empty0 = full0 + 8 * MAX_STAGES,
                  tfull = empty0 + 8 * MAX_STAGES, slot = tfull + 16;
   const int S = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
@@ -167,6 +168,18 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
         const Box x[3] = {{sa, ma, kx, f0}, {sa + A_BYTES / 2, ma + kMap, kx, f0}, {sa + A_BYTES, mb, kx, t0}};
         stage_loads<1>(1u, fb, stage_bytes, fb, x);
       });
+    else if (p.b_mn && p.nt > 64)
+      run([&](uint32_t fb, uint32_t sa, int seg, int kx) {
+        const Box x[4] = {{sa, ma + seg * kMap, f0, kx}, {sa + A_BYTES / 2, ma + seg * kMap, f0 + 64, kx},
+                          {sa + A_BYTES, mb + seg * kMap, t0, kx}, {sa + A_BYTES + 8192u, mb + seg * kMap, t0 + 64, kx}};
+        stage_loads<1>(1u, fb, stage_bytes, fb, x);
+      });
+    else if (p.b_mn)
+      run([&](uint32_t fb, uint32_t sa, int seg, int kx) {
+        const Box x[3] = {{sa, ma + seg * kMap, f0, kx}, {sa + A_BYTES / 2, ma + seg * kMap, f0 + 64, kx},
+                          {sa + A_BYTES, mb + seg * kMap, t0, kx}};
+        stage_loads<1>(1u, fb, stage_bytes, fb, x);
+      });
     else if (p.a_mn)
       run([&](uint32_t fb, uint32_t sa, int seg, int kx) {
         const Box x[3] = {{sa, ma + seg * kMap, f0, kx}, {sa + A_BYTES / 2, ma + seg * kMap, f0 + 64, kx},
@@ -183,10 +196,10 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
         wait_bar(p.err, full0 + 8u * (j % stages), (j / stages) & 1u, S_DRAIN, false);
     __syncwarp();
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_n(make_idesc(FP8, FT), p.nt) | (p.a_mn ? 1u << 15 : 0u);
+    const uint32_t idesc = idesc_n(make_idesc(FP8, FT), p.nt) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u);
     const uint64_t da0 = p.a_mn ? desc_mn(sbase) : smem_desc_sw128(sbase);
-    const uint64_t db0 = smem_desc_sw128(sbase + A_BYTES);
-    const uint64_t step_a = p.a_mn ? 128u : 2u;
+    const uint64_t db0 = p.b_mn ? desc_mn(sbase + A_BYTES) : smem_desc_sw128(sbase + A_BYTES);
+    const uint64_t step_a = p.a_mn ? 128u : 2u, step_b = p.b_mn ? 128u : 2u;
     uint32_t stage = 0, phase = 0;
     for (int i = lo; i < hi; ++i) {
       if (!wait_bar_warp(p.err, full0 + 8u * stage, phase, S_FULL)) {
@@ -195,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
       }
       tc_fence_after();
       const uint64_t off = static_cast<uint64_t>(stage_bytes >> 4) * stage;
-      mma_kblock<1, FP8>(tmem, da0 + off, db0 + off, idesc, i > lo ? 1u : 0u, step_a);
+      mma_kblock<1, FP8>(tmem, da0 + off, db0 + off, idesc, i > lo ? 1u : 0u, step_a, step_b);
       mma_commit_cg<1>(empty0 + 8u * stage);
       if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
     }
@@ -328,43 +341,59 @@ cudaError_t configure_split(Machine* m) {
   return cudaSuccess;
 }
 
+// Bytes of a stage's tokens.
+static int token_bytes(int nt, bool b_mn) { return b_mn ? (nt + 63) / 64 * 8192 : nt * KB; }
+
 // Tokens of a tile, stages and the cluster size: the largest with which all
 // tiles are resident at once (a second round of clusters costs more than
 // longer slices) and a CTA still has four K blocks (below that the cluster's
-// additions cost more than the slices save).
-static SplitPlan plan_split(const Machine& mc, const Product& q, bool fp8, bool gated, double* us) {
-  SplitPlan o;
+// additions cost more than the slices save).  False if not all tiles are.
+static bool plan_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t split, SplitPlan* plan,
+                       double* us) {
+  SplitPlan& o = *plan;
+  const bool b_mn = q.a[0].mn_major;
   const int kb = ceil_div(q.K, fp8 ? KB : KB / 2) * q.terms;
-  const int tiles_t = ceil_div(q.M, 256);
+  const int tiles_t = ceil_div(q.M, b_mn ? 128 : 256);
   o.nt = ceil_div(ceil_div(q.M, tiles_t), 16) * 16;
   const int64_t tiles = static_cast<int64_t>(tiles_t) * ceil_div(q.N, gated ? FT / 2 : FT);
-  const int stage = A_BYTES + o.nt * KB;
+  const int stage = A_BYTES + token_bytes(o.nt, b_mn);
   // two CTAs per SM while they hold at least three stages each
   const int per_sm = (SMEM_TWO - SMEM_TAIL) / stage >= 3 ? 2 : 1;
   o.stages = std::min(MAX_STAGES, ((per_sm == 2 ? SMEM_TWO : SMEM_ONE) - SMEM_TAIL) / stage);
   o.split = 1;
   for (int s = 2; s <= MAX_SPLIT && s * 4 <= kb; ++s)
     if (tiles <= mc.clusters[per_sm - 1][s]) o.split = s;
-  // measured at one CTA per SM: 8.0 us and 0.32 us a K block with 192 tokens, 9.1 and 0.39 with 256
+  if (split > 0) o.split = static_cast<int>(std::min<int64_t>(split, kb));
+  // measured: 9.6 us and 0.31 us a K block with 128 tokens, two CTAs per SM; one per SM, 8.0 and 0.32 with 192, 9.1
+  // and 0.39 with 256
   const int64_t places = std::max(1, mc.clusters[per_sm - 1][o.split]);
-  *us = 4.5 + 0.018 * o.nt +
-        static_cast<double>((tiles + places - 1) / places) * ((kb + o.split - 1) / o.split) * (0.13 + 0.001 * o.nt);
-  return o;
+  const int64_t blocks = (tiles + places - 1) / places * ((kb + o.split - 1) / o.split);
+  *us = per_sm == 2 ? 6.0 + 0.028 * o.nt + static_cast<double>(blocks) * (0.2 + 0.0009 * o.nt)
+                    : 4.5 + 0.018 * o.nt + static_cast<double>(blocks) * (0.13 + 0.001 * o.nt);
+  return tiles <= places;
 }
 
 // By rule: up to 128 tokens always (at 96 and 128 tokens it is level with the
-// pairs on 14336x4096 and 1024x1024, and ahead on 4096x4096, 13.5 to 17.2 us,
-// and 3584x8192, 17.3 to 27), up to 256 where the models say so, never above
-// (512 tokens, 4096x4096: 21.8 us, 18.2 on pairs).
+// pairs on 14336x4096 and 1024x1024, and ahead on 4096x4096, 13.6 to 17 us,
+// and 3584x8192, 17.3 to 27), otherwise where all tiles are resident and the
+// models say so (512 tokens, 1000x5000: 15 us, 29 on pairs; 4096x4096: 21.8 us,
+// 18.2 on pairs).  A weight's gradient has the weight's rows for tokens and the
+// tokens for its contraction: few tiles of a small weight, long ones of a long batch.
 bool use_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t path, int64_t split,
                SplitPlan* plan) {
-  if (path == 1 || (path == 0 && q.M > 256)) return false;
+  if (path == 1) return false;
   double split_us = 0, pairs_us = 0;
-  *plan = plan_split(mc, q, fp8, gated, &split_us);
-  if (split > 0) plan->split = static_cast<int>(std::min<int64_t>(split, ceil_div(q.K, fp8 ? KB : KB / 2) * q.terms));
+  const bool fits = plan_split(mc, q, fp8, gated, split, plan, &split_us);
   if (path == 2 || q.M <= 128) return true;
-  plan_width(mc, &q, 1, fp8, gated, &pairs_us);
+  if (!fits) return false;
+  int width;
+  plan_width(mc, &q, 1, fp8, gated, &width, &pairs_us);
   return split_us < pairs_us;
+}
+
+bool split_cost(const Machine& mc, const Product& q, int64_t path, int64_t split, SplitPlan* plan, double* us) {
+  const bool fits = plan_split(mc, q, false, false, split, plan, us);
+  return path == 2 || (path == 0 && fits);
 }
 
 cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, const Epi& e, uint32_t* err,
@@ -379,6 +408,8 @@ cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, cons
   p.kb_seg = ceil_div(c.K, fp8 ? KB : KB / 2);
   p.kb = p.kb_seg * c.terms;
   p.a_mn = c.b[0].mn_major;
+  p.b_mn = c.a[0].mn_major;
+  p.b_bytes = token_bytes(plan.nt, p.b_mn);
   p.stages = plan.stages;
   p.tmem_cols = 32;
   while (p.tmem_cols < p.nt) p.tmem_cols *= 2;
@@ -398,7 +429,7 @@ cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, cons
   p.sx = e.sx, p.sw0 = e.sw0, p.sw1 = e.sw1;
   p.err = err;
   const int tiles = p.tiles_f * ceil_div(c.M, p.nt);
-  const int smem = p.stages * (A_BYTES + p.nt * KB) + SMEM_TAIL;
+  const int smem = p.stages * (A_BYTES + p.b_bytes) + SMEM_TAIL;
   switch (e.kind) {
     case EPI_LINEAR: return fp8 ? launch_split_as<EPI_LINEAR, true>(p, tiles, plan.split, smem, s)
                                 : launch_split_as<EPI_LINEAR, false>(p, tiles, plan.split, smem, s);
