@@ -570,7 +570,7 @@ void plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool g
         ns = longest;
       else
         ns = std::max(longest, ns + tail + (part > 0 ? std::max(0.0, free - part * full) : 0.0));
-      if (!best[0] || ns < 0.99 * best_ns) best[0] = w[0], best[1] = w[1], best_ns = ns;
+      if (!best[0] || ns < 0.97 * best_ns) best[0] = w[0], best[1] = w[1], best_ns = ns;
     }
   for (int i = 0; i < count; ++i) widths[i] = best[i == 0 ? 0 : 1];
   if (us) *us = 4.0 + best_ns * 1e-3;
