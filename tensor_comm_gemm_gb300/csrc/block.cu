@@ -328,7 +328,6 @@ tpo_status tpo_layer_norm(tpo_block* b, int64_t n, int64_t k, int dtype, int wdt
   if (tpo_status st = check_block(b, 0)) return st;
   if (n == 0) return TPO_OK;
   tpo::NormArgs a{};
-  a.err = b->err();
   a.n = n, a.k = k, a.x = x, a.ldx = ldx, a.gamma = gamma, a.beta = beta, a.eps = eps;
   a.y = y, a.ldy = ldy, a.mean = mean, a.rstd = rstd;
   return launched(tpo::launch_norm(b->machine, a, dtype, wdtype, static_cast<cudaStream_t>(stream)));
@@ -357,7 +356,6 @@ tpo_status tpo_layer_norm_bwd(tpo_block* b, int64_t n, int64_t k, int dtype, int
   if (tpo_status st = check_vec("rstd", rstd, 4)) return st;
   if (tpo_status st = check_block(b, dgamma || dbeta ? need_norm_bwd(n, k) : 0)) return st;
   tpo::NormArgs a{};
-  a.err = b->err();
   a.n = n, a.k = k, a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.gamma = gamma, a.dres = dres;
   a.lddres = lddres, a.y = n > 0 ? dx : nullptr, a.ldy = lddx, a.dgamma = dgamma, a.dbeta = dbeta;
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);

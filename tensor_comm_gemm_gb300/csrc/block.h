@@ -52,10 +52,10 @@ struct Machine {
 // Also set the kernels' attributes.
 cudaError_t configure_products(Machine* m);
 // The column tiles' width of each product of a launch (all after the first are
-// of one shape), and the launch's modelled time.  Narrower tiles than the widest cost more per column, so they
-// are taken where they fill a last round or spread few tiles over the pairs
-// (4096^3: 224 columns 84.8 us, 256 86.7, 192 88.2; 1777x4096x2*14336: 256
-// columns 246 us, 192 253).
+// of one shape), and the launch's modelled time.  Narrower tiles than the
+// widest cost more per column, so they are taken where they fill a last round
+// or spread few tiles over the pairs (4096^3: 224 columns 84.8 us, 256 86.7, 192
+// 88.2; 1777x4096x2*14336: 256 columns 246 us, 192 253).
 void plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, int* widths, double* us);
 // Runs `count` (1 to 3) products in one launch; more than one take EPI_PLAIN.
 cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, uint32_t* err,
@@ -83,7 +83,6 @@ struct NormArgs {
   float *mean, *rstd;              // forward: written; backward: read
   void *dgamma, *dbeta;
   float eps;
-  uint32_t* err;                   // the handle's error word
 };
 
 // out0 and out1 (of TPO_BF16 or TPO_F32, NULL: not wanted) from per-block sums part[parts][vectors][cols].
@@ -101,7 +100,7 @@ cudaError_t launch_gated_act_bwd(int64_t n, int64_t m, int act, const void* dh, 
                                  cudaStream_t s);
 cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdtype, cudaStream_t s);
 // part: workspace of min(n, NORM_PARTS) x 2 x k floats, the blocks' sums for dgamma and dbeta.
-constexpr int NORM_PARTS = 304;
+constexpr int NORM_PARTS = 152;
 cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int wdtype, float* part, cudaStream_t s);
 
 void set_last_error(const char* msg);  // ctx.cu: the message tpo_last_error returns

@@ -10,7 +10,7 @@ namespace tpo {
 constexpr int KB = 128;  // bytes of contraction elements per K block
 constexpr unsigned long long WAIT_NS = 2000000000ull;  // bound of every wait
 
-enum Site : uint32_t { S_EMPTY = 1, S_FULL = 2, S_TEMPTY = 3, S_TFULL = 4, S_DRAIN = 5, S_ROW = 6 };
+enum Site : uint32_t { S_EMPTY = 1, S_FULL = 2, S_TEMPTY = 3, S_TFULL = 4, S_DRAIN = 5 };
 
 __device__ inline void give_up(uint32_t* err, uint32_t site) {
   if (atomicCAS(err, 0u, 1u) == 0u) {

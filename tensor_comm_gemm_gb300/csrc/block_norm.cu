@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   extern __shared__ __align__(16) uint8_t smem[];  // gamma, the rows in flight, slack to read past them
   __shared__ float2 red[2][RING_THREADS / 32];
   constexpr int L = VEC > 1 ? 2 : 1, NN = VEC / L;
-  constexpr bool KEEP = NV * VEC <= 16;  // xhat and dy gamma stay in registers from the sums to dx
+  constexpr bool KEEP = NV * VEC <= 20;  // xhat and dy gamma stay in registers from the sums to dx
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = RING_THREADS / tpr;
@@ -758,16 +758,6 @@ Share share(int64_t vecs, int nv, int most_nv, int most_tpr, int least_tpr = 1) 
   return s;
 }
 
-// Single elements: 8, 12 or 16 a thread, whichever leaves the fewest threads idle.
-Share share_single(int64_t k) {
-  Share best{0, 0};
-  for (int nv : {16, 12, 8}) {
-    const Share s = share(k, nv, nv, 512, 32);
-    if (s.tpr && (!best.tpr || s.tpr * s.nv < best.tpr * best.nv)) best = s;
-  }
-  return best;
-}
-
 // Rows in flight per group and the shared memory of a block that also keeps
 // `fixed` bytes of weights; depth < 2: they do not fit.
 constexpr size_t RING_SMEM = 226 * 1024;
@@ -786,6 +776,21 @@ Ring ring_of(bool vec, const Share& h, int arrays, int64_t k, int elem, size_t f
   r.depth = static_cast<int>(std::min<size_t>(4, (RING_SMEM - rest) / slot));
   r.smem = rest + slot * r.depth;
   return r;
+}
+
+// Single elements: 8 to 20 a thread, whichever leaves the fewest idle while at
+// least two rows fit (three and more count for a sixth).
+Share share_single(int64_t k, int arrays, int elem, int welem, int weights) {
+  Share best{0, 0};
+  int64_t best_cost = 0;
+  for (int nv : {20, 16, 12, 8}) {
+    const Share s = share(k, nv, nv, RING_THREADS, 32);
+    if (!s.tpr) continue;
+    const int depth = ring_of(false, s, arrays, k, elem, weights * weight_bytes(s.tpr * nv, welem)).depth;
+    const int64_t cost = static_cast<int64_t>(s.tpr) * nv * (depth >= 3 ? 6 : 7);
+    if (depth >= 2 && (!best.tpr || cost < best_cost)) best = s, best_cost = cost;
+  }
+  return best;
 }
 
 template <class K>
@@ -808,7 +813,7 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
     // many threads as it has vectors (latency).  8192 rows of 8192, four
     // vectors a thread: 49 us; two blocks per SM, with 64 registers a thread:
     // 57, and then 70 with two vectors and 98 with eight.
-    const Share m = vec ? share(vecs, 4, 4, RING_THREADS, 32) : share_single(a.k);
+    const Share m = vec ? share(vecs, 4, 4, RING_THREADS, 32) : share_single(a.k, 1, sizeof(T), sizeof(W), 2);
     const int64_t sets = m.tpr ? (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr) : 0;
     // (rows of up to 64 vectors would leave half of a group's threads idle)
     if (sets >= (vec ? 2 : 1) * static_cast<int64_t>(mc.sms) && (!vec || vecs > 64)) {
@@ -823,7 +828,8 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
           return static_cast<int64_t>(m.tpr) * 4 == vecs ? run(norm_ring_kernel<T, W, V, 4, true>)
                                                          : run(norm_ring_kernel<T, W, V, 4, false>);
         if (m.nv == 8) return run(norm_ring_kernel<T, W, 1, 8, false>);
-        return m.nv == 12 ? run(norm_ring_kernel<T, W, 1, 12, false>) : run(norm_ring_kernel<T, W, 1, 16, false>);
+        if (m.nv == 12) return run(norm_ring_kernel<T, W, 1, 12, false>);
+        return m.nv == 16 ? run(norm_ring_kernel<T, W, 1, 16, false>) : run(norm_ring_kernel<T, W, 1, 20, false>);
       }
     }
     const Share h = share(vecs, 1, 8, 512);
@@ -853,7 +859,8 @@ cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int
     cudaError_t e = cudaSuccess;
     // 16 elements a thread (rows up to 8192), else 32 of whole vectors
     constexpr int NV = 16 / V;
-    const Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS, 32) : share_single(a.k);
+    const Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS, 32)
+                        : share_single(a.k, a.dres && a.y ? 3 : 2, sizeof(T), sizeof(W), 1);
     const size_t kept = vec && h.nv == NV && sizeof(W) == 2 ? 0 : weight_bytes(h.tpr * h.nv * (vec ? V : 1), sizeof(W));
     const Ring r = ring_of(vec, h, a.dres && a.y ? 3 : 2, a.k, sizeof(T), kept);
     if (r.depth >= 2 && a.n > 0) {
@@ -871,8 +878,10 @@ cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int
         e = run(norm_bwd_ring_kernel<T, W, 1, 8>);
       else if (h.nv == 12)
         e = run(norm_bwd_ring_kernel<T, W, 1, 12>);
-      else
+      else if (h.nv == 16)
         e = run(norm_bwd_ring_kernel<T, W, 1, 16>);
+      else
+        e = run(norm_bwd_ring_kernel<T, W, 1, 20>);
     } else if (a.n > 0) {
       // the weights' gradients first: dx may overwrite dy
       parts = static_cast<int>(std::min<int64_t>(a.n, 32));

@@ -131,6 +131,36 @@ def test_linear(any_path, block, n, k, m, dtype):
         R.check("z", z.get(), want["z"])
 
 
+LARGE = [(1500, 1200, 3000), (4100, 520, 2104), (300, 4104, 1000), (2504, 264, 5000), (6000, 256, 264),
+         (150, 264, 9000), (1030, 2056, 392)]
+
+
+@pytest.mark.parametrize("n,k,m", LARGE)
+def test_many_tiles(block, n, k, m):
+    """Several rounds of tiles, long and short contractions, as the rule runs them."""
+    g = gen_of(700 + LARGE.index((n, k, m)))
+    x, w, w2 = rnd(g, n, k), rnd(g, m, k, scale=k ** -0.5), rnd(g, m, k, scale=k ** -0.5)
+    bias, res, dy, z, u = rnd(g, m), rnd(g, n, m), rnd(g, n, m), rnd(g, n, m), rnd(g, n, m)
+    y, zo, h = Out(n, m), Out(n, m), Out(n, m)
+    dx, dw, gx, gg, gu = Out(n, k), Out(m, k), Out(n, k), Out(m, k), Out(m, k)
+    db = torch.empty_like(bias)
+    t.tpo_linear(block, x, w, y.t, bias=bias, act=ACT["gelu_tanh"], residual=res, z=zo.t)
+    t.tpo_gated(block, x, w, w2, h.t, act=ACT["silu"])
+    t.tpo_linear_bwd(block, dy, x, w, dx=dx.t, dw=dw.t, db=db, act=ACT["gelu"], z=z)
+    t.tpo_gated_bwd(block, dy, z, u, x, w, w2, dx=gx.t, dwg=gg.t, dwu=gu.t)
+    synced(block)
+    want = R.linear(d(x), d(w), d(bias), "gelu_tanh", d(res))
+    R.check("y", y.get(), want["y"])
+    R.check("z", zo.get(), want["z"])
+    R.check("h", h.get(), R.gated(d(x), d(w), d(w2), "silu")["h"])
+    want = R.linear_bwd(d(dy), d(x), d(w), d(z), "gelu")
+    for name, o in (("dx", dx.get()), ("dw", dw.get()), ("db", db)):
+        R.check(name, o, want[name])
+    want = R.gated_bwd(d(dy), d(z), d(u), d(x), d(w), d(w2))
+    for name, o in (("dx", gx), ("dwg", gg), ("dwu", gu)):
+        R.check(name, o.get(), want[name])
+
+
 @pytest.mark.parametrize("act", R.ACTS)
 @pytest.mark.parametrize("n", [1, 70, 600])
 def test_linear_every_epilogue(any_path, block, act, n):
@@ -340,7 +370,7 @@ def test_gradients_against_differences(block, act):
 
 NORMS = [(1, 1), (2, 2), (3, 7), (1, 64), (5, 100), (4, 255), (7, 256), (129, 1000), (3, 1024), (33, 1029), (2, 2048),
          (160, 4096), (6, 5003), (3, 8192), (5, 8200), (2, 16384), (3, 20001), (2, 40000), (2000, 8), (1500, 72),
-         (4200, 520)]
+         (4200, 520), (4000, 1003), (1000, 5003), (900, 7001), (700, 8192), (3000, 2048), (500, 12288), (9000, 136)]
 
 
 @pytest.mark.parametrize("n,k", NORMS)
@@ -531,6 +561,14 @@ def test_repeats_streams_and_graphs_give_the_same_bits(any_path, block, n, k, m)
     torch.cuda.synchronize()
     synced(block)
     assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_options_round_trip(block):
+    for key, value in (("path", 2), ("path", 0), ("split", 8), ("split", 0)):
+        t.tpo_block_set_opt(block, key, value)
+        assert t.tpo_block_get_opt(block, key) == value
+    with pytest.raises(t.TpoError, match="path"):
+        t.tpo_block_set_opt(block, "path", 3)
 
 
 def test_workspace_and_device_checks():
