@@ -60,45 +60,61 @@ __device__ __forceinline__ float lanes_sum(float a, int lanes) {
 }
 // Barrier of the `tpr` threads of a row.  (A kernel with it holds all 16 of a
 // block's barriers, so at most four such blocks run on an SM.)
-__device__ __forceinline__ void group_barrier(int tpr) {
+__device__ __forceinline__ void group_barrier(int group, int tpr) {
   if (tpr > 32)
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / tpr), "r"(tpr) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
   else
     __syncwarp();
 }
-// ALONE: the rows' groups keep their own pace; otherwise the block's rows go together.
-template <bool ALONE>
+// The block's rows go together.
 __device__ __forceinline__ float row_sum(float a, int tpr, float* red) {
   a = lanes_sum(a, tpr);
   if (tpr > 32) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5;
     if (lane == 0) red[warp] = a;
-    if constexpr (ALONE)
-      group_barrier(tpr);
-    else
-      __syncthreads();
+    __syncthreads();
     a = lanes_sum(red[(warp & ~(per - 1)) + (lane & (per - 1))], per);
   }
   return a;
 }
-__device__ __forceinline__ void lanes_sums(float& a, float& b, int lanes) {  // both chains at once
-#pragma unroll
-  for (int d = 16; d; d >>= 1)
-    if (d < lanes) {
-      a += __shfl_xor_sync(0xffffffffu, a, d);
-      b += __shfl_xor_sync(0xffffffffu, b, d);
-    }
+// The same where a row has whole warps, up to 16 of them, that keep their own
+// pace; of two values at once.  (No step depends on tpr: lanes past the row's
+// last warp add zeros.)  They also are a barrier of the row's threads.
+__device__ __forceinline__ float group_sum(float a, int group, int tpr, float* red) {
+  a = lanes_sum(a, 32);
+  if (tpr > 32) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5;
+    if (lane == 0) red[warp] = a;
+    group_barrier(group, tpr);
+    const int w = lane & 15;
+    a = w < per ? red[(warp & ~(per - 1)) + w] : 0.0f;
+    a = lanes_sum(a, 16);
+  } else {
+    __syncwarp();
+  }
+  return a;
 }
-__device__ __forceinline__ float2 row_sums(float a, float b, int tpr, float2* red) {
-  lanes_sums(a, b, tpr);
+template <int LANES>
+__device__ __forceinline__ void lanes_sums(float& a, float& b) {  // both chains at once
+#pragma unroll
+  for (int d = LANES / 2; d; d >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, d);
+    b += __shfl_xor_sync(0xffffffffu, b, d);
+  }
+}
+__device__ __forceinline__ float2 group_sums(float a, float b, int group, int tpr, float2* red) {
+  lanes_sums<32>(a, b);
   if (tpr > 32) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = tpr >> 5;
     if (lane == 0) red[warp] = make_float2(a, b);
-    group_barrier(tpr);
-    const float2 v = red[(warp & ~(per - 1)) + (lane & (per - 1))];
+    group_barrier(group, tpr);
+    const int w = lane & 15;
+    const float2 v = w < per ? red[(warp & ~(per - 1)) + w] : make_float2(0.0f, 0.0f);
     a = v.x;
     b = v.y;
-    lanes_sums(a, b, per);
+    lanes_sums<16>(a, b);
+  } else {
+    __syncwarp();
   }
   return make_float2(a, b);
 }
@@ -125,7 +141,7 @@ __global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int tpr) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) s += to_f(v[i].e[j]);
   const float inv_k = 1.0f / static_cast<float>(a.k);
-  const float mean = row_sum<false>(s, tpr, red[0]) * inv_k;
+  const float mean = row_sum(s, tpr, red[0]) * inv_k;
   s = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -135,7 +151,7 @@ __global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int tpr) {
         const float d = to_f(v[i].e[j]) - mean;
         s += d * d;
       }
-  const float rstd = rsqrtf(row_sum<false>(s, tpr, red[1]) * inv_k + a.eps);
+  const float rstd = rsqrtf(row_sum(s, tpr, red[1]) * inv_k + a.eps);
   if (!live) return;
   const W *gamma = static_cast<const W*>(a.gamma), *beta = static_cast<const W*>(a.beta);
   T* y = static_cast<T*>(a.y) + row * a.ldy;
@@ -160,16 +176,9 @@ __global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int tpr) {
 
 // ------------------------------------------------------------------ many rows
 
-// One value (L = 1) or two at a time (L = 2: the packed fp32 operations, which
-// halve the instructions that otherwise bound these kernels).
-template <int L>
-struct Num;
-template <>
-struct Num<1> {
-  float v;
-};
-template <>
-struct Num<2> {
+// Two values at a time (the packed fp32 operations, which halve the
+// instructions that otherwise bound these kernels).
+struct Num {
   uint64_t v;
 };
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -180,57 +189,63 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
 __device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
-template <int L>
-__device__ __forceinline__ Num<L> all(float x) {
-  if constexpr (L == 1) return {x};
-  else return {pack2(x, x)};
-}
-__device__ __forceinline__ Num<1> add(Num<1> a, Num<1> b) { return {a.v + b.v}; }
-__device__ __forceinline__ Num<1> mul(Num<1> a, Num<1> b) { return {a.v * b.v}; }
-__device__ __forceinline__ Num<1> fma(Num<1> a, Num<1> b, Num<1> c) { return {fmaf(a.v, b.v, c.v)}; }
-__device__ __forceinline__ Num<2> add(Num<2> a, Num<2> b) {
+__device__ __forceinline__ Num num(float a, float b) { return {pack2(a, b)}; }
+__device__ __forceinline__ Num all(float x) { return num(x, x); }
+__device__ __forceinline__ Num add(Num a, Num b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
   return {r};
 }
-__device__ __forceinline__ Num<2> mul(Num<2> a, Num<2> b) {
+__device__ __forceinline__ Num mul(Num a, Num b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
   return {r};
 }
-__device__ __forceinline__ Num<2> fma(Num<2> a, Num<2> b, Num<2> c) {
+__device__ __forceinline__ Num fma(Num a, Num b, Num c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
   return {r};
 }
-__device__ __forceinline__ float total(Num<1> a) { return a.v; }
-__device__ __forceinline__ float total(Num<2> a) {
+__device__ __forceinline__ float total(Num a) {
   float x, y;
   unpack2(a.v, x, y);
   return x + y;
 }
 
-// A vector's elements as fp32, and back (rounded).
-template <class T, int VEC, int L>
-__device__ __forceinline__ void to_nums(const Vec<T, VEC>& v, Num<L> (&o)[VEC / L]) {
-  if constexpr (L == 1) {
-    o[0].v = to_f(v.e[0]);
-  } else if constexpr (sizeof(T) == 4) {
+// A step of a thread's share of a row: a vector of VEC > 1 elements, or two
+// single ones 32 apart.  Its values as fp32, and back (rounded).
+constexpr int STRIDE1 = 32;
+template <int VEC>
+constexpr int NUMS = VEC > 1 ? VEC / 2 : 1;
+template <class T, int VEC>
+__device__ __forceinline__ void to_nums(const Vec<T, VEC>& v, Num (&o)[NUMS<VEC>]) {
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int j = 0; j < VEC / 2; ++j) o[j].v = pack2(v.e[2 * j], v.e[2 * j + 1]);
+    for (int j = 0; j < VEC / 2; ++j) o[j] = num(v.e[2 * j], v.e[2 * j + 1]);
   } else {
     uint32_t w[VEC / 2];
     memcpy(w, &v, sizeof(w));
 #pragma unroll
-    for (int j = 0; j < VEC / 2; ++j) o[j].v = pack2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+    for (int j = 0; j < VEC / 2; ++j) o[j] = num(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
   }
 }
-template <class T, int VEC, int L>
-__device__ __forceinline__ Vec<T, VEC> from_nums(const Num<L> (&a)[VEC / L]) {
-  Vec<T, VEC> v;
-  if constexpr (L == 1) {
-    put(&v.e[0], a[0].v);
-  } else {
+template <class T, int VEC>
+__device__ __forceinline__ void read_nums(const T* p, Num (&o)[NUMS<VEC>]) {
+  if constexpr (VEC > 1)
+    to_nums<T, VEC>(load<T, VEC>(p), o);
+  else
+    o[0] = num(to_f(p[0]), to_f(p[STRIDE1]));
+}
+// left: how many of the row's elements there are from p on (VEC = 1: of which the step has the first and the 33rd).
+template <class T, int VEC>
+__device__ __forceinline__ void write_nums(T* p, const Num (&a)[NUMS<VEC>], int left) {
+  if constexpr (VEC == 1) {
+    float x, y;
+    unpack2(a[0].v, x, y);
+    if (left > 0) put(p, x);
+    if (left > STRIDE1) put(p + STRIDE1, y);
+  } else if (left > 0) {
+    Vec<T, VEC> v;
     uint32_t w[VEC / 2];
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) {
@@ -245,8 +260,21 @@ __device__ __forceinline__ Vec<T, VEC> from_nums(const Num<L> (&a)[VEC / L]) {
       }
     }
     if constexpr (sizeof(T) == 2) memcpy(&v, w, sizeof(w));
+    *reinterpret_cast<Vec<T, VEC>*>(p) = v;
   }
-  return v;
+}
+// The values of a step that exist; zeros for the others.
+template <int VEC>
+__device__ __forceinline__ void mask_nums(Num (&a)[NUMS<VEC>], int left) {
+  if constexpr (VEC == 1) {
+    float x, y;
+    unpack2(a[0].v, x, y);
+    a[0] = num(left > 0 ? x : 0.0f, left > STRIDE1 ? y : 0.0f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NUMS<VEC>; ++j)
+      if (left <= 0) a[j] = all(0.0f);
+  }
 }
 
 // Asynchronous copy of 16 bytes to shared memory; zeros (and no access to src) if they do not exist.
@@ -268,60 +296,83 @@ __device__ __forceinline__ void copy_wait(int ahead) {
 // Rows in flight.  With VEC > 1 (16-byte rows) a thread copies the vectors that
 // it will read itself, so it needs no barrier before them.  With VEC = 1 the
 // group copies the aligned 16-byte units that hold the row, to the same offset
-// modulo 16, and reads single elements after a barrier.  Units at a row's ends
+// modulo 16, and reads single elements after a barrier; the slot is free after
+// the next one (that of the row's sum).  Units at a row's ends
 // bring a few bytes of what lies beside it, which nobody reads; where that
-// would be outside the matrix (before row 0, behind the last row) only the
-// row's own bytes are touched.
+// might be outside the matrix (`edge`: the first and the last edge_rows(k)
+// rows) only the row's own bytes are touched.
+__device__ __forceinline__ int64_t edge_rows(int k) { return k >= 16 ? 1 : 16; }
 __host__ __device__ inline uint32_t weight_bytes(int k, int elem) {
   return (static_cast<uint32_t>(k) * elem + 15u) & ~15u;
 }
 __host__ __device__ inline uint32_t row_bytes(int k, int elem) {
   return ((static_cast<uint32_t>(k) * elem + 15u) & ~15u) + 16u;
 }
-template <class T>
-__device__ __forceinline__ void copy_units(const T* src, int k, uint32_t dst, int lane, int tpr, bool first, bool last) {
-  const uint64_t p = reinterpret_cast<uint64_t>(src), lo = p & ~15ull, end = p + static_cast<uint64_t>(k) * sizeof(T);
-  const int units = static_cast<int>((end - lo + 15) >> 4);
-  for (int u = lane; u < units; u += tpr) {
-    const uint64_t at = lo + 16ull * u;
-    if (first && at < p) {  // the row's own elements of its first unit
-      const int own = min(k, static_cast<int>((at + 16 - p) / sizeof(T)));
+// A thread takes at most MOST of the units.
+template <class T, int MOST>
+__device__ __forceinline__ void copy_units(const T* src, int k, uint32_t dst, int lane, int tpr, bool edge) {
+  const uint64_t p = reinterpret_cast<uint64_t>(src), lo = p & ~15ull;
+  const int skip = static_cast<int>(p & 15), bytes = skip + k * static_cast<int>(sizeof(T));  // up to the row's end
+  if (!edge) {
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      const int u = 16 * (lane + i * tpr);
+      if (u < bytes)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + u), "l"(lo + u) : "memory");
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int u = 16 * lane; u < bytes; u += 16 * tpr) {
+    if (u < skip) {  // the row's own elements of its first unit
+      const int own = min(k, (16 - skip) / static_cast<int>(sizeof(T)));
       for (int c = 0; c < own; ++c) {
-        const uint32_t to = dst + static_cast<uint32_t>(p & 15) + c * static_cast<uint32_t>(sizeof(T));
+        const uint32_t to = dst + skip + c * static_cast<uint32_t>(sizeof(T));
         if constexpr (sizeof(T) == 4)
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(src[c]) : "memory");
         else
           asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(__bfloat16_as_ushort(src[c])) : "memory");
       }
     } else {
-      const int bytes = last && at + 16 > end ? static_cast<int>(end - at) : 16;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16u * u), "l"(at), "r"(bytes) : "memory");
+      const int own = min(16, bytes - u);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + u), "l"(lo + u), "r"(own) : "memory");
     }
   }
 }
-// Where element 0 of such a row is.
+// Where element 0 of row r of such a matrix is.
 template <class T>
-__device__ __forceinline__ const T* unit_row(const T* src, const uint8_t* slot) {
-  return reinterpret_cast<const T*>(slot + (reinterpret_cast<uint64_t>(src) & 15));
+__device__ __forceinline__ const T* unit_row(const void* p, int64_t r, int64_t ld, const uint8_t* slot) {
+  const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uint64_t>(p)) +
+                      static_cast<uint32_t>(r) * static_cast<uint32_t>(ld) * static_cast<uint32_t>(sizeof(T));
+  return reinterpret_cast<const T*>(slot + (at & 15u));
 }
 
 // A group is whole warps.  With VEC = 1, warp w of it holds the elements
-// [w NV 32, (w + 1) NV 32), lane l every 32nd of them: the offsets between a
-// thread's elements are known to the compiler, which saves a third of the
-// instructions.  Whole vectors are dealt out over the group instead (thread l
-// has l, l + tpr, ...), which keeps the group's accesses of one step together:
-// 16384 x 4096 backward 78 us, 87 with vectors dealt out by warp.
+// [w NV 32, (w + 1) NV 32), lane l every 32nd of them, two of them to a step:
+// the offsets between a thread's elements are known to the compiler, and all
+// warps but a row's last have nothing to mask.  Whole vectors are dealt out
+// over the group instead (thread l has l, l + tpr, ...), which keeps the
+// group's accesses of one step together: 16384 x 4096 backward 78 us, 87 with
+// vectors dealt out by warp.
 constexpr int RING_THREADS = 512;
-// Copies k weights to shared memory and adds zeros up to `all` (the block joins afterwards).
+// Copies k weights to shared memory (VEC = 1: `none` where there are none) and
+// adds zeros up to `all` (the block joins afterwards).
 template <class W, int VEC>
-__device__ __forceinline__ void keep_weights(W* to, const W* from, int k, int all) {
-  if (from)
+__device__ __forceinline__ void keep_weights(W* to, const W* from, int k, int all, float none) {
+  if (from || VEC == 1)
+#pragma unroll 4
     for (int c = threadIdx.x * VEC; c < all; c += RING_THREADS * VEC) {
       Vec<W, VEC> v = {};
-      if (c < k) v = load<W, VEC>(from + c);
+      if (c < k) {
+        if (from)
+          v = load<W, VEC>(from + c);
+        else
+          put(&v.e[0], none);
+      }
       *reinterpret_cast<Vec<W, VEC>*>(to + c) = v;
     }
 }
+// A thread's first element, how far apart its steps are, and how many it has.
 template <int VEC, int NV>
 __device__ __forceinline__ int first_column(int tpr) {
   const int lane = static_cast<int>(threadIdx.x & (tpr - 1));
@@ -329,8 +380,13 @@ __device__ __forceinline__ int first_column(int tpr) {
 }
 template <int VEC>
 __device__ __forceinline__ int column_step(int tpr) {
-  return VEC > 1 ? tpr * VEC : 32;
+  return VEC > 1 ? tpr * VEC : 2 * STRIDE1;
 }
+template <int VEC, int NV>
+constexpr int STEPS = VEC > 1 ? NV : NV / 2;
+// The most units of a row that a thread copies: up to NV elements a thread, and at most one unit more for the row.
+template <class T, int NV>
+constexpr int MOST_UNITS = NV * static_cast<int>(sizeof(T)) / 16 + 1;
 
 // Forward: `depth` rows of each group are in flight or in use.  FULL: the
 // group's vectors are exactly a row's.
@@ -338,7 +394,7 @@ template <class T, class W, int VEC, int NV, bool FULL>
 __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int tpr, int depth) {
   extern __shared__ __align__(16) uint8_t smem[];  // gamma, beta, the rows in flight, slack to read past them
   __shared__ float red[4][RING_THREADS / 32];
-  constexpr int L = VEC > 1 ? 2 : 1, NN = VEC / L;
+  constexpr int NN = NUMS<VEC>, ST = STEPS<VEC, NV>;
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = RING_THREADS / tpr;
@@ -352,6 +408,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
   // slot s of this thread's vectors, or of its group's row
   const uint32_t slot_bytes = VEC > 1 ? NV * RING_THREADS * 16 : groups * row_bytes(k, sizeof(T));
   uint8_t* const mine = ring + (VEC > 1 ? threadIdx.x * 16 : group * row_bytes(k, sizeof(T)));
+  const int64_t edge = edge_rows(k);
   auto fetch = [&](int64_t r, int slot) {
     const bool live = r < a.n;
     const T* x = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
@@ -363,78 +420,89 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
         copy_async(to + i * (RING_THREADS * 16), x + (FULL || c < k ? c : 0), live && (FULL || c < k));
       }
     } else if (live) {
-      copy_units(x, k, to, lane, tpr, r == 0, r == a.n - 1);
+      copy_units<T, MOST_UNITS<T, NV>>(x, k, to, lane, tpr, r < edge || r >= a.n - edge);
     }
     copy_commit();
   };
-  for (int d = 0; d < depth - (VEC == 1); ++d) fetch(row + d * step, d);
-  keep_weights<W, VEC>(gamma, static_cast<const W*>(a.gamma), k, k);
-  keep_weights<W, VEC>(beta, static_cast<const W*>(a.beta), k, k);
+  for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
+  keep_weights<W, VEC>(gamma, static_cast<const W*>(a.gamma), k, k, 1.0f);
+  keep_weights<W, VEC>(beta, static_cast<const W*>(a.beta), k, k, 0.0f);
   __syncthreads();
-  const bool has_gamma = a.gamma != nullptr, has_beta = a.beta != nullptr;
+  const bool has_gamma = VEC == 1 || a.gamma != nullptr, has_beta = VEC == 1 || a.beta != nullptr;
   const float inv_k = 1.0f / static_cast<float>(k);
   int slot = 0, buf = 0;
+  // WHOLE: all of this warp's elements exist.
+  auto work = [&](auto whole, bool live) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    const int own = WHOLE ? ST * step_c : live || VEC > 1 ? k - c0 : 0;  // elements from this thread's first on
+    Num v[ST][NN], s = all(0.0f);
+    if constexpr (VEC == 1) {
+      const T* x = unit_row<T>(a.x, row, a.ldx, mine + slot * slot_bytes) + c0;
+#pragma unroll
+      for (int i = 0; i < ST; ++i) {
+        read_nums<T, 1>(x + i * 64, v[i]);  // past the row's end: whatever lies there, in shared memory all the same
+        if constexpr (!WHOLE) mask_nums<1>(v[i], own - i * 64);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < ST; ++i)
+        read_nums<T, VEC>(reinterpret_cast<const T*>(mine + slot * slot_bytes + i * (RING_THREADS * 16)), v[i]);
+      fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+    }
+#pragma unroll
+    for (int i = 0; i < ST; ++i)
+#pragma unroll
+      for (int j = 0; j < NN; ++j) s = add(s, v[i][j]);
+    const float mean = group_sum(total(s), group, tpr, red[buf]) * inv_k;
+    if constexpr (VEC == 1) fetch(row + depth * step, slot);  // the slot has been read, by the whole group
+    const Num minus = all(-mean);
+    s = all(0.0f);
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+#pragma unroll
+      for (int j = 0; j < NN; ++j) v[i][j] = add(v[i][j], minus);
+      if constexpr (!WHOLE) mask_nums<VEC>(v[i], own - i * step_c);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) s = fma(v[i][j], v[i][j], s);
+    }
+    const float rstd = rsqrtf(group_sum(total(s), group, tpr, red[buf + 1]) * inv_k + a.eps);
+    const Num scale = all(rstd);
+    T* const y = static_cast<T*>(a.y) + row * a.ldy + c0;
+    if (live)
+#pragma unroll
+      for (int i = 0; i < ST; ++i) {
+        const int c = i * step_c;
+        if (!WHOLE && c >= own) continue;
+        Num g[NN], b[NN];
+        if (has_gamma) read_nums<W, VEC>(gamma + c0 + c, g);
+        if (has_beta) read_nums<W, VEC>(beta + c0 + c, b);
+#pragma unroll
+        for (int j = 0; j < NN; ++j) {
+          v[i][j] = mul(v[i][j], scale);
+          if (has_gamma) v[i][j] = mul(v[i][j], g[j]);
+          if (has_beta) v[i][j] = add(v[i][j], b[j]);
+        }
+        write_nums<T, VEC>(y + c, v[i], WHOLE ? 2 * STRIDE1 : own - c);
+      }
+    if (live && lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+  };
   // every group of the block runs the same number of rounds
   const int64_t sets = (a.n + groups - 1) / groups;
   for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
     const bool live = row < a.n;
-    Num<L> v[NV][NN], s = all<L>(0.0f);
     if constexpr (VEC > 1) {
       copy_wait(depth - 1);
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(mine + slot * slot_bytes + i * (RING_THREADS * 16)), v[i]);
-      fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+      work(std::bool_constant<FULL>(), live);
     } else {
-      copy_wait(depth - 2);
-      group_barrier(tpr);  // the row is there, and every thread is done with the one before
-      fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
-      const T* x = unit_row(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx, mine + slot * slot_bytes) + c0;
-      const int own = live ? k - c0 : 0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const float e = to_f(x[i * 32]);  // past the row's end: whatever lies there, in shared memory all the same
-        v[i][0].v = i * 32 < own ? e : 0.0f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < NN; ++j) s = add(s, v[i][j]);
-    const float mean = row_sum<true>(total(s), tpr, red[buf]) * inv_k;
-    const Num<L> minus = all<L>(-mean);
-    s = all<L>(0.0f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int j = 0; j < NN; ++j) {
-        v[i][j] = add(v[i][j], minus);
-        if constexpr (!FULL)
-          if ((c0 + i * step_c) >= k) v[i][j] = all<L>(0.0f);
-        s = fma(v[i][j], v[i][j], s);
-      }
-    }
-    const float rstd = rsqrtf(row_sum<true>(total(s), tpr, red[buf + 1]) * inv_k + a.eps);
-    const Num<L> scale = all<L>(rstd);
-    T* y = static_cast<T*>(a.y) + row * a.ldy;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (c0 + i * step_c);
-      if (!FULL && c >= k) continue;
-      Num<L> g[NN], b[NN];
-      if (has_gamma) to_nums<W, VEC, L>(load<W, VEC>(gamma + c), g);
-      if (has_beta) to_nums<W, VEC, L>(load<W, VEC>(beta + c), b);
-#pragma unroll
-      for (int j = 0; j < NN; ++j) {
-        v[i][j] = mul(v[i][j], scale);
-        if (has_gamma) v[i][j] = mul(v[i][j], g[j]);
-        if (has_beta) v[i][j] = add(v[i][j], b[j]);
-      }
-      if (live) *reinterpret_cast<Vec<T, VEC>*>(y + c) = from_nums<T, VEC, L>(v[i]);
-    }
-    if (live && lane == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
+      copy_wait(depth - 1);
+      group_barrier(group, tpr);  // the row is there
+      if (live && (c0 & ~31) + NV * 32 <= k)  // one answer per warp
+        work(std::true_type(), true);
+      else
+        work(std::false_type(), live);
     }
     if (++slot == depth) slot = 0;
     buf ^= 2;
@@ -443,29 +511,47 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
 }
 
 // Adds the sums of a block's row groups in their order and stores them:
-// part[blockIdx.x][2][k].  `sums`: [groups][2][k] floats of shared memory.
-template <int VEC, int NV, int L>
-__device__ __forceinline__ void store_sums(const Num<L> (&dg)[NV][VEC / L], const Num<L> (&db)[NV][VEC / L], int k,
-                                           int tpr, float* sums, float* part) {
+// part[blockIdx.x][2][k].  `sums`: [groups][2][k] floats of shared memory,
+// which a lone group of single elements does without.
+template <int VEC, int NV>
+__device__ __forceinline__ void store_sums(const Num (&dg)[STEPS<VEC, NV>][NUMS<VEC>],
+                                           const Num (&db)[STEPS<VEC, NV>][NUMS<VEC>], int k, int tpr, float* sums,
+                                           float* part) {
   const int c0 = first_column<VEC, NV>(tpr), step_c = column_step<VEC>(tpr);
-  const int group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  float* mine = sums + group * 2 * k;
+  const int group = threadIdx.x / tpr, groups = RING_THREADS / tpr;
+  float* const out = part + static_cast<int64_t>(blockIdx.x) * 2 * k;
+  auto put_all = [&](float* to) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (c0 + i * step_c);
-    if (c < k)
+    for (int i = 0; i < STEPS<VEC, NV>; ++i) {
+      const int c = c0 + i * step_c;
+      if constexpr (VEC == 1) {
+        write_nums<float, 1>(to + c, dg[i], k - c);
+        write_nums<float, 1>(to + k + c, db[i], k - c);
+      } else if (c < k) {
 #pragma unroll
-      for (int j = 0; j < VEC / L; ++j) {  // k is even where values come in pairs
-        memcpy(mine + c + j * L, &dg[i][j], sizeof(Num<L>));
-        memcpy(mine + k + c + j * L, &db[i][j], sizeof(Num<L>));
+        for (int j = 0; j < NUMS<VEC>; ++j) {  // k is even where values come in pairs
+          memcpy(to + c + j * 2, &dg[i][j], sizeof(Num));
+          memcpy(to + k + c + j * 2, &db[i][j], sizeof(Num));
+        }
       }
+    }
+  };
+  if (VEC == 1 && groups == 1) {
+    put_all(out);
+    return;
   }
+  put_all(sums + group * 2 * k);
   __syncthreads();
-  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * k;
-  for (int c = threadIdx.x; c < 2 * k; c += blockDim.x) {
-    float v = 0.0f;
-    for (int q = 0; q < groups; ++q) v += sums[q * 2 * k + c];
-    out[c] = v;
+  for (int c = threadIdx.x; c < 2 * k; c += 4 * RING_THREADS) {
+    float v[4] = {};
+#pragma unroll 1
+    for (int q = 0; q < groups; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j * RING_THREADS < 2 * k) v[j] += sums[q * 2 * k + c + j * RING_THREADS];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j * RING_THREADS < 2 * k) out[c + j * RING_THREADS] = v[j];
   }
 }
 
@@ -475,8 +561,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
                                                                         float* part) {
   extern __shared__ __align__(16) uint8_t smem[];  // gamma, the rows in flight, slack to read past them
   __shared__ float2 red[2][RING_THREADS / 32];
-  constexpr int L = VEC > 1 ? 2 : 1, NN = VEC / L;
+  constexpr int NN = NUMS<VEC>, ST = STEPS<VEC, NV>;
   constexpr bool KEEP = NV * VEC <= 20;  // xhat and dy gamma stay in registers from the sums to dx
+  static_assert(KEEP || VEC > 1, "single elements are read once");
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = RING_THREADS / tpr;
@@ -489,19 +576,26 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   constexpr bool GREG = KEEP && VEC > 1 && sizeof(W) == 2;
   W* const gamma = reinterpret_cast<W*>(smem);
   uint8_t* const ring = smem + (GREG ? 0u : weight_bytes(tpr * NV * VEC, sizeof(W)));
-  const bool has_gamma = a.gamma != nullptr;
+  const bool has_gamma = VEC == 1 || a.gamma != nullptr;
   // slot s, matrix w: this thread's vectors, or its group's row
   const uint32_t part_bytes = VEC > 1 ? NV * RING_THREADS * 16 : groups * row_bytes(k, sizeof(T));
   uint8_t* const mine = ring + (VEC > 1 ? threadIdx.x * 16 : group * row_bytes(k, sizeof(T)));
   auto at = [&](int slot, int which) { return mine + (slot * arrays + which) * part_bytes; };
   // a vector past the row's end, or of a row past the last, is zeros: it adds nothing to any sum
-  auto fetch = [&](int64_t r, int slot) {
+  const int64_t edge = edge_rows(k);
+  auto fetch_dres = [&](int64_t r, int slot) {  // VEC = 1
+    if (arrays == 3 && r < a.n)
+      copy_units<T, MOST_UNITS<T, NV>>(static_cast<const T*>(a.dres) + r * a.lddres, k, smem_u32(at(slot, 2)), lane,
+                                       tpr, r < edge || r >= a.n - edge);
+  };
+  auto fetch = [&](int64_t r, int slot) {  // dres with vectors only
     const bool live = r < a.n;
     const int64_t q = live ? r : 0;
     const T *x = static_cast<const T*>(a.x) + q * a.ldx, *dy = static_cast<const T*>(a.dy) + q * a.lddy;
-    const T* dres = static_cast<const T*>(a.dres) + q * a.lddres;
-    const uint32_t tx = smem_u32(at(slot, 0)), td = smem_u32(at(slot, 1)), tr = smem_u32(at(slot, 2));
+    const uint32_t tx = smem_u32(at(slot, 0)), td = smem_u32(at(slot, 1));
     if constexpr (VEC > 1) {
+      const T* dres = static_cast<const T*>(a.dres) + q * a.lddres;
+      const uint32_t tr = smem_u32(at(slot, 2));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (c0 + i * step_c);
@@ -512,14 +606,16 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
         if (arrays == 3) copy_async(tr + i * (RING_THREADS * 16), dres + o, in);
       }
     } else if (live) {
-      const bool first = r == 0, last = r == a.n - 1;
-      copy_units(x, k, tx, lane, tpr, first, last);
-      copy_units(dy, k, td, lane, tpr, first, last);
-      if (arrays == 3) copy_units(dres, k, tr, lane, tpr, first, last);
+      const bool at_edge = r < edge || r >= a.n - edge;
+      copy_units<T, MOST_UNITS<T, NV>>(x, k, tx, lane, tpr, at_edge);
+      copy_units<T, MOST_UNITS<T, NV>>(dy, k, td, lane, tpr, at_edge);
     }
     copy_commit();
   };
-  for (int d = 0; d < depth - (VEC == 1); ++d) fetch(row + d * step, d);
+  for (int d = 0; d < depth; ++d) {
+    if constexpr (VEC == 1) fetch_dres(row + d * step, d);
+    fetch(row + d * step, d);
+  }
   Vec<W, VEC> gk[GREG ? NV : 1];
   if constexpr (GREG) {
 #pragma unroll
@@ -529,53 +625,49 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
       if (has_gamma && c < k) gk[i] = load<W, VEC>(static_cast<const W*>(a.gamma) + c);
     }
   } else {
-    keep_weights<W, VEC>(gamma, static_cast<const W*>(a.gamma), k, tpr * NV * VEC);  // zeros past the row's end
+    // zeros past the row's end
+    keep_weights<W, VEC>(gamma, static_cast<const W*>(a.gamma), k, tpr * NV * VEC, 1.0f);
     __syncthreads();
   }
-  Num<L> dg[NV][NN], db[NV][NN];
+  Num dg[ST][NN], db[ST][NN];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < ST; ++i)
 #pragma unroll
-    for (int j = 0; j < NN; ++j) dg[i][j] = db[i][j] = all<L>(0.0f);
+    for (int j = 0; j < NN; ++j) dg[i][j] = db[i][j] = all(0.0f);
   const float inv_k = 1.0f / static_cast<float>(k);
   int slot = 0, buf = 0;
   float mean = row < a.n ? a.mean[row] : 0.0f, rstd = row < a.n ? a.rstd[row] : 0.0f;
-  const int64_t sets = (a.n + groups - 1) / groups;
-  for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
-    const bool live = row < a.n;
-    const float mean_n = row + step < a.n ? a.mean[row + step] : 0.0f;
-    const float rstd_n = row + step < a.n ? a.rstd[row + step] : 0.0f;
-    copy_wait(VEC > 1 ? depth - 1 : depth - 2);
+  // WHOLE (VEC = 1): all of this warp's elements exist.
+  auto work = [&](auto whole, bool live) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    const T *ux = nullptr, *ud = nullptr;  // VEC = 1: this thread's first element of each row
     if constexpr (VEC == 1) {
-      group_barrier(tpr);  // the row is there, and every thread is done with the one before
-      fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+      ux = unit_row<T>(a.x, row, a.ldx, at(slot, 0)) + c0;
+      ud = unit_row<T>(a.dy, row, a.lddy, at(slot, 1)) + c0;
     }
-    const int64_t q = live ? row : 0;
-    // VEC = 1: this thread's first element of each row, and how far the row reaches past it
-    const T* ux = unit_row(static_cast<const T*>(a.x) + q * a.ldx, at(slot, 0)) + c0;
-    const T* ud = unit_row(static_cast<const T*>(a.dy) + q * a.lddy, at(slot, 1)) + c0;
-    const int own = live ? k - c0 : 0;
-    const Num<L> minus = all<L>(-mean), scale = all<L>(rstd);
-    Num<L> s1 = all<L>(0.0f), s2 = s1;
-    // xhat and w = dy gamma of vector i
-    auto values = [&](int i, Num<L>(&h)[NN], Num<L>(&w)[NN], bool first) {
-      const int c = (c0 + i * step_c);
-      Num<L> g[NN];
+    const int own = live ? k - c0 : 0;  // elements from this thread's first on
+    const Num minus = all(-mean), scale = all(rstd);
+    Num s1 = all(0.0f), s2 = s1;
+    // xhat and w = dy gamma of step i
+    auto values = [&](int i, Num(&h)[NN], Num(&w)[NN], bool first) {
+      Num g[NN];
       if constexpr (VEC > 1) {
-        to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 0) + i * (RING_THREADS * 16)), h);
-        to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 1) + i * (RING_THREADS * 16)), w);
+        read_nums<T, VEC>(reinterpret_cast<const T*>(at(slot, 0) + i * (RING_THREADS * 16)), h);
+        read_nums<T, VEC>(reinterpret_cast<const T*>(at(slot, 1) + i * (RING_THREADS * 16)), w);
       } else {
         // past the row's end: whatever lies there, in shared memory all the same
-        const float ex = to_f(ux[i * 32]), ed = to_f(ud[i * 32]);
-        const bool in = i * 32 < own;
-        h[0].v = in ? ex : 0.0f;
-        w[0].v = in ? ed : 0.0f;
+        read_nums<T, 1>(ux + i * 64, h);
+        read_nums<T, 1>(ud + i * 64, w);
+        if constexpr (!WHOLE) {
+          mask_nums<1>(h, own - i * 64);
+          mask_nums<1>(w, own - i * 64);
+        }
       }
       if (has_gamma) {
         if constexpr (GREG)
-          to_nums<W, VEC, L>(gk[i], g);
+          to_nums<W, VEC>(gk[i], g);
         else
-          to_nums<W, VEC, L>(load<W, VEC>(gamma + c), g);
+          read_nums<W, VEC>(gamma + c0 + i * step_c, g);
       }
 #pragma unroll
       for (int j = 0; j < NN; ++j) {
@@ -587,11 +679,11 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
         if (has_gamma) w[j] = mul(w[j], g[j]);
       }
     };
-    Num<L> hk[KEEP ? NV : 1][NN], wk[KEEP ? NV : 1][NN];
+    Num hk[KEEP ? ST : 1][NN], wk[KEEP ? ST : 1][NN];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      Num<L>(&h)[NN] = hk[KEEP ? i : 0];
-      Num<L>(&w)[NN] = wk[KEEP ? i : 0];
+    for (int i = 0; i < ST; ++i) {
+      Num(&h)[NN] = hk[KEEP ? i : 0];
+      Num(&w)[NN] = wk[KEEP ? i : 0];
       values(i, h, w, true);
 #pragma unroll
       for (int j = 0; j < NN; ++j) {
@@ -599,33 +691,60 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
         s2 = fma(w[j], h[j], s2);
       }
     }
-    if (a.y) {
-      const float2 t = row_sums(total(s1), total(s2), tpr, red[buf]);
-      const Num<L> m1 = all<L>(-t.x * inv_k), m2 = all<L>(-t.y * inv_k);
-      T* o = static_cast<T*>(a.y) + row * a.ldy;
-      const T* ur = unit_row(static_cast<const T*>(a.dres) + q * a.lddres, at(slot, 2)) + c0;
+    if (!a.y) {
+      if constexpr (VEC == 1) {
+        group_barrier(group, tpr);
+        fetch(row + depth * step, slot);
+      }
+      return;
+    }
+    if (VEC == 1 && arrays == 3) copy_wait(depth - 2);  // this row's dres is there
+    const float2 t = group_sums(total(s1), total(s2), group, tpr, red[buf]);
+    if constexpr (VEC == 1) fetch(row + depth * step, slot);  // x and dy have been read, by the whole group
+    const Num m1 = all(-t.x * inv_k), m2 = all(-t.y * inv_k);
+    T* const dx = static_cast<T*>(a.y) + row * a.ldy + c0;
+    const T* ur = unit_row<T>(a.dres, row, a.lddres, at(slot, 2)) + c0;
+    auto finish = [&](auto with) {
+      constexpr bool DRES = decltype(with)::value;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        Num<L>(&h)[NN] = hk[KEEP ? i : 0];
-        Num<L>(&w)[NN] = wk[KEEP ? i : 0];
+      for (int i = 0; i < ST; ++i) {
+        Num(&h)[NN] = hk[KEEP ? i : 0];
+        Num(&w)[NN] = wk[KEEP ? i : 0];
         if constexpr (!KEEP) values(i, h, w, false);
-        Num<L> r[NN];
-        const int c = (c0 + i * step_c);
-        if (arrays == 3) {
-          if constexpr (VEC > 1)
-            to_nums<T, VEC, L>(*reinterpret_cast<const Vec<T, VEC>*>(at(slot, 2) + i * (RING_THREADS * 16)), r);
-          else
-            r[0].v = to_f(ur[i * 32]);
-        }
+        Num r[NN];
+        if constexpr (DRES)
+          read_nums<T, VEC>(VEC > 1 ? reinterpret_cast<const T*>(at(slot, 2) + i * (RING_THREADS * 16)) : ur + i * 64, r);
 #pragma unroll
         for (int j = 0; j < NN; ++j) {
-          const Num<L> q = fma(h[j], m2, add(w[j], m1));
-          r[j] = arrays == 3 ? fma(q, scale, r[j]) : mul(q, scale);
+          const Num q = fma(h[j], m2, add(w[j], m1));
+          r[j] = DRES ? fma(q, scale, r[j]) : mul(q, scale);
         }
-        if (live && c < k) *reinterpret_cast<Vec<T, VEC>*>(o + c) = from_nums<T, VEC, L>(r);
+        write_nums<T, VEC>(dx + i * step_c, r, WHOLE ? 2 * STRIDE1 : own - i * step_c);
       }
+    };
+    if (arrays == 3)
+      finish(std::true_type());
+    else
+      finish(std::false_type());
+  };
+  const int64_t sets = (a.n + groups - 1) / groups;
+  for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
+    const bool live = row < a.n;
+    const float mean_n = row + step < a.n ? a.mean[row + step] : 0.0f;
+    const float rstd_n = row + step < a.n ? a.rstd[row + step] : 0.0f;
+    if constexpr (VEC > 1) {
+      copy_wait(depth - 1);
+      work(std::false_type(), live);
+      fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+    } else {
+      copy_wait(depth - 1);
+      group_barrier(group, tpr);  // x and dy are there, and every thread is done with the dres before
+      if (set != blockIdx.x) fetch_dres(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+      if (live && (c0 & ~31) + NV * 32 <= k)  // one answer per warp
+        work(std::true_type(), true);
+      else
+        work(std::false_type(), live);
     }
-    if constexpr (VEC > 1) fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
     if (++slot == depth) slot = 0;
     buf ^= 1;
     mean = mean_n;
@@ -634,7 +753,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!part) return;
   __syncthreads();  // the ring is free: it holds the columns' sums now
-  store_sums<VEC, NV, L>(dg, db, k, tpr, reinterpret_cast<float*>(ring), part);
+  store_sums<VEC, NV>(dg, db, k, tpr, reinterpret_cast<float*>(ring), part);
 }
 
 // ------------------------------------------------------------------ long rows
