@@ -297,7 +297,8 @@ __device__ __forceinline__ void copy_wait(int ahead) {
 // it will read itself, so it needs no barrier before them.  With VEC = 1 the
 // group copies the aligned 16-byte units that hold the row, to the same offset
 // modulo 16, and reads single elements after a barrier; the slot is free after
-// the next one (that of the row's sum).  Units at a row's ends
+// the next one: that of the row's sum forward, where the registers hold the
+// row then, and that before the next row backward.  Units at a row's ends
 // bring a few bytes of what lies beside it, which nobody reads; where that
 // might be outside the matrix (`edge`: the first and the last edge_rows(k)
 // rows) only the row's own bytes are touched.
@@ -583,19 +584,13 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   auto at = [&](int slot, int which) { return mine + (slot * arrays + which) * part_bytes; };
   // a vector past the row's end, or of a row past the last, is zeros: it adds nothing to any sum
   const int64_t edge = edge_rows(k);
-  auto fetch_dres = [&](int64_t r, int slot) {  // VEC = 1
-    if (arrays == 3 && r < a.n)
-      copy_units<T, MOST_UNITS<T, NV>>(static_cast<const T*>(a.dres) + r * a.lddres, k, smem_u32(at(slot, 2)), lane,
-                                       tpr, r < edge || r >= a.n - edge);
-  };
-  auto fetch = [&](int64_t r, int slot) {  // dres with vectors only
+  auto fetch = [&](int64_t r, int slot) {
     const bool live = r < a.n;
     const int64_t q = live ? r : 0;
     const T *x = static_cast<const T*>(a.x) + q * a.ldx, *dy = static_cast<const T*>(a.dy) + q * a.lddy;
-    const uint32_t tx = smem_u32(at(slot, 0)), td = smem_u32(at(slot, 1));
+    const T* dres = static_cast<const T*>(a.dres) + q * a.lddres;
+    const uint32_t tx = smem_u32(at(slot, 0)), td = smem_u32(at(slot, 1)), tr = smem_u32(at(slot, 2));
     if constexpr (VEC > 1) {
-      const T* dres = static_cast<const T*>(a.dres) + q * a.lddres;
-      const uint32_t tr = smem_u32(at(slot, 2));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (c0 + i * step_c);
@@ -609,13 +604,11 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
       const bool at_edge = r < edge || r >= a.n - edge;
       copy_units<T, MOST_UNITS<T, NV>>(x, k, tx, lane, tpr, at_edge);
       copy_units<T, MOST_UNITS<T, NV>>(dy, k, td, lane, tpr, at_edge);
+      if (arrays == 3) copy_units<T, MOST_UNITS<T, NV>>(dres, k, tr, lane, tpr, at_edge);
     }
     copy_commit();
   };
-  for (int d = 0; d < depth; ++d) {
-    if constexpr (VEC == 1) fetch_dres(row + d * step, d);
-    fetch(row + d * step, d);
-  }
+  for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
   Vec<W, VEC> gk[GREG ? NV : 1];
   if constexpr (GREG) {
 #pragma unroll
@@ -691,16 +684,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
         s2 = fma(w[j], h[j], s2);
       }
     }
-    if (!a.y) {
-      if constexpr (VEC == 1) {
-        group_barrier(group, tpr);
-        fetch(row + depth * step, slot);
-      }
-      return;
-    }
-    if (VEC == 1 && arrays == 3) copy_wait(depth - 2);  // this row's dres is there
+    if (!a.y) return;
     const float2 t = group_sums(total(s1), total(s2), group, tpr, red[buf]);
-    if constexpr (VEC == 1) fetch(row + depth * step, slot);  // x and dy have been read, by the whole group
     const Num m1 = all(-t.x * inv_k), m2 = all(-t.y * inv_k);
     T* const dx = static_cast<T*>(a.y) + row * a.ldy + c0;
     const T* ur = unit_row<T>(a.dres, row, a.lddres, at(slot, 2)) + c0;
@@ -737,9 +722,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
       work(std::false_type(), live);
       fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
     } else {
-      copy_wait(depth - 1);
-      group_barrier(group, tpr);  // x and dy are there, and every thread is done with the dres before
-      if (set != blockIdx.x) fetch_dres(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+      const bool later = set != blockIdx.x;
+      copy_wait(later ? depth - 2 : depth - 1);
+      group_barrier(group, tpr);  // the row is there, and every thread is done with the one before
+      if (later) fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
       if (live && (c0 & ~31) + NV * 32 <= k)  // one answer per warp
         work(std::true_type(), true);
       else

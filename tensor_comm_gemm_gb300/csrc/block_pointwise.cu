@@ -144,9 +144,16 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* part, in
   W* out = blockIdx.y ? out1 : out0;
   if (!out) return;
   float v = 0.0f;
-  if (c < cols)
-#pragma unroll 4
-    for (int p = slice; p < parts; p += 32) v += part[(static_cast<int64_t>(p) * gridDim.y + blockIdx.y) * cols + c];
+  // five loads in flight: all that a slice of the most parts (152) has
+  const int64_t vectors = gridDim.y;
+  for (int p = slice; c < cols && p < parts; p += 32 * 5) {
+    float w[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j)
+      w[j] = p + 32 * j < parts ? part[((p + 32 * j) * vectors + blockIdx.y) * cols + c] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 5; ++j) v += w[j];
+  }
   s[slice][lane] = v;
   __syncthreads();
   v = s[lane][slice];
