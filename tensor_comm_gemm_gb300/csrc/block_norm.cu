@@ -10,8 +10,8 @@
 //
 // With many rows a block is persistent: its row groups take rows g, g + G, ...,
 // and every thread keeps the vectors of its next rows in flight with
-// asynchronous copies into its own part of shared memory (two to four rows
-// ahead, up to 226 KB per SM), so no barrier is needed before they are read.
+// asynchronous copies into its own part of shared memory, so no barrier is
+// needed before they are read.
 //
 // Backward, a block also keeps the sums over its rows of dy xhat and dy for the
 // columns its threads own in fp32 registers; they go to the workspace once,
@@ -19,6 +19,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 
 #include <cuda_bf16.h>
 
@@ -286,16 +287,10 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool e
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(exists ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most `ahead` of this thread's latest copy groups are in flight.
-__device__ __forceinline__ void copy_wait(int ahead) {
-  if (ahead >= 3)
-    asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (ahead == 2)
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (ahead == 1)
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+// Waits until at most AHEAD of this thread's latest copy groups are in flight.
+template <int AHEAD>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
 }
 // Rows in flight.  With VEC > 1 (16-byte rows) a thread copies the vectors that
 // it will read itself, so it needs no barrier before them.  With VEC = 1 the
@@ -393,12 +388,17 @@ constexpr int STEPS = VEC > 1 ? NV : NV / 2;
 template <class T, int NV>
 constexpr int MOST_UNITS = NV * static_cast<int>(sizeof(T)) / 16 + 1;
 
-// Forward: `depth` rows of each group are in flight or in use.  FULL: the
-// group's vectors are exactly a row's.  8192 x 8192 bf16 in 48 us, 5.6 TB/s of
-// 6.8; 2000 x 7777 (single elements) in 28 us, where the shared-memory accesses
+// Rows of each group in flight or in use.  Two: with 32 KB and more a row set,
+// that covers the memory's latency, and more only puts off the first rows and
+// with them the first stores: 2048 x 4096 bf16 forward 10.6 us, 11.5 with three,
+// 11.8 with four; 16384 x 4096 backward 76.8 (90.2 with dres), 77.4 (91.7).
+constexpr int DEPTH = 2;
+
+// Forward.  FULL: the group's vectors are exactly a row's.  8192 x 8192 bf16 in
+// 46 us, 5.8 TB/s of 6.8; 2000 x 7777 (single elements) in 28 us, where the shared-memory accesses
 // and the three barriers of a row, with 16 warps in step, bound it.
 template <class T, class W, int VEC, int NV, bool FULL>
-__global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int tpr, int depth) {
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int tpr) {
   extern __shared__ __align__(16) uint8_t smem[];  // gamma, beta, the rows in flight, slack to read past them
   __shared__ float red[4][RING_THREADS / 32];
   constexpr int NN = NUMS<VEC>, ST = STEPS<VEC, NV>;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
     }
     copy_commit();
   };
-  for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
+  for (int d = 0; d < DEPTH; ++d) fetch(row + d * step, d);
   keep_weights<W, VEC>(gamma, static_cast<const W*>(a.gamma), k, k, 1.0f);
   keep_weights<W, VEC>(beta, static_cast<const W*>(a.beta), k, k, 0.0f);
   __syncthreads();
@@ -454,14 +454,14 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < ST; ++i)
         read_nums<T, VEC>(reinterpret_cast<const T*>(mine + slot * slot_bytes + i * (RING_THREADS * 16)), v[i]);
-      fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+      fetch(row + DEPTH * step, slot);  // the slot has been read (by this thread, its only reader)
     }
 #pragma unroll
     for (int i = 0; i < ST; ++i)
 #pragma unroll
       for (int j = 0; j < NN; ++j) s = add(s, v[i][j]);
     const float mean = group_sum(total(s), group, tpr, red[buf]) * inv_k;
-    if constexpr (VEC == 1) fetch(row + depth * step, slot);  // the slot has been read, by the whole group
+    if constexpr (VEC == 1) fetch(row + DEPTH * step, slot);  // the slot has been read, by the whole group
     const Num minus = all(-mean);
     s = all(0.0f);
 #pragma unroll
@@ -501,17 +501,17 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
   for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
     const bool live = row < a.n;
     if constexpr (VEC > 1) {
-      copy_wait(depth - 1);
+      copy_wait<DEPTH - 1>();
       work(std::bool_constant<FULL>(), live);
     } else {
-      copy_wait(depth - 1);
+      copy_wait<DEPTH - 1>();
       group_barrier(group, tpr);  // the row is there
       if (live && (c0 & ~31) + NV * 32 <= k)  // one answer per warp
         work(std::true_type(), true);
       else
         work(std::false_type(), live);
     }
-    if (++slot == depth) slot = 0;
+    if (++slot == DEPTH) slot = 0;
     buf ^= 2;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -565,11 +565,11 @@ __device__ __forceinline__ void store_sums(const Num (&dg)[STEPS<VEC, NV>][NUMS<
 // Backward, rows in flight as forward: x, dy and (if given) dres of a row.
 // With xhat = (x - mean) rstd and w = dy gamma:
 // dx = rstd (w - mean(w) - xhat mean(w xhat)) + dres.  16384 x 4096 bf16 with
-// dres in 78 us and the column sums' 6 behind it (537 MB, 6.2 TB/s in all);
+// dres in 85 us with the column sums behind it (537 MB, 6.3 TB/s in all);
 // 777 x 5003 f32 in 22 us with them: 5.1 rows per SM in two groups are three
 // rounds, and the start, the last round and the sums do not overlap.
 template <class T, class W, int VEC, int NV>
-__global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const NormArgs a, int tpr, int depth,
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const NormArgs a, int tpr,
                                                                         float* part) {
   extern __shared__ __align__(16) uint8_t smem[];  // gamma, the rows in flight, slack to read past them
   __shared__ float2 red[2][RING_THREADS / 32];
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
     }
     copy_commit();
   };
-  for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
+  for (int d = 0; d < DEPTH; ++d) fetch(row + d * step, d);
   Vec<W, VEC> gk[GREG ? NV : 1];
   if constexpr (GREG) {
 #pragma unroll
@@ -708,8 +708,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
         Num(&w)[NN] = wk[KEEP ? i : 0];
         if constexpr (!KEEP) values(i, h, w, false);
         Num r[NN];
-        if constexpr (DRES)
-          read_nums<T, VEC>(VEC > 1 ? reinterpret_cast<const T*>(at(slot, 2) + i * (RING_THREADS * 16)) : ur + i * 64, r);
+        if constexpr (DRES && VEC > 1)
+          read_nums<T, VEC>(reinterpret_cast<const T*>(at(slot, 2) + i * (RING_THREADS * 16)), r);
+        else if constexpr (DRES)
+          read_nums<T, VEC>(ur + i * 64, r);
 #pragma unroll
         for (int j = 0; j < NN; ++j) {
           const Num q = fma(h[j], m2, add(w[j], m1));
@@ -729,20 +731,23 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
     const float mean_n = row + step < a.n ? a.mean[row + step] : 0.0f;
     const float rstd_n = row + step < a.n ? a.rstd[row + step] : 0.0f;
     if constexpr (VEC > 1) {
-      copy_wait(depth - 1);
+      copy_wait<DEPTH - 1>();
       work(std::false_type(), live);
-      fetch(row + depth * step, slot);  // the slot has been read (by this thread, its only reader)
+      fetch(row + DEPTH * step, slot);  // the slot has been read (by this thread, its only reader)
     } else {
       const bool later = set != blockIdx.x;
-      copy_wait(later ? depth - 2 : depth - 1);
+      if (later)
+        copy_wait<DEPTH - 2>();
+      else
+        copy_wait<DEPTH - 1>();
       group_barrier(group, tpr);  // the row is there, and every thread is done with the one before
-      if (later) fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+      if (later) fetch(row + (DEPTH - 1) * step, slot == 0 ? DEPTH - 1 : slot - 1);
       if (live && (c0 & ~31) + NV * 32 <= k)  // one answer per warp
         work(std::true_type(), true);
       else
         work(std::false_type(), live);
     }
-    if (++slot == depth) slot = 0;
+    if (++slot == DEPTH) slot = 0;
     buf ^= 1;
     mean = mean_n;
     rstd = rstd_n;
@@ -875,42 +880,34 @@ Share share(int64_t vecs, int nv, int most_nv, int most_tpr, int least_tpr = 1) 
   return s;
 }
 
-// Rows in flight per group and the shared memory of a block that also keeps
-// `fixed` bytes of weights; depth < 2: they do not fit.
+// The shared memory of a block with DEPTH rows per group and `fixed` bytes of
+// weights; 0: too much.
 constexpr size_t RING_SMEM = 226 * 1024;
-struct Ring {
-  int depth;
-  size_t smem;
-};
-Ring ring_of(bool vec, const Share& h, int arrays, int64_t k, int elem, size_t fixed) {
-  if (!h.tpr) return {0, 0};
+size_t ring_smem(bool vec, const Share& h, int arrays, int64_t k, int elem, size_t fixed) {
+  if (!h.tpr) return 0;
   const size_t slot = arrays * (vec ? static_cast<size_t>(RING_THREADS) * h.nv * 16
                                     : static_cast<size_t>(RING_THREADS / h.tpr) * row_bytes(static_cast<int>(k), elem));
   // single elements are also read past the row's end
-  const size_t rest = fixed + (vec ? 0 : static_cast<size_t>(h.tpr) * h.nv * elem);
-  if (rest >= RING_SMEM) return {0, 0};
-  Ring r;
-  r.depth = static_cast<int>(std::min<size_t>(4, (RING_SMEM - rest) / slot));
-  r.smem = rest + slot * r.depth;
-  return r;
+  const size_t all = fixed + (vec ? 0 : static_cast<size_t>(h.tpr) * h.nv * elem) + DEPTH * slot;
+  return all <= RING_SMEM ? all : 0;
 }
 
-// Single elements: 8 to 20 a thread, whichever leaves the fewest places of the
-// group without an element; at least two rows fit, and a choice by which only
-// two do has to save a seventh of the places.  (Fewer idle threads against
-// deeper prefetch: f32 777x5003 backward, 20 elements and two rows 18.9 us, 12
-// and four 20.2; bf16 1000x9001, 20 28.6, 16 45.)
-Share share_single(int64_t k, int arrays, int elem, int welem, int weights) {
+// Of some numbers of vectors a thread, the one that leaves the fewest of a
+// group's places without a vector (the first of equals); f: whether it will do.
+template <class F>
+Share share_best(int64_t vecs, std::initializer_list<int> nvs, F f) {
   Share best{0, 0};
-  int64_t best_cost = 0;
-  for (int nv : {20, 16, 12, 8}) {
-    const Share s = share(k, nv, nv, RING_THREADS, 32);
-    if (!s.tpr) continue;
-    const int depth = ring_of(false, s, arrays, k, elem, weights * weight_bytes(s.tpr * nv, welem)).depth;
-    const int64_t cost = static_cast<int64_t>(s.tpr) * nv * (depth >= 3 ? 6 : 7);
-    if (depth >= 2 && (!best.tpr || cost < best_cost)) best = s, best_cost = cost;
+  for (int nv : nvs) {
+    const Share s = share(vecs, nv, nv, RING_THREADS, 32);
+    if (s.tpr && f(s) && (!best.tpr || s.tpr * nv < best.tpr * best.nv)) best = s;
   }
   return best;
+}
+// Single elements (f32 777x5003 backward, 20 a thread 18.9 us, 12 20.2; bf16 1000x9001, 20 28.6, 16 45).
+Share share_single(int64_t k, int arrays, int elem, int welem, int weights) {
+  return share_best(k, {20, 16, 12, 8}, [&](const Share& s) {
+    return ring_smem(false, s, arrays, k, elem, weights * weight_bytes(s.tpr * s.nv, welem)) > 0;
+  });
 }
 
 template <class K>
@@ -928,25 +925,33 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
     const bool vec = a.k % V == 0 && vec_ok(a.x, a.ldx, a.n, sizeof(T)) && vec_ok(a.y, a.ldy, a.n, sizeof(T)) &&
                      vec_ok(a.gamma, 0, 1, 4) && vec_ok(a.beta, 0, 1, 4);
     const int64_t vecs = vec ? a.k / V : a.k;
-    // Several rows for every group of a persistent block (one block of 512
-    // threads per SM): keep rows in flight.  Fewer rows: one row per group, as
-    // many threads as it has vectors (latency).  8192 rows of 8192, four
-    // vectors a thread: 48 us; two blocks per SM, with 64 registers a thread:
-    // 57, and then 70 with two vectors and 98 with eight.
-    const Share m = vec ? share(vecs, 4, 4, RING_THREADS, 32) : share_single(a.k, 1, sizeof(T), sizeof(W), 2);
+    // Rows for most of the SMs' persistent blocks (one of 512 threads per SM):
+    // keep rows in flight.  Fewer rows: one row per group, as many threads as it
+    // has vectors (latency).  700 rows of 4096 6.5 us and 6.6, 400 4.7 and 4.1;
+    // 1024 of 8192 10.7 and 15.0, 152 4.8 and 4.2; single elements, 400 of 5003
+    // 8.0 and 11.4.  8192 rows of 8192, 46 us: two blocks per SM, with 64
+    // registers a thread, were a sixth slower than one.
+    const Share m = vec ? share_best(vecs, {4, 3, 5}, [](const Share&) { return true; })
+                        : share_single(a.k, 1, sizeof(T), sizeof(W), 2);
     const int64_t sets = m.tpr ? (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr) : 0;
-    // (rows of up to 64 vectors would leave half of a group's threads idle)
-    if (sets >= (vec ? 2 : 1) * static_cast<int64_t>(mc.sms) && (!vec || vecs > 64)) {
-      const Ring r = ring_of(vec, m, 1, a.k, sizeof(T), 2 * weight_bytes(static_cast<int>(a.k), sizeof(W)));
+    // (16384 rows of 256, a third of whose group's places would hold a vector: 6.9 us, 8.5 in flight; of 512, two
+    // thirds: 12.8 and 10.1)
+    if (3 * sets >= 2 * static_cast<int64_t>(mc.sms) && (!vec || 2 * vecs >= m.tpr * m.nv)) {
+      const size_t smem = ring_smem(vec, m, 1, a.k, sizeof(T), 2 * weight_bytes(static_cast<int>(a.k), sizeof(W)));
       const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sets, mc.sms)));
       auto run = [&](auto kernel) {
         const cudaError_t e = allow_smem(kernel);
-        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(RING_THREADS), r.smem, s, a, m.tpr, r.depth);
+        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(RING_THREADS), smem, s, a, m.tpr);
       };
-      if (r.depth >= 2) {
-        if (vec)
-          return static_cast<int64_t>(m.tpr) * 4 == vecs ? run(norm_ring_kernel<T, W, V, 4, true>)
-                                                         : run(norm_ring_kernel<T, W, V, 4, false>);
+      auto run_vec = [&](auto nv) {
+        constexpr int NV = decltype(nv)::value;
+        return static_cast<int64_t>(m.tpr) * NV == vecs ? run(norm_ring_kernel<T, W, V, NV, true>)
+                                                        : run(norm_ring_kernel<T, W, V, NV, false>);
+      };
+      if (smem) {
+        if (vec && m.nv == 3) return run_vec(std::integral_constant<int, 3>());
+        if (vec && m.nv == 4) return run_vec(std::integral_constant<int, 4>());
+        if (vec) return run_vec(std::integral_constant<int, 5>());
         if (m.nv == 8) return run(norm_ring_kernel<T, W, 1, 8, false>);
         if (m.nv == 12) return run(norm_ring_kernel<T, W, 1, 12, false>);
         return m.nv == 16 ? run(norm_ring_kernel<T, W, 1, 16, false>) : run(norm_ring_kernel<T, W, 1, 20, false>);
@@ -977,23 +982,42 @@ cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int
     if (!wants) part = nullptr;
     int parts = 0;
     cudaError_t e = cudaSuccess;
-    // 16 elements a thread (rows up to 8192), else 32 of whole vectors
+    // Whole vectors: 16 elements a thread, whose xhat and dy gamma then stay in
+    // registers; 24 or (bf16: fp32 rows in flight would not fit) 32 where rows
+    // are too long for that, and 24 where that leaves a quarter fewer places,
+    // in bf16 rows long enough for it to pay: 8192 x 5120 59 us, 67 with 16;
+    // 2560 33.7 and 36.1; but 1536 22.6 and 21.8; fp32 4096 x 6144 57.5 and 55.2.
     constexpr int NV = 16 / V;
-    const Share h = vec ? share(vecs, NV, 2 * NV, RING_THREADS, 32)
-                        : share_single(a.k, a.dres && a.y ? 3 : 2, sizeof(T), sizeof(W), 1);
-    const size_t kept = vec && h.nv == NV && sizeof(W) == 2 ? 0 : weight_bytes(h.tpr * h.nv * (vec ? V : 1), sizeof(W));
-    const Ring r = ring_of(vec, h, a.dres && a.y ? 3 : 2, a.k, sizeof(T), kept);
-    if (r.depth >= 2 && a.n > 0) {
+    const int arrays = a.dres && a.y ? 3 : 2;
+    auto kept = [&](const Share& s) -> size_t {  // gamma in shared memory
+      return vec && s.nv == NV && sizeof(W) == 2 ? 0 : weight_bytes(s.tpr * s.nv * (vec ? V : 1), sizeof(W));
+    };
+    Share h{0, 0};
+    if (vec) {
+      h = share(vecs, NV, NV, RING_THREADS, 32);
+      auto fits = [&](const Share& s) { return ring_smem(true, s, arrays, a.k, sizeof(T), kept(s)) > 0; };
+      const Share more =
+          sizeof(T) == 2 ? share_best(vecs, {2 * NV, 3 * NV / 2}, fits) : share_best(vecs, {3 * NV / 2}, fits);
+      if (!h.tpr || (sizeof(T) == 2 && a.k > 2048 && more.tpr && 4 * more.tpr * more.nv <= 3 * h.tpr * h.nv)) h = more;
+    } else {
+      h = share_single(a.k, arrays, sizeof(T), sizeof(W), 1);
+    }
+    const size_t ring = ring_smem(vec, h, arrays, a.k, sizeof(T), kept(h));
+    if (ring && a.n > 0) {
       const int64_t sets = (a.n + RING_THREADS / h.tpr - 1) / (RING_THREADS / h.tpr);
       parts = static_cast<int>(std::min<int64_t>({sets, mc.sms, NORM_PARTS}));
       // the slots later hold every group's fp32 sums
-      const size_t smem = std::max(r.smem, kept + static_cast<size_t>(RING_THREADS / h.tpr) * 8 * a.k);
+      const size_t smem = std::max(ring, kept(h) + static_cast<size_t>(RING_THREADS / h.tpr) * 8 * a.k);
       auto run = [&](auto kernel) {
         const cudaError_t c = allow_smem(kernel);
-        return c != cudaSuccess ? c : launch_pdl(kernel, dim3(parts), dim3(RING_THREADS), smem, s, a, h.tpr, r.depth, part);
+        return c != cudaSuccess ? c : launch_pdl(kernel, dim3(parts), dim3(RING_THREADS), smem, s, a, h.tpr, part);
       };
-      if (vec)
-        e = h.nv == NV ? run(norm_bwd_ring_kernel<T, W, V, NV>) : run(norm_bwd_ring_kernel<T, W, V, 2 * NV>);
+      if (vec && h.nv == NV)
+        e = run(norm_bwd_ring_kernel<T, W, V, NV>);
+      else if (vec && h.nv == 3 * NV / 2)
+        e = run(norm_bwd_ring_kernel<T, W, V, 3 * NV / 2>);
+      else if (vec)
+        e = run(norm_bwd_ring_kernel<T, W, V, sizeof(T) == 2 ? 2 * NV : NV>);
       else if (h.nv == 8)
         e = run(norm_bwd_ring_kernel<T, W, 1, 8>);
       else if (h.nv == 12)
