@@ -416,6 +416,54 @@ def test_layer_norm_bwd(block, n, k, dt, wt):
     R.check("dbeta", db, want["dbeta"])
 
 
+# Aligned rows that give a thread each number of vectors, exactly or with some left over, in many rows and in few.
+WIDTHS = [(1700, 640), (1700, 768), (900, 1280), (900, 1248), (1700, 1024), (700, 2560), (700, 2504), (300, 5120),
+          (250, 6144), (220, 8448), (130, 9000), (120, 12288), (110, 16384), (105, 20480), (16400, 264), (16400, 512)]
+
+
+@pytest.mark.parametrize("n,k", WIDTHS)
+@pytest.mark.parametrize("dt,wt", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+def test_layer_norm_widths(block, n, k, dt, wt):
+    i = WIDTHS.index((n, k))
+    g = gen_of(700 + i)
+    x, dy = rnd(g, n, k, dtype=dt, scale=3) + 2.0, rnd(g, n, k, dtype=dt)
+    gamma = rnd(g, k, dtype=wt) if i % 4 != 3 else None
+    beta = rnd(g, k, dtype=wt) if i % 3 != 2 else None
+    dres = rnd(g, n, k, dtype=dt) if i % 2 else None
+    want = R.layer_norm(d(x), d(gamma), d(beta), 1e-5)
+    y = Out(n, k, dt, unit=8, extra=1)
+    mean, rstd = (torch.full((n,), float("nan"), device="cuda") for _ in range(2))
+    t.tpo_layer_norm(block, x, gamma, beta, y.t, mean=mean, rstd=rstd)
+    synced(block)
+    for name, v in (("y", y.get()), ("mean", mean), ("rstd", rstd)):
+        R.check(name, v, want[name])
+    want = R.layer_norm_bwd(d(dy), d(x), d(gamma), d(mean), d(rstd), d(dres))
+    dx = Out(n, k, dt, unit=8, extra=1)
+    dg, db = (torch.full((k,), float("nan"), dtype=wt, device="cuda") for _ in range(2))
+    t.tpo_layer_norm_bwd(block, dy, x, gamma, mean, rstd, dx.t, dgamma=dg, dbeta=db, dres=dres)
+    synced(block)
+    for name, v in (("dx", dx.get()), ("dgamma", dg), ("dbeta", db)):
+        R.check(name, v, want[name])
+
+
+@pytest.mark.parametrize("n,k", [(1200, 1003), (400, 5003), (1100, 4096), (2000, 24)])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_layer_norm_many_rows_in_place(block, n, k, dt):
+    g = gen_of(n)
+    x, dy, gamma, beta = rnd(g, n, k, dtype=dt), rnd(g, n, k, dtype=dt), rnd(g, k, dtype=dt), rnd(g, k, dtype=dt)
+    mean, rstd = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    y = x.clone()
+    t.tpo_layer_norm(block, y, gamma, beta, y, mean=mean, rstd=rstd)
+    synced(block)
+    R.check("y", y, R.layer_norm(d(x), d(gamma), d(beta), 1e-5)["y"])
+    want = R.layer_norm_bwd(d(dy), d(x), d(gamma), d(mean), d(rstd))
+    dg, db = torch.empty_like(gamma), torch.empty_like(beta)
+    t.tpo_layer_norm_bwd(block, dy, x, gamma, mean, rstd, dy, dgamma=dg, dbeta=db)
+    synced(block)
+    for name, v in (("dx", dy), ("dgamma", dg), ("dbeta", db)):
+        R.check(name, v, want[name])
+
+
 @pytest.mark.parametrize("which", ["dx", "dgamma", "dbeta", "dx dgamma", "dgamma dbeta", ""])
 def test_layer_norm_bwd_parts(block, which):
     g = gen_of(12)
