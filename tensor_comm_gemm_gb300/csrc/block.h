@@ -91,7 +91,7 @@ cudaError_t launch_column_sums(const float* part, int parts, int vectors, int64_
 // dz = dy act'(z) as bf16 [n, m] with pitch ldo (NULL: not written) and db = column sums (NULL: not wanted; part:
 // workspace of act_parts(n) x m floats).
 constexpr int ACT_PARTS = 152;
-inline int64_t act_parts(int64_t n) { return (n + 7) / 8 < ACT_PARTS ? (n + 7) / 8 : ACT_PARTS; }
+inline int64_t act_parts(int64_t n) { return (n + 15) / 16 < ACT_PARTS ? (n + 15) / 16 : ACT_PARTS; }
 cudaError_t launch_act_bwd(int64_t n, int64_t m, int act, const void* dy, int64_t lddy, const void* z, int64_t ldz,
                            void* dz, int64_t ldo, float* part, void* db, cudaStream_t s);
 // dg = dh u act'(g), du = dh act(g), bf16 with pitch ldo.

@@ -22,19 +22,24 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-// Columns [c, c + 8) of a row of m elements as fp32 (0 past its end); p is 16-byte aligned.
-__device__ __forceinline__ void load8(const bf16* p, int64_t c, int64_t m, float (&v)[8]) {
-  if (c + 8 <= m) {
-    const uint4 h = *reinterpret_cast<const uint4*>(p + c);
-    const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+// Columns [c, c + 8) of a row of m elements as they lie in memory (0 past its end); p is 16-byte aligned.
+__device__ __forceinline__ uint4 raw8(const bf16* p, int64_t c, int64_t m) {
+  if (c + 8 <= m) return *reinterpret_cast<const uint4*>(p + c);
+  uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  } else {
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = c + 2 * j < m ? __bfloat16_as_ushort(p[c + 2 * j]) : 0;
+    const uint32_t hi = c + 2 * j + 1 < m ? __bfloat16_as_ushort(p[c + 2 * j + 1]) : 0;
+    w[j] = lo | hi << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void widen8(const uint4& h, float (&v)[8]) {
+  const uint32_t w[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < m ? __bfloat162float(p[c + j]) : 0.0f;
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
 }
 // Rounds eight values to bf16 into a workspace row, whose pitch covers whole groups of eight.
@@ -48,29 +53,34 @@ __device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// One row's eight columns from c on: dz from dy and z, stored if wanted, and added to the sums.  WHOLE: all eight exist.
+// Eight columns from c on of some rows: dz from dy and z, stored if wanted, and
+// added to the sums.  WHOLE: all eight exist.
 template <int ACT, bool WHOLE>
 __device__ __forceinline__ void act_bwd_rows(int64_t first, int64_t n, int64_t step, int64_t c, int64_t m,
                                              const bf16* dy, int64_t lddy, const bf16* z, int64_t ldz, bf16* dz,
                                              int64_t ldo, float (&sum)[8]) {
-  constexpr int R = 4;  // rows whose loads are in flight together
+  constexpr int R = 2;  // rows whose loads are in flight together
   for (int64_t i0 = first; i0 < n; i0 += R * step) {
-    float d[R][8], v[R][8];
+    uint4 hd[R], hz[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t i = i0 + r * step < n ? i0 + r * step : i0;
-      load8(dy + i * lddy, c, WHOLE ? c + 8 : m, d[r]);
-      if constexpr (ACT != TPO_ACT_NONE) load8(z + i * ldz, c, WHOLE ? c + 8 : m, v[r]);
+      hd[r] = raw8(dy + i * lddy, c, WHOLE ? c + 8 : m);
+      if constexpr (ACT != TPO_ACT_NONE) hz[r] = raw8(z + i * ldz, c, WHOLE ? c + 8 : m);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (i0 + r * step >= n) break;
-      if constexpr (ACT != TPO_ACT_NONE)
+      float d[8], v[8];
+      widen8(hd[r], d);
+      if constexpr (ACT != TPO_ACT_NONE) {
+        widen8(hz[r], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[r][j] *= act_grad_f<ACT>(v[r][j]);
-      if (dz) store8(dz + (i0 + r * step) * ldo + c, d[r]);
+        for (int j = 0; j < 8; ++j) d[j] *= act_grad_f<ACT>(v[j]);
+      }
+      if (dz) store8(dz + (i0 + r * step) * ldo + c, d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += d[r][j];
+      for (int j = 0; j < 8; ++j) sum[j] += d[j];
     }
   }
 }
@@ -78,10 +88,11 @@ __device__ __forceinline__ void act_bwd_rows(int64_t first, int64_t n, int64_t s
 // Block (x, y): columns [256 x, 256 x + 256) of the rows 8 y + w + 8 i gridDim.y,
 // warp w.  With `part`, the sums over the block's rows (fp32, before dz is
 // rounded) go to part[y][m].  No atomics: the sums come out the same every time.
-// 4096 x 4096 in 23 us with cold caches (100 MB, 4.4 TB/s), about 10 behind the
-// product that made dy, which leaves it in L2.
+// 4096 x 4096 with GELU's tanh form and db: 18 us with them (67 MB read; with
+// dz written too 100 MB).  64 registers, four blocks per SM: with two of them
+// and four rows in flight, 26 us.
 template <int ACT>
-__global__ void __launch_bounds__(256) act_bwd_kernel(int64_t n, int64_t m, const bf16* dy, int64_t lddy,
+__global__ void __launch_bounds__(256, 4) act_bwd_kernel(int64_t n, int64_t m, const bf16* dy, int64_t lddy,
                                                       const bf16* z, int64_t ldz, bf16* dz, int64_t ldo,
                                                       float* part) {
   __shared__ float red[8][256];
@@ -119,9 +130,9 @@ __global__ void __launch_bounds__(256) gated_act_bwd_kernel(int64_t n, int64_t m
   if (idx >= n * per_row) return;
   const int64_t i = idx / per_row, c = (idx - i * per_row) * 8;
   float d[8], gv[8], uv[8], og[8], ou[8];
-  load8(dh + i * lddh, c, m, d);
-  load8(g + i * ldg, c, m, gv);
-  load8(u + i * ldu, c, m, uv);
+  widen8(raw8(dh + i * lddh, c, m), d);
+  widen8(raw8(g + i * ldg, c, m), gv);
+  widen8(raw8(u + i * ldu, c, m), uv);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     og[j] = d[j] * uv[j] * act_grad_f<ACT>(gv[j]);
@@ -182,10 +193,10 @@ cudaError_t launch_column_sums(const float* part, int parts, int vectors, int64_
 
 cudaError_t launch_act_bwd(int64_t n, int64_t m, int act, const void* dy, int64_t lddy, const void* z, int64_t ldz,
                            void* dz, int64_t ldo, float* part, void* db, cudaStream_t s) {
-  // about eight blocks per SM in all, at most ACT_PARTS over the rows
+  // about eight blocks per SM in all, at most ACT_PARTS over the rows, and two rows for each warp
   const int64_t cols = (m + 255) / 256;
   const int64_t want = std::max<int64_t>(1, 1216 / cols);
-  const int parts = static_cast<int>(std::min<int64_t>({(n + 7) / 8, want, ACT_PARTS}));
+  const int parts = static_cast<int>(std::min(want, act_parts(n)));
   cudaError_t e = with_act(act, [&](auto a) {
     return launch_pdl(act_bwd_kernel<decltype(a)::value>, dim3(static_cast<unsigned>(cols), parts), dim3(256), 0, s, n,
                       m, static_cast<const bf16*>(dy), lddy, static_cast<const bf16*>(z), ldz, static_cast<bf16*>(dz),
