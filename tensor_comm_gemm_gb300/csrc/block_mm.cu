@@ -15,11 +15,11 @@
 //
 // Bound by the tensor cores: 4096^3 with bias, GELU and z takes 80 us by itself
 // (1.71 PFLOP/s, tensor pipe 83 % busy), dx and dw of that layer in one launch
-// 142 us (1.93, 93 %), the gradients of gate and up of 3584 x 8192 from 8192
-// tokens 992 us (1.94, 98 %; 1.7 under the power limit of a long run).  What is lost is the start (the first loads'
-// latency, ~2 us), the last tile's epilogue (~4 us) and the last round's idle
-// pairs, which plan_width trades against the higher cost per column of narrower
-// tiles.  The loads are issued by a converged warp, one elected lane: from a
+// 141 to 145 us (1.9, 93 %), the gradients of gate and up of 3584 x 8192 from 8192
+// tokens 992 to 1043 us (1.85 to 1.94, 98 %; 1.7 under the power limit of a
+// long run).  What is lost is the start (the first loads' latency, ~2 us), the
+// last tile's epilogue (~4 us) and the last round's idle pairs, which plan_width
+// trades against the higher cost per column of narrower tiles.  The loads are issued by a converged warp, one elected lane: from a
 // thread of a diverged warp a TMA load cost 80 to 270 cycles and bounded every
 // shape (4096^3 then 88 us).
 //

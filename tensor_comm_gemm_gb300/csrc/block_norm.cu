@@ -120,8 +120,8 @@ __device__ __forceinline__ float2 group_sums(float a, float b, int group, int tp
   return make_float2(a, b);
 }
 
-// Few rows, short rows and rows of up to 32768 elements: one row per group, read
-// once.  Latency bounds it: one row of 4096 2.9 us in a row of calls, 512 rows
+// Few rows, short rows and long ones (bf16 vectors up to 32768 elements): one
+// row per group, read once.  Latency bounds it: one row of 4096 2.9 us in a row of calls, 512 rows
 // 5.1 us.  The variance is the mean square of the differences from the mean, of
 // values that are already in registers.
 template <class T, class W, int VEC, int NV>
@@ -395,8 +395,9 @@ constexpr int MOST_UNITS = NV * static_cast<int>(sizeof(T)) / 16 + 1;
 constexpr int DEPTH = 2;
 
 // Forward.  FULL: the group's vectors are exactly a row's.  8192 x 8192 bf16 in
-// 46 us, 5.8 TB/s of 6.8; 2000 x 7777 (single elements) in 28 us, where the shared-memory accesses
-// and the three barriers of a row, with 16 warps in step, bound it.
+// 46 us, 5.8 TB/s of 6.8; 2000 x 7777 (single elements) in 28 us, where the
+// shared-memory accesses and the three barriers of a row, with 16 warps in
+// step, bound it.
 template <class T, class W, int VEC, int NV, bool FULL>
 __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int tpr) {
   extern __shared__ __align__(16) uint8_t smem[];  // gamma, beta, the rows in flight, slack to read past them
