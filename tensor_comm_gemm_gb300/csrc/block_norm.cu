@@ -759,6 +759,96 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
   store_sums<VEC, NV>(dg, db, k, tpr, reinterpret_cast<float*>(ring), part);
 }
 
+// ----------------------------------------------------------------- short rows
+
+// Backward for many rows of up to 128 elements: `tpr` lanes a row, a vector
+// each, several rows a warp where they are shorter, and U rows at a time whose
+// loads are all in flight before the first is used.  No barriers; the
+// weights of a lane's columns and their gradients' sums stay in registers.
+// 262144 x 128 bf16 54 us, 95 in the kernel above, whose groups are whole warps;
+// 262144 x 64 30 and 95; fp32 262144 x 128 88 and 125.  (Forward the same
+// arrangement was level with one row per group, 38 and 40 us.)  What is left over the memory's 30 and 15 us are the
+// sums over the lanes, two for each row.
+template <class T, int VEC>
+__device__ __forceinline__ void read_or_zeros(const T* p, bool exists, Num (&v)[NUMS<VEC>]) {
+  Vec<T, VEC> e = {};
+  if (exists) e = load<T, VEC>(p);
+  to_nums<T, VEC>(e, v);
+}
+constexpr int SHORT_THREADS = 640;  // one block per SM: a part of the columns' sums each
+template <class T, class W, int VEC>
+__global__ void __launch_bounds__(SHORT_THREADS, 1) norm_short_bwd_kernel(const NormArgs a, int tpr, float* part) {
+  extern __shared__ __align__(16) uint8_t smem[];  // [groups][2][k] floats
+  constexpr int NN = NUMS<VEC>, U = 2;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int per_warp = 32 / tpr, k = static_cast<int>(a.k), c = (threadIdx.x & (tpr - 1)) * VEC;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (SHORT_THREADS / 32) + (threadIdx.x >> 5);
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (SHORT_THREADS / 32) * per_warp;
+  const bool has_dres = a.dres && a.y;
+  Num g[NN], dg[NN], db[NN];
+  if (a.gamma) read_or_zeros<W, VEC>(static_cast<const W*>(a.gamma) + c, c < k, g);
+#pragma unroll
+  for (int j = 0; j < NN; ++j) dg[j] = db[j] = all(0.0f);
+  const float inv_k = 1.0f / static_cast<float>(k);
+  for (int64_t base = warp * per_warp; base < a.n; base += U * groups) {  // the same rounds for all of the warp
+    const int64_t row = base + (threadIdx.x & 31) / tpr;
+    Num h[U][NN], w[U][NN];
+    float mean[U], rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = row + u * groups;
+      const bool live = r < a.n;
+      read_or_zeros<T, VEC>(static_cast<const T*>(a.x) + r * a.ldx + c, live && c < k, h[u]);
+      read_or_zeros<T, VEC>(static_cast<const T*>(a.dy) + r * a.lddy + c, live && c < k, w[u]);
+      mean[u] = live ? a.mean[r] : 0.0f;
+      rstd[u] = live ? a.rstd[r] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = row + u * groups;
+      const Num minus = all(-mean[u]), scale = all(rstd[u]);
+      Num s1 = all(0.0f), s2 = s1, q[NN];
+      if (has_dres) read_or_zeros<T, VEC>(static_cast<const T*>(a.dres) + r * a.lddres + c, r < a.n && c < k, q);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) {  // where there is no element dy is 0, and xhat adds nothing
+        Num &hv = h[u][j], &wv = w[u][j];
+        hv = mul(add(hv, minus), scale);
+        dg[j] = fma(wv, hv, dg[j]);
+        db[j] = add(db[j], wv);
+        if (a.gamma) wv = mul(wv, g[j]);
+        s1 = add(s1, wv);
+        s2 = fma(wv, hv, s2);
+      }
+      if (!a.y) continue;
+      const Num m1 = all(-lanes_sum(total(s1), tpr) * inv_k), m2 = all(-lanes_sum(total(s2), tpr) * inv_k);
+      if (r >= a.n) continue;
+#pragma unroll
+      for (int j = 0; j < NN; ++j) {
+        const Num d = fma(h[u][j], m2, add(w[u][j], m1));
+        q[j] = has_dres ? fma(d, scale, q[j]) : mul(d, scale);
+      }
+      write_nums<T, VEC>(static_cast<T*>(a.y) + r * a.ldy + c, q, k - c);
+    }
+  }
+  if (!part) return;
+  float* const sums = reinterpret_cast<float*>(smem);
+  float* const mine = sums + static_cast<int>(threadIdx.x / tpr) * 2 * k + c;
+  if (c < k)
+#pragma unroll
+    for (int j = 0; j < NN; ++j) {
+      memcpy(mine + 2 * j, &dg[j], sizeof(Num));
+      memcpy(mine + k + 2 * j, &db[j], sizeof(Num));
+    }
+  __syncthreads();
+  // 2 k columns, up to 256 of them; each the groups' sums in their order
+  for (int o = threadIdx.x; o < 2 * k; o += SHORT_THREADS) {
+    float v = 0.0f;
+    for (int q = 0; q < SHORT_THREADS / tpr; ++q) v += sums[q * 2 * k + o];
+    part[static_cast<int64_t>(blockIdx.x) * 2 * k + o] = v;
+  }
+}
+
 // ------------------------------------------------------------------ long rows
 
 __device__ float block_sum(float v, float* part) {
@@ -1004,7 +1094,15 @@ cudaError_t launch_norm_bwd(const Machine& mc, const NormArgs& a, int dtype, int
       h = share_single(a.k, arrays, sizeof(T), sizeof(W), 1);
     }
     const size_t ring = ring_smem(vec, h, arrays, a.k, sizeof(T), kept(h));
-    if (ring && a.n > 0) {
+    // Rows that would have a vector in at most a quarter of a warp's places, where every block's warps have some
+    const Share few = vec && vecs <= 8 * NV ? share(vecs, 1, 1, 32) : Share{0, 0};
+    if (few.tpr && a.n / (32 / few.tpr) >= static_cast<int64_t>(mc.sms) * (SHORT_THREADS / 32)) {
+      parts = std::min(mc.sms, NORM_PARTS);
+      const size_t smem = static_cast<size_t>(SHORT_THREADS / few.tpr) * 8 * a.k;
+      e = allow_smem(norm_short_bwd_kernel<T, W, V>);
+      if (e == cudaSuccess)
+        e = launch_pdl(norm_short_bwd_kernel<T, W, V>, dim3(parts), dim3(SHORT_THREADS), smem, s, a, few.tpr, part);
+    } else if (ring && a.n > 0) {
       const int64_t sets = (a.n + RING_THREADS / h.tpr - 1) / (RING_THREADS / h.tpr);
       parts = static_cast<int>(std::min<int64_t>({sets, mc.sms, NORM_PARTS}));
       // the slots later hold every group's fp32 sums

@@ -446,6 +446,30 @@ def test_layer_norm_widths(block, n, k, dt, wt):
         R.check(name, v, want[name])
 
 
+# Rows shorter than a warp, many and few of them.
+@pytest.mark.parametrize("n,k", [(22001, 64), (100000, 8), (22000, 40), (11003, 128), (6000, 120), (300, 64), (1, 8)])
+@pytest.mark.parametrize("dt,wt", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("parts", ["all", "plain", "weights"])
+def test_layer_norm_bwd_short_rows(block, n, k, dt, wt, parts):
+    g = gen_of(n + k)
+    x, dy = rnd(g, n, k, dtype=dt, scale=2) + 1.0, rnd(g, n, k, dtype=dt)
+    gamma = rnd(g, k, dtype=wt) if parts != "plain" else None
+    dres = rnd(g, n, k, dtype=dt) if parts == "all" else None
+    f = R.layer_norm(d(x), d(gamma), None, 1e-5)
+    mean, rstd = f["mean"][0].float(), f["rstd"][0].float()
+    want = R.layer_norm_bwd(d(dy), d(x), d(gamma), d(mean), d(rstd), d(dres))
+    dx = Out(n, k, dt, unit=8, extra=1)
+    dg, db = (torch.full((k,), float("nan"), dtype=wt, device="cuda") for _ in range(2))
+    t.tpo_layer_norm_bwd(block, dy, x, gamma, mean, rstd, None if parts == "weights" else dx.t,
+                         dgamma=None if parts == "plain" else dg, dbeta=None if parts == "plain" else db, dres=dres)
+    synced(block)
+    if parts != "weights":
+        R.check("dx", dx.get(), want["dx"])
+    if parts != "plain":
+        R.check("dgamma", dg, want["dgamma"])
+        R.check("dbeta", db, want["dbeta"])
+
+
 @pytest.mark.parametrize("n,k", [(1200, 1003), (400, 5003), (1100, 4096), (2000, 24)])
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_layer_norm_many_rows_in_place(block, n, k, dt):
