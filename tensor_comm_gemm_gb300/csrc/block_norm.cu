@@ -120,67 +120,6 @@ __device__ __forceinline__ float2 group_sums(float a, float b, int group, int tp
   return make_float2(a, b);
 }
 
-// Few rows, short rows and long ones (bf16 vectors up to 32768 elements): one
-// row per group, read once.  Latency bounds it: one row of 4096 2.9 us in a row of calls, 512 rows
-// 5.1 us.  The variance is the mean square of the differences from the mean, of
-// values that are already in registers.
-template <class T, class W, int VEC, int NV>
-__global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int tpr) {
-  __shared__ float red[2][32];
-  grid_dep_launch();
-  grid_dep_wait();
-  const int lane = threadIdx.x & (tpr - 1);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
-  const bool live = row < a.n;
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  Vec<T, VEC> v[NV];
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * tpr) * VEC;
-    if (live && c < a.k) v[i] = load<T, VEC>(x + c);
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (live && (lane + i * tpr) * VEC < a.k)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) s += to_f(v[i].e[j]);
-  const float inv_k = 1.0f / static_cast<float>(a.k);
-  const float mean = row_sum(s, tpr, red[0]) * inv_k;
-  s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (live && (lane + i * tpr) * VEC < a.k)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float d = to_f(v[i].e[j]) - mean;
-        s += d * d;
-      }
-  const float rstd = rsqrtf(row_sum(s, tpr, red[1]) * inv_k + a.eps);
-  if (!live) return;
-  const W *gamma = static_cast<const W*>(a.gamma), *beta = static_cast<const W*>(a.beta);
-  T* y = static_cast<T*>(a.y) + row * a.ldy;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * tpr) * VEC;
-    if (c >= a.k) continue;
-    Vec<T, VEC> o;
-    Vec<W, VEC> g, b;
-    if (gamma) g = load<W, VEC>(gamma + c);
-    if (beta) b = load<W, VEC>(beta + c);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      put(&o.e[j], (to_f(v[i].e[j]) - mean) * rstd * (gamma ? to_f(g.e[j]) : 1.0f) + (beta ? to_f(b.e[j]) : 0.0f));
-    *reinterpret_cast<Vec<T, VEC>*>(y + c) = o;
-  }
-  if (lane == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
-}
-
-// ------------------------------------------------------------------ many rows
-
 // Two values at a time (the packed fp32 operations, which halve the
 // instructions that otherwise bound these kernels).
 struct Num {
@@ -281,6 +220,100 @@ __device__ __forceinline__ void mask_nums(Num (&a)[NUMS<VEC>], int left) {
       if (left <= 0) a[j] = all(0.0f);
   }
 }
+
+// ------------------------------------------------------------ one row per group
+
+// Few rows, short rows and long ones (bf16 vectors up to 32768 elements): one
+// row per group of 2^lg threads, read once.  Latency bounds few rows: one of
+// 4096 2.1 us in a row of calls, 256 3.4 us; instructions bound many short
+// ones: 262144 x 128 36 us.  The variance is the mean square of the
+// differences from the mean, of values that are already in registers.
+template <class T, class W, int VEC, int NV>
+__global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int lg) {
+  __shared__ float red[2][32];
+  constexpr int NN = NUMS<VEC>;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int tpr = 1 << lg, lane = threadIdx.x & (tpr - 1), k = static_cast<int>(a.k);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> lg) + (threadIdx.x >> lg);
+  const bool live = row < a.n;
+  const T* const x = static_cast<const T*>(a.x) + row * a.ldx;
+  T* const y = static_cast<T*>(a.y) + row * a.ldy;
+  const W *const gamma = static_cast<const W*>(a.gamma), *const beta = static_cast<const W*>(a.beta);
+  const float inv_k = 1.0f / static_cast<float>(k);
+  float mean, rstd;
+  if constexpr (VEC > 1) {
+    Vec<T, VEC> e[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * tpr) * VEC;
+      e[i] = {};
+      if (live && c < k) e[i] = load<T, VEC>(x + c);
+    }
+    Num v[NV][NN], s = all(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      to_nums<T, VEC>(e[i], v[i]);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) s = add(s, v[i][j]);
+    }
+    mean = row_sum(total(s), tpr, red[0]) * inv_k;
+    const Num minus = all(-mean);
+    s = all(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < NN; ++j) v[i][j] = add(v[i][j], minus);
+      mask_nums<VEC>(v[i], k - (lane + i * tpr) * VEC);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) s = fma(v[i][j], v[i][j], s);
+    }
+    rstd = rsqrtf(row_sum(total(s), tpr, red[1]) * inv_k + a.eps);
+    if (!live) return;
+    const Num scale = all(rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * tpr) * VEC;
+      if (c >= k) continue;
+      Num g[NN], b[NN];
+      if (gamma) read_nums<W, VEC>(gamma + c, g);
+      if (beta) read_nums<W, VEC>(beta + c, b);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) {
+        v[i][j] = mul(v[i][j], scale);
+        if (gamma) v[i][j] = mul(v[i][j], g[j]);
+        if (beta) v[i][j] = add(v[i][j], b[j]);
+      }
+      write_nums<T, VEC>(y + c, v[i], k - c);
+    }
+  } else {
+    float v[NV], s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = live && lane + i * tpr < k ? to_f(x[lane + i * tpr]) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s += v[i];
+    mean = row_sum(s, tpr, red[0]) * inv_k;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = lane + i * tpr < k ? v[i] - mean : 0.0f;
+      s += v[i] * v[i];
+    }
+    rstd = rsqrtf(row_sum(s, tpr, red[1]) * inv_k + a.eps);
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = lane + i * tpr;
+      if (c < k) put(y + c, v[i] * rstd * (gamma ? to_f(gamma[c]) : 1.0f) + (beta ? to_f(beta[c]) : 0.0f));
+    }
+  }
+  if (lane == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+}
+
+// ------------------------------------------------------------------ many rows
 
 // Asynchronous copy of 16 bytes to shared memory; zeros (and no access to src) if they do not exist.
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool exists) {
@@ -767,7 +800,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
 // weights of a lane's columns and their gradients' sums stay in registers.
 // 262144 x 128 bf16 54 us, 95 in the kernel above, whose groups are whole warps;
 // 262144 x 64 30 and 95; fp32 262144 x 128 88 and 125.  (Forward the same
-// arrangement was level with one row per group, 38 and 40 us.)  What is left over the memory's 30 and 15 us are the
+// arrangement was no faster than one row per group: 38 and 36 us.)  What is left over the memory's 30 and 15 us are the
 // sums over the lanes, two for each row.
 template <class T, int VEC>
 __device__ __forceinline__ void read_or_zeros(const T* p, bool exists, Num (&v)[NUMS<VEC>]) {
@@ -1018,15 +1051,15 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
     const int64_t vecs = vec ? a.k / V : a.k;
     // Rows for most of the SMs' persistent blocks (one of 512 threads per SM):
     // keep rows in flight.  Fewer rows: one row per group, as many threads as it
-    // has vectors (latency).  700 rows of 4096 6.5 us and 6.6, 400 4.7 and 4.1;
-    // 1024 of 8192 10.7 and 15.0, 152 4.8 and 4.2; single elements, 400 of 5003
-    // 8.0 and 11.4.  8192 rows of 8192, 46 us: two blocks per SM, with 64
+    // has vectors (latency).  1024 rows of 4096 7.0 us and 8.3, 400 4.7 and 3.8;
+    // 1024 of 8192 10.7 and 13.1, 152 4.8 and 3.8; single elements, 400 of 5003
+    // 7.9 and 11.3.  8192 rows of 8192, 46 us: two blocks per SM, with 64
     // registers a thread, were a sixth slower than one.
     const Share m = vec ? share_best(vecs, {4, 3, 5}, [](const Share&) { return true; })
                         : share_single(a.k, 1, sizeof(T), sizeof(W), 2);
     const int64_t sets = m.tpr ? (a.n + RING_THREADS / m.tpr - 1) / (RING_THREADS / m.tpr) : 0;
-    // (16384 rows of 256, a third of whose group's places would hold a vector: 6.9 us, 8.5 in flight; of 512, two
-    // thirds: 12.8 and 10.1)
+    // (16384 rows of 256, a third of whose group's places would hold a vector: 6.4 us, 8.4 in flight; of 512, two
+    // thirds: 11.3 and 10.0)
     if (3 * sets >= 2 * static_cast<int64_t>(mc.sms) && (!vec || 2 * vecs >= m.tpr * m.nv)) {
       const size_t smem = ring_smem(vec, m, 1, a.k, sizeof(T), 2 * weight_bytes(static_cast<int>(a.k), sizeof(W)));
       const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sets, mc.sms)));
@@ -1051,11 +1084,13 @@ cudaError_t launch_norm(const Machine& mc, const NormArgs& a, int dtype, int wdt
     const Share h = share(vecs, 1, 8, 512);
     if (!h.tpr) return launch_pdl(norm_long_kernel<T, W>, dim3(static_cast<unsigned>(a.n)), dim3(1024), 0, s, a);
     const int threads = std::max(h.tpr, 128), rows = threads / h.tpr;
+    int lg = 0;
+    while (1 << lg < h.tpr) ++lg;
     const dim3 grid(static_cast<unsigned>((a.n + rows - 1) / rows));
     return with_nv(h.nv, [&](auto nv) {
       constexpr int NV = decltype(nv)::value;
-      if (vec) return launch_pdl(norm_kernel<T, W, V, NV>, grid, dim3(threads), 0, s, a, h.tpr);
-      return launch_pdl(norm_kernel<T, W, 1, NV>, grid, dim3(threads), 0, s, a, h.tpr);
+      if (vec) return launch_pdl(norm_kernel<T, W, V, NV>, grid, dim3(threads), 0, s, a, lg);
+      return launch_pdl(norm_kernel<T, W, 1, NV>, grid, dim3(threads), 0, s, a, lg);
     });
   });
 }
