@@ -49,6 +49,7 @@ struct Args {
   int stages, tmem_cols;
   int act;
   const __nv_bfloat16 *bias, *residual;
+  int bias_vec;                      // the bias is 8-byte aligned
   __nv_bfloat16 *out, *out1, *out2;  // [tokens, features]
   int64_t ldr, ldo, ld1, ld2;
   const float *sx, *sw0, *sw1;
@@ -84,9 +85,9 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&v)[4], int 
     for (int j = 0; j < count; ++j) p[j] = __float2bfloat16_rn(v[j]);
   }
 }
-// Four consecutive bf16 values (0 past `count`), as they lie in memory.
-__device__ __forceinline__ uint2 get4(const __nv_bfloat16* p, int count) {
-  if (count >= 4) return *reinterpret_cast<const uint2*>(p);
+// Four consecutive bf16 values (0 past `count`), as they lie in memory; `vec`: p is 8-byte aligned.
+__device__ __forceinline__ uint2 get4(const __nv_bfloat16* p, int count, bool vec) {
+  if (vec && count >= 4) return *reinterpret_cast<const uint2*>(p);
   uint32_t h[4] = {};
   for (int j = 0; j < 4; ++j)
     if (j < count) h[j] = __bfloat16_as_ushort(p[j]);
@@ -145,8 +146,8 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
   auto fetch = [&](int i) {
     const int col = f0 + i % QUADS * 4, count = p.M - col;
     if (KIND != EPI_LINEAR || i >= tokens * QUADS || count <= 0) return;
-    if (p.bias) pre_b = get4(p.bias + col, count);
-    if (p.residual) pre_r = get4(p.residual + (t0 + i / QUADS) * p.ldr + col, count);
+    if (p.bias) pre_b = get4(p.bias + col, count, p.bias_vec);
+    if (p.residual) pre_r = get4(p.residual + (t0 + i / QUADS) * p.ldr + col, count, true);
   };
   fetch(first);
   bool ok = true;
@@ -429,6 +430,7 @@ cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, cons
   if (!ok) return cudaErrorInvalidValue;
   p.act = e.act;
   p.bias = static_cast<const __nv_bfloat16*>(e.bias);
+  p.bias_vec = reinterpret_cast<uintptr_t>(e.bias) % 8 == 0;  // callers may slice it from a packed vector
   p.residual = static_cast<const __nv_bfloat16*>(e.residual);
   p.out = static_cast<__nv_bfloat16*>(c.out);
   p.out1 = static_cast<__nv_bfloat16*>(e.out1);
