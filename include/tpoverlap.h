@@ -448,11 +448,12 @@ tpo_block* tpo_block_create(int64_t workspace_bytes);
 tpo_status tpo_block_destroy(tpo_block* blk);
 
 /*
- * Options (integers, 0 by default) that choose how the products run; results
- * agree within the rounding of fp32 sums.
- *   "path"   0 by rule; 1 CTA pairs (256-row tiles); 2 clusters that cut the
- *            contraction (for few rows, or small weights' gradients)
- *   "split"  CTAs of such a cluster, 1..8; 0 by rule
+ * Options (integers).  The first two choose how the products run; results agree
+ * within the rounding of fp32 sums.
+ *   "path"   0 (default) by rule; 1 CTA pairs (256-row tiles); 2 clusters that
+ *            cut the contraction (for few rows, or small weights' gradients)
+ *   "split"  CTAs of such a cluster, 1..8; 0 (default) by rule
+ *   "wait_timeout_ms"  bound of every device-side wait, 1..600000 (default 2000)
  * Unknown keys or values out of range: TPO_ERR_INVALID_ARG.
  */
 tpo_status tpo_block_set_opt(tpo_block* blk, const char* key, int64_t value);

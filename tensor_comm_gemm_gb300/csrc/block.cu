@@ -42,12 +42,27 @@ struct tpo_block {
   uint8_t* mem = nullptr;  // error words, then the workspace
   int64_t ws_bytes = 0;
   tpo::Machine machine{};
-  int64_t path = 0, split = 0;  // options
+  int64_t path = 0, split = 0, wait_timeout_ms = 2000;  // options
   uint32_t* err() const { return reinterpret_cast<uint32_t*>(mem); }
+  tpo::Watch watch() const { return {err(), static_cast<unsigned long long>(wait_timeout_ms) * 1000000ull}; }
   uint8_t* ws() const { return mem + kErrBytes; }
 };
 
 namespace {
+
+struct Option {
+  const char* key;
+  int64_t tpo_block::*field;
+  int64_t lo, hi;
+};
+const Option* find_option(const char* key) {
+  static const Option options[] = {{"path", &tpo_block::path, 0, 2},
+                                   {"split", &tpo_block::split, 0, tpo::MAX_SPLIT},
+                                   {"wait_timeout_ms", &tpo_block::wait_timeout_ms, 1, 600000}};
+  for (const Option& o : options)
+    if (std::strcmp(key, o.key) == 0) return &o;
+  return nullptr;
+}
 
 // A matrix argument: `rows` x `cols` elements of `elem` bytes, `ld` elements apart.
 struct Mat {
@@ -137,8 +152,8 @@ tpo_status check_block(const tpo_block* b, int64_t need) {
 cudaError_t run_product(tpo_block* b, const tpo::Product& q, bool fp8, const tpo::Epi& e, cudaStream_t s) {
   tpo::SplitPlan plan;
   if (tpo::use_split(b->machine, q, fp8, e.kind == tpo::EPI_GATED, b->path, b->split, &plan))
-    return tpo::launch_split(q, plan, fp8, e, b->err(), s);
-  return tpo::launch_products(b->machine, &q, 1, fp8, e, b->err(), s);
+    return tpo::launch_split(q, plan, fp8, e, b->watch(), s);
+  return tpo::launch_products(b->machine, &q, 1, fp8, e, b->watch(), s);
 }
 
 // The gradients' products: dx (if wanted) first, then the weights' gradients,
@@ -180,10 +195,10 @@ cudaError_t run_products(tpo_block* b, const tpo::Product* q, int count, int dx,
       rest[left++] = q[i];
       continue;
     }
-    const cudaError_t e = tpo::launch_split(q[i], plans[i], false, tpo::Epi(), b->err(), s);
+    const cudaError_t e = tpo::launch_split(q[i], plans[i], false, tpo::Epi(), b->watch(), s);
     if (e != cudaSuccess) return e;
   }
-  return left ? tpo::launch_products(b->machine, rest, left, false, tpo::Epi(), b->err(), s) : cudaSuccess;
+  return left ? tpo::launch_products(b->machine, rest, left, false, tpo::Epi(), b->watch(), s) : cudaSuccess;
 }
 
 tpo_status launched(cudaError_t e) { return e == cudaSuccess ? TPO_OK : cuda_fail(e, "kernel launch"); }
@@ -278,21 +293,22 @@ tpo_status tpo_block_destroy(tpo_block* b) {
 
 tpo_status tpo_block_set_opt(tpo_block* b, const char* key, int64_t value) {
   if (!key) return fail(TPO_ERR_INVALID_ARG, "NULL option key");
-  const bool path = std::strcmp(key, "path") == 0;
-  if (!path && std::strcmp(key, "split") != 0) return fail(TPO_ERR_INVALID_ARG, "unknown option '%s'", key);
-  if (value < 0 || value > (path ? 2 : 8))
-    return fail(TPO_ERR_INVALID_ARG, "option '%s'=%lld outside [0, %d]", key, (long long)value, path ? 2 : 8);
+  const Option* o = find_option(key);
+  if (!o) return fail(TPO_ERR_INVALID_ARG, "unknown option '%s'", key);
+  if (value < o->lo || value > o->hi)
+    return fail(TPO_ERR_INVALID_ARG, "option '%s'=%lld outside [%lld, %lld]", key, (long long)value, (long long)o->lo,
+                (long long)o->hi);
   if (!b) return fail(TPO_ERR_INVALID_ARG, "NULL block handle");
-  (path ? b->path : b->split) = value;
+  b->*(o->field) = value;
   return TPO_OK;
 }
 
 tpo_status tpo_block_get_opt(tpo_block* b, const char* key, int64_t* value) {
   if (!key || !value) return fail(TPO_ERR_INVALID_ARG, "NULL option key or value");
-  const bool path = std::strcmp(key, "path") == 0;
-  if (!path && std::strcmp(key, "split") != 0) return fail(TPO_ERR_INVALID_ARG, "unknown option '%s'", key);
+  const Option* o = find_option(key);
+  if (!o) return fail(TPO_ERR_INVALID_ARG, "unknown option '%s'", key);
   if (!b) return fail(TPO_ERR_INVALID_ARG, "NULL block handle");
-  *value = path ? b->path : b->split;
+  *value = b->*(o->field);
   return TPO_OK;
 }
 

@@ -43,6 +43,12 @@ struct Epi {
   const float *sx = nullptr, *sw0 = nullptr, *sw1 = nullptr;  // e4m3 scales or NULL
 };
 
+// A launch's error word, and how long a wait of its kernels may last.
+struct Watch {
+  uint32_t* err;
+  unsigned long long limit_ns;
+};
+
 // What the current device holds at a time.
 constexpr int MAX_SPLIT = 8;  // CTAs of a cluster that cuts a contraction
 struct Machine {
@@ -58,7 +64,7 @@ cudaError_t configure_products(Machine* m);
 // 88.2; 1777x4096x2*14336: 256 columns 246 us, 192 253).
 void plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, int* widths, double* us);
 // Runs `count` (1 to 3) products in one launch; more than one take EPI_PLAIN.
-cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, uint32_t* err,
+cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, const Watch& w,
                             cudaStream_t s);
 
 // The same for one product with few rows (M tokens): S CTAs of a cluster cut the contraction.
@@ -72,7 +78,7 @@ cudaError_t configure_split(Machine* m);
 bool use_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t path, int64_t split, SplitPlan* plan);
 // Its plan and modelled time for a bf16 product without an epilogue; false if path or the device rule it out.
 bool split_cost(const Machine& mc, const Product& q, int64_t path, int64_t split, SplitPlan* plan, double* us);
-cudaError_t launch_split(const Product& q, const SplitPlan& plan, bool fp8, const Epi& e, uint32_t* err,
+cudaError_t launch_split(const Product& q, const SplitPlan& plan, bool fp8, const Epi& e, const Watch& w,
                          cudaStream_t s);
 
 struct NormArgs {

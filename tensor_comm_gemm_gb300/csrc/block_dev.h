@@ -8,7 +8,6 @@
 namespace tpo {
 
 constexpr int KB = 128;  // bytes of contraction elements per K block
-constexpr unsigned long long WAIT_NS = 2000000000ull;  // bound of every wait
 
 enum Site : uint32_t { S_EMPTY = 1, S_FULL = 2, S_TEMPTY = 3, S_TFULL = 4, S_DRAIN = 5 };
 
@@ -20,25 +19,25 @@ __device__ inline void give_up(uint32_t* err, uint32_t site) {
   }
 }
 // Bounded wait; with honor_abort a failure recorded by any CTA also ends it.
-__device__ inline bool wait_bar(uint32_t* err, uint32_t bar, uint32_t parity, uint32_t site, bool honor_abort = true) {
+__device__ inline bool wait_bar(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site, bool honor_abort = true) {
   if (mbar_test(bar, parity)) return true;
   const unsigned long long t0 = gtime();
   for (uint32_t i = 1;; ++i) {
     if (mbar_test(bar, parity)) return true;
     if ((i & 15u) == 0u) {
-      if (honor_abort && *reinterpret_cast<volatile uint32_t*>(err) != 0u) return false;
-      if (gtime() - t0 > WAIT_NS) {
-        give_up(err, site);
+      if (honor_abort && *reinterpret_cast<volatile uint32_t*>(w.err) != 0u) return false;
+      if (gtime() - t0 > w.limit_ns) {
+        give_up(w.err, site);
         return false;
       }
     }
   }
 }
 // The same for a converged warp, with one result and every lane ordered after the phase.
-__device__ __forceinline__ bool wait_bar_warp(uint32_t* err, uint32_t bar, uint32_t parity, uint32_t site) {
+__device__ __forceinline__ bool wait_bar_warp(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site) {
   if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait_bar(err, bar, parity, site) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(w, bar, parity, site) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
   if (ok) (void)mbar_test(bar, parity);
   return ok != 0;

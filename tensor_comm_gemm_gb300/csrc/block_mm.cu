@@ -23,8 +23,9 @@
 // thread of a diverged warp a TMA load cost 80 to 270 cycles and bounded every
 // shape (4096^3 then 88 us).
 //
-// Every wait is bounded by the device global timer; on expiry the waiting
-// thread records it in the handle's error word and the CTA winds down.
+// Every wait is bounded by the device global timer (option wait_timeout_ms); on
+// expiry the waiting thread records it in the handle's error word and the CTA
+// winds down.
 
 #include <algorithm>
 #include <cstring>
@@ -86,7 +87,7 @@ struct Args {
   int bias_vec;         // the bias is 16-byte aligned
   int has1;             // y1 (and for EPI_GATED y2) are stored
   const float *sx, *sw0, *sw1;
-  uint32_t* err;
+  Watch watch;
 };
 
 struct TileAt {
@@ -127,7 +128,7 @@ __device__ __forceinline__ bool load_tile(const Args& p, Ring& g, uint32_t sbase
     [[maybe_unused]] const uint64_t map_a = reinterpret_cast<uint64_t>(ma), map_b = reinterpret_cast<uint64_t>(mb);
     int kx = 0;
     for (int kk = 0; kk < kb_seg; ++kk, kx += KEL) {
-      if (!wait_bar_warp(p.err, empty0 + 8u * g.stage, g.phase ^ 1u, S_EMPTY)) return false;
+      if (!wait_bar_warp(p.watch, empty0 + 8u * g.stage, g.phase ^ 1u, S_EMPTY)) return false;
       const uint32_t sa = sbase + g.stage * g.bytes, sb = sa + A_BYTES;
       Box x[NA + NB];
       if constexpr (AMN) {
@@ -189,7 +190,7 @@ __device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_
   if (!ok && (threadIdx.x & 31) == 0) {  // loads in flight must land before the CTA gives up its shared memory
     if (rank == 0) {
       for (uint32_t j = g.armed > g.stages ? g.armed - g.stages : 0u; j < g.armed; ++j)
-        wait_bar(p.err, full0 + 8u * (j % g.stages), (j / g.stages) & 1u, S_DRAIN, false);
+        wait_bar(p.watch, full0 + 8u * (j % g.stages), (j / g.stages) & 1u, S_DRAIN, false);
     } else if (g.armed > 0) {  // they signal the even CTA's barriers
       const unsigned long long t0 = gtime();
       while (gtime() - t0 < 200000ull) __nanosleep(1000);
@@ -213,14 +214,14 @@ __device__ void mma_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t 
     const uint64_t da0 = a_mn ? desc_mn(sbase) : smem_desc_sw128(sbase);
     const uint64_t db0 = b_mn ? desc_mn(sbase + A_BYTES) : smem_desc_sw128(sbase + A_BYTES);
     const uint64_t step_a = a_mn ? 128u : 2u, step_b = b_mn ? 128u : 2u;
-    if (!wait_bar_warp(p.err, tempty0 + 8u * acc, ((ul >> 1) & 1u) ^ 1u, S_TEMPTY)) {
+    if (!wait_bar_warp(p.watch, tempty0 + 8u * acc, ((ul >> 1) & 1u) ^ 1u, S_TEMPTY)) {
       ok = false;
       break;
     }
     tc_fence_after();
     const uint32_t d = tmem + acc * TN;
     for (int i = 0; i < kb; ++i) {
-      if (!wait_bar_warp(p.err, full0 + 8u * stage, phase, S_FULL)) {
+      if (!wait_bar_warp(p.watch, full0 + 8u * stage, phase, S_FULL)) {
         ok = false;
         break;
       }
@@ -235,7 +236,7 @@ __device__ void mma_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t 
   }
   if (!ok) {  // every MMA issued must complete before tensor memory is freed
     mma_commit_local_cg<2>(drain);
-    if ((threadIdx.x & 31) == 0) wait_bar(p.err, drain, 0u, S_DRAIN, false);
+    if ((threadIdx.x & 31) == 0) wait_bar(p.watch, drain, 0u, S_DRAIN, false);
     __syncwarp();
   }
 }
@@ -328,7 +329,7 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
     const Prob& q = p.q[T.q];
     const uint32_t acc = ul & 1u;
     if (wide) {
-      if (!wait_bar_warp(p.err, tfull0 + 8u * acc, (ul >> 1) & 1u, S_TFULL)) break;
+      if (!wait_bar_warp(p.watch, tfull0 + 8u * acc, (ul >> 1) & 1u, S_TFULL)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * TN;
       const int oy = T.row + TM * static_cast<int>(rank) + quad * 32, nw = (q.w + 63) / 64;
@@ -391,7 +392,7 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
         load_row(p.residual + row * p.ldr + ox, res);
     };
     fetch_residual(half);
-    if (!wait_bar_warp(p.err, tfull0 + 8u * acc, (ul >> 1) & 1u, S_TFULL)) break;
+    if (!wait_bar_warp(p.watch, tfull0 + 8u * acc, (ul >> 1) & 1u, S_TFULL)) break;
     tc_fence_after();
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * TN;
     const int last = (nch - 1 - half) / 2 * 2 + half;  // this warp's last chunk (if it has any)
@@ -644,7 +645,7 @@ cudaError_t configure_products(Machine* m) {
   return e;
 }
 
-cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, uint32_t* err,
+cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, const Watch& w,
                             cudaStream_t s) {
   Args p;
   std::memset(&p, 0, sizeof(p));
@@ -686,7 +687,7 @@ cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool
   p.residual = static_cast<const __nv_bfloat16*>(e.residual);
   p.ldr = e.ldr;
   p.sx = e.sx, p.sw0 = e.sw0, p.sw1 = e.sw1;
-  p.err = err;
+  p.watch = w;
   const int pairs = std::min(mc.pairs, p.total);
   switch (e.kind) {
     case EPI_LINEAR: return fp8 ? launch_pairs<EPI_LINEAR, true>(p, pairs, s) : launch_pairs<EPI_LINEAR, false>(p, pairs, s);

@@ -53,7 +53,7 @@ struct Args {
   __nv_bfloat16 *out, *out1, *out2;  // [tokens, features]
   int64_t ldr, ldo, ld1, ld2;
   const float *sx, *sw0, *sw1;
-  uint32_t* err;
+  Watch watch;
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     auto run = [&](auto boxes) {
       int seg = lo >= static_cast<int>(kb_seg) ? 1 : 0, kk = lo - seg * static_cast<int>(kb_seg);
       for (int i = lo; i < hi; ++i) {
-        if (!wait_bar_warp(p.err, empty0 + 8u * stage, phase ^ 1u, S_EMPTY)) {
+        if (!wait_bar_warp(p.watch, empty0 + 8u * stage, phase ^ 1u, S_EMPTY)) {
           ok = false;
           return;
         }
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
       });
     if (!ok && lane == 0)  // loads in flight must land before the CTA gives up its shared memory
       for (uint32_t j = armed > stages ? armed - stages : 0u; j < armed; ++j)
-        wait_bar(p.err, full0 + 8u * (j % stages), (j / stages) & 1u, S_DRAIN, false);
+        wait_bar(p.watch, full0 + 8u * (j % stages), (j / stages) & 1u, S_DRAIN, false);
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = idesc_n(make_idesc(FP8, FT), p.nt) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     const uint64_t step_a = p.a_mn ? 128u : 2u, step_b = p.b_mn ? 128u : 2u;
     uint32_t stage = 0, phase = 0;
     for (int i = lo; i < hi; ++i) {
-      if (!wait_bar_warp(p.err, full0 + 8u * stage, phase, S_FULL)) {
+      if (!wait_bar_warp(p.watch, full0 + 8u * stage, phase, S_FULL)) {
         ok = false;
         break;
       }
@@ -223,12 +223,12 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     }
     // also after a failure: every MMA issued must complete before tensor memory is freed
     mma_commit_cg<1>(tfull);
-    if (!wait_bar_warp(p.err, tfull, 0, S_TFULL) && lane == 0) wait_bar(p.err, tfull, 0, S_DRAIN, false);
+    if (!wait_bar_warp(p.watch, tfull, 0, S_TFULL) && lane == 0) wait_bar(p.watch, tfull, 0, S_DRAIN, false);
     __syncwarp();
   }
   // ---- the accumulator, [token][feature] in fp32, over the pipeline's memory
   if (warp >= 4) {
-    if (wait_bar_warp(p.err, tfull, 0, S_TFULL)) {
+    if (wait_bar_warp(p.watch, tfull, 0, S_TFULL)) {
       tc_fence_after();
       const int quad = warp & 3;
       for (int c = 0; c < tokens; c += 32) {
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
   // ---- sums over the cluster and the epilogue: four features of one token at a time
   const float s0 = FP8 ? __ldg(p.sx) * __ldg(p.sw0) : 1.0f;
   const float s1 = FP8 && KIND == EPI_GATED ? __ldg(p.sx) * __ldg(p.sw1) : 1.0f;
-  const bool good = *reinterpret_cast<volatile uint32_t*>(p.err) == 0u;
+  const bool good = *reinterpret_cast<volatile uint32_t*>(p.watch.err) == 0u;
   for (int i = first; good && i < tokens * QUADS; i += S * THREADS) {
     const int tok = i / QUADS, fq = i % QUADS * 4;
     const int64_t row = t0 + tok;
@@ -405,7 +405,7 @@ bool split_cost(const Machine& mc, const Product& q, int64_t path, int64_t split
   return path == 2 || (path == 0 && fits);
 }
 
-cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, const Epi& e, uint32_t* err,
+cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, const Epi& e, const Watch& w,
                          cudaStream_t s) {
   Args p;
   std::memset(&p, 0, sizeof(p));
@@ -437,7 +437,7 @@ cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, cons
   p.out2 = static_cast<__nv_bfloat16*>(e.out2);
   p.ldr = e.ldr, p.ldo = c.ldo, p.ld1 = e.ld1, p.ld2 = e.ld2;
   p.sx = e.sx, p.sw0 = e.sw0, p.sw1 = e.sw1;
-  p.err = err;
+  p.watch = w;
   const int tiles = p.tiles_f * ceil_div(c.M, p.nt);
   const int smem = p.stages * (A_BYTES + p.b_bytes) + SMEM_TAIL;
   switch (e.kind) {
