@@ -9,6 +9,9 @@ namespace tpo {
 
 constexpr int KB = 128;  // bytes of contraction elements per K block
 
+// Bound of the waits of a CTA that gave up, for what it has in flight.
+constexpr unsigned long long DRAIN_NS = 2000000000ull;
+
 enum Site : uint32_t { S_EMPTY = 1, S_FULL = 2, S_TEMPTY = 3, S_TFULL = 4, S_DRAIN = 5 };
 
 __device__ inline void give_up(uint32_t* err, uint32_t site) {
@@ -18,15 +21,17 @@ __device__ inline void give_up(uint32_t* err, uint32_t site) {
     __threadfence();
   }
 }
-// Bounded wait; with honor_abort a failure recorded by any CTA also ends it.
+// Bounded wait; with honor_abort a failure recorded by any CTA also ends it,
+// without it (draining) the limit is DRAIN_NS.
 __device__ inline bool wait_bar(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site, bool honor_abort = true) {
   if (mbar_test(bar, parity)) return true;
+  const unsigned long long limit = honor_abort ? w.limit_ns : DRAIN_NS;
   const unsigned long long t0 = gtime();
   for (uint32_t i = 1;; ++i) {
     if (mbar_test(bar, parity)) return true;
     if ((i & 15u) == 0u) {
       if (honor_abort && *reinterpret_cast<volatile uint32_t*>(w.err) != 0u) return false;
-      if (gtime() - t0 > w.limit_ns) {
+      if (gtime() - t0 > limit) {
         give_up(w.err, site);
         return false;
       }

@@ -57,6 +57,9 @@ static_assert(OFF_BARS == STAGES_WIDE + EPI_WARPS_N * 2 * 2 * BOX, "one layout b
 constexpr int WIDE_KB = 16;  // K blocks of a product up to which its launch takes the wide boxes
 constexpr int N_BARS = 2 * MAX_STAGES + 2 + 2 + 1;
 constexpr int OFF_TMEM = OFF_BARS + 8 * N_BARS;
+// Behind the tensor memory's address: whether a wait of the pair ran out, and
+// (in the even CTA) the K blocks that it and its peer have loaded.
+constexpr int OFF_FAILED = OFF_TMEM + 4, OFF_LOADED = OFF_TMEM + 8;
 constexpr int SMEM = OFF_TMEM + 16 + 1024;  // and the slack to align the base
 static_assert(SMEM <= 232448, "shared memory of one CTA");
 
@@ -151,6 +154,20 @@ __device__ __forceinline__ bool load_tile(const Args& p, Ring& g, uint32_t sbase
   return true;
 }
 
+// Bytes that one CTA loads for a K block.
+template <int KIND>
+__device__ __forceinline__ uint32_t kblock_bytes(const Prob& q) {
+  if constexpr (KIND == EPI_GATED) return A_BYTES + q.w * KB;
+  const int hb = q.w / 2;
+  return A_BYTES + (q.b_mn ? (hb + 63) / 64 * 8192u : static_cast<uint32_t>(hb) * KB);
+}
+
+// Tells both CTAs of the pair that a wait ran out (one thread).
+__device__ __forceinline__ void mark_failed(uint32_t sbase) {
+  st_shared_cluster_u32(map_to_rank(sbase + OFF_FAILED, 0), 1u);
+  st_shared_cluster_u32(map_to_rank(sbase + OFF_FAILED, 1), 1u);
+}
+
 // The load warp, converged (one elected lane issues each stage's loads).
 template <int KIND, bool FP8>
 __device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_t empty0, uint32_t rank, int pair,
@@ -164,12 +181,12 @@ __device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_
     const int a0 = T.row + TM * static_cast<int>(rank);
     if constexpr (KIND == EPI_GATED) {
       // the even CTA holds the tile's rows of wg, the odd one those of wu
-      ok = load_tile<FP8, false, 0>(p, g, sbase, full0, full_lead, empty0, lead, 2u * (A_BYTES + q.w * KB), &q.a[0],
+      ok = load_tile<FP8, false, 0>(p, g, sbase, full0, full_lead, empty0, lead, 2u * kblock_bytes<KIND>(q), &q.a[0],
                                     &q.b[rank], 1, q.kb_seg, a0, T.col);
     } else {
       const int hb = q.w / 2, b0 = T.col + hb * static_cast<int>(rank), terms = q.terms, kbs = q.kb_seg;
       const int boxes = q.b_mn ? (hb + 63) / 64 : 0;
-      const uint32_t bytes = 2u * (A_BYTES + (boxes ? boxes * 8192u : static_cast<uint32_t>(hb) * KB));
+      const uint32_t bytes = 2u * kblock_bytes<KIND>(q);
       if constexpr (KIND == EPI_PLAIN) {
         if (q.a_mn)
           ok = boxes == 2 ? load_tile<FP8, true, 2>(p, g, sbase, full0, full_lead, empty0, lead, bytes, q.a, q.b,
@@ -187,16 +204,39 @@ __device__ void load_role(const Args& p, uint32_t sbase, uint32_t full0, uint32_
       }
     }
   }
-  if (!ok && (threadIdx.x & 31) == 0) {  // loads in flight must land before the CTA gives up its shared memory
-    if (rank == 0) {
-      for (uint32_t j = g.armed > g.stages ? g.armed - g.stages : 0u; j < g.armed; ++j)
-        wait_bar(p.watch, full0 + 8u * (j % g.stages), (j / g.stages) & 1u, S_DRAIN, false);
-    } else if (g.armed > 0) {  // they signal the even CTA's barriers
-      const unsigned long long t0 = gtime();
-      while (gtime() - t0 < 200000ull) __nanosleep(1000);
-    }
+  if ((threadIdx.x & 31) == 0) {
+    st_shared_cluster_u32(map_to_rank(sbase + OFF_LOADED + 4u * rank, 0), g.armed);
+    if (!ok) mark_failed(sbase);
   }
   __syncwarp();
+}
+
+// After a wait of the pair ran out, in one thread of the even CTA, whose
+// barriers all loads of the pair signal: waits until those in flight have
+// landed, before either CTA gives up its shared memory.  Use j of the ring
+// completes with its own arming and the bytes of both CTAs; where only one of
+// them came to load K block j, the other's part is made up here.  (A K block is
+// loaded once the MMAs have consumed the one that was in its stage, so only the
+// latest `stages` can be in flight.)
+template <int KIND>
+__device__ __noinline__ void drain_loads(const Args& p, uint32_t sbase, uint32_t full0, int pair, int pairs) {
+  const uint32_t own = ld_shared_u32(sbase + OFF_LOADED), peer = ld_shared_u32(sbase + OFF_LOADED + 4u);
+  const uint32_t both = min(own, peer), end = max(own, peer), first = end > p.stages ? end - p.stages : 0u;
+  uint32_t at = 0;  // the tile's first K block in the pair's sequence
+  for (int t = pair; t < p.total && at < end; t += pairs) {
+    const Prob& q = p.q[tile_at(p, t).q];
+    const uint32_t next = at + static_cast<uint32_t>(q.kb), bytes = kblock_bytes<KIND>(q);
+    for (uint32_t j = max(max(at, both), first); j < min(next, end); ++j) {
+      const uint32_t bar = full0 + 8u * (j % p.stages);
+      if (j < own)
+        mbar_complete_tx(bar, bytes);  // armed for both, and the peer's will not come
+      else
+        mbar_expect_tx(bar, bytes);    // the peer's alone, not armed
+    }
+    at = next;
+  }
+  for (uint32_t j = first; j < end; ++j)
+    wait_bar(p.watch, full0 + 8u * (j % p.stages), (j / p.stages) & 1u, S_DRAIN, false);
 }
 
 template <int KIND, bool FP8>
@@ -234,11 +274,15 @@ __device__ void mma_role(const Args& p, uint32_t sbase, uint32_t tmem, uint32_t 
     if (!ok) break;
     mma_commit_cg<2>(tfull0 + 8u * acc);
   }
-  if (!ok) {  // every MMA issued must complete before tensor memory is freed
-    mma_commit_local_cg<2>(drain);
-    if ((threadIdx.x & 31) == 0) wait_bar(p.watch, drain, 0u, S_DRAIN, false);
-    __syncwarp();
+  // Every MMA issued must complete before tensor memory is freed, also where
+  // the epilogue has given up and nobody waits for the last tile.  (The arrival
+  // in the odd CTA is the last of those from here.)
+  mma_commit_cg<2>(drain);
+  if ((threadIdx.x & 31) == 0) {
+    wait_bar(p.watch, drain, 0u, S_DRAIN, false);
+    if (!ok) mark_failed(sbase);
   }
+  __syncwarp();
 }
 
 // 32 consecutive bf16 values as they lie in memory, and their addition.
@@ -483,6 +527,7 @@ __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_const
       mbar_init(tempty0 + 8u * a, 2 * EPI_WARPS_N);
     }
     mbar_init(drain, 1);
+    st_shared_u32(sbase + OFF_FAILED, 0u);
     fence_barrier_init();
     for (int i = 0; i < p.count; ++i) {
       tma_prefetch_map(&p.q[i].a[0]);
@@ -511,7 +556,14 @@ __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // neither CTA leaves while its peer may still use it
+  if (ld_shared_u32(sbase + OFF_FAILED)) {  // the same in both CTAs: written before the barrier only
+    if (rank == 0 && threadIdx.x == 0) drain_loads<KIND>(p, sbase, full0, pair, pairs);
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == 1) {
+    if (rank == 1 && (threadIdx.x & 31) == 0) wait_bar(p.watch, drain, 0u, S_DRAIN, false);
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc_cg<2>(tmem, 2 * TN);
   }

@@ -150,7 +150,6 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     if (p.residual) pre_r = get4(p.residual + (t0 + i / QUADS) * p.ldr + col, count, true);
   };
   fetch(first);
-  bool ok = true;
   if (warp == 0) {
     // the load warp, converged
     const uint32_t stages = static_cast<uint32_t>(p.stages), kb_seg = static_cast<uint32_t>(p.kb_seg);
@@ -159,10 +158,7 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     auto run = [&](auto boxes) {
       int seg = lo >= static_cast<int>(kb_seg) ? 1 : 0, kk = lo - seg * static_cast<int>(kb_seg);
       for (int i = lo; i < hi; ++i) {
-        if (!wait_bar_warp(p.watch, empty0 + 8u * stage, phase ^ 1u, S_EMPTY)) {
-          ok = false;
-          return;
-        }
+        if (!wait_bar_warp(p.watch, empty0 + 8u * stage, phase ^ 1u, S_EMPTY)) return;
         const uint32_t fb = full0 + 8u * stage;
         boxes(fb, sbase + stage * stage_bytes, seg, kk * KEL);
         ++armed;
@@ -200,7 +196,8 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
         const Box x[2] = {{sa, ma + seg * kMap, kx, f0}, {sa + A_BYTES, mb + seg * kMap, kx, t0}};
         stage_loads<1>(1u, fb, stage_bytes, fb, x);
       });
-    if (!ok && lane == 0)  // loads in flight must land before the CTA gives up its shared memory
+    // whatever became of the MMAs, the loads must land before the CTA gives up its shared memory
+    if (lane == 0)
       for (uint32_t j = armed > stages ? armed - stages : 0u; j < armed; ++j)
         wait_bar(p.watch, full0 + 8u * (j % stages), (j / stages) & 1u, S_DRAIN, false);
     __syncwarp();
@@ -211,10 +208,7 @@ __global__ void __launch_bounds__(THREADS, 2) split_kernel(const __grid_constant
     const uint64_t step_a = p.a_mn ? 128u : 2u, step_b = p.b_mn ? 128u : 2u;
     uint32_t stage = 0, phase = 0;
     for (int i = lo; i < hi; ++i) {
-      if (!wait_bar_warp(p.watch, full0 + 8u * stage, phase, S_FULL)) {
-        ok = false;
-        break;
-      }
+      if (!wait_bar_warp(p.watch, full0 + 8u * stage, phase, S_FULL)) break;
       tc_fence_after();
       const uint64_t off = static_cast<uint64_t>(stage_bytes >> 4) * stage;
       mma_kblock<1, FP8>(tmem, da0 + off, db0 + off, idesc, i > lo ? 1u : 0u, step_a, step_b);
