@@ -509,7 +509,7 @@ tpo_status tpo_linear(tpo_block* blk, int64_t n, int64_t k, int64_t m, int dtype
  * Gradient of tpo_linear (bf16):  dz = dy act'(z);
  *   dx [n, k] = dz w,  dw [m, k] = dz^T x,  db [m] = sum over rows of dz
  * z is the forward call's (TPO_ACT_NONE: NULL).  dx, dw and db may each be
- * NULL (w is then not needed for dx, x not for dw).  The residual's gradient
+ * NULL; without dx, w may be NULL, and without dw, x.  The residual's gradient
  * is dy itself.
  */
 tpo_status tpo_linear_bwd(tpo_block* blk, int64_t n, int64_t k, int64_t m, int act, const void* dy, int64_t lddy,
@@ -531,7 +531,8 @@ tpo_status tpo_gated(tpo_block* blk, int64_t n, int64_t k, int64_t m, int dtype,
 /*
  * Gradient of tpo_gated (bf16):  dg = dh u act'(g),  du = dh act(g);
  *   dx [n, k] = dg wg + du wu,  dwg [m, k] = dg^T x,  dwu [m, k] = du^T x
- * dx may be NULL, and dwg and dwu together.
+ * dx may be NULL (wg and wu may then be, too), and dwg and dwu together (x may
+ * then be, too).
  */
 tpo_status tpo_gated_bwd(tpo_block* blk, int64_t n, int64_t k, int64_t m, int act, const void* dh, int64_t lddh,
                          const void* g, int64_t ldg, const void* u, int64_t ldu, const void* x, int64_t ldx,

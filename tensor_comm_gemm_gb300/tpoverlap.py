@@ -467,7 +467,8 @@ def tpo_gated(block: int, x, wg, wu, h, act: int = TPO_ACT_SILU, g=None, u=None,
 def tpo_gated_bwd(block: int, dh, g, u, x, wg, wu, dx=None, dwg=None, dwu=None, act: int = TPO_ACT_SILU,
                   stream=None) -> None:
     n, m = _shape2("dh", dh)
-    k = _shape2("x", x)[1]
+    wide = next((t for t in (x, wg, wu, dx, dwg, dwu) if t is not None), None)
+    k = 1 if wide is None else _shape2("x, wg, wu, dx, dwg and dwu", wide)[1]
     args = []
     for name, t, rows, cols in (("dh", dh, n, m), ("g", g, n, m), ("u", u, n, m), ("x", x, n, k), ("wg", wg, m, k),
                                 ("wu", wu, m, k), ("dx", dx, n, k), ("dwg", dwg, m, k), ("dwu", dwu, m, k)):
