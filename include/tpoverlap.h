@@ -419,7 +419,8 @@ typedef struct tpo_block tpo_block; /* opaque */
 
 /* Activations.  GELU is x Phi(x), GELU_TANH its tanh form
  * x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))), SILU x / (1 + exp(-x)).
- * RELU's derivative at 0 is 0. */
+ * RELU's derivative at 0 is 0.  At NaN every activation is NaN, and so is every
+ * derivative but NONE's. */
 typedef enum { TPO_ACT_NONE = 0, TPO_ACT_RELU = 1, TPO_ACT_GELU = 2, TPO_ACT_GELU_TANH = 3, TPO_ACT_SILU = 4 } tpo_act;
 
 /* The block operators, as tpo_block_workspace names them. */
