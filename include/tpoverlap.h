@@ -411,7 +411,10 @@ tpo_status tpo_ag_gemm_noalloc(int tp, int64_t n, int64_t k, int64_t m, int dtyp
  * its own type.  The backward products take the gradient of the
  * pre-activation as a matrix operand, so it is rounded to bf16 in between (the
  * gradient of the bias is summed before that rounding).  No call uses atomics
- * on data: the same inputs, sizes and options give the same bits.
+ * on data: calls with the same values, sizes, pitches, address alignments and
+ * options on the same kind of device give the same bits.  (Pitches, alignments
+ * and the number of SMs enter the choice of kernel and with it the order in
+ * which fp32 terms are added.)
  * NaN and infinities in the inputs spread as the formulas say, and only there:
  * a row of the output never sees another row's input.
  */
