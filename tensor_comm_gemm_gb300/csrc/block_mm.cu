@@ -699,6 +699,14 @@ cudaError_t configure_products(Machine* m) {
 
 cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, const Watch& w,
                             cudaStream_t s) {
+  // The forms of operands that the kernel has: with an epilogue, both K-major and one term; without, bf16 and B MN-major.
+  const bool plain = e.kind == EPI_PLAIN;
+  if (count > 1 && !plain) return cudaErrorInvalidValue;
+  for (int i = 0; i < count; ++i)
+    for (int t = 0; t < (e.kind == EPI_GATED ? 2 : q[i].terms); ++t)
+      if (q[i].b[t].mn_major != plain || (plain ? fp8 || q[i].a[t].mn_major != q[i].a[0].mn_major
+                                                : q[i].a[0].mn_major || q[i].terms != 1))
+        return cudaErrorInvalidValue;
   Args p;
   std::memset(&p, 0, sizeof(p));
   p.count = count;

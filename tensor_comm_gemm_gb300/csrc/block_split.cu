@@ -401,9 +401,16 @@ bool split_cost(const Machine& mc, const Product& q, int64_t path, int64_t split
 
 cudaError_t launch_split(const Product& c, const SplitPlan& plan, bool fp8, const Epi& e, const Watch& w,
                          cudaStream_t s) {
+  const bool gated = e.kind == EPI_GATED;
+  // The forms of operands that the kernel has: features may be MN-major by themselves, tokens only with them, and
+  // the gated form has both K-major.
+  for (int t = 0; t < (gated ? 2 : c.terms); ++t)
+    if (c.b[t].mn_major != c.b[0].mn_major || (t < c.terms && c.a[t].mn_major != c.a[0].mn_major))
+      return cudaErrorInvalidValue;
+  if ((c.a[0].mn_major && !c.b[0].mn_major) || (c.b[0].mn_major && (gated || fp8)) || (gated && c.terms != 1))
+    return cudaErrorInvalidValue;
   Args p;
   std::memset(&p, 0, sizeof(p));
-  const bool gated = e.kind == EPI_GATED;
   // the roles are swapped: B's rows (features) are the MMA's M, A's rows (tokens) its N
   p.M = static_cast<int>(c.N), p.N = static_cast<int>(c.M);
   p.tiles_f = ceil_div(c.N, gated ? FT / 2 : FT);
