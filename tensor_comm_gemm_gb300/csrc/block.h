@@ -60,8 +60,9 @@ cudaError_t configure_products(Machine* m);
 // The column tiles' width of each product of a launch (all after the first are
 // of one shape), and the launch's modelled time.  Narrower tiles than the
 // widest cost more per column, so they are taken where they fill a last round
-// or spread few tiles over the pairs (4096^3: 224 columns 84.8 us, 256 86.7, 192
-// 88.2; 1777x4096x2*14336: 256 columns 246 us, 192 253).
+// or spread few tiles over the pairs (in rows of calls: 4096^3 without an
+// epilogue 86.3 us with 224 columns, 87.5 with 256, 90.2 with 192;
+// 1777x4096x2*14336 249 us with 256, 260 with 192).
 void plan_width(const Machine& mc, const Product* q, int count, bool fp8, bool gated, int* widths, double* us);
 // Runs `count` (1 to 3) products in one launch; more than one take EPI_PLAIN.
 cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, const Watch& w,

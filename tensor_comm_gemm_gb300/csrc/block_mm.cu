@@ -13,15 +13,17 @@
 // the 128-byte swizzle, as [rows][64 contraction elements] or as blocks of
 // [64 contraction rows][64 elements], and the MMA's descriptors say which.
 //
-// Bound by the tensor cores: 4096^3 with bias, GELU and z takes 80 us by itself
-// (1.71 PFLOP/s, tensor pipe 83 % busy), dx and dw of that layer in one launch
-// 141 to 145 us (1.9, 93 %), the gradients of gate and up of 3584 x 8192 from 8192
-// tokens 992 to 1043 us (1.85 to 1.94, 98 %; 1.7 under the power limit of a
-// long run).  What is lost is the start (the first loads' latency, ~2 us), the
-// last tile's epilogue (~4 us) and the last round's idle pairs, which plan_width
-// trades against the higher cost per column of narrower tiles.  The loads are issued by a converged warp, one elected lane: from a
-// thread of a diverged warp a TMA load cost 80 to 270 cycles and bounded every
-// shape (4096^3 then 88 us).
+// Bound by the tensor cores, and in a row of calls by the power limit, which
+// lowers the clock.  4096^3 takes 86 us in a row of calls (1.60 PFLOP/s), with
+// bias, GELU and z 92 there and 77 to 85 as a single launch under the profiler
+// (tensor pipe 84 % busy); dx and dw of that layer in one launch 163 in a row
+// (1.69) and 140 to 148 single (93 %); the gradients of gate and up of
+// 3584 x 8192 from 8192 tokens 992 to 1043 single (1.85 to 1.94, 98 %; 1.7 in a
+// row).  What is lost is the start (the first loads' latency, ~2 us), the last
+// tile's epilogue (~4 us) and the last round's idle pairs, which plan_width
+// trades against the higher cost per column of narrower tiles.  The loads are
+// issued by a converged warp, one elected lane: from a thread of a diverged warp
+// a TMA load cost 80 to 270 cycles and bounded every shape.
 //
 // Every wait is bounded by the device global timer (option wait_timeout_ms); on
 // expiry the waiting thread records it in the handle's error word and the CTA
@@ -50,7 +52,7 @@ constexpr int BOX = 32 * CHUNK * 2;         // bytes of one output box: 32 rows 
 // The plain epilogue of products with few K blocks (weight gradients of few
 // tokens), which the stores bound, takes 64 columns at a time, boxes of
 // 128-byte rows, and gives a pipeline stage up for them: 4096x4096 from 16
-// tokens 13.9 us, 15.7 with the narrow boxes; with 64 K blocks 79 and 76.
+// tokens 12.4 us, 12.7 with the narrow boxes; with 64 K blocks 91.4 and 90.0.
 constexpr int STAGES_NARROW = 196608, STAGES_WIDE = 163840;  // bytes of pipeline stages
 constexpr int OFF_BARS = STAGES_NARROW + EPI_WARPS_N * 2 * BOX;  // behind the staging boxes, two a warp
 static_assert(OFF_BARS == STAGES_WIDE + EPI_WARPS_N * 2 * 2 * BOX, "one layout behind the stages and boxes");
@@ -505,8 +507,8 @@ __device__ void epilogue_role(const Args& p, uint32_t sbase, uint32_t tmem, uint
 
 // Grid: two CTAs (a cluster) per pair, at most as many pairs as the device
 // holds at once; pair p takes the tiles p, p + pairs, ... (claims from a
-// counter kept late pairs busier but cost each tile a round trip: 4096^3 89 us,
-// 85 without).
+// counter kept late pairs busier but cost each tile a round trip: 4096^3 took
+// 4 us longer with them).
 template <int KIND, bool FP8>
 __global__ void __launch_bounds__(THREADS, 1) products_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -699,7 +701,8 @@ cudaError_t configure_products(Machine* m) {
 
 cudaError_t launch_products(const Machine& mc, const Product* q, int count, bool fp8, const Epi& e, const Watch& w,
                             cudaStream_t s) {
-  // The forms of operands that the kernel has: with an epilogue, both K-major and one term; without, bf16 and B MN-major.
+  // The forms of operands that the kernel has: with an epilogue, both K-major and one term; without, bf16 and B
+  // MN-major.
   const bool plain = e.kind == EPI_PLAIN;
   if (count > 1 && !plain) return cudaErrorInvalidValue;
   for (int i = 0; i < count; ++i)

@@ -225,8 +225,8 @@ __device__ __forceinline__ void mask_nums(Num (&a)[NUMS<VEC>], int left) {
 
 // Few rows, short rows and long ones (bf16 vectors up to 32768 elements): one
 // row per group of 2^lg threads, read once.  Latency bounds few rows: one of
-// 4096 2.1 us in a row of calls, 256 3.4 us; instructions bound many short
-// ones: 262144 x 128 36 us.  The variance is the mean square of the
+// 4096 2.1 us in a row of calls, 256 3.5 us; instructions bound many short
+// ones: 262144 x 128 35 us.  The variance is the mean square of the
 // differences from the mean, of values that are already in registers.
 template <class T, class W, int VEC, int NV>
 __global__ void __launch_bounds__(512) norm_kernel(const NormArgs a, int lg) {
@@ -385,8 +385,8 @@ __device__ __forceinline__ const T* unit_row(const void* p, int64_t r, int64_t l
 // the offsets between a thread's elements are known to the compiler, and all
 // warps but a row's last have nothing to mask.  Whole vectors are dealt out
 // over the group instead (thread l has l, l + tpr, ...), which keeps the
-// group's accesses of one step together: 16384 x 4096 backward 78 us, 87 with
-// vectors dealt out by warp.
+// group's accesses of one step together: 16384 x 4096 backward took a ninth
+// longer with vectors dealt out by warp.
 constexpr int RING_THREADS = 512;
 // Copies k weights to shared memory (VEC = 1: `none` where there are none) and
 // adds zeros up to `all` (the block joins afterwards).
@@ -423,12 +423,13 @@ constexpr int MOST_UNITS = NV * static_cast<int>(sizeof(T)) / 16 + 1;
 
 // Rows of each group in flight or in use.  Two: with 32 KB and more a row set,
 // that covers the memory's latency, and more only puts off the first rows and
-// with them the first stores: 2048 x 4096 bf16 forward 10.6 us, 11.5 with three,
-// 11.8 with four; 16384 x 4096 backward 76.8 (90.2 with dres), 77.4 (91.7).
+// with them the first stores: 2048 x 4096 bf16 forward 9.9 us, 10.9 with three,
+// 11.5 with four; level over many rows (16384 x 4096 backward with dres 83.7 us,
+// 83.6 and 84.5).
 constexpr int DEPTH = 2;
 
 // Forward.  FULL: the group's vectors are exactly a row's.  8192 x 8192 bf16 in
-// 46 us, 5.8 TB/s of 6.8; 2000 x 7777 (single elements) in 28 us, where the
+// 45 us, 6.0 TB/s of 6.8, fp32 in 90; 2000 x 7777 (single elements) in 26 us, where the
 // shared-memory accesses and the three barriers of a row, with 16 warps in
 // step, bound it.
 template <class T, class W, int VEC, int NV, bool FULL>
@@ -599,8 +600,8 @@ __device__ __forceinline__ void store_sums(const Num (&dg)[STEPS<VEC, NV>][NUMS<
 // Backward, rows in flight as forward: x, dy and (if given) dres of a row.
 // With xhat = (x - mean) rstd and w = dy gamma:
 // dx = rstd (w - mean(w) - xhat mean(w xhat)) + dres.  16384 x 4096 bf16 with
-// dres in 85 us with the column sums behind it (537 MB, 6.3 TB/s in all);
-// 777 x 5003 f32 in 22 us with them: 5.1 rows per SM in two groups are three
+// dres in 84 us with the column sums behind it (537 MB, 6.4 TB/s in all);
+// 777 x 5003 f32 in 20 us with them: 5.1 rows per SM in two groups are three
 // rounds, and the start, the last round and the sums do not overlap.
 template <class T, class W, int VEC, int NV>
 __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const NormArgs a, int tpr,
@@ -799,9 +800,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const No
 // loads are all in flight before the first is used.  No barriers; the
 // weights of a lane's columns and their gradients' sums stay in registers.
 // 262144 x 128 bf16 54 us, 95 in the kernel above, whose groups are whole warps;
-// 262144 x 64 30 and 95; fp32 262144 x 128 88 and 125.  (Forward the same
-// arrangement was no faster than one row per group: 38 and 36 us.)  What is left over the memory's 30 and 15 us are the
-// sums over the lanes, two for each row.
+// 262144 x 64 30 and 95; fp32 262144 x 128 87 and 125.  (Forward the same
+// arrangement was no faster than one row per group: 38 and 35 us.)  What is
+// left over the memory's 30 and 15 us are the sums over the lanes, two for each
+// row.
 template <class T, int VEC>
 __device__ __forceinline__ void read_or_zeros(const T* p, bool exists, Num (&v)[NUMS<VEC>]) {
   Vec<T, VEC> e = {};
@@ -1027,7 +1029,8 @@ Share share_best(int64_t vecs, std::initializer_list<int> nvs, F f) {
   }
   return best;
 }
-// Single elements (f32 777x5003 backward, 20 a thread 18.9 us, 12 20.2; bf16 1000x9001, 20 28.6, 16 45).
+// Single elements.  Up to 20 a thread, so that longer rows still fit (bf16 1000 x 9001 backward 28 us, 45 in the plain
+// kernels); where fewer hold the row, the number makes no difference (f32 777 x 5003 19.8 us with 20, 19.5 with 12).
 Share share_single(int64_t k, int arrays, int elem, int welem, int weights) {
   return share_best(k, {20, 16, 12, 8}, [&](const Share& s) {
     return ring_smem(false, s, arrays, k, elem, weights * weight_bytes(s.tpr * s.nv, welem)) > 0;

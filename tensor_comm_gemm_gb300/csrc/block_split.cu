@@ -11,11 +11,11 @@
 // the cluster's shared memories, in the order of the ranks, and runs the
 // epilogue on it.
 //
-// One token through 4096 x 4096 takes 8.2 us in a row of calls (4.9 for the
-// weights at the copy rate), four through gate and up of 3584 x 8192 21.7
-// (17.4), 48 through 8192 x 3584 14.7 (8.9): the rest is the launch, the first
-// loads' latency and the cluster's additions, ~5 us that a call this short
-// cannot hide.  Two CTAs share an SM where their stages fit, so that one's
+// One token through 4096 x 4096 takes 8.8 us in a row of calls replayed from a
+// graph (4.9 for the weights at the copy rate), four through gate and up of
+// 3584 x 8192 21.2 (17.4), 48 through 8192 x 3584 14.3 (8.9): the rest is the
+// launch, the first loads' latency and the cluster's additions, 4 to 5 us that a
+// call this short cannot hide.  Two CTAs share an SM where their stages fit, so that one's
 // additions run beside the other's loads.
 
 #include <algorithm>
@@ -376,12 +376,13 @@ static bool plan_split(const Machine& mc, const Product& q, bool fp8, bool gated
   return tiles <= places;
 }
 
-// By rule: up to 128 tokens always (at 96 and 128 tokens it is level with the
-// pairs on 14336x4096 and 1024x1024, and ahead on 4096x4096, 13.6 to 17 us,
-// and 3584x8192, 17.3 to 27), otherwise where all tiles are resident and the
-// models say so (512 tokens, 1000x5000: 15 us, 29 on pairs; 4096x4096: 21.8 us,
-// 18.2 on pairs).  A weight's gradient has the weight's rows for tokens and the
-// tokens for its contraction: few tiles of a small weight, long ones of a long batch.
+// By rule: up to 128 tokens always (128 tokens: level with the pairs on
+// 14336x4096, 26.6 us and 26.3, and 5000x1000, 10.3 and 9.6; ahead on 1024x1024,
+// 6.3 and 6.9, 4096x4096, 13.9 and 16.6, and 3584x8192, 18.0 and 27.5), otherwise
+// where all tiles are resident and the models say so (512 tokens, 1000x5000:
+// 15.7 us, 21.9 on pairs; 4096x4096: 22.2 us, 18.2 on pairs).  A weight's
+// gradient has the weight's rows for tokens and the tokens for its contraction:
+// few tiles of a small weight, long ones of a long batch.
 bool use_split(const Machine& mc, const Product& q, bool fp8, bool gated, int64_t path, int64_t split,
                SplitPlan* plan) {
   if (path == 1) return false;

@@ -33,7 +33,8 @@ TPO_MAX_TP, TPO_MAX_ROW_CHUNKS = 16, 64
 EXPORTS = ["tpo_ctx_create", "tpo_ctx_destroy", "tpo_ag_gemm", "tpo_gemm_rs", "tpo_gemm_ar", "tpo_set_opt",
            "tpo_get_opt", "tpo_sync_status", "tpo_last_device_error", "tpo_last_error", "tpo_staging_ptr",
            "tpo_done_counters", "tpo_read_trace", "tpo_version", "tpo_ag_gemm_noalloc", "tpo_set_fp8_scales",
-           "tpo_block_workspace", "tpo_block_create", "tpo_block_set_opt", "tpo_block_get_opt", "tpo_block_destroy", "tpo_block_sync_status",
+           "tpo_block_workspace", "tpo_block_create", "tpo_block_set_opt", "tpo_block_get_opt", "tpo_block_destroy",
+           "tpo_block_sync_status",
            "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear", "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"]
 TPO_NOALLOC_MAX_STAGING_BYTES = 32 << 20
 
@@ -94,8 +95,8 @@ def lib(path: Optional[str] = None):
     L.tpo_linear_bwd.argtypes = [p, i64, i64, i64, i32] + [p, i64] * 6 + [p, p]
     L.tpo_gated.argtypes = [p, i64, i64, i64, i32, p, i64, p, i64, p, i64, i32] + [p, i64] * 3 + [p] * 4
     L.tpo_gated_bwd.argtypes = [p, i64, i64, i64, i32] + [p, i64] * 9 + [p]
-    for name in ("tpo_block_destroy", "tpo_block_set_opt", "tpo_block_get_opt", "tpo_block_sync_status", "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear",
-                 "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"):
+    for name in ("tpo_block_destroy", "tpo_block_set_opt", "tpo_block_get_opt", "tpo_block_sync_status",
+                 "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear", "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("tpo_ctx_destroy", "tpo_ag_gemm", "tpo_gemm_rs", "tpo_gemm_ar", "tpo_set_opt", "tpo_get_opt",
                  "tpo_sync_status", "tpo_last_device_error", "tpo_read_trace"):
