@@ -543,6 +543,111 @@ tpo_status tpo_gated_bwd(tpo_block* blk, int64_t n, int64_t k, int64_t m, int ac
                          const void* wg, int64_t ldwg, const void* wu, int64_t ldwu, void* dx, int64_t lddx,
                          void* dwg, int64_t lddwg, void* dwu, int64_t lddwu, void* stream);
 
+/*
+ * The attention sublayer: what lies between a column-parallel projection of
+ * queries, keys and values and the row-parallel output projection.  Rotary
+ * positions and attention with grouped heads, on the same handle and under the
+ * same rules as the block operators above.
+ *
+ * Layout: q and its like are [n, heads, dim], k and v [nk, kv_heads, dim], bf16,
+ * with unit stride in dim, a pitch `ld` from one row (token) to the next and a
+ * pitch `h` from one head to the next, in elements.  A slice of a fused
+ * projection's output, a cache of rows and a cache of heads are all of this
+ * form.  A pitch that a single row or a single head does not need is ignored.
+ */
+
+/* How a head's first `rot` elements form pairs: element i with i + rot / 2, or
+ * 2 i with 2 i + 1. */
+typedef enum { TPO_ROTARY_HALVES = 0, TPO_ROTARY_PAIRS = 1 } tpo_rotary_layout;
+/* Frequencies for contexts longer than the trained one: as they are, all
+ * divided by `factor`, or each by how many turns it makes over the trained
+ * context of `original` positions: kept from `high` turns on, divided by
+ * `factor` up to `low`, and a linear blend of the two between. */
+typedef enum { TPO_ROTARY_UNSCALED = 0, TPO_ROTARY_LINEAR = 1, TPO_ROTARY_BY_PARTS = 2 } tpo_rotary_scaling;
+
+/*
+ * Writes the rot / 2 entries of a table in host memory (the caller copies it to
+ * the device; needs no GPU).  Pair i turns by f_i = base^(-2 i / rot) radians a
+ * position, scaled as above; its entry is 2^64 f_i / (2 pi) modulo 2^64, the
+ * turns per position as a 64-bit fraction.  Any other frequencies may be put
+ * into a table in the same form.
+ */
+tpo_status tpo_rotary_table(int64_t rot, double base, int scaling, double factor, double low, double high,
+                            int64_t original, uint64_t* table);
+
+/*
+ * Rotary positions: each pair (a, b) of the first `rot` elements of a head
+ * becomes magnitude (a cos t - b sin t, a sin t + b cos t), t = position times
+ * the pair's frequency; the other elements are copied.
+ *   dtype      of x and y: TPO_BF16 or TPO_F32; pitches and addresses as their
+ *              element type allows
+ *   inverse    not 0: turns the other way, which is the gradient (of dy to dx)
+ *   pos        [n] positions, any of 32 bits; NULL: the row's number
+ *   table      [rot / 2] in device memory, as tpo_rotary_table writes it
+ *   rows       [n] the row of y that each row goes to (as into a cache), NULL:
+ *              its own, with ny = n.  Rows that are negative or at least ny are
+ *              left out; no two may be the same.
+ * The angle is exact for every position (64-bit arithmetic); sine, cosine and
+ * the turn are computed in fp32, and the result is rounded once.  y may be x,
+ * with the same pitches and without rows.  rot = 0 copies.
+ */
+tpo_status tpo_rotary(tpo_block* blk, int64_t n, int64_t heads, int64_t dim, int64_t rot, int dtype, int layout,
+                      int inverse, float magnitude, const int32_t* pos, const uint64_t* table, const void* x,
+                      int64_t ldx, int64_t hx, const int32_t* rows, int64_t ny, void* y, int64_t ldy, int64_t hy,
+                      void* stream);
+
+/* Bytes of workspace that a call with up to n and nk rows needs (batch does not
+ * enter), or -1 with tpo_last_error set; need no GPU. */
+int64_t tpo_attention_workspace(int64_t n, int64_t nk, int64_t heads, int64_t kv_heads, int64_t dim);
+int64_t tpo_attention_bwd_workspace(int64_t n, int64_t nk, int64_t heads, int64_t kv_heads, int64_t dim);
+
+/*
+ * Attention, sequence by sequence:
+ *   out = softmax(scale q k^T) v
+ *   lse = log sum exp(scale q k^T)  (natural logarithm)
+ * heads is a multiple of kv_heads (up to 128 times); query head h reads key head
+ * h / (heads / kv_heads).  dim is a multiple of 8 up to 128.  Addresses are
+ * 16-byte aligned and pitches multiples of 16 bytes.
+ *   q_start    [batch + 1] device: sequence i has the queries of rows
+ *              q_start[i] up to q_start[i + 1]
+ *   k_start, k_len  device: its keys are k_len[i] rows from k_start[i] on, or
+ *              with k_len NULL (k_start then has batch + 1 entries) the rows
+ *              up to k_start[i + 1], or with both NULL the queries' rows.
+ *              With one sequence each may be NULL: all rows, k_len of them.
+ *   causal     not 0: the sequence's last query sees all of its keys, each
+ *              earlier one a key less (query t of nq sees t + 1 + nk - nq)
+ *   lse        [n, heads] fp32 for the backward pass, or NULL
+ * Lengths are read on the device: a captured call follows them as they change.
+ * Starts and lengths are held inside the tensors, so that no call reads or
+ * writes outside them.  A sequence may have no queries or no keys; a query that
+ * sees no key gets zeros and lse = -infinity.  Rows of no sequence are left as
+ * they were, and what they or the unused rows of a cache hold is never used.
+ * Scores, weights and sums are held in fp32; the weights are rounded to bf16
+ * as operands of the product with v (their sum is taken before that).
+ */
+tpo_status tpo_attention(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, int64_t heads, int64_t kv_heads,
+                         int64_t dim, const int32_t* q_start, const int32_t* k_start, const int32_t* k_len,
+                         int causal, float scale, const void* q, int64_t ldq, int64_t hq, const void* k, int64_t ldk,
+                         int64_t hk, const void* v, int64_t ldv, int64_t hv, void* out, int64_t ldo, int64_t ho,
+                         float* lse, void* stream);
+
+/*
+ * Gradient of tpo_attention, with p = exp(scale q k^T - lse) and
+ * delta = sum over dim of dout out:
+ *   ds = p (dout v^T - delta);  dq = scale ds k,  dk = scale ds^T q,  dv = p^T dout
+ * dk and dv are summed over the query heads that share a key head.  out and lse
+ * are the forward call's.  The sequences' keys must not overlap.  A key that no
+ * query sees gets zeros.  p and ds are rounded to bf16 as operands of the
+ * products.
+ */
+tpo_status tpo_attention_bwd(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, int64_t heads, int64_t kv_heads,
+                             int64_t dim, const int32_t* q_start, const int32_t* k_start, const int32_t* k_len,
+                             int causal, float scale, const void* dout, int64_t lddo, int64_t hdo, const void* q,
+                             int64_t ldq, int64_t hq, const void* k, int64_t ldk, int64_t hk, const void* v,
+                             int64_t ldv, int64_t hv, const void* out, int64_t ldo, int64_t ho, const float* lse,
+                             void* dq, int64_t lddq, int64_t hdq, void* dk, int64_t lddk, int64_t hdk, void* dv,
+                             int64_t lddv, int64_t hdv, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

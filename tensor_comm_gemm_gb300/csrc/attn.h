@@ -1,0 +1,71 @@
+// Shared by the host side (attention.cu) and the kernels of the attention
+// sublayer's operators.  Private to libtpoverlap; include/tpoverlap.h has the
+// contract.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "block.h"
+
+namespace tpo {
+
+// [rows, heads, dim] with unit stride in dim: element (i, h, j) at p + i * ld + h * hs + j.
+struct Heads {
+  const void* p;
+  int64_t ld, hs;
+};
+
+// Where the sequences lie: rows [q_start[i], q_start[i + 1]) of the queries, and
+// of the keys k_len[i] rows from k_start[i] on (k_len NULL: up to k_start[i + 1]).
+// Both NULL: one sequence of all rows.
+struct Sequences {
+  int64_t batch, n, nk;
+  const int32_t *q_start, *k_start, *k_len;
+};
+struct Seq {
+  int64_t q0, nq, k0, nk;
+};
+// Sequence i, held inside the tensors whatever the arrays say.
+__device__ __forceinline__ Seq sequence(const Sequences& s, int64_t i) {
+  auto in = [](int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; };
+  Seq r;
+  r.q0 = s.q_start ? in(s.q_start[i], 0, s.n) : 0;
+  r.nq = (s.q_start ? in(s.q_start[i + 1], r.q0, s.n) : s.n) - r.q0;
+  r.k0 = s.k_start ? in(s.k_start[i], 0, s.nk) : 0;
+  if (s.k_len)
+    r.nk = in(s.k_len[i], 0, s.nk - r.k0);
+  else
+    r.nk = (s.k_start ? in(s.k_start[i + 1], r.k0, s.nk) : s.nk) - r.k0;
+  return r;
+}
+
+struct AttnArgs {
+  Sequences seq;
+  int64_t heads, kv_heads, dim;
+  int causal;
+  float scale;
+  Heads q, k, v, out;
+  float* lse;  // [n, heads]
+  Heads dout, dq, dk, dv;
+};
+
+cudaError_t launch_attention(const Machine& mc, const AttnArgs& a, const Watch& w, uint32_t* arrivals, void* ws,
+                             cudaStream_t s);
+int64_t need_attention(int64_t n, int64_t nk, int64_t heads, int64_t kv_heads, int64_t dim);
+cudaError_t launch_attention_bwd(const Machine& mc, const AttnArgs& a, const Watch& w, uint32_t* arrivals, void* ws,
+                                 cudaStream_t s);
+int64_t need_attention_bwd(int64_t n, int64_t nk, int64_t heads, int64_t kv_heads, int64_t dim);
+
+struct RotaryArgs {
+  int64_t n, heads, dim, rot;
+  Heads x, y;
+  const int32_t *pos, *rows;
+  int64_t ny;
+  const uint64_t* table;
+  float magnitude;
+  int layout, inverse;
+};
+cudaError_t launch_rotary(const Machine& mc, const RotaryArgs& a, int dtype, cudaStream_t s);
+
+}  // namespace tpo

@@ -3,50 +3,14 @@
 
 #include <cuda_runtime.h>
 
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
 #include <cstring>
 #include <new>
 
 #include "block.h"
+#include "block_host.h"
 
-namespace {
-
-tpo_status fail(tpo_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  tpo::set_last_error(buf);
-  return s;
-}
-
-tpo_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(TPO_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
-}
-
-constexpr int64_t kMaxSize = 1ll << 30;
-constexpr size_t kErrBytes = 256;  // the error words ahead of the workspace
-
-int64_t round_up(int64_t v, int64_t q) { return (v + q - 1) / q * q; }
-
-// Pitch of a bf16 workspace matrix: whole 128-byte lines.
-int64_t ws_pitch(int64_t m) { return round_up(m, 64); }
-
-}  // namespace
-
-struct tpo_block {
-  int device = 0;
-  uint8_t* mem = nullptr;  // error words, then the workspace
-  int64_t ws_bytes = 0;
-  tpo::Machine machine{};
-  int64_t path = 0, split = 0, wait_timeout_ms = 2000;  // options
-  uint32_t* err() const { return reinterpret_cast<uint32_t*>(mem); }
-  tpo::Watch watch() const { return {err(), static_cast<unsigned long long>(wait_timeout_ms) * 1000000ull}; }
-  uint8_t* ws() const { return mem + kErrBytes; }
-};
+using namespace tpo;
 
 namespace {
 
@@ -103,12 +67,6 @@ tpo_status check_rows(const Mat& a) {
   return TPO_OK;
 }
 
-tpo_status check_vec(const char* name, const void* p, int elem) {
-  if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(elem))
-    return fail(TPO_ERR_INVALID_ARG, "%s must be aligned to its elements", name);
-  return TPO_OK;
-}
-
 tpo_status check_sizes(int64_t n, int64_t k, int64_t m) {
   if (n < 0 || n > kMaxSize || k < 1 || k > kMaxSize || m < 1 || m > kMaxSize)
     return fail(TPO_ERR_INVALID_ARG, "sizes out of range: n=%lld in [0, 2^30], k=%lld and m=%lld in [1, 2^30]",
@@ -131,20 +89,6 @@ tpo_status check_types(int dtype, const float* const* scales, int count) {
       return fail(TPO_ERR_INVALID_ARG, "bf16 inputs take no scale_inv pointers (pass NULL)");
     if (tpo_status st = check_vec("a scale_inv pointer", scales[i], 4)) return st;
   }
-  return TPO_OK;
-}
-
-// The handle, checked last so that the other argument errors need no GPU.
-tpo_status check_block(const tpo_block* b, int64_t need) {
-  if (!b) return fail(TPO_ERR_INVALID_ARG, "NULL block handle");
-  if (need > b->ws_bytes)
-    return fail(TPO_ERR_INVALID_ARG, "the call needs %lld bytes of workspace, the handle has %lld", (long long)need,
-                (long long)b->ws_bytes);
-  int dev = -1;
-  const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "no usable CUDA device");
-  if (dev != b->device)
-    return fail(TPO_ERR_INVALID_ARG, "the handle is of device %d, the current device is %d", b->device, dev);
   return TPO_OK;
 }
 
@@ -200,8 +144,6 @@ cudaError_t run_products(tpo_block* b, const tpo::Product* q, int count, int dx,
   }
   return left ? tpo::launch_products(b->machine, rest, left, false, tpo::Epi(), b->watch(), s) : cudaSuccess;
 }
-
-tpo_status launched(cudaError_t e) { return e == cudaSuccess ? TPO_OK : cuda_fail(e, "kernel launch"); }
 
 // dz, then the bias gradient's per-block sums.  dz, dg and du are kept in bf16: they are operands of the products that
 // follow, which the tensor cores take in that type.  It is one rounding more than those of the results (the gradients'
@@ -268,14 +210,14 @@ tpo_block* tpo_block_create(int64_t workspace_bytes) {
     return nullptr;
   }
   b->ws_bytes = workspace_bytes;
-  e = cudaMalloc(&b->mem, kErrBytes + static_cast<size_t>(workspace_bytes));
+  e = cudaMalloc(&b->mem, kHeadBytes + static_cast<size_t>(workspace_bytes));
   if (e != cudaSuccess) {
     fail(TPO_ERR_OOM, "workspace of %lld bytes: %s", (long long)workspace_bytes, cudaGetErrorString(e));
     cudaGetLastError();
     delete b;
     return nullptr;
   }
-  e = cudaMemset(b->mem, 0, kErrBytes);
+  e = cudaMemset(b->mem, 0, kHeadBytes);
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess) {
     cuda_fail(e, "block set-up");
@@ -322,7 +264,7 @@ tpo_status tpo_block_sync_status(tpo_block* b, void* stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "synchronise");
   if (err[0] == 0) return TPO_OK;
-  e = cudaMemsetAsync(b->mem, 0, kErrBytes, s);
+  e = cudaMemsetAsync(b->mem, 0, kHeadBytes, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "reset after device failure");
   return fail(TPO_ERR_TIMEOUT, "device wait timed out (site %u, block %u)", err[1], err[2]);

@@ -20,6 +20,8 @@ TPO_BF16, TPO_FP8_E4M3, TPO_F32 = 0, 1, 2
 TPO_ACT_NONE, TPO_ACT_RELU, TPO_ACT_GELU, TPO_ACT_GELU_TANH, TPO_ACT_SILU = 0, 1, 2, 3, 4
 TPO_OP_LAYER_NORM, TPO_OP_LAYER_NORM_BWD, TPO_OP_LINEAR = 0, 1, 2
 TPO_OP_LINEAR_BWD, TPO_OP_GATED, TPO_OP_GATED_BWD = 3, 4, 5
+TPO_ROTARY_HALVES, TPO_ROTARY_PAIRS = 0, 1
+TPO_ROTARY_UNSCALED, TPO_ROTARY_LINEAR, TPO_ROTARY_BY_PARTS = 0, 1, 2
 TPO_ERR_INVALID_ARG, TPO_ERR_UNSUPPORTED = 1, 2
 STATUS = {0: "TPO_OK", 1: "TPO_ERR_INVALID_ARG", 2: "TPO_ERR_UNSUPPORTED", 3: "TPO_ERR_CUDA",
           4: "TPO_ERR_TIMEOUT", 5: "TPO_ERR_OOM"}
@@ -35,7 +37,9 @@ EXPORTS = ["tpo_ctx_create", "tpo_ctx_destroy", "tpo_ag_gemm", "tpo_gemm_rs", "t
            "tpo_done_counters", "tpo_read_trace", "tpo_version", "tpo_ag_gemm_noalloc", "tpo_set_fp8_scales",
            "tpo_block_workspace", "tpo_block_create", "tpo_block_set_opt", "tpo_block_get_opt", "tpo_block_destroy",
            "tpo_block_sync_status",
-           "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear", "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"]
+           "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear", "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd",
+           "tpo_rotary_table", "tpo_rotary", "tpo_attention_workspace", "tpo_attention_bwd_workspace", "tpo_attention",
+           "tpo_attention_bwd"]
 TPO_NOALLOC_MAX_STAGING_BYTES = 32 << 20
 
 
@@ -95,6 +99,17 @@ def lib(path: Optional[str] = None):
     L.tpo_linear_bwd.argtypes = [p, i64, i64, i64, i32] + [p, i64] * 6 + [p, p]
     L.tpo_gated.argtypes = [p, i64, i64, i64, i32, p, i64, p, i64, p, i64, i32] + [p, i64] * 3 + [p] * 4
     L.tpo_gated_bwd.argtypes = [p, i64, i64, i64, i32] + [p, i64] * 9 + [p]
+    f64 = ctypes.c_double
+    L.tpo_rotary_table.argtypes = [i64, f64, i32, f64, f64, f64, i64, p]
+    L.tpo_rotary.argtypes = [p, i64, i64, i64, i64, i32, i32, i32, f32, p, p, p, i64, i64, p, i64, p, i64, i64, p]
+    for name in ("tpo_attention_workspace", "tpo_attention_bwd_workspace"):
+        getattr(L, name).argtypes = [i64] * 5
+        getattr(L, name).restype = i64
+    L.tpo_attention.argtypes = [p] + [i64] * 6 + [p, p, p, i32, f32] + [p, i64, i64] * 4 + [p, p]
+    L.tpo_attention_bwd.argtypes = ([p] + [i64] * 6 + [p, p, p, i32, f32] + [p, i64, i64] * 5 + [p] +
+                                    [p, i64, i64] * 3 + [p])
+    for name in ("tpo_rotary_table", "tpo_rotary", "tpo_attention", "tpo_attention_bwd"):
+        getattr(L, name).restype = ctypes.c_int
     for name in ("tpo_block_destroy", "tpo_block_set_opt", "tpo_block_get_opt", "tpo_block_sync_status",
                  "tpo_layer_norm", "tpo_layer_norm_bwd", "tpo_linear", "tpo_linear_bwd", "tpo_gated", "tpo_gated_bwd"):
         getattr(L, name).restype = ctypes.c_int
@@ -475,3 +490,126 @@ def tpo_gated_bwd(block: int, dh, g, u, x, wg, wu, dx=None, dwg=None, dwu=None, 
                                 ("wu", wu, m, k), ("dx", dx, n, k), ("dwg", dwg, m, k), ("dwu", dwu, m, k)):
         args += _mat(name, t, rows, cols, TPO_BF16)
     _check(lib().tpo_gated_bwd(block, n, k, m, act, *args, _stream_of(stream, dh)))
+
+
+# ------------------------------------------------------------------ the attention sublayer
+#
+# Tensors [rows, heads, dim] with unit stride in the last dimension carry their
+# sizes and the pitches of rows and heads.
+
+def _shape3(name, t):
+    s = t.shape
+    if len(s) != 3:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be 3-D" % name)
+    return s
+
+
+def _heads(name, t, rows, heads, dim, code):
+    """(pointer, row pitch, head pitch) of an [rows, heads, dim] CUDA tensor of type `code`."""
+    if t.shape != (rows, heads, dim):
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s has shape %s, expected (%d, %d, %d)" % (name, tuple(t.shape), rows,
+                                                                                      heads, dim))
+    if not t.is_cuda:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
+    if _CODES.get(t.dtype) != code and _code(name, t) != code:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
+    ld, hs, unit = t.stride()
+    if unit != 1 and dim > 1:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must have unit stride in its last dimension" % name)
+    return t.data_ptr(), ld, hs
+
+
+def _ints(name, t, count, bits=32):
+    """Pointer of `count` contiguous CUDA integers; None for None."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype != (torch.int32 if bits == 32 else torch.int64):
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s, expected int%d" % (name, t.dtype, bits))
+    if t.numel() != count or not t.is_contiguous():
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must hold %d contiguous elements" % (name, count))
+    if not t.is_cuda:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
+    return t.data_ptr()
+
+
+def tpo_rotary_table(rot: int, base: float = 10000.0, scaling: int = TPO_ROTARY_UNSCALED, factor: float = 1.0,
+                     low: float = 1.0, high: float = 4.0, original: int = 1):
+    """The table as a host tensor of `rot` / 2 int64 (the entries' 64 bits); copy it to the device once."""
+    import torch
+    table = torch.empty(max(rot, 0) // 2, dtype=torch.int64)
+    _check(lib().tpo_rotary_table(rot, base, scaling, factor, low, high, original, table.data_ptr()))
+    return table
+
+
+def tpo_rotary(block: int, x, table, y, pos=None, layout: int = TPO_ROTARY_HALVES, inverse: bool = False,
+               magnitude: float = 1.0, rows=None, stream=None) -> None:
+    n, heads, dim = _shape3("x", x)
+    ny = _shape3("y", y)[0]
+    dt = _code("x", x)
+    half = 0 if table is None else table.numel()
+    px, ldx, hx = _heads("x", x, n, heads, dim, dt)
+    py, ldy, hy = _heads("y", y, ny if rows is not None else n, heads, dim, dt)
+    _check(lib().tpo_rotary(block, n, heads, dim, 2 * half, dt, layout, inverse, magnitude, _ints("pos", pos, n),
+                            _ints("table", table, half, 64), px, ldx, hx, _ints("rows", rows, n), ny, py, ldy, hy,
+                            _stream_of(stream, x)))
+
+
+def tpo_attention_workspace(n: int, nk: int, heads: int, kv_heads: int, dim: int) -> int:
+    b = lib().tpo_attention_workspace(n, nk, heads, kv_heads, dim)
+    if b < 0:
+        raise TpoError(TPO_ERR_INVALID_ARG, tpo_last_error())
+    return b
+
+
+def tpo_attention_bwd_workspace(n: int, nk: int, heads: int, kv_heads: int, dim: int) -> int:
+    b = lib().tpo_attention_bwd_workspace(n, nk, heads, kv_heads, dim)
+    if b < 0:
+        raise TpoError(TPO_ERR_INVALID_ARG, tpo_last_error())
+    return b
+
+
+def _sequences(q_start, k_start, k_len):
+    """(number of sequences, pointers of the three arrays)."""
+    if q_start is not None:
+        batch = q_start.numel() - 1
+    elif k_len is not None:
+        batch = k_len.numel()
+    else:
+        batch = 1
+    # with lengths, k_start may have an entry more than it needs, as cumulative sums do
+    count = batch if k_len is not None else batch + 1
+    if k_start is not None and k_len is not None and k_start.numel() == batch + 1:
+        count = batch + 1
+    return batch, _ints("q_start", q_start, batch + 1), _ints("k_start", k_start, count), _ints("k_len", k_len, batch)
+
+
+def tpo_attention(block: int, q, k, v, out, q_start=None, k_start=None, k_len=None, causal: bool = True,
+                  scale: Optional[float] = None, lse=None, stream=None) -> None:
+    n, heads, dim = _shape3("q", q)
+    nk, kv = _shape3("k", k)[:2]
+    batch, pqs, pks, pkl = _sequences(q_start, k_start, k_len)
+    _check(lib().tpo_attention(block, batch, n, nk, heads, kv, dim, pqs, pks, pkl, causal,
+                               dim ** -0.5 if scale is None else scale, *_heads("q", q, n, heads, dim, TPO_BF16),
+                               *_heads("k", k, nk, kv, dim, TPO_BF16), *_heads("v", v, nk, kv, dim, TPO_BF16),
+                               *_heads("out", out, n, heads, dim, TPO_BF16), _vec("lse", lse, n * heads, TPO_F32),
+                               _stream_of(stream, q)))
+
+
+def tpo_attention_bwd(block: int, dout, q, k, v, out, lse, dq, dk, dv, q_start=None, k_start=None, k_len=None,
+                      causal: bool = True, scale: Optional[float] = None, stream=None) -> None:
+    n, heads, dim = _shape3("q", q)
+    nk, kv = _shape3("k", k)[:2]
+    batch, pqs, pks, pkl = _sequences(q_start, k_start, k_len)
+    args = []
+    for name, t in (("dout", dout), ("q", q)):
+        args += _heads(name, t, n, heads, dim, TPO_BF16)
+    for name, t in (("k", k), ("v", v)):
+        args += _heads(name, t, nk, kv, dim, TPO_BF16)
+    args += _heads("out", out, n, heads, dim, TPO_BF16)
+    args.append(_vec("lse", lse, n * heads, TPO_F32))
+    args += _heads("dq", dq, n, heads, dim, TPO_BF16)
+    for name, t in (("dk", dk), ("dv", dv)):
+        args += _heads(name, t, nk, kv, dim, TPO_BF16)
+    _check(lib().tpo_attention_bwd(block, batch, n, nk, heads, kv, dim, pqs, pks, pkl, causal,
+                                   dim ** -0.5 if scale is None else scale, *args, _stream_of(stream, q)))
