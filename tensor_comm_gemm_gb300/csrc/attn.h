@@ -24,20 +24,25 @@ struct Sequences {
   const int32_t *q_start, *k_start, *k_len;
 };
 struct Seq {
-  int64_t q0, nq, k0, nk;
+  int q0, nq, k0, nk;  // rows of a tensor: at most 2^30
 };
 // Sequence i, held inside the tensors whatever the arrays say.
 __device__ __forceinline__ Seq sequence(const Sequences& s, int64_t i) {
-  auto in = [](int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; };
+  auto in = [](int64_t v, int64_t lo, int64_t hi) { return static_cast<int>(v < lo ? lo : v > hi ? hi : v); };
   Seq r;
   r.q0 = s.q_start ? in(s.q_start[i], 0, s.n) : 0;
-  r.nq = (s.q_start ? in(s.q_start[i + 1], r.q0, s.n) : s.n) - r.q0;
+  r.nq = (s.q_start ? in(s.q_start[i + 1], r.q0, s.n) : static_cast<int>(s.n)) - r.q0;
   r.k0 = s.k_start ? in(s.k_start[i], 0, s.nk) : 0;
   if (s.k_len)
     r.nk = in(s.k_len[i], 0, s.nk - r.k0);
   else
-    r.nk = (s.k_start ? in(s.k_start[i + 1], r.k0, s.nk) : s.nk) - r.k0;
+    r.nk = (s.k_start ? in(s.k_start[i + 1], r.k0, s.nk) : static_cast<int>(s.nk)) - r.k0;
   return r;
+}
+
+// Keys that query t of a sequence sees.
+__device__ __forceinline__ int keys_seen(const Seq& s, int t, int causal) {
+  return causal ? max(0, t - s.nq + 1 + s.nk) : s.nk;
 }
 
 struct AttnArgs {
@@ -50,6 +55,8 @@ struct AttnArgs {
   Heads dout, dq, dk, dv;
 };
 
+// Set the kernels' attributes.
+cudaError_t configure_attention();
 cudaError_t launch_attention(const Machine& mc, const AttnArgs& a, const Watch& w, uint32_t* arrivals, void* ws,
                              cudaStream_t s);
 int64_t need_attention(int64_t n, int64_t nk, int64_t heads, int64_t kv_heads, int64_t dim);

@@ -1,4 +1,4 @@
-// Attention and its gradient, one warp a row (sm_103a).
+// Gradient of attention, one warp a row (sm_103a).
 
 #include <cuda_bf16.h>
 
@@ -36,43 +36,6 @@ __device__ __forceinline__ float dot(const float (&a)[PER_LANE], const float (&b
   return s;
 }
 
-// Keys that query t of the sequence sees.
-__device__ __forceinline__ int64_t keys_of(const Seq& q, int64_t t, int causal) {
-  if (!causal) return q.nk;
-  const int64_t e = t + 1 + q.nk - q.nq;
-  return e < 0 ? 0 : e;
-}
-
-__global__ void __launch_bounds__(32 * WARPS) rows_kernel(AttnArgs a) {
-  grid_dep_launch();
-  grid_dep_wait();
-  const int lane = threadIdx.x & 31, dim = static_cast<int>(a.dim);
-  const int64_t h = blockIdx.y, kv = h / (a.heads / a.kv_heads);
-  for (int64_t i = blockIdx.z; i < a.seq.batch; i += gridDim.z) {
-    const Seq q = sequence(a.seq, i);
-    for (int64_t t = blockIdx.x * WARPS + (threadIdx.x >> 5); t < q.nq; t += gridDim.x * WARPS) {
-      float x[PER_LANE], o[PER_LANE] = {}, y[PER_LANE];
-      load(row_of(a.q, q.q0 + t, h), lane, dim, x);
-      float m = -INFINITY, l = 0.0f;
-      const int64_t end = keys_of(q, t, a.causal);
-      for (int64_t j = 0; j < end; ++j) {
-        load(row_of(a.k, q.k0 + j, kv), lane, dim, y);
-        const float s = dot(x, y) * a.scale, top = fmaxf(m, s);
-        const float keep = m == -INFINITY ? 0.0f : expf(m - top), p = expf(s - top);
-        m = top;
-        l = l * keep + p;
-        load(row_of(a.v, q.k0 + j, kv), lane, dim, y);
-#pragma unroll
-        for (int e = 0; e < PER_LANE; ++e) o[e] = o[e] * keep + p * y[e];
-      }
-#pragma unroll
-      for (int e = 0; e < PER_LANE; ++e) o[e] = end ? o[e] / l : 0.0f;
-      store(const_cast<bf16*>(row_of(a.out, q.q0 + t, h)), lane, dim, o);
-      if (a.lse && lane == 0) a.lse[(q.q0 + t) * a.heads + h] = end ? m + logf(l) : -INFINITY;
-    }
-  }
-}
-
 __global__ void __launch_bounds__(32 * WARPS) rows_dq_kernel(AttnArgs a) {
   grid_dep_launch();
   grid_dep_wait();
@@ -86,7 +49,7 @@ __global__ void __launch_bounds__(32 * WARPS) rows_dq_kernel(AttnArgs a) {
       load(row_of(a.out, q.q0 + t, h), lane, dim, y);
       load(row_of(a.dout, q.q0 + t, h), lane, dim, dy);
       const float delta = dot(y, dy), lse = a.lse[(q.q0 + t) * a.heads + h];
-      const int64_t end = keys_of(q, t, a.causal);
+      const int64_t end = keys_seen(q, static_cast<int>(t), a.causal);
       for (int64_t j = 0; j < end; ++j) {
         load(row_of(a.v, q.k0 + j, kv), lane, dim, y);
         const float dp = dot(dy, y);
@@ -141,12 +104,8 @@ dim3 grid_of(int64_t rows, int64_t heads, int64_t batch) {
 
 }  // namespace
 
-int64_t need_attention(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
 int64_t need_attention_bwd(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
 
-cudaError_t launch_attention(const Machine&, const AttnArgs& a, const Watch&, uint32_t*, void*, cudaStream_t s) {
-  return launch_pdl(rows_kernel, grid_of(a.seq.n, a.heads, a.seq.batch), dim3(32 * WARPS), 0, s, a);
-}
 cudaError_t launch_attention_bwd(const Machine&, const AttnArgs& a, const Watch&, uint32_t*, void*, cudaStream_t s) {
   if (a.seq.n > 0) {
     const cudaError_t e =

@@ -7,6 +7,7 @@
 #include <cstring>
 #include <new>
 
+#include "attn.h"
 #include "block.h"
 #include "block_host.h"
 
@@ -204,6 +205,7 @@ tpo_block* tpo_block_create(int64_t workspace_bytes) {
   }
   e = tpo::configure_products(&b->machine);
   if (e == cudaSuccess) e = tpo::configure_split(&b->machine);
+  if (e == cudaSuccess) e = tpo::configure_attention();
   if (e != cudaSuccess) {
     cuda_fail(e, "kernel configuration");
     delete b;
