@@ -206,6 +206,7 @@ tpo_block* tpo_block_create(int64_t workspace_bytes) {
   e = tpo::configure_products(&b->machine);
   if (e == cudaSuccess) e = tpo::configure_split(&b->machine);
   if (e == cudaSuccess) e = tpo::configure_attention();
+  if (e == cudaSuccess) e = tpo::configure_attention_bwd();
   if (e != cudaSuccess) {
     cuda_fail(e, "kernel configuration");
     delete b;
