@@ -78,7 +78,8 @@ struct Layout {
   static constexpr int BARS = STATS + STAGES * 1024;
   static constexpr int N_BARS = 6 * STAGES + 9;
   static constexpr int SLOT = BARS + 8 * N_BARS, LAST = SLOT + 4;
-  static constexpr int PLAN = (SLOT + 8 + 15) / 16 * 16;
+  static constexpr int STAGE = (SLOT + 8 + 15) / 16 * 16;  // a staging box for each computing warp
+  static constexpr int PLAN = STAGE + 8 * 2048;
   static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
   static_assert(SMEM <= 232448, "shared memory of one block");
 };
@@ -127,7 +128,7 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
     auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int head, int row) {
       for (int d = 0; d < DP / 64; ++d) tma_load_3d(dst + d * 16384, map, bar, d * 64, head, row);
     };
-    if (!(ok = wait_bar_warp(a.watch, b.fempty, (fn & 1u) ^ 1u, S_EMPTY))) break;
+    if (!(ok = wait_warp(a.watch, b.fempty, (fn & 1u) ^ 1u, S_EMPTY))) break;
     if (lead) {
       const int head = KEYS ? kh : qh, row = KEYS ? w.s.k0 + w.tile * BLK : w.s.q0 + w.tile * a.tokens;
       mbar_expect_tx(b.ffull, 2 * (KEYS ? kbytes : qbytes));
@@ -139,14 +140,14 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
     for (int j = p.lo; j < p.hi; ++j) {
       const int head = KEYS ? qh : kh, row = KEYS ? w.s.q0 + j * a.tokens : w.s.k0 + j * BLK;
       const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
-      if (!(ok = wait_bar_warp(a.watch, b.empty0 + 8 * st, ph ^ 1u, S_EMPTY))) break;
+      if (!(ok = wait_warp(a.watch, b.empty0 + 8 * st, ph ^ 1u, S_EMPTY))) break;
       if (lead) {
         mbar_expect_tx(b.full0 + 8 * st, KEYS ? qbytes : kbytes);
         load(sbase + L::R0 + st * L::TILE, r0, b.full0 + 8 * st, head, row);
       }
       __syncwarp();
       ++n;
-      if (!(ok = wait_bar_warp(a.watch, b.empty1 + 8 * st, ph ^ 1u, S_EMPTY))) break;
+      if (!(ok = wait_warp(a.watch, b.empty1 + 8 * st, ph ^ 1u, S_EMPTY))) break;
       if (lead) {
         mbar_expect_tx(b.full1 + 8 * st, KEYS ? qbytes : kbytes);
         load(sbase + L::R1 + st * L::TILE, r1, b.full1 + 8 * st, head, row);
@@ -186,42 +187,41 @@ __device__ void mma_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& 
     auto stage = [&](uint32_t s) { return static_cast<uint64_t>(s % L::STAGES) * (L::TILE >> 4); };
     // step s of the launch: S and dP from shared memory
     auto scores = [&](uint32_t s) {
-      if (!wait_bar_warp(a.watch, b.full0 + 8 * (s % L::STAGES), s / L::STAGES & 1u, S_FULL)) return false;
+      if (!wait_warp(a.watch, b.full0 + 8 * (s % L::STAGES), s / L::STAGES & 1u, S_FULL)) return false;
       tc_fence_after();
       const uint32_t d = KEYS || !(s & 1u) ? tmem : acc1;
-      for (int k = 0; k < ksteps; ++k) mma_ss(d, desc_k(f0, k), desc_k(r0 + stage(s), k), idesc_s, k > 0);
+      mma_head<DP>(d, f0, r0 + stage(s), idesc_s, ksteps);
       mma_commit_cg<1>(b.sfull + 8 * (s & 1u));  // two: the threads may still be at the step before
       return true;
     };
     auto dots = [&](uint32_t s) {
-      if (!wait_bar_warp(a.watch, b.full1 + 8 * (s % L::STAGES), s / L::STAGES & 1u, S_FULL)) return false;
+      if (!wait_warp(a.watch, b.full1 + 8 * (s % L::STAGES), s / L::STAGES & 1u, S_FULL)) return false;
       tc_fence_after();
-      for (int k = 0; k < ksteps; ++k) mma_ss(dp, desc_k(f1, k), desc_k(r1 + stage(s), k), idesc_s, k > 0);
+      mma_head<DP>(dp, f1, r1 + stage(s), idesc_s, ksteps);
       mma_commit_cg<1>(b.dpfull);
       return true;
     };
     // an accumulator += bf16 columns at `from` (64 and 64 columns apart) . rows of a ring's stage
     auto add = [&](uint32_t acc, uint32_t from, uint64_t rows, bool fresh) {
       tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mma_ts(acc, from + (k >> 2) * 64 + (k & 3) * 8, rows + 128u * k, idesc_o, !fresh || k > 0);
+      mma4_ts(acc, from, rows, idesc_o, !fresh);
+      mma4_ts(acc, from + 64, rows + 512, idesc_o, 1u);
     };
-    if (!(ok = wait_bar_warp(a.watch, b.ffull, fn & 1u, S_FULL))) break;
+    if (!(ok = wait_warp(a.watch, b.ffull, fn & 1u, S_FULL))) break;
     ok = scores(n) && dots(n);
     for (int i = 0; ok && i < steps; ++i, ++n) {
       const uint32_t st = n % L::STAGES;
       if constexpr (KEYS) {
-        if (!(ok = wait_bar_warp(a.watch, b.pfull, n & 1u, S_TFULL))) break;
+        if (!(ok = wait_warp(a.watch, b.pfull, n & 1u, S_TFULL))) break;
         add(acc0, tmem, t1 + stage(n), i == 0);  // dV
         mma_commit_cg<1>(b.empty1 + 8 * st);
         if (i + 1 < steps && !(ok = scores(n + 1))) break;
-        if (!(ok = wait_bar_warp(a.watch, b.dsfull, n & 1u, S_TFULL))) break;
+        if (!(ok = wait_warp(a.watch, b.dsfull, n & 1u, S_TFULL))) break;
         add(acc1, dp, t0 + stage(n), i == 0);  // dK
         mma_commit_cg<1>(b.empty0 + 8 * st);
       } else {
         if (i + 1 < steps && !(ok = scores(n + 1))) break;
-        if (!(ok = wait_bar_warp(a.watch, b.dsfull, n & 1u, S_TFULL))) break;
+        if (!(ok = wait_warp(a.watch, b.dsfull, n & 1u, S_TFULL))) break;
         mma_commit_cg<1>(b.empty1 + 8 * st);  // V: dP of this step is done
         add(acc0, dp, t0 + stage(n), i == 0);  // dQ
         mma_commit_cg<1>(b.empty0 + 8 * st);
@@ -255,7 +255,7 @@ __device__ void aux_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& 
       const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
       const int left = KEYS ? min(a.tokens, w.s.nq - j * a.tokens) * a.group : w.s.nk - j * BLK;  // rows in use
       if constexpr (KEYS) {
-        if (!wait_bar_warp(a.watch, b.free + 8 * st, ph ^ 1u, S_EMPTY)) return;
+        if (!wait_warp(a.watch, b.free + 8 * st, ph ^ 1u, S_EMPTY)) return;
         float* stats = reinterpret_cast<float*>(smem + L::STATS) + st * 256;
 #pragma unroll
         for (int r = me; r < BLK; r += 64) {
@@ -269,8 +269,8 @@ __device__ void aux_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& 
           stats[BLK + r] = v.y;
         }
       }
-      if (!wait_bar_warp(a.watch, b.full0 + 8 * st, ph, S_FULL)) return;
-      if (KEYS && !wait_bar_warp(a.watch, b.full1 + 8 * st, ph, S_FULL)) return;
+      if (!wait_warp(a.watch, b.full0 + 8 * st, ph, S_FULL)) return;
+      if (KEYS && !wait_warp(a.watch, b.full1 + 8 * st, ph, S_FULL)) return;
       if (left < (KEYS ? used : BLK)) {
         for (int r = me; r < BLK; r += 64) {
           if (r < left) continue;
@@ -325,8 +325,8 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
       const bool all = __all_sync(0xffffffffu, from <= 0 && to >= 64);
       const float* stats = reinterpret_cast<const float*>(smem + L::STATS) + st * 256 + half * 64;
       float2 pr[32];
-      if (ok) ok = wait_bar_warp(a.watch, b.sfull + 8 * (n & 1u), n >> 1 & 1u, S_TFULL);
-      if (KEYS && ok) ok = wait_bar_warp(a.watch, b.fix + 8 * st, ph, S_FULL);
+      if (ok) ok = wait_warp(a.watch, b.sfull + 8 * (n & 1u), n >> 1 & 1u, S_TFULL);
+      if (KEYS && ok) ok = wait_warp(a.watch, b.fix + 8 * st, ph, S_FULL);
       if (ok) {
         tc_fence_after();
         uint32_t x[64];
@@ -363,8 +363,8 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
         __syncwarp();
         if (lane == 0) mbar_arrive(b.pfull);
       }
-      if (ok) ok = wait_bar_warp(a.watch, b.dpfull, n & 1u, S_TFULL);
-      if (!KEYS && ok) ok = wait_bar_warp(a.watch, b.fix + 8 * st, ph, S_FULL);
+      if (ok) ok = wait_warp(a.watch, b.dpfull, n & 1u, S_TFULL);
+      if (!KEYS && ok) ok = wait_warp(a.watch, b.fix + 8 * st, ph, S_FULL);
       if (ok) {
         tc_fence_after();
         uint32_t x[64], h[32];
@@ -398,7 +398,7 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
       }
     }
     // ---- the end of the part: one group writes dV, the other dK; or each its chunks of dQ
-    if (ok) ok = wait_bar_warp(a.watch, b.accfull, fn & 1u, S_TFULL);
+    if (ok) ok = wait_warp(a.watch, b.accfull, fn & 1u, S_TFULL);
     tc_fence_after();
     const bool second = KEYS && half == 1;
     const float scale = KEYS && !second ? 1.0f : a.scale;
@@ -407,28 +407,21 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
     const int64_t out_row = KEYS ? static_cast<int64_t>(w.s.k0) + w.tile * BLK + row : static_cast<int64_t>(w.s.q0) + tok;
     const int head = KEYS ? w.head : w.head * a.group + head_in;
     const int64_t slot = static_cast<int64_t>(KEYS ? 2 : 1) * BLK * a.dim;
-    float* part = a.part + part_slot(w) * slot + static_cast<int64_t>(second ? BLK : 0) * a.dim + static_cast<int64_t>(row) * a.dim;
-    if (ok)
-      for (int c = KEYS ? 0 : half; c < chunks; c += KEYS ? 1 : 2) {
-        uint32_t o[32];
-        tmem_ld32_sync(lanes + (second ? 3 : 2) * BLK + c * 32, o);
-        if (!valid) continue;
+    float* part = a.part + part_slot(w) * slot + static_cast<int64_t>(second ? BLK : 0) * a.dim;
+    uint8_t* stage = smem + L::STAGE + (warp - 4) * 2048;
+    const RowsOut to_rows = rows_out(valid && p.whole ? out + out_row * ld + head * hs : nullptr);
+#pragma unroll 1
+    for (int c = KEYS ? 0 : half; ok && c < chunks; c += KEYS ? 1 : 2) {
+      uint32_t o[32];
+      float v[32];
+      tmem_ld32_sync(lanes + (second ? 3 : 2) * BLK + c * 32, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int col = c * 32 + g * 8;
-          if (col >= a.dim) continue;
-          auto f = [&](int e) { return __uint_as_float(o[8 * g + e]); };
-          if (p.whole) {
-            *reinterpret_cast<uint4*>(out + out_row * ld + head * hs + col) =
-                make_uint4(pack_bf16(f(0), f(1)), pack_bf16(f(2), f(3)), pack_bf16(f(4), f(5)), pack_bf16(f(6), f(7)));
-          } else {
-            *reinterpret_cast<float4*>(part + col) = make_float4(f(0), f(1), f(2), f(3));
-            *reinterpret_cast<float4*>(part + col + 4) = make_float4(f(4), f(5), f(6), f(7));
-          }
-        }
-      }
+      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * scale;
+      if (p.whole)
+        store_rows(stage, v, to_rows, c * 32, a.dim - c * 32);
+      else if (valid)
+        store_part(part, BLK, row, v, c * 32, a.dim);
+    }
     tc_fence_before();
     if (p.whole) continue;
     // ---- a divided tile: whoever comes last adds its parts
@@ -444,31 +437,54 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
     bar_compute();
     if (*last) {
       __threadfence();
-      const int quads = a.dim / 4;
-      for (int i = me; i < (KEYS ? 2 : 1) * BLK * quads; i += COMPUTE) {
-        const int r = i / quads, col = (i - r * quads) * 4, in = r & (BLK - 1);
-        int64_t o_row;
-        int h = w.head;
-        bf16* to_out = KEYS && r >= BLK ? a.out1 : a.out0;
-        const int64_t old = KEYS && r >= BLK ? a.ld1 : a.ld0, ohs = KEYS && r >= BLK ? a.h1 : a.h0;
-        if constexpr (KEYS) {
-          if (w.tile * BLK + in >= w.s.nk) continue;
-          o_row = static_cast<int64_t>(w.s.k0) + w.tile * BLK + in;
-        } else {
-          const int d = in / a.group;
-          if (d >= a.tokens || w.tile * a.tokens + d >= w.s.nq) continue;
-          o_row = static_cast<int64_t>(w.s.q0) + w.tile * a.tokens + d;
-          h = w.head * a.group + in - d * a.group;
+      // a matrix's rows side by side, eight columns at a time, and two such groups
+      constexpr int U = 2;
+      const int groups = (KEYS ? 2 : 1) * BLK * (a.dim / 8);
+      for (int i0 = me; i0 < groups; i0 += U * COMPUTE) {
+        float4 v[U][2];
+        const float* src[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = min(i0 + u * COMPUTE, groups - 1);
+          v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          src[u] = a.part + (static_cast<int64_t>(2 * (i >> 7)) * BLK + (i & (BLK - 1))) * 4;
         }
-        float v[4] = {};
-#pragma unroll 4
-        for (int s = 0; s < shares; ++s) {
-          const float4 x = *reinterpret_cast<const float4*>(a.part + tile_slot(first, s) * slot +
-                                                            static_cast<int64_t>(r) * a.dim + col);
-          v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        auto add = [&](int s) {
+          const int64_t at = tile_slot(first, s) * slot;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 y = *reinterpret_cast<const float4*>(src[u] + at + j * BLK * 4);
+              v[u][j].x += y.x, v[u][j].y += y.y, v[u][j].z += y.z, v[u][j].w += y.w;
+            }
+        };
+        int s = 0;
+#pragma unroll 1
+        for (; s + 4 <= shares; s += 4) add(s), add(s + 1), add(s + 2), add(s + 3);
+        if (s + 2 <= shares) add(s), add(s + 1), s += 2;
+        if (s < shares) add(s);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * COMPUTE, in = i & (BLK - 1), g = i >> 7;
+          if (i >= groups) continue;
+          const bool two = KEYS && g >= a.dim / 8;  // the second matrix
+          const int col = (g - (two ? a.dim / 8 : 0)) * 8;
+          int64_t o_row;
+          int h = w.head;
+          if constexpr (KEYS) {
+            if (w.tile * BLK + in >= w.s.nk) continue;
+            o_row = static_cast<int64_t>(w.s.k0) + w.tile * BLK + in;
+          } else {
+            const int d = in / a.group;
+            if (d >= a.tokens || w.tile * a.tokens + d >= w.s.nq) continue;
+            o_row = static_cast<int64_t>(w.s.q0) + w.tile * a.tokens + d;
+            h = w.head * a.group + in - d * a.group;
+          }
+          *reinterpret_cast<uint4*>((two ? a.out1 : a.out0) + o_row * (two ? a.ld1 : a.ld0) + h * (two ? a.h1 : a.h0) + col) =
+              make_uint4(pack_bf16(v[u][0].x, v[u][0].y), pack_bf16(v[u][0].z, v[u][0].w),
+                         pack_bf16(v[u][1].x, v[u][1].y), pack_bf16(v[u][1].z, v[u][1].w));
         }
-        *reinterpret_cast<uint2*>(to_out + o_row * old + h * ohs + col) =
-            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
       }
     }
     bar_compute();

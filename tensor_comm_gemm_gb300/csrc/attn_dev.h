@@ -244,34 +244,98 @@ __device__ __forceinline__ int part_slot(const Walk& w) {
 }
 __device__ __forceinline__ int tile_slot(int first, int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
 
+// ------------------------------------------------------------------ waits
+
+// A converged warp's bounded wait.  The first tries (each of which the hardware may hold for a while) cost nothing
+// but the instruction itself; the clock is read only when they have failed.
+__device__ __forceinline__ bool wait_warp_long(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site) {
+  const unsigned long long t0 = gtime();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    if ((i & 15u) == 0u) {
+      int stop = 0;
+      if ((threadIdx.x & 31) == 0) {
+        if (*reinterpret_cast<volatile uint32_t*>(w.err) != 0u) {
+          stop = 1;
+        } else if (gtime() - t0 > w.limit_ns) {
+          give_up(w.err, site);
+          stop = 1;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_warp(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  return wait_warp_long(w, bar, parity, site);
+}
+
 // ------------------------------------------------------------------ matrix instructions
 
-// A K-major tile of 128 rows by up to 128 elements: blocks of 64 elements, 128-byte swizzle, 16 KiB each.  Start of
-// the 16 elements from 16 k on.
-__device__ __forceinline__ uint64_t desc_k(uint64_t d, int k) {
-  return d + static_cast<uint64_t>((k >> 2) * (16384 >> 4) + (k & 3) * 2);
-}
-// The same memory as an MN-major operand (its 128 rows are the contraction): 64 elements further on the next block.
+// A tile of 128 rows by up to 128 elements lies in blocks of 64 elements, 128-byte swizzle, 16 KiB each.  As a K-major
+// operand a block is one of smem_desc_sw128.
+// As an MN-major operand (the 128 rows are the contraction): 64 elements further on the next block.
 __device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
   uint64_t v = smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
   return v | (static_cast<uint64_t>(16384 >> 4) << 16);
 }
 
-// D[tensor memory] (+)= A . B^T, 16 contraction elements, bf16, one elected lane of a converged warp; A in shared
-// memory or in tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D[tensor memory] (+)= A . B^T over `count` (1 to 4) times 16 contraction elements, bf16; a whole converged warp, in
+// which one elected lane issues.  All four in one statement: one at a time, with the descriptors' arithmetic between
+// them, an instruction took about 120 cycles to issue, and the tensor core needs 64 for it.
+// Both operands K-major in shared memory: a block of 64 elements.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, int count) {
   asm volatile(
-      "{\n\t.reg .pred E, A;\n\t.reg .b32 r;\n\tsetp.ne.b32 A, %4, 0;\n\telect.sync r|E, 0xffffffff;\n\t"
-      "@E tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, A;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+      "{\n\t.reg .pred E, A, T, P1, P2, P3;\n\t.reg .b32 r;\n\tsetp.ne.b32 A, %4, 0;\n\tsetp.ne.b32 T, 1, 0;\n\t"
+      "elect.sync r|E, 0xffffffff;\n\tsetp.gt.and.s32 P1, %5, 1, E;\n\tsetp.gt.and.s32 P2, %5, 2, E;\n\t"
+      "setp.gt.and.s32 P3, %5, 3, E;\n\t"
+      "@E tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, A;\n\t"
+      "@P1 tcgen05.mma.cta_group::1.kind::f16 [%0], %6, %7, %3, T;\n\t"
+      "@P2 tcgen05.mma.cta_group::1.kind::f16 [%0], %8, %9, %3, T;\n\t"
+      "@P3 tcgen05.mma.cta_group::1.kind::f16 [%0], %10, %11, %3, T;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(count), "l"(a + 2), "l"(b + 2), "l"(a + 4), "l"(b + 4), "l"(a + 6),
+      "l"(b + 6));
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// A in tensor memory (8 columns each time), B MN-major (16 rows each time): 64 contraction elements.
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred E, A;\n\t.reg .b32 r;\n\tsetp.ne.b32 A, %4, 0;\n\telect.sync r|E, 0xffffffff;\n\t"
-      "@E tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, A;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+      "{\n\t.reg .pred E, A, T;\n\t.reg .b32 r;\n\tsetp.ne.b32 A, %4, 0;\n\tsetp.ne.b32 T, 1, 0;\n\t"
+      "elect.sync r|E, 0xffffffff;\n\t"
+      "@E tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, A;\n\t"
+      "@E tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %6, %3, T;\n\t"
+      "@E tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %8, %3, T;\n\t"
+      "@E tcgen05.mma.cta_group::1.kind::f16 [%0], [%9], %10, %3, T;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(a + 8), "l"(b + 128), "r"(a + 16), "l"(b + 256), "r"(a + 24),
+      "l"(b + 384));
+}
+// All of a head's elements: blocks of 64, `ksteps` times 16 of them.
+template <int DP>
+__device__ __forceinline__ void mma_head(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int ksteps) {
+  mma4_ss(d, a, b, idesc, 0u, ksteps);
+  if (DP == 128) mma4_ss(d, a + (16384 >> 4), b + (16384 >> 4), idesc, 1u, ksteps - 4);
 }
 
+__device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -309,9 +373,56 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
+// The largest of three; NaN only if all are.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// ------------------------------------------------------------------ results
+
+// A warp stores 32 columns of its 32 rows (v: the lane's row) as bf16, through 2 KiB of shared memory at `stage`:
+// row by row 64 bytes of a line at a time.  (Each lane storing 16 bytes of its own row costs a cycle of the SM's
+// memory pipe for each lane, 7000 for the 256 rows of a tile.)  to[i], where rows (lane / 4 + 8 i) go, 0: nowhere;
+// `cols` of the 32 exist.
+struct RowsOut {
+  uint64_t to[4];
+};
+__device__ __forceinline__ RowsOut rows_out(const void* mine) {  // mine: the lane's own row, NULL: none
+  RowsOut r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r.to[i] = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), ((threadIdx.x & 31) >> 2) + 8 * i);
+  return r;
+}
+__device__ __forceinline__ void store_rows(uint8_t* stage, const float (&v)[32], const RowsOut& r, int col, int cols) {
+  const int lane = threadIdx.x & 31, part = lane & 3;
+  __syncwarp();  // the chunk before has been read
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(pack_bf16(v[8 * g], v[8 * g + 1]), pack_bf16(v[8 * g + 2], v[8 * g + 3]),
+                   pack_bf16(v[8 * g + 4], v[8 * g + 5]), pack_bf16(v[8 * g + 6], v[8 * g + 7]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = (lane >> 2) + 8 * i;
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 64 + ((part ^ ((row >> 1) & 3)) << 4));
+    if (r.to[i] && part * 8 < cols) *reinterpret_cast<uint4*>(r.to[i] + (col + part * 8) * 2) = x;
+  }
+}
+// Parts of divided tiles lie as [dim / 4][rows][4] floats: a warp's 32 rows side by side.
+__device__ __forceinline__ void store_part(float* part, int rows, int row, const float (&v)[32], int col, int dim) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+    if (col + 4 * g < dim)
+      *reinterpret_cast<float4*>(part + (static_cast<int64_t>((col >> 2) + g) * rows + row) * 4) =
+          make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
 }
 
 // ------------------------------------------------------------------ host side

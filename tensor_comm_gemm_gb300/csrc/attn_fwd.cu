@@ -37,6 +37,7 @@ using bf16 = __nv_bfloat16;
 constexpr int THREADS = 384;
 constexpr int SOFTMAX = 256;             // threads of the two softmax groups
 constexpr float GROWTH = 8.0f;           // of the maximum, in powers of two, before O is rescaled
+constexpr int JOIN = 2048;               // parts of rows whose weights are in shared memory at a time
 constexpr int BAD_SETS = 8, BAD_STEPS = 3;  // steps of a tile that only some of its rows see whole
 
 struct Args {
@@ -73,12 +74,14 @@ struct Layout {
   static constexpr int TILE = BLK * DP * 2;          // 128 rows of a head
   static constexpr int STAGES = DP == 128 ? 2 : 4;   // of K, and of V
   static constexpr int K0 = 2 * TILE, V0 = K0 + STAGES * TILE, BARS = V0 + STAGES * TILE;
-  static constexpr int N_BARS = 5 * STAGES + 9;
+  static constexpr int N_BARS = 5 * STAGES + 11;
   static constexpr int SLOT = BARS + 8 * N_BARS;
   static constexpr int LAST = SLOT + 4;
   static constexpr int BAD = SLOT + 8;               // [BAD_SETS][BAD_STEPS][4] keys, a bit each
-  static constexpr int ROWS = BAD + BAD_SETS * BAD_STEPS * 16;  // [2][256] floats: maxima and sums, or their joins
-  static constexpr int PLAN = (ROWS + 2048 + 15) / 16 * 16;
+  static constexpr int ROWS = (BAD + BAD_SETS * BAD_STEPS * 16 + 15) / 16 * 16;  // [2][256] floats: maxima and sums
+  static constexpr int JOIN_AT = ROWS + 2048;        // [2][JOIN] floats
+  static constexpr int PLAN = JOIN_AT + 8 * JOIN;
+  static_assert(JOIN_AT % 16 == 0 && 8 * JOIN >= 8 * 2048, "also a staging box for each warp");
   static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
   static_assert(SMEM <= 232448, "shared memory of one block");
 };
@@ -114,7 +117,7 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
   for (walk_begin(tiles, a.seq, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
     const Item it = item_of(a, w);
     const int q_head = w.head * a.group;
-    if (!(ok = wait_bar_warp(a.watch, qempty, (qn & 1u) ^ 1u, S_EMPTY))) break;
+    if (!(ok = wait_warp(a.watch, qempty, (qn & 1u) ^ 1u, S_EMPTY))) break;
     if (lead) {
       const uint32_t box = static_cast<uint32_t>(a.group * a.tokens) * 128u;
       mbar_expect_tx(qfull, box * (DP / 64) * it.halves);
@@ -127,7 +130,7 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
     ++qn;
     auto load = [&](const CUtensorMap* map, uint32_t full, uint32_t empty, uint32_t base, uint32_t& n, int j) {
       const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
-      if (!wait_bar_warp(a.watch, empty + 8 * st, ph ^ 1u, S_EMPTY)) return false;
+      if (!wait_warp(a.watch, empty + 8 * st, ph ^ 1u, S_EMPTY)) return false;
       if (lead) {
         mbar_expect_tx(full + 8 * st, L::TILE);
         for (int d = 0; d < DP / 64; ++d)
@@ -160,29 +163,29 @@ __device__ void mma_role(const Args& a, const Tiles& tiles, const Shares& sh, ui
   using L = Layout<DP>;
   const uint32_t kfull = sbase + L::BARS, kempty = kfull + 8 * L::STAGES, vfull = kempty + 8 * L::STAGES,
                  vempty = vfull + 8 * L::STAGES, vfix = vempty + 8 * L::STAGES, qfull = vfix + 8 * L::STAGES,
-                 qempty = qfull + 8, sfull = qempty + 8, pfull = sfull + 16, ofull = pfull + 16, drain = ofull + 16;
+                 qempty = qfull + 8, sfull = qempty + 8, pfull = sfull + 16, ofull = pfull + 32, drain = ofull + 16;
   const int ksteps = (a.dim + 15) / 16;
   const uint32_t idesc_s = idesc_n(make_idesc(false, BLK), BLK);
   const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), ksteps * 16) | 1u << 16;
   const uint64_t dq = smem_desc_sw128(sbase), dk = smem_desc_sw128(sbase + L::K0), dv = desc_rows(sbase + L::V0);
-  uint32_t kn = 0, vn = 0, qn = 0, pn[2] = {0, 0};
+  uint32_t kn = 0, vn = 0, qn = 0, pn0 = 0, pn1 = 0;
   uint32_t fixed[L::STAGES] = {};
   bool ok = true;
   Walk w;
   for (walk_begin(tiles, a.seq, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
     const Item it = item_of(a, w);
     const int steps = it.p.hi - it.p.lo, units = it.halves * steps;
-    if (!(ok = wait_bar_warp(a.watch, qfull, qn & 1u, S_FULL))) break;
+    if (!(ok = wait_warp(a.watch, qfull, qn & 1u, S_FULL))) break;
     ++qn;
     // unit u: half (or turn) u & 1 of a step
     auto scores = [&](int u) {
       const bool first = it.halves == 1 || !(u & 1), last = it.halves == 1 || (u & 1);
       const uint32_t st = kn % L::STAGES;
-      if (first && !wait_bar_warp(a.watch, kfull + 8 * st, kn / L::STAGES & 1u, S_FULL)) return false;
+      if (first && !wait_warp(a.watch, kfull + 8 * st, kn / L::STAGES & 1u, S_FULL)) return false;
       tc_fence_after();
       const uint32_t half = u & 1;
       const uint64_t qd = dq + (it.halves == 2 ? half * (L::TILE >> 4) : 0u), kd = dk + st * (L::TILE >> 4);
-      for (int k = 0; k < ksteps; ++k) mma_ss(tmem + half * BLK, desc_k(qd, k), desc_k(kd, k), idesc_s, k > 0);
+      mma_head<DP>(tmem + half * BLK, qd, kd, idesc_s, ksteps);
       mma_commit_cg<1>(sfull + 8 * half);
       if (last) mma_commit_cg<1>(kempty + 8 * st), ++kn;
       if (u == units - 1) mma_commit_cg<1>(qempty);
@@ -194,24 +197,26 @@ __device__ void mma_role(const Args& a, const Tiles& tiles, const Shares& sh, ui
       const bool first = it.halves == 1 || !half, last = it.halves == 1 || half;
       const int j = it.p.lo + (it.halves == 1 ? u : u >> 1);
       const uint32_t st = vn % L::STAGES;
-      if (!(ok = wait_bar_warp(a.watch, pfull + 8 * half, pn[half] & 1u, S_FULL))) break;
-      ++pn[half];
+      const uint32_t turn = half ? pn1++ : pn0++;
+      if (!(ok = wait_warp(a.watch, pfull + 16 * half, turn & 1u, S_FULL))) break;
       if (first) {
-        if (!(ok = wait_bar_warp(a.watch, vfull + 8 * st, vn / L::STAGES & 1u, S_FULL))) break;
+        if (!(ok = wait_warp(a.watch, vfull + 8 * st, vn / L::STAGES & 1u, S_FULL))) break;
         if (needs_fix(it, j)) {
           uint32_t n = 0;
 #pragma unroll
           for (int i = 0; i < L::STAGES; ++i)
             if (i == static_cast<int>(st)) n = fixed[i]++;
-          if (!(ok = wait_bar_warp(a.watch, vfix + 8 * st, n & 1u, S_FULL))) break;
+          if (!(ok = wait_warp(a.watch, vfix + 8 * st, n & 1u, S_FULL))) break;
         }
       }
       tc_fence_after();
       const uint64_t vd = dv + st * (L::TILE >> 4);
       const uint32_t p = tmem + half * BLK, o = tmem + 2 * BLK + half * BLK;
       const bool fresh = u < 2;  // this half's first product of the part
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mma_ts(o, p + 8 * k, vd + 128u * k, idesc_o, !fresh || k > 0);
+      mma4_ts(o, p, vd, idesc_o, !fresh);
+      if (!(ok = wait_warp(a.watch, pfull + 16 * half + 8, turn & 1u, S_FULL))) break;
+      tc_fence_after();
+      mma4_ts(o, p + 64, vd + 512, idesc_o, 1u);
       if (u >= units - 2) mma_commit_cg<1>(ofull + 8 * half);
       if (last) mma_commit_cg<1>(vempty + 8 * st), ++vn;
       if (u + 2 < units) ok = scores(u + 2);
@@ -240,7 +245,7 @@ __device__ void fix_role(const Args& a, const Tiles& tiles, const Shares& sh, ui
     __syncwarp();
     for (int j = it.p.lo; j < it.p.hi; ++j, ++vn) {
       const uint32_t st = vn % L::STAGES;
-      if (!wait_bar_warp(a.watch, vfull + 8 * st, vn / L::STAGES & 1u, S_FULL)) return;
+      if (!wait_warp(a.watch, vfull + 8 * st, vn / L::STAGES & 1u, S_FULL)) return;
       if (needs_fix(it, j)) {
         uint8_t* v = smem + L::V0 + st * L::TILE;
 #pragma unroll 1
@@ -292,7 +297,7 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
                              uint32_t tmem) {
   using L = Layout<DP>;
   const uint32_t qempty = sbase + L::BARS + 40 * L::STAGES + 8, sfull = qempty + 8, pfull = sfull + 16,
-                 ofull = pfull + 16;
+                 ofull = pfull + 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, half = (warp - 4) >> 2;
   const int row = quad * 32 + lane, me = threadIdx.x - 128;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -314,70 +319,82 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
     float m = -INFINITY, l = 0.0f;  // the maximum that is subtracted (in powers of two), the sum
     const int first = it.halves == 2 ? 0 : half, by = it.halves == 2 ? 1 : 2;
     for (int i = first; i < steps; i += by, ++sn) {
-      if (ok) ok = wait_bar_warp(a.watch, sfull + 8 * half, sn & 1u, S_TFULL);
-      if (ok && !idle) {
-        tc_fence_after();
-        uint32_t x[64], y[64];
-        tmem_ld64_sync(ts, x);
-        tmem_ld64_sync(ts + 64, y);
-        const int left = limit - (it.p.lo + i) * BLK;
-        if (!__all_sync(0xffffffffu, left >= BLK)) {
+      if (ok) ok = wait_warp(a.watch, sfull + 8 * half, sn & 1u, S_TFULL);
+      auto arrive = [&](uint32_t bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      };
+      if (!ok || idle) {
+        arrive(pfull + 16 * half);
+        arrive(pfull + 16 * half + 8);
+        continue;
+      }
+      // Half of the scores at a time, each read twice, first for the maximum: a thread holds 64 of them and not 128, and
+      // the code is short (its first pass runs at the speed of the instruction fetches).  A half's weights go over its
+      // own columns, and the product with the first half's runs beside the second's.
+      uint32_t x[64];
+      const int left = limit - (it.p.lo + i) * BLK;
+      const bool all = __all_sync(0xffffffffu, left >= BLK);
+      auto read = [&](int from) {
+        tmem_ld64_sync(ts + from, x);
+        if (!all) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            if (e >= left) x[e] = 0xff800000u;
-            if (e + 64 >= left) y[e] = 0xff800000u;
-          }
+          for (int e = 0; e < 64; ++e)
+            if (from + e >= left) x[e] = 0xff800000u;
         }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      };
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tc_fence_after();
+#pragma unroll 1
+      for (int from = 0; from < BLK; from += 64) {
+        read(from);
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
+        for (int e = 0; e < 64; e += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[e + k]), __uint_as_float(y[e + k])));
-        }
-        const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.c;
-        const bool grow = peak > m + GROWTH;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? exp2_fast(m - peak) : 1.0f;  // from -infinity: 0
-          if (grow) m = peak;
-          l *= f;
-          if (i != first) {  // the products before this step's scores are done
-            for (int c = 0; c < chunks; ++c) {
-              uint32_t o[32];
-              tmem_ld32_sync(to + c * 32, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(to + c * 32, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        const float sub = m == -INFINITY ? 0.0f : -m;
-        const float2 sub2 = make_float2(sub, sub);
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        auto weights = [&](uint32_t(&z)[64], uint32_t to_col) {
-          uint32_t h[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 s = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2, sub2);
-            const float2 p = make_float2(exp2_fast(s.x), exp2_fast(s.y));
-            sum[e & 1] = add2(sum[e & 1], p);
-            h[e] = pack_bf16(p.x, p.y);
-          }
-          tmem_st32(ts + to_col, h);
-        };
-        weights(x, 0);
-        weights(y, 32);
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_wait_st();
+            top[k] = max3(top[k], __uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pfull + 8 * half);
+      const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.c;
+      const bool grow = peak > m + GROWTH;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? exp2_fast(m - peak) : 1.0f;  // from -infinity: 0
+        if (grow) m = peak;
+        l *= f;
+        if (i != first) {  // the products before this step's scores are done
+#pragma unroll 1
+          for (int c = 0; c < 2 * chunks; ++c) {
+            uint32_t o[16];
+            tmem_ld16_sync(to + c * 16, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(to + c * 16, o);
+          }
+        }
+      }
+      const float sub = m == -INFINITY ? 0.0f : -m;
+      const float2 sub2 = make_float2(sub, sub);
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+      for (int from = 0; from < BLK; from += 64) {
+        read(from);
+        uint32_t h[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float2 s = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, sub2);
+          const float2 p = make_float2(exp2_fast(s.x), exp2_fast(s.y));
+          sum[e & 1] = add2(sum[e & 1], p);
+          h[e] = pack_bf16(p.x, p.y);
+        }
+        tmem_st32(ts + from, h);
+        tmem_wait_st();
+        arrive(pfull + 16 * half + from / 8);
+      }
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     // ---- the end of the part
     if (steps > first) {
-      if (ok) ok = wait_bar_warp(a.watch, ofull + 8 * half, on & 1u, S_TFULL);
+      if (ok) ok = wait_warp(a.watch, ofull + 8 * half, on & 1u, S_TFULL);
       ++on;
     }
     tc_fence_after();
@@ -403,60 +420,41 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
     const int prow = it.halves == 2 ? half * BLK + row : row;
     float* part = a.part + static_cast<int64_t>(part_slot(w)) * a.part_rows * (a.dim + 2);
     const float scale = !it.p.whole ? 1.0f : l == 0.0f ? (limit > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / l;
-    if (ok && !idle)
-      for (int c = it.halves == 1 ? half : 0; c < chunks; c += by) {
-        uint32_t o[32];
-        float v[32];
+    uint8_t* stage = smem + L::JOIN_AT + (warp - 4) * 2048;
+    const RowsOut to_rows = rows_out(valid && it.p.whole ? a.out + q_row * a.ldo + head * a.ho : nullptr);
+    const float f0 = (it.halves == 1 ? w0 : 1.0f) * scale, f1 = w1 * scale;
+#pragma unroll 1
+    for (int c = it.halves == 1 ? half : 0; ok && c < chunks; c += by) {
+      uint32_t o[32];
+      float v[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+      if (!idle) {  // an accumulator that does not count may hold anything
         tmem_ld32_sync((it.halves == 1 ? lanes + 2 * BLK : to) + c * 32, o);
-        const float f0 = it.halves == 1 ? w0 : 1.0f;
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
         if (two) {
           tmem_ld32_sync(lanes + 3 * BLK + c * 32, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] += w1 == 0.0f ? 0.0f : __uint_as_float(o[e]) * w1;
-        }
-        if (any_bad)  // the noted values, for a row that sees their keys
-          for (int i = 0; i < BAD_STEPS * 4; ++i)
-            for (uint32_t left = bad[i]; left; left &= left - 1) {
-              const int key = it.some / BLK * BLK + 32 * i + __ffs(left) - 1;
-              if (key >= limit) continue;
-              const bf16* x = a.values + (static_cast<int64_t>(w.s.k0) + key) * a.ldv + w.head * a.hv + c * 32;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float f = c * 32 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
-                if (!isfinite(f)) v[e] += f;
-              }
-            }
-        if (!valid) continue;
-        if (it.p.whole) {
-          bf16* to_row = a.out + q_row * a.ldo + head * a.ho + c * 32;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = limit > 0 ? v[e] * scale : 0.0f;
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (c * 32 + g * 8 < a.dim)
-              *reinterpret_cast<uint4*>(to_row + g * 8) =
-                  make_uint4(pack_bf16(v[8 * g], v[8 * g + 1]), pack_bf16(v[8 * g + 2], v[8 * g + 3]),
-                             pack_bf16(v[8 * g + 4], v[8 * g + 5]), pack_bf16(v[8 * g + 6], v[8 * g + 7]));
-        } else {
-          float* to_row = part + static_cast<int64_t>(prow) * a.dim + c * 32;
-#pragma unroll
-          for (int g = 0; g < 8; ++g)
-            if (c * 32 + g * 4 < a.dim)
-              *reinterpret_cast<float4*>(to_row + g * 4) = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+          for (int e = 0; e < 32; ++e) v[e] += f1 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f1;
         }
       }
-    else if (ok && valid) {  // rows of a warp without keys
-      for (int c = it.halves == 1 ? half : 0; c < chunks; c += by)
-        for (int g = 0; g < 8; ++g) {
-          if (c * 32 + g * 4 >= a.dim) continue;
-          if (it.p.whole)
-            *reinterpret_cast<uint2*>(a.out + q_row * a.ldo + head * a.ho + c * 32 + g * 4) = make_uint2(0, 0);
-          else
-            *reinterpret_cast<float4*>(part + static_cast<int64_t>(prow) * a.dim + c * 32 + g * 4) =
-                make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
+      if (any_bad)  // the noted values, for a row that sees their keys
+        for (int i = 0; i < BAD_STEPS * 4; ++i)
+          for (uint32_t left = bad[i]; left; left &= left - 1) {
+            const int key = it.some / BLK * BLK + 32 * i + __ffs(left) - 1;
+            if (key >= limit) continue;
+            const bf16* x = a.values + (static_cast<int64_t>(w.s.k0) + key) * a.ldv + w.head * a.hv + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float f = c * 32 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
+              if (!isfinite(f)) v[e] += f;
+            }
+          }
+      if (it.p.whole)
+        store_rows(stage, v, to_rows, c * 32, a.dim - c * 32);
+      else if (valid)
+        store_part(part, a.part_rows, prow, v, c * 32, a.dim);
     }
     if (ok && valid && (it.halves == 2 || half == 0)) {
       if (!it.p.whole) {
@@ -486,48 +484,89 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
       continue;
     }
     __threadfence();
-    const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2);
-    const int count = it.halves == 2 ? 2 * BLK : BLK;
+    const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), stats = static_cast<int64_t>(a.part_rows) * a.dim;
     auto place = [&](int r, int* tok, int* h) {  // of row r of the tile
       const int in = r & (BLK - 1), dtok = in / a.group;
       *tok = it.tok + (r >> 7) * a.tokens + dtok;
       *h = w.head * a.group + in - dtok * a.group;
       return dtok < a.tokens && *tok < w.s.nq;
     };
-    if (me < count) {
-      int tok, h;
-      if (place(me, &tok, &h)) {
-        const int lim = keys_seen(w.s, tok, a.causal);
+    // as many rows at a time as their parts' weights find room: a warp makes a row's weights, then every thread adds
+    // four columns of some rows
+    const int left = w.s.nq - it.tok;
+    const int count = left <= a.tokens ? left * a.group : left < 2 * a.tokens ? BLK + (left - a.tokens) * a.group : 2 * BLK;
+    const int batch = min(count, JOIN / shares);
+    float* table = reinterpret_cast<float*>(smem + L::JOIN_AT);
+    for (int r0 = 0; r0 < count; r0 += batch) {
+      const int rows_now = min(batch, count - r0);
+      for (int i = me; i < rows_now * shares; i += SOFTMAX) {
+        const int s = i / rows_now, r = i - s * rows_now;
+        const float* ml = a.part + tile_slot(from, s) * slot + stats + r0 + r;
+        table[r * shares + s] = ml[0];
+        table[JOIN + r * shares + s] = ml[a.part_rows];
+      }
+      bar_softmax();
+      for (int r = warp - 4; r < rows_now; r += SOFTMAX / 32) {
+        float* tm = table + r * shares;
         float top = -INFINITY, sum = 0.0f;
-        for (int i = 0; i < shares; ++i)
-          top = fmaxf(top, a.part[tile_slot(from, i) * slot + static_cast<int64_t>(a.part_rows) * a.dim + me]);
+        for (int s = lane; s < shares; s += 32) top = fmaxf(top, tm[s]);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float base = top == -INFINITY ? 0.0f : top;
-        for (int i = 0; i < shares; ++i) {
-          const float* ml = a.part + tile_slot(from, i) * slot + static_cast<int64_t>(a.part_rows) * a.dim + me;
-          sum += ml[a.part_rows] * exp2_fast(ml[0] - base);
+        for (int s = lane; s < shares; s += 32) {
+          const float f = exp2_fast(tm[s] - base);
+          sum += tm[JOIN + s] * f;
+          tm[s] = f;
         }
-        rows[me] = base;
-        rows[256 + me] = lim == 0 ? 0.0f : sum == 0.0f ? __uint_as_float(0x7fc00000u) : 1.0f / sum;
-        if (a.lse) a.lse[(static_cast<int64_t>(w.s.q0) + tok) * a.heads + h] = lim > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        int tok, h;
+        if (!place(r0 + r, &tok, &h)) continue;
+        const int lim = keys_seen(w.s, tok, a.causal);
+        const float inv = lim == 0 ? 0.0f : sum == 0.0f ? __uint_as_float(0x7fc00000u) : 1.0f / sum;
+        for (int s = lane; s < shares; s += 32) tm[s] *= inv;
+        if (a.lse && lane == 0)
+          a.lse[(static_cast<int64_t>(w.s.q0) + tok) * a.heads + h] = lim > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
       }
-    }
-    bar_softmax();
-    const int quads = a.dim / 4;
-    for (int i = me; i < count * quads; i += SOFTMAX) {
-      const int r = i / quads, col = (i - r * quads) * 4;
-      int tok, h;
-      if (!place(r, &tok, &h)) continue;
-      const float base = rows[r], inv = rows[256 + r];
-      float v[4] = {};
-#pragma unroll 8
-      for (int s = 0; s < shares; ++s) {
-        const float* p = a.part + tile_slot(from, s) * slot;
-        const float4 x = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(r) * a.dim + col);
-        const float f = exp2_fast(p[static_cast<int64_t>(a.part_rows) * a.dim + r] - base);
-        v[0] += x.x * f, v[1] += x.y * f, v[2] += x.z * f, v[3] += x.w * f;
+      bar_softmax();
+      constexpr int U = 2;  // two groups of eight columns at a time
+      const int groups = rows_now * (a.dim / 8);
+      for (int i0 = me; i0 < groups; i0 += U * SOFTMAX) {
+        float4 v[U][2];
+        const float *src[U], *f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = min(i0 + u * SOFTMAX, groups - 1), g = i / rows_now, r = i - g * rows_now;
+          v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          f[u] = table + r * shares;
+          src[u] = a.part + (static_cast<int64_t>(2 * g) * a.part_rows + r0 + r) * 4;
+        }
+        auto add = [&](int s) {
+          const int64_t at = tile_slot(from, s) * slot;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float k = f[u][s];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 y = *reinterpret_cast<const float4*>(src[u] + at + static_cast<int64_t>(j) * a.part_rows * 4);
+              v[u][j].x += y.x * k, v[u][j].y += y.y * k, v[u][j].z += y.z * k, v[u][j].w += y.w * k;
+            }
+          }
+        };
+        int s = 0;
+#pragma unroll 1
+        for (; s + 4 <= shares; s += 4) add(s), add(s + 1), add(s + 2), add(s + 3);
+        if (s + 2 <= shares) add(s), add(s + 1), s += 2;
+        if (s < shares) add(s);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * SOFTMAX, g = i / rows_now, r = i - g * rows_now;
+          int tok, h;
+          if (i < groups && place(r0 + r, &tok, &h))
+            *reinterpret_cast<uint4*>(a.out + (static_cast<int64_t>(w.s.q0) + tok) * a.ldo + h * a.ho + g * 8) =
+                make_uint4(pack_bf16(v[u][0].x, v[u][0].y), pack_bf16(v[u][0].z, v[u][0].w),
+                           pack_bf16(v[u][1].x, v[u][1].y), pack_bf16(v[u][1].z, v[u][1].w));
+        }
       }
-      *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(w.s.q0) + tok) * a.ldo + h * a.ho + col) =
-          make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+      bar_softmax();
     }
     bar_softmax();
   }
@@ -553,7 +592,7 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
     init(L::STAGES, 2);      // vfix
     init(2, 1);              // qfull, qempty
     init(2, 1);              // sfull
-    init(2, 4);              // pfull: the half's warps
+    init(4, 4);              // pfull: the half's warps, 64 keys at a time
     init(2, 1);              // ofull
     init(1, 1);              // drain
     fence_barrier_init();
