@@ -122,7 +122,7 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
   uint32_t n = 0, n1 = 0, fn = 0;  // loads so far
   bool ok = true;
   Walk w;
-  for (walk_begin(tiles, a.seq, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
+  for (walk_begin(tiles, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
     const Part p = walk_part(w);
     const int qh = w.head * a.group, kh = w.head;
     auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int head, int row) {
@@ -181,7 +181,7 @@ __device__ void mma_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& 
   uint32_t n = 0, fn = 0;  // steps and parts so far
   bool ok = true;
   Walk w;
-  for (walk_begin(tiles, a.seq, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w), ++fn) {
+  for (walk_begin(tiles, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w), ++fn) {
     const Part p = walk_part(w);
     const int steps = p.hi - p.lo;
     auto stage = [&](uint32_t s) { return static_cast<uint64_t>(s % L::STAGES) * (L::TILE >> 4); };
@@ -190,14 +190,14 @@ __device__ void mma_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& 
       if (!wait_warp(a.watch, b.full0 + 8 * (s % L::STAGES), s / L::STAGES & 1u, S_FULL)) return false;
       tc_fence_after();
       const uint32_t d = KEYS || !(s & 1u) ? tmem : acc1;
-      mma_head<DP>(d, f0, r0 + stage(s), idesc_s, ksteps);
+      mma_head<DP>(d, f0, r0 + stage(s), idesc_s);
       mma_commit_cg<1>(b.sfull + 8 * (s & 1u));  // two: the threads may still be at the step before
       return true;
     };
     auto dots = [&](uint32_t s) {
       if (!wait_warp(a.watch, b.full1 + 8 * (s % L::STAGES), s / L::STAGES & 1u, S_FULL)) return false;
       tc_fence_after();
-      mma_head<DP>(dp, f1, r1 + stage(s), idesc_s, ksteps);
+      mma_head<DP>(dp, f1, r1 + stage(s), idesc_s);
       mma_commit_cg<1>(b.dpfull);
       return true;
     };
@@ -249,7 +249,7 @@ __device__ void aux_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& 
   const int used = a.group * a.tokens;
   uint32_t n = 0;
   Walk w;
-  for (walk_begin(tiles, a.seq, sh, w); walk_has(w); walk_next(tiles, a.seq, w)) {
+  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w)) {
     const Part p = walk_part(w);
     for (int j = p.lo; j < p.hi; ++j, ++n) {
       const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
@@ -305,7 +305,7 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
   uint32_t n = 0, fn = 0;
   bool ok = true;
   Walk w;
-  for (walk_begin(tiles, a.seq, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++fn) {
+  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++fn) {
     const Part p = walk_part(w);
     // KEYS: this row's key, and the first token that sees it; otherwise the row's query and the keys that it sees
     const int tok = w.tile * a.tokens + dt;
@@ -427,7 +427,8 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
     // ---- a divided tile: whoever comes last adds its parts
     __threadfence();
     bar_compute();
-    const int first = share_of(sh, p.begin), shares = share_of(sh, p.end - 1) - first + 1;
+    int first;
+    const int shares = tile_shares(sh, w, &first);
     volatile int* last = reinterpret_cast<volatile int*>(smem + L::LAST);
     if (me == 0) {
       const uint32_t before = atomicAdd(a.arrivals + first, ok ? 1u : 0u);
@@ -496,7 +497,8 @@ template <int DP, bool KEYS>
 __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__ Args a) {
   using L = Layout<DP>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
   grid_dep_launch();
   const int warp = threadIdx.x >> 5;
@@ -541,14 +543,14 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
   grid_dep_wait();
   const Tiles<KEYS> tiles{a.kv_heads, a.tokens, a.causal};
   plan_shares<THREADS>(tiles, a.seq, plan);
-  const Shares sh = plan->shares;
+  const Shares& sh = plan->shares;
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
     if (warp == 0) load_role<DP, KEYS>(a, tiles, sh, sbase);
     if (warp == 1) mma_role<DP, KEYS>(a, tiles, sh, sbase, tmem);
     if (warp >= 2) aux_role<DP, KEYS>(a, tiles, sh, sbase, smem);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
     compute_role<DP, KEYS>(a, tiles, sh, sbase, smem, tmem);
   }
   tc_fence_before();

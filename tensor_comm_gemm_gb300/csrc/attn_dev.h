@@ -27,32 +27,39 @@ constexpr float kLog2e = 1.4426950408889634074f, kLn2 = 0.69314718055994530942f;
 
 // A share's place in the list, tile by tile.
 struct Walk {
-  // the share
-  int64_t at, end;  // steps of the whole list
-  // where it is
+  int done, left;   // steps of the share before this tile, and from here on
+  int off;          // steps of the tile that an earlier share has
   int seq, head, tile, tiles;
   Seq s;
   int lo, hi;       // the tile's steps
-  int64_t begin;    // of the tile, in the list
+};
+// The share's steps of a tile.
+struct Part {
+  int lo, hi;
+  bool whole;
 };
 
-struct Part {
-  int lo, hi;           // steps of this share
-  bool whole;
-  int64_t begin, end;   // of the tile, in the list
-};
+// a / b for numbers that mostly have 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 struct Shares {
-  int64_t total;    // steps
-  int count;        // shares
-  int seq;          // where this block's share begins: sequence,
-  int64_t before;   // and steps ahead of the sequence
+  int64_t total, each;  // steps in all and of a share; the first `more` have one more
+  int count, more;
+  int64_t at, end;      // this block's share
+  int seq;              // where it begins: sequence,
+  int64_t before;       // steps ahead of the sequence,
+  int64_t a_head;       // and steps of one of its key heads
+  Seq s;
 };
 
-__device__ __forceinline__ int64_t share_begin(const Shares& p, int64_t c) { return c * p.total / p.count; }
+__device__ __forceinline__ int64_t share_begin(const Shares& p, int c) { return c * p.each + min(c, p.more); }
 // The share that holds step x.
 __device__ __forceinline__ int share_of(const Shares& p, int64_t x) {
-  return static_cast<int>(((x + 1) * p.count - 1) / p.total);
+  const int64_t longer = p.more * (p.each + 1);
+  return static_cast<int>(x < longer ? quotient(x, p.each + 1) : p.more + quotient(x - longer, p.each));
 }
 
 // Steps of all tiles of a sequence (one key head), by a converged warp.
@@ -68,118 +75,108 @@ __device__ __forceinline__ int64_t steps_by_warp(const T& t, const Seq& s, int t
   return sum;
 }
 
-// Steps of sequence i over all key heads; every thread of the block calls it,
-// with its own i (at or past `batch`: none), and `tiles` gets the tiles' number.
+// Steps of sequence i for one key head; every thread of the block calls it, with
+// its own i (at or past `batch`: none).  *s gets the sequence, *tiles the tiles' number.
 template <class T>
-__device__ int64_t cost_of(const T& t, const Sequences& q, int64_t i, int64_t* tiles) {
-  Seq s{};
+__device__ __forceinline__ int64_t cost_of(const T& t, const Sequences& q, int64_t i, Seq* s, int* tiles) {
   int n = 0;
   int64_t sum = 0;
+  *s = Seq{0, 0, 0, 0};
   if (i < q.batch) {
-    s = sequence(q, i);
-    n = t.tiles(s);
+    *s = sequence(q, i);
+    n = t.tiles(*s);
     if (n <= 4)
       for (int k = 0; k < n; ++k) {
         int lo, hi;
-        t.range(s, k, &lo, &hi);
+        t.range(*s, k, &lo, &hi);
         sum += hi - lo;
       }
   }
   for (uint32_t many = __ballot_sync(0xffffffffu, n > 4); many; many &= many - 1) {
     const int l = __ffs(many) - 1;
-    Seq o;
-    o.q0 = 0, o.k0 = 0;
-    o.nq = __shfl_sync(0xffffffffu, s.nq, l);
-    o.nk = __shfl_sync(0xffffffffu, s.nk, l);
+    Seq o{0, 0, 0, 0};
+    o.nq = __shfl_sync(0xffffffffu, s->nq, l);
+    o.nk = __shfl_sync(0xffffffffu, s->nk, l);
     const int64_t v = steps_by_warp(t, o, __shfl_sync(0xffffffffu, n, l));
     if ((threadIdx.x & 31) == l) sum = v;
   }
-  *tiles = static_cast<int64_t>(n) * t.kv_heads;
-  return sum * t.kv_heads;
+  *tiles = n;
+  return sum;
 }
 
 struct PlanScratch {
-  int64_t warp[32], warp2[32];
+  int64_t steps[32], tiles[32];  // of a warp's sequences
   Shares shares;
 };
-
-// Inclusive sum over the block's threads; *all gets the block's.
-template <int THREADS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int o = 1; o < 32; o *= 2) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  __syncthreads();
-  if (lane == 31) scratch[warp] = v;
-  __syncthreads();
-  int64_t before = 0, sum = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w == warp) before = sum;
-    sum += scratch[w];
-  }
-  *all = sum;
-  return v + before;
-}
 
 // Cuts the list; every thread of the block takes part.  At least MIN_STEPS a
 // share, unless there are more tiles than such shares.
 template <int THREADS, class T>
 __device__ __noinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc) {
   constexpr int64_t MIN_STEPS = 2;
-  int64_t total = 0, tiles = 0, mine = 0, scanned = 0;
-  for (int64_t base = 0; base < q.batch; base += THREADS) {
-    int64_t n, all;
-    mine = cost_of(t, q, base + threadIdx.x, &n);
-    scanned = block_scan<THREADS>(mine, sc->warp, &all) + total;
-    total += all;
-    block_scan<THREADS>(n, sc->warp2, &all);
-    tiles += all;
-  }
-  Shares p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t total = 0, all_tiles = 0, mine = 0, upto = 0;  // mine: steps of this thread's sequence, upto: with those before
+  Seq s;
+  auto scan = [&](int64_t base) {
+    int n;
+    mine = cost_of(t, q, base + threadIdx.x, &s, &n);
+    upto = mine;
+    int64_t tiles = n;
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+      tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    }
+    __syncthreads();
+    if (lane == 31) sc->steps[warp] = upto, sc->tiles[warp] = tiles;
+    __syncthreads();
+    int64_t all = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w == warp) upto += all;
+      all += sc->steps[w];
+      all_tiles += sc->tiles[w];
+    }
+    return all;
+  };
+  for (int64_t base = 0; base < q.batch; base += THREADS) total += scan(base);
+  total *= t.kv_heads, all_tiles *= t.kv_heads;
+  Shares p{};
   p.total = total;
-  p.count = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(max(total / MIN_STEPS, tiles), int64_t(1))));
-  p.count = static_cast<int>(min(static_cast<int64_t>(p.count), max(total, int64_t(1))));
-  p.seq = p.before = 0;
+  p.count = static_cast<int>(max(int64_t(1), min(min(static_cast<int64_t>(gridDim.x), total), max(total / MIN_STEPS, all_tiles))));
+  p.each = quotient(total, p.count);
+  p.more = static_cast<int>(total - p.each * p.count);
+  const int block = blockIdx.x;
+  if (block < p.count && total > 0) p.at = share_begin(p, block), p.end = share_begin(p, block + 1);
   if (threadIdx.x == 0) sc->shares = p;
   __syncthreads();
-  if (blockIdx.x >= p.count || total == 0) return;
-  const int64_t at = share_begin(p, blockIdx.x);
+  if (p.at >= p.end) return;
   int64_t ahead = 0;
   for (int64_t base = 0; base < q.batch; base += THREADS) {
-    int64_t n, all = total;
-    if (q.batch > THREADS) {
-      mine = cost_of(t, q, base + threadIdx.x, &n);
-      scanned = block_scan<THREADS>(mine, sc->warp, &all) + ahead;
+    int64_t all = 0;
+    if (q.batch > THREADS) all = scan(base);
+    const int64_t from = ahead + (upto - mine) * t.kv_heads;
+    if (from <= p.at && p.at < from + mine * t.kv_heads) {
+      sc->shares.seq = static_cast<int>(base + threadIdx.x);
+      sc->shares.before = from;
+      sc->shares.a_head = mine;
+      sc->shares.s = s;
     }
-    if (scanned - mine <= at && at < scanned) sc->shares.seq = static_cast<int>(base + threadIdx.x), sc->shares.before = scanned - mine;
-    ahead += all;
+    ahead += all * t.kv_heads;
   }
   __syncthreads();
 }
 
 // The first tile of this block's share, by a converged warp.
 template <class T>
-__device__ void walk_begin(const T& t, const Sequences& q, const Shares& p, Walk& w) {
-  w.at = share_begin(p, blockIdx.x);
-  w.end = share_begin(p, blockIdx.x + 1);
-  if (blockIdx.x >= p.count || p.total == 0) w.at = w.end = 0;
-  if (w.at >= w.end) return;
+__device__ __forceinline__ void walk_begin(const T& t, const Shares& p, Walk& w) {
+  w.done = 0;
+  w.left = static_cast<int>(p.end - p.at);
+  if (w.left <= 0) return;
   w.seq = p.seq;
-  w.s = sequence(q, w.seq);
+  w.s = p.s;
   w.tiles = t.tiles(w.s);
-  int64_t ahead = p.before;
-  const int64_t a_head = w.tiles <= 1 ? 0 : steps_by_warp(t, w.s, w.tiles);
-  if (w.tiles <= 1) {
-    t.range(w.s, 0, &w.lo, &w.hi);
-    w.head = static_cast<int>((w.at - ahead) / (w.hi - w.lo));
-    w.tile = 0;
-    w.begin = ahead + static_cast<int64_t>(w.head) * (w.hi - w.lo);
-    return;
-  }
-  w.head = static_cast<int>((w.at - ahead) / a_head);
-  ahead += a_head * w.head;
+  w.head = static_cast<int>(quotient(p.at - p.before, p.a_head));
+  int64_t ahead = p.before + p.a_head * w.head;
   const int lane = threadIdx.x & 31;
   for (int base = 0;; base += 32) {
     int lo = 0, hi = 0;
@@ -189,45 +186,44 @@ __device__ void walk_begin(const T& t, const Sequences& q, const Shares& p, Walk
       const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += u;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, ahead + v > w.at);
+    const uint32_t past = __ballot_sync(0xffffffffu, ahead + v > p.at);
     if (past) {
       const int l = __ffs(past) - 1;
       w.tile = base + l;
       w.lo = __shfl_sync(0xffffffffu, lo, l);
       w.hi = __shfl_sync(0xffffffffu, hi, l);
-      w.begin = ahead + __shfl_sync(0xffffffffu, v, l) - (w.hi - w.lo);
+      w.off = static_cast<int>(p.at - ahead - __shfl_sync(0xffffffffu, v, l)) + (w.hi - w.lo);
       return;
     }
     if (base + 32 >= w.tiles) {  // not reached: the tile exists
-      w.end = w.at;
+      w.left = 0;
       return;
     }
     ahead += __shfl_sync(0xffffffffu, v, 31);
   }
 }
-__device__ __forceinline__ bool walk_has(const Walk& w) { return w.at < w.end; }
+__device__ __forceinline__ bool walk_has(const Walk& w) { return w.left > 0; }
 __device__ __forceinline__ Part walk_part(const Walk& w) {
   Part r;
-  r.begin = w.begin;
-  r.end = w.begin + (w.hi - w.lo);
-  const int64_t stop = w.end < r.end ? w.end : r.end;
-  r.lo = w.lo + static_cast<int>(w.at - w.begin);
-  r.hi = w.lo + static_cast<int>(stop - w.begin);
+  r.lo = w.lo + w.off;
+  r.hi = min(w.hi, r.lo + w.left);
   r.whole = r.lo == w.lo && r.hi == w.hi;
   return r;
 }
 template <class T>
 __device__ __forceinline__ void walk_next(const T& t, const Sequences& q, Walk& w) {
-  w.begin += w.hi - w.lo;
-  w.at = w.begin;
-  if (w.at >= w.end) return;
+  const int steps = w.hi - w.lo - w.off;
+  w.done += steps;
+  w.left -= steps;
+  w.off = 0;
+  if (w.left <= 0) return;
   if (++w.tile == w.tiles) {
     w.tile = 0;
     if (++w.head == t.kv_heads) {
       w.head = 0;
       do {
         if (++w.seq >= q.batch) {  // not reached: steps are left
-          w.at = w.end;
+          w.left = 0;
           return;
         }
         w.s = sequence(q, w.seq);
@@ -239,8 +235,12 @@ __device__ __forceinline__ void walk_next(const T& t, const Sequences& q, Walk& 
 }
 
 // Where a part of a divided tile goes: two slots a share, the first for the tile that it did not begin.
-__device__ __forceinline__ int part_slot(const Walk& w) {
-  return 2 * static_cast<int>(blockIdx.x) + (w.at == w.begin ? 1 : 0);
+__device__ __forceinline__ int part_slot(const Walk& w) { return 2 * static_cast<int>(blockIdx.x) + (w.off == 0 ? 1 : 0); }
+// The first of the shares that have a part of the tile, and their number.
+__device__ __forceinline__ int tile_shares(const Shares& p, const Walk& w, int* first) {
+  const int64_t begin = p.at + w.done - w.off;
+  *first = share_of(p, begin);
+  return share_of(p, begin + (w.hi - w.lo) - 1) - *first + 1;
 }
 __device__ __forceinline__ int tile_slot(int first, int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
 
@@ -283,22 +283,9 @@ __device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
   return v | (static_cast<uint64_t>(16384 >> 4) << 16);
 }
 
-// D[tensor memory] (+)= A . B^T over `count` (1 to 4) times 16 contraction elements, bf16; a whole converged warp, in
-// which one elected lane issues.  All four in one statement: one at a time, with the descriptors' arithmetic between
-// them, an instruction took about 120 cycles to issue, and the tensor core needs 64 for it.
-// Both operands K-major in shared memory: a block of 64 elements.
-__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, int count) {
-  asm volatile(
-      "{\n\t.reg .pred E, A, T, P1, P2, P3;\n\t.reg .b32 r;\n\tsetp.ne.b32 A, %4, 0;\n\tsetp.ne.b32 T, 1, 0;\n\t"
-      "elect.sync r|E, 0xffffffff;\n\tsetp.gt.and.s32 P1, %5, 1, E;\n\tsetp.gt.and.s32 P2, %5, 2, E;\n\t"
-      "setp.gt.and.s32 P3, %5, 3, E;\n\t"
-      "@E tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, A;\n\t"
-      "@P1 tcgen05.mma.cta_group::1.kind::f16 [%0], %6, %7, %3, T;\n\t"
-      "@P2 tcgen05.mma.cta_group::1.kind::f16 [%0], %8, %9, %3, T;\n\t"
-      "@P3 tcgen05.mma.cta_group::1.kind::f16 [%0], %10, %11, %3, T;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(count), "l"(a + 2), "l"(b + 2), "l"(a + 4), "l"(b + 4), "l"(a + 6),
-      "l"(b + 6));
-}
+// D[tensor memory] (+)= A . B^T over four times 16 contraction elements, bf16; a whole converged warp, in which one
+// elected lane issues.  All four in one statement, as mma_kblock: one at a time, with the descriptors' arithmetic
+// between them, an instruction took about 120 cycles to issue, and the tensor core needs 64 for it.
 // A in tensor memory (8 columns each time), B MN-major (16 rows each time): 64 contraction elements.
 __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -311,13 +298,46 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint
       "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(a + 8), "l"(b + 128), "r"(a + 16), "l"(b + 256), "r"(a + 24),
       "l"(b + 384));
 }
-// All of a head's elements: blocks of 64, `ksteps` times 16 of them.
+// All of a head's elements: blocks of 64, whole (the loads fill what a head lacks with zeros).
 template <int DP>
-__device__ __forceinline__ void mma_head(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int ksteps) {
-  mma4_ss(d, a, b, idesc, 0u, ksteps);
-  if (DP == 128) mma4_ss(d, a + (16384 >> 4), b + (16384 >> 4), idesc, 1u, ksteps - 4);
+__device__ __forceinline__ void mma_head(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  mma_kblock<1, false>(d, a, b, idesc, 0u);
+  if (DP == 128) mma_kblock<1, false>(d, a + (16384 >> 4), b + (16384 >> 4), idesc, 1u);
 }
 
+// 128 columns, loaded and waited for in one statement.
+__device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, uint32_t (&x)[64], uint32_t (&y)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+      "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+      "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+      "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+        "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]),
+        "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
+        "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31]),
+        "=r"(x[32]), "=r"(x[33]), "=r"(x[34]), "=r"(x[35]), "=r"(x[36]), "=r"(x[37]), "=r"(x[38]), "=r"(x[39]),
+        "=r"(x[40]), "=r"(x[41]), "=r"(x[42]), "=r"(x[43]), "=r"(x[44]), "=r"(x[45]), "=r"(x[46]), "=r"(x[47]),
+        "=r"(x[48]), "=r"(x[49]), "=r"(x[50]), "=r"(x[51]), "=r"(x[52]), "=r"(x[53]), "=r"(x[54]), "=r"(x[55]),
+        "=r"(x[56]), "=r"(x[57]), "=r"(x[58]), "=r"(x[59]), "=r"(x[60]), "=r"(x[61]), "=r"(x[62]), "=r"(x[63]),
+        "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]), "=r"(y[4]), "=r"(y[5]), "=r"(y[6]), "=r"(y[7]),
+        "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]), "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15]),
+        "=r"(y[16]), "=r"(y[17]), "=r"(y[18]), "=r"(y[19]), "=r"(y[20]), "=r"(y[21]), "=r"(y[22]), "=r"(y[23]),
+        "=r"(y[24]), "=r"(y[25]), "=r"(y[26]), "=r"(y[27]), "=r"(y[28]), "=r"(y[29]), "=r"(y[30]), "=r"(y[31]),
+        "=r"(y[32]), "=r"(y[33]), "=r"(y[34]), "=r"(y[35]), "=r"(y[36]), "=r"(y[37]), "=r"(y[38]), "=r"(y[39]),
+        "=r"(y[40]), "=r"(y[41]), "=r"(y[42]), "=r"(y[43]), "=r"(y[44]), "=r"(y[45]), "=r"(y[46]), "=r"(y[47]),
+        "=r"(y[48]), "=r"(y[49]), "=r"(y[50]), "=r"(y[51]), "=r"(y[52]), "=r"(y[53]), "=r"(y[54]), "=r"(y[55]),
+        "=r"(y[56]), "=r"(y[57]), "=r"(y[58]), "=r"(y[59]), "=r"(y[60]), "=r"(y[61]), "=r"(y[62]), "=r"(y[63])
+      : "r"(taddr), "r"(taddr + 64)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -327,6 +347,11 @@ __device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, uint32_t (&r)[16]
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(

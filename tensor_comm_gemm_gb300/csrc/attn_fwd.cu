@@ -18,8 +18,16 @@
 // cleared in shared memory before the product, and a value that is not finite
 // where only some rows see it is added to those rows alone at the end.
 //
-// Roles: warp 0 loads (TMA), warp 1 issues the MMAs, warps 2 and 3 clear V,
-// warps 4-7 and 8-11 are the two halves' softmax.
+// Roles: warp 0 loads (TMA), warps 1 and 2 issue the two halves' MMAs, warp 3
+// clears V, warps 4-7 and 8-11 are the two halves' softmax, warps 12-15 divide by
+// the sums and store, beside the next tile's scores and weights.
+//
+// The tensor core takes about two instructions ahead of time, a wait costs the
+// issuing warp 130 cycles even when there is nothing to wait for and a commit 60.
+// One warp with all of them needed 1760 cycles for a half's products, which take
+// 1033.  With two, one waits while the other issues; they issue the end of a step
+// in turns, since otherwise both halves come to run in step, softmax against
+// softmax (3950 cycles a step).
 
 #include <algorithm>
 #include <cstring>
@@ -34,8 +42,8 @@ namespace tpo {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int THREADS = 384;
-constexpr int SOFTMAX = 256;             // threads of the two softmax groups
+constexpr int THREADS = 512;
+constexpr int STORE = 128;               // threads of the storing group
 constexpr float GROWTH = 8.0f;           // of the maximum, in powers of two, before O is rescaled
 constexpr int JOIN = 2048;               // parts of rows whose weights are in shared memory at a time
 constexpr int BAD_SETS = 8, BAD_STEPS = 3;  // steps of a tile that only some of its rows see whole
@@ -74,19 +82,36 @@ struct Layout {
   static constexpr int TILE = BLK * DP * 2;          // 128 rows of a head
   static constexpr int STAGES = DP == 128 ? 2 : 4;   // of K, and of V
   static constexpr int K0 = 2 * TILE, V0 = K0 + STAGES * TILE, BARS = V0 + STAGES * TILE;
-  static constexpr int N_BARS = 5 * STAGES + 11;
+  static constexpr int N_BARS = 5 * STAGES + 18;
   static constexpr int SLOT = BARS + 8 * N_BARS;
   static constexpr int LAST = SLOT + 4;
   static constexpr int BAD = SLOT + 8;               // [BAD_SETS][BAD_STEPS][4] keys, a bit each
-  static constexpr int ROWS = (BAD + BAD_SETS * BAD_STEPS * 16 + 15) / 16 * 16;  // [2][256] floats: maxima and sums
-  static constexpr int JOIN_AT = ROWS + 2048;        // [2][JOIN] floats
+  static constexpr int ROWS = (BAD + BAD_SETS * BAD_STEPS * 16 + 15) / 16 * 16;  // [2][2][128] floats: maxima and sums
+  static constexpr int JOIN_AT = ROWS + 2048;        // [2][JOIN] floats, or the storing warps' staging boxes
   static constexpr int PLAN = JOIN_AT + 8 * JOIN;
-  static_assert(JOIN_AT % 16 == 0 && 8 * JOIN >= 8 * 2048, "also a staging box for each warp");
+  static_assert(JOIN_AT % 16 == 0 && 8 * JOIN >= 4 * 2048, "also a staging box for each warp");
   static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
   static_assert(SMEM <= 232448, "shared memory of one block");
 };
 
-__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, %0;" ::"n"(SOFTMAX) : "memory"); }
+template <int DP>
+struct Bars {
+  uint32_t kfull, kempty, vfull, vempty, vfix, qfull, qempty, sfull, pfull, ofull, ofree, lfull, lfree, drain;
+  __device__ explicit Bars(uint32_t sbase) {
+    uint32_t b = sbase + Layout<DP>::BARS;
+    auto next = [&](int n) {
+      const uint32_t r = b;
+      b += 8 * n;
+      return r;
+    };
+    constexpr int S = Layout<DP>::STAGES;
+    kfull = next(S), kempty = next(S), vfull = next(S), vempty = next(S), vfix = next(S), qfull = next(1);
+    qempty = next(1), sfull = next(2), pfull = next(4), ofull = next(2), ofree = next(2), lfull = next(2);
+    lfree = next(2), drain = next(2);
+  }
+};
+
+__device__ __forceinline__ void bar_store() { asm volatile("bar.sync 1, %0;" ::"n"(STORE) : "memory"); }
 
 // What the roles derive from a part of a tile.
 struct Item {
@@ -108,22 +133,19 @@ __device__ __forceinline__ bool needs_fix(const Item& i, int j) { return (j + 1)
 template <int DP>
 __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase) {
   using L = Layout<DP>;
-  const uint32_t kfull = sbase + L::BARS, kempty = kfull + 8 * L::STAGES, vfull = kempty + 8 * L::STAGES,
-                 vempty = vfull + 8 * L::STAGES, qfull = vempty + 16 * L::STAGES, qempty = qfull + 8;
+  const Bars<DP> b(sbase);
   const bool lead = (threadIdx.x & 31) == 0;
   uint32_t kn = 0, vn = 0, qn = 0;  // loads so far
   bool ok = true;
   Walk w;
-  for (walk_begin(tiles, a.seq, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
+  for (walk_begin(tiles, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
     const Item it = item_of(a, w);
-    const int q_head = w.head * a.group;
-    if (!(ok = wait_warp(a.watch, qempty, (qn & 1u) ^ 1u, S_EMPTY))) break;
+    if (!(ok = wait_warp(a.watch, b.qempty, (qn & 1u) ^ 1u, S_EMPTY))) break;
     if (lead) {
-      const uint32_t box = static_cast<uint32_t>(a.group * a.tokens) * 128u;
-      mbar_expect_tx(qfull, box * (DP / 64) * it.halves);
+      mbar_expect_tx(b.qfull, static_cast<uint32_t>(a.group * a.tokens) * 128u * (DP / 64) * it.halves);
       for (int h = 0; h < it.halves; ++h)
         for (int d = 0; d < DP / 64; ++d)
-          tma_load_3d(sbase + h * L::TILE + d * 16384, &a.q, qfull, d * 64, q_head,
+          tma_load_3d(sbase + h * L::TILE + d * 16384, &a.q, b.qfull, d * 64, w.head * a.group,
                       w.s.q0 + it.tok + h * a.tokens);
     }
     __syncwarp();
@@ -134,97 +156,164 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
       if (lead) {
         mbar_expect_tx(full + 8 * st, L::TILE);
         for (int d = 0; d < DP / 64; ++d)
-          tma_load_3d(base + st * L::TILE + d * 16384, map, full + 8 * st, d * 64, w.head,
-                      w.s.k0 + j * BLK);
+          tma_load_3d(base + st * L::TILE + d * 16384, map, full + 8 * st, d * 64, w.head, w.s.k0 + j * BLK);
       }
       __syncwarp();
       ++n;
       return true;
     };
     // K one step ahead of V, as the products take them
-    ok = load(&a.k, kfull, kempty, sbase + L::K0, kn, it.p.lo);
-    for (int j = it.p.lo; ok && j < it.p.hi; ++j) {
-      if (j + 1 < it.p.hi) ok = load(&a.k, kfull, kempty, sbase + L::K0, kn, j + 1);
-      if (ok) ok = load(&a.v, vfull, vempty, sbase + L::V0, vn, j);
+    for (int j = it.p.lo; ok && j <= it.p.hi; ++j) {
+      if (j < it.p.hi) ok = load(&a.k, b.kfull, b.kempty, sbase + L::K0, kn, j);
+      if (ok && j > it.p.lo) ok = load(&a.v, b.vfull, b.vempty, sbase + L::V0, vn, j - 1);
     }
   }
   if (!ok && lead) {  // what is in flight must land before the block gives up its shared memory
     for (uint32_t j = kn > L::STAGES ? kn - L::STAGES : 0u; j < kn; ++j)
-      wait_bar(a.watch, kfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
+      wait_bar(a.watch, b.kfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
     for (uint32_t j = vn > L::STAGES ? vn - L::STAGES : 0u; j < vn; ++j)
-      wait_bar(a.watch, vfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
-    if (qn) wait_bar(a.watch, qfull, (qn - 1) & 1u, S_DRAIN, false);
+      wait_bar(a.watch, b.vfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
+    if (qn) wait_bar(a.watch, b.qfull, (qn - 1) & 1u, S_DRAIN, false);
   }
   __syncwarp();
 }
 
+// The turns of the two issuing warps, by named barriers: pass_turn lets the other's next take_turn through.
+__device__ __forceinline__ void take_turn(int half) {
+  if (half)
+    asm volatile("bar.sync 2, 64;" ::: "memory");
+  else
+    asm volatile("bar.sync 3, 64;" ::: "memory");
+}
+__device__ __forceinline__ void pass_turn(int half) {
+  if (half)
+    asm volatile("bar.arrive 3, 64;" ::: "memory");
+  else
+    asm volatile("bar.arrive 2, 64;" ::: "memory");
+}
+
+// The products of one half.  Where a tile has one half only, the warps (and accumulators) take its steps by turns, and
+// pass over the other's: both release a stage.
 template <int DP>
-__device__ void mma_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint32_t tmem) {
+__device__ void mma_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint32_t tmem, int half) {
   using L = Layout<DP>;
-  const uint32_t kfull = sbase + L::BARS, kempty = kfull + 8 * L::STAGES, vfull = kempty + 8 * L::STAGES,
-                 vempty = vfull + 8 * L::STAGES, vfix = vempty + 8 * L::STAGES, qfull = vfix + 8 * L::STAGES,
-                 qempty = qfull + 8, sfull = qempty + 8, pfull = sfull + 16, ofull = pfull + 32, drain = ofull + 16;
-  const int ksteps = (a.dim + 15) / 16;
+  const Bars<DP> b(sbase);
+  const bool lead = (threadIdx.x & 31) == 0;
   const uint32_t idesc_s = idesc_n(make_idesc(false, BLK), BLK);
-  const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), ksteps * 16) | 1u << 16;
-  const uint64_t dq = smem_desc_sw128(sbase), dk = smem_desc_sw128(sbase + L::K0), dv = desc_rows(sbase + L::V0);
-  uint32_t kn = 0, vn = 0, qn = 0, pn0 = 0, pn1 = 0;
-  uint32_t fixed[L::STAGES] = {};
-  bool ok = true;
+  const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), (a.dim + 15) / 16 * 16) | 1u << 16;
+  const uint64_t dk = smem_desc_sw128(sbase + L::K0), dv = desc_rows(sbase + L::V0);
+  const uint32_t s = tmem + half * BLK, o = tmem + 2 * BLK + half * BLK;
+  uint32_t kn = 0, vn = 0, qn = 0, pn = 0;
+  uint32_t fixed = 0;  // parity of each stage's next clearing
+  bool ok = true;      // after a failure the turns go on, without waits and products
+  bool turns = false;  // whether there was a turn: the first is half 0's without asking
   Walk w;
-  for (walk_begin(tiles, a.seq, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
+  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++qn) {
     const Item it = item_of(a, w);
-    const int steps = it.p.hi - it.p.lo, units = it.halves * steps;
-    if (!(ok = wait_warp(a.watch, qfull, qn & 1u, S_FULL))) break;
-    ++qn;
-    // unit u: half (or turn) u & 1 of a step
-    auto scores = [&](int u) {
-      const bool first = it.halves == 1 || !(u & 1), last = it.halves == 1 || (u & 1);
-      const uint32_t st = kn % L::STAGES;
-      if (first && !wait_warp(a.watch, kfull + 8 * st, kn / L::STAGES & 1u, S_FULL)) return false;
-      tc_fence_after();
-      const uint32_t half = u & 1;
-      const uint64_t qd = dq + (it.halves == 2 ? half * (L::TILE >> 4) : 0u), kd = dk + st * (L::TILE >> 4);
-      mma_head<DP>(tmem + half * BLK, qd, kd, idesc_s, ksteps);
-      mma_commit_cg<1>(sfull + 8 * half);
-      if (last) mma_commit_cg<1>(kempty + 8 * st), ++kn;
-      if (u == units - 1) mma_commit_cg<1>(qempty);
-      return true;
+    const int steps = it.p.hi - it.p.lo;
+    const uint64_t dq = smem_desc_sw128(sbase + (it.halves == 2 ? half * L::TILE : 0));
+    auto await = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = wait_warp(a.watch, bar, parity & 1u, S_FULL);
     };
-    ok = scores(0) && (units < 2 || scores(1));
-    for (int u = 0; ok && u < units; ++u) {
-      const uint32_t half = u & 1;
-      const bool first = it.halves == 1 || !half, last = it.halves == 1 || half;
-      const int j = it.p.lo + (it.halves == 1 ? u : u >> 1);
+    auto await_k = [&] { await(b.kfull + 8 * (kn % L::STAGES), kn / L::STAGES); };
+    auto await_v = [&](int i) {
       const uint32_t st = vn % L::STAGES;
-      const uint32_t turn = half ? pn1++ : pn0++;
-      if (!(ok = wait_warp(a.watch, pfull + 16 * half, turn & 1u, S_FULL))) break;
-      if (first) {
-        if (!(ok = wait_warp(a.watch, vfull + 8 * st, vn / L::STAGES & 1u, S_FULL))) break;
-        if (needs_fix(it, j)) {
-          uint32_t n = 0;
-#pragma unroll
-          for (int i = 0; i < L::STAGES; ++i)
-            if (i == static_cast<int>(st)) n = fixed[i]++;
-          if (!(ok = wait_warp(a.watch, vfix + 8 * st, n & 1u, S_FULL))) break;
-        }
+      await(b.vfull + 8 * st, vn / L::STAGES);
+      if (needs_fix(it, it.p.lo + i)) {
+        await(b.vfix + 8 * st, fixed >> st);
+        fixed ^= 1u << st;
       }
+    };
+    auto scores = [&] {
+      if (!ok) return;
       tc_fence_after();
-      const uint64_t vd = dv + st * (L::TILE >> 4);
-      const uint32_t p = tmem + half * BLK, o = tmem + 2 * BLK + half * BLK;
-      const bool fresh = u < 2;  // this half's first product of the part
-      mma4_ts(o, p, vd, idesc_o, !fresh);
-      if (!(ok = wait_warp(a.watch, pfull + 16 * half + 8, turn & 1u, S_FULL))) break;
+      mma_head<DP>(s, dq, dk + (kn % L::STAGES) * (L::TILE >> 4), idesc_s);
+      mma_commit_cg<1>(b.sfull + 8 * half);
+    };
+    auto free_k = [&] {
+      if (ok) mma_commit_cg<1>(b.kempty + 8 * (kn % L::STAGES));
+      ++kn;
+    };
+    auto free_v = [&] {
+      if (ok) mma_commit_cg<1>(b.vempty + 8 * (vn % L::STAGES));
+      ++vn;
+    };
+    auto product = [&](int part, bool fresh) {  // 64 keys
+      if (!ok) return;
       tc_fence_after();
-      mma4_ts(o, p + 64, vd + 512, idesc_o, 1u);
-      if (u >= units - 2) mma_commit_cg<1>(ofull + 8 * half);
-      if (last) mma_commit_cg<1>(vempty + 8 * st), ++vn;
-      if (u + 2 < units) ok = scores(u + 2);
+      mma4_ts(o, s + 64 * part, dv + (vn % L::STAGES) * (L::TILE >> 4) + 512 * part, idesc_o, fresh ? 0u : 1u);
+    };
+    await(b.qfull, qn);
+    if (it.halves == 2) {
+      await_k();
+      scores();
+      free_k();
+      if (steps == 1 && ok) mma_commit_cg<1>(b.qempty);
+      for (int i = 0; i < steps; ++i, ++pn) {
+        const bool more = i + 1 < steps;
+        // the accumulator is free once the part before has been stored
+        if (i == 0 && qn > 0) await(b.ofree + 8 * half, qn - 1);
+        await_v(i);
+        if (more) await_k();
+        await(b.pfull + 16 * half, pn);
+        product(0, i == 0);
+        await(b.pfull + 16 * half + 8, pn);
+        if (half || turns) take_turn(half);
+        turns = true;
+        product(1, false);
+        if (more)
+          scores();
+        else if (ok)
+          mma_commit_cg<1>(b.ofull + 8 * half);
+        pass_turn(half);
+        free_v();
+        if (more) free_k();
+        if (i + 2 == steps && ok) mma_commit_cg<1>(b.qempty);
+      }
+    } else {
+      auto skip_k = [&] {
+        await_k();
+        if (lead) mbar_arrive(b.kempty + 8 * (kn % L::STAGES));
+        ++kn;
+      };
+      auto skip_v = [&](int i) {
+        await(b.vfull + 8 * (vn % L::STAGES), vn / L::STAGES);
+        if (needs_fix(it, it.p.lo + i)) fixed ^= 1u << (vn % L::STAGES);
+        if (lead) mbar_arrive(b.vempty + 8 * (vn % L::STAGES));
+        ++vn;
+      };
+      if (half) skip_k();
+      if (half < steps) {
+        await_k();
+        scores();
+        free_k();
+      }
+      if (qn > 0) await(b.ofree + 8 * half, qn - 1);
+      if (half) skip_v(0);
+      for (int i = half; i < steps; i += 2, ++pn) {
+        await_v(i);
+        await(b.pfull + 16 * half, pn);
+        product(0, i < 2);
+        await(b.pfull + 16 * half + 8, pn);
+        product(1, false);
+        free_v();
+        if (i + 1 < steps) skip_k();
+        if (i + 2 < steps) {
+          await_k();
+          scores();
+          free_k();
+        } else if (ok) {
+          mma_commit_cg<1>(b.ofull + 8 * half);
+        }
+        if (i + 1 < steps) skip_v(i + 1);
+      }
+      if (ok) mma_commit_cg<1>(b.qempty);
     }
   }
+  if (!half && turns) take_turn(half);  // the last one that was passed
   // also after a failure: every MMA issued must complete before tensor memory is freed
-  mma_commit_cg<1>(drain);
-  if ((threadIdx.x & 31) == 0) wait_bar(a.watch, drain, 0u, S_DRAIN, false);
+  mma_commit_cg<1>(b.drain + 8 * half);
+  if (lead) wait_bar(a.watch, b.drain + 8 * half, 0u, S_DRAIN, false);
   __syncwarp();
 }
 
@@ -233,23 +322,22 @@ __device__ void mma_role(const Args& a, const Tiles& tiles, const Shares& sh, ui
 template <int DP>
 __device__ void fix_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem) {
   using L = Layout<DP>;
-  const uint32_t vfull = sbase + L::BARS + 16 * L::STAGES, vempty = vfull + 8 * L::STAGES,
-                 vfix = vempty + 8 * L::STAGES;
-  const int lane = threadIdx.x & 31, mine = (threadIdx.x >> 5) - 2;  // this warp's rows: 32 mine, and 64 further on
+  const Bars<DP> b(sbase);
+  const int lane = threadIdx.x & 31;
   uint32_t vn = 0, item = 0;
   Walk w;
-  for (walk_begin(tiles, a.seq, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++item) {
+  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++item) {
     const Item it = item_of(a, w);
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::BAD) + item % BAD_SETS * BAD_STEPS * 4;
-    if (lane < 2 * BAD_STEPS) bad[2 * lane + mine] = 0;
+    if (lane < 4 * BAD_STEPS) bad[lane] = 0;
     __syncwarp();
     for (int j = it.p.lo; j < it.p.hi; ++j, ++vn) {
       const uint32_t st = vn % L::STAGES;
-      if (!wait_warp(a.watch, vfull + 8 * st, vn / L::STAGES & 1u, S_FULL)) return;
+      if (!wait_warp(a.watch, b.vfull + 8 * st, vn / L::STAGES & 1u, S_FULL)) return;
       if (needs_fix(it, j)) {
         uint8_t* v = smem + L::V0 + st * L::TILE;
 #pragma unroll 1
-        for (int g = mine; g < 4; g += 2) {
+        for (int g = 0; g < 4; ++g) {
           const int r = 32 * g + lane, key = j * BLK + r;
           uint32_t top = 0;  // the row's largest magnitudes, as a pair of bf16
           if (key >= w.s.nk) {
@@ -284,76 +372,77 @@ __device__ void fix_role(const Args& a, const Tiles& tiles, const Shares& sh, ui
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(vfix + 8 * st);
+        if (lane == 0) mbar_arrive(b.vfix + 8 * st);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(vempty + 8 * st);
+      if (lane == 0) mbar_arrive(b.vempty + 8 * st);
     }
   }
 }
 
+// A thread's row of a tile.
+struct Row {
+  int t, limit;  // its token, the keys that it sees
+  bool valid;
+};
+__device__ __forceinline__ Row row_of(const Args& a, const Walk& w, const Item& it, int half, int dt) {
+  Row r;
+  r.t = it.tok + (it.halves == 2 ? half * a.tokens : 0) + dt;
+  r.valid = dt < a.tokens && r.t < w.s.nq;
+  r.limit = r.valid ? keys_seen(w.s, r.t, a.causal) : 0;
+  return r;
+}
+
 template <int DP>
 __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem,
-                             uint32_t tmem) {
+                             uint32_t tmem, int half) {
   using L = Layout<DP>;
-  const uint32_t qempty = sbase + L::BARS + 40 * L::STAGES + 8, sfull = qempty + 8, pfull = sfull + 16,
-                 ofull = pfull + 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, half = (warp - 4) >> 2;
-  const int row = quad * 32 + lane, me = threadIdx.x - 128;
+  const Bars<DP> b(sbase);
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
   const uint32_t ts = lanes + half * BLK, to = lanes + 2 * BLK + half * BLK;
-  const int dt = row / a.group, head_in = row - dt * a.group;  // the row's token in its half, its head in the group
-  const int chunks = (a.dim + 31) / 32;
-  float* rows = reinterpret_cast<float*>(smem + L::ROWS);
+  const int dt = row / a.group, chunks = (a.dim + 15) / 16;
+  float* stats = reinterpret_cast<float*>(smem + L::ROWS) + half * 256;
   const float2 c2 = make_float2(a.c, a.c);
-  uint32_t sn = 0, on = 0, item = 0;
+  uint32_t sn = 0, item = 0;
   bool ok = true;
+  auto arrive = [&](uint32_t bar) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
   Walk w;
-  for (walk_begin(tiles, a.seq, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++item) {
+  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++item) {
     const Item it = item_of(a, w);
     const int steps = it.p.hi - it.p.lo;
-    const int t = it.tok + (it.halves == 2 ? half * a.tokens : 0) + dt;
-    const bool valid = dt < a.tokens && t < w.s.nq;
-    const int limit = valid ? keys_seen(w.s, t, a.causal) : 0;
+    const int limit = row_of(a, w, it, half, dt).limit;
     const bool idle = __all_sync(0xffffffffu, limit == 0);
     float m = -INFINITY, l = 0.0f;  // the maximum that is subtracted (in powers of two), the sum
     const int first = it.halves == 2 ? 0 : half, by = it.halves == 2 ? 1 : 2;
     for (int i = first; i < steps; i += by, ++sn) {
-      if (ok) ok = wait_warp(a.watch, sfull + 8 * half, sn & 1u, S_TFULL);
-      auto arrive = [&](uint32_t bar) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      };
+      if (ok) ok = wait_warp(a.watch, b.sfull + 8 * half, sn & 1u, S_TFULL);
       if (!ok || idle) {
-        arrive(pfull + 16 * half);
-        arrive(pfull + 16 * half + 8);
+        arrive(b.pfull + 16 * half);
+        arrive(b.pfull + 16 * half + 8);
         continue;
       }
-      // Half of the scores at a time, each read twice, first for the maximum: a thread holds 64 of them and not 128, and
-      // the code is short (its first pass runs at the speed of the instruction fetches).  A half's weights go over its
-      // own columns, and the product with the first half's runs beside the second's.
-      uint32_t x[64];
+      // all of the row's scores in registers
+      uint32_t x[64], y[64];
       const int left = limit - (it.p.lo + i) * BLK;
-      const bool all = __all_sync(0xffffffffu, left >= BLK);
-      auto read = [&](int from) {
-        tmem_ld64_sync(ts + from, x);
-        if (!all) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (from + e >= left) x[e] = 0xff800000u;
-        }
-      };
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       tc_fence_after();
-#pragma unroll 1
-      for (int from = 0; from < BLK; from += 64) {
-        read(from);
+      tmem_ld128_sync(ts, x, y);
+      if (!__all_sync(0xffffffffu, left >= BLK)) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 8)
+        for (int e = 0; e < 64; ++e) {
+          if (e >= left) x[e] = 0xff800000u;
+          if (e + 64 >= left) y[e] = 0xff800000u;
+        }
+      }
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            top[k] = max3(top[k], __uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
+      for (int e = 0; e < 64; e += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = max3(top[k], __uint_as_float(x[e + k]), __uint_as_float(y[e + k]));
       }
       const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.c;
       const bool grow = peak > m + GROWTH;
@@ -363,7 +452,7 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
         l *= f;
         if (i != first) {  // the products before this step's scores are done
 #pragma unroll 1
-          for (int c = 0; c < 2 * chunks; ++c) {
+          for (int c = 0; c < chunks; ++c) {
             uint32_t o[16];
             tmem_ld16_sync(to + c * 16, o);
 #pragma unroll
@@ -375,112 +464,153 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
       const float sub = m == -INFINITY ? 0.0f : -m;
       const float2 sub2 = make_float2(sub, sub);
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll 1
-      for (int from = 0; from < BLK; from += 64) {
-        read(from);
-        uint32_t h[32];
+      // 64 keys' weights, rounded, over their own columns; the product with the first 64 runs beside the others
+      auto weights = [&](uint32_t(&z)[64], uint32_t at, uint32_t bar) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 s = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, sub2);
-          const float2 p = make_float2(exp2_fast(s.x), exp2_fast(s.y));
-          sum[e & 1] = add2(sum[e & 1], p);
-          h[e] = pack_bf16(p.x, p.y);
+        for (int g = 0; g < 4; ++g) {
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = 16 * g + 2 * e;
+            const float2 s = fma2(make_float2(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), c2, sub2);
+            const float2 p = make_float2(exp2_fast(s.x), exp2_fast(s.y));
+            sum[e & 1] = add2(sum[e & 1], p);
+            h[e] = pack_bf16(p.x, p.y);
+          }
+          tmem_st8(at + 8 * g, h);
         }
-        tmem_st32(ts + from, h);
         tmem_wait_st();
-        arrive(pfull + 16 * half + from / 8);
-      }
+        arrive(bar);
+      };
+      weights(x, ts, b.pfull + 16 * half);
+      weights(y, ts + 64, b.pfull + 16 * half + 8);
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
-    // ---- the end of the part
-    if (steps > first) {
-      if (ok) ok = wait_warp(a.watch, ofull + 8 * half, on & 1u, S_TFULL);
-      ++on;
-    }
-    tc_fence_after();
-    float w0 = 1.0f, w1 = 0.0f;  // weights of the two accumulators
-    const bool two = it.halves == 1 && steps > 1;
-    if (it.halves == 1) {  // both groups end with the joined maximum and sum
-      rows[half * 256 + row] = m;
-      rows[half * 256 + 128 + row] = l;
-      bar_softmax();
-      tc_fence_after();
-      const float m0 = rows[row], l0 = rows[128 + row], m1 = rows[256 + row], l1 = rows[384 + row];
-      m = fmaxf(m0, m1);
-      w0 = m0 == -INFINITY ? 0.0f : exp2_fast(m0 - m);
-      w1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - m);
-      l = l0 * w0 + l1 * w1;
-    }
-    const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L::BAD) + item % BAD_SETS * BAD_STEPS * 4;
-    uint32_t any_bad = 0;
-    if (ok && a.causal)
-      for (int i = 0; i < BAD_STEPS * 4; ++i) any_bad |= bad[i];
-    const int64_t q_row = static_cast<int64_t>(w.s.q0) + t;
-    const int head = w.head * a.group + head_in;
-    const int prow = it.halves == 2 ? half * BLK + row : row;
+    if (ok && item > 0) ok = wait_warp(a.watch, b.lfree + 8 * half, (item - 1) & 1u, S_TEMPTY);
+    stats[row] = m;
+    stats[128 + row] = l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b.lfull + 8 * half);
+  }
+}
+
+// Divides by the sums and stores, and joins the parts of divided tiles.
+template <int DP>
+__device__ void store_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem,
+                           uint32_t tmem) {
+  using L = Layout<DP>;
+  const Bars<DP> b(sbase);
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane, me = threadIdx.x - 384;
+  const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * BLK;
+  const int dt = row / a.group, head_in = row - dt * a.group;  // the row's token in its half, its head in the group
+  const int chunks = (a.dim + 31) / 32;
+  const float* stats = reinterpret_cast<const float*>(smem + L::ROWS);
+  uint8_t* stage = smem + L::JOIN_AT + quad * 2048;
+  uint32_t item = 0, on[2] = {0, 0};
+  bool ok = true;
+  Walk w;
+  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++item) {
+    const Item it = item_of(a, w);
+    const int steps = it.p.hi - it.p.lo, head = w.head * a.group + head_in;
     float* part = a.part + static_cast<int64_t>(part_slot(w)) * a.part_rows * (a.dim + 2);
-    const float scale = !it.p.whole ? 1.0f : l == 0.0f ? (limit > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / l;
-    uint8_t* stage = smem + L::JOIN_AT + (warp - 4) * 2048;
-    const RowsOut to_rows = rows_out(valid && it.p.whole ? a.out + q_row * a.ldo + head * a.ho : nullptr);
-    const float f0 = (it.halves == 1 ? w0 : 1.0f) * scale, f1 = w1 * scale;
+    const bool both = it.halves == 1;  // the two accumulators are of the same rows
 #pragma unroll 1
-    for (int c = it.halves == 1 ? half : 0; ok && c < chunks; c += by) {
-      uint32_t o[32];
-      float v[32];
+    for (int half = 0; half < it.halves; ++half) {
+      const Row r = row_of(a, w, it, half, dt);
+      const bool idle = __all_sync(0xffffffffu, r.limit == 0);
+      float ms[2] = {-INFINITY, -INFINITY}, ls[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-      if (!idle) {  // an accumulator that does not count may hold anything
-        tmem_ld32_sync((it.halves == 1 ? lanes + 2 * BLK : to) + c * 32, o);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
-        if (two) {
-          tmem_ld32_sync(lanes + 3 * BLK + c * 32, o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] += f1 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f1;
+      for (int h = 0; h < 2; ++h) {  // h: the accumulator
+        if (!both && h != half) continue;
+        if (ok) ok = wait_warp(a.watch, b.lfull + 8 * h, item & 1u, S_TFULL);
+        ms[h] = stats[h * 256 + row];
+        ls[h] = stats[h * 256 + 128 + row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.lfree + 8 * h);
+        if (!both || h < steps) {  // else it has no product
+          if (ok) ok = wait_warp(a.watch, b.ofull + 8 * h, on[h] & 1u, S_TFULL);
+          ++on[h];
         }
       }
-      if (any_bad)  // the noted values, for a row that sees their keys
-        for (int i = 0; i < BAD_STEPS * 4; ++i)
-          for (uint32_t left = bad[i]; left; left &= left - 1) {
-            const int key = it.some / BLK * BLK + 32 * i + __ffs(left) - 1;
-            if (key >= limit) continue;
-            const bf16* x = a.values + (static_cast<int64_t>(w.s.k0) + key) * a.ldv + w.head * a.hv + c * 32;
+      tc_fence_after();
+      const float m = fmaxf(ms[0], ms[1]);
+      float f[2];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float f = c * 32 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
-              if (!isfinite(f)) v[e] += f;
-            }
+      for (int h = 0; h < 2; ++h) f[h] = ms[h] == -INFINITY ? 0.0f : exp2_fast(ms[h] - m);
+      const float l = ls[0] * f[0] + ls[1] * f[1];
+      const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L::BAD) + item % BAD_SETS * BAD_STEPS * 4;
+      uint32_t any_bad = 0;
+      if (ok && a.causal && lane < BAD_STEPS * 4) any_bad = bad[lane];
+      any_bad = __any_sync(0xffffffffu, any_bad != 0);
+      const int64_t q_row = static_cast<int64_t>(w.s.q0) + r.t;
+      const float scale = !it.p.whole ? 1.0f : l == 0.0f ? (r.limit > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / l;
+      const float f0 = f[both ? 0 : half] * scale, f1 = f[1] * scale;
+      const RowsOut to_rows = rows_out(r.valid && it.p.whole ? a.out + q_row * a.ldo + head * a.ho : nullptr);
+#pragma unroll 1
+      for (int c = 0; ok && c < chunks; ++c) {
+        float v[32];
+        if (idle) {  // no product: the accumulator may hold anything
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+        } else {
+          uint32_t o[32];
+          tmem_ld32_sync(to + half * BLK + c * 32, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f0;
+          if (both && steps > 1) {
+            tmem_ld32_sync(to + BLK + c * 32, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
           }
-      if (it.p.whole)
-        store_rows(stage, v, to_rows, c * 32, a.dim - c * 32);
-      else if (valid)
-        store_part(part, a.part_rows, prow, v, c * 32, a.dim);
-    }
-    if (ok && valid && (it.halves == 2 || half == 0)) {
-      if (!it.p.whole) {
-        float* ml = part + static_cast<int64_t>(a.part_rows) * a.dim;
-        ml[prow] = m;
-        ml[a.part_rows + prow] = l;
-      } else if (a.lse) {
-        a.lse[q_row * a.heads + head] = limit > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+        if (any_bad)  // the noted values, for a row that sees their keys
+          for (int i = 0; i < BAD_STEPS * 4; ++i)
+            for (uint32_t left = bad[i]; left; left &= left - 1) {
+              const int key = it.some / BLK * BLK + 32 * i + __ffs(left) - 1;
+              if (key >= r.limit) continue;
+              const bf16* x = a.values + (static_cast<int64_t>(w.s.k0) + key) * a.ldv + w.head * a.hv + c * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float y = c * 32 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
+                if (!isfinite(y)) v[e] += y;
+              }
+            }
+        if (it.p.whole)
+          store_rows(stage, v, to_rows, c * 32, a.dim - c * 32);
+        else if (r.valid)
+          store_part(part, a.part_rows, half * BLK + row, v, c * 32, a.dim);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(b.ofree + 8 * half);
+        if (both) mbar_arrive(b.ofree + 8);
+      }
+      if (ok && r.valid) {
+        if (!it.p.whole) {
+          float* ml = part + static_cast<int64_t>(a.part_rows) * a.dim;
+          ml[half * BLK + row] = m;
+          ml[a.part_rows + half * BLK + row] = l;
+        } else if (a.lse) {
+          a.lse[q_row * a.heads + head] = r.limit > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
       }
     }
-    tc_fence_before();
-    if (it.halves == 1) bar_softmax();  // both have read both accumulators, and the rows' sums
     if (it.p.whole) continue;
     // ---- a divided tile: whoever comes last joins its parts
     __threadfence();
-    bar_softmax();
-    const int from = share_of(sh, it.p.begin), shares = share_of(sh, it.p.end - 1) - from + 1;
+    bar_store();
+    int from;
+    const int shares = tile_shares(sh, w, &from);
     volatile int* last = reinterpret_cast<volatile int*>(smem + L::LAST);
     if (me == 0) {
       const uint32_t before = atomicAdd(a.arrivals + from, ok ? 1u : 0u);
       *last = ok && before + 1 == static_cast<uint32_t>(shares);
       if (*last) a.arrivals[from] = 0;
     }
-    bar_softmax();
+    bar_store();
     if (!*last) {
-      bar_softmax();
+      bar_store();
       continue;
     }
     __threadfence();
@@ -499,42 +629,46 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
     float* table = reinterpret_cast<float*>(smem + L::JOIN_AT);
     for (int r0 = 0; r0 < count; r0 += batch) {
       const int rows_now = min(batch, count - r0);
-      for (int i = me; i < rows_now * shares; i += SOFTMAX) {
+      for (int i = me; i < rows_now * shares; i += STORE) {
         const int s = i / rows_now, r = i - s * rows_now;
         const float* ml = a.part + tile_slot(from, s) * slot + stats + r0 + r;
         table[r * shares + s] = ml[0];
         table[JOIN + r * shares + s] = ml[a.part_rows];
       }
-      bar_softmax();
-      for (int r = warp - 4; r < rows_now; r += SOFTMAX / 32) {
-        float* tm = table + r * shares;
+      bar_store();
+      // as many lanes a row as it has parts, up to a warp
+      int wide = 1;
+      while (wide < shares && wide < 32) wide *= 2;
+      const int in = me & (wide - 1);
+#pragma unroll 1
+      for (int r0w = 0; r0w < rows_now; r0w += STORE / wide) {
+        const int r = r0w + me / wide;
+        float* tm = table + min(r, rows_now - 1) * shares;
         float top = -INFINITY, sum = 0.0f;
-        for (int s = lane; s < shares; s += 32) top = fmaxf(top, tm[s]);
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int s = in; s < shares; s += wide) top = fmaxf(top, tm[s]);
+        for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float base = top == -INFINITY ? 0.0f : top;
-        for (int s = lane; s < shares; s += 32) {
-          const float f = exp2_fast(tm[s] - base);
-          sum += tm[JOIN + s] * f;
-          tm[s] = f;
-        }
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int s = in; s < shares; s += wide) sum += tm[JOIN + s] * exp2_fast(tm[s] - base);
+        for (int o = wide / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         int tok, h;
-        if (!place(r0 + r, &tok, &h)) continue;
-        const int lim = keys_seen(w.s, tok, a.causal);
+        const bool there = r < rows_now && place(r0 + r, &tok, &h);
+        const int lim = there ? keys_seen(w.s, tok, a.causal) : 0;
         const float inv = lim == 0 ? 0.0f : sum == 0.0f ? __uint_as_float(0x7fc00000u) : 1.0f / sum;
-        for (int s = lane; s < shares; s += 32) tm[s] *= inv;
-        if (a.lse && lane == 0)
+        __syncwarp();  // rows past the last one read its entries
+        if (r < rows_now)
+          for (int s = in; s < shares; s += wide) tm[s] = exp2_fast(tm[s] - base) * inv;
+        if (there && a.lse && in == 0)
           a.lse[(static_cast<int64_t>(w.s.q0) + tok) * a.heads + h] = lim > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
       }
-      bar_softmax();
+      bar_store();
       constexpr int U = 2;  // two groups of eight columns at a time
       const int groups = rows_now * (a.dim / 8);
-      for (int i0 = me; i0 < groups; i0 += U * SOFTMAX) {
+      for (int i0 = me; i0 < groups; i0 += U * STORE) {
         float4 v[U][2];
         const float *src[U], *f[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int i = min(i0 + u * SOFTMAX, groups - 1), g = i / rows_now, r = i - g * rows_now;
+          const int i = min(i0 + u * STORE, groups - 1), g = i / rows_now, r = i - g * rows_now;
           v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           f[u] = table + r * shares;
           src[u] = a.part + (static_cast<int64_t>(2 * g) * a.part_rows + r0 + r) * 4;
@@ -558,7 +692,7 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
         if (s < shares) add(s);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int i = i0 + u * SOFTMAX, g = i / rows_now, r = i - g * rows_now;
+          const int i = i0 + u * STORE, g = i / rows_now, r = i - g * rows_now;
           int tok, h;
           if (i < groups && place(r0 + r, &tok, &h))
             *reinterpret_cast<uint4*>(a.out + (static_cast<int64_t>(w.s.q0) + tok) * a.ldo + h * a.ho + g * 8) =
@@ -566,9 +700,9 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
                            pack_bf16(v[u][1].x, v[u][1].y), pack_bf16(v[u][1].z, v[u][1].w));
         }
       }
-      bar_softmax();
+      bar_store();
     }
-    bar_softmax();
+    bar_store();
   }
 }
 
@@ -577,24 +711,31 @@ template <int DP>
 __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__ Args a) {
   using L = Layout<DP>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
   grid_dep_launch();
   const int warp = threadIdx.x >> 5;
   PlanScratch* plan = reinterpret_cast<PlanScratch*>(smem + L::PLAN);
   if (threadIdx.x == 0) {
-    uint32_t bar = sbase + L::BARS;
-    auto init = [&](int n, uint32_t count) {
-      for (int i = 0; i < n; ++i, bar += 8) mbar_init(bar, count);
+    const Bars<DP> b(sbase);
+    auto init = [&](uint32_t bar, int n, uint32_t count) {
+      for (int i = 0; i < n; ++i) mbar_init(bar + 8 * i, count);
     };
-    init(3 * L::STAGES, 1);  // kfull, kempty, vfull
-    init(L::STAGES, 3);      // vempty: the products and the two clearing warps
-    init(L::STAGES, 2);      // vfix
-    init(2, 1);              // qfull, qempty
-    init(2, 1);              // sfull
-    init(4, 4);              // pfull: the half's warps, 64 keys at a time
-    init(2, 1);              // ofull
-    init(1, 1);              // drain
+    init(b.kfull, L::STAGES, 1);
+    init(b.kempty, L::STAGES, 2);  // both halves' products
+    init(b.vfull, L::STAGES, 1);
+    init(b.vempty, L::STAGES, 3);  // and the clearing warp
+    init(b.vfix, L::STAGES, 1);
+    init(b.qfull, 1, 1);
+    init(b.qempty, 1, 2);
+    init(b.sfull, 2, 1);
+    init(b.pfull, 4, 4);           // a half's warps, 64 keys at a time
+    init(b.ofull, 2, 1);
+    init(b.ofree, 2, 4);
+    init(b.lfull, 2, 4);
+    init(b.lfree, 2, 4);
+    init(b.drain, 2, 1);
     fence_barrier_init();
     tma_prefetch_map(&a.q);
     tma_prefetch_map(&a.k);
@@ -612,15 +753,19 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
   grid_dep_wait();
   const Tiles tiles{a.kv_heads, a.tokens, a.causal};
   plan_shares<THREADS>(tiles, a.seq, plan);
-  const Shares sh = plan->shares;
+  const Shares& sh = plan->shares;
+  // registers: 128 a thread at launch, 65536 in all, shared out as the roles need them
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
     if (warp == 0) load_role<DP>(a, tiles, sh, sbase);
-    if (warp == 1) mma_role<DP>(a, tiles, sh, sbase, tmem);
-    if (warp >= 2) fix_role<DP>(a, tiles, sh, sbase, smem);
+    if (warp == 1 || warp == 2) mma_role<DP>(a, tiles, sh, sbase, tmem, warp - 1);
+    if (warp == 3) fix_role<DP>(a, tiles, sh, sbase, smem);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
+    softmax_role<DP>(a, tiles, sh, sbase, smem, tmem, (warp - 4) >> 2);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    softmax_role<DP>(a, tiles, sh, sbase, smem, tmem);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
+    store_role<DP>(a, tiles, sh, sbase, smem, tmem);
   }
   tc_fence_before();
   __syncthreads();
