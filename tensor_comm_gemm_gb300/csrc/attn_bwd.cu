@@ -409,18 +409,22 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
     const int64_t slot = static_cast<int64_t>(KEYS ? 2 : 1) * BLK * a.dim;
     float* part = a.part + part_slot(w) * slot + static_cast<int64_t>(second ? BLK : 0) * a.dim;
     uint8_t* stage = smem + L::STAGE + (warp - 4) * 2048;
-    const RowsOut to_rows = rows_out(valid && p.whole ? out + out_row * ld + head * hs : nullptr);
+    const void* to_row = valid && p.whole ? out + out_row * ld + head * hs : nullptr;
 #pragma unroll 1
-    for (int c = KEYS ? 0 : half; ok && c < chunks; c += KEYS ? 1 : 2) {
+    for (int c = KEYS ? 0 : half; ok && c < chunks; c += KEYS ? 1 : 2) {  // 32 columns
       uint32_t o[32];
-      float v[32];
       tmem_ld32_sync(lanes + (second ? 3 : 2) * BLK + c * 32, o);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * scale;
-      if (p.whole)
-        store_rows(stage, v, to_rows, c * 32, a.dim - c * 32);
-      else if (valid)
-        store_part(part, BLK, row, v, c * 32, a.dim);
+      for (int g = 0; g < 4; ++g) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * g + e]) * scale;
+        if (p.whole)
+          stage_row<32>(stage, g, v);
+        else if (valid)
+          store_part(part, BLK, row, v, c * 32 + g * 8, a.dim);
+      }
+      if (p.whole) store_staged<32>(stage, to_row, c * 32, a.dim - c * 32);
     }
     tc_fence_before();
     if (p.whole) continue;
@@ -428,7 +432,7 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
     __threadfence();
     bar_compute();
     int first;
-    const int shares = tile_shares(sh, w, &first);
+    const int shares = tile_shares(sh, tile_begin(sh, w), w.hi - w.lo, &first);
     volatile int* last = reinterpret_cast<volatile int*>(smem + L::LAST);
     if (me == 0) {
       const uint32_t before = atomicAdd(a.arrivals + first, ok ? 1u : 0u);

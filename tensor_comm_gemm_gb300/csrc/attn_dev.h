@@ -39,65 +39,45 @@ struct Part {
   bool whole;
 };
 
-// a / b for numbers that mostly have 32 bits.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
 struct Shares {
-  int64_t total, each;  // steps in all and of a share; the first `more` have one more
+  int total, each;      // steps in all (the host holds them below 2^31) and of a share; the first `more` have one more
   int count, more;
-  int64_t at, end;      // this block's share
+  int at, end;          // this block's share
   int seq;              // where it begins: sequence,
-  int64_t before;       // steps ahead of the sequence,
-  int64_t a_head;       // and steps of one of its key heads
+  int before;           // steps ahead of the sequence,
+  int a_head;           // and steps of one of its key heads
   Seq s;
 };
 
-__device__ __forceinline__ int64_t share_begin(const Shares& p, int c) { return c * p.each + min(c, p.more); }
+__device__ __forceinline__ int share_begin(const Shares& p, int c) { return c * p.each + min(c, p.more); }
 // The share that holds step x.
-__device__ __forceinline__ int share_of(const Shares& p, int64_t x) {
-  const int64_t longer = p.more * (p.each + 1);
-  return static_cast<int>(x < longer ? quotient(x, p.each + 1) : p.more + quotient(x - longer, p.each));
-}
-
-// Steps of all tiles of a sequence (one key head), by a converged warp.
-template <class T>
-__device__ __forceinline__ int64_t steps_by_warp(const T& t, const Seq& s, int tiles) {
-  int64_t sum = 0;
-  for (int i = threadIdx.x & 31; i < tiles; i += 32) {
-    int lo, hi;
-    t.range(s, i, &lo, &hi);
-    sum += hi - lo;
-  }
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
+__device__ __forceinline__ int share_of(const Shares& p, int x) {
+  const int longer = p.more * (p.each + 1);
+  const bool in = x < longer;
+  return (in ? 0 : p.more) + static_cast<int>(static_cast<uint32_t>(in ? x : x - longer) / static_cast<uint32_t>(p.each + (in ? 1 : 0)));
 }
 
 // Steps of sequence i for one key head; every thread of the block calls it, with
 // its own i (at or past `batch`: none).  *s gets the sequence, *tiles the tiles' number.
 template <class T>
-__device__ __forceinline__ int64_t cost_of(const T& t, const Sequences& q, int64_t i, Seq* s, int* tiles) {
-  int n = 0;
-  int64_t sum = 0;
+__device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i, Seq* s, int* tiles) {
   *s = Seq{0, 0, 0, 0};
-  if (i < q.batch) {
-    *s = sequence(q, i);
-    n = t.tiles(*s);
-    if (n <= 4)
-      for (int k = 0; k < n; ++k) {
-        int lo, hi;
-        t.range(*s, k, &lo, &hi);
-        sum += hi - lo;
-      }
-  }
-  for (uint32_t many = __ballot_sync(0xffffffffu, n > 4); many; many &= many - 1) {
-    const int l = __ffs(many) - 1;
+  if (i < q.batch) *s = sequence(q, i);
+  const int n = i < q.batch ? t.tiles(*s) : 0;
+  int sum = 0;
+  // one tile by the thread itself, the tiles of longer sequences by the whole warp
+  int lo, hi;
+  if (n == 1) t.range(*s, 0, &lo, &hi), sum = hi - lo;
+#pragma unroll 1
+  for (uint32_t many = __ballot_sync(0xffffffffu, n > 1); many; many &= many - 1) {
+    const int l = __ffs(many) - 1, count = __shfl_sync(0xffffffffu, n, l);
     Seq o{0, 0, 0, 0};
     o.nq = __shfl_sync(0xffffffffu, s->nq, l);
     o.nk = __shfl_sync(0xffffffffu, s->nk, l);
-    const int64_t v = steps_by_warp(t, o, __shfl_sync(0xffffffffu, n, l));
+    int v = 0;
+#pragma unroll 1
+    for (int k = threadIdx.x & 31; k < count; k += 32) t.range(o, k, &lo, &hi), v += hi - lo;
+    v = __reduce_add_sync(0xffffffffu, v);
     if ((threadIdx.x & 31) == l) sum = v;
   }
   *tiles = n;
@@ -105,85 +85,89 @@ __device__ __forceinline__ int64_t cost_of(const T& t, const Sequences& q, int64
 }
 
 struct PlanScratch {
-  int64_t steps[32], tiles[32];  // of a warp's sequences
+  int steps[32], tiles[32];  // of a warp's sequences
   Shares shares;
 };
 
 // Cuts the list; every thread of the block takes part.  At least MIN_STEPS a
 // share, unless there are more tiles than such shares.
 template <int THREADS, class T>
-__device__ __noinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc) {
-  constexpr int64_t MIN_STEPS = 2;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t total = 0, all_tiles = 0, mine = 0, upto = 0;  // mine: steps of this thread's sequence, upto: with those before
+__device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc) {
+  constexpr int MIN_STEPS = 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x;
+  int mine = 0, upto = 0;  // steps of this thread's sequence, and with those of the block's threads before it
   Seq s;
-  auto scan = [&](int64_t base) {
-    int n;
-    mine = cost_of(t, q, base + threadIdx.x, &s, &n);
-    upto = mine;
-    int64_t tiles = n;
-    for (int o = 1; o < 32; o *= 2) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += u;
-      tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-    }
-    __syncthreads();
-    if (lane == 31) sc->steps[warp] = upto, sc->tiles[warp] = tiles;
-    __syncthreads();
-    int64_t all = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w == warp) upto += all;
-      all += sc->steps[w];
-      all_tiles += sc->tiles[w];
-    }
-    return all;
-  };
-  for (int64_t base = 0; base < q.batch; base += THREADS) total += scan(base);
-  total *= t.kv_heads, all_tiles *= t.kv_heads;
   Shares p{};
-  p.total = total;
-  p.count = static_cast<int>(max(int64_t(1), min(min(static_cast<int64_t>(gridDim.x), total), max(total / MIN_STEPS, all_tiles))));
-  p.each = quotient(total, p.count);
-  p.more = static_cast<int>(total - p.each * p.count);
-  const int block = blockIdx.x;
-  if (block < p.count && total > 0) p.at = share_begin(p, block), p.end = share_begin(p, block + 1);
-  if (threadIdx.x == 0) sc->shares = p;
-  __syncthreads();
-  if (p.at >= p.end) return;
-  int64_t ahead = 0;
-  for (int64_t base = 0; base < q.batch; base += THREADS) {
-    int64_t all = 0;
-    if (q.batch > THREADS) all = scan(base);
-    const int64_t from = ahead + (upto - mine) * t.kv_heads;
-    if (from <= p.at && p.at < from + mine * t.kv_heads) {
-      sc->shares.seq = static_cast<int>(base + threadIdx.x);
-      sc->shares.before = from;
-      sc->shares.a_head = mine;
-      sc->shares.s = s;
+  // first all steps and tiles; then, once the share is known, where it begins (another scan, if there are more
+  // sequences than threads)
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int ahead = 0, tiles = 0;
+#pragma unroll 1
+    for (int64_t base = 0; base < q.batch; base += THREADS) {
+      int all = 0;
+      if (pass == 0 || q.batch > THREADS) {
+        int n;
+        mine = cost_of(t, q, base + threadIdx.x, &s, &n);
+        n = __reduce_add_sync(0xffffffffu, n);
+        upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int u = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += u;
+        }
+        __syncthreads();
+        if (lane == 31) sc->steps[warp] = upto, sc->tiles[warp] = n;
+        __syncthreads();
+        const int w_steps = lane < THREADS / 32 ? sc->steps[lane] : 0;
+        upto += __reduce_add_sync(0xffffffffu, lane < warp ? w_steps : 0);
+        all = __reduce_add_sync(0xffffffffu, w_steps);
+        tiles += __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? sc->tiles[lane] : 0);
+      }
+      if (pass == 1) {
+        const int from = ahead + (upto - mine) * t.kv_heads;
+        if (from <= p.at && p.at < from + mine * t.kv_heads) {
+          sc->shares.seq = static_cast<int>(base + threadIdx.x);
+          sc->shares.before = from;
+          sc->shares.a_head = mine;
+          sc->shares.s = s;
+        }
+      }
+      ahead += all * t.kv_heads;
     }
-    ahead += all * t.kv_heads;
+    if (pass == 0) {
+      p.total = ahead;
+      p.count = max(1, min(min(static_cast<int>(gridDim.x), ahead), max(ahead / MIN_STEPS, tiles * t.kv_heads)));
+      p.each = p.total / p.count;
+      p.more = p.total - p.each * p.count;
+      if (block < p.count && p.total > 0) p.at = share_begin(p, block), p.end = share_begin(p, block + 1);
+      if (threadIdx.x == 0) sc->shares = p;
+    }
+    __syncthreads();
+    if (p.at >= p.end) return;
   }
-  __syncthreads();
 }
 
 // The first tile of this block's share, by a converged warp.
 template <class T>
 __device__ __forceinline__ void walk_begin(const T& t, const Shares& p, Walk& w) {
   w.done = 0;
-  w.left = static_cast<int>(p.end - p.at);
+  w.left = p.end - p.at;
   if (w.left <= 0) return;
   w.seq = p.seq;
   w.s = p.s;
   w.tiles = t.tiles(w.s);
-  w.head = static_cast<int>(quotient(p.at - p.before, p.a_head));
-  int64_t ahead = p.before + p.a_head * w.head;
+  w.head = (p.at - p.before) / p.a_head;
+  int ahead = p.before + p.a_head * w.head;
   const int lane = threadIdx.x & 31;
-  for (int base = 0;; base += 32) {
+#pragma unroll 1
+  for (int base = 0; base < w.tiles; base += 32) {
     int lo = 0, hi = 0;
     if (base + lane < w.tiles) t.range(w.s, base + lane, &lo, &hi);
-    int64_t v = hi - lo;
+    int v = hi - lo;
+#pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += u;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, ahead + v > p.at);
@@ -192,15 +176,12 @@ __device__ __forceinline__ void walk_begin(const T& t, const Shares& p, Walk& w)
       w.tile = base + l;
       w.lo = __shfl_sync(0xffffffffu, lo, l);
       w.hi = __shfl_sync(0xffffffffu, hi, l);
-      w.off = static_cast<int>(p.at - ahead - __shfl_sync(0xffffffffu, v, l)) + (w.hi - w.lo);
-      return;
-    }
-    if (base + 32 >= w.tiles) {  // not reached: the tile exists
-      w.left = 0;
+      w.off = p.at - ahead - __shfl_sync(0xffffffffu, v, l) + (w.hi - w.lo);
       return;
     }
     ahead += __shfl_sync(0xffffffffu, v, 31);
   }
+  w.left = 0;  // not reached: the tile exists
 }
 __device__ __forceinline__ bool walk_has(const Walk& w) { return w.left > 0; }
 __device__ __forceinline__ Part walk_part(const Walk& w) {
@@ -236,41 +217,107 @@ __device__ __forceinline__ void walk_next(const T& t, const Sequences& q, Walk& 
 
 // Where a part of a divided tile goes: two slots a share, the first for the tile that it did not begin.
 __device__ __forceinline__ int part_slot(const Walk& w) { return 2 * static_cast<int>(blockIdx.x) + (w.off == 0 ? 1 : 0); }
-// The first of the shares that have a part of the tile, and their number.
-__device__ __forceinline__ int tile_shares(const Shares& p, const Walk& w, int* first) {
-  const int64_t begin = p.at + w.done - w.off;
+// The first of the shares that have a part of the tile that begins at step `begin`, and their number.
+__device__ __forceinline__ int tile_shares(const Shares& p, int begin, int steps, int* first) {
   *first = share_of(p, begin);
-  return share_of(p, begin + (w.hi - w.lo) - 1) - *first + 1;
+  return share_of(p, begin + steps - 1) - *first + 1;
 }
+__device__ __forceinline__ int tile_begin(const Shares& p, const Walk& w) { return p.at + w.done - w.off; }
 __device__ __forceinline__ int tile_slot(int first, int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
 
 // ------------------------------------------------------------------ waits
 
-// A converged warp's bounded wait.  The first tries (each of which the hardware may hold for a while) cost nothing
-// but the instruction itself; the clock is read only when they have failed.
-__device__ __forceinline__ bool wait_warp_long(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site) {
-  const unsigned long long t0 = gtime();
-  for (uint32_t i = 1;; ++i) {
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-    if ((i & 15u) == 0u) {
-      int stop = 0;
-      if ((threadIdx.x & 31) == 0) {
-        if (*reinterpret_cast<volatile uint32_t*>(w.err) != 0u) {
-          stop = 1;
-        } else if (gtime() - t0 > w.limit_ns) {
-          give_up(w.err, site);
-          stop = 1;
-        }
-      }
-      if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+// A converged warp's bounded wait, in few instructions: the kernels' roles share the instruction cache, and a kernel
+// that outgrows it runs at the speed of its misses (320 KB of code: a tile's stores took 8000 cycles instead of 3500).
+__device__ __forceinline__ bool wait_warp(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site) {
+  uint32_t tries = 0;
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  while (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
+    if ((++tries & 63u) != 0u) continue;
+    const unsigned long long now = gtime();
+    if (tries == 64u) t0 = now;
+    const bool late = now - t0 > w.limit_ns;
+    if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile uint32_t*>(w.err) != 0u)) {
+      if (late && (threadIdx.x & 31) == 0) give_up(w.err, site);
+      return false;
     }
   }
+  return true;
 }
-__device__ __forceinline__ bool wait_warp(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site) {
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i)
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  return wait_warp_long(w, bar, parity, site);
+
+// ------------------------------------------------------------------ items
+//
+// The loading warp walks over the share and hands its tiles to the other roles
+// through a ring in shared memory.  It needs no wait for free entries: it loads at
+// most two parts ahead of the products, which are at most two ahead of the stores.
+
+struct Entry {
+  Seq s;
+  int head, tile, lo, hi;  // the share's steps of the tile; none: the end
+  int from, shares;        // the shares that have parts of it (1: it is whole)
+  int slot;                // where a part goes
+  int direct;              // the other of two parts is there: join it as this one is stored
+};
+constexpr int RING = 8;
+static_assert(sizeof(Entry) == 48, "three 16-byte words");
+
+// By the loading warp: entry n of the ring; `w` has no more: the end.
+__device__ __forceinline__ Entry put_item(const Shares& sh, const Walk& w, uint8_t* ring, uint32_t full, uint32_t n,
+                                          const uint32_t* arrivals) {
+  Entry e;
+  e.s = w.s, e.head = w.head, e.tile = w.tile;
+  e.lo = e.hi = 0, e.from = 0, e.shares = 1, e.slot = 0, e.direct = 0;
+  if (walk_has(w)) {
+    const Part p = walk_part(w);
+    e.lo = p.lo, e.hi = p.hi;
+    if (!p.whole) {
+      e.shares = tile_shares(sh, tile_begin(sh, w), w.hi - w.lo, &e.from);
+      e.slot = part_slot(w);
+      if (e.shares == 2) e.direct = ld_acquire(arrivals + e.from) == 1u;
+      e.direct = __shfl_sync(0xffffffffu, e.direct, 0);
+    }
+  }
+  if ((threadIdx.x & 31) == 0) {
+    int4* to = reinterpret_cast<int4*>(ring + n % RING * sizeof(Entry));
+    to[0] = make_int4(e.s.q0, e.s.nq, e.s.k0, e.s.nk);
+    to[1] = make_int4(e.head, e.tile, e.lo, e.hi);
+    to[2] = make_int4(e.from, e.shares, e.slot, e.direct);
+    mbar_arrive(full + 8 * (n % RING));
+  }
+  __syncwarp();
+  return e;
+}
+// By the others: false at the end, or if the wait ran out.
+__device__ __forceinline__ bool get_item(const Watch& w, const uint8_t* ring, uint32_t full, uint32_t n, Entry* e) {
+  if (!wait_warp(w, full + 8 * (n % RING), n / RING & 1u, S_FULL)) return false;
+  const int4* from = reinterpret_cast<const int4*>(ring + n % RING * sizeof(Entry));
+  const int4 a = from[0], b = from[1], c = from[2];
+  e->s = {a.x, a.y, a.z, a.w};
+  e->head = b.x, e->tile = b.y, e->lo = b.z, e->hi = b.w;
+  e->from = c.x, e->shares = c.y, e->slot = c.z, e->direct = c.w;
+  return e->hi > e->lo;
+}
+
+// The storing warps of a block count themselves for each divided tile; the last of them counts the part, and if all of
+// the tile's are there, notes the tile for the end of the block, when all its threads join the parts.
+struct Pending {
+  Entry tile[2];  // the one that the share did not begin, and the one that it did
+  int due[2];
+  int warps[2];
+};
+__device__ __forceinline__ void part_stored(Pending* p, const Entry& e, int warps, uint32_t* arrivals) {
+  __threadfence();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0 && atomicAdd(&p->warps[e.slot & 1], 1) == warps - 1) {
+    __threadfence();
+    if (atomicAdd(arrivals + e.from, 1u) + 1 == static_cast<uint32_t>(e.shares)) {
+      arrivals[e.from] = 0;
+      p->tile[e.slot & 1] = e;
+      p->due[e.slot & 1] = 1;
+    }
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ matrix instructions
@@ -411,43 +458,39 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // ------------------------------------------------------------------ results
 
-// A warp stores 32 columns of its 32 rows (v: the lane's row) as bf16, through 2 KiB of shared memory at `stage`:
-// row by row 64 bytes of a line at a time.  (Each lane storing 16 bytes of its own row costs a cycle of the SM's
-// memory pipe for each lane, 7000 for the 256 rows of a tile.)  to[i], where rows (lane / 4 + 8 i) go, 0: nowhere;
-// `cols` of the 32 exist.
-struct RowsOut {
-  uint64_t to[4];
-};
-__device__ __forceinline__ RowsOut rows_out(const void* mine) {  // mine: the lane's own row, NULL: none
-  RowsOut r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r.to[i] = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), ((threadIdx.x & 31) >> 2) + 8 * i);
-  return r;
+// A warp stores W (32 or 64) columns of its 32 rows as bf16 through 64 W bytes of shared memory at `stage`, row by row:
+// lines of 2 W bytes.  (Each lane storing 16 bytes of its own row costs a cycle of the SM's memory pipe for each lane,
+// 7000 for the 256 rows of a tile.)  First each lane brings its own row, eight columns from 8 g on at a time; then
+// `mine`, the lane's row in global memory (NULL: none), gets columns [col, col + W), of which `cols` exist.
+template <int W>
+__device__ __forceinline__ uint32_t stage_at(int row, int g) {
+  return W == 64 ? row * 128 + ((g ^ (row & 7)) << 4) : row * 64 + ((g ^ ((row >> 1) & 3)) << 4);
 }
-__device__ __forceinline__ void store_rows(uint8_t* stage, const float (&v)[32], const RowsOut& r, int col, int cols) {
-  const int lane = threadIdx.x & 31, part = lane & 3;
-  __syncwarp();  // the chunk before has been read
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-    *reinterpret_cast<uint4*>(stage + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(pack_bf16(v[8 * g], v[8 * g + 1]), pack_bf16(v[8 * g + 2], v[8 * g + 3]),
-                   pack_bf16(v[8 * g + 4], v[8 * g + 5]), pack_bf16(v[8 * g + 6], v[8 * g + 7]));
+template <int W>
+__device__ __forceinline__ void stage_row(uint8_t* stage, int g, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(stage + stage_at<W>(threadIdx.x & 31, g)) =
+      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+template <int W>
+__device__ __forceinline__ void store_staged(const uint8_t* stage, const void* mine, int col, int cols) {
+  constexpr int G = W / 8;  // lanes a row
+  const int lane = threadIdx.x & 31, part = lane % G;
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = (lane >> 2) + 8 * i;
-    const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 64 + ((part ^ ((row >> 1) & 3)) << 4));
-    if (r.to[i] && part * 8 < cols) *reinterpret_cast<uint4*>(r.to[i] + (col + part * 8) * 2) = x;
+  for (int i = 0; i < G; ++i) {
+    const int row = lane / G + 32 / G * i;
+    const uint64_t to = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), row);
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + stage_at<W>(row, part));
+    if (to && part * 8 < cols) *reinterpret_cast<uint4*>(to + (col + part * 8) * 2) = x;
   }
+  __syncwarp();  // before the next columns
 }
-// Parts of divided tiles lie as [dim / 4][rows][4] floats: a warp's 32 rows side by side.
-__device__ __forceinline__ void store_part(float* part, int rows, int row, const float (&v)[32], int col, int dim) {
-#pragma unroll
-  for (int g = 0; g < 8; ++g)
-    if (col + 4 * g < dim)
-      *reinterpret_cast<float4*>(part + (static_cast<int64_t>((col >> 2) + g) * rows + row) * 4) =
-          make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+// Parts of divided tiles lie as [dim / 4][rows][4] floats: a warp's 32 rows side by side.  Eight columns from col on.
+__device__ __forceinline__ void store_part(float* part, int rows, int row, const float (&v)[8], int col, int dim) {
+  if (col >= dim) return;
+  float* p = part + (static_cast<int64_t>(col >> 2) * rows + row) * 4;
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + static_cast<int64_t>(rows) * 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 // ------------------------------------------------------------------ host side

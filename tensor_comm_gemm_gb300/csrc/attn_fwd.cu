@@ -43,7 +43,6 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int THREADS = 512;
-constexpr int STORE = 128;               // threads of the storing group
 constexpr float GROWTH = 8.0f;           // of the maximum, in powers of two, before O is rescaled
 constexpr int JOIN = 2048;               // parts of rows whose weights are in shared memory at a time
 constexpr int BAD_SETS = 8, BAD_STEPS = 3;  // steps of a tile that only some of its rows see whole
@@ -82,21 +81,22 @@ struct Layout {
   static constexpr int TILE = BLK * DP * 2;          // 128 rows of a head
   static constexpr int STAGES = DP == 128 ? 2 : 4;   // of K, and of V
   static constexpr int K0 = 2 * TILE, V0 = K0 + STAGES * TILE, BARS = V0 + STAGES * TILE;
-  static constexpr int N_BARS = 5 * STAGES + 18;
-  static constexpr int SLOT = BARS + 8 * N_BARS;
-  static constexpr int LAST = SLOT + 4;
-  static constexpr int BAD = SLOT + 8;               // [BAD_SETS][BAD_STEPS][4] keys, a bit each
-  static constexpr int ROWS = (BAD + BAD_SETS * BAD_STEPS * 16 + 15) / 16 * 16;  // [2][2][128] floats: maxima and sums
-  static constexpr int JOIN_AT = ROWS + 2048;        // [2][JOIN] floats, or the storing warps' staging boxes
-  static constexpr int PLAN = JOIN_AT + 8 * JOIN;
-  static_assert(JOIN_AT % 16 == 0 && 8 * JOIN >= 4 * 2048, "also a staging box for each warp");
+  static constexpr int N_BARS = 5 * STAGES + RING + 18;
+  static constexpr int SLOT = BARS + 8 * N_BARS;     // the address of tensor memory, then the issuing warps' turns
+  static constexpr int RING_AT = (SLOT + 16 + 15) / 16 * 16;
+  static constexpr int BAD = RING_AT + RING * static_cast<int>(sizeof(Entry));  // [BAD_SETS][BAD_STEPS][4] keys, a bit each
+  static constexpr int ROWS = BAD + BAD_SETS * BAD_STEPS * 16;  // [2][2][128] floats: maxima and sums
+  static constexpr int PENDING = ROWS + 2048;
+  static constexpr int STAGE = PENDING + (static_cast<int>(sizeof(Pending)) + 15) / 16 * 16;  // the storing warps' boxes
+  static constexpr int PLAN = STAGE + 4 * 4096;
   static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
-  static_assert(SMEM <= 232448, "shared memory of one block");
+  static constexpr int TABLE = 0, SUMS = 8 * JOIN;   // at the end, over the tiles: [2][JOIN] and [THREADS][8] floats
+  static_assert(SMEM <= 232448 && RING_AT % 16 == 0, "shared memory of one block");
 };
 
 template <int DP>
 struct Bars {
-  uint32_t kfull, kempty, vfull, vempty, vfix, qfull, qempty, sfull, pfull, ofull, ofree, lfull, lfree, drain;
+  uint32_t kfull, kempty, vfull, vempty, vfix, items, qfull, qempty, sfull, pfull, ofull, ofree, lfull, lfree, drain;
   __device__ explicit Bars(uint32_t sbase) {
     uint32_t b = sbase + Layout<DP>::BARS;
     auto next = [&](int n) {
@@ -105,72 +105,81 @@ struct Bars {
       return r;
     };
     constexpr int S = Layout<DP>::STAGES;
-    kfull = next(S), kempty = next(S), vfull = next(S), vempty = next(S), vfix = next(S), qfull = next(1);
-    qempty = next(1), sfull = next(2), pfull = next(4), ofull = next(2), ofree = next(2), lfull = next(2);
-    lfree = next(2), drain = next(2);
+    kfull = next(S), kempty = next(S), vfull = next(S), vempty = next(S), vfix = next(S), items = next(RING);
+    qfull = next(1), qempty = next(1), sfull = next(2), pfull = next(4), ofull = next(2), ofree = next(2);
+    lfull = next(2), lfree = next(2), drain = next(2);
   }
 };
 
-__device__ __forceinline__ void bar_store() { asm volatile("bar.sync 1, %0;" ::"n"(STORE) : "memory"); }
-
-// What the roles derive from a part of a tile.
-struct Item {
-  Part p;
+// What the roles derive from an entry.
+struct Item : Entry {
   int tok;    // first token of the tile, in the sequence
   int halves;
   int some;   // keys from here on are not seen by all queries
 };
-__device__ __forceinline__ Item item_of(const Args& a, const Walk& w) {
-  Item i;
-  i.p = walk_part(w);
-  i.tok = w.tile * 2 * a.tokens;
-  i.halves = w.s.nq - i.tok <= a.tokens ? 1 : 2;
-  i.some = keys_seen(w.s, i.tok, a.causal);
-  return i;
+__device__ __forceinline__ void derive(const Args& a, Item& i) {
+  i.tok = i.tile * 2 * a.tokens;
+  i.halves = i.s.nq - i.tok <= a.tokens ? 1 : 2;
+  i.some = keys_seen(i.s, i.tok, a.causal);
+}
+template <int DP>
+__device__ __forceinline__ bool next_item(const Args& a, const Bars<DP>& b, const uint8_t* smem, uint32_t n, Item& i) {
+  if (!get_item(a.watch, smem + Layout<DP>::RING_AT, b.items, n, &i)) return false;
+  derive(a, i);
+  return true;
 }
 __device__ __forceinline__ bool needs_fix(const Item& i, int j) { return (j + 1) * BLK > i.some; }
 
 template <int DP>
-__device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase) {
+__device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const bool lead = (threadIdx.x & 31) == 0;
   uint32_t kn = 0, vn = 0, qn = 0;  // loads so far
   bool ok = true;
-  Walk w;
-  for (walk_begin(tiles, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
-    const Item it = item_of(a, w);
+  Walk w{};
+  for (walk_begin(tiles, sh, w); ok; walk_next(tiles, a.seq, w)) {
+    Item it;
+    static_cast<Entry&>(it) = put_item(sh, w, smem + L::RING_AT, b.items, qn, a.arrivals);
+    if (it.hi <= it.lo) break;
+    derive(a, it);
     if (!(ok = wait_warp(a.watch, b.qempty, (qn & 1u) ^ 1u, S_EMPTY))) break;
     if (lead) {
       mbar_expect_tx(b.qfull, static_cast<uint32_t>(a.group * a.tokens) * 128u * (DP / 64) * it.halves);
+#pragma unroll 1
       for (int h = 0; h < it.halves; ++h)
         for (int d = 0; d < DP / 64; ++d)
-          tma_load_3d(sbase + h * L::TILE + d * 16384, &a.q, b.qfull, d * 64, w.head * a.group,
-                      w.s.q0 + it.tok + h * a.tokens);
+          tma_load_3d(sbase + h * L::TILE + d * 16384, &a.q, b.qfull, d * 64, it.head * a.group,
+                      it.s.q0 + it.tok + h * a.tokens);
     }
     __syncwarp();
     ++qn;
-    auto load = [&](const CUtensorMap* map, uint32_t full, uint32_t empty, uint32_t base, uint32_t& n, int j) {
-      const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
-      if (!wait_warp(a.watch, empty + 8 * st, ph ^ 1u, S_EMPTY)) return false;
+    // K one step ahead of V, as the products take them: K, K, V, K, V, .. V
+    const int loads = 2 * (it.hi - it.lo);
+#pragma unroll 1
+    for (int i = 0; ok && i < loads; ++i) {
+      const bool v = i == loads - 1 || (i > 1 && !(i & 1));
+      const int j = it.lo + (v ? (i - 1) >> 1 : (i + 1) >> 1);
+      const uint32_t n = v ? vn : kn, st = n % L::STAGES, full = (v ? b.vfull : b.kfull) + 8 * st;
+      if (!(ok = wait_warp(a.watch, (v ? b.vempty : b.kempty) + 8 * st, (n / L::STAGES & 1u) ^ 1u, S_EMPTY))) break;
       if (lead) {
-        mbar_expect_tx(full + 8 * st, L::TILE);
+        mbar_expect_tx(full, L::TILE);
         for (int d = 0; d < DP / 64; ++d)
-          tma_load_3d(base + st * L::TILE + d * 16384, map, full + 8 * st, d * 64, w.head, w.s.k0 + j * BLK);
+          tma_load_3d(sbase + (v ? L::V0 : L::K0) + st * L::TILE + d * 16384, v ? &a.v : &a.k, full, d * 64, it.head,
+                      it.s.k0 + j * BLK);
       }
       __syncwarp();
-      ++n;
-      return true;
-    };
-    // K one step ahead of V, as the products take them
-    for (int j = it.p.lo; ok && j <= it.p.hi; ++j) {
-      if (j < it.p.hi) ok = load(&a.k, b.kfull, b.kempty, sbase + L::K0, kn, j);
-      if (ok && j > it.p.lo) ok = load(&a.v, b.vfull, b.vempty, sbase + L::V0, vn, j - 1);
+      if (v)
+        ++vn;
+      else
+        ++kn;
     }
   }
   if (!ok && lead) {  // what is in flight must land before the block gives up its shared memory
+#pragma unroll 1
     for (uint32_t j = kn > L::STAGES ? kn - L::STAGES : 0u; j < kn; ++j)
       wait_bar(a.watch, b.kfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
+#pragma unroll 1
     for (uint32_t j = vn > L::STAGES ? vn - L::STAGES : 0u; j < vn; ++j)
       wait_bar(a.watch, b.vfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
     if (qn) wait_bar(a.watch, b.qfull, (qn - 1) & 1u, S_DRAIN, false);
@@ -178,24 +187,10 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
   __syncwarp();
 }
 
-// The turns of the two issuing warps, by named barriers: pass_turn lets the other's next take_turn through.
-__device__ __forceinline__ void take_turn(int half) {
-  if (half)
-    asm volatile("bar.sync 2, 64;" ::: "memory");
-  else
-    asm volatile("bar.sync 3, 64;" ::: "memory");
-}
-__device__ __forceinline__ void pass_turn(int half) {
-  if (half)
-    asm volatile("bar.arrive 3, 64;" ::: "memory");
-  else
-    asm volatile("bar.arrive 2, 64;" ::: "memory");
-}
-
 // The products of one half.  Where a tile has one half only, the warps (and accumulators) take its steps by turns, and
 // pass over the other's: both release a stage.
 template <int DP>
-__device__ void mma_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint32_t tmem, int half) {
+__device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, int half) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const bool lead = (threadIdx.x & 31) == 0;
@@ -203,114 +198,102 @@ __device__ void mma_role(const Args& a, const Tiles& tiles, const Shares& sh, ui
   const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), (a.dim + 15) / 16 * 16) | 1u << 16;
   const uint64_t dk = smem_desc_sw128(sbase + L::K0), dv = desc_rows(sbase + L::V0);
   const uint32_t s = tmem + half * BLK, o = tmem + 2 * BLK + half * BLK;
-  uint32_t kn = 0, vn = 0, qn = 0, pn = 0;
+  uint32_t kn = 0, vn = 0, qn = 0, pn = 0, on = 0, turn = 0;
   uint32_t fixed = 0;  // parity of each stage's next clearing
-  bool ok = true;      // after a failure the turns go on, without waits and products
-  bool turns = false;  // whether there was a turn: the first is half 0's without asking
-  Walk w;
-  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++qn) {
-    const Item it = item_of(a, w);
-    const int steps = it.p.hi - it.p.lo;
-    const uint64_t dq = smem_desc_sw128(sbase + (it.halves == 2 ? half * L::TILE : 0));
-    auto await = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = wait_warp(a.watch, bar, parity & 1u, S_FULL);
-    };
-    auto await_k = [&] { await(b.kfull + 8 * (kn % L::STAGES), kn / L::STAGES); };
-    auto await_v = [&](int i) {
-      const uint32_t st = vn % L::STAGES;
-      await(b.vfull + 8 * st, vn / L::STAGES);
-      if (needs_fix(it, it.p.lo + i)) {
-        await(b.vfix + 8 * st, fixed >> st);
-        fixed ^= 1u << st;
+  volatile uint32_t* turns = reinterpret_cast<volatile uint32_t*>(smem + L::SLOT + 4);  // taken by each warp
+  bool ok = true;
+  auto await = [&](uint32_t bar, uint32_t parity) {
+    if (ok) ok = wait_warp(a.watch, bar, parity & 1u, S_FULL);
+  };
+  for (Item it; ok && next_item(a, b, smem, qn, it); ++qn) {
+    const int steps = it.hi - it.lo;
+    const bool two = it.halves == 2;
+    const uint64_t dq = smem_desc_sw128(sbase + (two ? half * L::TILE : 0));
+    await(b.qfull, qn);
+    // The next scores: of step i, if it is this warp's.  With one half the other turn's are only released.
+    auto scores = [&](int i) {
+      const uint32_t st = kn % L::STAGES;
+      const bool mine = two || (i & 1) == half;
+      await(b.kfull + 8 * st, kn / L::STAGES);
+      if (ok && mine) {
+        tc_fence_after();
+        mma_head<DP>(s, dq, dk + st * (L::TILE >> 4), idesc_s);
+        mma_commit_cg<1>(b.sfull + 8 * half);
       }
     };
-    auto scores = [&] {
-      if (!ok) return;
-      tc_fence_after();
-      mma_head<DP>(s, dq, dk + (kn % L::STAGES) * (L::TILE >> 4), idesc_s);
-      mma_commit_cg<1>(b.sfull + 8 * half);
-    };
-    auto free_k = [&] {
-      if (ok) mma_commit_cg<1>(b.kempty + 8 * (kn % L::STAGES));
+    auto free_k = [&](int i) {
+      const uint32_t st = kn % L::STAGES;
+      if (ok && (two || (i & 1) == half))
+        mma_commit_cg<1>(b.kempty + 8 * st);
+      else if (lead)
+        mbar_arrive(b.kempty + 8 * st);
       ++kn;
     };
-    auto free_v = [&] {
-      if (ok) mma_commit_cg<1>(b.vempty + 8 * (vn % L::STAGES));
-      ++vn;
-    };
-    auto product = [&](int part, bool fresh) {  // 64 keys
-      if (!ok) return;
-      tc_fence_after();
-      mma4_ts(o, s + 64 * part, dv + (vn % L::STAGES) * (L::TILE >> 4) + 512 * part, idesc_o, fresh ? 0u : 1u);
-    };
-    await(b.qfull, qn);
-    if (it.halves == 2) {
-      await_k();
-      scores();
-      free_k();
-      if (steps == 1 && ok) mma_commit_cg<1>(b.qempty);
-      for (int i = 0; i < steps; ++i, ++pn) {
-        const bool more = i + 1 < steps;
-        // the accumulator is free once the part before has been stored
-        if (i == 0 && qn > 0) await(b.ofree + 8 * half, qn - 1);
-        await_v(i);
-        if (more) await_k();
-        await(b.pfull + 16 * half, pn);
-        product(0, i == 0);
-        await(b.pfull + 16 * half + 8, pn);
-        if (half || turns) take_turn(half);
-        turns = true;
-        product(1, false);
-        if (more)
-          scores();
-        else if (ok)
-          mma_commit_cg<1>(b.ofull + 8 * half);
-        pass_turn(half);
-        free_v();
-        if (more) free_k();
-        if (i + 2 == steps && ok) mma_commit_cg<1>(b.qempty);
+    int k = 0;  // steps whose scores are made
+#pragma unroll 1
+    while (k < steps && k <= (two ? 0 : half)) {
+      scores(k);
+      free_k(k);
+      if (++k == steps && ok) mma_commit_cg<1>(b.qempty);
+    }
+    // the accumulator is free once the last part that used it has been stored
+    if (two || half < steps) {
+      if (on > 0) await(b.ofree + 8 * half, on - 1);
+      ++on;
+    }
+#pragma unroll 1
+    for (int i = 0; ok && i < steps; ++i) {
+      const uint32_t st = vn % L::STAGES;
+      const bool mine = two || (i & 1) == half;
+      await(b.vfull + 8 * st, vn / L::STAGES);
+      if (needs_fix(it, it.lo + i)) {
+        if (mine) await(b.vfix + 8 * st, fixed >> st);
+        fixed ^= 1u << st;
       }
-    } else {
-      auto skip_k = [&] {
-        await_k();
-        if (lead) mbar_arrive(b.kempty + 8 * (kn % L::STAGES));
-        ++kn;
-      };
-      auto skip_v = [&](int i) {
-        await(b.vfull + 8 * (vn % L::STAGES), vn / L::STAGES);
-        if (needs_fix(it, it.p.lo + i)) fixed ^= 1u << (vn % L::STAGES);
-        if (lead) mbar_arrive(b.vempty + 8 * (vn % L::STAGES));
-        ++vn;
-      };
-      if (half) skip_k();
-      if (half < steps) {
-        await_k();
-        scores();
-        free_k();
-      }
-      if (qn > 0) await(b.ofree + 8 * half, qn - 1);
-      if (half) skip_v(0);
-      for (int i = half; i < steps; i += 2, ++pn) {
-        await_v(i);
+      if (mine) {
+        const uint64_t vd = dv + st * (L::TILE >> 4);
+        // with two halves the next keys are long there: no wait between this product and their scores
+        if (two && k < steps) await(b.kfull + 8 * (kn % L::STAGES), kn / L::STAGES);
         await(b.pfull + 16 * half, pn);
-        product(0, i < 2);
-        await(b.pfull + 16 * half + 8, pn);
-        product(1, false);
-        free_v();
-        if (i + 1 < steps) skip_k();
-        if (i + 2 < steps) {
-          await_k();
-          scores();
-          free_k();
-        } else if (ok) {
-          mma_commit_cg<1>(b.ofull + 8 * half);
+        if (ok) {
+          tc_fence_after();
+          mma4_ts(o, s, vd, idesc_o, i > (two ? 0 : half) ? 1u : 0u);
         }
-        if (i + 1 < steps) skip_v(i + 1);
+        await(b.pfull + 16 * half + 8, pn++);
+        if (two) {  // half 0's nth turn comes after half 1's one before, half 1's nth after half 0's nth
+          const uint32_t due = turn + half;
+          uint32_t tries = 0;
+#pragma unroll 1
+          while (ok && !__all_sync(0xffffffffu, static_cast<int32_t>(turns[1 - half] - due) >= 0))
+            if ((++tries & 255u) == 0u)
+              ok = __all_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(a.watch.err) == 0u);
+        }
+        if (ok) {
+          tc_fence_after();
+          mma4_ts(o, s + 64, vd + 512, idesc_o, 1u);
+          if (two && k < steps) {
+            mma_head<DP>(s, dq, dk + (kn % L::STAGES) * (L::TILE >> 4), idesc_s);
+            mma_commit_cg<1>(b.sfull + 8 * half);
+          }
+        }
+        if (two) {
+          ++turn;
+          if (lead) turns[half] = turn;
+          __syncwarp();
+        }
+        if (ok) mma_commit_cg<1>(b.vempty + 8 * st);
+        if (ok && i + (two ? 1 : 2) >= steps) mma_commit_cg<1>(b.ofull + 8 * half);
+      } else if (lead) {
+        mbar_arrive(b.vempty + 8 * st);
       }
-      if (ok) mma_commit_cg<1>(b.qempty);
+      ++vn;
+      if (k < steps) {
+        if (!two) scores(k);
+        free_k(k);
+        if (++k == steps && ok) mma_commit_cg<1>(b.qempty);
+      }
     }
   }
-  if (!half && turns) take_turn(half);  // the last one that was passed
   // also after a failure: every MMA issued must complete before tensor memory is freed
   mma_commit_cg<1>(b.drain + 8 * half);
   if (lead) wait_bar(a.watch, b.drain + 8 * half, 0u, S_DRAIN, false);
@@ -320,18 +303,17 @@ __device__ void mma_role(const Args& a, const Tiles& tiles, const Shares& sh, ui
 // Clears the rows of V behind the last key, and takes values that are not finite
 // out of rows that only some queries see, noting their keys.
 template <int DP>
-__device__ void fix_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem) {
+__device__ void fix_role(const Args& a, uint32_t sbase, uint8_t* smem) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const int lane = threadIdx.x & 31;
   uint32_t vn = 0, item = 0;
-  Walk w;
-  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++item) {
-    const Item it = item_of(a, w);
+  for (Item it; next_item(a, b, smem, item, it); ++item) {
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::BAD) + item % BAD_SETS * BAD_STEPS * 4;
     if (lane < 4 * BAD_STEPS) bad[lane] = 0;
     __syncwarp();
-    for (int j = it.p.lo; j < it.p.hi; ++j, ++vn) {
+#pragma unroll 1
+    for (int j = it.lo; j < it.hi; ++j, ++vn) {
       const uint32_t st = vn % L::STAGES;
       if (!wait_warp(a.watch, b.vfull + 8 * st, vn / L::STAGES & 1u, S_FULL)) return;
       if (needs_fix(it, j)) {
@@ -340,33 +322,29 @@ __device__ void fix_role(const Args& a, const Tiles& tiles, const Shares& sh, ui
         for (int g = 0; g < 4; ++g) {
           const int r = 32 * g + lane, key = j * BLK + r;
           uint32_t top = 0;  // the row's largest magnitudes, as a pair of bf16
-          if (key >= w.s.nk) {
+#pragma unroll 1
+          for (int d = 0; d < DP / 64; ++d)
 #pragma unroll
-            for (int d = 0; d < DP / 64; ++d)
+            for (int i = 0; i < 8; ++i) {
+              uint4* x = reinterpret_cast<uint4*>(v + d * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
+              if (key >= it.s.nk) {
+                *x = make_uint4(0, 0, 0, 0);
+              } else if (key >= it.some) {
+                const uint32_t y[4] = {x->x, x->y, x->z, x->w};
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(v + d * 16384 + r * 128 + ((i ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-          } else if (key >= it.some) {
-            auto most = [&](uint32_t x) {
-              asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(x & 0x7fff7fffu));
-            };
-#pragma unroll
-            for (int d = 0; d < DP / 64; ++d)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4*>(v + d * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
-                most(x.x), most(x.y), most(x.z), most(x.w);
+                for (int k = 0; k < 4; ++k) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(y[k] & 0x7fff7fffu));
               }
-          }
+            }
           const bool found = (top & 0x7f80u) == 0x7f80u || (top & 0x7f800000u) == 0x7f800000u;
           const uint32_t all = __ballot_sync(0xffffffffu, found);
           if (!all) continue;
-          if (found)
-            for (int d = 0; d < DP / 64; ++d)
-              for (int i = 0; i < 64; ++i) {
-                uint16_t* x = reinterpret_cast<uint16_t*>(v + d * 16384 + r * 128) + i;
-                if ((*x & 0x7f80u) == 0x7f80u) *x = 0;
-              }
+          if (found) {
+#pragma unroll 1
+            for (int i = 0; i < DP; ++i) {
+              uint16_t* x = reinterpret_cast<uint16_t*>(v + (i >> 6) * 16384 + r * 128) + (i & 63);
+              if ((*x & 0x7f80u) == 0x7f80u) *x = 0;
+            }
+          }
           if (lane == 0) bad[(j - it.some / BLK) * 4 + g] = all;  // from the step that holds key `some` on
           __syncwarp();
         }
@@ -385,17 +363,16 @@ struct Row {
   int t, limit;  // its token, the keys that it sees
   bool valid;
 };
-__device__ __forceinline__ Row row_of(const Args& a, const Walk& w, const Item& it, int half, int dt) {
+__device__ __forceinline__ Row row_of(const Args& a, const Item& it, int half, int dt) {
   Row r;
   r.t = it.tok + (it.halves == 2 ? half * a.tokens : 0) + dt;
-  r.valid = dt < a.tokens && r.t < w.s.nq;
-  r.limit = r.valid ? keys_seen(w.s, r.t, a.causal) : 0;
+  r.valid = dt < a.tokens && r.t < it.s.nq;
+  r.limit = r.valid ? keys_seen(it.s, r.t, a.causal) : 0;
   return r;
 }
 
 template <int DP>
-__device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem,
-                             uint32_t tmem, int half) {
+__device__ void softmax_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, int half) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
@@ -411,32 +388,38 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  Walk w;
-  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++item) {
-    const Item it = item_of(a, w);
-    const int steps = it.p.hi - it.p.lo;
-    const int limit = row_of(a, w, it, half, dt).limit;
+  for (Item it; ok && next_item(a, b, smem, item, it); ++item) {
+    const int steps = it.hi - it.lo;
+    const int limit = row_of(a, it, half, dt).limit;
     const bool idle = __all_sync(0xffffffffu, limit == 0);
     float m = -INFINITY, l = 0.0f;  // the maximum that is subtracted (in powers of two), the sum
     const int first = it.halves == 2 ? 0 : half, by = it.halves == 2 ? 1 : 2;
+#pragma unroll 1
     for (int i = first; i < steps; i += by, ++sn) {
-      if (ok) ok = wait_warp(a.watch, b.sfull + 8 * half, sn & 1u, S_TFULL);
-      if (!ok || idle) {
+      if (!(ok = wait_warp(a.watch, b.sfull + 8 * half, sn & 1u, S_TFULL))) break;
+      if (idle) {
         arrive(b.pfull + 16 * half);
         arrive(b.pfull + 16 * half + 8);
         continue;
       }
       // all of the row's scores in registers
       uint32_t x[64], y[64];
-      const int left = limit - (it.p.lo + i) * BLK;
+      const int left = limit - (it.lo + i) * BLK;
       tc_fence_after();
       tmem_ld128_sync(ts, x, y);
-      if (!__all_sync(0xffffffffu, left >= BLK)) {
+      const int least = __reduce_min_sync(0xffffffffu, left);
+      if (least < BLK) {  // only the columns that some row does not see
+        auto mask = [&](uint32_t(&z)[64], int from) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          if (e >= left) x[e] = 0xff800000u;
-          if (e + 64 >= left) y[e] = 0xff800000u;
-        }
+          for (int g = 0; g < 4; ++g)
+            if (from + 16 * g + 16 > least) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (from + 16 * g + e >= left) z[16 * g + e] = 0xff800000u;
+            }
+        };
+        mask(x, 0);
+        mask(y, 64);
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -494,66 +477,76 @@ __device__ void softmax_role(const Args& a, const Tiles& tiles, const Shares& sh
   }
 }
 
-// Divides by the sums and stores, and joins the parts of divided tiles.
+// Divides by the sums and stores.
 template <int DP>
-__device__ void store_role(const Args& a, const Tiles& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem,
-                           uint32_t tmem) {
+__device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane, me = threadIdx.x - 384;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
   const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * BLK;
   const int dt = row / a.group, head_in = row - dt * a.group;  // the row's token in its half, its head in the group
   const int chunks = (a.dim + 31) / 32;
   const float* stats = reinterpret_cast<const float*>(smem + L::ROWS);
-  uint8_t* stage = smem + L::JOIN_AT + quad * 2048;
-  uint32_t item = 0, on[2] = {0, 0};
+  uint8_t* stage = smem + L::STAGE + quad * 4096;
+  const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
+  uint32_t item = 0, on0 = 0, on1 = 0;
   bool ok = true;
-  Walk w;
-  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++item) {
-    const Item it = item_of(a, w);
-    const int steps = it.p.hi - it.p.lo, head = w.head * a.group + head_in;
-    float* part = a.part + static_cast<int64_t>(part_slot(w)) * a.part_rows * (a.dim + 2);
+  for (Item it; ok && next_item(a, b, smem, item, it); ++item) {
+    const int steps = it.hi - it.lo, head = it.head * a.group + head_in;
     const bool both = it.halves == 1;  // the two accumulators are of the same rows
+    const bool store = it.shares == 1 || it.direct;
+    float* part = a.part + it.slot * slot;
+    // the other part of a tile that is joined here, and whether it comes first
+    const bool ahead = it.slot & 1 ? false : true;
+    const float* other = a.part + tile_slot(it.from, ahead ? 0 : 1) * slot;
 #pragma unroll 1
-    for (int half = 0; half < it.halves; ++half) {
-      const Row r = row_of(a, w, it, half, dt);
+    for (int half = 0; ok && half < it.halves; ++half) {
+      const Row r = row_of(a, it, half, dt);
       const bool idle = __all_sync(0xffffffffu, r.limit == 0);
-      float ms[2] = {-INFINITY, -INFINITY}, ls[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // h: the accumulator
-        if (!both && h != half) continue;
-        if (ok) ok = wait_warp(a.watch, b.lfull + 8 * h, item & 1u, S_TFULL);
-        ms[h] = stats[h * 256 + row];
-        ls[h] = stats[h * 256 + 128 + row];
+      const int prow = half * BLK + row;
+      float m = -INFINITY, l = 0.0f, f0 = 1.0f, f1 = 0.0f;
+#pragma unroll 1
+      for (int h = half; ok && h < (both ? 2 : half + 1); ++h) {  // h: the accumulator
+        ok = wait_warp(a.watch, b.lfull + 8 * h, item & 1u, S_TFULL);
+        const float mh = stats[h * 256 + row], lh = stats[h * 256 + 128 + row];
         __syncwarp();
         if (lane == 0) mbar_arrive(b.lfree + 8 * h);
-        if (!both || h < steps) {  // else it has no product
-          if (ok) ok = wait_warp(a.watch, b.ofull + 8 * h, on[h] & 1u, S_TFULL);
-          ++on[h];
+        if (ok && (!both || h < steps)) ok = wait_warp(a.watch, b.ofull + 8 * h, (h ? on1++ : on0++) & 1u, S_TFULL);
+        if (h == half) {
+          m = mh, l = lh;
+        } else {
+          const float top = fmaxf(m, mh);
+          f0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+          f1 = mh == -INFINITY ? 0.0f : exp2_fast(mh - top);
+          m = top, l = l * f0 + lh * f1;
         }
       }
+      if (!ok) break;
       tc_fence_after();
-      const float m = fmaxf(ms[0], ms[1]);
-      float f[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) f[h] = ms[h] == -INFINITY ? 0.0f : exp2_fast(ms[h] - m);
-      const float l = ls[0] * f[0] + ls[1] * f[1];
       const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L::BAD) + item % BAD_SETS * BAD_STEPS * 4;
-      uint32_t any_bad = 0;
-      if (ok && a.causal && lane < BAD_STEPS * 4) any_bad = bad[lane];
-      any_bad = __any_sync(0xffffffffu, any_bad != 0);
-      const int64_t q_row = static_cast<int64_t>(w.s.q0) + r.t;
-      const float scale = !it.p.whole ? 1.0f : l == 0.0f ? (r.limit > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / l;
-      const float f0 = f[both ? 0 : half] * scale, f1 = f[1] * scale;
-      const RowsOut to_rows = rows_out(r.valid && it.p.whole ? a.out + q_row * a.ldo + head * a.ho : nullptr);
+      const bool any_bad = __any_sync(0xffffffffu, a.causal && lane < BAD_STEPS * 4 && bad[lane] != 0);
+      const int64_t q_row = static_cast<int64_t>(it.s.q0) + r.t;
+      float w0 = 1.0f, w1 = 0.0f, sum = l, top = m;  // weights of this part and the other, all parts' sum and maximum
+      if (it.direct) {
+        const float pm = r.valid ? other[ml_at + prow] : -INFINITY, pl = r.valid ? other[ml_at + a.part_rows + prow] : 0.0f;
+        top = fmaxf(m, pm);
+        const float base = top == -INFINITY ? 0.0f : top;
+        w0 = exp2_fast(m - base), w1 = exp2_fast(pm - base);
+        sum = __fadd_rn(__fmul_rn(l, w0), __fmul_rn(pl, w1));  // as join_parts
+      }
+      if (store) {
+        const float inv = sum == 0.0f ? (r.limit > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / sum;
+        w0 *= inv, w1 *= inv;
+      }
+      if (!it.direct) f0 *= w0, f1 *= w0;
+      const void* to_row = r.valid && store ? a.out + q_row * a.ldo + head * a.ho : nullptr;
 #pragma unroll 1
-      for (int c = 0; ok && c < chunks; ++c) {
+      for (int c = 0; c < chunks; ++c) {  // 32 columns
+        uint32_t o[32];
         float v[32];
-        if (idle) {  // no product: the accumulator may hold anything
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-        } else {
-          uint32_t o[32];
+        for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+        if (!idle) {  // else no product: the accumulator may hold anything
           tmem_ld32_sync(to + half * BLK + c * 32, o);
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f0;
@@ -563,146 +556,183 @@ __device__ void store_role(const Args& a, const Tiles& tiles, const Shares& sh, 
             for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
           }
         }
-        if (any_bad)  // the noted values, for a row that sees their keys
-          for (int i = 0; i < BAD_STEPS * 4; ++i)
-            for (uint32_t left = bad[i]; left; left &= left - 1) {
-              const int key = it.some / BLK * BLK + 32 * i + __ffs(left) - 1;
-              if (key >= r.limit) continue;
-              const bf16* x = a.values + (static_cast<int64_t>(w.s.k0) + key) * a.ldv + w.head * a.hv + c * 32;
+        if (any_bad) {  // the noted values, for a row that sees their keys
+#pragma unroll 1
+          for (int i = 0; i < BAD_STEPS * 128; ++i) {
+            const int key = it.some / BLK * BLK + i;
+            if (!(bad[i >> 5] >> (i & 31) & 1u) || key >= r.limit) continue;
+            const bf16* x = a.values + (static_cast<int64_t>(it.s.k0) + key) * a.ldv + it.head * a.hv + c * 32;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float y = c * 32 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
-                if (!isfinite(y)) v[e] += y;
-              }
+            for (int e = 0; e < 32; ++e) {
+              const float y = c * 32 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
+              if (!isfinite(y)) v[e] += y;
             }
-        if (it.p.whole)
-          store_rows(stage, v, to_rows, c * 32, a.dim - c * 32);
-        else if (r.valid)
-          store_part(part, a.part_rows, half * BLK + row, v, c * 32, a.dim);
+          }
+        }
+        if (it.direct) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const int col = c * 32 + g * 4;
+            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r.valid && col < a.dim)
+              y = *reinterpret_cast<const float4*>(other + (static_cast<int64_t>(col >> 2) * a.part_rows + prow) * 4);
+            const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // the parts in their order
+              const float p0 = ahead ? z[e] : v[4 * g + e], p1 = ahead ? v[4 * g + e] : z[e];
+              v[4 * g + e] = fmaf(p1, ahead ? w0 : w1, __fmul_rn(p0, ahead ? w1 : w0));
+            }
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float z[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = v[8 * g + e];
+          if (store)
+            stage_row<64>(stage, 4 * (c & 1) + g, z);
+          else if (r.valid)
+            store_part(part, a.part_rows, prow, z, c * 32 + g * 8, a.dim);
+        }
+        if (store && ((c & 1) || c + 1 == chunks)) store_staged<64>(stage, to_row, (c & ~1) * 32, a.dim - (c & ~1) * 32);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(b.ofree + 8 * half);
-        if (both) mbar_arrive(b.ofree + 8);
+        if (both && steps > 1) mbar_arrive(b.ofree + 8);
       }
-      if (ok && r.valid) {
-        if (!it.p.whole) {
-          float* ml = part + static_cast<int64_t>(a.part_rows) * a.dim;
-          ml[half * BLK + row] = m;
-          ml[a.part_rows + half * BLK + row] = l;
+      if (r.valid) {
+        if (!store) {
+          part[ml_at + prow] = m;
+          part[ml_at + a.part_rows + prow] = l;
         } else if (a.lse) {
-          a.lse[q_row * a.heads + head] = r.limit > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+          a.lse[q_row * a.heads + head] = r.limit > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
         }
       }
     }
-    if (it.p.whole) continue;
-    // ---- a divided tile: whoever comes last joins its parts
-    __threadfence();
-    bar_store();
-    int from;
-    const int shares = tile_shares(sh, w, &from);
-    volatile int* last = reinterpret_cast<volatile int*>(smem + L::LAST);
-    if (me == 0) {
-      const uint32_t before = atomicAdd(a.arrivals + from, ok ? 1u : 0u);
-      *last = ok && before + 1 == static_cast<uint32_t>(shares);
-      if (*last) a.arrivals[from] = 0;
+    if (!ok) break;
+    if (!store) part_stored(reinterpret_cast<Pending*>(smem + L::PENDING), it, 4, a.arrivals);
+    if (it.direct && quad == 0 && lane == 0) a.arrivals[it.from] = 0;
+  }
+}
+
+// Joins the parts of a divided tile, in the order of the shares, by the whole
+// block.  As many rows at a time as their parts' weights find room in shared
+// memory: some lanes make a row's weights, as many as it has parts, then every
+// thread adds eight columns of a row, over a slice of the parts where there are
+// threads to spare.  (Slices go by the sizes alone, so the order does not depend
+// on which block joins.)
+template <int DP>
+__device__ __forceinline__ void join_parts(const Args& a, const Item& it, uint8_t* smem) {
+  using L = Layout<DP>;
+  const int me = threadIdx.x, shares = it.shares;
+  const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
+  auto place = [&](int r, int* tok, int* h) {  // of row r of the tile
+    const int in = r & (BLK - 1), dtok = in / a.group;
+    *tok = it.tok + (r >> 7) * a.tokens + dtok;
+    *h = it.head * a.group + in - dtok * a.group;
+    return dtok < a.tokens && *tok < it.s.nq;
+  };
+  const int left = it.s.nq - it.tok;
+  const int count = left <= a.tokens ? left * a.group : left < 2 * a.tokens ? BLK + (left - a.tokens) * a.group : 2 * BLK;
+  const int batch = min(count, JOIN / shares);
+  float* table = reinterpret_cast<float*>(smem + L::TABLE);
+  float* sums = reinterpret_cast<float*>(smem + L::SUMS);
+  int wide = 1;
+  while (wide < shares && wide < 32) wide *= 2;
+#pragma unroll 1
+  for (int r0 = 0; r0 < count; r0 += batch) {
+    const int rows_now = min(batch, count - r0);
+#pragma unroll 2
+    for (int i = me; i < rows_now * shares; i += THREADS) {
+      const int s = i / rows_now, r = i - s * rows_now;
+      const float* ml = a.part + tile_slot(it.from, s) * slot + ml_at + r0 + r;
+      table[r * shares + s] = ml[0];
+      table[JOIN + r * shares + s] = ml[a.part_rows];
     }
-    bar_store();
-    if (!*last) {
-      bar_store();
-      continue;
+    __syncthreads();
+    const int in = me & (wide - 1);
+#pragma unroll 1
+    for (int r0w = 0; r0w < rows_now; r0w += THREADS / wide) {
+      const int r = r0w + me / wide;
+      const bool mine = r < rows_now;
+      float* tm = table + (mine ? r : 0) * shares;
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+      for (int s = in; mine && s < shares; s += wide) top = fmaxf(top, tm[s]);
+#pragma unroll 1
+      for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll 1
+      for (int s = in; mine && s < shares; s += wide) sum += tm[JOIN + s] * exp2_fast(tm[s] - base);
+#pragma unroll 1
+      for (int o = wide / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      int tok, h;
+      const bool there = mine && place(r0 + r, &tok, &h);
+      const int lim = there ? keys_seen(it.s, tok, a.causal) : 0;
+      const float inv = sum == 0.0f ? (lim > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / sum;
+#pragma unroll 1
+      for (int s = in; mine && s < shares; s += wide) tm[s] = exp2_fast(tm[s] - base) * inv;
+      if (there && a.lse && in == 0)
+        a.lse[(static_cast<int64_t>(it.s.q0) + tok) * a.heads + h] = lim > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
     }
-    __threadfence();
-    const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), stats = static_cast<int64_t>(a.part_rows) * a.dim;
-    auto place = [&](int r, int* tok, int* h) {  // of row r of the tile
-      const int in = r & (BLK - 1), dtok = in / a.group;
-      *tok = it.tok + (r >> 7) * a.tokens + dtok;
-      *h = w.head * a.group + in - dtok * a.group;
-      return dtok < a.tokens && *tok < w.s.nq;
+    __syncthreads();
+    const int groups = rows_now * (a.dim / 8), slices = shares == 2 ? 1 : max(1, min(THREADS / groups, shares));
+    const int each = (shares + slices - 1) / slices;
+    auto put = [&](int i, const float(&v)[8]) {
+      const int g = i / rows_now, r = i - g * rows_now;
+      int tok, h;
+      if (place(r0 + r, &tok, &h))
+        *reinterpret_cast<uint4*>(a.out + (static_cast<int64_t>(it.s.q0) + tok) * a.ldo + h * a.ho + g * 8) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     };
-    // as many rows at a time as their parts' weights find room: a warp makes a row's weights, then every thread adds
-    // four columns of some rows
-    const int left = w.s.nq - it.tok;
-    const int count = left <= a.tokens ? left * a.group : left < 2 * a.tokens ? BLK + (left - a.tokens) * a.group : 2 * BLK;
-    const int batch = min(count, JOIN / shares);
-    float* table = reinterpret_cast<float*>(smem + L::JOIN_AT);
-    for (int r0 = 0; r0 < count; r0 += batch) {
-      const int rows_now = min(batch, count - r0);
-      for (int i = me; i < rows_now * shares; i += STORE) {
-        const int s = i / rows_now, r = i - s * rows_now;
-        const float* ml = a.part + tile_slot(from, s) * slot + stats + r0 + r;
-        table[r * shares + s] = ml[0];
-        table[JOIN + r * shares + s] = ml[a.part_rows];
-      }
-      bar_store();
-      // as many lanes a row as it has parts, up to a warp
-      int wide = 1;
-      while (wide < shares && wide < 32) wide *= 2;
-      const int in = me & (wide - 1);
 #pragma unroll 1
-      for (int r0w = 0; r0w < rows_now; r0w += STORE / wide) {
-        const int r = r0w + me / wide;
-        float* tm = table + min(r, rows_now - 1) * shares;
-        float top = -INFINITY, sum = 0.0f;
-        for (int s = in; s < shares; s += wide) top = fmaxf(top, tm[s]);
-        for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float base = top == -INFINITY ? 0.0f : top;
-        for (int s = in; s < shares; s += wide) sum += tm[JOIN + s] * exp2_fast(tm[s] - base);
-        for (int o = wide / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        int tok, h;
-        const bool there = r < rows_now && place(r0 + r, &tok, &h);
-        const int lim = there ? keys_seen(w.s, tok, a.causal) : 0;
-        const float inv = lim == 0 ? 0.0f : sum == 0.0f ? __uint_as_float(0x7fc00000u) : 1.0f / sum;
-        __syncwarp();  // rows past the last one read its entries
-        if (r < rows_now)
-          for (int s = in; s < shares; s += wide) tm[s] = exp2_fast(tm[s] - base) * inv;
-        if (there && a.lse && in == 0)
-          a.lse[(static_cast<int64_t>(w.s.q0) + tok) * a.heads + h] = lim > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
-      }
-      bar_store();
-      constexpr int U = 2;  // two groups of eight columns at a time
-      const int groups = rows_now * (a.dim / 8);
-      for (int i0 = me; i0 < groups; i0 += U * STORE) {
-        float4 v[U][2];
-        const float *src[U], *f[U];
+    for (int j = me; j < groups * slices; j += THREADS) {
+      const int slice = j / groups, i = j - slice * groups, g = i / rows_now, r = i - g * rows_now;
+      float v[8] = {};
+      const float* f = table + r * shares;
+      const float* src = a.part + (static_cast<int64_t>(2 * g) * a.part_rows + r0 + r) * 4;
+      const int end = min(shares, (slice + 1) * each);
+#pragma unroll 1
+      for (int s = slice * each; s < end; s += 8) {
+        float4 lo[8], hi[8];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = min(i0 + u * STORE, groups - 1), g = i / rows_now, r = i - g * rows_now;
-          v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          f[u] = table + r * shares;
-          src[u] = a.part + (static_cast<int64_t>(2 * g) * a.part_rows + r0 + r) * 4;
+        for (int u = 0; u < 8; ++u) {
+          const float* p = src + tile_slot(it.from, min(s + u, end - 1)) * slot;
+          lo[u] = *reinterpret_cast<const float4*>(p);
+          hi[u] = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(a.part_rows) * 4);
         }
-        auto add = [&](int s) {
-          const int64_t at = tile_slot(from, s) * slot;
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const float k = f[u][s];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 y = *reinterpret_cast<const float4*>(src[u] + at + static_cast<int64_t>(j) * a.part_rows * 4);
-              v[u][j].x += y.x * k, v[u][j].y += y.y * k, v[u][j].z += y.z * k, v[u][j].w += y.w * k;
-            }
-          }
-        };
-        int s = 0;
-#pragma unroll 1
-        for (; s + 4 <= shares; s += 4) add(s), add(s + 1), add(s + 2), add(s + 3);
-        if (s + 2 <= shares) add(s), add(s + 1), s += 2;
-        if (s < shares) add(s);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = i0 + u * STORE, g = i / rows_now, r = i - g * rows_now;
-          int tok, h;
-          if (i < groups && place(r0 + r, &tok, &h))
-            *reinterpret_cast<uint4*>(a.out + (static_cast<int64_t>(w.s.q0) + tok) * a.ldo + h * a.ho + g * 8) =
-                make_uint4(pack_bf16(v[u][0].x, v[u][0].y), pack_bf16(v[u][0].z, v[u][0].w),
-                           pack_bf16(v[u][1].x, v[u][1].y), pack_bf16(v[u][1].z, v[u][1].w));
+        for (int u = 0; u < 8; ++u) {
+          if (s + u >= end) break;
+          const float k = f[s + u];
+          v[0] = fmaf(lo[u].x, k, v[0]), v[1] = fmaf(lo[u].y, k, v[1]), v[2] = fmaf(lo[u].z, k, v[2]), v[3] = fmaf(lo[u].w, k, v[3]);
+          v[4] = fmaf(hi[u].x, k, v[4]), v[5] = fmaf(hi[u].y, k, v[5]), v[6] = fmaf(hi[u].z, k, v[6]), v[7] = fmaf(hi[u].w, k, v[7]);
         }
       }
-      bar_store();
+      if (slices == 1) {
+        put(i, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[j * 8 + e] = v[e];
+      }
     }
-    bar_store();
+    if (slices > 1) {
+      __syncthreads();
+#pragma unroll 1
+      for (int i = me; i < groups; i += THREADS) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = sums[i * 8 + e];
+#pragma unroll 1
+        for (int t = 1; t < slices; ++t)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += sums[(t * groups + i) * 8 + e];
+        put(i, v);
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -727,6 +757,7 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
     init(b.vfull, L::STAGES, 1);
     init(b.vempty, L::STAGES, 3);  // and the clearing warp
     init(b.vfix, L::STAGES, 1);
+    init(b.items, RING, 1);
     init(b.qfull, 1, 1);
     init(b.qempty, 1, 2);
     init(b.sfull, 2, 1);
@@ -736,6 +767,10 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
     init(b.lfull, 2, 4);
     init(b.lfree, 2, 4);
     init(b.drain, 2, 1);
+    st_shared_u32(sbase + L::SLOT + 4, 0u);
+    st_shared_u32(sbase + L::SLOT + 8, 0u);
+    Pending* p = reinterpret_cast<Pending*>(smem + L::PENDING);
+    p->due[0] = p->due[1] = p->warps[0] = p->warps[1] = 0;
     fence_barrier_init();
     tma_prefetch_map(&a.q);
     tma_prefetch_map(&a.k);
@@ -757,15 +792,21 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
   // registers: 128 a thread at launch, 65536 in all, shared out as the roles need them
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
-    if (warp == 0) load_role<DP>(a, tiles, sh, sbase);
-    if (warp == 1 || warp == 2) mma_role<DP>(a, tiles, sh, sbase, tmem, warp - 1);
-    if (warp == 3) fix_role<DP>(a, tiles, sh, sbase, smem);
+    if (warp == 0) load_role<DP>(a, tiles, sh, sbase, smem);
+    if (warp == 1 || warp == 2) mma_role<DP>(a, sbase, smem, tmem, warp - 1);
+    if (warp == 3) fix_role<DP>(a, sbase, smem);
+    __syncwarp();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;" : "+r"(sbase)::"memory");
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
-    softmax_role<DP>(a, tiles, sh, sbase, smem, tmem, (warp - 4) >> 2);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" : "+r"(sbase)::"memory");
+    softmax_role<DP>(a, sbase, smem, tmem, (warp - 4) >> 2);
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 128;" : "+r"(sbase)::"memory");
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
-    store_role<DP>(a, tiles, sh, sbase, smem, tmem);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" : "+r"(sbase)::"memory");
+    store_role<DP>(a, sbase, smem, tmem);
+    __syncwarp();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;" : "+r"(sbase)::"memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -773,6 +814,17 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
     tc_fence_after();
     tmem_dealloc_cg<1>(tmem, 512);
   }
+  // ---- tiles whose last part came from this block (the loads and products are done: their memory is free)
+  const Pending* pending = reinterpret_cast<const Pending*>(smem + L::PENDING);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i)
+    if (pending->due[i]) {
+      Item it;
+      static_cast<Entry&>(it) = pending->tile[i];
+      derive(a, it);
+      __threadfence();
+      join_parts<DP>(a, it, smem);
+    }
 }
 
 int64_t part_rows(int64_t n, int64_t group) { return n <= BLK / group ? BLK : 2 * BLK; }
