@@ -43,6 +43,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int THREADS = 512;
+constexpr int JOINERS = 256;             // the softmax groups, at the end
 constexpr float GROWTH = 8.0f;           // of the maximum, in powers of two, before O is rescaled
 constexpr int JOIN = 2048;               // parts of rows whose weights are in shared memory at a time
 constexpr int BAD_SETS = 8, BAD_STEPS = 3;  // steps of a tile that only some of its rows see whole
@@ -81,7 +82,7 @@ struct Layout {
   static constexpr int TILE = BLK * DP * 2;          // 128 rows of a head
   static constexpr int STAGES = DP == 128 ? 2 : 4;   // of K, and of V
   static constexpr int K0 = 2 * TILE, V0 = K0 + STAGES * TILE, BARS = V0 + STAGES * TILE;
-  static constexpr int N_BARS = 5 * STAGES + RING + 18;
+  static constexpr int N_BARS = 5 * STAGES + RING + 20;
   static constexpr int SLOT = BARS + 8 * N_BARS;     // the address of tensor memory, then the issuing warps' turns
   static constexpr int RING_AT = (SLOT + 16 + 15) / 16 * 16;
   static constexpr int BAD = RING_AT + RING * static_cast<int>(sizeof(Entry));  // [BAD_SETS][BAD_STEPS][4] keys, a bit each
@@ -90,7 +91,7 @@ struct Layout {
   static constexpr int STAGE = PENDING + (static_cast<int>(sizeof(Pending)) + 15) / 16 * 16;  // the storing warps' boxes
   static constexpr int PLAN = STAGE + 4 * 4096;
   static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
-  static constexpr int TABLE = 0, SUMS = 8 * JOIN;   // at the end, over the tiles: [2][JOIN] and [THREADS][8] floats
+  static constexpr int TABLE = 0, SUMS = 8 * JOIN;   // at the end, over the tiles: [2][JOIN] and [JOINERS][8] floats
   static_assert(SMEM <= 232448 && RING_AT % 16 == 0, "shared memory of one block");
 };
 
@@ -106,7 +107,7 @@ struct Bars {
     };
     constexpr int S = Layout<DP>::STAGES;
     kfull = next(S), kempty = next(S), vfull = next(S), vempty = next(S), vfix = next(S), items = next(RING);
-    qfull = next(1), qempty = next(1), sfull = next(2), pfull = next(4), ofull = next(2), ofree = next(2);
+    qfull = next(2), qempty = next(2), sfull = next(2), pfull = next(4), ofull = next(2), ofree = next(2);
     lfull = next(2), lfree = next(2), drain = next(2);
   }
 };
@@ -135,7 +136,7 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const bool lead = (threadIdx.x & 31) == 0;
-  uint32_t kn = 0, vn = 0, qn = 0;  // loads so far
+  uint32_t kn = 0, vn = 0, qn = 0, loaded = 0;  // loads so far; of Q by half
   bool ok = true;
   Walk w{};
   for (walk_begin(tiles, sh, w); ok; walk_next(tiles, a.seq, w)) {
@@ -143,36 +144,33 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
     static_cast<Entry&>(it) = put_item(sh, w, smem + L::RING_AT, b.items, qn, a.arrivals);
     if (it.hi <= it.lo) break;
     derive(a, it);
-    if (!(ok = wait_warp(a.watch, b.qempty, (qn & 1u) ^ 1u, S_EMPTY))) break;
-    if (lead) {
-      mbar_expect_tx(b.qfull, static_cast<uint32_t>(a.group * a.tokens) * 128u * (DP / 64) * it.halves);
-#pragma unroll 1
-      for (int h = 0; h < it.halves; ++h)
-        for (int d = 0; d < DP / 64; ++d)
-          tma_load_3d(sbase + h * L::TILE + d * 16384, &a.q, b.qfull, d * 64, it.head * a.group,
-                      it.s.q0 + it.tok + h * a.tokens);
-    }
-    __syncwarp();
-    ++qn;
-    // K one step ahead of V, as the products take them: K, K, V, K, V, .. V
-    const int loads = 2 * (it.hi - it.lo);
+    // K one step ahead of V, as the products take them: K, Q, Q, K, V, K, V, .. V.  Each half (or turn) has its own Q,
+    // which the next tile's replaces as soon as the half has made its last scores.
+    const int loads = 2 + 2 * (it.hi - it.lo);
 #pragma unroll 1
     for (int i = 0; ok && i < loads; ++i) {
-      const bool v = i == loads - 1 || (i > 1 && !(i & 1));
-      const int j = it.lo + (v ? (i - 1) >> 1 : (i + 1) >> 1);
-      const uint32_t n = v ? vn : kn, st = n % L::STAGES, full = (v ? b.vfull : b.kfull) + 8 * st;
-      if (!(ok = wait_warp(a.watch, (v ? b.vempty : b.kempty) + 8 * st, (n / L::STAGES & 1u) ^ 1u, S_EMPTY))) break;
+      const bool q = i == 1 || i == 2, v = !q && i > 0 && (i == loads - 1 || !(i & 1));
+      const uint32_t n = q ? qn : v ? vn : kn, ring = q ? 1u : static_cast<uint32_t>(L::STAGES), st = n % ring;
+      const uint32_t full = q ? b.qfull + 8 * (i - 1) : (v ? b.vfull : b.kfull) + 8 * st;
+      const uint32_t empty = q ? b.qempty + 8 * (i - 1) : (v ? b.vempty : b.kempty) + 8 * st;
+      if (!(ok = wait_warp(a.watch, empty, (n / ring & 1u) ^ 1u, S_EMPTY))) break;
       if (lead) {
-        mbar_expect_tx(full, L::TILE);
+        const CUtensorMap* map = q ? &a.q : v ? &a.v : &a.k;
+        const uint32_t to = sbase + (q ? (i - 1) * L::TILE : (v ? L::V0 : L::K0) + st * L::TILE);
+        const int j = it.lo + (i == 0 ? 0 : v ? (i - 3) >> 1 : (i - 1) >> 1);
+        const int row = q ? it.s.q0 + it.tok + (it.halves == 2 ? i - 1 : 0) * a.tokens : it.s.k0 + j * BLK;
+        mbar_expect_tx(full, q ? static_cast<uint32_t>(a.group * a.tokens) * 128u * (DP / 64) : L::TILE);
         for (int d = 0; d < DP / 64; ++d)
-          tma_load_3d(sbase + (v ? L::V0 : L::K0) + st * L::TILE + d * 16384, v ? &a.v : &a.k, full, d * 64, it.head,
-                      it.s.k0 + j * BLK);
+          tma_load_3d(to + d * 16384, map, full, d * 64, q ? it.head * a.group : it.head, row);
       }
       __syncwarp();
-      if (v)
+      if (q)
+        qn += i - 1;  // both are of the same tile
+      else if (v)
         ++vn;
       else
         ++kn;
+      loaded += i == 1 ? 1u : i == 2 ? 0x10000u : 0u;
     }
   }
   if (!ok && lead) {  // what is in flight must land before the block gives up its shared memory
@@ -182,7 +180,8 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
 #pragma unroll 1
     for (uint32_t j = vn > L::STAGES ? vn - L::STAGES : 0u; j < vn; ++j)
       wait_bar(a.watch, b.vfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
-    if (qn) wait_bar(a.watch, b.qfull, (qn - 1) & 1u, S_DRAIN, false);
+    if (loaded & 0xffffu) wait_bar(a.watch, b.qfull, (loaded - 1) & 1u, S_DRAIN, false);
+    if (loaded >> 16) wait_bar(a.watch, b.qfull + 8, (loaded >> 16) - 1 & 1u, S_DRAIN, false);
   }
   __syncwarp();
 }
@@ -208,8 +207,8 @@ __device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t 
   for (Item it; ok && next_item(a, b, smem, qn, it); ++qn) {
     const int steps = it.hi - it.lo;
     const bool two = it.halves == 2;
-    const uint64_t dq = smem_desc_sw128(sbase + (two ? half * L::TILE : 0));
-    await(b.qfull, qn);
+    const uint64_t dq = smem_desc_sw128(sbase + half * L::TILE);
+    await(b.qfull + 8 * half, qn);
     // The next scores: of step i, if it is this warp's.  With one half the other turn's are only released.
     auto scores = [&](int i) {
       const uint32_t st = kn % L::STAGES;
@@ -234,7 +233,7 @@ __device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t 
     while (k < steps && k <= (two ? 0 : half)) {
       scores(k);
       free_k(k);
-      if (++k == steps && ok) mma_commit_cg<1>(b.qempty);
+      if (++k == steps && ok) mma_commit_cg<1>(b.qempty + 8 * half);
     }
     // the accumulator is free once the last part that used it has been stored
     if (two || half < steps) {
@@ -290,7 +289,7 @@ __device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t 
       if (k < steps) {
         if (!two) scores(k);
         free_k(k);
-        if (++k == steps && ok) mma_commit_cg<1>(b.qempty);
+        if (++k == steps && ok) mma_commit_cg<1>(b.qempty + 8 * half);
       }
     }
   }
@@ -485,7 +484,7 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
   const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * BLK;
   const int dt = row / a.group, head_in = row - dt * a.group;  // the row's token in its half, its head in the group
-  const int chunks = (a.dim + 31) / 32;
+  const int chunks = (a.dim + 63) / 64;
   const float* stats = reinterpret_cast<const float*>(smem + L::ROWS);
   uint8_t* stage = smem + L::STAGE + quad * 4096;
   const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
@@ -540,20 +539,56 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
       }
       if (!it.direct) f0 *= w0, f1 *= w0;
       const void* to_row = r.valid && store ? a.out + q_row * a.ldo + head * a.ho : nullptr;
+      if (it.shares == 1 && !both && !any_bad) {  // most tiles: in few instructions
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {  // 32 columns
-        uint32_t o[32];
-        float v[32];
+        for (int c = 0; c < a.dim; c += 16) {
+          uint32_t o[16];
+          float z[16];
+          tmem_ld16_sync(to + half * BLK + c, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-        if (!idle) {  // else no product: the accumulator may hold anything
-          tmem_ld32_sync(to + half * BLK + c * 32, o);
+          for (int e = 0; e < 16; ++e) z[e] = idle ? 0.0f : __uint_as_float(o[e]) * f0;
+          *reinterpret_cast<uint4*>(stage + stage_at<64>(lane, (c >> 3) & 7)) = make_uint4(
+              pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+          *reinterpret_cast<uint4*>(stage + stage_at<64>(lane, ((c >> 3) & 7) + 1)) = make_uint4(
+              pack_bf16(z[8], z[9]), pack_bf16(z[10], z[11]), pack_bf16(z[12], z[13]), pack_bf16(z[14], z[15]));
+          if (c + 16 >= a.dim) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b.ofree + 8 * half);
+          }
+          if ((c & 48) == 48 || c + 16 >= a.dim) store_staged<64>(stage, to_row, c & ~63, a.dim - (c & ~63));
+        }
+        if (r.valid && a.lse) a.lse[q_row * a.heads + head] = r.limit > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        continue;
+      }
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {  // 64 columns
+        uint32_t o[64];
+        if (idle) {  // no product: the accumulator may hold anything
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f0;
+          for (int e = 0; e < 64; ++e) o[e] = 0u;
+        } else {
+          tmem_ld64_sync(to + half * BLK + c * 64, o);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
           if (both && steps > 1) {
-            tmem_ld32_sync(to + BLK + c * 32, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
+            for (int g = 0; g < 4; ++g) {
+              uint32_t x[16];
+              tmem_ld16_sync(to + BLK + c * 64 + g * 16, x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[16 * g + e] = __float_as_uint(fmaf(__uint_as_float(x[e]), f1, __uint_as_float(o[16 * g + e])));
+            }
+          }
+        }
+        auto v = [&](int e) { return __uint_as_float(o[e]); };
+        if (c + 1 == chunks) {  // the accumulator is read: the next tile's products may begin
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(b.ofree + 8 * half);
+            if (both && steps > 1) mbar_arrive(b.ofree + 8);
           }
         }
         if (any_bad) {  // the noted values, for a row that sees their keys
@@ -561,46 +596,40 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
           for (int i = 0; i < BAD_STEPS * 128; ++i) {
             const int key = it.some / BLK * BLK + i;
             if (!(bad[i >> 5] >> (i & 31) & 1u) || key >= r.limit) continue;
-            const bf16* x = a.values + (static_cast<int64_t>(it.s.k0) + key) * a.ldv + it.head * a.hv + c * 32;
+            const bf16* x = a.values + (static_cast<int64_t>(it.s.k0) + key) * a.ldv + it.head * a.hv + c * 64;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = c * 32 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
-              if (!isfinite(y)) v[e] += y;
+            for (int e = 0; e < 64; ++e) {
+              const float y = c * 64 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
+              if (!isfinite(y)) o[e] = __float_as_uint(v(e) + y);
             }
           }
         }
         if (it.direct) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const int col = c * 32 + g * 4;
+          for (int g = 0; g < 16; ++g) {
+            const int col = c * 64 + g * 4;
             float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (r.valid && col < a.dim)
               y = *reinterpret_cast<const float4*>(other + (static_cast<int64_t>(col >> 2) * a.part_rows + prow) * 4);
             const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {  // the parts in their order
-              const float p0 = ahead ? z[e] : v[4 * g + e], p1 = ahead ? v[4 * g + e] : z[e];
-              v[4 * g + e] = fmaf(p1, ahead ? w0 : w1, __fmul_rn(p0, ahead ? w1 : w0));
+              const float p0 = ahead ? z[e] : v(4 * g + e), p1 = ahead ? v(4 * g + e) : z[e];
+              o[4 * g + e] = __float_as_uint(fmaf(p1, ahead ? w0 : w1, __fmul_rn(p0, ahead ? w1 : w0)));
             }
           }
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 8; ++g) {
           float z[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = v[8 * g + e];
+          for (int e = 0; e < 8; ++e) z[e] = v(8 * g + e);
           if (store)
-            stage_row<64>(stage, 4 * (c & 1) + g, z);
+            stage_row<64>(stage, g, z);
           else if (r.valid)
-            store_part(part, a.part_rows, prow, z, c * 32 + g * 8, a.dim);
+            store_part(part, a.part_rows, prow, z, c * 64 + g * 8, a.dim);
         }
-        if (store && ((c & 1) || c + 1 == chunks)) store_staged<64>(stage, to_row, (c & ~1) * 32, a.dim - (c & ~1) * 32);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(b.ofree + 8 * half);
-        if (both && steps > 1) mbar_arrive(b.ofree + 8);
+        if (store) store_staged<64>(stage, to_row, c * 64, a.dim - c * 64);
       }
       if (r.valid) {
         if (!store) {
@@ -617,8 +646,11 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
   }
 }
 
-// Joins the parts of a divided tile, in the order of the shares, by the whole
-// block.  As many rows at a time as their parts' weights find room in shared
+__device__ __forceinline__ void bar_all() { asm volatile("bar.sync 0, %0;" ::"n"(THREADS) : "memory"); }
+__device__ __forceinline__ void bar_join() { asm volatile("bar.sync 1, %0;" ::"n"(JOINERS) : "memory"); }
+
+// Joins the parts of a divided tile, in the order of the shares, by the softmax
+// groups.  As many rows at a time as their parts' weights find room in shared
 // memory: some lanes make a row's weights, as many as it has parts, then every
 // thread adds eight columns of a row, over a slice of the parts where there are
 // threads to spare.  (Slices go by the sizes alone, so the order does not depend
@@ -626,7 +658,7 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
 template <int DP>
 __device__ __forceinline__ void join_parts(const Args& a, const Item& it, uint8_t* smem) {
   using L = Layout<DP>;
-  const int me = threadIdx.x, shares = it.shares;
+  const int me = threadIdx.x - 128, shares = it.shares;
   const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
   auto place = [&](int r, int* tok, int* h) {  // of row r of the tile
     const int in = r & (BLK - 1), dtok = in / a.group;
@@ -645,16 +677,16 @@ __device__ __forceinline__ void join_parts(const Args& a, const Item& it, uint8_
   for (int r0 = 0; r0 < count; r0 += batch) {
     const int rows_now = min(batch, count - r0);
 #pragma unroll 2
-    for (int i = me; i < rows_now * shares; i += THREADS) {
+    for (int i = me; i < rows_now * shares; i += JOINERS) {
       const int s = i / rows_now, r = i - s * rows_now;
       const float* ml = a.part + tile_slot(it.from, s) * slot + ml_at + r0 + r;
       table[r * shares + s] = ml[0];
       table[JOIN + r * shares + s] = ml[a.part_rows];
     }
-    __syncthreads();
+    bar_join();
     const int in = me & (wide - 1);
 #pragma unroll 1
-    for (int r0w = 0; r0w < rows_now; r0w += THREADS / wide) {
+    for (int r0w = 0; r0w < rows_now; r0w += JOINERS / wide) {
       const int r = r0w + me / wide;
       const bool mine = r < rows_now;
       float* tm = table + (mine ? r : 0) * shares;
@@ -677,8 +709,8 @@ __device__ __forceinline__ void join_parts(const Args& a, const Item& it, uint8_
       if (there && a.lse && in == 0)
         a.lse[(static_cast<int64_t>(it.s.q0) + tok) * a.heads + h] = lim > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
     }
-    __syncthreads();
-    const int groups = rows_now * (a.dim / 8), slices = shares == 2 ? 1 : max(1, min(THREADS / groups, shares));
+    bar_join();
+    const int groups = rows_now * (a.dim / 8), slices = shares == 2 ? 1 : max(1, min(JOINERS / groups, shares));
     const int each = (shares + slices - 1) / slices;
     auto put = [&](int i, const float(&v)[8]) {
       const int g = i / rows_now, r = i - g * rows_now;
@@ -688,7 +720,7 @@ __device__ __forceinline__ void join_parts(const Args& a, const Item& it, uint8_
             make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     };
 #pragma unroll 1
-    for (int j = me; j < groups * slices; j += THREADS) {
+    for (int j = me; j < groups * slices; j += JOINERS) {
       const int slice = j / groups, i = j - slice * groups, g = i / rows_now, r = i - g * rows_now;
       float v[8] = {};
       const float* f = table + r * shares;
@@ -719,9 +751,9 @@ __device__ __forceinline__ void join_parts(const Args& a, const Item& it, uint8_
       }
     }
     if (slices > 1) {
-      __syncthreads();
+      bar_join();
 #pragma unroll 1
-      for (int i = me; i < groups; i += THREADS) {
+      for (int i = me; i < groups; i += JOINERS) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = sums[i * 8 + e];
@@ -732,7 +764,7 @@ __device__ __forceinline__ void join_parts(const Args& a, const Item& it, uint8_
         put(i, v);
       }
     }
-    __syncthreads();
+    bar_join();
   }
 }
 
@@ -758,8 +790,7 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
     init(b.vempty, L::STAGES, 3);  // and the clearing warp
     init(b.vfix, L::STAGES, 1);
     init(b.items, RING, 1);
-    init(b.qfull, 1, 1);
-    init(b.qempty, 1, 2);
+    init(b.qfull, 4, 1);           // and qempty
     init(b.sfull, 2, 1);
     init(b.pfull, 4, 4);           // a half's warps, 64 keys at a time
     init(b.ofull, 2, 1);
@@ -789,42 +820,44 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
   const Tiles tiles{a.kv_heads, a.tokens, a.causal};
   plan_shares<THREADS>(tiles, a.seq, plan);
   const Shares& sh = plan->shares;
-  // registers: 128 a thread at launch, 65536 in all, shared out as the roles need them
+  // Registers: 128 a thread at launch, 65536 in all, shared out once as the roles need them.  So the roles meet at a
+  // barrier of their own code, and what follows it is done by threads that have enough of them.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
     if (warp == 0) load_role<DP>(a, tiles, sh, sbase, smem);
     if (warp == 1 || warp == 2) mma_role<DP>(a, sbase, smem, tmem, warp - 1);
     if (warp == 3) fix_role<DP>(a, sbase, smem);
+    tc_fence_before();
     __syncwarp();
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;" : "+r"(sbase)::"memory");
+    bar_all();
+    if (warp == 1) {
+      tc_fence_after();
+      tmem_dealloc_cg<1>(tmem, 512);
+    }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" : "+r"(sbase)::"memory");
     softmax_role<DP>(a, sbase, smem, tmem, (warp - 4) >> 2);
+    tc_fence_before();
     __syncwarp();
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 128;" : "+r"(sbase)::"memory");
+    bar_all();
+    // tiles whose last part came from this block (the loads and products are done: their memory is free)
+    const Pending* pending = reinterpret_cast<const Pending*>(smem + L::PENDING);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+      if (pending->due[i]) {
+        Item it;
+        static_cast<Entry&>(it) = pending->tile[i];
+        derive(a, it);
+        __threadfence();
+        join_parts<DP>(a, it, smem);
+      }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" : "+r"(sbase)::"memory");
     store_role<DP>(a, sbase, smem, tmem);
+    tc_fence_before();
     __syncwarp();
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;" : "+r"(sbase)::"memory");
+    bar_all();
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc_cg<1>(tmem, 512);
-  }
-  // ---- tiles whose last part came from this block (the loads and products are done: their memory is free)
-  const Pending* pending = reinterpret_cast<const Pending*>(smem + L::PENDING);
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i)
-    if (pending->due[i]) {
-      Item it;
-      static_cast<Entry&>(it) = pending->tile[i];
-      derive(a, it);
-      __threadfence();
-      join_parts<DP>(a, it, smem);
-    }
 }
 
 int64_t part_rows(int64_t n, int64_t group) { return n <= BLK / group ? BLK : 2 * BLK; }
