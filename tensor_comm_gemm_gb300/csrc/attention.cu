@@ -169,7 +169,7 @@ tpo_status tpo_attention(tpo_block* b, int64_t batch, int64_t n, int64_t nk, int
   if (n == 0) return TPO_OK;
   a.heads = heads, a.kv_heads = kv_heads, a.dim = dim, a.causal = causal != 0, a.scale = scale;
   a.q = aq.get(), a.k = ak.get(), a.v = av.get(), a.out = ao.get(), a.lse = lse;
-  return launched(launch_attention(b->machine, a, b->watch(), b->arrivals(), b->ws(), static_cast<cudaStream_t>(stream)));
+  return launched(launch_attention(b->machine, a, b->watch(), b->ws(), static_cast<cudaStream_t>(stream)));
 }
 
 tpo_status tpo_attention_bwd(tpo_block* b, int64_t batch, int64_t n, int64_t nk, int64_t heads, int64_t kv_heads,

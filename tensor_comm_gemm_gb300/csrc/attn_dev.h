@@ -21,9 +21,8 @@ constexpr float kLog2e = 1.4426950408889634074f, kLn2 = 0.69314718055994530942f;
 // 128 at a time).  The lengths are known on the device only, and differ: so the
 // list is cut by steps into as many equal shares as there are blocks, wherever
 // the cuts fall.  A tile that a cut divides is computed in parts, in fp32, which
-// the block that arrives last at the tile's counter joins in the shares' order:
-// the same bits whoever comes last.  At most one tile begins and does not end
-// in a share, and that share's number is the tile's counter.
+// a second kernel joins in the shares' order.  At most one tile begins and does
+// not end in a share, so that the share's number is the tile's in that kernel.
 
 // A share's place in the list, tile by tile.
 struct Walk {
@@ -57,37 +56,48 @@ __device__ __forceinline__ int share_of(const Shares& p, int x) {
   return (in ? 0 : p.more) + static_cast<int>(static_cast<uint32_t>(in ? x : x - longer) / static_cast<uint32_t>(p.each + (in ? 1 : 0)));
 }
 
+constexpr int PLAN_SEQS = 512;  // sequences at a time, at most as many as the block's threads
+struct PlanScratch {
+  int steps[32], tiles[32];  // of a warp's sequences
+  int longer;                // sequences of more than one tile: their number, their lengths and then their steps
+  int nq[PLAN_SEQS], nk[PLAN_SEQS];
+  Shares shares;
+};
+
 // Steps of sequence i for one key head; every thread of the block calls it, with
-// its own i (at or past `batch`: none).  *s gets the sequence, *tiles the tiles' number.
-template <class T>
-__device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i, Seq* s, int* tiles) {
+// its own i (at or past `batch`: none).  *s gets the sequence, *tiles the tiles'
+// number.  A thread counts a single tile itself; those of longer sequences are
+// counted by a warp each.
+template <int THREADS, class T>
+__device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i, Seq* s, int* tiles, PlanScratch* sc) {
+  static_assert(THREADS <= PLAN_SEQS, "a place for each thread's sequence");
   *s = Seq{0, 0, 0, 0};
   if (i < q.batch) *s = sequence(q, i);
   const int n = i < q.batch ? t.tiles(*s) : 0;
-  int sum = 0;
-  // one tile by the thread itself, the tiles of longer sequences by the whole warp
-  int lo, hi;
+  int sum = 0, at = 0, lo, hi;
+  if (threadIdx.x == 0) sc->longer = 0;
+  __syncthreads();
   if (n == 1) t.range(*s, 0, &lo, &hi), sum = hi - lo;
+  if (n > 1) {
+    at = atomicAdd(&sc->longer, 1);
+    sc->nq[at] = s->nq, sc->nk[at] = s->nk;
+  }
+  __syncthreads();
 #pragma unroll 1
-  for (uint32_t many = __ballot_sync(0xffffffffu, n > 1); many; many &= many - 1) {
-    const int l = __ffs(many) - 1, count = __shfl_sync(0xffffffffu, n, l);
-    Seq o{0, 0, 0, 0};
-    o.nq = __shfl_sync(0xffffffffu, s->nq, l);
-    o.nk = __shfl_sync(0xffffffffu, s->nk, l);
+  for (int k = threadIdx.x >> 5; k < sc->longer; k += THREADS / 32) {
+    const Seq o{0, sc->nq[k], 0, sc->nk[k]};
+    const int count = t.tiles(o);
     int v = 0;
 #pragma unroll 1
-    for (int k = threadIdx.x & 31; k < count; k += 32) t.range(o, k, &lo, &hi), v += hi - lo;
+    for (int j = threadIdx.x & 31; j < count; j += 32) t.range(o, j, &lo, &hi), v += hi - lo;
     v = __reduce_add_sync(0xffffffffu, v);
-    if ((threadIdx.x & 31) == l) sum = v;
+    if ((threadIdx.x & 31) == 0) sc->nq[k] = v;
   }
+  __syncthreads();
+  if (n > 1) sum = sc->nq[at];
   *tiles = n;
   return sum;
 }
-
-struct PlanScratch {
-  int steps[32], tiles[32];  // of a warp's sequences
-  Shares shares;
-};
 
 // Cuts the list; every thread of the block takes part.  At least MIN_STEPS a
 // share, unless there are more tiles than such shares.
@@ -108,7 +118,7 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
       int all = 0;
       if (pass == 0 || q.batch > THREADS) {
         int n;
-        mine = cost_of(t, q, base + threadIdx.x, &s, &n);
+        mine = cost_of<THREADS>(t, q, base + threadIdx.x, &s, &n, sc);
         n = __reduce_add_sync(0xffffffffu, n);
         upto = mine;
 #pragma unroll
@@ -228,23 +238,25 @@ __device__ __forceinline__ int tile_slot(int first, int i) { return i == 0 ? 2 *
 // ------------------------------------------------------------------ waits
 
 // A converged warp's bounded wait, in few instructions: the kernels' roles share the instruction cache, and a kernel
-// that outgrows it runs at the speed of its misses (320 KB of code: a tile's stores took 8000 cycles instead of 3500).
+// that outgrows it runs at the speed of its misses (with 320 KB of code a tile's stores took 8000 cycles, with 130 KB
+// 4000).  So what a wait does when it has lasted long is one function.
+static __device__ __noinline__ bool waited_long(unsigned long long t0, unsigned long long limit_ns, uint32_t* err, uint32_t site) {
+  const bool late = gtime() - t0 > limit_ns;
+  const bool over = __any_sync(0xffffffffu, late || *reinterpret_cast<volatile uint32_t*>(err) != 0u);
+  if (over && late && (threadIdx.x & 31) == 0) give_up(err, site);
+  return over;
+}
 __device__ __forceinline__ bool wait_warp(const Watch& w, uint32_t bar, uint32_t parity, uint32_t site) {
-  uint32_t tries = 0;
-  unsigned long long t0 = 0;
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  const unsigned long long t0 = gtime();
 #pragma unroll 1
-  while (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
-    if ((++tries & 63u) != 0u) continue;
-    const unsigned long long now = gtime();
-    if (tries == 64u) t0 = now;
-    const bool late = now - t0 > w.limit_ns;
-    if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile uint32_t*>(w.err) != 0u)) {
-      if (late && (threadIdx.x & 31) == 0) give_up(w.err, site);
-      return false;
-    }
-  }
+  while (!__all_sync(0xffffffffu, mbar_test(bar, parity)))
+    if (waited_long(t0, w.limit_ns, w.err, site)) return false;
   return true;
 }
+
+// A value that the compiler must take as new here: it makes no copies of a loop for each of its values.
+__device__ __forceinline__ void anew(int& v) { asm volatile("" : "+r"(v)); }
 
 // ------------------------------------------------------------------ items
 //
@@ -257,34 +269,39 @@ struct Entry {
   int head, tile, lo, hi;  // the share's steps of the tile; none: the end
   int from, shares;        // the shares that have parts of it (1: it is whole)
   int slot;                // where a part goes
-  int direct;              // the other of two parts is there: join it as this one is stored
+  int begins;              // this share has the first of them
 };
 constexpr int RING = 8;
 static_assert(sizeof(Entry) == 48, "three 16-byte words");
 
-// By the loading warp: entry n of the ring; `w` has no more: the end.
+// By the loading warp: entry n of the ring; `w` has no more: the end.  begun: a place in the workspace for each share.
 __device__ __forceinline__ Entry put_item(const Shares& sh, const Walk& w, uint8_t* ring, uint32_t full, uint32_t n,
-                                          const uint32_t* arrivals) {
+                                          Entry* begun, bool* open) {
   Entry e;
   e.s = w.s, e.head = w.head, e.tile = w.tile;
-  e.lo = e.hi = 0, e.from = 0, e.shares = 1, e.slot = 0, e.direct = 0;
+  e.lo = e.hi = 0, e.from = 0, e.shares = 1, e.slot = 0, e.begins = 0;
   if (walk_has(w)) {
     const Part p = walk_part(w);
     e.lo = p.lo, e.hi = p.hi;
     if (!p.whole) {
       e.shares = tile_shares(sh, tile_begin(sh, w), w.hi - w.lo, &e.from);
       e.slot = part_slot(w);
-      if (e.shares == 2) e.direct = ld_acquire(arrivals + e.from) == 1u;
-      e.direct = __shfl_sync(0xffffffffu, e.direct, 0);
+      e.begins = w.off == 0;
     }
   }
   if ((threadIdx.x & 31) == 0) {
     int4* to = reinterpret_cast<int4*>(ring + n % RING * sizeof(Entry));
-    to[0] = make_int4(e.s.q0, e.s.nq, e.s.k0, e.s.nk);
-    to[1] = make_int4(e.head, e.tile, e.lo, e.hi);
-    to[2] = make_int4(e.from, e.shares, e.slot, e.direct);
+    const int4 x = make_int4(e.s.q0, e.s.nq, e.s.k0, e.s.nk), y = make_int4(e.head, e.tile, e.lo, e.hi),
+               z = make_int4(e.from, e.shares, e.slot, e.begins);
+    to[0] = x, to[1] = y, to[2] = z;
     mbar_arrive(full + 8 * (n % RING));
+    // for the kernel that joins: the tile that this share begins and does not end, or at its end that there is none
+    if (e.begins || (e.hi <= e.lo && !*open)) {
+      to = reinterpret_cast<int4*>(begun + blockIdx.x);
+      to[0] = x, to[1] = y, to[2] = z;
+    }
   }
+  *open |= e.begins != 0;
   __syncwarp();
   return e;
 }
@@ -295,29 +312,8 @@ __device__ __forceinline__ bool get_item(const Watch& w, const uint8_t* ring, ui
   const int4 a = from[0], b = from[1], c = from[2];
   e->s = {a.x, a.y, a.z, a.w};
   e->head = b.x, e->tile = b.y, e->lo = b.z, e->hi = b.w;
-  e->from = c.x, e->shares = c.y, e->slot = c.z, e->direct = c.w;
+  e->from = c.x, e->shares = c.y, e->slot = c.z, e->begins = c.w;
   return e->hi > e->lo;
-}
-
-// The storing warps of a block count themselves for each divided tile; the last of them counts the part, and if all of
-// the tile's are there, notes the tile for the end of the block, when all its threads join the parts.
-struct Pending {
-  Entry tile[2];  // the one that the share did not begin, and the one that it did
-  int due[2];
-  int warps[2];
-};
-__device__ __forceinline__ void part_stored(Pending* p, const Entry& e, int warps, uint32_t* arrivals) {
-  __threadfence();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0 && atomicAdd(&p->warps[e.slot & 1], 1) == warps - 1) {
-    __threadfence();
-    if (atomicAdd(arrivals + e.from, 1u) + 1 == static_cast<uint32_t>(e.shares)) {
-      arrivals[e.from] = 0;
-      p->tile[e.slot & 1] = e;
-      p->due[e.slot & 1] = 1;
-    }
-  }
-  __syncwarp();
 }
 
 // ------------------------------------------------------------------ matrix instructions
@@ -476,7 +472,7 @@ __device__ __forceinline__ void store_staged(const uint8_t* stage, const void* m
   constexpr int G = W / 8;  // lanes a row
   const int lane = threadIdx.x & 31, part = lane % G;
   __syncwarp();
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < G; ++i) {
     const int row = lane / G + 32 / G * i;
     const uint64_t to = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), row);

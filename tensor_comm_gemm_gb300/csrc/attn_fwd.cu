@@ -43,9 +43,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int THREADS = 512;
-constexpr int JOINERS = 256;             // the softmax groups, at the end
 constexpr float GROWTH = 8.0f;           // of the maximum, in powers of two, before O is rescaled
-constexpr int JOIN = 2048;               // parts of rows whose weights are in shared memory at a time
 constexpr int BAD_SETS = 8, BAD_STEPS = 3;  // steps of a tile that only some of its rows see whole
 
 struct Args {
@@ -59,9 +57,9 @@ struct Args {
   bf16* out;
   int64_t ldo, ho;
   float* lse;
-  float* part;
+  Entry* begun;                        // [MAX_SHARES]: the tile that a share begins and does not end
+  float* part;                         // its parts: two slots a share, [dim / 4][rows][4], then maxima and sums
   int part_rows;
-  uint32_t* arrivals;
   Watch watch;
 };
 
@@ -87,11 +85,9 @@ struct Layout {
   static constexpr int RING_AT = (SLOT + 16 + 15) / 16 * 16;
   static constexpr int BAD = RING_AT + RING * static_cast<int>(sizeof(Entry));  // [BAD_SETS][BAD_STEPS][4] keys, a bit each
   static constexpr int ROWS = BAD + BAD_SETS * BAD_STEPS * 16;  // [2][2][128] floats: maxima and sums
-  static constexpr int PENDING = ROWS + 2048;
-  static constexpr int STAGE = PENDING + (static_cast<int>(sizeof(Pending)) + 15) / 16 * 16;  // the storing warps' boxes
+  static constexpr int STAGE = ROWS + 2048;  // the storing warps' boxes
   static constexpr int PLAN = STAGE + 4 * 4096;
   static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
-  static constexpr int TABLE = 0, SUMS = 8 * JOIN;   // at the end, over the tiles: [2][JOIN] and [JOINERS][8] floats
   static_assert(SMEM <= 232448 && RING_AT % 16 == 0, "shared memory of one block");
 };
 
@@ -137,11 +133,11 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
   const Bars<DP> b(sbase);
   const bool lead = (threadIdx.x & 31) == 0;
   uint32_t kn = 0, vn = 0, qn = 0, loaded = 0;  // loads so far; of Q by half
-  bool ok = true;
+  bool ok = true, open = false;
   Walk w{};
   for (walk_begin(tiles, sh, w); ok; walk_next(tiles, a.seq, w)) {
     Item it;
-    static_cast<Entry&>(it) = put_item(sh, w, smem + L::RING_AT, b.items, qn, a.arrivals);
+    static_cast<Entry&>(it) = put_item(sh, w, smem + L::RING_AT, b.items, qn, a.begun, &open);
     if (it.hi <= it.lo) break;
     derive(a, it);
     // K one step ahead of V, as the products take them: K, Q, Q, K, V, K, V, .. V.  Each half (or turn) has its own Q,
@@ -206,7 +202,7 @@ __device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t 
   };
   for (Item it; ok && next_item(a, b, smem, qn, it); ++qn) {
     const int steps = it.hi - it.lo;
-    const bool two = it.halves == 2;
+    int two = it.halves - 1;
     const uint64_t dq = smem_desc_sw128(sbase + half * L::TILE);
     await(b.qfull + 8 * half, qn);
     // The next scores: of step i, if it is this warp's.  With one half the other turn's are only released.
@@ -231,6 +227,7 @@ __device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t 
     int k = 0;  // steps whose scores are made
 #pragma unroll 1
     while (k < steps && k <= (two ? 0 : half)) {
+      anew(two);
       scores(k);
       free_k(k);
       if (++k == steps && ok) mma_commit_cg<1>(b.qempty + 8 * half);
@@ -242,6 +239,7 @@ __device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t 
     }
 #pragma unroll 1
     for (int i = 0; ok && i < steps; ++i) {
+      anew(two);
       const uint32_t st = vn % L::STAGES;
       const bool mine = two || (i & 1) == half;
       await(b.vfull + 8 * st, vn / L::STAGES);
@@ -476,7 +474,7 @@ __device__ void softmax_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
   }
 }
 
-// Divides by the sums and stores.
+// Divides by the sums and stores; parts of divided tiles as they are, with their maxima and sums.
 template <int DP>
 __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem) {
   using L = Layout<DP>;
@@ -484,25 +482,19 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
   const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * BLK;
   const int dt = row / a.group, head_in = row - dt * a.group;  // the row's token in its half, its head in the group
-  const int chunks = (a.dim + 63) / 64;
   const float* stats = reinterpret_cast<const float*>(smem + L::ROWS);
   uint8_t* stage = smem + L::STAGE + quad * 4096;
-  const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
+  const int64_t ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
   uint32_t item = 0, on0 = 0, on1 = 0;
   bool ok = true;
   for (Item it; ok && next_item(a, b, smem, item, it); ++item) {
     const int steps = it.hi - it.lo, head = it.head * a.group + head_in;
     const bool both = it.halves == 1;  // the two accumulators are of the same rows
-    const bool store = it.shares == 1 || it.direct;
-    float* part = a.part + it.slot * slot;
-    // the other part of a tile that is joined here, and whether it comes first
-    const bool ahead = it.slot & 1 ? false : true;
-    const float* other = a.part + tile_slot(it.from, ahead ? 0 : 1) * slot;
+    const bool two = both && steps > 1, whole = it.shares == 1;
 #pragma unroll 1
     for (int half = 0; ok && half < it.halves; ++half) {
       const Row r = row_of(a, it, half, dt);
       const bool idle = __all_sync(0xffffffffu, r.limit == 0);
-      const int prow = half * BLK + row;
       float m = -INFINITY, l = 0.0f, f0 = 1.0f, f1 = 0.0f;
 #pragma unroll 1
       for (int h = half; ok && h < (both ? 2 : half + 1); ++h) {  // h: the accumulator
@@ -525,57 +517,32 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
       const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L::BAD) + item % BAD_SETS * BAD_STEPS * 4;
       const bool any_bad = __any_sync(0xffffffffu, a.causal && lane < BAD_STEPS * 4 && bad[lane] != 0);
       const int64_t q_row = static_cast<int64_t>(it.s.q0) + r.t;
-      float w0 = 1.0f, w1 = 0.0f, sum = l, top = m;  // weights of this part and the other, all parts' sum and maximum
-      if (it.direct) {
-        const float pm = r.valid ? other[ml_at + prow] : -INFINITY, pl = r.valid ? other[ml_at + a.part_rows + prow] : 0.0f;
-        top = fmaxf(m, pm);
-        const float base = top == -INFINITY ? 0.0f : top;
-        w0 = exp2_fast(m - base), w1 = exp2_fast(pm - base);
-        sum = __fadd_rn(__fmul_rn(l, w0), __fmul_rn(pl, w1));  // as join_parts
+      float* part = a.part + it.slot * (ml_at + 2 * a.part_rows) + (half * BLK + row) * 4;
+      if (whole) {
+        const float inv = l == 0.0f ? (r.limit > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / l;
+        f0 *= inv, f1 *= inv;
+        if (r.valid && a.lse) a.lse[q_row * a.heads + head] = r.limit > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+      } else if (r.valid) {
+        float* ml = part - 3 * (half * BLK + row) + ml_at;
+        ml[0] = m;
+        ml[a.part_rows] = l;
       }
-      if (store) {
-        const float inv = sum == 0.0f ? (r.limit > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / sum;
-        w0 *= inv, w1 *= inv;
-      }
-      if (!it.direct) f0 *= w0, f1 *= w0;
-      const void* to_row = r.valid && store ? a.out + q_row * a.ldo + head * a.ho : nullptr;
-      if (it.shares == 1 && !both && !any_bad) {  // most tiles: in few instructions
+      const void* to_row = r.valid ? a.out + q_row * a.ldo + head * a.ho : nullptr;
 #pragma unroll 1
-        for (int c = 0; c < a.dim; c += 16) {
-          uint32_t o[16];
-          float z[16];
-          tmem_ld16_sync(to + half * BLK + c, o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) z[e] = idle ? 0.0f : __uint_as_float(o[e]) * f0;
-          *reinterpret_cast<uint4*>(stage + stage_at<64>(lane, (c >> 3) & 7)) = make_uint4(
-              pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
-          *reinterpret_cast<uint4*>(stage + stage_at<64>(lane, ((c >> 3) & 7) + 1)) = make_uint4(
-              pack_bf16(z[8], z[9]), pack_bf16(z[10], z[11]), pack_bf16(z[12], z[13]), pack_bf16(z[14], z[15]));
-          if (c + 16 >= a.dim) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b.ofree + 8 * half);
-          }
-          if ((c & 48) == 48 || c + 16 >= a.dim) store_staged<64>(stage, to_row, c & ~63, a.dim - (c & ~63));
-        }
-        if (r.valid && a.lse) a.lse[q_row * a.heads + head] = r.limit > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
-        continue;
-      }
-#pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {  // 64 columns
+      for (int c = 0; c < a.dim; c += 64) {
         uint32_t o[64];
         if (idle) {  // no product: the accumulator may hold anything
 #pragma unroll
           for (int e = 0; e < 64; ++e) o[e] = 0u;
         } else {
-          tmem_ld64_sync(to + half * BLK + c * 64, o);
+          tmem_ld64_sync(to + half * BLK + c, o);
 #pragma unroll
           for (int e = 0; e < 64; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-          if (both && steps > 1) {
+          if (two) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               uint32_t x[16];
-              tmem_ld16_sync(to + BLK + c * 64 + g * 16, x);
+              tmem_ld16_sync(to + BLK + c + g * 16, x);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 o[16 * g + e] = __float_as_uint(fmaf(__uint_as_float(x[e]), f1, __uint_as_float(o[16 * g + e])));
@@ -583,12 +550,12 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
           }
         }
         auto v = [&](int e) { return __uint_as_float(o[e]); };
-        if (c + 1 == chunks) {  // the accumulator is read: the next tile's products may begin
+        if (c + 64 >= a.dim) {  // the accumulator is read: the next tile's products may begin
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(b.ofree + 8 * half);
-            if (both && steps > 1) mbar_arrive(b.ofree + 8);
+            if (two) mbar_arrive(b.ofree + 8);
           }
         }
         if (any_bad) {  // the noted values, for a row that sees their keys
@@ -596,175 +563,31 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
           for (int i = 0; i < BAD_STEPS * 128; ++i) {
             const int key = it.some / BLK * BLK + i;
             if (!(bad[i >> 5] >> (i & 31) & 1u) || key >= r.limit) continue;
-            const bf16* x = a.values + (static_cast<int64_t>(it.s.k0) + key) * a.ldv + it.head * a.hv + c * 64;
+            const bf16* x = a.values + (static_cast<int64_t>(it.s.k0) + key) * a.ldv + it.head * a.hv + c;
 #pragma unroll
             for (int e = 0; e < 64; ++e) {
-              const float y = c * 64 + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
+              const float y = c + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
               if (!isfinite(y)) o[e] = __float_as_uint(v(e) + y);
             }
           }
         }
-        if (it.direct) {
+        if (whole) {
 #pragma unroll
-          for (int g = 0; g < 16; ++g) {
-            const int col = c * 64 + g * 4;
-            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r.valid && col < a.dim)
-              y = *reinterpret_cast<const float4*>(other + (static_cast<int64_t>(col >> 2) * a.part_rows + prow) * 4);
-            const float z[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {  // the parts in their order
-              const float p0 = ahead ? z[e] : v(4 * g + e), p1 = ahead ? v(4 * g + e) : z[e];
-              o[4 * g + e] = __float_as_uint(fmaf(p1, ahead ? w0 : w1, __fmul_rn(p0, ahead ? w1 : w0)));
-            }
-          }
-        }
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float z[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = v(8 * g + e);
-          if (store)
+          for (int g = 0; g < 8; ++g) {
+            const float z[8] = {v(8 * g),     v(8 * g + 1), v(8 * g + 2), v(8 * g + 3),
+                                v(8 * g + 4), v(8 * g + 5), v(8 * g + 6), v(8 * g + 7)};
             stage_row<64>(stage, g, z);
-          else if (r.valid)
-            store_part(part, a.part_rows, prow, z, c * 64 + g * 8, a.dim);
-        }
-        if (store) store_staged<64>(stage, to_row, c * 64, a.dim - c * 64);
-      }
-      if (r.valid) {
-        if (!store) {
-          part[ml_at + prow] = m;
-          part[ml_at + a.part_rows + prow] = l;
-        } else if (a.lse) {
-          a.lse[q_row * a.heads + head] = r.limit > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
+          }
+          store_staged<64>(stage, to_row, c, a.dim - c);
+        } else if (r.valid) {
+#pragma unroll
+          for (int g = 0; g < 16; ++g)
+            if (c + 4 * g < a.dim)
+              *reinterpret_cast<float4*>(part + static_cast<int64_t>((c >> 2) + g) * a.part_rows * 4) =
+                  make_float4(v(4 * g), v(4 * g + 1), v(4 * g + 2), v(4 * g + 3));
         }
       }
     }
-    if (!ok) break;
-    if (!store) part_stored(reinterpret_cast<Pending*>(smem + L::PENDING), it, 4, a.arrivals);
-    if (it.direct && quad == 0 && lane == 0) a.arrivals[it.from] = 0;
-  }
-}
-
-__device__ __forceinline__ void bar_all() { asm volatile("bar.sync 0, %0;" ::"n"(THREADS) : "memory"); }
-__device__ __forceinline__ void bar_join() { asm volatile("bar.sync 1, %0;" ::"n"(JOINERS) : "memory"); }
-
-// Joins the parts of a divided tile, in the order of the shares, by the softmax
-// groups.  As many rows at a time as their parts' weights find room in shared
-// memory: some lanes make a row's weights, as many as it has parts, then every
-// thread adds eight columns of a row, over a slice of the parts where there are
-// threads to spare.  (Slices go by the sizes alone, so the order does not depend
-// on which block joins.)
-template <int DP>
-__device__ __forceinline__ void join_parts(const Args& a, const Item& it, uint8_t* smem) {
-  using L = Layout<DP>;
-  const int me = threadIdx.x - 128, shares = it.shares;
-  const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
-  auto place = [&](int r, int* tok, int* h) {  // of row r of the tile
-    const int in = r & (BLK - 1), dtok = in / a.group;
-    *tok = it.tok + (r >> 7) * a.tokens + dtok;
-    *h = it.head * a.group + in - dtok * a.group;
-    return dtok < a.tokens && *tok < it.s.nq;
-  };
-  const int left = it.s.nq - it.tok;
-  const int count = left <= a.tokens ? left * a.group : left < 2 * a.tokens ? BLK + (left - a.tokens) * a.group : 2 * BLK;
-  const int batch = min(count, JOIN / shares);
-  float* table = reinterpret_cast<float*>(smem + L::TABLE);
-  float* sums = reinterpret_cast<float*>(smem + L::SUMS);
-  int wide = 1;
-  while (wide < shares && wide < 32) wide *= 2;
-#pragma unroll 1
-  for (int r0 = 0; r0 < count; r0 += batch) {
-    const int rows_now = min(batch, count - r0);
-#pragma unroll 2
-    for (int i = me; i < rows_now * shares; i += JOINERS) {
-      const int s = i / rows_now, r = i - s * rows_now;
-      const float* ml = a.part + tile_slot(it.from, s) * slot + ml_at + r0 + r;
-      table[r * shares + s] = ml[0];
-      table[JOIN + r * shares + s] = ml[a.part_rows];
-    }
-    bar_join();
-    const int in = me & (wide - 1);
-#pragma unroll 1
-    for (int r0w = 0; r0w < rows_now; r0w += JOINERS / wide) {
-      const int r = r0w + me / wide;
-      const bool mine = r < rows_now;
-      float* tm = table + (mine ? r : 0) * shares;
-      float top = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-      for (int s = in; mine && s < shares; s += wide) top = fmaxf(top, tm[s]);
-#pragma unroll 1
-      for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll 1
-      for (int s = in; mine && s < shares; s += wide) sum += tm[JOIN + s] * exp2_fast(tm[s] - base);
-#pragma unroll 1
-      for (int o = wide / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      int tok, h;
-      const bool there = mine && place(r0 + r, &tok, &h);
-      const int lim = there ? keys_seen(it.s, tok, a.causal) : 0;
-      const float inv = sum == 0.0f ? (lim > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / sum;
-#pragma unroll 1
-      for (int s = in; mine && s < shares; s += wide) tm[s] = exp2_fast(tm[s] - base) * inv;
-      if (there && a.lse && in == 0)
-        a.lse[(static_cast<int64_t>(it.s.q0) + tok) * a.heads + h] = lim > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
-    }
-    bar_join();
-    const int groups = rows_now * (a.dim / 8), slices = shares == 2 ? 1 : max(1, min(JOINERS / groups, shares));
-    const int each = (shares + slices - 1) / slices;
-    auto put = [&](int i, const float(&v)[8]) {
-      const int g = i / rows_now, r = i - g * rows_now;
-      int tok, h;
-      if (place(r0 + r, &tok, &h))
-        *reinterpret_cast<uint4*>(a.out + (static_cast<int64_t>(it.s.q0) + tok) * a.ldo + h * a.ho + g * 8) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    };
-#pragma unroll 1
-    for (int j = me; j < groups * slices; j += JOINERS) {
-      const int slice = j / groups, i = j - slice * groups, g = i / rows_now, r = i - g * rows_now;
-      float v[8] = {};
-      const float* f = table + r * shares;
-      const float* src = a.part + (static_cast<int64_t>(2 * g) * a.part_rows + r0 + r) * 4;
-      const int end = min(shares, (slice + 1) * each);
-#pragma unroll 1
-      for (int s = slice * each; s < end; s += 8) {
-        float4 lo[8], hi[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float* p = src + tile_slot(it.from, min(s + u, end - 1)) * slot;
-          lo[u] = *reinterpret_cast<const float4*>(p);
-          hi[u] = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(a.part_rows) * 4);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (s + u >= end) break;
-          const float k = f[s + u];
-          v[0] = fmaf(lo[u].x, k, v[0]), v[1] = fmaf(lo[u].y, k, v[1]), v[2] = fmaf(lo[u].z, k, v[2]), v[3] = fmaf(lo[u].w, k, v[3]);
-          v[4] = fmaf(hi[u].x, k, v[4]), v[5] = fmaf(hi[u].y, k, v[5]), v[6] = fmaf(hi[u].z, k, v[6]), v[7] = fmaf(hi[u].w, k, v[7]);
-        }
-      }
-      if (slices == 1) {
-        put(i, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sums[j * 8 + e] = v[e];
-      }
-    }
-    if (slices > 1) {
-      bar_join();
-#pragma unroll 1
-      for (int i = me; i < groups; i += JOINERS) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = sums[i * 8 + e];
-#pragma unroll 1
-        for (int t = 1; t < slices; ++t)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += sums[(t * groups + i) * 8 + e];
-        put(i, v);
-      }
-    }
-    bar_join();
   }
 }
 
@@ -800,8 +623,6 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
     init(b.drain, 2, 1);
     st_shared_u32(sbase + L::SLOT + 4, 0u);
     st_shared_u32(sbase + L::SLOT + 8, 0u);
-    Pending* p = reinterpret_cast<Pending*>(smem + L::PENDING);
-    p->due[0] = p->due[1] = p->warps[0] = p->warps[1] = 0;
     fence_barrier_init();
     tma_prefetch_map(&a.q);
     tma_prefetch_map(&a.k);
@@ -820,46 +641,128 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
   const Tiles tiles{a.kv_heads, a.tokens, a.causal};
   plan_shares<THREADS>(tiles, a.seq, plan);
   const Shares& sh = plan->shares;
-  // Registers: 128 a thread at launch, 65536 in all, shared out once as the roles need them.  So the roles meet at a
-  // barrier of their own code, and what follows it is done by threads that have enough of them.
+  // registers: 128 a thread at launch, 65536 in all, shared out as the roles need them
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
     if (warp == 0) load_role<DP>(a, tiles, sh, sbase, smem);
     if (warp == 1 || warp == 2) mma_role<DP>(a, sbase, smem, tmem, warp - 1);
     if (warp == 3) fix_role<DP>(a, sbase, smem);
-    tc_fence_before();
-    __syncwarp();
-    bar_all();
-    if (warp == 1) {
-      tc_fence_after();
-      tmem_dealloc_cg<1>(tmem, 512);
-    }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" : "+r"(sbase)::"memory");
     softmax_role<DP>(a, sbase, smem, tmem, (warp - 4) >> 2);
-    tc_fence_before();
-    __syncwarp();
-    bar_all();
-    // tiles whose last part came from this block (the loads and products are done: their memory is free)
-    const Pending* pending = reinterpret_cast<const Pending*>(smem + L::PENDING);
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i)
-      if (pending->due[i]) {
-        Item it;
-        static_cast<Entry&>(it) = pending->tile[i];
-        derive(a, it);
-        __threadfence();
-        join_parts<DP>(a, it, smem);
-      }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" : "+r"(sbase)::"memory");
     store_role<DP>(a, sbase, smem, tmem);
-    tc_fence_before();
-    __syncwarp();
-    bar_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<1>(tmem, 512);
   }
 }
 
+// Joins the parts of the tile that share blockIdx.x began and did not end, in the
+// order of the shares; block y takes its rows y, y + ROW_BLOCKS, ...  A row at a
+// time: its weights by all threads, then eight columns a thread, over a slice of
+// the parts where there are more than a few.  With few parts 16 rows at a time.
+constexpr int JOIN_THREADS = 256, ROW_BLOCKS = 16;
+struct JoinArgs {
+  const Entry* begun;
+  const float* part;
+  int part_rows, heads, group, tokens, dim, causal;
+  bf16* out;
+  int64_t ldo, ho;
+  float* lse;
+  const uint32_t* err;
+};
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(JoinArgs a) {
+  __shared__ float weight[MAX_SHARES * 16];
+  __shared__ float sums[JOIN_THREADS][8];
+  grid_dep_launch();
+  grid_dep_wait();
+  const Entry e = a.begun[blockIdx.x];
+  if (*a.err != 0u || !e.begins || e.hi <= e.lo) return;  // after a failure the entries may be an earlier call's
+  const int me = threadIdx.x, shares = e.shares, columns = a.dim / 8;
+  const int tok0 = e.tile * 2 * a.tokens, left = e.s.nq - tok0;
+  const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
+  const int halves = left <= a.tokens ? 1 : 2;
+  // rows at a time, and slices of the parts, so that there is about a thread for each row's eight columns and slice
+  const int slices = shares <= 8 ? 1 : min(JOIN_THREADS / columns, (shares + 7) / 8), at_once = slices == 1 ? 16 : 1;
+  const int used = a.tokens * a.group;
+  for (int first = blockIdx.y * at_once; first < halves * BLK; first += ROW_BLOCKS * at_once) {
+    auto place = [&](int r, int64_t* q_row, int* h, int* limit) {  // of row r of the tile
+      const int in = r & (BLK - 1), dtok = in / a.group, t = tok0 + (r >> 7) * a.tokens + dtok;
+      *q_row = static_cast<int64_t>(e.s.q0) + t;
+      *h = e.head * a.group + in - dtok * a.group;
+      *limit = keys_seen(e.s, t, a.causal);
+      return in < used && t < e.s.nq;
+    };
+    int64_t q_row;
+    int h, limit;
+    if (at_once == 1 && !place(first, &q_row, &h, &limit)) continue;  // the same for all threads
+    // ---- the weights: sixteen lanes a row
+    const int wr = me >> 4, wl = me & 15;
+    if (wr < at_once) {
+      const float* ml = a.part + ml_at + first + wr;
+      float top = -INFINITY, sum = 0.0f;
+      for (int s = wl; s < shares; s += 16) top = fmaxf(top, ml[tile_slot(e.from, s) * slot]);
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffu << (me & 16), top, o));
+      const float base = top == -INFINITY ? 0.0f : top;
+      for (int s = wl; s < shares; s += 16) {
+        const float* p = ml + tile_slot(e.from, s) * slot;
+        const float f = exp2_fast(p[0] - base);
+        weight[wr * MAX_SHARES + s] = f;
+        sum += p[a.part_rows] * f;
+      }
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffu << (me & 16), sum, o);
+      const bool there = place(first + wr, &q_row, &h, &limit);
+      const float inv = sum == 0.0f ? (limit > 0 ? __uint_as_float(0x7fc00000u) : 0.0f) : 1.0f / sum;
+      for (int s = wl; s < shares; s += 16) weight[wr * MAX_SHARES + s] *= inv;
+      if (there && a.lse && wl == 0) a.lse[q_row * a.heads + h] = limit > 0 ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    }
+    __syncthreads();
+    // ---- the sums
+    const int r = at_once == 1 ? 0 : me & 15, c = at_once == 1 ? me % columns : me >> 4, slice = at_once == 1 ? me / columns : 0;
+    const bool mine = c < columns && slice < slices && place(first + r, &q_row, &h, &limit);
+    float v[8] = {};
+    if (mine) {
+      const int each = (shares + slices - 1) / slices, end = min(shares, (slice + 1) * each);
+      const float* src = a.part + (static_cast<int64_t>(2 * c) * a.part_rows + first + r) * 4;
+      const float* f = weight + r * MAX_SHARES;
+      for (int s = slice * each; s < end; s += 8) {
+        float4 lo[8], hi[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float* p = src + tile_slot(e.from, min(s + u, end - 1)) * slot;
+          lo[u] = *reinterpret_cast<const float4*>(p);
+          hi[u] = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(a.part_rows) * 4);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (s + u >= end) break;
+          const float k = f[s + u];
+          v[0] = fmaf(lo[u].x, k, v[0]), v[1] = fmaf(lo[u].y, k, v[1]), v[2] = fmaf(lo[u].z, k, v[2]), v[3] = fmaf(lo[u].w, k, v[3]);
+          v[4] = fmaf(hi[u].x, k, v[4]), v[5] = fmaf(hi[u].y, k, v[5]), v[6] = fmaf(hi[u].z, k, v[6]), v[7] = fmaf(hi[u].w, k, v[7]);
+        }
+      }
+    }
+    if (slices > 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sums[me][i] = v[i];
+      __syncthreads();
+      for (int t = 1; slice == 0 && mine && t < slices; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += sums[t * columns + me][i];
+    }
+    if (mine && slice == 0)
+      *reinterpret_cast<uint4*>(a.out + q_row * a.ldo + h * a.ho + c * 8) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    __syncthreads();
+  }
+}
+
+constexpr int64_t BEGUN_BYTES = (MAX_SHARES * static_cast<int64_t>(sizeof(Entry)) + 255) / 256 * 256;
 int64_t part_rows(int64_t n, int64_t group) { return n <= BLK / group ? BLK : 2 * BLK; }
 
 template <int DP>
@@ -877,11 +780,10 @@ cudaError_t configure_attention() {
 }
 
 int64_t need_attention(int64_t n, int64_t, int64_t heads, int64_t kv_heads, int64_t dim) {
-  return 2ll * MAX_SHARES * part_rows(n, heads / kv_heads) * (dim + 2) * 4;
+  return BEGUN_BYTES + 2ll * MAX_SHARES * part_rows(n, heads / kv_heads) * (dim + 2) * 4;
 }
 
-cudaError_t launch_attention(const Machine& mc, const AttnArgs& x, const Watch& w, uint32_t* arrivals, void* ws,
-                             cudaStream_t s) {
+cudaError_t launch_attention(const Machine& mc, const AttnArgs& x, const Watch& w, void* ws, cudaStream_t s) {
   Args a;
   std::memset(static_cast<void*>(&a), 0, sizeof(a));
   a.seq = x.seq;
@@ -890,7 +792,8 @@ cudaError_t launch_attention(const Machine& mc, const AttnArgs& x, const Watch& 
   a.dim = static_cast<int>(x.dim), a.causal = x.causal, a.c = x.scale * kLog2e;
   a.values = static_cast<const bf16*>(x.v.p), a.ldv = x.v.ld, a.hv = x.v.hs;
   a.out = static_cast<bf16*>(const_cast<void*>(x.out.p)), a.ldo = x.out.ld, a.ho = x.out.hs;
-  a.lse = x.lse, a.part = static_cast<float*>(ws), a.arrivals = arrivals, a.watch = w;
+  a.lse = x.lse, a.watch = w;
+  a.begun = static_cast<Entry*>(ws), a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + BEGUN_BYTES);
   a.part_rows = static_cast<int>(part_rows(x.seq.n, a.group));
   // without keys the loads go to the queries, which no row sees
   const bool keys = x.seq.nk > 0;
@@ -903,7 +806,10 @@ cudaError_t launch_attention(const Machine& mc, const AttnArgs& x, const Watch& 
   const int64_t tiles = (x.seq.n / (2 * a.tokens) + std::min(x.seq.batch, x.seq.n)) * x.kv_heads;
   const int64_t most = tiles * (x.seq.nk / BLK + 1);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(mc.sms, MAX_SHARES), most)));
-  return x.dim <= 64 ? launch_as<64>(a, grid, s) : launch_as<128>(a, grid, s);
+  const cudaError_t e = x.dim <= 64 ? launch_as<64>(a, grid, s) : launch_as<128>(a, grid, s);
+  if (e != cudaSuccess || x.seq.nk <= BLK) return e;  // tiles of one step are never divided
+  const JoinArgs j{a.begun, a.part, a.part_rows, a.heads, a.group, a.tokens, a.dim, a.causal, a.out, a.ldo, a.ho, a.lse, w.err};
+  return launch_pdl(join_kernel, dim3(static_cast<unsigned>(grid), ROW_BLOCKS), dim3(JOIN_THREADS), 0, s, j);
 }
 
 }  // namespace tpo
