@@ -198,7 +198,7 @@ tpo_status tpo_attention_bwd(tpo_block* b, int64_t batch, int64_t n, int64_t nk,
   a.q = aq.get(), a.k = ak.get(), a.v = av.get(), a.out = ao.get(), a.lse = const_cast<float*>(lse);
   a.dout = ado.get(), a.dq = adq.get(), a.dk = adk.get(), a.dv = adv.get();
   return launched(
-      launch_attention_bwd(b->machine, a, b->watch(), b->arrivals(), b->ws(), static_cast<cudaStream_t>(stream)));
+      launch_attention_bwd(b->machine, a, b->watch(), b->ws(), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -60,8 +60,7 @@ cudaError_t configure_attention();
 cudaError_t launch_attention(const Machine& mc, const AttnArgs& a, const Watch& w, void* ws, cudaStream_t s);
 int64_t need_attention(int64_t n, int64_t nk, int64_t heads, int64_t kv_heads, int64_t dim);
 cudaError_t configure_attention_bwd();
-cudaError_t launch_attention_bwd(const Machine& mc, const AttnArgs& a, const Watch& w, uint32_t* arrivals, void* ws,
-                                 cudaStream_t s);
+cudaError_t launch_attention_bwd(const Machine& mc, const AttnArgs& a, const Watch& w, void* ws, cudaStream_t s);
 int64_t need_attention_bwd(int64_t n, int64_t nk, int64_t heads, int64_t kv_heads, int64_t dim);
 
 struct RotaryArgs {

@@ -16,11 +16,14 @@
 // shared memory.  The products are ordered so that the tensor core has one to
 // work on while the threads are at the other half of a step.
 //
-// Roles: warp 0 loads (TMA), warp 1 issues the MMAs, warps 2 and 3 bring the
-// rows' statistics and clear rows that belong to no query (or key) of the
-// sequence, warps 4-7 and 8-11 compute, each group half of a step's columns.
+// Roles: warp 0 loads (TMA), warps 1 and 2 issue the MMAs (a wait or a commit
+// delays the warp that makes it by 60 to 130 cycles, and the tensor core takes few
+// instructions ahead of time), warp 3 brings the rows' statistics and clears rows
+// that belong to no query (or key) of the sequence, warps 4-7 and 8-11 compute,
+// each group half of a step's columns, and store.
 
 #include <algorithm>
+#include <climits>
 #include <cstring>
 
 #include <cuda_bf16.h>
@@ -34,7 +37,6 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int THREADS = 384;
-constexpr int COMPUTE = 256;  // threads of the two computing groups
 
 struct Args {
   CUtensorMap q, dout, k, v;
@@ -45,8 +47,8 @@ struct Args {
   const float2* stats;  // [n, heads]: -lse log2(e), -delta
   bf16 *out0, *out1;    // dv and dk, or dq
   int64_t ld0, h0, ld1, h1;
-  float* part;
-  uint32_t* arrivals;
+  Entry* begun;         // [MAX_SHARES]: the tile that a share begins and does not end
+  float* part;          // its parts, two slots a share: matrices [dim / 4][128][4]
   Watch watch;
 };
 
@@ -76,9 +78,10 @@ struct Layout {
   static constexpr int F1 = TILE, R0 = 2 * TILE, R1 = R0 + STAGES * TILE;  // the tile's two matrices, the rings
   static constexpr int STATS = R1 + STAGES * TILE;  // [stage][2][128]: -lse log2(e), -delta
   static constexpr int BARS = STATS + STAGES * 1024;
-  static constexpr int N_BARS = 6 * STAGES + 9;
-  static constexpr int SLOT = BARS + 8 * N_BARS, LAST = SLOT + 4;
-  static constexpr int STAGE = (SLOT + 8 + 15) / 16 * 16;  // a staging box for each computing warp
+  static constexpr int N_BARS = 6 * STAGES + RING + 11;
+  static constexpr int SLOT = BARS + 8 * N_BARS;
+  static constexpr int RING_AT = (SLOT + 8 + 15) / 16 * 16;
+  static constexpr int STAGE = RING_AT + RING * static_cast<int>(sizeof(Entry));  // a staging box for each computing warp
   static constexpr int PLAN = STAGE + 8 * 2048;
   static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
   static_assert(SMEM <= 232448, "shared memory of one block");
@@ -86,7 +89,7 @@ struct Layout {
 
 template <int DP>
 struct Bars {
-  uint32_t full0, full1, empty0, empty1, fix, free, ffull, fempty, sfull, pfull, dpfull, dsfull, accfull, drain;
+  uint32_t full0, full1, empty0, empty1, fix, free, items, ffull, fempty, sfull, pfull, dpfull, dsfull, accfull, drain;
   __device__ explicit Bars(uint32_t sbase) {
     uint32_t b = sbase + Layout<DP>::BARS;
     auto next = [&](int n) {
@@ -96,12 +99,11 @@ struct Bars {
     };
     constexpr int S = Layout<DP>::STAGES;
     full0 = next(S), full1 = next(S), empty0 = next(S), empty1 = next(S), fix = next(S), free = next(S);
-    ffull = next(1), fempty = next(1), sfull = next(2), pfull = next(1), dpfull = next(1), dsfull = next(1);
-    accfull = next(1), drain = next(1);
+    items = next(RING), ffull = next(1), fempty = next(1), sfull = next(2), pfull = next(2), dpfull = next(1);
+    dsfull = next(1), accfull = next(1), drain = next(2);
   }
 };
 
-__device__ __forceinline__ void bar_compute() { asm volatile("bar.sync 1, %0;" ::"n"(COMPUTE) : "memory"); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
@@ -112,129 +114,124 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 }
 
 template <int DP, bool KEYS>
-__device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& sh, uint32_t sbase) {
+__device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const bool lead = (threadIdx.x & 31) == 0;
   const uint32_t qbytes = static_cast<uint32_t>(a.group * a.tokens) * 128u * (DP / 64), kbytes = L::TILE;
-  const CUtensorMap *f0 = KEYS ? &a.k : &a.q, *f1 = KEYS ? &a.v : &a.dout, *r0 = KEYS ? &a.q : &a.k,
-                    *r1 = KEYS ? &a.dout : &a.v;
-  uint32_t n = 0, n1 = 0, fn = 0;  // loads so far
-  bool ok = true;
-  Walk w;
-  for (walk_begin(tiles, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w)) {
-    const Part p = walk_part(w);
-    const int qh = w.head * a.group, kh = w.head;
-    auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int head, int row) {
-      for (int d = 0; d < DP / 64; ++d) tma_load_3d(dst + d * 16384, map, bar, d * 64, head, row);
-    };
-    if (!(ok = wait_warp(a.watch, b.fempty, (fn & 1u) ^ 1u, S_EMPTY))) break;
-    if (lead) {
-      const int head = KEYS ? kh : qh, row = KEYS ? w.s.k0 + w.tile * BLK : w.s.q0 + w.tile * a.tokens;
-      mbar_expect_tx(b.ffull, 2 * (KEYS ? kbytes : qbytes));
-      load(sbase, f0, b.ffull, head, row);
-      load(sbase + L::F1, f1, b.ffull, head, row);
-    }
-    __syncwarp();
-    ++fn;
-    for (int j = p.lo; j < p.hi; ++j) {
-      const int head = KEYS ? qh : kh, row = KEYS ? w.s.q0 + j * a.tokens : w.s.k0 + j * BLK;
-      const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
-      if (!(ok = wait_warp(a.watch, b.empty0 + 8 * st, ph ^ 1u, S_EMPTY))) break;
+  uint32_t n0 = 0, n1 = 0, fn = 0, fixed = 0;  // loads so far
+  bool ok = true, open = false;
+  Walk w{};
+  for (walk_begin(tiles, sh, w); ok; walk_next(tiles, a.seq, w), ++fn) {
+    const Entry e = put_item(sh, w, smem + L::RING_AT, b.items, fn, a.begun, &open);
+    if (e.hi <= e.lo) break;
+    const int qh = e.head * a.group;
+    // the rings' first, the tile itself as soon as the one before it is done with, then the rings in turns
+    const int loads = 1 + 2 * (e.hi - e.lo);
+#pragma unroll 1
+    for (int i = 0; ok && i < loads; ++i) {
+      const bool tile = i == 1, second = i > 1 && !(i & 1);
+      const uint32_t n = tile ? fn : second ? n1 : n0, ring = tile ? 1u : static_cast<uint32_t>(L::STAGES), st = n % ring;
+      const uint32_t full = tile ? b.ffull : (second ? b.full1 : b.full0) + 8 * st;
+      const uint32_t empty = tile ? b.fempty : (second ? b.empty1 : b.empty0) + 8 * st;
+      if (!(ok = wait_warp(a.watch, empty, (n / ring & 1u) ^ 1u, S_EMPTY))) break;
       if (lead) {
-        mbar_expect_tx(b.full0 + 8 * st, KEYS ? qbytes : kbytes);
-        load(sbase + L::R0 + st * L::TILE, r0, b.full0 + 8 * st, head, row);
+        const bool queries = KEYS != tile;  // or keys
+        const int j = e.lo + (i == 0 ? 0 : second ? (i - 2) >> 1 : (i - 1) >> 1), at = tile ? e.tile : j;
+        const int row = queries ? e.s.q0 + at * a.tokens : e.s.k0 + at * BLK;
+        const uint32_t to = sbase + (tile ? 0u : (second ? L::R1 : L::R0) + st * L::TILE);
+        mbar_expect_tx(full, (queries ? qbytes : kbytes) * (tile ? 2u : 1u));
+#pragma unroll 1
+        for (int m = second ? 1 : 0; m < (tile || second ? 2 : 1); ++m)  // q or k, dout or v
+          for (int d = 0; d < DP / 64; ++d)
+            tma_load_3d(to + (tile ? m * L::TILE : 0) + d * 16384, queries ? (m ? &a.dout : &a.q) : (m ? &a.v : &a.k), full,
+                        d * 64, queries ? qh : e.head, row);
       }
       __syncwarp();
-      ++n;
-      if (!(ok = wait_warp(a.watch, b.empty1 + 8 * st, ph ^ 1u, S_EMPTY))) break;
-      if (lead) {
-        mbar_expect_tx(b.full1 + 8 * st, KEYS ? qbytes : kbytes);
-        load(sbase + L::R1 + st * L::TILE, r1, b.full1 + 8 * st, head, row);
-      }
-      __syncwarp();
-      ++n1;
+      if (tile)
+        ++fixed;
+      else if (second)
+        ++n1;
+      else
+        ++n0;
     }
   }
   if (!ok && lead) {  // what is in flight must land before the block gives up its shared memory
-    for (uint32_t j = n > L::STAGES ? n - L::STAGES : 0u; j < n; ++j)
+#pragma unroll 1
+    for (uint32_t j = n0 > L::STAGES ? n0 - L::STAGES : 0u; j < n0; ++j)
       wait_bar(a.watch, b.full0 + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
+#pragma unroll 1
     for (uint32_t j = n1 > L::STAGES ? n1 - L::STAGES : 0u; j < n1; ++j)
       wait_bar(a.watch, b.full1 + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
-    if (fn) wait_bar(a.watch, b.ffull, (fn - 1) & 1u, S_DRAIN, false);
+    if (fixed) wait_bar(a.watch, b.ffull, (fixed - 1) & 1u, S_DRAIN, false);
   }
   __syncwarp();
 }
 
-// Tensor memory: KEYS S, dP, dV and dK; otherwise S of even steps, dP, dQ and S of odd steps.
+// Tensor memory: KEYS S, dP, dV and dK; otherwise S of even steps, dP, dQ and S of odd steps.  One warp issues S and what
+// overwrites it or is made of it (dV = P^T dO), the other dP and dK or dQ.
 template <int DP, bool KEYS>
-__device__ void mma_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& sh, uint32_t sbase, uint32_t tmem) {
+__device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, int second) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
-  const int ksteps = (a.dim + 15) / 16;
   const uint32_t idesc_s = idesc_n(make_idesc(false, BLK), BLK);
-  const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), ksteps * 16) | 1u << 16;
-  const uint64_t f0 = smem_desc_sw128(sbase), f1 = smem_desc_sw128(sbase + L::F1),
-                 r0 = smem_desc_sw128(sbase + L::R0), r1 = smem_desc_sw128(sbase + L::R1),
-                 t0 = desc_rows(sbase + L::R0), t1 = desc_rows(sbase + L::R1);
-  const uint32_t dp = tmem + BLK, acc0 = tmem + 2 * BLK, acc1 = tmem + 3 * BLK;
+  const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), (a.dim + 15) / 16 * 16) | 1u << 16;
+  const uint64_t f = smem_desc_sw128(sbase + (second ? L::F1 : 0)), r = smem_desc_sw128(sbase + (second ? L::R1 : L::R0));
+  // dV and dK or dQ read rows of the other warp's ring
+  const uint64_t t = desc_rows(sbase + (second ? L::R0 : L::R1));
+  const uint32_t full = second ? b.full1 : b.full0, empty = second ? b.empty1 : b.empty0;
+  const uint32_t t_full = second ? b.full0 : b.full1, t_empty = second ? b.empty0 : b.empty1;
+  const uint32_t from = tmem + (second ? BLK : 0), acc = tmem + (KEYS && second ? 3 : 2) * BLK;
+  const uint32_t ready = second ? b.dsfull : b.pfull, made = second ? b.dpfull : b.sfull;
+  const bool adds = KEYS || second;
   uint32_t n = 0, fn = 0;  // steps and parts so far
   bool ok = true;
-  Walk w;
-  for (walk_begin(tiles, sh, w); ok && walk_has(w); walk_next(tiles, a.seq, w), ++fn) {
-    const Part p = walk_part(w);
-    const int steps = p.hi - p.lo;
-    auto stage = [&](uint32_t s) { return static_cast<uint64_t>(s % L::STAGES) * (L::TILE >> 4); };
-    // step s of the launch: S and dP from shared memory
+  auto await = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+    if (ok) ok = wait_warp(a.watch, bar, parity & 1u, site);
+  };
+  for (Entry e; ok && get_item(a.watch, smem + L::RING_AT, b.items, fn, &e); ++fn) {
+    const int steps = e.hi - e.lo;
+    // S or dP of step s of the launch, from shared memory
     auto scores = [&](uint32_t s) {
-      if (!wait_warp(a.watch, b.full0 + 8 * (s % L::STAGES), s / L::STAGES & 1u, S_FULL)) return false;
+      await(full + 8 * (s % L::STAGES), s / L::STAGES, S_FULL);
+      if (!KEYS && !second && s >= 2) await(b.pfull + 8 * (s & 1u), s / 2 - 1, S_TEMPTY);  // S of step s - 2 has been read
+      if (!ok) return;
       tc_fence_after();
-      const uint32_t d = KEYS || !(s & 1u) ? tmem : acc1;
-      mma_head<DP>(d, f0, r0 + stage(s), idesc_s);
-      mma_commit_cg<1>(b.sfull + 8 * (s & 1u));  // two: the threads may still be at the step before
-      return true;
+      mma_head<DP>(!KEYS && !second && (s & 1u) ? tmem + 3 * BLK : from, f, r + (s % L::STAGES) * (L::TILE >> 4), idesc_s);
+      mma_commit_cg<1>(made + (second ? 0u : 8 * (s & 1u)));
     };
-    auto dots = [&](uint32_t s) {
-      if (!wait_warp(a.watch, b.full1 + 8 * (s % L::STAGES), s / L::STAGES & 1u, S_FULL)) return false;
-      tc_fence_after();
-      mma_head<DP>(dp, f1, r1 + stage(s), idesc_s);
-      mma_commit_cg<1>(b.dpfull);
-      return true;
-    };
-    // an accumulator += bf16 columns at `from` (64 and 64 columns apart) . rows of a ring's stage
-    auto add = [&](uint32_t acc, uint32_t from, uint64_t rows, bool fresh) {
-      tc_fence_after();
-      mma4_ts(acc, from, rows, idesc_o, !fresh);
-      mma4_ts(acc, from + 64, rows + 512, idesc_o, 1u);
-    };
-    if (!(ok = wait_warp(a.watch, b.ffull, fn & 1u, S_FULL))) break;
-    ok = scores(n) && dots(n);
-    for (int i = 0; ok && i < steps; ++i, ++n) {
-      const uint32_t st = n % L::STAGES;
-      if constexpr (KEYS) {
-        if (!(ok = wait_warp(a.watch, b.pfull, n & 1u, S_TFULL))) break;
-        add(acc0, tmem, t1 + stage(n), i == 0);  // dV
-        mma_commit_cg<1>(b.empty1 + 8 * st);
-        if (i + 1 < steps && !(ok = scores(n + 1))) break;
-        if (!(ok = wait_warp(a.watch, b.dsfull, n & 1u, S_TFULL))) break;
-        add(acc1, dp, t0 + stage(n), i == 0);  // dK
-        mma_commit_cg<1>(b.empty0 + 8 * st);
-      } else {
-        if (i + 1 < steps && !(ok = scores(n + 1))) break;
-        if (!(ok = wait_warp(a.watch, b.dsfull, n & 1u, S_TFULL))) break;
-        mma_commit_cg<1>(b.empty1 + 8 * st);  // V: dP of this step is done
-        add(acc0, dp, t0 + stage(n), i == 0);  // dQ
-        mma_commit_cg<1>(b.empty0 + 8 * st);
+    await(b.ffull, fn, S_FULL);
+    scores(n);
+    if (!adds) {  // S alone
+#pragma unroll 1
+      for (int i = 0; ok && i < steps; ++i, ++n) {
+        if (i > 0) scores(n);
+        if (ok) mma_commit_cg<1>(empty + 8 * (n % L::STAGES));
       }
-      if (i + 1 < steps && !(ok = dots(n + 1))) break;
+    } else {
+#pragma unroll 1
+      for (int i = 0; ok && i < steps; ++i, ++n) {
+        const uint32_t st = n % L::STAGES;
+        if (!KEYS) mma_commit_cg<1>(empty + 8 * st);  // V is not read again
+        await(t_full + 8 * st, n / L::STAGES, S_FULL);
+        await(ready, n, S_TFULL);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t rows = t + st * (L::TILE >> 4);
+        mma4_ts(acc, from, rows, idesc_o, i > 0);
+        mma4_ts(acc, from + 64, rows + 512, idesc_o, 1u);
+        mma_commit_cg<1>(t_empty + 8 * st);
+        if (KEYS) mma_commit_cg<1>(empty + 8 * st);  // this step's S or dP is long done
+        if (i + 1 < steps) scores(n + 1);
+      }
     }
     if (!ok) break;
     mma_commit_cg<1>(b.fempty);
-    mma_commit_cg<1>(b.accfull);
+    if (adds) mma_commit_cg<1>(b.accfull);
   }
   // also after a failure: every MMA issued must complete before tensor memory is freed
-  mma_commit_cg<1>(b.drain);
-  if ((threadIdx.x & 31) == 0) wait_bar(a.watch, b.drain, 0u, S_DRAIN, false);
+  mma_commit_cg<1>(b.drain + 8 * second);
+  if ((threadIdx.x & 31) == 0) wait_bar(a.watch, b.drain + 8 * second, 0u, S_DRAIN, false);
   __syncwarp();
 }
 
@@ -242,39 +239,39 @@ __device__ void mma_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& 
 // no query or key of the sequence cleared, since they are operands of the products
 // with P and dS.
 template <int DP, bool KEYS>
-__device__ void aux_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem) {
+__device__ void aux_role(const Args& a, uint32_t sbase, uint8_t* smem) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
-  const int lane = threadIdx.x & 31, me = threadIdx.x - 64;
+  const int lane = threadIdx.x & 31;
   const int used = a.group * a.tokens;
-  uint32_t n = 0;
-  Walk w;
-  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w)) {
-    const Part p = walk_part(w);
-    for (int j = p.lo; j < p.hi; ++j, ++n) {
+  uint32_t n = 0, fn = 0;
+  for (Entry e; get_item(a.watch, smem + L::RING_AT, b.items, fn, &e); ++fn) {
+#pragma unroll 1
+    for (int j = e.lo; j < e.hi; ++j, ++n) {
       const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
-      const int left = KEYS ? min(a.tokens, w.s.nq - j * a.tokens) * a.group : w.s.nk - j * BLK;  // rows in use
+      const int left = KEYS ? min(a.tokens, e.s.nq - j * a.tokens) * a.group : e.s.nk - j * BLK;  // rows in use
       if constexpr (KEYS) {
         if (!wait_warp(a.watch, b.free + 8 * st, ph ^ 1u, S_EMPTY)) return;
         float* stats = reinterpret_cast<float*>(smem + L::STATS) + st * 256;
+        float2 v[4];
 #pragma unroll
-        for (int r = me; r < BLK; r += 64) {
-          float2 v = make_float2(-INFINITY, 0.0f);  // a weight of 0
-          if (r < left) {
-            const int tok = r / a.group;
-            v = a.stats[(static_cast<int64_t>(w.s.q0) + j * a.tokens + tok) * a.heads + w.head * a.group +
-                        (r - tok * a.group)];
-          }
-          stats[r] = v.x;
-          stats[BLK + r] = v.y;
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i, tok = r / a.group;
+          v[i] = make_float2(-INFINITY, 0.0f);  // a weight of 0
+          if (r < left)
+            v[i] = a.stats[(static_cast<int64_t>(e.s.q0) + j * a.tokens + tok) * a.heads + e.head * a.group +
+                           (r - tok * a.group)];
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) stats[lane + 32 * i] = v[i].x, stats[BLK + lane + 32 * i] = v[i].y;
       }
       if (!wait_warp(a.watch, b.full0 + 8 * st, ph, S_FULL)) return;
       if (KEYS && !wait_warp(a.watch, b.full1 + 8 * st, ph, S_FULL)) return;
       if (left < (KEYS ? used : BLK)) {
-        for (int r = me; r < BLK; r += 64) {
+#pragma unroll 1
+        for (int r = lane; r < BLK; r += 32) {
           if (r < left) continue;
-#pragma unroll
+#pragma unroll 1
           for (int d = 0; d < DP / 64; ++d)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -292,45 +289,48 @@ __device__ void aux_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& 
 }
 
 template <int DP, bool KEYS>
-__device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem,
-                             uint32_t tmem) {
+__device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, half = (warp - 4) >> 2;
-  const int row = quad * 32 + lane, me = threadIdx.x - 128;
+  const int row = quad * 32 + lane;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16), mine = lanes + half * 64;
   const int dt = row / a.group, head_in = row - dt * a.group;
   const int chunks = (a.dim + 31) / 32;
   const float2 c2 = make_float2(a.c, a.c);
   uint32_t n = 0, fn = 0;
   bool ok = true;
-  Walk w;
-  for (walk_begin(tiles, sh, w); walk_has(w); walk_next(tiles, a.seq, w), ++fn) {
-    const Part p = walk_part(w);
+  for (Entry e; ok && get_item(a.watch, smem + L::RING_AT, b.items, fn, &e); ++fn) {
     // KEYS: this row's key, and the first token that sees it; otherwise the row's query and the keys that it sees
-    const int tok = w.tile * a.tokens + dt;
-    const bool valid = KEYS ? w.tile * BLK + row < w.s.nk : dt < a.tokens && tok < w.s.nq;
-    const int seen = KEYS ? (a.causal ? w.tile * BLK + row - w.s.nk + w.s.nq : 0)
-                          : (valid ? keys_seen(w.s, tok, a.causal) : 0);
+    const int tok = e.tile * a.tokens + dt;
+    const bool valid = KEYS ? e.tile * BLK + row < e.s.nk : dt < a.tokens && tok < e.s.nq;
+    const int seen = KEYS ? (a.causal ? e.tile * BLK + row - e.s.nk + e.s.nq : 0)
+                          : (valid ? keys_seen(e.s, tok, a.causal) : INT_MAX);  // a row that is none may come to anything
     float2 nl = make_float2(0.0f, 0.0f), nd = nl;
     if (!KEYS && valid) {
-      const float2 v = a.stats[(static_cast<int64_t>(w.s.q0) + tok) * a.heads + w.head * a.group + head_in];
+      const float2 v = a.stats[(static_cast<int64_t>(e.s.q0) + tok) * a.heads + e.head * a.group + head_in];
       nl = make_float2(v.x, v.x), nd = make_float2(v.y, v.y);
     }
-    for (int j = p.lo; j < p.hi; ++j, ++n) {
+#pragma unroll 1
+    for (int j = e.lo; j < e.hi; ++j, ++n) {
       const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
       // columns [from, to) of the group's 64 that the row sees
       const int from = KEYS ? min(a.tokens, max(0, seen - j * a.tokens)) * a.group - half * 64 : 0;
-      const int to = (KEYS ? min(a.tokens, w.s.nq - j * a.tokens) * a.group : seen - j * BLK) - half * 64;
+      const int to = (KEYS ? min(a.tokens, e.s.nq - j * a.tokens) * a.group : seen - j * BLK) - half * 64;
       const bool all = __all_sync(0xffffffffu, from <= 0 && to >= 64);
       const float* stats = reinterpret_cast<const float*>(smem + L::STATS) + st * 256 + half * 64;
       float2 pr[32];
-      if (ok) ok = wait_warp(a.watch, b.sfull + 8 * (n & 1u), n >> 1 & 1u, S_TFULL);
-      if (KEYS && ok) ok = wait_warp(a.watch, b.fix + 8 * st, ph, S_FULL);
-      if (ok) {
+      if (!(ok = wait_warp(a.watch, b.sfull + 8 * (n & 1u), n >> 1 & 1u, S_TFULL))) break;
+      if (KEYS && !(ok = wait_warp(a.watch, b.fix + 8 * st, ph, S_FULL))) break;
+      {
         tc_fence_after();
         uint32_t x[64];
         tmem_ld64_sync(mine + (KEYS || !(n & 1u) ? 0 : 3 * BLK), x);
+        if (!KEYS) {  // S is read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b.pfull + 8 * (n & 1u));
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float2 l0 = nl, l1 = nl;
@@ -363,9 +363,9 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
         __syncwarp();
         if (lane == 0) mbar_arrive(b.pfull);
       }
-      if (ok) ok = wait_warp(a.watch, b.dpfull, n & 1u, S_TFULL);
-      if (!KEYS && ok) ok = wait_warp(a.watch, b.fix + 8 * st, ph, S_FULL);
-      if (ok) {
+      if (!(ok = wait_warp(a.watch, b.dpfull, n & 1u, S_TFULL))) break;
+      if (!KEYS && !(ok = wait_warp(a.watch, b.fix + 8 * st, ph, S_FULL))) break;
+      {
         tc_fence_after();
         uint32_t x[64], h[32];
         tmem_ld64_sync(mine + BLK, x);
@@ -397,102 +397,35 @@ __device__ void compute_role(const Args& a, const Tiles<KEYS>& tiles, const Shar
         mbar_arrive(b.free + 8 * st);
       }
     }
-    // ---- the end of the part: one group writes dV, the other dK; or each its chunks of dQ
-    if (ok) ok = wait_warp(a.watch, b.accfull, fn & 1u, S_TFULL);
+    // ---- the end of the part: one group writes dV, the other dK; or each its columns of dQ
+    if (!ok || !(ok = wait_warp(a.watch, b.accfull, fn & 1u, S_TFULL))) break;
     tc_fence_after();
-    const bool second = KEYS && half == 1;
+    const bool second = KEYS && half == 1, whole = e.shares == 1;
     const float scale = KEYS && !second ? 1.0f : a.scale;
     bf16* out = second ? a.out1 : a.out0;
     const int64_t ld = second ? a.ld1 : a.ld0, hs = second ? a.h1 : a.h0;
-    const int64_t out_row = KEYS ? static_cast<int64_t>(w.s.k0) + w.tile * BLK + row : static_cast<int64_t>(w.s.q0) + tok;
-    const int head = KEYS ? w.head : w.head * a.group + head_in;
-    const int64_t slot = static_cast<int64_t>(KEYS ? 2 : 1) * BLK * a.dim;
-    float* part = a.part + part_slot(w) * slot + static_cast<int64_t>(second ? BLK : 0) * a.dim;
+    const int64_t out_row = KEYS ? static_cast<int64_t>(e.s.k0) + e.tile * BLK + row : static_cast<int64_t>(e.s.q0) + tok;
+    const int head = KEYS ? e.head : e.head * a.group + head_in;
+    float* part = a.part + static_cast<int64_t>(e.slot * (KEYS ? 2 : 1) + second) * BLK * a.dim;
     uint8_t* stage = smem + L::STAGE + (warp - 4) * 2048;
-    const void* to_row = valid && p.whole ? out + out_row * ld + head * hs : nullptr;
+    const void* to_row = valid ? out + out_row * ld + head * hs : nullptr;
 #pragma unroll 1
-    for (int c = KEYS ? 0 : half; ok && c < chunks; c += KEYS ? 1 : 2) {  // 32 columns
+    for (int c = KEYS ? 0 : half; c < chunks; c += KEYS ? 1 : 2) {  // 32 columns
       uint32_t o[32];
       tmem_ld32_sync(lanes + (second ? 3 : 2) * BLK + c * 32, o);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * g + e]) * scale;
-        if (p.whole)
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[8 * g + i]) * scale;
+        if (whole)
           stage_row<32>(stage, g, v);
         else if (valid)
           store_part(part, BLK, row, v, c * 32 + g * 8, a.dim);
       }
-      if (p.whole) store_staged<32>(stage, to_row, c * 32, a.dim - c * 32);
+      if (whole) store_staged<32>(stage, to_row, c * 32, a.dim - c * 32);
     }
     tc_fence_before();
-    if (p.whole) continue;
-    // ---- a divided tile: whoever comes last adds its parts
-    __threadfence();
-    bar_compute();
-    int first;
-    const int shares = tile_shares(sh, tile_begin(sh, w), w.hi - w.lo, &first);
-    volatile int* last = reinterpret_cast<volatile int*>(smem + L::LAST);
-    if (me == 0) {
-      const uint32_t before = atomicAdd(a.arrivals + first, ok ? 1u : 0u);
-      *last = ok && before + 1 == static_cast<uint32_t>(shares);
-      if (*last) a.arrivals[first] = 0;
-    }
-    bar_compute();
-    if (*last) {
-      __threadfence();
-      // a matrix's rows side by side, eight columns at a time, and two such groups
-      constexpr int U = 2;
-      const int groups = (KEYS ? 2 : 1) * BLK * (a.dim / 8);
-      for (int i0 = me; i0 < groups; i0 += U * COMPUTE) {
-        float4 v[U][2];
-        const float* src[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = min(i0 + u * COMPUTE, groups - 1);
-          v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          src[u] = a.part + (static_cast<int64_t>(2 * (i >> 7)) * BLK + (i & (BLK - 1))) * 4;
-        }
-        auto add = [&](int s) {
-          const int64_t at = tile_slot(first, s) * slot;
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 y = *reinterpret_cast<const float4*>(src[u] + at + j * BLK * 4);
-              v[u][j].x += y.x, v[u][j].y += y.y, v[u][j].z += y.z, v[u][j].w += y.w;
-            }
-        };
-        int s = 0;
-#pragma unroll 1
-        for (; s + 4 <= shares; s += 4) add(s), add(s + 1), add(s + 2), add(s + 3);
-        if (s + 2 <= shares) add(s), add(s + 1), s += 2;
-        if (s < shares) add(s);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = i0 + u * COMPUTE, in = i & (BLK - 1), g = i >> 7;
-          if (i >= groups) continue;
-          const bool two = KEYS && g >= a.dim / 8;  // the second matrix
-          const int col = (g - (two ? a.dim / 8 : 0)) * 8;
-          int64_t o_row;
-          int h = w.head;
-          if constexpr (KEYS) {
-            if (w.tile * BLK + in >= w.s.nk) continue;
-            o_row = static_cast<int64_t>(w.s.k0) + w.tile * BLK + in;
-          } else {
-            const int d = in / a.group;
-            if (d >= a.tokens || w.tile * a.tokens + d >= w.s.nq) continue;
-            o_row = static_cast<int64_t>(w.s.q0) + w.tile * a.tokens + d;
-            h = w.head * a.group + in - d * a.group;
-          }
-          *reinterpret_cast<uint4*>((two ? a.out1 : a.out0) + o_row * (two ? a.ld1 : a.ld0) + h * (two ? a.h1 : a.h0) + col) =
-              make_uint4(pack_bf16(v[u][0].x, v[u][0].y), pack_bf16(v[u][0].z, v[u][0].w),
-                         pack_bf16(v[u][1].x, v[u][1].y), pack_bf16(v[u][1].z, v[u][1].w));
-        }
-      }
-    }
-    bar_compute();
   }
 }
 
@@ -512,15 +445,20 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
     auto init = [&](uint32_t bar, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) mbar_init(bar + 8 * i, count);
     };
-    init(b.full0, 4 * L::STAGES, 1);  // and full1, empty0, empty1
-    init(b.fix, L::STAGES, 2);
+    init(b.full0, 2 * L::STAGES, 1);  // and full1
+    init(b.empty0, L::STAGES, 2);     // both issuing warps
+    init(b.empty1, L::STAGES, KEYS ? 2 : 1);
+    init(b.fix, L::STAGES, 1);
     init(b.free, L::STAGES, 8);
-    init(b.ffull, 2, 1);  // and fempty
+    init(b.items, RING, 1);
+    init(b.ffull, 1, 1);
+    init(b.fempty, 1, 2);
     init(b.sfull, 2, 1);
-    init(b.pfull, 1, 8);
+    init(b.pfull, 2, 8);
     init(b.dpfull, 1, 1);
     init(b.dsfull, 1, 8);
-    init(b.accfull, 2, 1);  // and drain
+    init(b.accfull, 1, KEYS ? 2 : 1);
+    init(b.drain, 2, 1);
     fence_barrier_init();
     tma_prefetch_map(&a.q);
     tma_prefetch_map(&a.dout);
@@ -550,12 +488,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
   const Shares& sh = plan->shares;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
-    if (warp == 0) load_role<DP, KEYS>(a, tiles, sh, sbase);
-    if (warp == 1) mma_role<DP, KEYS>(a, tiles, sh, sbase, tmem);
-    if (warp >= 2) aux_role<DP, KEYS>(a, tiles, sh, sbase, smem);
+    if (warp == 0) load_role<DP, KEYS>(a, tiles, sh, sbase, smem);
+    if (warp == 1 || warp == 2) mma_role<DP, KEYS>(a, sbase, smem, tmem, warp - 1);
+    if (warp == 3) aux_role<DP, KEYS>(a, sbase, smem);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
-    compute_role<DP, KEYS>(a, tiles, sh, sbase, smem, tmem);
+    compute_role<DP, KEYS>(a, sbase, smem, tmem);
   }
   tc_fence_before();
   __syncthreads();
@@ -563,6 +501,51 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
     tc_fence_after();
     tmem_dealloc_cg<1>(tmem, 512);
   }
+}
+
+// Adds the parts of the tile that share blockIdx.x began and did not end, in the order of the shares; block y takes 16
+// rows of a matrix (dq, or dv and then dk), eight columns a thread.
+constexpr int JOIN_THREADS = 256, JOIN_ROWS = 16;
+__global__ void __launch_bounds__(JOIN_THREADS) join_bwd_kernel(const __grid_constant__ Args a, int keys) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const Entry e = a.begun[blockIdx.x];
+  if (*a.watch.err != 0u || !e.begins || e.hi <= e.lo) return;  // after a failure the entries may be an earlier call's
+  const int y = blockIdx.y, second = y >= BLK / JOIN_ROWS, r = (y * JOIN_ROWS & (BLK - 1)) + (threadIdx.x & 15);
+  const int c = threadIdx.x >> 4, matrices = keys ? 2 : 1;
+  int64_t out_row;
+  int head = e.head;
+  if (keys) {
+    if (e.tile * BLK + r >= e.s.nk) return;
+    out_row = static_cast<int64_t>(e.s.k0) + e.tile * BLK + r;
+  } else {
+    const int dt = r / a.group, tok = e.tile * a.tokens + dt;
+    if (dt >= a.tokens || tok >= e.s.nq) return;
+    out_row = static_cast<int64_t>(e.s.q0) + tok;
+    head = e.head * a.group + r - dt * a.group;
+  }
+  if (c * 8 >= a.dim) return;
+  const int64_t slot = static_cast<int64_t>(matrices) * BLK * a.dim;
+  const float* src = a.part + static_cast<int64_t>(second) * BLK * a.dim + (static_cast<int64_t>(2 * c) * BLK + r) * 4;
+  float v[8] = {};
+  for (int s = 0; s < e.shares; s += 8) {
+    float4 lo[8], hi[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float* p = src + tile_slot(e.from, min(s + u, e.shares - 1)) * slot;
+      lo[u] = *reinterpret_cast<const float4*>(p);
+      hi[u] = *reinterpret_cast<const float4*>(p + BLK * 4);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (s + u >= e.shares) break;
+      v[0] += lo[u].x, v[1] += lo[u].y, v[2] += lo[u].z, v[3] += lo[u].w;
+      v[4] += hi[u].x, v[5] += hi[u].y, v[6] += hi[u].z, v[7] += hi[u].w;
+    }
+  }
+  bf16* out = second ? a.out1 : a.out0;
+  *reinterpret_cast<uint4*>(out + out_row * (second ? a.ld1 : a.ld0) + head * (second ? a.h1 : a.h0) + c * 8) =
+      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
 // -lse log2(e) and -delta of each row and head, sixteen lanes a head.  Bound by
@@ -612,6 +595,14 @@ template <int DP, bool KEYS>
 cudaError_t launch_as(const Args& a, int grid, cudaStream_t s) {
   return launch_pdl(bwd_kernel<DP, KEYS>, dim3(static_cast<unsigned>(grid)), dim3(THREADS), Layout<DP>::SMEM, s, a);
 }
+// steps: the most that a tile can have; tiles of one are never divided
+template <bool KEYS>
+cudaError_t launch_both(const Args& a, int grid, int64_t steps, cudaStream_t s) {
+  const cudaError_t e = a.dim <= 64 ? launch_as<64, KEYS>(a, grid, s) : launch_as<128, KEYS>(a, grid, s);
+  if (e != cudaSuccess || steps <= 1) return e;
+  return launch_pdl(join_bwd_kernel, dim3(static_cast<unsigned>(grid), (KEYS ? 2 : 1) * BLK / JOIN_ROWS), dim3(JOIN_THREADS),
+                    0, s, a, KEYS ? 1 : 0);
+}
 template <int DP, bool KEYS>
 cudaError_t configure_as() {
   return cudaFuncSetAttribute(bwd_kernel<DP, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::SMEM);
@@ -628,11 +619,10 @@ cudaError_t configure_attention_bwd() {
 }
 
 int64_t need_attention_bwd(int64_t n, int64_t, int64_t heads, int64_t, int64_t dim) {
-  return stats_bytes(n, heads) + 2ll * MAX_SHARES * 2 * BLK * dim * 4;
+  return stats_bytes(n, heads) + BEGUN_BYTES + 2ll * MAX_SHARES * 2 * BLK * dim * 4;
 }
 
-cudaError_t launch_attention_bwd(const Machine& mc, const AttnArgs& x, const Watch& w, uint32_t* arrivals, void* ws,
-                                 cudaStream_t s) {
+cudaError_t launch_attention_bwd(const Machine& mc, const AttnArgs& x, const Watch& w, void* ws, cudaStream_t s) {
   const int64_t n = x.seq.n, nk = x.seq.nk;
   Args a;
   std::memset(static_cast<void*>(&a), 0, sizeof(a));
@@ -641,8 +631,9 @@ cudaError_t launch_attention_bwd(const Machine& mc, const AttnArgs& x, const Wat
   a.group = a.heads / a.kv_heads, a.tokens = BLK / a.group;
   a.dim = static_cast<int>(x.dim), a.causal = x.causal, a.scale = x.scale, a.c = x.scale * kLog2e;
   a.stats = static_cast<const float2*>(ws);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + stats_bytes(n, x.heads));
-  a.arrivals = arrivals, a.watch = w;
+  a.begun = reinterpret_cast<Entry*>(static_cast<uint8_t*>(ws) + stats_bytes(n, x.heads));
+  a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.begun) + BEGUN_BYTES);
+  a.watch = w;
   // without keys (or queries) the loads go to the others, which no row sees
   const int64_t rq = n ? n : nk, hq = n ? x.heads : x.kv_heads, rk = nk ? nk : n, hk = nk ? x.kv_heads : x.heads;
   if (!encode_heads(&a.q, n ? x.q : x.k, rq, hq, x.dim, a.group, a.tokens) ||
@@ -662,15 +653,13 @@ cudaError_t launch_attention_bwd(const Machine& mc, const AttnArgs& x, const Wat
                                static_cast<const float*>(x.lse), static_cast<float2*>(ws));
     if (e != cudaSuccess) return e;
     a.out0 = static_cast<bf16*>(const_cast<void*>(x.dq.p)), a.ld0 = x.dq.ld, a.h0 = x.dq.hs;
-    const int g = grid(q_tiles, nk / BLK + 1);
-    e = x.dim <= 64 ? launch_as<64, false>(a, g, s) : launch_as<128, false>(a, g, s);
+    e = launch_both<false>(a, grid(q_tiles, nk / BLK + 1), (nk + BLK - 1) / BLK, s);
     if (e != cudaSuccess) return e;
   }
   if (nk == 0) return cudaSuccess;
   a.out0 = static_cast<bf16*>(const_cast<void*>(x.dv.p)), a.ld0 = x.dv.ld, a.h0 = x.dv.hs;
   a.out1 = static_cast<bf16*>(const_cast<void*>(x.dk.p)), a.ld1 = x.dk.ld, a.h1 = x.dk.hs;
-  const int g = grid(k_tiles, n / a.tokens + 1);
-  return x.dim <= 64 ? launch_as<64, true>(a, g, s) : launch_as<128, true>(a, g, s);
+  return launch_both<true>(a, grid(k_tiles, n / a.tokens + 1), (n + a.tokens - 1) / a.tokens, s);
 }
 
 }  // namespace tpo

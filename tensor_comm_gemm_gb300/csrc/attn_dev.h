@@ -11,7 +11,6 @@ namespace tpo {
 
 constexpr int BLK = 128;           // rows of a tile's half, and keys (or queries) of a step
 constexpr int MAX_SHARES = 152;    // blocks of a launch
-static_assert(MAX_SHARES <= ARRIVALS, "one arrival counter a block");
 constexpr float kLog2e = 1.4426950408889634074f, kLn2 = 0.69314718055994530942f;
 
 // ------------------------------------------------------------------ equal shares
@@ -272,6 +271,7 @@ struct Entry {
   int begins;              // this share has the first of them
 };
 constexpr int RING = 8;
+constexpr int64_t BEGUN_BYTES = (MAX_SHARES * 48ll + 255) / 256 * 256;  // an entry for each share in the workspace
 static_assert(sizeof(Entry) == 48, "three 16-byte words");
 
 // By the loading warp: entry n of the ring; `w` has no more: the end.  begun: a place in the workspace for each share.

@@ -30,6 +30,7 @@
 // softmax (3950 cycles a step).
 
 #include <algorithm>
+#include <climits>
 #include <cstring>
 
 #include <cuda_bf16.h>
@@ -387,8 +388,9 @@ __device__ void softmax_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
   };
   for (Item it; ok && next_item(a, b, smem, item, it); ++item) {
     const int steps = it.hi - it.lo;
-    const int limit = row_of(a, it, half, dt).limit;
-    const bool idle = __all_sync(0xffffffffu, limit == 0);
+    const Row r = row_of(a, it, half, dt);
+    const bool idle = __all_sync(0xffffffffu, r.limit == 0);
+    const int limit = r.valid ? r.limit : INT_MAX;  // a row that is none may come to anything
     float m = -INFINITY, l = 0.0f;  // the maximum that is subtracted (in powers of two), the sum
     const int first = it.halves == 2 ? 0 : half, by = it.halves == 2 ? 1 : 2;
 #pragma unroll 1
@@ -425,7 +427,7 @@ __device__ void softmax_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
         for (int k = 0; k < 4; ++k) top[k] = max3(top[k], __uint_as_float(x[e + k]), __uint_as_float(y[e + k]));
       }
       const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.c;
-      const bool grow = peak > m + GROWTH;
+      const bool grow = r.valid && peak > m + GROWTH;
       if (__any_sync(0xffffffffu, grow)) {
         const float f = grow ? exp2_fast(m - peak) : 1.0f;  // from -infinity: 0
         if (grow) m = peak;
@@ -688,8 +690,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(JoinArgs a) {
   const int64_t slot = static_cast<int64_t>(a.part_rows) * (a.dim + 2), ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
   const int halves = left <= a.tokens ? 1 : 2;
   // rows at a time, and slices of the parts, so that there is about a thread for each row's eight columns and slice
-  const int slices = shares <= 8 ? 1 : min(JOIN_THREADS / columns, (shares + 7) / 8), at_once = slices == 1 ? 16 : 1;
-  const int used = a.tokens * a.group;
+  const int used = a.tokens * a.group, rows = left <= a.tokens ? left * a.group : 2 * BLK;
+  const int slices = shares <= 8 || rows > 2 * ROW_BLOCKS ? 1 : min(JOIN_THREADS / columns, (shares + 7) / 8);
+  const int at_once = slices == 1 ? 16 : 1;
   for (int first = blockIdx.y * at_once; first < halves * BLK; first += ROW_BLOCKS * at_once) {
     auto place = [&](int r, int64_t* q_row, int* h, int* limit) {  // of row r of the tile
       const int in = r & (BLK - 1), dtok = in / a.group, t = tok0 + (r >> 7) * a.tokens + dtok;
@@ -762,7 +765,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(JoinArgs a) {
   }
 }
 
-constexpr int64_t BEGUN_BYTES = (MAX_SHARES * static_cast<int64_t>(sizeof(Entry)) + 255) / 256 * 256;
 int64_t part_rows(int64_t n, int64_t group) { return n <= BLK / group ? BLK : 2 * BLK; }
 
 template <int DP>

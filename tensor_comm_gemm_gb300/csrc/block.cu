@@ -213,14 +213,14 @@ tpo_block* tpo_block_create(int64_t workspace_bytes) {
     return nullptr;
   }
   b->ws_bytes = workspace_bytes;
-  e = cudaMalloc(&b->mem, kHeadBytes + static_cast<size_t>(workspace_bytes));
+  e = cudaMalloc(&b->mem, kErrBytes + static_cast<size_t>(workspace_bytes));
   if (e != cudaSuccess) {
     fail(TPO_ERR_OOM, "workspace of %lld bytes: %s", (long long)workspace_bytes, cudaGetErrorString(e));
     cudaGetLastError();
     delete b;
     return nullptr;
   }
-  e = cudaMemset(b->mem, 0, kHeadBytes);
+  e = cudaMemset(b->mem, 0, kErrBytes);
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess) {
     cuda_fail(e, "block set-up");
@@ -267,7 +267,7 @@ tpo_status tpo_block_sync_status(tpo_block* b, void* stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "synchronise");
   if (err[0] == 0) return TPO_OK;
-  e = cudaMemsetAsync(b->mem, 0, kHeadBytes, s);
+  e = cudaMemsetAsync(b->mem, 0, kErrBytes, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "reset after device failure");
   return fail(TPO_ERR_TIMEOUT, "device wait timed out (site %u, block %u)", err[1], err[2]);

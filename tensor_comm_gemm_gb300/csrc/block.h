@@ -49,9 +49,6 @@ struct Watch {
   unsigned long long limit_ns;
 };
 
-// Arrival counters of a handle: one for each block of a launch that joins partial results.
-constexpr int ARRIVALS = 192;
-
 // What the current device holds at a time.
 constexpr int MAX_SPLIT = 8;  // CTAs of a cluster that cuts a contraction
 struct Machine {

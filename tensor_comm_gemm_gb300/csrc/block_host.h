@@ -27,10 +27,7 @@ inline tpo_status cuda_fail(cudaError_t e, const char* what) {
 }
 
 constexpr int64_t kMaxSize = 1ll << 30;
-// Ahead of the workspace: the error words, then the arrival counters of calls
-// whose blocks join partial results (0 between calls).
-constexpr size_t kErrBytes = 256;
-constexpr size_t kHeadBytes = kErrBytes + 4 * ARRIVALS;
+constexpr size_t kErrBytes = 256;  // the error words ahead of the workspace
 
 inline int64_t round_up(int64_t v, int64_t q) { return (v + q - 1) / q * q; }
 
@@ -41,14 +38,13 @@ inline int64_t ws_pitch(int64_t m) { return round_up(m, 64); }
 
 struct tpo_block {
   int device = 0;
-  uint8_t* mem = nullptr;  // error words, arrival counters, then the workspace
+  uint8_t* mem = nullptr;  // error words, then the workspace
   int64_t ws_bytes = 0;
   tpo::Machine machine{};
   int64_t path = 0, split = 0, wait_timeout_ms = 2000;  // options
   uint32_t* err() const { return reinterpret_cast<uint32_t*>(mem); }
   tpo::Watch watch() const { return {err(), static_cast<unsigned long long>(wait_timeout_ms) * 1000000ull}; }
-  uint32_t* arrivals() const { return err() + tpo::kErrBytes / 4; }
-  uint8_t* ws() const { return mem + tpo::kHeadBytes; }
+  uint8_t* ws() const { return mem + tpo::kErrBytes; }
 };
 
 namespace tpo {
