@@ -78,7 +78,7 @@ struct Layout {
   static constexpr int F1 = TILE, R0 = 2 * TILE, R1 = R0 + STAGES * TILE;  // the tile's two matrices, the rings
   static constexpr int STATS = R1 + STAGES * TILE;  // [stage][2][128]: -lse log2(e), -delta
   static constexpr int BARS = STATS + STAGES * 1024;
-  static constexpr int N_BARS = 6 * STAGES + RING + 11;
+  static constexpr int N_BARS = 6 * STAGES + RING + 13;
   static constexpr int SLOT = BARS + 8 * N_BARS;
   static constexpr int RING_AT = (SLOT + 8 + 15) / 16 * 16;
   static constexpr int STAGE = RING_AT + RING * static_cast<int>(sizeof(Entry));  // a staging box for each computing warp
@@ -89,7 +89,7 @@ struct Layout {
 
 template <int DP>
 struct Bars {
-  uint32_t full0, full1, empty0, empty1, fix, free, items, ffull, fempty, sfull, pfull, dpfull, dsfull, accfull, drain;
+  uint32_t full0, full1, empty0, empty1, fix, free, items, ffull, fempty, sfull, pfull, dpfull, dsfull, done, accfull, drain;
   __device__ explicit Bars(uint32_t sbase) {
     uint32_t b = sbase + Layout<DP>::BARS;
     auto next = [&](int n) {
@@ -99,8 +99,8 @@ struct Bars {
     };
     constexpr int S = Layout<DP>::STAGES;
     full0 = next(S), full1 = next(S), empty0 = next(S), empty1 = next(S), fix = next(S), free = next(S);
-    items = next(RING), ffull = next(1), fempty = next(1), sfull = next(2), pfull = next(2), dpfull = next(1);
-    dsfull = next(1), accfull = next(1), drain = next(2);
+    items = next(RING), ffull = next(1), fempty = next(1), sfull = next(1), pfull = next(1), dpfull = next(2);
+    dsfull = next(2), done = next(2), accfull = next(1), drain = next(2);
   }
 };
 
@@ -168,22 +168,19 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
   __syncwarp();
 }
 
-// Tensor memory: KEYS S, dP, dV and dK; otherwise S of even steps, dP, dQ and S of odd steps.  One warp issues S and what
-// overwrites it or is made of it (dV = P^T dO), the other dP and dK or dQ.
-template <int DP, bool KEYS>
-__device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, int second) {
+// KEYS: tensor memory S, dP, dV, dK.  One warp issues S and, from what overwrites it, dV = P^T dO, the other dP and dK.
+template <int DP>
+__device__ void mma_keys_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, int second) {
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const uint32_t idesc_s = idesc_n(make_idesc(false, BLK), BLK);
   const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), (a.dim + 15) / 16 * 16) | 1u << 16;
   const uint64_t f = smem_desc_sw128(sbase + (second ? L::F1 : 0)), r = smem_desc_sw128(sbase + (second ? L::R1 : L::R0));
-  // dV and dK or dQ read rows of the other warp's ring
+  // dV and dK read rows of the other warp's ring
   const uint64_t t = desc_rows(sbase + (second ? L::R0 : L::R1));
   const uint32_t full = second ? b.full1 : b.full0, empty = second ? b.empty1 : b.empty0;
   const uint32_t t_full = second ? b.full0 : b.full1, t_empty = second ? b.empty0 : b.empty1;
-  const uint32_t from = tmem + (second ? BLK : 0), acc = tmem + (KEYS && second ? 3 : 2) * BLK;
-  const uint32_t ready = second ? b.dsfull : b.pfull, made = second ? b.dpfull : b.sfull;
-  const bool adds = KEYS || second;
+  const uint32_t from = tmem + (second ? BLK : 0), acc = tmem + (second ? 3 : 2) * BLK;
   uint32_t n = 0, fn = 0;  // steps and parts so far
   bool ok = true;
   auto await = [&](uint32_t bar, uint32_t parity, uint32_t site) {
@@ -191,43 +188,92 @@ __device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t 
   };
   for (Entry e; ok && get_item(a.watch, smem + L::RING_AT, b.items, fn, &e); ++fn) {
     const int steps = e.hi - e.lo;
-    // S or dP of step s of the launch, from shared memory
-    auto scores = [&](uint32_t s) {
+    auto scores = [&](uint32_t s) {  // S or dP of step s of the launch
       await(full + 8 * (s % L::STAGES), s / L::STAGES, S_FULL);
-      if (!KEYS && !second && s >= 2) await(b.pfull + 8 * (s & 1u), s / 2 - 1, S_TEMPTY);  // S of step s - 2 has been read
       if (!ok) return;
       tc_fence_after();
-      mma_head<DP>(!KEYS && !second && (s & 1u) ? tmem + 3 * BLK : from, f, r + (s % L::STAGES) * (L::TILE >> 4), idesc_s);
-      mma_commit_cg<1>(made + (second ? 0u : 8 * (s & 1u)));
+      mma_head<DP>(from, f, r + (s % L::STAGES) * (L::TILE >> 4), idesc_s);
+      mma_commit_cg<1>(second ? b.dpfull + 8 * (s & 1u) : b.sfull);
     };
     await(b.ffull, fn, S_FULL);
     scores(n);
-    if (!adds) {  // S alone
 #pragma unroll 1
-      for (int i = 0; ok && i < steps; ++i, ++n) {
-        if (i > 0) scores(n);
-        if (ok) mma_commit_cg<1>(empty + 8 * (n % L::STAGES));
-      }
-    } else {
-#pragma unroll 1
-      for (int i = 0; ok && i < steps; ++i, ++n) {
-        const uint32_t st = n % L::STAGES;
-        if (!KEYS) mma_commit_cg<1>(empty + 8 * st);  // V is not read again
-        await(t_full + 8 * st, n / L::STAGES, S_FULL);
-        await(ready, n, S_TFULL);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t rows = t + st * (L::TILE >> 4);
-        mma4_ts(acc, from, rows, idesc_o, i > 0);
-        mma4_ts(acc, from + 64, rows + 512, idesc_o, 1u);
-        mma_commit_cg<1>(t_empty + 8 * st);
-        if (KEYS) mma_commit_cg<1>(empty + 8 * st);  // this step's S or dP is long done
-        if (i + 1 < steps) scores(n + 1);
-      }
+    for (int i = 0; ok && i < steps; ++i, ++n) {
+      const uint32_t st = n % L::STAGES;
+      await(t_full + 8 * st, n / L::STAGES, S_FULL);
+      await(second ? b.dsfull + 8 * (n & 1u) : b.pfull, second ? n >> 1 : n, S_TFULL);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t rows = t + st * (L::TILE >> 4);
+      mma4_ts(acc, from, rows, idesc_o, i > 0);
+      mma4_ts(acc, from + 64, rows + 512, idesc_o, 1u);
+      mma_commit_cg<1>(t_empty + 8 * st);
+      mma_commit_cg<1>(empty + 8 * st);  // this step's S or dP is long done
+      if (i + 1 < steps) scores(n + 1);
     }
     if (!ok) break;
     mma_commit_cg<1>(b.fempty);
-    if (adds) mma_commit_cg<1>(b.accfull);
+    mma_commit_cg<1>(b.accfull);
+  }
+  // also after a failure: every MMA issued must complete before tensor memory is freed
+  mma_commit_cg<1>(b.drain + 8 * second);
+  if ((threadIdx.x & 31) == 0) wait_bar(a.watch, b.drain + 8 * second, 0u, S_DRAIN, false);
+  __syncwarp();
+}
+
+// Otherwise: tensor memory S, dP of even steps, dQ, dP of odd steps.  One warp issues S as soon as the one before has been
+// read, and dP, a step ahead of what the threads are at; the other dQ.
+template <int DP>
+__device__ void mma_queries_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, int second) {
+  using L = Layout<DP>;
+  const Bars<DP> b(sbase);
+  const uint32_t idesc_s = idesc_n(make_idesc(false, BLK), BLK);
+  const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), (a.dim + 15) / 16 * 16) | 1u << 16;
+  const uint64_t f0 = smem_desc_sw128(sbase), f1 = smem_desc_sw128(sbase + L::F1), r0 = smem_desc_sw128(sbase + L::R0),
+                 r1 = smem_desc_sw128(sbase + L::R1), t = desc_rows(sbase + L::R0);
+  const uint32_t acc = tmem + 2 * BLK;
+  uint32_t n = 0, fn = 0;  // steps and parts so far
+  bool ok = true;
+  auto await = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+    if (ok) ok = wait_warp(a.watch, bar, parity & 1u, site);
+  };
+  for (Entry e; ok && get_item(a.watch, smem + L::RING_AT, b.items, fn, &e); ++fn) {
+    const int steps = e.hi - e.lo;
+    if (!second) await(b.ffull, fn, S_FULL);
+#pragma unroll 1
+    for (int i = 0; ok && i < steps; ++i, ++n) {
+      const uint32_t st = n % L::STAGES, at = st * (L::TILE >> 4), odd = n & 1u;
+      const uint32_t dp = tmem + (odd ? 3 : 1) * BLK;
+      if (!second) {
+        await(b.full0 + 8 * st, n / L::STAGES, S_FULL);
+        if (n >= 1) await(b.pfull, n - 1, S_TEMPTY);  // S has been read
+        if (ok) {
+          tc_fence_after();
+          mma_head<DP>(tmem, f0, r0 + at, idesc_s);
+          mma_commit_cg<1>(b.sfull);
+          mma_commit_cg<1>(b.empty0 + 8 * st);
+        }
+        await(b.full1 + 8 * st, n / L::STAGES, S_FULL);
+        if (n >= 2) await(b.done + 8 * odd, n / 2 - 1, S_TEMPTY);  // dS over this dP has been used
+        if (ok) {
+          tc_fence_after();
+          mma_head<DP>(dp, f1, r1 + at, idesc_s);
+          mma_commit_cg<1>(b.dpfull + 8 * odd);
+          mma_commit_cg<1>(b.empty1 + 8 * st);
+        }
+      } else {
+        await(b.full0 + 8 * st, n / L::STAGES, S_FULL);
+        await(b.dsfull + 8 * odd, n >> 1, S_TFULL);
+        if (ok) {
+          tc_fence_after();
+          mma4_ts(acc, dp, t + at, idesc_o, i > 0);
+          mma4_ts(acc, dp + 64, t + at + 512, idesc_o, 1u);
+          mma_commit_cg<1>(b.done + 8 * odd);
+          mma_commit_cg<1>(b.empty0 + 8 * st);
+        }
+      }
+    }
+    if (ok) mma_commit_cg<1>(second ? b.accfull : b.fempty);
   }
   // also after a failure: every MMA issued must complete before tensor memory is freed
   mma_commit_cg<1>(b.drain + 8 * second);
@@ -320,16 +366,17 @@ __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
       const bool all = __all_sync(0xffffffffu, from <= 0 && to >= 64);
       const float* stats = reinterpret_cast<const float*>(smem + L::STATS) + st * 256 + half * 64;
       float2 pr[32];
-      if (!(ok = wait_warp(a.watch, b.sfull + 8 * (n & 1u), n >> 1 & 1u, S_TFULL))) break;
+      const uint32_t odd = n & 1u, dp = KEYS || !odd ? BLK : 3 * BLK;
+      if (!(ok = wait_warp(a.watch, b.sfull, odd, S_TFULL))) break;
       if (KEYS && !(ok = wait_warp(a.watch, b.fix + 8 * st, ph, S_FULL))) break;
       {
         tc_fence_after();
         uint32_t x[64];
-        tmem_ld64_sync(mine + (KEYS || !(n & 1u) ? 0 : 3 * BLK), x);
+        tmem_ld64_sync(mine, x);
         if (!KEYS) {  // S is read
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b.pfull + 8 * (n & 1u));
+          if (lane == 0) mbar_arrive(b.pfull);
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -363,12 +410,12 @@ __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
         __syncwarp();
         if (lane == 0) mbar_arrive(b.pfull);
       }
-      if (!(ok = wait_warp(a.watch, b.dpfull, n & 1u, S_TFULL))) break;
+      if (!(ok = wait_warp(a.watch, b.dpfull + 8 * odd, n >> 1 & 1u, S_TFULL))) break;
       if (!KEYS && !(ok = wait_warp(a.watch, b.fix + 8 * st, ph, S_FULL))) break;
       {
         tc_fence_after();
         uint32_t x[64], h[32];
-        tmem_ld64_sync(mine + BLK, x);
+        tmem_ld64_sync(mine + dp, x);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float2 d0 = nd, d1 = nd;
@@ -387,13 +434,13 @@ __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
           h[e] = pack_bf16(g0.x, g0.y);
           h[e + 1] = pack_bf16(g1.x, g1.y);
         }
-        tmem_st32(mine + BLK, h);
+        tmem_st32(mine + dp, h);
         tmem_wait_st();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(b.dsfull);
+        mbar_arrive(b.dsfull + 8 * odd);
         mbar_arrive(b.free + 8 * st);
       }
     }
@@ -452,11 +499,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
     init(b.free, L::STAGES, 8);
     init(b.items, RING, 1);
     init(b.ffull, 1, 1);
-    init(b.fempty, 1, 2);
-    init(b.sfull, 2, 1);
-    init(b.pfull, 2, 8);
-    init(b.dpfull, 1, 1);
-    init(b.dsfull, 1, 8);
+    init(b.fempty, 1, KEYS ? 2 : 1);
+    init(b.sfull, 1, 1);
+    init(b.pfull, 1, 8);
+    init(b.dpfull, 2, 1);
+    init(b.dsfull, 2, 8);
+    init(b.done, 2, 1);
     init(b.accfull, 1, KEYS ? 2 : 1);
     init(b.drain, 2, 1);
     fence_barrier_init();
@@ -489,7 +537,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
     if (warp == 0) load_role<DP, KEYS>(a, tiles, sh, sbase, smem);
-    if (warp == 1 || warp == 2) mma_role<DP, KEYS>(a, sbase, smem, tmem, warp - 1);
+    if (warp == 1 || warp == 2) {
+      if constexpr (KEYS)
+        mma_keys_role<DP>(a, sbase, smem, tmem, warp - 1);
+      else
+        mma_queries_role<DP>(a, sbase, smem, tmem, warp - 1);
+    }
     if (warp == 3) aux_role<DP, KEYS>(a, sbase, smem);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
@@ -563,7 +616,8 @@ __global__ void __launch_bounds__(STAT_THREADS) stats_kernel(int64_t rows, int h
     uint4 x[STAT_ROWS], y[STAT_ROWS];
 #pragma unroll
     for (int r = 0; r < STAT_ROWS; ++r) {
-      const int64_t i = first + (k * STAT_ROWS + r) * step, row = i / heads, h = i - row * heads;
+      const int64_t i = first + (k * STAT_ROWS + r) * step;
+      const int64_t row = i >> 32 ? i / heads : static_cast<uint32_t>(i) / static_cast<uint32_t>(heads), h = i - row * heads;
       x[r] = y[r] = make_uint4(0, 0, 0, 0);
       if (i < rows && lane * 8 < dim) {
         x[r] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(out.p) + row * out.ld + h * out.hs + lane * 8);
