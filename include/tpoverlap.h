@@ -624,6 +624,12 @@ int64_t tpo_attention_bwd_workspace(int64_t n, int64_t nk, int64_t heads, int64_
  * they were, and what they or the unused rows of a cache hold is never used.
  * Scores, weights and sums are held in fp32; the weights are rounded to bf16
  * as operands of the product with v (their sum is taken before that).
+ * A call's work is counted in products of tiles of 256 rows (256 / group tokens
+ * of group = heads / kv_heads heads; 128 in the gradient) with 128 keys, and is
+ * at most 2^31 - 1 of those that have to be computed.  Sizes of which a single
+ * sequence could have more are refused with TPO_ERR_UNSUPPORTED; if the sequences
+ * have more together (their lengths are on the device), nothing is computed and
+ * tpo_block_sync_status reports the same error.  Outputs overlap no input.
  */
 tpo_status tpo_attention(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, int64_t heads, int64_t kv_heads,
                          int64_t dim, const int32_t* q_start, const int32_t* k_start, const int32_t* k_len,
@@ -636,9 +642,12 @@ tpo_status tpo_attention(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, i
  * delta = sum over dim of dout out:
  *   ds = p (dout v^T - delta);  dq = scale ds k,  dk = scale ds^T q,  dv = p^T dout
  * dk and dv are summed over the query heads that share a key head.  out and lse
- * are the forward call's.  The sequences' keys must not overlap.  A key that no
+ * are the forward call's.  The sequences' keys must not overlap, nor an output
+ * an input.  A key that no
  * query sees gets zeros.  p and ds are rounded to bf16 as operands of the
- * products.
+ * products.  Rows of other sequences and of none never reach a gradient; within
+ * a sequence a value that is not finite may also reach gradients that it has no
+ * part in, of rows that share a product of 128 by 128 with it.
  */
 tpo_status tpo_attention_bwd(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, int64_t heads, int64_t kv_heads,
                              int64_t dim, const int32_t* q_start, const int32_t* k_start, const int32_t* k_len,

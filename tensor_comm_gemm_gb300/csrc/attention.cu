@@ -61,6 +61,30 @@ tpo_status check_shape(int64_t batch, int64_t n, int64_t nk, int64_t heads, int6
   return TPO_OK;
 }
 
+// The sum over i < count of max(0, a + d i).
+double ramp(double a, double d, double count) {
+  const double first = std::fmax(0.0, std::ceil(-a / d)), m = count - first;
+  return m <= 0.0 ? 0.0 : m * (a + d * first) + d * m * (m - 1.0) / 2.0;
+}
+
+// The device counts a launch's steps in 32 bits.  This bounds those of one sequence, of all rows at most, from above
+// (tiles of `tokens` queries, and for a gradient tiles of 128 keys); of more sequences together the device finds it.
+tpo_status check_steps(const AttnArgs& a, int64_t tile_tokens, bool gradient) {
+  const double n = static_cast<double>(a.seq.n), nk = static_cast<double>(a.seq.nk);
+  const double tok = static_cast<double>(tile_tokens);
+  const double tiles = std::ceil(n / tok), blocks = std::ceil(nk / 128.0);
+  // a shorter sequence's tiles may lie elsewhere, by up to `tok` keys
+  double most = a.causal ? (2.0 + tok / 128.0) * tiles + ramp(nk - n + tok, tok, tiles) / 128.0
+                         : tiles * std::fmax(1.0, blocks);
+  if (gradient)
+    most = std::fmax(most, blocks * (tiles + 2.0) - (a.causal ? ramp(n - nk, 128.0, blocks) / tok : 0.0));
+  if (most * static_cast<double>(a.kv_heads) > 2147483647.0)
+    return fail(TPO_ERR_UNSUPPORTED,
+                "%lld queries of %lld heads with %lld keys: more than 2^31 - 1 products of a tile and 128 keys",
+                (long long)a.seq.n, (long long)a.heads, (long long)a.seq.nk);
+  return TPO_OK;
+}
+
 // Also lets keys that have no arrays of their own lie as the queries do.
 tpo_status check_sequences(Sequences& s, float scale) {
   if (!(scale > 0.0f) || std::isinf(scale)) return fail(TPO_ERR_INVALID_ARG, "scale must be positive and finite");
@@ -159,6 +183,8 @@ tpo_status tpo_attention(tpo_block* b, int64_t batch, int64_t n, int64_t nk, int
   AttnArgs a{};
   a.seq = {batch, n, nk, q_start, k_start, k_len};
   if (tpo_status st = check_sequences(a.seq, scale)) return st;
+  a.heads = heads, a.kv_heads = kv_heads, a.dim = dim, a.causal = causal != 0, a.scale = scale;
+  if (tpo_status st = check_steps(a, 128 / (heads / kv_heads) * 2, false)) return st;
   HeadsArg aq{"q", q, n, heads, dim, ldq, hq, 2}, ak{"k", k, nk, kv_heads, dim, ldk, hk, 2},
       av{"v", v, nk, kv_heads, dim, ldv, hv, 2}, ao{"out", out, n, heads, dim, ldo, ho, 2};
   HeadsArg* need[] = {&aq, &ak, &av, &ao};
@@ -167,7 +193,6 @@ tpo_status tpo_attention(tpo_block* b, int64_t batch, int64_t n, int64_t nk, int
   if (tpo_status st = check_vec("lse", lse, 4)) return st;
   if (tpo_status st = check_block(b, need_attention(n, nk, heads, kv_heads, dim))) return st;
   if (n == 0) return TPO_OK;
-  a.heads = heads, a.kv_heads = kv_heads, a.dim = dim, a.causal = causal != 0, a.scale = scale;
   a.q = aq.get(), a.k = ak.get(), a.v = av.get(), a.out = ao.get(), a.lse = lse;
   return launched(launch_attention(b->machine, a, b->watch(), b->ws(), static_cast<cudaStream_t>(stream)));
 }
@@ -183,6 +208,8 @@ tpo_status tpo_attention_bwd(tpo_block* b, int64_t batch, int64_t n, int64_t nk,
   AttnArgs a{};
   a.seq = {batch, n, nk, q_start, k_start, k_len};
   if (tpo_status st = check_sequences(a.seq, scale)) return st;
+  a.heads = heads, a.kv_heads = kv_heads, a.dim = dim, a.causal = causal != 0, a.scale = scale;
+  if (tpo_status st = check_steps(a, 128 / (heads / kv_heads), true)) return st;
   HeadsArg ado{"dout", dout, n, heads, dim, lddo, hdo, 2}, aq{"q", q, n, heads, dim, ldq, hq, 2},
       ak{"k", k, nk, kv_heads, dim, ldk, hk, 2}, av{"v", v, nk, kv_heads, dim, ldv, hv, 2},
       ao{"out", out, n, heads, dim, ldo, ho, 2}, adq{"dq", dq, n, heads, dim, lddq, hdq, 2},
@@ -194,7 +221,6 @@ tpo_status tpo_attention_bwd(tpo_block* b, int64_t batch, int64_t n, int64_t nk,
   if (tpo_status st = check_vec("lse", lse, 4)) return st;
   if (tpo_status st = check_block(b, need_attention_bwd(n, nk, heads, kv_heads, dim))) return st;
   if (n == 0 && nk == 0) return TPO_OK;
-  a.heads = heads, a.kv_heads = kv_heads, a.dim = dim, a.causal = causal != 0, a.scale = scale;
   a.q = aq.get(), a.k = ak.get(), a.v = av.get(), a.out = ao.get(), a.lse = const_cast<float*>(lse);
   a.dout = ado.get(), a.dq = adq.get(), a.dk = adk.get(), a.dv = adv.get();
   return launched(

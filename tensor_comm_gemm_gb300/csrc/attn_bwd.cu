@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
   const uint32_t tmem = ld_shared_u32(sbase + L::SLOT);
   grid_dep_wait();
   const Tiles<KEYS> tiles{a.kv_heads, a.tokens, a.causal};
-  plan_shares<THREADS>(tiles, a.seq, plan);
+  plan_shares<THREADS>(tiles, a.seq, plan, a.watch.err);
   const Shares& sh = plan->shares;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it

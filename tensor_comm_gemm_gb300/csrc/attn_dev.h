@@ -38,7 +38,7 @@ struct Part {
 };
 
 struct Shares {
-  int total, each;      // steps in all (the host holds them below 2^31) and of a share; the first `more` have one more
+  int total, each;      // steps in all and of a share; the first `more` have one more
   int count, more;
   int at, end;          // this block's share
   int seq;              // where it begins: sequence,
@@ -98,10 +98,19 @@ __device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i
   return sum;
 }
 
+// The sum of a warp's 32 values, none of them negative, held at 2^31.
+__device__ __forceinline__ uint32_t sum_held(int v) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0xffffu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) >> 16) + (lo >> 16);
+  return hi >> 15 ? 1u << 31 : hi << 16 | (lo & 0xffffu);
+}
+
 // Cuts the list; every thread of the block takes part.  At least MIN_STEPS a
-// share, unless there are more tiles than such shares.
+// share, unless there are more tiles than such shares.  Steps are counted in 32
+// bits: the host refuses sizes of which a single sequence could have 2^31; more
+// sequences than that allows are found here, reported, and nothing is done.
 template <int THREADS, class T>
-__device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc) {
+__device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc, uint32_t* err) {
   constexpr int MIN_STEPS = 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x;
   int mine = 0, upto = 0;  // steps of this thread's sequence, and with those of the block's threads before it
@@ -112,6 +121,7 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     int ahead = 0, tiles = 0;
+    bool over = false;
 #pragma unroll 1
     for (int64_t base = 0; base < q.batch; base += THREADS) {
       int all = 0;
@@ -125,10 +135,13 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
           const int u = __shfl_up_sync(0xffffffffu, upto, o);
           if (lane >= o) upto += u;
         }
+        const uint32_t held = sum_held(mine);
         __syncthreads();
-        if (lane == 31) sc->steps[warp] = upto, sc->tiles[warp] = n;
+        if (lane == 31) sc->steps[warp] = held >> 31 ? -1 : upto, sc->tiles[warp] = n;
         __syncthreads();
         const int w_steps = lane < THREADS / 32 ? sc->steps[lane] : 0;
+        over = over || __any_sync(0xffffffffu, w_steps < 0) ||
+               ahead + static_cast<uint64_t>(sum_held(max(w_steps, 0))) * t.kv_heads > INT_MAX;
         upto += __reduce_add_sync(0xffffffffu, lane < warp ? w_steps : 0);
         all = __reduce_add_sync(0xffffffffu, w_steps);
         tiles += __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? sc->tiles[lane] : 0);
@@ -145,6 +158,10 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
       ahead += all * t.kv_heads;
     }
     if (pass == 0) {
+      if (over) {
+        ahead = 0;
+        if (block == 0 && threadIdx.x == 0) give_up(err, S_STEPS);
+      }
       p.total = ahead;
       p.count = max(1, min(min(static_cast<int>(gridDim.x), ahead), max(ahead / MIN_STEPS, tiles * t.kv_heads)));
       p.each = p.total / p.count;

@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
   const uint32_t tmem = ld_shared_u32(sbase + L::SLOT);
   grid_dep_wait();
   const Tiles tiles{a.kv_heads, a.tokens, a.causal};
-  plan_shares<THREADS>(tiles, a.seq, plan);
+  plan_shares<THREADS>(tiles, a.seq, plan, a.watch.err);
   const Shares& sh = plan->shares;
   // registers: 128 a thread at launch, 65536 in all, shared out as the roles need them
   if (warp < 4) {

@@ -49,6 +49,9 @@ struct Watch {
   unsigned long long limit_ns;
 };
 
+// In the place of a wait's site: an attention launch with more steps than it can count.
+constexpr uint32_t kSiteSteps = 6;
+
 // What the current device holds at a time.
 constexpr int MAX_SPLIT = 8;  // CTAs of a cluster that cuts a contraction
 struct Machine {

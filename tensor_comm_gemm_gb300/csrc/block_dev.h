@@ -12,7 +12,7 @@ constexpr int KB = 128;  // bytes of contraction elements per K block
 // Bound of the waits of a CTA that gave up, for what it has in flight.
 constexpr unsigned long long DRAIN_NS = 2000000000ull;
 
-enum Site : uint32_t { S_EMPTY = 1, S_FULL = 2, S_TEMPTY = 3, S_TFULL = 4, S_DRAIN = 5 };
+enum Site : uint32_t { S_EMPTY = 1, S_FULL = 2, S_TEMPTY = 3, S_TFULL = 4, S_DRAIN = 5, S_STEPS = kSiteSteps };
 
 __device__ inline void give_up(uint32_t* err, uint32_t site) {
   if (atomicCAS(err, 0u, 1u) == 0u) {

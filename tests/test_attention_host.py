@@ -74,6 +74,7 @@ COMMON = [
     (dict(scale=0.0), INVALID, "scale"), (dict(scale=-1.0), INVALID, "scale"), (dict(scale=math.nan), INVALID, "scale"),
     (dict(scale=math.inf), INVALID, "scale"), (dict(q_start=P + 2), INVALID, "q_start"),
     (dict(k_start=P + 1), INVALID, "k_start"), (dict(k_len=P + 3), INVALID, "k_len"),
+    (dict(n=1 << 30, nk=1 << 17, causal=0), UNSUPPORTED, "2^31"), (dict(n=1 << 20, nk=1 << 30), UNSUPPORTED, "2^31"),
     (dict(q_start=None), INVALID, "q_start"), (dict(k_start=None), INVALID, "k_start"), (dict(), INVALID, "handle"),
 ]
 
