@@ -64,7 +64,8 @@ def test_more_steps_than_are_counted(block):
     t.tpo_attention(block, q, k, v, out, q_start=at, k_start=start, k_len=lens)
     synced(block)
     some = q[:100]
-    want = A.attention(some.double(), k[:3].double(), v[:3].double(), [(i, 1, 0, 3) for i in range(100)], True, 8 ** -0.5)
+    want = A.attention(some.double(), k[:3].double(), v[:3].double(), [(i, 1, 0, 3) for i in range(100)], True,
+                       8 ** -0.5)
     R.check("out", out[:100], want["out"])
     last = A.attention(q[-1:].double(), k[:3].double(), v[:3].double(), [(0, 1, 0, 3)], True, 8 ** -0.5)
     R.check("out", out[-1:], last["out"])
@@ -103,7 +104,8 @@ def test_wait_that_runs_out_is_reported_once(block):
 def far(rows, heads, dim, ld):
     """[rows, heads, dim] whose last rows lie past 2^32 elements."""
     assert (rows - 1) * ld > 1 << 32
-    return torch.empty((rows - 1) * ld + heads * dim, dtype=BF16, device="cuda").as_strided((rows, heads, dim), (ld, dim, 1))
+    buf = torch.empty((rows - 1) * ld + heads * dim, dtype=BF16, device="cuda")
+    return buf.as_strided((rows, heads, dim), (ld, dim, 1))
 
 
 def test_offsets_past_32_bits(block):
@@ -156,7 +158,8 @@ def test_many_sequences(block):
     at = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)])
     n = int(at[-1])
     q, k, v, dout = rnd(g, n, 4, 64), rnd(g, n, 1, 64), rnd(g, n, 1, 64), rnd(g, n, 4, 64)
-    out, lse, dq, dk, dv = torch.empty_like(q), torch.empty(n, 4, device="cuda"), *(torch.empty_like(x) for x in (q, k, v))
+    lse = torch.empty(n, 4, device="cuda")
+    out, dq, dk, dv = (torch.empty_like(x) for x in (q, q, k, v))
     t.tpo_attention(block, q, k, v, out, q_start=at.int().cuda(), lse=lse)
     t.tpo_attention_bwd(block, dout, q, k, v, out, lse, dq, dk, dv, q_start=at.int().cuda())
     synced(block)
