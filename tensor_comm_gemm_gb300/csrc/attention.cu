@@ -74,10 +74,11 @@ tpo_status check_steps(const AttnArgs& a, int64_t tile_tokens, bool gradient) {
   const double tok = static_cast<double>(tile_tokens);
   const double tiles = std::ceil(n / tok), blocks = std::ceil(nk / 128.0);
   // a shorter sequence's tiles may lie elsewhere, by up to `tok` keys
-  double most = a.causal ? (2.0 + tok / 128.0) * tiles + ramp(nk - n + tok, tok, tiles) / 128.0
-                         : tiles * std::fmax(1.0, blocks);
+  const double cost = gradient ? BWD_TILE_COST : FWD_TILE_COST;
+  double most = cost * tiles + (a.causal ? (2.0 + tok / 128.0) * tiles + ramp(nk - n + tok, tok, tiles) / 128.0
+                                         : tiles * std::fmax(1.0, blocks));
   if (gradient)
-    most = std::fmax(most, blocks * (tiles + 2.0) - (a.causal ? ramp(n - nk, 128.0, blocks) / tok : 0.0));
+    most = std::fmax(most, blocks * (cost + 2.0 + tiles) - (a.causal ? ramp(n - nk, 128.0, blocks) / tok : 0.0));
   if (most * static_cast<double>(a.kv_heads) > 2147483647.0)
     return fail(TPO_ERR_UNSUPPORTED,
                 "%lld queries of %lld heads with %lld keys: more than 2^31 - 1 products of a tile and 128 keys",

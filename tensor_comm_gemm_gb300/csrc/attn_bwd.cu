@@ -55,6 +55,7 @@ struct Args {
 // KEYS: tiles of keys, steps of queries; otherwise the other way round.
 template <bool KEYS>
 struct Tiles {
+  static constexpr int COST = BWD_TILE_COST;
   int kv_heads, tokens, causal;
   __device__ __forceinline__ int tiles(const Seq& s) const {
     return KEYS ? (s.nk + BLK - 1) / BLK : (s.nq + tokens - 1) / tokens;
@@ -122,14 +123,20 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
   uint32_t n0 = 0, n1 = 0, fn = 0, fixed = 0;  // loads so far
   bool ok = true, open = false;
   Walk w{};
-  for (walk_begin(tiles, sh, w); ok; walk_next(tiles, a.seq, w), ++fn) {
-    const Entry e = put_item(sh, w, smem + L::RING_AT, b.items, fn, a.begun, &open);
-    if (e.hi <= e.lo) break;
+  walk_begin(tiles, sh, w);
+  Entry e, next = put_item<Tiles<KEYS>>(sh, w, smem + L::RING_AT, b.items, 0, a.begun, &open);
+  for (; ok && next.hi > next.lo; ++fn) {
+    e = next;
     const int qh = e.head * a.group;
     // the rings' first, the tile itself as soon as the one before it is done with, then the rings in turns
     const int loads = 1 + 2 * (e.hi - e.lo);
 #pragma unroll 1
-    for (int i = 0; ok && i < loads; ++i) {
+    for (int i = 0; ok && i <= loads; ++i) {
+      if (i == min(loads, 4)) {  // the next tile is looked up while this one's products run, not when its loads are due
+        walk_next(tiles, a.seq, w);
+        next = put_item<Tiles<KEYS>>(sh, w, smem + L::RING_AT, b.items, fn + 1, a.begun, &open);
+      }
+      if (i == loads) break;
       const bool tile = i == 1, second = i > 1 && !(i & 1);
       const uint32_t n = tile ? fn : second ? n1 : n0, ring = tile ? 1u : static_cast<uint32_t>(L::STAGES), st = n % ring;
       const uint32_t full = tile ? b.ffull : (second ? b.full1 : b.full0) + 8 * st;

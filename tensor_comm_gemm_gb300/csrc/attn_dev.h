@@ -19,26 +19,28 @@ constexpr float kLog2e = 1.4426950408889634074f, kLn2 = 0.69314718055994530942f;
 // sequence, key head and position, each of some steps (what it contracts over,
 // 128 at a time).  The lengths are known on the device only, and differ: so the
 // list is cut by steps into as many equal shares as there are blocks, wherever
-// the cuts fall.  A tile that a cut divides is computed in parts, in fp32, which
-// a second kernel joins in the shares' order.  At most one tile begins and does
-// not end in a share, so that the share's number is the tile's in that kernel.
+// the cuts fall.  (A tile counts T::COST more, ahead of its steps: a share of many
+// short tiles took twice the time of one of a long tile.)  A tile that a cut
+// divides is computed in parts, in fp32, which a second kernel joins in the
+// shares' order.  At most one tile begins and does not end in a share, so that
+// the share's number is the tile's in that kernel.
 
 // A share's place in the list, tile by tile.
 struct Walk {
-  int done, left;   // steps of the share before this tile, and from here on
-  int off;          // steps of the tile that an earlier share has
+  int done, left;   // of the share before this tile, and from here on
+  int off;          // of the tile, that earlier shares have
   int seq, head, tile, tiles;
   Seq s;
-  int lo, hi;       // the tile's steps
+  int lo, hi;       // the tile's steps, lo with its cost ahead of them
 };
 // The share's steps of a tile.
 struct Part {
-  int lo, hi;
+  int lo, hi;  // none where the share has but the tile's cost
   bool whole;
 };
 
 struct Shares {
-  int total, each;      // steps in all and of a share; the first `more` have one more
+  int total, each;      // steps (and tiles' costs) in all and of a share; the first `more` have one more
   int count, more;
   int at, end;          // this block's share
   int seq;              // where it begins: sequence,
@@ -76,7 +78,7 @@ __device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i
   int sum = 0, at = 0, lo, hi;
   if (threadIdx.x == 0) sc->longer = 0;
   __syncthreads();
-  if (n == 1) t.range(*s, 0, &lo, &hi), sum = hi - lo;
+  if (n == 1) t.range(*s, 0, &lo, &hi), sum = hi - lo + T::COST;
   if (n > 1) {
     at = atomicAdd(&sc->longer, 1);
     sc->nq[at] = s->nq, sc->nk[at] = s->nk;
@@ -93,7 +95,7 @@ __device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i
     if ((threadIdx.x & 31) == 0) sc->nq[k] = v;
   }
   __syncthreads();
-  if (n > 1) sum = sc->nq[at];
+  if (n > 1) sum = sc->nq[at] + n * T::COST;
   *tiles = n;
   return sum;
 }
@@ -163,7 +165,11 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
         if (block == 0 && threadIdx.x == 0) give_up(err, S_STEPS);
       }
       p.total = ahead;
-      p.count = max(1, min(min(static_cast<int>(gridDim.x), ahead), max(ahead / MIN_STEPS, tiles * t.kv_heads)));
+      tiles *= t.kv_heads;
+      const int steps = ahead - tiles * T::COST;
+      // where the tiles are long their costs have shares of their own, so that no other has more than MIN_STEPS
+      const int shares = (steps >= 8 * static_cast<int64_t>(tiles) ? ahead : steps) / MIN_STEPS;
+      p.count = max(1, min(min(static_cast<int>(gridDim.x), steps), max(shares, tiles)));
       p.each = p.total / p.count;
       p.more = p.total - p.each * p.count;
       if (block < p.count && p.total > 0) p.at = share_begin(p, block), p.end = share_begin(p, block + 1);
@@ -190,6 +196,7 @@ __device__ __forceinline__ void walk_begin(const T& t, const Shares& p, Walk& w)
   for (int base = 0; base < w.tiles; base += 32) {
     int lo = 0, hi = 0;
     if (base + lane < w.tiles) t.range(w.s, base + lane, &lo, &hi);
+    if (hi > lo) lo -= T::COST;
     int v = hi - lo;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -210,11 +217,12 @@ __device__ __forceinline__ void walk_begin(const T& t, const Shares& p, Walk& w)
   w.left = 0;  // not reached: the tile exists
 }
 __device__ __forceinline__ bool walk_has(const Walk& w) { return w.left > 0; }
+template <class T>
 __device__ __forceinline__ Part walk_part(const Walk& w) {
   Part r;
-  r.lo = w.lo + w.off;
-  r.hi = min(w.hi, r.lo + w.left);
-  r.whole = r.lo == w.lo && r.hi == w.hi;
+  r.lo = w.lo + max(w.off, T::COST);
+  r.hi = min(w.hi, w.lo + w.off + w.left);
+  r.whole = w.off <= T::COST && r.hi == w.hi;
   return r;
 }
 template <class T>
@@ -239,16 +247,19 @@ __device__ __forceinline__ void walk_next(const T& t, const Sequences& q, Walk& 
     }
   }
   t.range(w.s, w.tile, &w.lo, &w.hi);
+  w.lo -= T::COST;
 }
 
 // Where a part of a divided tile goes: two slots a share, the first for the tile that it did not begin.
-__device__ __forceinline__ int part_slot(const Walk& w) { return 2 * static_cast<int>(blockIdx.x) + (w.off == 0 ? 1 : 0); }
+template <class T>
+__device__ __forceinline__ int part_slot(const Walk& w) { return 2 * static_cast<int>(blockIdx.x) + (w.off <= T::COST ? 1 : 0); }
 // The first of the shares that have a part of the tile that begins at step `begin`, and their number.
 __device__ __forceinline__ int tile_shares(const Shares& p, int begin, int steps, int* first) {
   *first = share_of(p, begin);
   return share_of(p, begin + steps - 1) - *first + 1;
 }
-__device__ __forceinline__ int tile_begin(const Shares& p, const Walk& w) { return p.at + w.done - w.off; }
+template <class T>
+__device__ __forceinline__ int tile_begin(const Shares& p, const Walk& w) { return p.at + w.done - w.off + T::COST; }
 __device__ __forceinline__ int tile_slot(int first, int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
 
 // ------------------------------------------------------------------ waits
@@ -292,18 +303,19 @@ constexpr int64_t BEGUN_BYTES = (MAX_SHARES * 48ll + 255) / 256 * 256;  // an en
 static_assert(sizeof(Entry) == 48, "three 16-byte words");
 
 // By the loading warp: entry n of the ring; `w` has no more: the end.  begun: a place in the workspace for each share.
+template <class T>
 __device__ __forceinline__ Entry put_item(const Shares& sh, const Walk& w, uint8_t* ring, uint32_t full, uint32_t n,
                                           Entry* begun, bool* open) {
   Entry e;
   e.s = w.s, e.head = w.head, e.tile = w.tile;
   e.lo = e.hi = 0, e.from = 0, e.shares = 1, e.slot = 0, e.begins = 0;
   if (walk_has(w)) {
-    const Part p = walk_part(w);
+    const Part p = walk_part<T>(w);
     e.lo = p.lo, e.hi = p.hi;
-    if (!p.whole) {
-      e.shares = tile_shares(sh, tile_begin(sh, w), w.hi - w.lo, &e.from);
-      e.slot = part_slot(w);
-      e.begins = w.off == 0;
+    if (!p.whole && p.hi > p.lo) {
+      e.shares = tile_shares(sh, tile_begin<T>(sh, w), w.hi - w.lo - T::COST, &e.from);
+      e.slot = part_slot<T>(w);
+      e.begins = w.off <= T::COST;
     }
   }
   if ((threadIdx.x & 31) == 0) {

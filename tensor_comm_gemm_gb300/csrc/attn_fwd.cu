@@ -65,6 +65,7 @@ struct Args {
 };
 
 struct Tiles {
+  static constexpr int COST = FWD_TILE_COST;
   int kv_heads, tokens, causal;
   __device__ __forceinline__ int tiles(const Seq& s) const {
     return (s.nq + 2 * tokens - 1) / (2 * tokens);
@@ -136,16 +137,22 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
   uint32_t kn = 0, vn = 0, qn = 0, loaded = 0;  // loads so far; of Q by half
   bool ok = true, open = false;
   Walk w{};
-  for (walk_begin(tiles, sh, w); ok; walk_next(tiles, a.seq, w)) {
-    Item it;
-    static_cast<Entry&>(it) = put_item(sh, w, smem + L::RING_AT, b.items, qn, a.begun, &open);
-    if (it.hi <= it.lo) break;
+  walk_begin(tiles, sh, w);
+  Item it, next;
+  static_cast<Entry&>(next) = put_item<Tiles>(sh, w, smem + L::RING_AT, b.items, 0, a.begun, &open);
+  while (ok && next.hi > next.lo) {
+    it = next;
     derive(a, it);
     // K one step ahead of V, as the products take them: K, Q, Q, K, V, K, V, .. V.  Each half (or turn) has its own Q,
     // which the next tile's replaces as soon as the half has made its last scores.
     const int loads = 2 + 2 * (it.hi - it.lo);
 #pragma unroll 1
-    for (int i = 0; ok && i < loads; ++i) {
+    for (int i = 0; ok && i <= loads; ++i) {
+      if (i == min(loads, 5)) {  // the next tile is looked up while this one's products run, not when its loads are due
+        walk_next(tiles, a.seq, w);
+        static_cast<Entry&>(next) = put_item<Tiles>(sh, w, smem + L::RING_AT, b.items, qn, a.begun, &open);
+      }
+      if (i == loads) break;
       const bool q = i == 1 || i == 2, v = !q && i > 0 && (i == loads - 1 || !(i & 1));
       const uint32_t n = q ? qn : v ? vn : kn, ring = q ? 1u : static_cast<uint32_t>(L::STAGES), st = n % ring;
       const uint32_t full = q ? b.qfull + 8 * (i - 1) : (v ? b.vfull : b.kfull) + 8 * st;
