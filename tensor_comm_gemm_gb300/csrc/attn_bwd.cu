@@ -72,34 +72,40 @@ struct Tiles {
   }
 };
 
-template <int DP>
+// A step's row of ring 0 is held from its first product to its last, of ring 1 (V; KEYS: dO) for a product of its own or
+// (KEYS) as long.  Where 128 elements of a head leave no memory for more, ring 0 of the other kernel gets a third stage
+// for its staging boxes: with two, each step waited for its keys (the long training case 778 us, with three XXX).
+template <int DP, bool KEYS>
 struct Layout {
+  static constexpr bool TIGHT = DP == 128 && !KEYS;
   static constexpr int TILE = BLK * DP * 2;
-  static constexpr int STAGES = DP == 128 ? 2 : 4;  // of each ring
-  static constexpr int F1 = TILE, R0 = 2 * TILE, R1 = R0 + STAGES * TILE;  // the tile's two matrices, the rings
-  static constexpr int STATS = R1 + STAGES * TILE;  // [stage][2][128]: -lse log2(e), -delta
-  static constexpr int BARS = STATS + STAGES * 1024;
-  static constexpr int N_BARS = 6 * STAGES + RING + 13;
+  static constexpr int S0 = TIGHT ? 3 : DP == 128 ? 2 : 4, S1 = DP == 128 ? 2 : 4;
+  static constexpr int F1 = TILE, R0 = 2 * TILE, R1 = R0 + S0 * TILE;  // the tile's two matrices, the rings
+  static constexpr int STATS = R1 + S1 * TILE;  // KEYS: [stage][2][128]: -lse log2(e), -delta
+  static constexpr int BARS = STATS + (KEYS ? S0 * 1024 : 0);
+  static constexpr int N_BARS = 4 * S0 + 2 * S1 + RING + 13;
   static constexpr int SLOT = BARS + 8 * N_BARS;
   static constexpr int RING_AT = (SLOT + 8 + 15) / 16 * 16;
-  static constexpr int STAGE = RING_AT + RING * static_cast<int>(sizeof(Entry));  // a staging box for each computing warp
-  static constexpr int PLAN = STAGE + 8 * 2048;
-  static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
+  static constexpr int SHARES = RING_AT + RING * static_cast<int>(sizeof(Entry));
+  static constexpr int STAGE = (SHARES + static_cast<int>(sizeof(Shares)) + 15) / 16 * 16;
+  static constexpr int END = STAGE + (TIGHT ? 0 : 8 * 2048);  // a staging box for each computing warp
+  static constexpr int PLAN = TIGHT ? R0 : END;               // scratch, before the loads
+  static constexpr int SMEM = (TIGHT ? END : END + static_cast<int>(sizeof(PlanScratch))) + 1024;
   static_assert(SMEM <= 232448, "shared memory of one block");
 };
 
-template <int DP>
+template <int DP, bool KEYS>
 struct Bars {
   uint32_t full0, full1, empty0, empty1, fix, free, items, ffull, fempty, sfull, pfull, dpfull, dsfull, done, accfull, drain;
   __device__ explicit Bars(uint32_t sbase) {
-    uint32_t b = sbase + Layout<DP>::BARS;
+    uint32_t b = sbase + Layout<DP, KEYS>::BARS;
     auto next = [&](int n) {
       const uint32_t r = b;
       b += 8 * n;
       return r;
     };
-    constexpr int S = Layout<DP>::STAGES;
-    full0 = next(S), full1 = next(S), empty0 = next(S), empty1 = next(S), fix = next(S), free = next(S);
+    constexpr int S0 = Layout<DP, KEYS>::S0, S1 = Layout<DP, KEYS>::S1;
+    full0 = next(S0), full1 = next(S1), empty0 = next(S0), empty1 = next(S1), fix = next(S0), free = next(S0);
     items = next(RING), ffull = next(1), fempty = next(1), sfull = next(1), pfull = next(1), dpfull = next(2);
     dsfull = next(2), done = next(2), accfull = next(1), drain = next(2);
   }
@@ -116,8 +122,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 template <int DP, bool KEYS>
 __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares& sh, uint32_t sbase, uint8_t* smem) {
-  using L = Layout<DP>;
-  const Bars<DP> b(sbase);
+  using L = Layout<DP, KEYS>;
+  const Bars<DP, KEYS> b(sbase);
   const bool lead = (threadIdx.x & 31) == 0;
   const uint32_t qbytes = static_cast<uint32_t>(a.group * a.tokens) * 128u * (DP / 64), kbytes = L::TILE;
   uint32_t n0 = 0, n1 = 0, fn = 0, fixed = 0;  // loads so far
@@ -138,7 +144,7 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
       }
       if (i == loads) break;
       const bool tile = i == 1, second = i > 1 && !(i & 1);
-      const uint32_t n = tile ? fn : second ? n1 : n0, ring = tile ? 1u : static_cast<uint32_t>(L::STAGES), st = n % ring;
+      const uint32_t n = tile ? fn : second ? n1 : n0, ring = tile ? 1u : second ? L::S1 : L::S0, st = n % ring;
       const uint32_t full = tile ? b.ffull : (second ? b.full1 : b.full0) + 8 * st;
       const uint32_t empty = tile ? b.fempty : (second ? b.empty1 : b.empty0) + 8 * st;
       if (!(ok = wait_warp(a.watch, empty, (n / ring & 1u) ^ 1u, S_EMPTY))) break;
@@ -165,11 +171,11 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
   }
   if (!ok && lead) {  // what is in flight must land before the block gives up its shared memory
 #pragma unroll 1
-    for (uint32_t j = n0 > L::STAGES ? n0 - L::STAGES : 0u; j < n0; ++j)
-      wait_bar(a.watch, b.full0 + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
+    for (uint32_t j = n0 > L::S0 ? n0 - L::S0 : 0u; j < n0; ++j)
+      wait_bar(a.watch, b.full0 + 8 * (j % L::S0), j / L::S0 & 1u, S_DRAIN, false);
 #pragma unroll 1
-    for (uint32_t j = n1 > L::STAGES ? n1 - L::STAGES : 0u; j < n1; ++j)
-      wait_bar(a.watch, b.full1 + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
+    for (uint32_t j = n1 > L::S1 ? n1 - L::S1 : 0u; j < n1; ++j)
+      wait_bar(a.watch, b.full1 + 8 * (j % L::S1), j / L::S1 & 1u, S_DRAIN, false);
     if (fixed) wait_bar(a.watch, b.ffull, (fixed - 1) & 1u, S_DRAIN, false);
   }
   __syncwarp();
@@ -178,8 +184,8 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
 // KEYS: tensor memory S, dP, dV, dK.  One warp issues S and, from what overwrites it, dV = P^T dO, the other dP and dK.
 template <int DP>
 __device__ void mma_keys_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, int second) {
-  using L = Layout<DP>;
-  const Bars<DP> b(sbase);
+  using L = Layout<DP, true>;
+  const Bars<DP, true> b(sbase);
   const uint32_t idesc_s = idesc_n(make_idesc(false, BLK), BLK);
   const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), (a.dim + 15) / 16 * 16) | 1u << 16;
   const uint64_t f = smem_desc_sw128(sbase + (second ? L::F1 : 0)), r = smem_desc_sw128(sbase + (second ? L::R1 : L::R0));
@@ -196,18 +202,18 @@ __device__ void mma_keys_role(const Args& a, uint32_t sbase, uint8_t* smem, uint
   for (Entry e; ok && get_item(a.watch, smem + L::RING_AT, b.items, fn, &e); ++fn) {
     const int steps = e.hi - e.lo;
     auto scores = [&](uint32_t s) {  // S or dP of step s of the launch
-      await(full + 8 * (s % L::STAGES), s / L::STAGES, S_FULL);
+      await(full + 8 * (s % L::S0), s / L::S0, S_FULL);
       if (!ok) return;
       tc_fence_after();
-      mma_head<DP>(from, f, r + (s % L::STAGES) * (L::TILE >> 4), idesc_s);
+      mma_head<DP>(from, f, r + (s % L::S0) * (L::TILE >> 4), idesc_s);
       mma_commit_cg<1>(second ? b.dpfull + 8 * (s & 1u) : b.sfull);
     };
     await(b.ffull, fn, S_FULL);
     scores(n);
 #pragma unroll 1
     for (int i = 0; ok && i < steps; ++i, ++n) {
-      const uint32_t st = n % L::STAGES;
-      await(t_full + 8 * st, n / L::STAGES, S_FULL);
+      const uint32_t st = n % L::S0;
+      await(t_full + 8 * st, n / L::S0, S_FULL);
       await(second ? b.dsfull + 8 * (n & 1u) : b.pfull, second ? n >> 1 : n, S_TFULL);
       if (!ok) break;
       tc_fence_after();
@@ -232,8 +238,8 @@ __device__ void mma_keys_role(const Args& a, uint32_t sbase, uint8_t* smem, uint
 // read, and dP, a step ahead of what the threads are at; the other dQ.
 template <int DP>
 __device__ void mma_queries_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, int second) {
-  using L = Layout<DP>;
-  const Bars<DP> b(sbase);
+  using L = Layout<DP, false>;
+  const Bars<DP, false> b(sbase);
   const uint32_t idesc_s = idesc_n(make_idesc(false, BLK), BLK);
   const uint32_t idesc_o = idesc_n(make_idesc(false, BLK), (a.dim + 15) / 16 * 16) | 1u << 16;
   const uint64_t f0 = smem_desc_sw128(sbase), f1 = smem_desc_sw128(sbase + L::F1), r0 = smem_desc_sw128(sbase + L::R0),
@@ -249,10 +255,10 @@ __device__ void mma_queries_role(const Args& a, uint32_t sbase, uint8_t* smem, u
     if (!second) await(b.ffull, fn, S_FULL);
 #pragma unroll 1
     for (int i = 0; ok && i < steps; ++i, ++n) {
-      const uint32_t st = n % L::STAGES, at = st * (L::TILE >> 4), odd = n & 1u;
+      const uint32_t st = n % L::S0, at = st * (L::TILE >> 4), sv = n % L::S1, odd = n & 1u;
       const uint32_t dp = tmem + (odd ? 3 : 1) * BLK;
       if (!second) {
-        await(b.full0 + 8 * st, n / L::STAGES, S_FULL);
+        await(b.full0 + 8 * st, n / L::S0, S_FULL);
         if (n >= 1) await(b.pfull, n - 1, S_TEMPTY);  // S has been read
         if (ok) {
           tc_fence_after();
@@ -260,16 +266,16 @@ __device__ void mma_queries_role(const Args& a, uint32_t sbase, uint8_t* smem, u
           mma_commit_cg<1>(b.sfull);
           mma_commit_cg<1>(b.empty0 + 8 * st);
         }
-        await(b.full1 + 8 * st, n / L::STAGES, S_FULL);
+        await(b.full1 + 8 * sv, n / L::S1, S_FULL);
         if (n >= 2) await(b.done + 8 * odd, n / 2 - 1, S_TEMPTY);  // dS over this dP has been used
         if (ok) {
           tc_fence_after();
-          mma_head<DP>(dp, f1, r1 + at, idesc_s);
+          mma_head<DP>(dp, f1, r1 + sv * (L::TILE >> 4), idesc_s);
           mma_commit_cg<1>(b.dpfull + 8 * odd);
-          mma_commit_cg<1>(b.empty1 + 8 * st);
+          mma_commit_cg<1>(b.empty1 + 8 * sv);
         }
       } else {
-        await(b.full0 + 8 * st, n / L::STAGES, S_FULL);
+        await(b.full0 + 8 * st, n / L::S0, S_FULL);
         await(b.dsfull + 8 * odd, n >> 1, S_TFULL);
         if (ok) {
           tc_fence_after();
@@ -293,15 +299,15 @@ __device__ void mma_queries_role(const Args& a, uint32_t sbase, uint8_t* smem, u
 // with P and dS.
 template <int DP, bool KEYS>
 __device__ void aux_role(const Args& a, uint32_t sbase, uint8_t* smem) {
-  using L = Layout<DP>;
-  const Bars<DP> b(sbase);
+  using L = Layout<DP, KEYS>;
+  const Bars<DP, KEYS> b(sbase);
   const int lane = threadIdx.x & 31;
   const int used = a.group * a.tokens;
   uint32_t n = 0, fn = 0;
   for (Entry e; get_item(a.watch, smem + L::RING_AT, b.items, fn, &e); ++fn) {
 #pragma unroll 1
     for (int j = e.lo; j < e.hi; ++j, ++n) {
-      const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
+      const uint32_t st = n % L::S0, ph = n / L::S0 & 1u;
       const int left = KEYS ? min(a.tokens, e.s.nq - j * a.tokens) * a.group : e.s.nk - j * BLK;  // rows in use
       if constexpr (KEYS) {
         if (!wait_warp(a.watch, b.free + 8 * st, ph ^ 1u, S_EMPTY)) return;
@@ -343,8 +349,8 @@ __device__ void aux_role(const Args& a, uint32_t sbase, uint8_t* smem) {
 
 template <int DP, bool KEYS>
 __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t tmem) {
-  using L = Layout<DP>;
-  const Bars<DP> b(sbase);
+  using L = Layout<DP, KEYS>;
+  const Bars<DP, KEYS> b(sbase);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, half = (warp - 4) >> 2;
   const int row = quad * 32 + lane;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16), mine = lanes + half * 64;
@@ -366,7 +372,7 @@ __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
     }
 #pragma unroll 1
     for (int j = e.lo; j < e.hi; ++j, ++n) {
-      const uint32_t st = n % L::STAGES, ph = n / L::STAGES & 1u;
+      const uint32_t st = n % L::S0, ph = n / L::S0 & 1u;
       // columns [from, to) of the group's 64 that the row sees
       const int from = KEYS ? min(a.tokens, max(0, seen - j * a.tokens)) * a.group - half * 64 : 0;
       const int to = (KEYS ? min(a.tokens, e.s.nq - j * a.tokens) * a.group : seen - j * BLK) - half * 64;
@@ -472,12 +478,16 @@ __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[8 * g + i]) * scale;
-        if (whole)
+        if (!whole) {
+          if (valid) store_part(part, BLK, row, v, c * 32 + g * 8, a.dim);
+        } else if (!L::TIGHT) {
           stage_row<32>(stage, g, v);
-        else if (valid)
-          store_part(part, BLK, row, v, c * 32 + g * 8, a.dim);
+        } else if (valid && c * 32 + g * 8 < a.dim) {
+          *reinterpret_cast<uint4*>(out + out_row * ld + head * hs + c * 32 + g * 8) =
+              make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        }
       }
-      if (whole) store_staged<32>(stage, to_row, c * 32, a.dim - c * 32);
+      if (whole && !L::TIGHT) store_staged<32>(stage, to_row, c * 32, a.dim - c * 32);
     }
     tc_fence_before();
   }
@@ -486,7 +496,7 @@ __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
 // Grid: one block per SM at most, each an equal share of the steps.
 template <int DP, bool KEYS>
 __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__ Args a) {
-  using L = Layout<DP>;
+  using L = Layout<DP, KEYS>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -495,15 +505,15 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
   const int warp = threadIdx.x >> 5;
   PlanScratch* plan = reinterpret_cast<PlanScratch*>(smem + L::PLAN);
   if (threadIdx.x == 0) {
-    const Bars<DP> b(sbase);
+    const Bars<DP, KEYS> b(sbase);
     auto init = [&](uint32_t bar, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) mbar_init(bar + 8 * i, count);
     };
-    init(b.full0, 2 * L::STAGES, 1);  // and full1
-    init(b.empty0, L::STAGES, 2);     // both issuing warps
-    init(b.empty1, L::STAGES, KEYS ? 2 : 1);
-    init(b.fix, L::STAGES, 1);
-    init(b.free, L::STAGES, 8);
+    init(b.full0, L::S0 + L::S1, 1);  // and full1
+    init(b.empty0, L::S0, 2);     // both issuing warps
+    init(b.empty1, L::S1, KEYS ? 2 : 1);
+    init(b.fix, L::S0, 1);
+    init(b.free, L::S0, 8);
     init(b.items, RING, 1);
     init(b.ffull, 1, 1);
     init(b.fempty, 1, KEYS ? 2 : 1);
@@ -527,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
   }
   if (KEYS) {  // rows of a query tile that no load writes are operands of the products too
     const int unused = BLK - a.group * a.tokens;
-    for (int i = threadIdx.x; i < unused * 8 * (DP / 64) * 2 * L::STAGES; i += THREADS) {
+    for (int i = threadIdx.x; i < unused * 8 * (DP / 64) * 2 * L::S0; i += THREADS) {
       const int r = i / 8 % unused, block = i / 8 / unused;
       *reinterpret_cast<uint4*>(smem + L::R0 + block * 16384 + (BLK - 1 - r) * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
     }
@@ -539,8 +549,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(const __grid_constant__
   const uint32_t tmem = ld_shared_u32(sbase + L::SLOT);
   grid_dep_wait();
   const Tiles<KEYS> tiles{a.kv_heads, a.tokens, a.causal};
-  plan_shares<THREADS>(tiles, a.seq, plan, a.watch.err);
-  const Shares& sh = plan->shares;
+  Shares& sh = *reinterpret_cast<Shares*>(smem + L::SHARES);
+  plan_shares<THREADS>(tiles, a.seq, plan, &sh, a.watch.err);
+  if (L::TIGHT) {  // loads follow where the scratch was
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
     if (warp == 0) load_role<DP, KEYS>(a, tiles, sh, sbase, smem);
@@ -654,7 +668,7 @@ int64_t stats_bytes(int64_t n, int64_t heads) { return (n * heads * 8 + 255) / 2
 
 template <int DP, bool KEYS>
 cudaError_t launch_as(const Args& a, int grid, cudaStream_t s) {
-  return launch_pdl(bwd_kernel<DP, KEYS>, dim3(static_cast<unsigned>(grid)), dim3(THREADS), Layout<DP>::SMEM, s, a);
+  return launch_pdl(bwd_kernel<DP, KEYS>, dim3(static_cast<unsigned>(grid)), dim3(THREADS), Layout<DP, KEYS>::SMEM, s, a);
 }
 // steps: the most that a tile can have; tiles of one are never divided
 template <bool KEYS>
@@ -666,7 +680,7 @@ cudaError_t launch_both(const Args& a, int grid, int64_t steps, cudaStream_t s) 
 }
 template <int DP, bool KEYS>
 cudaError_t configure_as() {
-  return cudaFuncSetAttribute(bwd_kernel<DP, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::SMEM);
+  return cudaFuncSetAttribute(bwd_kernel<DP, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP, KEYS>::SMEM);
 }
 
 }  // namespace

@@ -62,7 +62,6 @@ struct PlanScratch {
   int steps[32], tiles[32];  // of a warp's sequences
   int longer;                // sequences of more than one tile: their number, their lengths and then their steps
   int nq[PLAN_SEQS], nk[PLAN_SEQS];
-  Shares shares;
 };
 
 // Steps of sequence i for one key head; every thread of the block calls it, with
@@ -110,9 +109,10 @@ __device__ __forceinline__ uint32_t sum_held(int v) {
 // Cuts the list; every thread of the block takes part.  At least MIN_STEPS a
 // share, unless there are more tiles than such shares.  Steps are counted in 32
 // bits: the host refuses sizes of which a single sequence could have 2^31; more
-// sequences than that allows are found here, reported, and nothing is done.
+// sequences than that allows are found here, reported, and nothing is done.  The
+// scratch is free at the end.
 template <int THREADS, class T>
-__device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc, uint32_t* err) {
+__device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc, Shares* shares, uint32_t* err) {
   constexpr int MIN_STEPS = 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x;
   int mine = 0, upto = 0;  // steps of this thread's sequence, and with those of the block's threads before it
@@ -151,10 +151,10 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
       if (pass == 1) {
         const int from = ahead + (upto - mine) * t.kv_heads;
         if (from <= p.at && p.at < from + mine * t.kv_heads) {
-          sc->shares.seq = static_cast<int>(base + threadIdx.x);
-          sc->shares.before = from;
-          sc->shares.a_head = mine;
-          sc->shares.s = s;
+          shares->seq = static_cast<int>(base + threadIdx.x);
+          shares->before = from;
+          shares->a_head = mine;
+          shares->s = s;
         }
       }
       ahead += all * t.kv_heads;
@@ -168,12 +168,12 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
       tiles *= t.kv_heads;
       const int steps = ahead - tiles * T::COST;
       // where the tiles are long their costs have shares of their own, so that no other has more than MIN_STEPS
-      const int shares = (steps >= 8 * static_cast<int64_t>(tiles) ? ahead : steps) / MIN_STEPS;
-      p.count = max(1, min(min(static_cast<int>(gridDim.x), steps), max(shares, tiles)));
+      const int most = (steps >= 8 * static_cast<int64_t>(tiles) ? ahead : steps) / MIN_STEPS;
+      p.count = max(1, min(min(static_cast<int>(gridDim.x), steps), max(most, tiles)));
       p.each = p.total / p.count;
       p.more = p.total - p.each * p.count;
       if (block < p.count && p.total > 0) p.at = share_begin(p, block), p.end = share_begin(p, block + 1);
-      if (threadIdx.x == 0) sc->shares = p;
+      if (threadIdx.x == 0) *shares = p;
     }
     __syncthreads();
     if (p.at >= p.end) return;

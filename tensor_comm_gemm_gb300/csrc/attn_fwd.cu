@@ -89,7 +89,8 @@ struct Layout {
   static constexpr int ROWS = BAD + BAD_SETS * BAD_STEPS * 16;  // [2][2][128] floats: maxima and sums
   static constexpr int STAGE = ROWS + 2048;  // the storing warps' boxes
   static constexpr int PLAN = STAGE + 4 * 4096;
-  static constexpr int SMEM = PLAN + static_cast<int>(sizeof(PlanScratch)) + 1024;
+  static constexpr int SHARES = PLAN + static_cast<int>(sizeof(PlanScratch));
+  static constexpr int SMEM = SHARES + static_cast<int>(sizeof(Shares)) + 1024;
   static_assert(SMEM <= 232448 && RING_AT % 16 == 0, "shared memory of one block");
 };
 
@@ -648,8 +649,8 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_kernel(const __grid_constant__
   const uint32_t tmem = ld_shared_u32(sbase + L::SLOT);
   grid_dep_wait();
   const Tiles tiles{a.kv_heads, a.tokens, a.causal};
-  plan_shares<THREADS>(tiles, a.seq, plan, a.watch.err);
-  const Shares& sh = plan->shares;
+  Shares& sh = *reinterpret_cast<Shares*>(smem + L::SHARES);
+  plan_shares<THREADS>(tiles, a.seq, plan, &sh, a.watch.err);
   // registers: 128 a thread at launch, 65536 in all, shared out as the roles need them
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" : "+r"(sbase)::"memory");  // nothing of a role is computed ahead of it
