@@ -8,7 +8,10 @@
 // 2^-26 turns.  A block computes its tokens' sines and cosines once, in shared
 // memory, and all heads of the token use them.
 //
-// Bound by memory: every element is read and written once.
+// Bound by memory: every element is read and written once.  Measured with a flushed
+// L2: a prompt's queries and keys in bf16 (302 MB moved) 50.5 us, 5.98 TB/s or 90 %
+// of the measured copy bandwidth; 29 MB in fp32 12.2 us and one token 7.0 us, of
+// which about 6 are a launch on a cold cache.
 
 #include <cuda_bf16.h>
 
