@@ -612,21 +612,22 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_bwd_kernel(const __grid_con
   const int64_t slot = static_cast<int64_t>(matrices) * BLK * a.dim;
   const float* src = a.part + static_cast<int64_t>(second) * BLK * a.dim + (static_cast<int64_t>(2 * c) * BLK + r) * 4;
   float v[8] = {};
-  for (int s = 0; s < e.shares; s += 8) {
-    float4 lo[8], hi[8];
+  some_parts(0, e.shares, [&](auto count, int s) {
+    constexpr int U = decltype(count)::value;
+    float4 lo[U], hi[U];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < U; ++u) {
       const float* p = src + tile_slot(e.from, min(s + u, e.shares - 1)) * slot;
       lo[u] = *reinterpret_cast<const float4*>(p);
       hi[u] = *reinterpret_cast<const float4*>(p + BLK * 4);
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < U; ++u) {
       if (s + u >= e.shares) break;
       v[0] += lo[u].x, v[1] += lo[u].y, v[2] += lo[u].z, v[3] += lo[u].w;
       v[4] += hi[u].x, v[5] += hi[u].y, v[6] += hi[u].z, v[7] += hi[u].w;
     }
-  }
+  });
   bf16* out = second ? a.out1 : a.out0;
   *reinterpret_cast<uint4*>(out + out_row * (second ? a.ld1 : a.ld0) + head * (second ? a.h1 : a.h0) + c * 8) =
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));

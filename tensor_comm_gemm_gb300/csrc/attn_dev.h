@@ -262,6 +262,22 @@ template <class T>
 __device__ __forceinline__ int tile_begin(const Shares& p, const Walk& w) { return p.at + w.done - w.off + T::COST; }
 __device__ __forceinline__ int tile_slot(int first, int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
 
+// For the kernels that join: parts s up to `end`, eight, four or two at a time, so that their loads are in flight
+// together and few are made for nothing (most divided tiles have two or three parts).
+template <int U>
+struct Count {
+  static constexpr int value = U;
+};
+template <class F>
+__device__ __forceinline__ void some_parts(int s, int end, F f) {
+#pragma unroll 1
+  while (end - s > 4) f(Count<8>{}, s), s += 8;
+  if (end - s > 2)
+    f(Count<4>{}, s);
+  else if (end > s)
+    f(Count<2>{}, s);
+}
+
 // ------------------------------------------------------------------ waits
 
 // A converged warp's bounded wait, in few instructions: the kernels' roles share the instruction cache, and a kernel

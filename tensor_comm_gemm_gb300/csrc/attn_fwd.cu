@@ -753,22 +753,23 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(JoinArgs a) {
       const int each = (shares + slices - 1) / slices, end = min(shares, (slice + 1) * each);
       const float* src = a.part + (static_cast<int64_t>(2 * c) * a.part_rows + first + r) * 4;
       const float* f = weight + r * MAX_SHARES;
-      for (int s = slice * each; s < end; s += 8) {
-        float4 lo[8], hi[8];
+      some_parts(slice * each, end, [&](auto count, int s) {
+        constexpr int U = decltype(count)::value;
+        float4 lo[U], hi[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < U; ++u) {
           const float* p = src + tile_slot(e.from, min(s + u, end - 1)) * slot;
           lo[u] = *reinterpret_cast<const float4*>(p);
           hi[u] = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(a.part_rows) * 4);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < U; ++u) {
           if (s + u >= end) break;
           const float k = f[s + u];
           v[0] = fmaf(lo[u].x, k, v[0]), v[1] = fmaf(lo[u].y, k, v[1]), v[2] = fmaf(lo[u].z, k, v[2]), v[3] = fmaf(lo[u].w, k, v[3]);
           v[4] = fmaf(hi[u].x, k, v[4]), v[5] = fmaf(hi[u].y, k, v[5]), v[6] = fmaf(hi[u].z, k, v[6]), v[7] = fmaf(hi[u].w, k, v[7]);
         }
-      }
+      });
     }
     if (slices > 1) {
 #pragma unroll
