@@ -23,12 +23,12 @@
 // each group half of a step's columns, and store.
 //
 // Measured (back-to-back calls with a flushed L2): two sequences of 4096 causal
-// tokens, 32 heads of 128 over 8, 748 us, or 1.29 PFLOP/s of the seven products
-// (66 % of the measured matrix rate; 919 TFLOP/s of the five that a single pass
-// would need).  Bound by a step's chain of product, exponentials, product and
+// tokens, 32 heads of 128 over 8, 730 to 739 us, or 1.31 PFLOP/s of the seven
+// products (67 % of the measured matrix rate; 940 TFLOP/s of the five that a single
+// pass would need).  Bound by a step's chain of product, exponentials, product and
 // store to tensor memory, with 512 columns of it all in use: sixteen computing
 // warps of half the columns took 842 us, groups that take the steps in turns as
-// long as these.  Odd sequences of 9 heads of 80 over 3: 76.5 us, bound by the five
+// long as these.  Odd sequences of 9 heads of 80 over 3: 72 us, bound by the five
 // launches' starts and by filling the pipeline at each tile.
 
 #include <algorithm>
@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_bwd_kernel(const __grid_con
 }
 
 // -lse log2(e) and -delta of each row and head, sixteen lanes a head.  Bound by
-// memory: out and dout are read once.
+// memory: out and dout are read once, 135 MB in 25 us of a cold start (43 when
+// blocks went round in a grid of eight an SM and lse came last).
 constexpr int STAT_THREADS = 256, STAT_ROWS = 4;  // rows of a group of lanes in flight together
 __global__ void __launch_bounds__(STAT_THREADS) stats_kernel(int64_t rows, int heads, int dim, Heads out, Heads dout,
                                                             const float* lse, float2* stats) {

@@ -30,7 +30,7 @@
 // softmax (3950 cycles a step, now 2850, of which the tensor core works 2080).
 //
 // Measured (times of back-to-back calls with a flushed L2): 8192 causal tokens of
-// 32 heads of 128 over 8 take 401 us, 1.37 PFLOP/s, 70 % of the measured matrix
+// 32 heads of 128 over 8 take 398 to 405 us, 1.37 PFLOP/s, 70 % of the measured matrix
 // rate; bound by that step: a half's scores, softmax (about 1450 cycles, 512 of
 // them exponentials at 32 a cycle) and P V follow one another, and two halves do
 // not quite fill each other's gaps.  12 packed sequences of 8 heads over 1:
