@@ -616,6 +616,7 @@ int64_t tpo_attention_bwd_workspace(int64_t n, int64_t nk, int64_t heads, int64_
  *              With one sequence each may be NULL: all rows, k_len of them.
  *   causal     not 0: the sequence's last query sees all of its keys, each
  *              earlier one a key less (query t of nq sees t + 1 + nk - nq)
+ *   scale      positive, at most 1e38
  *   lse        [n, heads] fp32 for the backward pass, or NULL
  * Lengths are read on the device: a captured call follows them as they change.
  * Starts and lengths are held inside the tensors, so that no call reads or
@@ -645,7 +646,8 @@ tpo_status tpo_attention(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, i
  * are the forward call's.  The sequences' keys must not overlap, nor an output
  * an input.  A key that no
  * query sees gets zeros.  p and ds are rounded to bf16 as operands of the
- * products.  Rows of other sequences and of none never reach a gradient; within
+ * products.  Rows of no sequence are left as they were, in dq, dk and dv too.
+ * Rows of other sequences and of none never reach a gradient; within
  * a sequence a value that is not finite may also reach gradients that it has no
  * part in, of rows that share a product of 128 by 128 with it.
  */

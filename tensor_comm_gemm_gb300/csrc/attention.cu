@@ -88,7 +88,7 @@ tpo_status check_steps(const AttnArgs& a, int64_t tile_tokens, bool gradient) {
 
 // Also lets keys that have no arrays of their own lie as the queries do.
 tpo_status check_sequences(Sequences& s, float scale) {
-  if (!(scale > 0.0f) || std::isinf(scale)) return fail(TPO_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (!(scale > 0.0f) || scale > 1e38f) return fail(TPO_ERR_INVALID_ARG, "scale must be positive, at most 1e38");
   if (tpo_status st = check_vec("q_start", s.q_start, 4)) return st;
   if (tpo_status st = check_vec("k_start", s.k_start, 4)) return st;
   if (tpo_status st = check_vec("k_len", s.k_len, 4)) return st;
