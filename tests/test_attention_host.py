@@ -72,7 +72,8 @@ COMMON = [
     (dict(heads=1 << 17), INVALID, "heads"), (dict(heads=130, kv_heads=1), UNSUPPORTED, "heads"),
     (dict(dim=0), INVALID, "dim"), (dict(dim=20), UNSUPPORTED, "dim"), (dict(dim=256), UNSUPPORTED, "dim"),
     (dict(scale=0.0), INVALID, "scale"), (dict(scale=-1.0), INVALID, "scale"), (dict(scale=math.nan), INVALID, "scale"),
-    (dict(scale=math.inf), INVALID, "scale"), (dict(scale=2e38), INVALID, "scale"), (dict(q_start=P + 2), INVALID, "q_start"),
+    (dict(scale=math.inf), INVALID, "scale"), (dict(scale=2e38), INVALID, "scale"),
+    (dict(q_start=P + 2), INVALID, "q_start"),
     (dict(k_start=P + 1), INVALID, "k_start"), (dict(k_len=P + 3), INVALID, "k_len"),
     (dict(n=1 << 30, nk=1 << 17, causal=0), UNSUPPORTED, "2^31"), (dict(n=1 << 20, nk=1 << 30), UNSUPPORTED, "2^31"),
     (dict(q_start=None), INVALID, "q_start"), (dict(k_start=None), INVALID, "k_start"), (dict(), INVALID, "handle"),
