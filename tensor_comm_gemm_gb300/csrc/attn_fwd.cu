@@ -98,7 +98,7 @@ struct Layout {
   static constexpr int BAD = RING_AT + RING * static_cast<int>(sizeof(Entry));  // [BAD_SETS][BAD_STEPS][4] keys, a bit each
   static constexpr int ROWS = BAD + BAD_SETS * BAD_STEPS * 16;  // [2][2][128] floats: maxima and sums
   static constexpr int STAGE = ROWS + 2048;  // the storing warps' boxes
-  static constexpr int PLAN = STAGE + 4 * 4096;
+  static constexpr int PLAN = STAGE + 4 * 2048;
   static constexpr int SHARES = PLAN + static_cast<int>(sizeof(PlanScratch));
   static constexpr int SMEM = SHARES + static_cast<int>(sizeof(Shares)) + 1024;
   static_assert(SMEM <= 232448 && RING_AT % 16 == 0, "shared memory of one block");
@@ -503,7 +503,7 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
   const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * BLK;
   const int dt = row / a.group, head_in = row - dt * a.group;  // the row's token in its half, its head in the group
   const float* stats = reinterpret_cast<const float*>(smem + L::ROWS);
-  uint8_t* stage = smem + L::STAGE + quad * 4096;
+  uint8_t* stage = smem + L::STAGE + quad * 2048;
   const int64_t ml_at = static_cast<int64_t>(a.part_rows) * a.dim;
   uint32_t item = 0, on0 = 0, on1 = 0;
   bool ok = true;
@@ -549,18 +549,18 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
       }
       const void* to_row = r.valid ? a.out + q_row * a.ldo + head * a.ho : nullptr;
 #pragma unroll 1
-      for (int c = 0; c < a.dim; c += 64) {
-        uint32_t o[64];
+      for (int c = 0; c < a.dim; c += 32) {  // few at a time: the code is fetched for each tile anew
+        uint32_t o[32];
         if (idle) {  // no product: the accumulator may hold anything
 #pragma unroll
-          for (int e = 0; e < 64; ++e) o[e] = 0u;
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
         } else {
-          tmem_ld64_sync(to + half * BLK + c, o);
+          tmem_ld32_sync(to + half * BLK + c, o);
 #pragma unroll
-          for (int e = 0; e < 64; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
           if (two) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < 2; ++g) {
               uint32_t x[16];
               tmem_ld16_sync(to + BLK + c + g * 16, x);
 #pragma unroll
@@ -570,7 +570,7 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
           }
         }
         auto v = [&](int e) { return __uint_as_float(o[e]); };
-        if (c + 64 >= a.dim) {  // the accumulator is read: the next tile's products may begin
+        if (c + 32 >= a.dim) {  // the accumulator is read: the next tile's products may begin
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -585,7 +585,7 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
             if (!(bad[i >> 5] >> (i & 31) & 1u) || key >= r.limit) continue;
             const bf16* x = a.values + (static_cast<int64_t>(it.s.k0) + key) * a.ldv + it.head * a.hv + c;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
+            for (int e = 0; e < 32; ++e) {
               const float y = c + e < a.dim ? __bfloat162float(x[e]) : 0.0f;
               if (!isfinite(y)) o[e] = __float_as_uint(v(e) + y);
             }
@@ -593,15 +593,15 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
         }
         if (whole) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
+          for (int g = 0; g < 4; ++g) {
             const float z[8] = {v(8 * g),     v(8 * g + 1), v(8 * g + 2), v(8 * g + 3),
                                 v(8 * g + 4), v(8 * g + 5), v(8 * g + 6), v(8 * g + 7)};
-            stage_row<64>(stage, g, z);
+            stage_row<32>(stage, g, z);
           }
-          store_staged<64>(stage, to_row, c, a.dim - c);
+          store_staged<32>(stage, to_row, c, a.dim - c);
         } else if (r.valid) {
 #pragma unroll
-          for (int g = 0; g < 16; ++g)
+          for (int g = 0; g < 8; ++g)
             if (c + 4 * g < a.dim)
               *reinterpret_cast<float4*>(part + static_cast<int64_t>((c >> 2) + g) * a.part_rows * 4) =
                   make_float4(v(4 * g), v(4 * g + 1), v(4 * g + 2), v(4 * g + 3));
