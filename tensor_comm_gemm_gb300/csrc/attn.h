@@ -28,15 +28,16 @@ struct Seq {
 };
 // Sequence i, held inside the tensors whatever the arrays say.
 __device__ __forceinline__ Seq sequence(const Sequences& s, int64_t i) {
+  // all loads before the first use of one
+  const int32_t* ke = s.k_len ? s.k_len + i : s.k_start ? s.k_start + i + 1 : nullptr;
+  const int64_t q0 = s.q_start ? s.q_start[i] : 0, q1 = s.q_start ? s.q_start[i + 1] : s.n;
+  const int64_t k0 = s.k_start ? s.k_start[i] : 0, k1 = ke ? *ke : s.nk;
   auto in = [](int64_t v, int64_t lo, int64_t hi) { return static_cast<int>(v < lo ? lo : v > hi ? hi : v); };
   Seq r;
-  r.q0 = s.q_start ? in(s.q_start[i], 0, s.n) : 0;
-  r.nq = (s.q_start ? in(s.q_start[i + 1], r.q0, s.n) : static_cast<int>(s.n)) - r.q0;
-  r.k0 = s.k_start ? in(s.k_start[i], 0, s.nk) : 0;
-  if (s.k_len)
-    r.nk = in(s.k_len[i], 0, s.nk - r.k0);
-  else
-    r.nk = (s.k_start ? in(s.k_start[i + 1], r.k0, s.nk) : static_cast<int>(s.nk)) - r.k0;
+  r.q0 = in(q0, 0, s.n);
+  r.nq = in(q1, r.q0, s.n) - r.q0;
+  r.k0 = in(k0, 0, s.nk);
+  r.nk = s.k_len ? in(k1, 0, s.nk - r.k0) : in(k1, r.k0, s.nk) - r.k0;
   return r;
 }
 
