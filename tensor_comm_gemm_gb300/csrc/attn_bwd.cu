@@ -491,13 +491,13 @@ __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
         if (!whole) {
           if (valid) store_part(part, BLK, row, v, c * 32 + g * 8, a.dim);
         } else if (!L::TIGHT) {
-          stage_row<32>(stage, g, v);
+          stage_row(stage, g, v);
         } else if (valid && c * 32 + g * 8 < a.dim) {
           *reinterpret_cast<uint4*>(out + out_row * ld + head * hs + c * 32 + g * 8) =
               make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
         }
       }
-      if (whole && !L::TIGHT) store_staged<32>(stage, to_row, c * 32, a.dim - c * 32);
+      if (whole && !L::TIGHT) store_staged(stage, to_row, c * 32, a.dim - c * 32);
     }
     tc_fence_before();
   }

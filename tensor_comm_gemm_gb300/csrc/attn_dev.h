@@ -499,29 +499,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // ------------------------------------------------------------------ results
 
-// A warp stores W (32 or 64) columns of its 32 rows as bf16 through 64 W bytes of shared memory at `stage`, row by row:
-// lines of 2 W bytes.  (Each lane storing 16 bytes of its own row costs a cycle of the SM's memory pipe for each lane,
-// 7000 for the 256 rows of a tile.)  First each lane brings its own row, eight columns from 8 g on at a time; then
-// `mine`, the lane's row in global memory (NULL: none), gets columns [col, col + W), of which `cols` exist.
-template <int W>
-__device__ __forceinline__ uint32_t stage_at(int row, int g) {
-  return W == 64 ? row * 128 + ((g ^ (row & 7)) << 4) : row * 64 + ((g ^ ((row >> 1) & 3)) << 4);
-}
-template <int W>
+// A warp stores 32 columns of its 32 rows as bf16 through 2 KB of shared memory at `stage`, row by row: lines of 64
+// bytes.  (Each lane storing 16 bytes of its own row costs a cycle of the SM's memory pipe for each lane, 7000 for the 256
+// rows of a tile.)  First each lane brings its own row, eight columns from 8 g on at a time; then `mine`, the lane's row
+// in global memory (NULL: none), gets columns [col, col + 32), of which `cols` exist.
+__device__ __forceinline__ uint32_t stage_at(int row, int g) { return row * 64 + ((g ^ ((row >> 1) & 3)) << 4); }
 __device__ __forceinline__ void stage_row(uint8_t* stage, int g, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(stage + stage_at<W>(threadIdx.x & 31, g)) =
+  *reinterpret_cast<uint4*>(stage + stage_at(threadIdx.x & 31, g)) =
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
-template <int W>
 __device__ __forceinline__ void store_staged(const uint8_t* stage, const void* mine, int col, int cols) {
-  constexpr int G = W / 8;  // lanes a row
-  const int lane = threadIdx.x & 31, part = lane % G;
+  const int lane = threadIdx.x & 31, part = lane % 4;
   __syncwarp();
-#pragma unroll 4
-  for (int i = 0; i < G; ++i) {
-    const int row = lane / G + 32 / G * i;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = lane / 4 + 8 * i;
     const uint64_t to = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), row);
-    const uint4 x = *reinterpret_cast<const uint4*>(stage + stage_at<W>(row, part));
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + stage_at(row, part));
     if (to && part * 8 < cols) *reinterpret_cast<uint4*>(to + (col + part * 8) * 2) = x;
   }
   __syncwarp();  // before the next columns

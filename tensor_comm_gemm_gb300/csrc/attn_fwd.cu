@@ -596,9 +596,9 @@ __device__ void store_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_
           for (int g = 0; g < 4; ++g) {
             const float z[8] = {v(8 * g),     v(8 * g + 1), v(8 * g + 2), v(8 * g + 3),
                                 v(8 * g + 4), v(8 * g + 5), v(8 * g + 6), v(8 * g + 7)};
-            stage_row<32>(stage, g, z);
+            stage_row(stage, g, z);
           }
-          store_staged<32>(stage, to_row, c, a.dim - c);
+          store_staged(stage, to_row, c, a.dim - c);
         } else if (r.valid) {
 #pragma unroll
           for (int g = 0; g < 8; ++g)
