@@ -627,10 +627,10 @@ int64_t tpo_attention_bwd_workspace(int64_t n, int64_t nk, int64_t heads, int64_
  * as operands of the product with v (their sum is taken before that).
  * A call's work is counted in products of tiles of 256 rows (256 / group tokens
  * of group = heads / kv_heads heads; 128 in the gradient) with 128 keys, and is
- * at most 2^31 - 1 of those that have to be computed.  Sizes of which a single
- * sequence could have more are refused with TPO_ERR_UNSUPPORTED; if the sequences
- * have more together (their lengths are on the device), nothing is computed and
- * tpo_block_sync_status reports the same error.  Outputs overlap no input.
+ * at most 2^31 - 1 of those that have to be computed.  One sequence without arrays
+ * that has more is refused with TPO_ERR_UNSUPPORTED; where lengths are on the
+ * device, nothing is computed and tpo_block_sync_status reports the same error.
+ * Outputs overlap no input.
  */
 tpo_status tpo_attention(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, int64_t heads, int64_t kv_heads,
                          int64_t dim, const int32_t* q_start, const int32_t* k_start, const int32_t* k_len,

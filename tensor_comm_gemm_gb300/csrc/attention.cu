@@ -67,15 +67,15 @@ double ramp(double a, double d, double count) {
   return m <= 0.0 ? 0.0 : m * (a + d * first) + d * m * (m - 1.0) / 2.0;
 }
 
-// The device counts a launch's steps in 32 bits.  This bounds those of one sequence, of all rows at most, from above
-// (tiles of `tokens` queries, and for a gradient tiles of 128 keys); of more sequences together the device finds it.
+// The device counts a launch's steps in 32 bits.  This bounds those of a sequence of all rows from above (tiles of
+// `tile_tokens` queries, and for a gradient tiles of 128 keys).  Where lengths are on the device, it finds too many itself.
 tpo_status check_steps(const AttnArgs& a, int64_t tile_tokens, bool gradient) {
+  if (a.seq.batch > 1 || a.seq.q_start || a.seq.k_start || a.seq.k_len) return TPO_OK;
   const double n = static_cast<double>(a.seq.n), nk = static_cast<double>(a.seq.nk);
   const double tok = static_cast<double>(tile_tokens);
   const double tiles = std::ceil(n / tok), blocks = std::ceil(nk / 128.0);
-  // a shorter sequence's tiles may lie elsewhere, by up to `tok` keys
   const double cost = gradient ? BWD_TILE_COST : FWD_TILE_COST;
-  double most = cost * tiles + (a.causal ? (2.0 + tok / 128.0) * tiles + ramp(nk - n + tok, tok, tiles) / 128.0
+  double most = cost * tiles + (a.causal ? tiles + ramp(nk - n + tok, tok, tiles) / 128.0
                                          : tiles * std::fmax(1.0, blocks));
   if (gradient)
     most = std::fmax(most, blocks * (cost + 2.0 + tiles) - (a.causal ? ramp(n - nk, 128.0, blocks) / tok : 0.0));

@@ -731,7 +731,7 @@ cudaError_t launch_attention_bwd(const Machine& mc, const AttnArgs& x, const Wat
     return cudaErrorInvalidValue;
   const int64_t sms = std::min(mc.sms, MAX_SHARES);
   auto grid = [&](int64_t tiles, int64_t steps) {  // no more blocks than the most steps that these sizes can have
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, tiles * x.kv_heads * steps)));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, std::min<int64_t>(tiles * x.kv_heads, MAX_SHARES) * steps)));
   };
   const int64_t q_tiles = n / a.tokens + std::min(x.seq.batch, n), k_tiles = nk / BLK + std::min(x.seq.batch, nk);
   if (n > 0) {

@@ -64,10 +64,17 @@ struct PlanScratch {
   int nq[PLAN_SEQS], nk[PLAN_SEQS];
 };
 
+// The sum of a warp's 32 values, none of them negative, held at 2^31.
+__device__ __forceinline__ uint32_t sum_held(int v) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0xffffu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) >> 16) + (lo >> 16);
+  return hi >> 15 ? 1u << 31 : hi << 16 | (lo & 0xffffu);
+}
+
 // Steps of sequence i for one key head; every thread of the block calls it, with
-// its own i (at or past `batch`: none).  *s gets the sequence, *tiles the tiles'
-// number.  A thread counts a single tile itself; those of longer sequences are
-// counted by a warp each.
+// its own i (at or past `batch`: none).  Held at 2^31 - 1.  *s gets the sequence,
+// *tiles the tiles' number.  A thread counts a single tile itself; those of longer
+// sequences are counted by a warp each.
 template <int THREADS, class T>
 __device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i, Seq* s, int* tiles, PlanScratch* sc) {
   static_assert(THREADS <= PLAN_SEQS, "a place for each thread's sequence");
@@ -87,30 +94,22 @@ __device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i
   for (int k = threadIdx.x >> 5; k < sc->longer; k += THREADS / 32) {
     const Seq o{0, sc->nq[k], 0, sc->nk[k]};
     const int count = t.tiles(o);
-    int v = 0;
+    int64_t v = 0;
 #pragma unroll 1
-    for (int j = threadIdx.x & 31; j < count; j += 32) t.range(o, j, &lo, &hi), v += hi - lo;
-    v = __reduce_add_sync(0xffffffffu, v);
-    if ((threadIdx.x & 31) == 0) sc->nq[k] = v;
+    for (int j = threadIdx.x & 31; j < count; j += 32) t.range(o, j, &lo, &hi), v += hi - lo + T::COST;
+    const uint32_t held = sum_held(static_cast<int>(min(v, static_cast<int64_t>(INT_MAX))));
+    if ((threadIdx.x & 31) == 0) sc->nq[k] = static_cast<int>(min(held, static_cast<uint32_t>(INT_MAX)));
   }
   __syncthreads();
-  if (n > 1) sum = sc->nq[at] + n * T::COST;
+  if (n > 1) sum = sc->nq[at];
   *tiles = n;
   return sum;
 }
 
-// The sum of a warp's 32 values, none of them negative, held at 2^31.
-__device__ __forceinline__ uint32_t sum_held(int v) {
-  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0xffffu);
-  const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) >> 16) + (lo >> 16);
-  return hi >> 15 ? 1u << 31 : hi << 16 | (lo & 0xffffu);
-}
-
 // Cuts the list; every thread of the block takes part.  At least MIN_STEPS a
 // share, unless there are more tiles than such shares.  Steps are counted in 32
-// bits: the host refuses sizes of which a single sequence could have 2^31; more
-// sequences than that allows are found here, reported, and nothing is done.  The
-// scratch is free at the end.
+// bits: more than that is found here, reported, and nothing is done.  The scratch
+// is free at the end.
 template <int THREADS, class T>
 __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc, Shares* shares, uint32_t* err) {
   constexpr int MIN_STEPS = 2;
@@ -137,7 +136,7 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
           const int u = __shfl_up_sync(0xffffffffu, upto, o);
           if (lane >= o) upto += u;
         }
-        const uint32_t held = sum_held(mine);
+        const uint32_t held = __any_sync(0xffffffffu, mine == INT_MAX) ? 1u << 31 : sum_held(mine);
         __syncthreads();
         if (lane == 31) sc->steps[warp] = held >> 31 ? -1 : upto, sc->tiles[warp] = n;
         __syncthreads();

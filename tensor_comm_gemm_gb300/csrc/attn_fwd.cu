@@ -827,7 +827,7 @@ cudaError_t launch_attention(const Machine& mc, const AttnArgs& x, const Watch& 
     return cudaErrorInvalidValue;
   // no more blocks than the most steps that these sizes can have
   const int64_t tiles = (x.seq.n / (2 * a.tokens) + std::min(x.seq.batch, x.seq.n)) * x.kv_heads;
-  const int64_t most = tiles * (x.seq.nk / BLK + 1);
+  const int64_t most = std::min<int64_t>(tiles, MAX_SHARES) * (x.seq.nk / BLK + 1);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(mc.sms, MAX_SHARES), most)));
   const cudaError_t e = x.dim <= 64 ? launch_as<64>(a, grid, s) : launch_as<128>(a, grid, s);
   if (e != cudaSuccess || x.seq.nk <= BLK) return e;  // tiles of one step are never divided

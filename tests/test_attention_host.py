@@ -66,6 +66,7 @@ def test_workspace(lib):
 
 
 SHAPE = dict(batch=2, n=4, nk=6, heads=4, kv_heads=2, dim=16, q_start=P, k_start=P, k_len=P, causal=1, scale=0.25)
+ALONE = dict(batch=1, q_start=None, k_start=None, k_len=None)
 COMMON = [
     (dict(batch=0), INVALID, "batch"), (dict(n=-1), INVALID, "sizes"), (dict(nk=(1 << 30) + 1), INVALID, "sizes"),
     (dict(heads=3), INVALID, "heads"), (dict(kv_heads=0), INVALID, "heads"), (dict(heads=0), INVALID, "heads"),
@@ -75,7 +76,8 @@ COMMON = [
     (dict(scale=math.inf), INVALID, "scale"), (dict(scale=2e38), INVALID, "scale"),
     (dict(q_start=P + 2), INVALID, "q_start"),
     (dict(k_start=P + 1), INVALID, "k_start"), (dict(k_len=P + 3), INVALID, "k_len"),
-    (dict(n=1 << 30, nk=1 << 17, causal=0), UNSUPPORTED, "2^31"), (dict(n=1 << 20, nk=1 << 30), UNSUPPORTED, "2^31"),
+    (dict(ALONE, n=1 << 30, nk=1 << 17, causal=0), UNSUPPORTED, "2^31"),
+    (dict(ALONE, n=1 << 20, nk=1 << 30), UNSUPPORTED, "2^31"),
     (dict(q_start=None), INVALID, "q_start"), (dict(k_start=None), INVALID, "k_start"), (dict(), INVALID, "handle"),
 ]
 
@@ -110,6 +112,32 @@ def test_attention_bwd_refuses(lib, kw, status, word):
     a.update(kw)
     assert lib.tpo_attention_bwd(None, *a.values(), None) == status
     assert word in t.tpo_last_error(), t.tpo_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ALONE, n=1 << 20, nk=1 << 20, heads=32, kv_heads=8),
+    dict(ALONE, n=1 << 17, nk=1 << 22, heads=8, kv_heads=8),
+    dict(batch=1 << 20, n=1 << 20, nk=1 << 26, heads=8, kv_heads=1),  # of a few keys each
+    dict(ALONE, n=1 << 30, nk=0, heads=1, kv_heads=1, causal=0)])
+def test_long_sequences_are_taken(lib, kw):
+    """Sizes whose steps 32 bits do count get as far as the handle."""
+    a = dict(SHAPE, dim=128)
+    a.update(kw)
+    heads, kv = a["heads"] * 128, a["kv_heads"] * 128
+    q, k = {"ld": heads, "h": 128}, {"ld": kv, "h": 128}
+
+    def of(names):
+        out = {}
+        for x in names:
+            at = q if x in ("q", "out", "dout", "dq") else k
+            out.update({x: P, "ld" + x: at["ld"], "h" + x: at["h"]})
+        return out
+
+    assert lib.tpo_attention(None, *a.values(), *of(("q", "k", "v", "out")).values(), None, None) == INVALID
+    assert "handle" in t.tpo_last_error(), t.tpo_last_error()
+    bwd = of(("dout", "q", "k", "v", "out")), of(("dq", "dk", "dv"))
+    assert lib.tpo_attention_bwd(None, *a.values(), *bwd[0].values(), P, *bwd[1].values(), None) == INVALID
+    assert "handle" in t.tpo_last_error(), t.tpo_last_error()
 
 
 @pytest.mark.parametrize("kw,word", [

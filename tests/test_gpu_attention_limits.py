@@ -71,6 +71,24 @@ def test_more_steps_than_are_counted(block):
     R.check("out", out[-1:], last["out"])
 
 
+def test_a_sequence_of_more_steps_than_are_counted(block):
+    """2^24 tokens that all see 2^24 keys: 2^33 steps, in one of two sequences."""
+    n = 1 << 24
+    q, k, v, dout = (torch.zeros(n, 1, 8, dtype=BF16, device="cuda") for _ in range(4))
+    out, dq, dk, dv = (torch.full_like(q, 7.0) for _ in range(4))
+    lse, at = torch.full((n, 1), 7.0, device="cuda"), ints([0, n, n])
+    mine = t.tpo_block_create(t.tpo_attention_bwd_workspace(n, n, 1, 1, 8))
+    try:
+        t.tpo_attention(mine, q, k, v, out, q_start=at, causal=False, lse=lse)
+        assert t.tpo_block_sync_status(mine) == t.TPO_ERR_UNSUPPORTED
+        t.tpo_attention_bwd(mine, dout, q, k, v, out, lse, dq, dk, dv, q_start=at, causal=False)
+        assert t.tpo_block_sync_status(mine) == t.TPO_ERR_UNSUPPORTED
+        synced(mine)
+    finally:
+        t.tpo_block_destroy(mine)
+    assert all((x == 7.0).all() for x in (out, lse, dq, dk, dv))
+
+
 def test_wait_that_runs_out_is_reported_once(block):
     """Parts of thousands of steps keep what writes them waiting for milliseconds: with a bound of one it gives up, with
     products and loads in flight, and a gradient behind it on the stream (whose own waits are all short) does too."""
