@@ -23,7 +23,7 @@
 // each group half of a step's columns, and store.
 //
 // Measured (back-to-back calls with a flushed L2): two sequences of 4096 causal
-// tokens, 32 heads of 128 over 8, 730 to 739 us, or 1.31 PFLOP/s of the seven
+// tokens, 32 heads of 128 over 8, 730 to 746 us, or 1.31 PFLOP/s of the seven
 // products (67 % of the measured matrix rate; 940 TFLOP/s of the five that a single
 // pass would need).  Bound by a step's chain of product, exponentials, product and
 // store to tensor memory, with 512 columns of it all in use: sixteen computing
