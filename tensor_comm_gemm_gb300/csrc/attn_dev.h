@@ -224,6 +224,7 @@ __device__ __forceinline__ Part walk_part(const Walk& w) {
   r.whole = w.off <= T::COST && r.hi == w.hi;
   return r;
 }
+// The next tile, by a converged warp.
 template <class T>
 __device__ __forceinline__ void walk_next(const T& t, const Sequences& q, Walk& w) {
   const int steps = w.hi - w.lo - w.off;
@@ -235,14 +236,28 @@ __device__ __forceinline__ void walk_next(const T& t, const Sequences& q, Walk& 
     w.tile = 0;
     if (++w.head == t.kv_heads) {
       w.head = 0;
-      do {
-        if (++w.seq >= q.batch) {  // not reached: steps are left
-          w.left = 0;
-          return;
-        }
-        w.s = sequence(q, w.seq);
-        w.tiles = t.tiles(w.s);
-      } while (w.tiles == 0);
+      // the next sequence with tiles, 32 at a time: a captured call's batch may be mostly slots without queries, and the
+      // other roles' waits are running (one at a time a million of them took more than 100 ms)
+      const int lane = threadIdx.x & 31;
+      uint32_t some = 0;
+#pragma unroll 1
+      for (w.seq += 1; w.seq < q.batch; w.seq += 32) {
+        const bool there = w.seq + lane < q.batch;
+        w.s = Seq{0, 0, 0, 0};
+        if (there) w.s = sequence(q, w.seq + lane);
+        w.tiles = there ? t.tiles(w.s) : 0;
+        some = __ballot_sync(0xffffffffu, w.tiles > 0);
+        if (some) break;
+      }
+      if (!some) {  // not reached: steps are left
+        w.left = 0;
+        return;
+      }
+      const int l = __ffs(some) - 1;
+      w.seq += l;
+      w.s.q0 = __shfl_sync(0xffffffffu, w.s.q0, l), w.s.nq = __shfl_sync(0xffffffffu, w.s.nq, l);
+      w.s.k0 = __shfl_sync(0xffffffffu, w.s.k0, l), w.s.nk = __shfl_sync(0xffffffffu, w.s.nk, l);
+      w.tiles = __shfl_sync(0xffffffffu, w.tiles, l);
     }
   }
   t.range(w.s, w.tile, &w.lo, &w.hi);
