@@ -625,11 +625,15 @@ int64_t tpo_attention_bwd_workspace(int64_t n, int64_t nk, int64_t heads, int64_
  * they were, and what they or the unused rows of a cache hold is never used.
  * Scores, weights and sums are held in fp32; the weights are rounded to bf16
  * as operands of the product with v (their sum is taken before that).
- * A call's work is counted in products of tiles of 256 rows (256 / group tokens
- * of group = heads / kv_heads heads; 128 in the gradient) with 128 keys, and is
- * at most 2^31 - 1 of those that have to be computed.  One sequence without arrays
- * that has more is refused with TPO_ERR_UNSUPPORTED; where lengths are on the
- * device, nothing is computed and tpo_block_sync_status reports the same error.
+ * A call's work is counted in steps.  A tile is 2 floor(128 / group) tokens of a
+ * sequence with the group = heads / kv_heads heads that share a key head; it has
+ * a step for every 128 keys that its last token sees, at least one, and four
+ * more.  (In the gradient: tiles of floor(128 / group) tokens over keys and, for
+ * dk and dv, tiles of 128 keys over those of tokens, each with two more; each of
+ * the two counts by itself.)  There may be 2^31 - 2 steps.  One sequence without
+ * arrays that has more is refused with TPO_ERR_UNSUPPORTED; where lengths are on
+ * the device, nothing is computed and tpo_block_sync_status reports the same
+ * error.
  * Outputs overlap no input.
  */
 tpo_status tpo_attention(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, int64_t heads, int64_t kv_heads,

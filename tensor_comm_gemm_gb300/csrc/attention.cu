@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -61,28 +62,45 @@ tpo_status check_shape(int64_t batch, int64_t n, int64_t nk, int64_t heads, int6
   return TPO_OK;
 }
 
-// The sum over i < count of max(0, a + d i).
-double ramp(double a, double d, double count) {
-  const double first = std::fmax(0.0, std::ceil(-a / d)), m = count - first;
-  return m <= 0.0 ? 0.0 : m * (a + d * first) + d * m * (m - 1.0) / 2.0;
+// The sum over i < count of (a i + b) / m, rounded down; none is negative.  m steps on, a term has grown by a.
+int64_t sum_of_quotients(int64_t count, int64_t a, int64_t b, int64_t m) {
+  int64_t sum = 0;
+  for (int64_t r = 0; r < std::min(count, m); ++r) {
+    const int64_t terms = (count - 1 - r) / m + 1;
+    sum += terms * ((a * r + b) / m) + a * (terms * (terms - 1) / 2);
+  }
+  return sum;
 }
 
-// The device counts a launch's steps in 32 bits.  This bounds those of a sequence of all rows from above (tiles of
-// `tile_tokens` queries, and for a gradient tiles of 128 keys).  Where lengths are on the device, it finds too many itself.
-tpo_status check_steps(const AttnArgs& a, int64_t tile_tokens, bool gradient) {
+// Steps and costs of one key head's tiles, as Tiles::range gives them on the device, for a sequence of all rows: of
+// queries, `tok` tokens a tile, and (a gradient's) of keys, 128 a tile.
+int64_t steps_of_queries(int64_t n, int64_t nk, int64_t tok, bool causal, int64_t cost) {
+  if (n == 0) return 0;
+  const int64_t tiles = (n + tok - 1) / tok, last = std::max<int64_t>(0, nk - 1) / 128;
+  if (!causal) return tiles * (cost + 1 + last);
+  // tile i's last token sees nk - n + (i + 1) tok keys, the last tile's all; a key more than 128 j are j steps more
+  const int64_t first = n - nk < tok ? 0 : (n - nk) / tok;
+  const int64_t before_last = std::max<int64_t>(0, tiles - 1 - first);
+  return tiles * (cost + 1) + last + sum_of_quotients(before_last, tok, nk - n + (first + 1) * tok - 1, 128);
+}
+int64_t steps_of_keys(int64_t n, int64_t nk, int64_t tok, bool causal, int64_t cost) {
+  const int64_t tiles = (nk + 127) / 128, queries = std::max<int64_t>(1, (n + tok - 1) / tok);
+  if (!causal || n == 0) return tiles * (cost + queries);
+  // the queries of the first (128 i - nk + n) / tok tiles do not see tile i's keys
+  const int64_t first = nk > n ? (nk - n + 127) / 128 : 0;
+  return tiles * (cost + queries) - sum_of_quotients(std::max<int64_t>(0, tiles - first), 128, 128 * first - nk + n, tok);
+}
+
+// The device counts a launch's steps in 32 bits.  It checks that itself where it has the lengths.
+tpo_status check_steps(const AttnArgs& a, bool gradient) {
   if (a.seq.batch > 1 || a.seq.q_start || a.seq.k_start || a.seq.k_len) return TPO_OK;
-  const double n = static_cast<double>(a.seq.n), nk = static_cast<double>(a.seq.nk);
-  const double tok = static_cast<double>(tile_tokens);
-  const double tiles = std::ceil(n / tok), blocks = std::ceil(nk / 128.0);
-  const double cost = gradient ? BWD_TILE_COST : FWD_TILE_COST;
-  double most = cost * tiles + (a.causal ? tiles + ramp(nk - n + tok, tok, tiles) / 128.0
-                                         : tiles * std::fmax(1.0, blocks));
-  if (gradient)
-    most = std::fmax(most, blocks * (cost + 2.0 + tiles) - (a.causal ? ramp(n - nk, 128.0, blocks) / tok : 0.0));
-  if (most * static_cast<double>(a.kv_heads) > 2147483647.0)
-    return fail(TPO_ERR_UNSUPPORTED,
-                "%lld queries of %lld heads with %lld keys: more than 2^31 - 1 products of a tile and 128 keys",
-                (long long)a.seq.n, (long long)a.heads, (long long)a.seq.nk);
+  const int64_t n = a.seq.n, nk = a.seq.nk, tok = 128 / (a.heads / a.kv_heads);
+  const int64_t most = gradient ? std::max(steps_of_queries(n, nk, tok, a.causal, BWD_TILE_COST),
+                                           steps_of_keys(n, nk, tok, a.causal, BWD_TILE_COST))
+                                : steps_of_queries(n, nk, 2 * tok, a.causal, FWD_TILE_COST);
+  if (most > MAX_STEPS / a.kv_heads)
+    return fail(TPO_ERR_UNSUPPORTED, "%lld queries of %lld heads with %lld keys have more than 2^31 - 2 steps",
+                (long long)n, (long long)a.heads, (long long)nk);
   return TPO_OK;
 }
 
@@ -185,7 +203,7 @@ tpo_status tpo_attention(tpo_block* b, int64_t batch, int64_t n, int64_t nk, int
   a.seq = {batch, n, nk, q_start, k_start, k_len};
   if (tpo_status st = check_sequences(a.seq, scale)) return st;
   a.heads = heads, a.kv_heads = kv_heads, a.dim = dim, a.causal = causal != 0, a.scale = scale;
-  if (tpo_status st = check_steps(a, 128 / (heads / kv_heads) * 2, false)) return st;
+  if (tpo_status st = check_steps(a, false)) return st;
   HeadsArg aq{"q", q, n, heads, dim, ldq, hq, 2}, ak{"k", k, nk, kv_heads, dim, ldk, hk, 2},
       av{"v", v, nk, kv_heads, dim, ldv, hv, 2}, ao{"out", out, n, heads, dim, ldo, ho, 2};
   HeadsArg* need[] = {&aq, &ak, &av, &ao};
@@ -210,7 +228,7 @@ tpo_status tpo_attention_bwd(tpo_block* b, int64_t batch, int64_t n, int64_t nk,
   a.seq = {batch, n, nk, q_start, k_start, k_len};
   if (tpo_status st = check_sequences(a.seq, scale)) return st;
   a.heads = heads, a.kv_heads = kv_heads, a.dim = dim, a.causal = causal != 0, a.scale = scale;
-  if (tpo_status st = check_steps(a, 128 / (heads / kv_heads), true)) return st;
+  if (tpo_status st = check_steps(a, true)) return st;
   HeadsArg ado{"dout", dout, n, heads, dim, lddo, hdo, 2}, aq{"q", q, n, heads, dim, ldq, hq, 2},
       ak{"k", k, nk, kv_heads, dim, ldk, hk, 2}, av{"v", v, nk, kv_heads, dim, ldv, hv, 2},
       ao{"out", out, n, heads, dim, ldo, ho, 2}, adq{"dq", dq, n, heads, dim, lddq, hdq, 2},

@@ -60,6 +60,8 @@ struct AttnArgs {
 // (attention over 8192 tokens took 446, 424, 405 and 406 us with 1 to 4, packed sequences 61, 56, 55 and 53; its
 // gradient 786, 785, 789 and 791, of odd sequences 82, 80, 82 and 84).
 constexpr int FWD_TILE_COST = 4, BWD_TILE_COST = 2;
+// Steps and costs that a launch can count in 32 bits (one more than these says that there are too many).
+constexpr int64_t MAX_STEPS = 2147483646;
 
 // Set the kernels' attributes.
 cudaError_t configure_attention();

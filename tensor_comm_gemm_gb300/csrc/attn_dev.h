@@ -108,7 +108,7 @@ __device__ __forceinline__ int cost_of(const T& t, const Sequences& q, int64_t i
 
 // Cuts the list; every thread of the block takes part.  At least MIN_STEPS a
 // share, unless there are more tiles than such shares.  Steps are counted in 32
-// bits: more than that is found here, reported, and nothing is done.  The scratch
+// bits: more than MAX_STEPS are found here, reported, and nothing is done.  The scratch
 // is free at the end.
 template <int THREADS, class T>
 __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, PlanScratch* sc, Shares* shares, uint32_t* err) {
@@ -142,7 +142,7 @@ __device__ __forceinline__ void plan_shares(const T& t, const Sequences& q, Plan
         __syncthreads();
         const int w_steps = lane < THREADS / 32 ? sc->steps[lane] : 0;
         over = over || __any_sync(0xffffffffu, w_steps < 0) ||
-               ahead + static_cast<uint64_t>(sum_held(max(w_steps, 0))) * t.kv_heads > INT_MAX;
+               ahead + static_cast<uint64_t>(sum_held(max(w_steps, 0))) * t.kv_heads > MAX_STEPS;
         upto += __reduce_add_sync(0xffffffffu, lane < warp ? w_steps : 0);
         all = __reduce_add_sync(0xffffffffu, w_steps);
         tiles += __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? sc->tiles[lane] : 0);

@@ -271,7 +271,7 @@ tpo_status tpo_block_sync_status(tpo_block* b, void* stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "reset after device failure");
   if (err[1] == kSiteSteps)
-    return fail(TPO_ERR_UNSUPPORTED, "the sequences of an attention call have more than 2^31 - 1 products of a tile and 128 keys; none was computed");
+    return fail(TPO_ERR_UNSUPPORTED, "the sequences of an attention call have more than 2^31 - 2 steps; none was computed");
   return fail(TPO_ERR_TIMEOUT, "device wait timed out (site %u, block %u)", err[1], err[2]);
 }
 
