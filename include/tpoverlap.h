@@ -570,7 +570,8 @@ typedef enum { TPO_ROTARY_UNSCALED = 0, TPO_ROTARY_LINEAR = 1, TPO_ROTARY_BY_PAR
  * the device; needs no GPU).  Pair i turns by f_i = base^(-2 i / rot) radians a
  * position, scaled as above; its entry is 2^64 f_i / (2 pi) modulo 2^64, the
  * turns per position as a 64-bit fraction.  Any other frequencies may be put
- * into a table in the same form.
+ * into a table in the same form.  TPO_ERR_INVALID_ARG, and nothing is written,
+ * if base and factor make a frequency that is not finite.
  */
 tpo_status tpo_rotary_table(int64_t rot, double base, int scaling, double factor, double low, double high,
                             int64_t original, uint64_t* table);

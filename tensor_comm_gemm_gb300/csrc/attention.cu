@@ -133,7 +133,7 @@ tpo_status tpo_rotary_table(int64_t rot, double base, int scaling, double factor
     return fail(TPO_ERR_INVALID_ARG, "low must be less than high, and original at least 1");
   if (!table && rot > 0) return fail(TPO_ERR_INVALID_ARG, "table must be non-NULL");
   constexpr double kTurn = 6.283185307179586476925;
-  for (int64_t i = 0; i < rot / 2; ++i) {
+  auto turns_of = [&](int64_t i) {  // pair i's, a position
     double f = std::pow(base, -2.0 * static_cast<double>(i) / static_cast<double>(rot));
     if (scaling == TPO_ROTARY_LINEAR) f /= factor;
     if (scaling == TPO_ROTARY_BY_PARTS) {
@@ -141,7 +141,14 @@ tpo_status tpo_rotary_table(int64_t rot, double base, int scaling, double factor
       const double keep = std::fmin(1.0, std::fmax(0.0, (turns - low) / (high - low)));
       f *= keep + (1.0 - keep) / factor;
     }
-    const double turns = f / kTurn;
+    return f / kTurn;
+  };
+  for (int64_t i = 0; i < rot / 2; ++i)
+    if (!std::isfinite(turns_of(i)))
+      return fail(TPO_ERR_INVALID_ARG, "the frequency of pair %lld is not finite: base=%g, factor=%g", (long long)i, base,
+                  factor);
+  for (int64_t i = 0; i < rot / 2; ++i) {
+    const double turns = turns_of(i);
     table[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));  // below 2^64: 53 bits
   }
   return TPO_OK;
