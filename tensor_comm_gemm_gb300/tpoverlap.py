@@ -584,13 +584,18 @@ def _sequences(q_start, k_start, k_len):
     return batch, _ints("q_start", q_start, batch + 1), _ints("k_start", k_start, count), _ints("k_len", k_len, batch)
 
 
+def _scale(scale, dim):
+    """dim^(-1/2) if there is none; the library refuses heads of no elements."""
+    return scale if scale is not None else dim ** -0.5 if dim else 1.0
+
+
 def tpo_attention(block: int, q, k, v, out, q_start=None, k_start=None, k_len=None, causal: bool = True,
                   scale: Optional[float] = None, lse=None, stream=None) -> None:
     n, heads, dim = _shape3("q", q)
     nk, kv = _shape3("k", k)[:2]
     batch, pqs, pks, pkl = _sequences(q_start, k_start, k_len)
     _check(lib().tpo_attention(block, batch, n, nk, heads, kv, dim, pqs, pks, pkl, causal,
-                               dim ** -0.5 if scale is None else scale, *_heads("q", q, n, heads, dim, TPO_BF16),
+                               _scale(scale, dim), *_heads("q", q, n, heads, dim, TPO_BF16),
                                *_heads("k", k, nk, kv, dim, TPO_BF16), *_heads("v", v, nk, kv, dim, TPO_BF16),
                                *_heads("out", out, n, heads, dim, TPO_BF16), _vec("lse", lse, n * heads, TPO_F32),
                                _stream_of(stream, q)))
@@ -612,4 +617,4 @@ def tpo_attention_bwd(block: int, dout, q, k, v, out, lse, dq, dk, dv, q_start=N
     for name, t in (("dk", dk), ("dv", dv)):
         args += _heads(name, t, nk, kv, dim, TPO_BF16)
     _check(lib().tpo_attention_bwd(block, batch, n, nk, heads, kv, dim, pqs, pks, pkl, causal,
-                                   dim ** -0.5 if scale is None else scale, *args, _stream_of(stream, q)))
+                                   _scale(scale, dim), *args, _stream_of(stream, q)))
