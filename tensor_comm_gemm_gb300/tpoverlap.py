@@ -201,6 +201,17 @@ def _raw_stream_getter():
 _RAW_STREAM = _raw_stream_getter()
 
 
+def _current_device_getter():  # of an initialised CUDA, as it is where there are CUDA tensors
+    try:
+        import torch
+        return getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    except Exception:
+        return None
+
+
+_CURRENT_DEVICE = _current_device_getter()
+
+
 def tpo_version() -> str:
     return lib().tpo_version().decode()
 
@@ -504,13 +515,27 @@ def _shape3(name, t):
     return s
 
 
-def _heads(name, t, rows, heads, dim, code):
+def _device_for(t) -> int:
+    """The current device, which a call's tensors must be on: another's memory would fault in its kernels.  -1 if t, the
+    call's first tensor, is not even a CUDA tensor."""
+    return _CURRENT_DEVICE() if t.is_cuda else -1
+
+
+def _elsewhere(name, t, dev):
+    """Refuses t, which is not on device `dev`; where that is -1 the call's first tensor is refused, if t is not."""
+    if not t.is_cuda:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
+    if dev >= 0:
+        raise TpoError(TPO_ERR_INVALID_ARG, "%s is on device %d, the current device is %d" % (name, t.get_device(), dev))
+
+
+def _heads(name, t, rows, heads, dim, code, dev):
     """(pointer, row pitch, head pitch) of an [rows, heads, dim] CUDA tensor of type `code`."""
     if t.shape != (rows, heads, dim):
         raise TpoError(TPO_ERR_INVALID_ARG, "%s has shape %s, expected (%d, %d, %d)" % (name, tuple(t.shape), rows,
                                                                                       heads, dim))
-    if not t.is_cuda:
-        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
+    if dev < 0 or t.get_device() != dev:
+        _elsewhere(name, t, dev)
     if _CODES.get(t.dtype) != code and _code(name, t) != code:
         raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s" % (name, t.dtype))
     ld, hs, unit = t.stride()
@@ -519,7 +544,7 @@ def _heads(name, t, rows, heads, dim, code):
     return t.data_ptr(), ld, hs
 
 
-def _ints(name, t, count, bits=32):
+def _ints(name, t, count, dev, bits=32):
     """Pointer of `count` contiguous CUDA integers; None for None."""
     if t is None:
         return None
@@ -528,8 +553,8 @@ def _ints(name, t, count, bits=32):
         raise TpoError(TPO_ERR_INVALID_ARG, "%s has type %s, expected int%d" % (name, t.dtype, bits))
     if t.numel() != count or not t.is_contiguous():
         raise TpoError(TPO_ERR_INVALID_ARG, "%s must hold %d contiguous elements" % (name, count))
-    if not t.is_cuda:
-        raise TpoError(TPO_ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
+    if dev < 0 or t.get_device() != dev:
+        _elsewhere(name, t, dev)
     return t.data_ptr()
 
 
@@ -548,11 +573,12 @@ def tpo_rotary(block: int, x, table, y, pos=None, layout: int = TPO_ROTARY_HALVE
     ny = _shape3("y", y)[0]
     dt = _code("x", x)
     half = 0 if table is None else table.numel()
-    px, ldx, hx = _heads("x", x, n, heads, dim, dt)
-    py, ldy, hy = _heads("y", y, ny if rows is not None else n, heads, dim, dt)
-    _check(lib().tpo_rotary(block, n, heads, dim, 2 * half, dt, layout, inverse, magnitude, _ints("pos", pos, n),
-                            _ints("table", table, half, 64), px, ldx, hx, _ints("rows", rows, n), ny, py, ldy, hy,
-                            _stream_of(stream, x)))
+    dev = _device_for(x)
+    px, ldx, hx = _heads("x", x, n, heads, dim, dt, dev)
+    py, ldy, hy = _heads("y", y, ny if rows is not None else n, heads, dim, dt, dev)
+    _check(lib().tpo_rotary(block, n, heads, dim, 2 * half, dt, layout, inverse, magnitude, _ints("pos", pos, n, dev),
+                            _ints("table", table, half, dev, 64), px, ldx, hx, _ints("rows", rows, n, dev), ny, py,
+                            ldy, hy, _stream_of(stream, x)))
 
 
 def tpo_attention_workspace(n: int, nk: int, heads: int, kv_heads: int, dim: int) -> int:
@@ -569,7 +595,7 @@ def tpo_attention_bwd_workspace(n: int, nk: int, heads: int, kv_heads: int, dim:
     return b
 
 
-def _sequences(q_start, k_start, k_len):
+def _sequences(q_start, k_start, k_len, dev):
     """(number of sequences, pointers of the three arrays)."""
     if q_start is not None:
         batch = q_start.numel() - 1
@@ -581,7 +607,14 @@ def _sequences(q_start, k_start, k_len):
     count = batch if k_len is not None else batch + 1
     if k_start is not None and k_len is not None and k_start.numel() == batch + 1:
         count = batch + 1
-    return batch, _ints("q_start", q_start, batch + 1), _ints("k_start", k_start, count), _ints("k_len", k_len, batch)
+    return (batch, _ints("q_start", q_start, batch + 1, dev), _ints("k_start", k_start, count, dev),
+            _ints("k_len", k_len, batch, dev))
+
+
+def _lse(lse, count, dev):
+    if lse is not None and lse.get_device() != dev:
+        _elsewhere("lse", lse, dev)
+    return _vec("lse", lse, count, TPO_F32)
 
 
 def _scale(scale, dim):
@@ -593,11 +626,12 @@ def tpo_attention(block: int, q, k, v, out, q_start=None, k_start=None, k_len=No
                   scale: Optional[float] = None, lse=None, stream=None) -> None:
     n, heads, dim = _shape3("q", q)
     nk, kv = _shape3("k", k)[:2]
-    batch, pqs, pks, pkl = _sequences(q_start, k_start, k_len)
-    _check(lib().tpo_attention(block, batch, n, nk, heads, kv, dim, pqs, pks, pkl, causal,
-                               _scale(scale, dim), *_heads("q", q, n, heads, dim, TPO_BF16),
-                               *_heads("k", k, nk, kv, dim, TPO_BF16), *_heads("v", v, nk, kv, dim, TPO_BF16),
-                               *_heads("out", out, n, heads, dim, TPO_BF16), _vec("lse", lse, n * heads, TPO_F32),
+    dev = _device_for(q)
+    batch, pqs, pks, pkl = _sequences(q_start, k_start, k_len, dev)
+    _check(lib().tpo_attention(block, batch, n, nk, heads, kv, dim, pqs, pks, pkl, causal, _scale(scale, dim),
+                               *_heads("q", q, n, heads, dim, TPO_BF16, dev), *_heads("k", k, nk, kv, dim, TPO_BF16, dev),
+                               *_heads("v", v, nk, kv, dim, TPO_BF16, dev),
+                               *_heads("out", out, n, heads, dim, TPO_BF16, dev), _lse(lse, n * heads, dev),
                                _stream_of(stream, q)))
 
 
@@ -605,16 +639,17 @@ def tpo_attention_bwd(block: int, dout, q, k, v, out, lse, dq, dk, dv, q_start=N
                       causal: bool = True, scale: Optional[float] = None, stream=None) -> None:
     n, heads, dim = _shape3("q", q)
     nk, kv = _shape3("k", k)[:2]
-    batch, pqs, pks, pkl = _sequences(q_start, k_start, k_len)
+    dev = _device_for(q)
+    batch, pqs, pks, pkl = _sequences(q_start, k_start, k_len, dev)
     args = []
     for name, t in (("dout", dout), ("q", q)):
-        args += _heads(name, t, n, heads, dim, TPO_BF16)
+        args += _heads(name, t, n, heads, dim, TPO_BF16, dev)
     for name, t in (("k", k), ("v", v)):
-        args += _heads(name, t, nk, kv, dim, TPO_BF16)
-    args += _heads("out", out, n, heads, dim, TPO_BF16)
-    args.append(_vec("lse", lse, n * heads, TPO_F32))
-    args += _heads("dq", dq, n, heads, dim, TPO_BF16)
+        args += _heads(name, t, nk, kv, dim, TPO_BF16, dev)
+    args += _heads("out", out, n, heads, dim, TPO_BF16, dev)
+    args.append(_lse(lse, n * heads, dev))
+    args += _heads("dq", dq, n, heads, dim, TPO_BF16, dev)
     for name, t in (("dk", dk), ("dv", dv)):
-        args += _heads(name, t, nk, kv, dim, TPO_BF16)
+        args += _heads(name, t, nk, kv, dim, TPO_BF16, dev)
     _check(lib().tpo_attention_bwd(block, batch, n, nk, heads, kv, dim, pqs, pks, pkl, causal,
                                    _scale(scale, dim), *args, _stream_of(stream, q)))
