@@ -145,7 +145,7 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
   using L = Layout<DP>;
   const Bars<DP> b(sbase);
   const bool lead = (threadIdx.x & 31) == 0;
-  uint32_t kn = 0, vn = 0, qn = 0, loaded = 0;  // loads so far; of Q by half
+  uint32_t kn = 0, vn = 0, q0 = 0, q1 = 0;  // loads so far; of Q by half
   bool ok = true, open = false;
   Walk w{};
   walk_begin(tiles, sh, w);
@@ -161,11 +161,11 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
     for (int i = 0; ok && i <= loads; ++i) {
       if (i == min(loads, 5)) {  // the next tile is looked up while this one's products run, not when its loads are due
         walk_next(tiles, a.seq, w);
-        static_cast<Entry&>(next) = put_item<Tiles>(sh, w, smem + L::RING_AT, b.items, qn, a.begun, &open);
+        static_cast<Entry&>(next) = put_item<Tiles>(sh, w, smem + L::RING_AT, b.items, q1, a.begun, &open);
       }
       if (i == loads) break;
       const bool q = i == 1 || i == 2, v = !q && i > 0 && (i == loads - 1 || !(i & 1));
-      const uint32_t n = q ? qn : v ? vn : kn, ring = q ? 1u : static_cast<uint32_t>(L::STAGES), st = n % ring;
+      const uint32_t n = q ? (i == 1 ? q0 : q1) : v ? vn : kn, ring = q ? 1u : static_cast<uint32_t>(L::STAGES), st = n % ring;
       const uint32_t full = q ? b.qfull + 8 * (i - 1) : (v ? b.vfull : b.kfull) + 8 * st;
       const uint32_t empty = q ? b.qempty + 8 * (i - 1) : (v ? b.vempty : b.kempty) + 8 * st;
       if (!(ok = wait_warp(a.watch, empty, (n / ring & 1u) ^ 1u, S_EMPTY))) break;
@@ -179,13 +179,14 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
           tma_load_3d(to + d * 16384, map, full, d * 64, q ? it.head * a.group : it.head, row);
       }
       __syncwarp();
-      if (q)
-        qn += i - 1;  // both are of the same tile
+      if (i == 1)
+        ++q0;
+      else if (i == 2)
+        ++q1;
       else if (v)
         ++vn;
       else
         ++kn;
-      loaded += i == 1 ? 1u : i == 2 ? 0x10000u : 0u;
     }
   }
   if (!ok && lead) {  // what is in flight must land before the block gives up its shared memory
@@ -195,8 +196,8 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
 #pragma unroll 1
     for (uint32_t j = vn > L::STAGES ? vn - L::STAGES : 0u; j < vn; ++j)
       wait_bar(a.watch, b.vfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
-    if (loaded & 0xffffu) wait_bar(a.watch, b.qfull, (loaded - 1) & 1u, S_DRAIN, false);
-    if (loaded >> 16) wait_bar(a.watch, b.qfull + 8, (loaded >> 16) - 1 & 1u, S_DRAIN, false);
+    if (q0) wait_bar(a.watch, b.qfull, (q0 - 1) & 1u, S_DRAIN, false);
+    if (q1) wait_bar(a.watch, b.qfull + 8, (q1 - 1) & 1u, S_DRAIN, false);
   }
   __syncwarp();
 }
