@@ -179,7 +179,9 @@ __device__ void load_role(const Args& a, const Tiles<KEYS>& tiles, const Shares&
         ++n0;
     }
   }
-  if (!ok && lead) {  // what is in flight must land before the block gives up its shared memory
+  // What is in flight must land before the block gives up its shared memory, whichever role gave up: this one may have had
+  // room for all of its loads, which nobody waits for then.  (After a call that went well all have landed.)
+  if (lead) {
 #pragma unroll 1
     for (uint32_t j = n0 > L::S0 ? n0 - L::S0 : 0u; j < n0; ++j)
       wait_bar(a.watch, b.full0 + 8 * (j % L::S0), j / L::S0 & 1u, S_DRAIN, false);

@@ -189,7 +189,9 @@ __device__ void load_role(const Args& a, const Tiles& tiles, const Shares& sh, u
         ++kn;
     }
   }
-  if (!ok && lead) {  // what is in flight must land before the block gives up its shared memory
+  // What is in flight must land before the block gives up its shared memory, whichever role gave up: this one may have had
+  // room for all of its loads, which nobody waits for then.  (After a call that went well all have landed.)
+  if (lead) {
 #pragma unroll 1
     for (uint32_t j = kn > L::STAGES ? kn - L::STAGES : 0u; j < kn; ++j)
       wait_bar(a.watch, b.kfull + 8 * (j % L::STAGES), j / L::STAGES & 1u, S_DRAIN, false);
