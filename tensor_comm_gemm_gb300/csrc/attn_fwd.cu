@@ -282,10 +282,12 @@ __device__ void mma_role(const Args& a, uint32_t sbase, uint8_t* smem, uint32_t 
         if (two) {  // half 0's nth turn comes after half 1's one before, half 1's nth after half 0's nth
           const uint32_t due = turn + half;
           uint32_t tries = 0;
+          unsigned long long t0 = 0;
 #pragma unroll 1
-          while (ok && !__all_sync(0xffffffffu, static_cast<int32_t>(turns[1 - half] - due) >= 0))
-            if ((++tries & 255u) == 0u)
-              ok = __all_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(a.watch.err) == 0u);
+          while (ok && !__all_sync(0xffffffffu, static_cast<int32_t>(turns[1 - half] - due) >= 0)) {
+            if (++tries == 256u) t0 = gtime();
+            if (tries > 256u && !(tries & 255u)) ok = !waited_long(t0, a.watch.limit_ns, a.watch.err, S_EMPTY);
+          }
         }
         if (ok) {
           tc_fence_after();
