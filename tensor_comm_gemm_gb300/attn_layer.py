@@ -10,8 +10,10 @@ sequence's rows of a cache of that many rows, and it attends over them.  With
 --tp 1 the output projection adds the residual in its epilogue, and --train runs
 the backward pass through all operators.  With more ranks each rank holds a slice
 of the heads, and the row-parallel output projection is the library's GEMM+AR
-over the ranks' slices.  Prints the time of a step and, with --check, the largest
-error of each result against 64-bit arithmetic.
+over the ranks' slices.  Prints the time of a step and, with --check, the relative
+error of each result against 64-bit arithmetic: of the output and of attention's
+alone, of the gradients, and of the rows that a step writes into a cache, whose
+other rows must stay as they were.
 """
 
 import argparse
@@ -150,14 +152,15 @@ def _turn(x, pos):
 
 
 def reference(layer: AttnLayer, x, pos, lens, dy=None, old=None):
-    """The sublayer in 64 bits, and its gradients by differentiation.  lens: the packed sequences' lengths, or with
-    `old` (caches before the step, of each rank) the keys of each token's sequence, its own the last of them."""
+    """The sublayer in 64 bits (y, and out of the attention alone), and its gradients by differentiation.  lens: the
+    packed sequences' lengths, or with `old` (caches before the step, of each rank) the keys of each token's sequence, its
+    own the last of them; k and v are then the tokens' rows of the caches."""
     leaf = dict(x=x.double(), gamma=layer.gamma.double(), beta=layer.beta.double(),
                 wqkv=torch.cat([w.double() for w in layer.wqkv]), wo=torch.cat([w.double() for w in layer.wo], 1))
     for v in leaf.values():
         v.requires_grad_()
     norm = torch.nn.functional.layer_norm(leaf["x"], (layer.hidden,), leaf["gamma"], leaf["beta"], EPS)
-    outs = []
+    outs, keys, values = [], [], []
     for r, w in enumerate(leaf["wqkv"].chunk(layer.tp)):
         q, k, v = layer.slices((norm @ w.T).view(len(x), -1, layer.dim))
         q, k = _turn(q, pos), _turn(k, pos)
@@ -176,12 +179,31 @@ def reference(layer: AttnLayer, x, pos, lens, dy=None, old=None):
             p = z.masked_fill(hidden, float("-inf")).softmax(2)
             rows.append(torch.einsum("hqk,khd->qhd", p, vs))
         outs.append(torch.cat(rows).flatten(1))
+        keys.append(k)
+        values.append(v)
     y = leaf["x"] + torch.cat(outs, 1) @ leaf["wo"].T
-    out = dict(y=y.detach())
+    out = dict(y=y.detach(), out=torch.cat(outs, 1).detach())
+    if old is not None:
+        out.update(k=torch.cat(keys, 1).detach(), v=torch.cat(values, 1).detach())
     if dy is not None:
         for name, g in zip(leaf, torch.autograd.grad(y, list(leaf.values()), dy.double())):
             out["d" + name] = g
     return out
+
+
+def compare(layer: AttnLayer, b, want, rows=None, old=None):
+    """The error of each of reference()'s results relative to its own size: y alone would hide attention's behind the
+    residual.  With caches (`old`: before the step) also how many elements behind the step's `rows` have changed."""
+    got, errors = dict(b, out=torch.cat([o.flatten(1) for o in b["out"]], 1)), {}
+    if old is not None:
+        rows = rows.long()
+        for name, now, before in (("k", layer.k, old[0]), ("v", layer.v, old[1])):
+            got[name] = torch.cat([c[rows] for c in now], 1)
+            changed = [(c.view(torch.int16) != o.view(torch.int16)).index_fill_(0, rows, False) for c, o in zip(now, before)]
+            errors["other rows of " + name] = float(sum(c.sum() for c in changed))
+    for name in want:
+        errors[name] = float((got[name].double() - want[name]).norm() / want[name].norm())
+    return errors
 
 
 def main(argv=None):
@@ -254,8 +276,7 @@ def main(argv=None):
         errors = {}
         if args.check:
             want = reference(layer, x, pos, lens, dy if args.train else None, old)
-            for name in want:
-                errors[name] = float((b[name].double() - want[name]).norm() / want[name].norm())
+            errors = compare(layer, b, want, where["rows"] if args.cache else None, old)
             print("relative errors: " + ", ".join("%s %.2e" % e for e in errors.items()))
         return errors
     finally:
