@@ -23,9 +23,9 @@
 // each group half of a step's columns, and store.
 //
 // Measured (back-to-back calls with a flushed L2): two sequences of 4096 causal
-// tokens, 32 heads of 128 over 8, 730 to 746 us, or 1.31 PFLOP/s of the seven
-// products (67 % of the measured matrix rate; 940 TFLOP/s of the five that a single
-// pass would need).  Bound by a step's chain of product, exponentials, product and
+// tokens, 32 heads of 128 over 8, 730 to 754 us, or 1.28 to 1.32 PFLOP/s of the seven
+// products (65 to 67 % of the measured matrix rate; 910 to 940 TFLOP/s of the five that
+// a single pass would need).  Bound by a step's chain of product, exponentials, product and
 // store to tensor memory, with 512 columns of it all in use: sixteen computing
 // warps of half the columns took 842 us, groups that take the steps in turns as
 // long as these.  Odd sequences of 9 heads of 80 over 3: 72 us, bound by the five
@@ -423,6 +423,8 @@ __device__ void compute_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
           }
         }
         if constexpr (KEYS) {
+          // p, and ds below, are operands of products with bf16 tensors, and take their type: the gradients are off by 0.0025
+          // of their size, for 0.0018 with both in fp32
           uint32_t h[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) h[e] = pack_bf16(pr[e].x, pr[e].y);

@@ -277,7 +277,8 @@ __device__ __forceinline__ int tile_begin(const Shares& p, const Walk& w) { retu
 __device__ __forceinline__ int tile_slot(int first, int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
 
 // For the kernels that join: parts s up to `end`, eight, four or two at a time, so that their loads are in flight
-// together and few are made for nothing (most divided tiles have two or three parts).
+// together and few are made for nothing: two or three parts of a long causal prompt's tile take one round, the ten or
+// eleven of a short prompt over a long cache two, and so do the nine of a slice of a single token's.
 template <int U>
 struct Count {
   static constexpr int value = U;
@@ -478,6 +479,8 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 // ------------------------------------------------------------------ arithmetic
 
+// 2^x by the special function unit, 2^-22 of the value: below the 2^-8 of a weight's rounding to bf16, and of either sign in
+// the sums.  Results below 2^-126 become 0: of a row's weights the largest is 1 to 2^8.
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -30,14 +30,17 @@
 // softmax (3950 cycles a step, now 2850, of which the tensor core works 2080).
 //
 // Measured (times of back-to-back calls with a flushed L2): 8192 causal tokens of
-// 32 heads of 128 over 8 take 398 to 405 us, 1.37 PFLOP/s, 70 % of the measured matrix
-// rate; bound by that step: a half's scores, softmax (about 1450 cycles, 512 of
+// 32 heads of 128 over 8 take 398 to 415 us, 1.33 to 1.38 PFLOP/s, 67 to 70 % of the
+// measured matrix rate; bound by that step: a half's scores, softmax (about 1450 cycles, 512 of
 // them exponentials at 32 a cycle) and P V follow one another, and two halves do
 // not quite fill each other's gaps.  12 packed sequences of 8 heads over 1:
 // 53 us, bound by filling the pipeline at the start and at each tile (about 6000
 // cycles).  One token of 64 sequences over 8 heads of keys: 181 us, 89 % of the
 // measured bandwidth.  One token over 32768 keys: 22 to 24 us, bound by latency (a
-// cold load, two steps and the join of 130 parts).
+// cold load, two steps and the join of 130 parts).  A step of heads of 64 takes as
+// long as one of 128, 2800 cycles (8192 tokens both ways, 16 heads: 303 us), though
+// its products take half: so a token of 64 sequences over 8 heads of 64 takes 135 us,
+// 4.0 TB/s.
 
 #include <algorithm>
 #include <climits>
@@ -469,7 +472,9 @@ __device__ void softmax_role(const Args& a, uint32_t sbase, uint8_t* smem, uint3
       const float sub = m == -INFINITY ? 0.0f : -m;
       const float2 sub2 = make_float2(sub, sub);
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      // 64 keys' weights, rounded, over their own columns; the product with the first 64 runs beside the others
+      // 64 keys' weights, over their own columns; the product with the first 64 runs beside the others.  They are rounded to
+      // bf16, since the matrix instruction takes both operands in V's type: out is off by 0.0018 to 0.0024 of its size, where
+      // weights in fp32 would give 0.0015 to 0.0017.  Their sum is taken before that.
       auto weights = [&](uint32_t(&z)[64], uint32_t at, uint32_t bar) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
