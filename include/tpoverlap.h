@@ -637,7 +637,8 @@ int64_t tpo_attention_bwd_workspace(int64_t n, int64_t nk, int64_t heads, int64_
  * the device, nothing is computed and tpo_block_sync_status reports the same
  * error.
  * What stores a tile waits for as long as its block works on it, about 1.5 us for
- * every 128 keys: from some 10^8 keys on, option "wait_timeout_ms" has to follow.
+ * every 128 keys, and the way past a million slots without queries takes some
+ * 10 ms: from 10^8 of either on, option "wait_timeout_ms" has to follow.
  * Outputs overlap no input.
  */
 tpo_status tpo_attention(tpo_block* blk, int64_t batch, int64_t n, int64_t nk, int64_t heads, int64_t kv_heads,
